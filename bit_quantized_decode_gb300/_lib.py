@@ -138,6 +138,11 @@ SIGNATURES["i8g32_quantize_host"] = ([_P, _I, _I, _P, _P], _I)
 SIGNATURES["w4_last_device_error"] = ([ctypes.POINTER(ctypes.c_uint)], _I)
 SIGNATURES["w4_hbm_read"] = ([_P, _SZ, _P, _P], _I)
 SIGNATURES["w4_selftest_wait_timeout"] = ([_I, ctypes.c_uint, _P], _I)
+SIGNATURES["w8a8_workspace_bytes"] = ([_I, _I, _I], _SZ)
+SIGNATURES["w8a8_matmul"] = ([_P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _P, _SZ, _P], _I)
+SIGNATURES["w8a8_linear"] = ([_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _PF, _U, _P, _SZ, _P], _I)
+ELEM_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # W4_F32, W4_F16, W4_BF16
+W4_MAX_TOKENS = 1 << 20
 W4_MAX_CHAIN = 128
 
 _lib = None
@@ -573,6 +578,75 @@ def w8a32_gemv(w, s_w, bias, x, y, flags: int = 0, stream=None):
     N = y.shape[1]
     _check("w8a32_gemv", load().w8a32_gemv(_ptr(w), _ptr(s_w), _ptr(bias), _ptr(x), M, N, K, _ptr(y), flags,
                                            _stream(stream)))
+
+
+# -------------------------------------------- INT8 x INT8, any number of tokens
+def _check_tensors(**specs):
+    """Each keyword: (tensor or None, dtypes, shape or None).  Contiguous, of one of the dtypes, of the shape, on the
+    current CUDA device."""
+    cur = None
+    for name, (t, dtypes, shape) in specs.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensor must live on a CUDA device")
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.device.index != cur:
+            raise ValueError(f"{name}: tensor lives on {t.device}, the current device is cuda:{cur}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensor must be contiguous")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: dtype {t.dtype} is not one of {[str(d) for d in dtypes]}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
+
+
+_F32 = (torch.float32,)
+_I8 = (torch.int8,)
+_U8 = (torch.uint8,)
+_FLOATS = tuple(ELEM_TYPES)
+
+
+def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().w8a8_workspace_bytes(M, N, K))
+
+
+def _w8_sizes(w, N, K):
+    need = w8_repacked_bytes(N, K)
+    if w.numel() < need:
+        raise ValueError(f"w: {w.numel()} bytes, {need} are needed")
+
+
+def w8a8_matmul(w, s_w, bias, qx, sx, y, workspace, stream=None):
+    """y [M][N] (fp32, fp16 or bf16) from per-row INT8 weights (w8_repack) and int8 codes qx [M][K], sx [M]."""
+    M, K = qx.shape
+    N = y.shape[1]
+    _check_tensors(w=(w, _U8, None), s_w=(s_w, _F32, (N,)), bias=(bias, _F32, (N,)), qx=(qx, _I8, None),
+                   sx=(sx, _F32, (M,)), y=(y, _FLOATS, (M, N)), workspace=(workspace, _U8, None))
+    _w8_sizes(w, N, K)
+    _check("w8a8_matmul", load().w8a8_matmul(_ptr(w), _ptr(s_w), _ptr(bias), _ptr(qx), _ptr(sx), M, N, K, _ptr(y),
+                                             ELEM_TYPES[y.dtype], _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def w8a8_linear(w, s_w, bias, x, y, qx, sx, workspace, norm=None, eps: float = 0.0, residual=None, flags: int = 0,
+                stream=None):
+    """Quantize x [M][K] (fp32, fp16 or bf16; RMSNorm first with norm) and form y [M][N] (any of the three types)
+    from per-row INT8 weights, for any number of tokens; residual float32 [M][N] is added before the rounding.
+    qx: int8 [M][K] to receive the codes, or None."""
+    M, K = x.shape
+    N = y.shape[1]
+    _check_tensors(w=(w, _U8, None), s_w=(s_w, _F32, (N,)), bias=(bias, _F32, (N,)), x=(x, _FLOATS, None),
+                   y=(y, _FLOATS, (M, N)), qx=(qx, _I8, (M, K)), sx=(sx, _F32, (M,)), workspace=(workspace, _U8, None),
+                   norm=(norm, _F32, (K,)), residual=(residual, _F32, (M, N)))
+    _w8_sizes(w, N, K)
+    fz = None
+    if norm is not None or residual is not None:
+        fz = ctypes.byref(Fusion(None if norm is None else norm.data_ptr(), float(eps), W4_GLU_NONE,
+                                 None if residual is None else residual.data_ptr()))
+    _check("w8a8_linear", load().w8a8_linear(_ptr(w), _ptr(s_w), _ptr(bias), _ptr(x), ELEM_TYPES[x.dtype], M, N, K,
+                                             _ptr(y), ELEM_TYPES[y.dtype], _ptr(qx), _ptr(sx), fz, flags,
+                                             _ptr(workspace), workspace.numel(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- chains

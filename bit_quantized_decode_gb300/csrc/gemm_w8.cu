@@ -1,0 +1,459 @@
+// INT8 x INT8 matrix product with a scale for each token and each output
+// channel, for any number of tokens, on the 5th-generation tensor cores:
+//   acc[m][j] = sum_i q_w[j][i] q_x[m][i]   (exact),
+//   y[m][j]   = fma(fp32(s_w[j] s_x[m]), fp32(acc), b[j]) (+ residual), rounded to y's type.
+//
+// The chip's integer tensor rate is far below its fp16 rate, and an int8 value
+// is an fp16 value exactly, so the product runs on tcgen05.mma kind::f16: a
+// product is at most 2^14, 1024 of them at most 2^24, so an fp32 accumulator
+// over 1024 K holds the integer sum exactly; each accumulator is then added
+// into int32 registers while the tensor cores fill the other one.
+//   * A (128 weight rows) streams as int8, is converted by eight warps (XOR,
+//     byte permute, one fp16 subtraction) and stored into tensor memory, so a
+//     weight costs one byte of HBM, L2 and shared-memory traffic.  The
+//     repacked layout (8-row tiles of 32-byte units) is read as it is: the
+//     same bytes serve every path of the format.
+//   * B (up to 128 tokens) comes as fp16 codes in the layout that the row
+//     quantizer writes: a K group of eight of a token tile is one contiguous
+//     run, copied by a 1-D bulk copy into the core-matrix layout without
+//     swizzle.
+//   * Persistent blocks, one per SM: a copy warp, an MMA lane, eight
+//     converting warps (two groups on alternate 64-K stages) and eight
+//     epilogue warps, joined by mbarriers only.
+//   * Few tiles: K is split over a thread-block cluster; the splits exchange
+//     their integer sums through distributed shared memory (split r owns the
+//     tokens c with c % splits = r), so every block writes a share of y.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "operators.h"
+#include "ptx.cuh"
+#include "typed_io.cuh"
+
+namespace w4k {
+namespace {
+
+constexpr uint64_t kG8WaitNs = 250ull * 1000ull * 1000ull;
+constexpr uint32_t kG8Cols = 512;
+constexpr uint32_t kG8ColAcc = 0;                       // two accumulators
+constexpr uint32_t kG8ColA = 2 * kG8MaxTok;             // kG8ABufs converted stages of 32 columns
+static_assert(kG8ColA + 32 * kG8ABufs <= kG8Cols, "tensor-memory columns");
+constexpr int kWarpMma = 1, kWarpConv = 4, kWarpEpi = 12;
+
+// One kind::f16 MMA (A in tensor memory, B from a shared-memory descriptor).
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Box of a 2-D tensor map -> shared memory.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t pol)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+        "%3}], [%4], %5;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar), "l"(pol)
+        : "memory");
+}
+
+// L2 policy for the activation codes, which every row group reads again.
+__device__ __forceinline__ uint64_t l2_policy_evict_last()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_constant__ Gemm8Args A)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = A.stages, nt = A.nt, ks = A.splits;
+    const Gemm8Smem L = gemm8_smem(S, nt, ks);
+    const int slot_bytes = kG8WBytes + nt * 128;
+    const uint32_t bars = smem_u32(smem + L.bars);
+    const uint32_t full_b = bars;                                  // [S] stage landed
+    const uint32_t empty_b = full_b + 8 * kG8MaxStages;            // [S] four converting warps and the MMA commit
+    const uint32_t ready_b = empty_b + 8 * kG8MaxStages;           // [kG8ABufs] converted (four warps)
+    const uint32_t free_b = ready_b + 8 * kG8ABufs;                // [kG8ABufs] read by the MMAs
+    const uint32_t accf_b = free_b + 8 * kG8ABufs;                 // [2] accumulator complete
+    const uint32_t acce_b = accf_b + 16;                           // [2] accumulator read (eight warps)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L.tmem);
+    volatile uint32_t* dead_s = tmem_slot + 1;
+
+    const int rank = ks > 1 ? static_cast<int>(blockIdx.x) % ks : 0;
+    const int tile_first = static_cast<int>(blockIdx.x) / ks;
+    const int tile_step = static_cast<int>(gridDim.x) / ks;
+    const int ntiles = A.n_g * A.n_tt;
+    const int nst = (A.C + kG8StageChunks - 1) / kG8StageChunks;
+    const int st0 = static_cast<int>(static_cast<long long>(rank) * nst / ks);
+    const int st1 = static_cast<int>(static_cast<long long>(rank + 1) * nst / ks);
+
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_b + 8 * s, 1);
+            mbar_init(empty_b + 8 * s, 5);
+        }
+        for (int j = 0; j < kG8ABufs; ++j) {
+            mbar_init(ready_b + 8 * j, 4);
+            mbar_init(free_b + 8 * j, 1);
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(accf_b + 8 * j, 1);
+            mbar_init(acce_b + 8 * j, 8);
+        }
+        fence_mbar_init();
+        *dead_s = 0u;
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(tmem_slot), kG8Cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // the next kernel's blocks may come only once this one holds its tensor memory
+    pdl_launch_dependents();
+    if (ks > 1) cluster_sync();          // the other splits' shared memory is there
+    const uint32_t tbase = *tmem_slot;
+    auto fail = [&]() {
+        *dead_s = 1u;
+        if (A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
+    };
+    if (warp == 0) {
+        // ------------------------------------------------------- copy warp
+        const uint64_t pol = l2_policy_evict_first(), pol_b = l2_policy_evict_last();
+        auto copy_w = [&](int tile, int st, int slot) {
+            if (lane == 0) {
+                const uint32_t bar = full_b + 8 * slot;
+                const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kG8WBytes + k8 * nt * 16));
+                // 16 row tiles x 64 K; tiles past T and chunks past C arrive as zeros
+                tma_load_2d(smem_u32(smem + L.ring + static_cast<size_t>(slot) * slot_bytes), &A.wmap,
+                            st * kG8StageChunks * 32, (tile / A.n_tt) * (kG8Rows / kRows), bar, pol);
+            }
+        };
+        auto copy_b = [&](int tile, int st, int slot) {
+            if (lane == 0) {
+                const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
+                const uint4* src = A.xh + (static_cast<size_t>(tile % A.n_tt) * (A.K >> 3) + st * kG8StageChunks * 4) * nt;
+                bulk_g2s(smem_u32(smem + L.ring + static_cast<size_t>(slot) * slot_bytes + kG8WBytes), src,
+                         static_cast<uint32_t>(k8 * nt * 16), full_b + 8 * slot, pol_b);
+            }
+        };
+        // the first tile's weights do not depend on the previous kernel
+        int ahead = 0;
+        if (tile_first < ntiles)
+            for (; ahead < S && st0 + ahead < st1; ++ahead) copy_w(tile_first, st0 + ahead, ahead);
+        pdl_wait();
+        int it = 0, slot = 0;
+        uint32_t ph = 1u;                // parity of the slot's previous release
+        bool ok = true;
+        for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
+            for (int st = st0; st < st1; ++st, ++it) {
+                if (it >= ahead) {
+                    if (it >= S) {
+                        ok = mbar_wait_bounded(empty_b + 8 * slot, ph, kG8WaitNs);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) {
+                            if (lane == 0) fail();
+                            break;
+                        }
+                        if (lane == 0) fence_proxy_async_smem();
+                    }
+                    copy_w(tile, st, slot);
+                }
+                copy_b(tile, st, slot);
+                if (++slot == S) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        // every copy has landed before the block ends (also after a failure)
+        for (int k = max(0, it - S); k < it; ++k)
+            if (!mbar_wait_bounded(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u, kG8WaitNs)) break;
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // -------------------------------------------------------- MMA lane
+        if (lane == 0) {
+            const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(kG8Rows >> 4) << 24);
+            int it = 0, ac = 0, slot = 0;
+            uint32_t sph = 0u;
+            bool ok = true;
+            for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
+                for (int st = st0; st < st1; ++st, ++it) {
+                    const int k16 = 2 * min(kG8StageChunks, A.C - st * kG8StageChunks);
+                    const int j = it % kG8ABufs;
+                    const bool first = (st - st0) % kG8AccStages == 0;
+                    const uint32_t dcol = tbase + kG8ColAcc + static_cast<uint32_t>(ac & 1) * kG8MaxTok;
+                    if (first && ac >= 2) ok = mbar_wait_bounded(acce_b + 8 * (ac & 1), static_cast<uint32_t>((ac >> 1) - 1) & 1u, kG8WaitNs);
+                    ok = ok && mbar_wait_bounded(full_b + 8 * slot, sph, kG8WaitNs);
+                    ok = ok && mbar_wait_bounded(ready_b + 8 * j, static_cast<uint32_t>(it / kG8ABufs) & 1u, kG8WaitNs);
+                    if (!ok) {
+                        fail();
+                        break;
+                    }
+                    tc_fence_after();
+                    // core matrices of 8 tokens x 8 K (128 B): token groups 128 B apart, K groups nt * 16 B
+                    const uint64_t bdesc = smem_desc_noswizzle(
+                        smem_u32(smem + L.ring + static_cast<size_t>(slot) * slot_bytes + kG8WBytes),
+                        static_cast<uint32_t>(nt * 16), 128u);
+                    const uint32_t acol = tbase + kG8ColA + 32u * static_cast<uint32_t>(j);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < k16)
+                            tc_mma_f16_ts(dcol, acol + 8 * kk, bdesc + static_cast<uint64_t>(kk * 2 * nt), idesc,
+                                          first && kk == 0 ? 0u : 1u);
+                    tc_commit(free_b + 8 * j);
+                    tc_commit(empty_b + 8 * slot);
+                    if (st + 1 == st1 || (st - st0) % kG8AccStages == kG8AccStages - 1) {
+                        tc_commit(accf_b + 8 * (ac & 1));
+                        ++ac;
+                    }
+                    if (++slot == S) {
+                        slot = 0;
+                        sph ^= 1u;
+                    }
+                }
+            }
+            // every MMA has completed before the tensor memory is freed
+            if (it > 0)
+                mbar_wait_bounded(free_b + 8 * ((it - 1) % kG8ABufs), static_cast<uint32_t>((it - 1) / kG8ABufs) & 1u, kG8WaitNs);
+        }
+        __syncwarp();
+    } else if (warp >= kWarpConv && warp < kWarpEpi) {
+        // ------------------------------------------------ converting warps
+        const int grp = (warp - kWarpConv) >> 2;
+        const int row = (warp & 3) * 32 + lane;                    // tensor-memory lane and weight row of the tile
+        const int hsel = (row >> 2) & 1;                           // reading order of a unit's halves (bank spread)
+        const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        int it = 0, slot = 0;
+        uint32_t sph = 0u;
+        bool ok = true;
+        for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
+            for (int st = st0; st < st1; ++st, ++it) {
+                if ((it & 1) == grp) {
+                    const int nch = min(kG8StageChunks, A.C - st * kG8StageChunks);
+                    const int j = it % kG8ABufs;
+                    ok = mbar_wait_bounded(full_b + 8 * slot, sph, kG8WaitNs);
+                    ok = ok && (it < kG8ABufs ||
+                                mbar_wait_bounded(free_b + 8 * j, static_cast<uint32_t>(it / kG8ABufs - 1) & 1u, kG8WaitNs));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) {
+                        if (lane == 0) fail();
+                        break;
+                    }
+                    const uint8_t* u = smem + L.ring + static_cast<size_t>(slot) * slot_bytes + (row >> 3) * 512 + (row & 7) * 32;
+                    uint4 a[kG8StageChunks], b[kG8StageChunks];
+#pragma unroll
+                    for (int e = 0; e < kG8StageChunks; ++e) {
+                        a[e] = *reinterpret_cast<const uint4*>(u + e * 256 + (hsel << 4));
+                        b[e] = *reinterpret_cast<const uint4*>(u + e * 256 + ((hsel ^ 1) << 4));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty_b + 8 * slot);
+                    tc_fence_after();
+#pragma unroll
+                    for (int e = 0; e < kG8StageChunks; ++e) {
+                        if (e < nch) {
+                            const uint4 lo = hsel ? b[e] : a[e], hi = hsel ? a[e] : b[e];
+                            uint32_t h[16];
+                            i8_to_f16(lo.x, h[0], h[1]);
+                            i8_to_f16(lo.y, h[2], h[3]);
+                            i8_to_f16(lo.z, h[4], h[5]);
+                            i8_to_f16(lo.w, h[6], h[7]);
+                            i8_to_f16(hi.x, h[8], h[9]);
+                            i8_to_f16(hi.y, h[10], h[11]);
+                            i8_to_f16(hi.z, h[12], h[13]);
+                            i8_to_f16(hi.w, h[14], h[15]);
+                            tmem_st16(tbase + tlane + kG8ColA + 32u * static_cast<uint32_t>(j) + 16u * e, h);
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ready_b + 8 * j);
+                }
+                if (++slot == S) {
+                    slot = 0;
+                    sph ^= 1u;
+                }
+            }
+        }
+    } else if (warp >= kWarpEpi) {
+        // -------------------------------------------------- epilogue warps
+        const int half = (warp - kWarpEpi) >> 2;
+        const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        int acc[4][16];                  // token columns 32 b + 16 half + i of this thread's row
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[b][i] = 0;
+        int ac = 0;
+        bool ok = true;
+        pdl_wait();
+        for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
+            const int row = (tile / A.n_tt) * kG8Rows + (warp & 3) * 32 + lane;
+            const float sw = row < A.N ? __ldg(A.s_w + row) : 0.0f;
+            const float bv = row < A.N && A.bias != nullptr ? __ldg(A.bias + row) : 0.0f;
+            for (int st = st0; st < st1; st += kG8AccStages, ++ac) {
+                ok = mbar_wait_bounded(accf_b + 8 * (ac & 1), static_cast<uint32_t>(ac >> 1) & 1u, kG8WaitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (32 * b + 16 * half < nt) {
+                        uint32_t d[16];
+                        tmem_ld16(tbase + tlane + kG8ColAcc + static_cast<uint32_t>((ac & 1) * kG8MaxTok + 32 * b + 16 * half), d);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[b][i] += __float2int_rn(__uint_as_float(d[i]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acce_b + 8 * (ac & 1));
+            }
+            if (ks > 1 || !ok) break;
+            const int m0 = (tile % A.n_tt) * nt;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (32 * b + 16 * half < nt) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int m = m0 + 32 * b + 16 * half + i;
+                        if (m < A.M && row < A.N) {
+                            float v = __fmaf_rn(__fmul_rn(sw, __ldg(A.sx + m)), __int2float_rn(acc[b][i]), bv);
+                            const size_t o = static_cast<size_t>(m) * A.N + row;
+                            if (A.residual != nullptr) v = __fadd_rn(A.residual[o], v);
+                            store_typed(A.y, A.ytype, o, v);
+                        }
+                        acc[b][i] = 0;
+                    }
+                }
+            }
+        }
+        if (ks > 1) {
+            // token column c of the tile belongs to split c % ks: its sums go there
+            const int per = nt / ks;
+            const uint32_t red_u = smem_u32(smem + L.red);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (32 * b + 16 * half < nt) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = 32 * b + 16 * half + i;
+                        const int o = (rank * per + c / ks) * kG8Rows + (warp & 3) * 32 + lane;
+                        st_cluster_u32(mapa_shared(red_u + 4u * static_cast<uint32_t>(o), static_cast<uint32_t>(c % ks)),
+                                       static_cast<uint32_t>(acc[b][i]));
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+
+    // ---- K splits: this split's columns, summed in order of the splits
+    if (ks > 1) {
+        const int per = nt / ks;
+        const int* red = reinterpret_cast<const int*>(smem + L.red);
+        cluster_sync();
+        pdl_wait();
+        const int m0 = (tile_first % A.n_tt) * nt;
+        const bool dead = *dead_s != 0u;
+        for (int idx = tid; idx < per * kG8Rows; idx += kG8Threads) {
+            const int r = idx % kG8Rows, c = idx / kG8Rows;
+            const int row = (tile_first / A.n_tt) * kG8Rows + r;
+            const int m = m0 + c * ks + rank;
+            if (row < A.N && m < A.M && !dead) {
+                int s = 0;
+                for (int q = 0; q < ks; ++q) s += red[(q * per + c) * kG8Rows + r];
+                float v = __fmaf_rn(__fmul_rn(__ldg(A.s_w + row), __ldg(A.sx + m)), __int2float_rn(s),
+                                    A.bias != nullptr ? __ldg(A.bias + row) : 0.0f);
+                const size_t o = static_cast<size_t>(m) * A.N + row;
+                if (A.residual != nullptr) v = __fadd_rn(A.residual[o], v);
+                store_typed(A.y, A.ytype, o, v);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tbase, kG8Cols);
+    }
+}
+
+}  // namespace
+
+namespace {
+// The weights as a 2-D array of 8-byte elements: a row per 8-row tile (C
+// chunks of 256 bytes), a box of 16 tiles x one stage.
+cudaError_t encode_wmap(Gemm8Args& a)
+{
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<void*> cached{nullptr};
+    void* fn = cached.load(std::memory_order_acquire);
+    if (fn == nullptr) {
+        cudaDriverEntryPointQueryResult got;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got);
+        if (e != cudaSuccess) return e;
+        if (got != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+        cached.store(fn, std::memory_order_release);
+    }
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.C) * 32, static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.C) * 256};
+    const cuuint32_t box[2] = {32 * kG8StageChunks, kG8Rows / kRows};
+    const cuuint32_t ones[2] = {1, 1};
+    const CUresult r = reinterpret_cast<Encode>(fn)(
+        &a.wmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, 2, const_cast<uint8_t*>(a.w), dims, strides, box, ones,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+cudaError_t launch_gemm_w8(Gemm8Args& a, int grid, size_t smem, bool pdl, cudaStream_t s)
+{
+    auto kern = gemm_w8_kernel;
+    static SmemLimit limit;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, smem);
+    if (e == cudaSuccess) e = encode_wmap(a);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kG8Threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (pdl) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    if (a.splits > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = static_cast<unsigned>(a.splits);
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    cfg.attrs = na > 0 ? attr : nullptr;
+    cfg.numAttrs = static_cast<unsigned>(na);
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace w4k

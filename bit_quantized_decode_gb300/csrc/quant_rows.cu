@@ -1,0 +1,170 @@
+// Per-token INT8 activation codes for any number of tokens and for fp32, fp16
+// or bf16 activations, with RMSNorm in front where asked: the codes and scales
+// of a8_quantize / rms_a8_quantize (every step an IEEE fp32 operation on the
+// activations widened to fp32, see quant_a8.cuh and fusion.cuh).
+//
+// One block per token; the row stays in registers between the norm, the
+// maximum and the rounding (K <= 20480; longer rows are read again).  Besides
+// the int8 codes it writes them as fp16 in the layout that the tensor-core
+// product copies tiles of (f16_word): a stage of a token tile is one
+// contiguous run in the MMA's core-matrix order.  It moves the activations once and the codes once (2 bytes each); its
+// time is HBM traffic for long prompts and one launch's latency for few tokens.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fusion.cuh"
+#include "operators.h"
+#include "ptx.cuh"
+#include "quant_a8.cuh"
+#include "typed_io.cuh"
+
+namespace w4k {
+namespace {
+
+constexpr int kQrThreads = 256;
+constexpr int kQrWarps = kQrThreads / 32;
+
+template <int XT, int NIT, bool kNorm>
+__global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsArgs a)
+{
+    __shared__ float red_s[2 * kQrWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int m = blockIdx.x;
+    const int K8 = a.K >> 3;
+    constexpr int kN = NIT > 0 ? NIT : 1;
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t row = static_cast<size_t>(m) * a.K;
+    float v[kN][8];
+    if constexpr (NIT > 0) {
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+            const int i = tid + it * kQrThreads;
+            if (i < K8) load8<XT>(a.x, row + 8 * static_cast<size_t>(i), v[it]);
+            else zero8(v[it]);
+        }
+    }
+    auto each = [&](auto&& f) {
+        if constexpr (NIT > 0) {
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+                const int i = tid + it * kQrThreads;
+                if (i < K8) f(i, v[it]);
+            }
+        } else {
+            for (int i = tid; i < K8; i += kQrThreads) {
+                load8<XT>(a.x, row + 8 * static_cast<size_t>(i), v[0]);
+                f(i, v[0]);
+            }
+        }
+    };
+    float r = 1.0f;
+    auto normed = [&](int i, float (&t)[8]) {
+        if constexpr (kNorm) {
+            float g[8];
+            load8<T_F32>(a.gamma, 8 * static_cast<size_t>(i), g);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = __fmul_rn(__fmul_rn(t[k], r), g[k]);
+        }
+    };
+    if constexpr (kNorm) {
+        float hi = 0.0f, lo = 0.0f;
+        each([&](int, float (&t)[8]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sq_acc(t[k], hi, lo);
+        });
+        warp_pair_sum(hi, lo);
+        if (lane == 0) {
+            red_s[2 * warp] = hi;
+            red_s[2 * warp + 1] = lo;
+        }
+        __syncthreads();
+        hi = red_s[0];
+        lo = red_s[1];
+#pragma unroll
+        for (int w = 1; w < kQrWarps; ++w) pair_merge(hi, lo, red_s[2 * w], red_s[2 * w + 1]);
+        r = rms_scale(hi, lo, a.K, a.eps);
+        __syncthreads();
+    }
+    float mx = 0.0f;
+    each([&](int i, float (&t)[8]) {
+        normed(i, t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(t[k]));
+    });
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    if (lane == 0) red_s[warp] = mx;
+    __syncthreads();
+    float amax = red_s[0];
+#pragma unroll
+    for (int w = 1; w < kQrWarps; ++w) amax = fmaxf(amax, red_s[w]);
+    const A8Scale ks = a8_scale(amax);
+    if (tid == 0) a.sx[m] = ks.s;
+    uint2* q8 = a.qx != nullptr ? reinterpret_cast<uint2*>(a.qx + row) : nullptr;
+    each([&](int i, float (&t)[8]) {
+        if constexpr (NIT == 0) normed(i, t);
+        const uint2 q = quant8(t, ks);
+        if (q8 != nullptr) q8[i] = q;
+        if (a.xh != nullptr) a.xh[f16_word(m, i, K8, a.nt)] = codes_f16(q);
+    });
+}
+
+__global__ void __launch_bounds__(256) expand_codes_kernel(const int8_t* __restrict__ qx, int M, int K8,
+                                                           uint4* __restrict__ xh, int nt)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int m = blockIdx.x;
+    const uint2* q = reinterpret_cast<const uint2*>(qx) + static_cast<size_t>(m) * K8;
+    for (int i = threadIdx.x; i < K8; i += 256) xh[f16_word(m, i, K8, nt)] = codes_f16(__ldg(q + i));
+}
+
+cudaLaunchConfig_t row_launch(int blocks, int threads, bool pdl, cudaStream_t s, cudaLaunchAttribute* attr)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = pdl ? attr : nullptr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cfg;
+}
+
+template <int XT, bool kNorm>
+cudaError_t launch_rows(const QuantRowsArgs& a, const cudaLaunchConfig_t& cfg)
+{
+    const int nit = (a.K / 8 + kQrThreads - 1) / kQrThreads;
+    if (nit <= 2) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 2, kNorm>, a);
+    if (nit <= 4) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 4, kNorm>, a);
+    if (nit <= 10) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 10, kNorm>, a);
+    return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 0, kNorm>, a);
+}
+
+template <int XT>
+cudaError_t launch_typed(const QuantRowsArgs& a, const cudaLaunchConfig_t& cfg)
+{
+    return a.gamma != nullptr ? launch_rows<XT, true>(a, cfg) : launch_rows<XT, false>(a, cfg);
+}
+
+}  // namespace
+
+cudaError_t launch_quant_rows(const QuantRowsArgs& a, int xtype, bool pdl, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = row_launch(a.M, kQrThreads, pdl, s, attr);
+    if (xtype == T_F32) return launch_typed<T_F32>(a, cfg);
+    if (xtype == T_F16) return launch_typed<T_F16>(a, cfg);
+    return launch_typed<T_BF16>(a, cfg);
+}
+
+cudaError_t launch_expand_codes(const int8_t* qx, int M, int K, uint4* xh, int nt, bool pdl, cudaStream_t s)
+{
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = row_launch(M, 256, pdl, s, attr);
+    return cudaLaunchKernelEx(&cfg, expand_codes_kernel, qx, M, K / 8, xh, nt);
+}
+
+}  // namespace w4k

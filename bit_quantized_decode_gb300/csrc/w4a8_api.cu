@@ -10,6 +10,7 @@
 
 #include "../../include/w4a8.h"
 #include "internal.h"
+#include "operators.h"
 
 using namespace w4k;
 
@@ -69,6 +70,14 @@ w4_status device_info(DeviceInfo** out)
 }  // namespace
 
 namespace w4k {
+bool device_facts(DeviceFacts* out)
+{
+    DeviceInfo* d = nullptr;
+    if (device_info(&d) != W4_OK) return false;
+    *out = DeviceFacts{d->sms, d->smem_optin, d->err};
+    return true;
+}
+
 cudaError_t raise_smem_limit(const void* kern, SmemLimit& rec, size_t smem)
 {
     int dev = 0;

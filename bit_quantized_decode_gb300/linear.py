@@ -15,7 +15,9 @@ from . import _lib
 
 # "w4a32" and "w8a32" are the weight-only paths on float activations (per-row
 # INT4 unpacked to float, per-row INT8); their calls ignore qx and sx.
-FORMATS = ("w4", "q4_0", "i8g32", "q6g32", "w4a32", "w8a32")
+# "w8" is the INT8 x INT8 linear: the weights of "w8a32" on quantized
+# activations, for any number of tokens and fp32, fp16 or bf16 x and y.
+FORMATS = ("w4", "q4_0", "i8g32", "q6g32", "w4a32", "w8a32", "w8")
 
 
 class QuantLinear:
@@ -26,7 +28,7 @@ class QuantLinear:
         self.fmt, self.N, self.K = fmt, N, K   # N: outputs per token (a paired gate/up linear: I)
         self.glu_pairs = glu_pairs
         self.w = w                  # repacked device layout, uint8
-        self.s_w = s_w              # float32 [N] (w4 only)
+        self.s_w = s_w              # float32 [N] (per-row formats)
         self.bias = bias            # float32 [N] or None
         self.canonical = canonical  # per-shard canonical tensors, if kept
 
@@ -46,7 +48,7 @@ class QuantLinear:
         canon, scales = [], []
         for W in shards:
             n = W.shape[0]
-            if fmt == "w8a32":
+            if fmt in ("w8a32", "w8"):
                 q = torch.empty((n, K), dtype=torch.int8, device=dev)
                 sw = torch.empty(n, dtype=torch.float32, device=dev)
                 _lib.w8_quantize_rows(W, q, sw)
@@ -75,7 +77,8 @@ class QuantLinear:
         return cls(fmt, N // 2 if glu_pairs else N, K, w, s_w, bias, canon if keep_canonical else None, glu_pairs)
 
     @classmethod
-    def from_canonical(cls, fmt: str, canon, K: int, scales=None, biases=None) -> "QuantLinear":
+    def from_canonical(cls, fmt: str, canon, K: int, scales=None, biases=None,
+                       keep_canonical: bool = True) -> "QuantLinear":
         """Repack already-quantized canonical shards (device tensors)."""
         grouped = fmt in ("i8g32", "q6g32")
         dev = (canon[0][0] if grouped else canon[0]).device
@@ -85,7 +88,7 @@ class QuantLinear:
         if biases is not None:
             bias = torch.empty(N, dtype=torch.float32, device=dev)
             _lib.w4_concat_f32([b.contiguous() for b in biases], bias)
-        return cls(fmt, N, K, w, s_w, bias, canon)
+        return cls(fmt, N, K, w, s_w, bias, canon if keep_canonical else None)
 
     @staticmethod
     def _repack(fmt, canon, scales, N, K, dev, glu_pairs=False):
@@ -106,7 +109,7 @@ class QuantLinear:
             _lib.w4_repack(canon, K, w)
             s_w = torch.empty(N, dtype=torch.float32, device=dev)
             _lib.w4_concat_f32(scales, s_w)
-        elif fmt == "w8a32":
+        elif fmt in ("w8a32", "w8"):
             w = torch.empty(_lib.w8_repacked_bytes(N, K), dtype=torch.uint8, device=dev)
             _lib.w8_repack(canon, K, w)
             s_w = torch.empty(N, dtype=torch.float32, device=dev)
@@ -123,17 +126,47 @@ class QuantLinear:
         return w, s_w
 
     # ------------------------------------------------------------ per token
-    def buffers(self, M: int):
+    def buffers(self, M: int, dtype=torch.float32):
+        """y, qx and sx for M tokens ("w8": y of `dtype`, and no qx, which its calls do not need)."""
         dev = self.w.device
+        if self.fmt == "w8":
+            return torch.empty((M, self.N), dtype=dtype, device=dev), None, torch.empty(M, device=dev)
+        if dtype != torch.float32:
+            raise ValueError(f"{self.fmt} outputs are float32")
         return (torch.empty((M, self.N), dtype=torch.float32, device=dev),
                 torch.empty((M, self.K), dtype=torch.int8, device=dev),
                 torch.empty(M, dtype=torch.float32, device=dev))
 
+    def workspace(self, M: int):
+        """Device memory that the calls of M tokens need ("w8" only; None for the others).  A caller that keeps it
+        passes it to its calls, which must then not overlap on the GPU."""
+        if self.fmt != "w8":
+            return None
+        return torch.empty(_lib.w8a8_workspace_bytes(M, self.N, self.K), dtype=torch.uint8, device=self.w.device)
+
+    def _call_w8(self, x, y, qx, sx, flags, stream, norm, eps, residual, workspace):
+        M, K = x.shape
+        if K != self.K:
+            raise ValueError(f"x has {K} columns, the linear takes {self.K}")
+        if y is None:
+            y = torch.empty((M, self.N), dtype=x.dtype if residual is None else torch.float32, device=x.device)
+        if sx is None:
+            sx = torch.empty(M, dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = self.workspace(M)
+        _lib.w8a8_linear(self.w, self.s_w, self.bias, x, y, qx, sx, workspace, norm, eps, residual, flags, stream)
+        return y
+
     def __call__(self, x, y=None, qx=None, sx=None, flags: int = 0, stream=None, norm=None, eps: float = 1e-6,
-                 glu: int = _lib.W4_GLU_NONE, residual=None):
+                 glu: int = _lib.W4_GLU_NONE, residual=None, workspace=None):
         """Quantize x [M][K] and compute y [M][N] (one fused launch when it fits).
         norm: RMSNorm weight [K] applied to x first (with eps); glu: W4_GLU_SILU or W4_GLU_GELU_TANH
-        (paired gate/up weights only); residual [M][N]: added to y last (may be y itself)."""
+        (paired gate/up weights only); residual [M][N]: added to y last (may be y itself); workspace: from
+        workspace(M) ("w8", any M and fp32, fp16 or bf16 x and y)."""
+        if self.fmt == "w8":
+            if glu != _lib.W4_GLU_NONE:
+                raise ValueError("glu is taken exactly by linears built with glu_pairs=True")
+            return self._call_w8(x, y, qx, sx, flags, stream, norm, eps, residual, workspace)
         M = x.shape[0]
         if y is None or qx is None or sx is None:
             y2, q2, s2 = self.buffers(M)
@@ -167,7 +200,9 @@ class QuantLinear:
 
     def gemv(self, qx, sx, y, stream=None):
         """GEMV on already-quantized activations."""
-        if self.fmt == "w4":
+        if self.fmt == "w8":
+            _lib.w8a8_matmul(self.w, self.s_w, self.bias, qx, sx, y, self.workspace(qx.shape[0]), stream)
+        elif self.fmt == "w4":
             _lib.w4a8_gemv(self.w, self.s_w, self.bias, qx, sx, y, stream)
         elif self.fmt == "q4_0":
             _lib.q4_0_gemv(self.w, self.bias, qx, sx, y, stream)

@@ -17,7 +17,8 @@
  *     W4_ERR_CUDA.  Kernels never trap: a bounded wait that runs out sets the
  *     device error word (see w4_device_error) and the kernel returns.
  *   - M = 0 or N = 0 is a valid empty call (returns W4_OK, launches nothing).
- *   - Shapes: 1 <= M <= 16 tokens, K > 0, K % 32 == 0.
+ *   - Shapes: 1 <= M <= 16 tokens (the INT8 x INT8 linear takes any number), K > 0,
+ *     K % 32 == 0.
  *   - Alignment: weight buffers, qx and x must be 16-byte aligned; float
  *     arrays 4-byte aligned.  A violation returns W4_ERR_MISALIGNED.
  *
@@ -425,6 +426,39 @@ w4_status w4a32_gemv(const void* w, const float* s_w, const float* bias, const f
                      float* y, unsigned flags, w4_stream_t s);
 w4_status w8a32_gemv(const void* w, const float* s_w, const float* bias, const float* x, int M, int N, int K,
                      float* y, unsigned flags, w4_stream_t s);
+
+/* ------------------------------------------------------------------------
+ * INT8 x INT8 linear with a scale for each token and each output channel, for
+ * any number of tokens (a prompt as well as a decode step):
+ *   acc[m][j] = sum_i q_w[j][i] * qx[m][i]   (exact int32),
+ *   y[m][j]   = fmaf(s_w[j] * sx[m], (float)acc[m][j], b[j]) (+ residual),
+ * rounded to y's type (to nearest even).  Weights: the per-row INT8 of
+ * w8_quantize_rows in the w8_repack layout (any int8, -128 included).
+ *   w8a8_matmul  takes codes and scales (as a8_quantize makes them);
+ *   w8a8_linear  quantizes x first, with f->norm_weight normalized as in the
+ *     *_linear_fused calls; the arithmetic of both is theirs, on x widened to
+ *     fp32.  qx: int8 [M][K] receives the codes, or NULL; sx: float [M]
+ *     receives the scales.
+ * x: [M][K] of x_type, 16-byte aligned; y: [M][N] of y_type; residual: float
+ * [M][N], added in fp32 before the rounding (it may be y itself where y is
+ * W4_F32).  x must not overlap y.  f may be NULL; a GLU is refused.
+ * 0 <= M <= W4_MAX_TOKENS, K % 32 == 0, any N.
+ * workspace: device memory of w8a8_workspace_bytes(M, N, K) bytes (2 K for each
+ * token and a few of padding), 16-byte aligned, with no contents to keep; calls that
+ * share one must not overlap on the GPU.  W4_FLAG_PDL as above: the weights
+ * are fetched before the dependency wait.
+ * Results do not depend on M: a token's row is the same in every batch.
+ * ------------------------------------------------------------------------ */
+#define W4_F32 0
+#define W4_F16 1
+#define W4_BF16 2
+#define W4_MAX_TOKENS (1 << 20)
+size_t w8a8_workspace_bytes(int M, int N, int K); /* 0 for a shape the calls refuse */
+w4_status w8a8_matmul(const void* w, const float* s_w, const float* bias, const int8_t* qx, const float* sx, int M,
+                      int N, int K, void* y, int y_type, void* workspace, size_t ws_bytes, w4_stream_t s);
+w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const void* x, int x_type, int M, int N,
+                      int K, void* y, int y_type, int8_t* qx, float* sx, const w4_fusion* f, unsigned flags,
+                      void* workspace, size_t ws_bytes, w4_stream_t s);
 
 /* ------------------------------------------------------------------------
  * A chain of per-row INT4 decode linears in one launch (a decode step's
