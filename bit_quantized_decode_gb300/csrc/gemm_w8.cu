@@ -17,8 +17,8 @@
 //     quantizer writes: a K group of eight of a token tile is one contiguous
 //     run, copied by a 1-D bulk copy into the core-matrix layout without
 //     swizzle.
-//   * Persistent blocks, one per SM: a copy warp, an MMA lane, eight
-//     converting warps (two groups on alternate 64-K stages) and eight
+//   * Persistent blocks, one per SM: a copy warp, an MMA warp, eight
+//     converting warps (two groups on alternate 128-K stages) and eight
 //     epilogue warps, joined by mbarriers only.
 //   * Few tiles: K is split over a thread-block cluster; the splits exchange
 //     their integer sums through distributed shared memory (split r owns the
@@ -35,10 +35,6 @@ namespace w4k {
 namespace {
 
 constexpr uint64_t kG8WaitNs = 250ull * 1000ull * 1000ull;
-constexpr uint32_t kG8Cols = 512;
-constexpr uint32_t kG8ColAcc = 0;                       // two accumulators
-constexpr uint32_t kG8ColA = 2 * kG8MaxTok;             // kG8ABufs converted stages of 32 columns
-static_assert(kG8ColA + 32 * kG8ABufs <= kG8Cols, "tensor-memory columns");
 constexpr int kWarpMma = 1, kWarpConv = 4, kWarpEpi = 12;
 
 // One kind::f16 MMA (A in tensor memory, B from a shared-memory descriptor).
@@ -50,6 +46,34 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// One lane of a converged warp.  The tensor-core and bulk-copy instructions
+// take uniform registers: under an elected lane the compiler issues them
+// once, where under "lane == 0" it loops over the lanes that might be active
+// (550 against some 60 cycles a stage).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Wait of a whole warp: a test first, as the phase is usually complete.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
+{
+    bool ok = mbar_test_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) ok = mbar_wait_bounded(bar, parity, kG8WaitNs);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// The same for two barriers of equal phase.
+__device__ __forceinline__ bool warp_wait2(uint32_t bar, uint32_t bar2, uint32_t parity)
+{
+    bool ok = mbar_test_wait(bar, parity) & mbar_test_wait(bar2, parity);
+    if (!__all_sync(0xffffffffu, ok))
+        ok = mbar_wait_bounded(bar, parity, kG8WaitNs) && mbar_wait_bounded(bar2, parity, kG8WaitNs);
+    return __all_sync(0xffffffffu, ok);
 }
 
 // Box of a 2-D tensor map -> shared memory.
@@ -70,19 +94,60 @@ __device__ __forceinline__ uint64_t l2_policy_evict_last()
     return p;
 }
 
+// Scales of a warp's tokens m + 32 b + i (b < 2, i < 16), token 16 b + i in lane 16 b + i.
+__device__ __forceinline__ float sx_of(const Gemm8Args& A, int m, int lane)
+{
+    m += lane + (lane & 16);
+    return m < A.M ? __ldg(A.sx + m) : 0.0f;
+}
+
+// Outputs of one weight row and the tokens m0 + 32 b + i (32 b < cols); clears acc.
+template <int YT>
+__device__ __forceinline__ void emit_tile(const Gemm8Args& A, int (&acc)[4][16], int m0, int cols, int row, float sw,
+                                          float bv, float sx0, float sx1)
+{
+    const bool have = row < A.N;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        if (32 * b < cols) {
+            const int mb = m0 + 32 * b;
+            const size_t at = static_cast<size_t>(mb) * A.N + row;
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float sx = __shfl_sync(0xffffffffu, b < 2 ? sx0 : sx1, 16 * (b & 1) + i);
+                v[i] = __fmaf_rn(__fmul_rn(sw, sx), __int2float_rn(acc[b][i]), bv);
+                acc[b][i] = 0;
+            }
+            if (A.residual != nullptr) {
+                // every residual before the first store: y may be the residual itself
+                float r[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    r[i] = have && mb + i < A.M ? A.residual[at + static_cast<size_t>(i) * A.N] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(r[i], v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (have && mb + i < A.M) store_typed(A.y, YT, at + static_cast<size_t>(i) * A.N, v[i]);
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_constant__ Gemm8Args A)
 {
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = A.stages, nt = A.nt, ks = A.splits;
     const Gemm8Smem L = gemm8_smem(S, nt, ks);
-    const int slot_bytes = kG8WBytes + nt * 128;
+    const int slot_bytes = kG8WBytes + nt * 64 * kG8StageChunks;
+    const uint32_t col_a = 2u * static_cast<uint32_t>(nt);        // two accumulators, then a converted stage per slot
     const uint32_t bars = smem_u32(smem + L.bars);
     const uint32_t full_b = bars;                                  // [S] stage landed
-    const uint32_t empty_b = full_b + 8 * kG8MaxStages;            // [S] four converting warps and the MMA commit
-    const uint32_t ready_b = empty_b + 8 * kG8MaxStages;           // [kG8ABufs] converted (four warps)
-    const uint32_t free_b = ready_b + 8 * kG8ABufs;                // [kG8ABufs] read by the MMAs
-    const uint32_t accf_b = free_b + 8 * kG8ABufs;                 // [2] accumulator complete
+    const uint32_t empty_b = full_b + 8 * kG8MaxStages;            // [S] slot and converted stage read: MMA commit
+    const uint32_t ready_b = empty_b + 8 * kG8MaxStages;           // [S] converted (four warps)
+    const uint32_t accf_b = ready_b + 8 * kG8MaxStages;            // [2] accumulator complete
     const uint32_t acce_b = accf_b + 16;                           // [2] accumulator read (eight warps)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L.tmem);
     volatile uint32_t* dead_s = tmem_slot + 1;
@@ -98,11 +163,8 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_b + 8 * s, 1);
-            mbar_init(empty_b + 8 * s, 5);
-        }
-        for (int j = 0; j < kG8ABufs; ++j) {
-            mbar_init(ready_b + 8 * j, 4);
-            mbar_init(free_b + 8 * j, 1);
+            mbar_init(empty_b + 8 * s, 1);
+            mbar_init(ready_b + 8 * s, 4);
         }
         for (int j = 0; j < 2; ++j) {
             mbar_init(accf_b + 8 * j, 1);
@@ -112,7 +174,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         *dead_s = 0u;
     }
     if (warp == kWarpMma) {
-        tmem_alloc(smem_u32(tmem_slot), kG8Cols);
+        tmem_alloc(smem_u32(tmem_slot), kG8TmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -129,47 +191,49 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
     if (warp == 0) {
         // ------------------------------------------------------- copy warp
         const uint64_t pol = l2_policy_evict_first(), pol_b = l2_policy_evict_last();
-        auto copy_w = [&](int tile, int st, int slot) {
-            if (lane == 0) {
+        auto copy_w = [&](int row_tile, int st, int slot) {
+            if (elect_one()) {
                 const uint32_t bar = full_b + 8 * slot;
                 const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
                 mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kG8WBytes + k8 * nt * 16));
-                // 16 row tiles x 64 K; tiles past T and chunks past C arrive as zeros
-                tma_load_2d(smem_u32(smem + L.ring + static_cast<size_t>(slot) * slot_bytes), &A.wmap,
-                            st * kG8StageChunks * 32, (tile / A.n_tt) * (kG8Rows / kRows), bar, pol);
+                // 16 row tiles x 128 K; tiles past T and chunks past C arrive as zeros
+                tma_load_2d(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes), &A.wmap,
+                            st * kG8StageChunks * 32, row_tile, bar, pol);
             }
         };
-        auto copy_b = [&](int tile, int st, int slot) {
-            if (lane == 0) {
+        auto copy_b = [&](const uint4* codes, int st, int slot) {
+            if (elect_one()) {
                 const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
-                const uint4* src = A.xh + (static_cast<size_t>(tile % A.n_tt) * (A.K >> 3) + st * kG8StageChunks * 4) * nt;
-                bulk_g2s(smem_u32(smem + L.ring + static_cast<size_t>(slot) * slot_bytes + kG8WBytes), src,
-                         static_cast<uint32_t>(k8 * nt * 16), full_b + 8 * slot, pol_b);
+                bulk_g2s(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
+                         codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt, static_cast<uint32_t>(k8 * nt * 16),
+                         full_b + 8 * slot, pol_b);
             }
         };
         // the first tile's weights do not depend on the previous kernel
         int ahead = 0;
         if (tile_first < ntiles)
-            for (; ahead < S && st0 + ahead < st1; ++ahead) copy_w(tile_first, st0 + ahead, ahead);
+            for (; ahead < S && st0 + ahead < st1; ++ahead)
+                copy_w((tile_first / A.n_tt) * (kG8Rows / kRows), st0 + ahead, ahead);
         pdl_wait();
         int it = 0, slot = 0;
         uint32_t ph = 1u;                // parity of the slot's previous release
         bool ok = true;
         for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
+            const int g = tile / A.n_tt;
+            const int row_tile = g * (kG8Rows / kRows);
+            const uint4* codes = A.xh + static_cast<size_t>(tile - g * A.n_tt) * (A.K >> 3) * nt;
             for (int st = st0; st < st1; ++st, ++it) {
                 if (it >= ahead) {
                     if (it >= S) {
-                        ok = mbar_wait_bounded(empty_b + 8 * slot, ph, kG8WaitNs);
-                        ok = __all_sync(0xffffffffu, ok);
+                        ok = warp_wait(empty_b + 8 * slot, ph);
                         if (!ok) {
                             if (lane == 0) fail();
                             break;
                         }
-                        if (lane == 0) fence_proxy_async_smem();
                     }
-                    copy_w(tile, st, slot);
+                    copy_w(row_tile, st, slot);
                 }
-                copy_b(tile, st, slot);
+                copy_b(codes, st, slot);
                 if (++slot == S) {
                     slot = 0;
                     ph ^= 1u;
@@ -181,52 +245,53 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
             if (!mbar_wait_bounded(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u, kG8WaitNs)) break;
         __syncwarp();
     } else if (warp == kWarpMma) {
-        // -------------------------------------------------------- MMA lane
-        if (lane == 0) {
-            const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(kG8Rows >> 4) << 24);
-            int it = 0, ac = 0, slot = 0;
-            uint32_t sph = 0u;
-            bool ok = true;
-            for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
-                for (int st = st0; st < st1; ++st, ++it) {
-                    const int k16 = 2 * min(kG8StageChunks, A.C - st * kG8StageChunks);
-                    const int j = it % kG8ABufs;
-                    const bool first = (st - st0) % kG8AccStages == 0;
-                    const uint32_t dcol = tbase + kG8ColAcc + static_cast<uint32_t>(ac & 1) * kG8MaxTok;
-                    if (first && ac >= 2) ok = mbar_wait_bounded(acce_b + 8 * (ac & 1), static_cast<uint32_t>((ac >> 1) - 1) & 1u, kG8WaitNs);
-                    ok = ok && mbar_wait_bounded(full_b + 8 * slot, sph, kG8WaitNs);
-                    ok = ok && mbar_wait_bounded(ready_b + 8 * j, static_cast<uint32_t>(it / kG8ABufs) & 1u, kG8WaitNs);
-                    if (!ok) {
-                        fail();
-                        break;
-                    }
-                    tc_fence_after();
-                    // core matrices of 8 tokens x 8 K (128 B): token groups 128 B apart, K groups nt * 16 B
-                    const uint64_t bdesc = smem_desc_noswizzle(
-                        smem_u32(smem + L.ring + static_cast<size_t>(slot) * slot_bytes + kG8WBytes),
-                        static_cast<uint32_t>(nt * 16), 128u);
-                    const uint32_t acol = tbase + kG8ColA + 32u * static_cast<uint32_t>(j);
+        // -------------------------------------------------------- MMA warp
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(kG8Rows >> 4) << 24);
+        int it = 0, ac = 0, slot = 0;
+        uint32_t sph = 0u;
+        bool ok = true;
+        for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
+            int run = 0;                 // stages in the current accumulator
+            for (int st = st0; st < st1; ++st, ++it) {
+                const int k16 = 2 * min(kG8StageChunks, A.C - st * kG8StageChunks);
+                const bool last = st + 1 == st1 || run == kG8AccStages - 1;
+                const uint32_t dcol = tbase + static_cast<uint32_t>((ac & 1) * nt);
+                if (run == 0 && ac >= 2) ok = warp_wait(acce_b + 8 * (ac & 1), static_cast<uint32_t>((ac >> 1) - 1) & 1u);
+                ok = ok && warp_wait2(full_b + 8 * slot, ready_b + 8 * slot, sph);
+                if (!ok) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                tc_fence_after();
+                // core matrices of 8 tokens x 8 K (128 B): token groups 128 B apart, K groups nt * 16 B
+                const uint64_t bdesc = smem_desc_noswizzle(
+                    smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
+                    static_cast<uint32_t>(nt * 16), 128u);
+                const uint32_t acol = tbase + col_a + static_cast<uint32_t>(kG8ACols * slot);
+                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
+                    for (int kk = 0; kk < 2 * kG8StageChunks; ++kk)
                         if (kk < k16)
                             tc_mma_f16_ts(dcol, acol + 8 * kk, bdesc + static_cast<uint64_t>(kk * 2 * nt), idesc,
-                                          first && kk == 0 ? 0u : 1u);
-                    tc_commit(free_b + 8 * j);
+                                          run == 0 && kk == 0 ? 0u : 1u);
                     tc_commit(empty_b + 8 * slot);
-                    if (st + 1 == st1 || (st - st0) % kG8AccStages == kG8AccStages - 1) {
-                        tc_commit(accf_b + 8 * (ac & 1));
-                        ++ac;
-                    }
-                    if (++slot == S) {
-                        slot = 0;
-                        sph ^= 1u;
-                    }
+                    if (last) tc_commit(accf_b + 8 * (ac & 1));
+                }
+                __syncwarp();
+                ++run;
+                if (last) {
+                    ++ac;
+                    run = 0;
+                }
+                if (++slot == S) {
+                    slot = 0;
+                    sph ^= 1u;
                 }
             }
-            // every MMA has completed before the tensor memory is freed
-            if (it > 0)
-                mbar_wait_bounded(free_b + 8 * ((it - 1) % kG8ABufs), static_cast<uint32_t>((it - 1) / kG8ABufs) & 1u, kG8WaitNs);
         }
+        // every MMA has completed before the tensor memory is freed
+        if (it > 0)
+            mbar_wait_bounded(empty_b + 8 * ((it - 1) % S), static_cast<uint32_t>((it - 1) / S) & 1u, kG8WaitNs);
         __syncwarp();
     } else if (warp >= kWarpConv && warp < kWarpEpi) {
         // ------------------------------------------------ converting warps
@@ -240,26 +305,22 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
             for (int st = st0; st < st1; ++st, ++it) {
                 if ((it & 1) == grp) {
+                    // the slot's refill follows the MMAs that read its last converted
+                    // stage, so a landed stage also has its tensor-memory columns free
                     const int nch = min(kG8StageChunks, A.C - st * kG8StageChunks);
-                    const int j = it % kG8ABufs;
-                    ok = mbar_wait_bounded(full_b + 8 * slot, sph, kG8WaitNs);
-                    ok = ok && (it < kG8ABufs ||
-                                mbar_wait_bounded(free_b + 8 * j, static_cast<uint32_t>(it / kG8ABufs - 1) & 1u, kG8WaitNs));
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = warp_wait(full_b + 8 * slot, sph);
                     if (!ok) {
                         if (lane == 0) fail();
                         break;
                     }
-                    const uint8_t* u = smem + L.ring + static_cast<size_t>(slot) * slot_bytes + (row >> 3) * 512 + (row & 7) * 32;
+                    tc_fence_after();
+                    const uint8_t* u = smem + L.ring + slot * slot_bytes + (row >> 3) * (256 * kG8StageChunks) + (row & 7) * 32;
                     uint4 a[kG8StageChunks], b[kG8StageChunks];
 #pragma unroll
                     for (int e = 0; e < kG8StageChunks; ++e) {
                         a[e] = *reinterpret_cast<const uint4*>(u + e * 256 + (hsel << 4));
                         b[e] = *reinterpret_cast<const uint4*>(u + e * 256 + ((hsel ^ 1) << 4));
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(empty_b + 8 * slot);
-                    tc_fence_after();
 #pragma unroll
                     for (int e = 0; e < kG8StageChunks; ++e) {
                         if (e < nch) {
@@ -273,13 +334,15 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                             i8_to_f16(hi.y, h[10], h[11]);
                             i8_to_f16(hi.z, h[12], h[13]);
                             i8_to_f16(hi.w, h[14], h[15]);
-                            tmem_st16(tbase + tlane + kG8ColA + 32u * static_cast<uint32_t>(j) + 16u * e, h);
+                            tmem_st16(tbase + tlane + col_a + static_cast<uint32_t>(kG8ACols * slot + 16 * e), h);
                         }
                     }
+                    // (the reads of the slot are ordered before the copy that refills it)
+                    fence_proxy_async_smem();
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(ready_b + 8 * j);
+                    if (lane == 0) mbar_arrive(ready_b + 8 * slot);
                 }
                 if (++slot == S) {
                     slot = 0;
@@ -300,12 +363,12 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         bool ok = true;
         pdl_wait();
         for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
-            const int row = (tile / A.n_tt) * kG8Rows + (warp & 3) * 32 + lane;
+            const int g = tile / A.n_tt;
+            const int row = g * kG8Rows + (warp & 3) * 32 + lane;
             const float sw = row < A.N ? __ldg(A.s_w + row) : 0.0f;
             const float bv = row < A.N && A.bias != nullptr ? __ldg(A.bias + row) : 0.0f;
             for (int st = st0; st < st1; st += kG8AccStages, ++ac) {
-                ok = mbar_wait_bounded(accf_b + 8 * (ac & 1), static_cast<uint32_t>(ac >> 1) & 1u, kG8WaitNs);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait(accf_b + 8 * (ac & 1), static_cast<uint32_t>(ac >> 1) & 1u);
                 if (!ok) {
                     if (lane == 0) fail();
                     break;
@@ -315,7 +378,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 for (int b = 0; b < 4; ++b) {
                     if (32 * b + 16 * half < nt) {
                         uint32_t d[16];
-                        tmem_ld16(tbase + tlane + kG8ColAcc + static_cast<uint32_t>((ac & 1) * kG8MaxTok + 32 * b + 16 * half), d);
+                        tmem_ld16(tbase + tlane + static_cast<uint32_t>((ac & 1) * nt + 32 * b + 16 * half), d);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) acc[b][i] += __float2int_rn(__uint_as_float(d[i]));
                     }
@@ -325,23 +388,11 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(acce_b + 8 * (ac & 1));
             }
             if (ks > 1 || !ok) break;
-            const int m0 = (tile % A.n_tt) * nt;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (32 * b + 16 * half < nt) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int m = m0 + 32 * b + 16 * half + i;
-                        if (m < A.M && row < A.N) {
-                            float v = __fmaf_rn(__fmul_rn(sw, __ldg(A.sx + m)), __int2float_rn(acc[b][i]), bv);
-                            const size_t o = static_cast<size_t>(m) * A.N + row;
-                            if (A.residual != nullptr) v = __fadd_rn(A.residual[o], v);
-                            store_typed(A.y, A.ytype, o, v);
-                        }
-                        acc[b][i] = 0;
-                    }
-                }
-            }
+            const int m0 = (tile - g * A.n_tt) * nt + 16 * half;
+            const float sx0 = sx_of(A, m0, lane), sx1 = sx_of(A, m0 + 64, lane);
+            if (A.ytype == T_F32) emit_tile<T_F32>(A, acc, m0, nt - 16 * half, row, sw, bv, sx0, sx1);
+            else if (A.ytype == T_F16) emit_tile<T_F16>(A, acc, m0, nt - 16 * half, row, sw, bv, sx0, sx1);
+            else emit_tile<T_BF16>(A, acc, m0, nt - 16 * half, row, sw, bv, sx0, sx1);
         }
         if (ks > 1) {
             // token column c of the tile belongs to split c % ks: its sums go there
@@ -390,7 +441,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
     __syncthreads();
     if (warp == kWarpMma) {
         tc_fence_after();
-        tmem_dealloc(tbase, kG8Cols);
+        tmem_dealloc(tbase, kG8TmemCols);
     }
 }
 

@@ -48,11 +48,12 @@ cudaError_t launch_expand_codes(const int8_t* qx, int M, int K, uint4* xh, int n
 // ------------------------------------------- INT8 x INT8 product (gemm_w8.cu)
 constexpr int kG8Rows = 128;                    // weight rows per tile (MMA M)
 constexpr int kG8MaxTok = 128;                  // tokens per tile at most (MMA N)
-constexpr int kG8StageChunks = 2;               // 32-weight chunks per stage: 64 K
+constexpr int kG8StageChunks = 4;               // 32-weight chunks per stage: 128 K
 constexpr int kG8WBytes = kG8Rows * 32 * kG8StageChunks;
-constexpr int kG8ABufs = 8;                     // converted weight stages in tensor memory
-constexpr int kG8AccStages = 16;                // stages per accumulator: 1024 K keep the fp32 sums exact
-constexpr int kG8MaxStages = 16;
+constexpr int kG8AccStages = 8;                 // stages per accumulator: 1024 K keep the fp32 sums exact
+constexpr int kG8TmemCols = 512;
+constexpr int kG8ACols = 16 * kG8StageChunks;   // tensor-memory columns of one converted stage
+constexpr int kG8MaxStages = 7;
 constexpr int kG8MaxSplit = 8;
 constexpr int kG8Threads = 640;
 
@@ -70,21 +71,22 @@ struct Gemm8Args {
     int nt;                   // tokens per tile (a multiple of 16)
     int n_tt, n_g;            // token tiles, row groups
     int splits;               // K splits per tile = cluster size (1: persistent blocks)
-    int stages;
+    int stages;               // ring slots in shared memory and converted stages in tensor memory
     unsigned* err;
 };
 
 struct Gemm8Smem {
-    int ring, red, bars, tmem, sx, total;
+    int ring, red, bars, tmem, total;
 };
+// Stages that tensor memory holds beside two accumulators of nt columns.
+__host__ __device__ inline int gemm8_max_stages(int nt) { return (kG8TmemCols - 2 * nt) / kG8ACols; }
 __host__ __device__ inline Gemm8Smem gemm8_smem(int stages, int nt, int splits)
 {
     Gemm8Smem L;
     int o = 0;
-    L.ring = o;  o += stages * (kG8WBytes + nt * 128);
+    L.ring = o;  o += stages * (kG8WBytes + nt * 64 * kG8StageChunks);
     L.red = o;   o += splits > 1 ? kG8Rows * nt * 4 : 0;
-    L.sx = o;    o += 2 * kG8MaxTok * 4;
-    L.bars = o;  o += (2 * kG8MaxStages + 2 * kG8ABufs + 4) * 8;
+    L.bars = o;  o += (3 * kG8MaxStages + 4) * 8;
     L.tmem = o;  o += 16;
     L.total = o;
     return L;

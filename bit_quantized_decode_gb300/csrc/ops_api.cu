@@ -45,8 +45,8 @@ bool plan_gemm8(const DeviceFacts& d, Gemm8Args& a, int& grid, size_t& smem)
     const int tiles = a.n_g * a.n_tt;
     const int nst = (a.C + kG8StageChunks - 1) / kG8StageChunks;
     a.splits = 1;
-    while (a.splits < kG8MaxSplit && tiles * 2 * a.splits <= d.sms && nst >= 8 * a.splits) a.splits *= 2;
-    a.stages = kG8MaxStages;
+    while (a.splits < kG8MaxSplit && tiles * 2 * a.splits <= d.sms && nst >= 4 * a.splits) a.splits *= 2;
+    a.stages = gemm8_max_stages(a.nt) < kG8MaxStages ? gemm8_max_stages(a.nt) : kG8MaxStages;
     while (a.stages > 2 && gemm8_smem(a.stages, a.nt, a.splits).total > d.smem_optin) --a.stages;
     smem = static_cast<size_t>(gemm8_smem(a.stages, a.nt, a.splits).total);
     grid = a.splits > 1 ? tiles * a.splits : (tiles < d.sms ? tiles : d.sms);
