@@ -141,6 +141,31 @@ SIGNATURES["w4_selftest_wait_timeout"] = ([_I, ctypes.c_uint, _P], _I)
 SIGNATURES["w8a8_workspace_bytes"] = ([_I, _I, _I], _SZ)
 SIGNATURES["w8a8_matmul"] = ([_P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _P, _SZ, _P], _I)
 SIGNATURES["w8a8_linear"] = ([_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _PF, _U, _P, _SZ, _P], _I)
+class Router(ctypes.Structure):
+    """w4_router of include/w4a8.h."""
+    _fields_ = [("norm_weight", _P), ("norm_eps", _F), ("w", _P), ("select_bias", _P), ("E", _I), ("top_k", _I),
+                ("score", _I), ("renormalize", _I), ("scale", _F)]
+
+
+class Experts(ctypes.Structure):
+    """w4_experts of include/w4a8.h."""
+    _fields_ = [("fmt", _I), ("E", _I), ("n_shared", _I), ("H", _I), ("I", _I), ("glu", _I), ("w_gu", _P),
+                ("s_gu", _P), ("b_gu", _P), ("w_dn", _P), ("s_dn", _P), ("b_dn", _P)]
+
+
+_PR = ctypes.POINTER(Router)
+_PE = ctypes.POINTER(Experts)
+SIGNATURES["w8_glu_repacked_bytes"] = ([_I, _I], _SZ)
+SIGNATURES["w8_repack_glu"] = ([_P, _P, _I, _I, _P, _SZ, _P], _I)
+SIGNATURES["w4_moe_route"] = ([_PR, _P, _I, _I, _I, _P, _P, _P, _P, _U, _P], _I)
+SIGNATURES["w4_moe_workspace_bytes"] = ([_PE, _I, _I], _SZ)
+SIGNATURES["w4_moe_experts"] = ([_PE, _P, _P, _P, _P, _I, _I, _P, _P, _I, _P, _SZ, _U, _P], _I)
+SIGNATURES["w4_moe_layer"] = ([_PR, _PE, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P, _SZ, _U, _P], _I)
+EXPERT_FORMATS = {"w4": 0, "w8": 5}                    # W4_FMT_W4, W4_FMT_W8
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+W4_MAX_TOP_K = 16
+W4_MAX_EXPERTS = 1024
+W4_MAX_SHARED = 4
 ELEM_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # W4_F32, W4_F16, W4_BF16
 W4_MAX_TOKENS = 1 << 20
 W4_MAX_CHAIN = 128
@@ -647,6 +672,88 @@ def w8a8_linear(w, s_w, bias, x, y, qx, sx, workspace, norm=None, eps: float = 0
     _check("w8a8_linear", load().w8a8_linear(_ptr(w), _ptr(s_w), _ptr(bias), _ptr(x), ELEM_TYPES[x.dtype], M, N, K,
                                              _ptr(y), ELEM_TYPES[y.dtype], _ptr(qx), _ptr(sx), fz, flags,
                                              _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+# ------------------------------------------------- mixture of experts, few tokens
+def w8_glu_repacked_bytes(I: int, K: int) -> int:
+    return int(load().w8_glu_repacked_bytes(I, K))
+
+
+def w8_repack_glu(gate, up, K, out, stream=None):
+    """int8 codes of gate and up [I][K] -> the paired device layout (the experts of w4_moe_experts)."""
+    _check_tensors(gate=(gate, _I8, None), up=(up, _I8, gate.shape), out=(out, _U8, None))
+    _check("w8_repack_glu", load().w8_repack_glu(_ptr(gate), _ptr(up), gate.shape[0], K, _ptr(out), out.numel(),
+                                                 _stream(stream)))
+
+
+_I32 = (torch.int32,)
+
+
+def moe_router(w, top_k: int, select_bias=None, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+               norm=None, eps: float = 1e-6):
+    """A w4_router descriptor: w float32 [E][K].  It holds references to its tensors."""
+    E, K = w.shape
+    _check_tensors(w=(w, _F32, None), select_bias=(select_bias, _F32, (E,)), norm=(norm, _F32, (K,)))
+    r = Router(None if norm is None else norm.data_ptr(), float(eps), w.data_ptr(),
+               None if select_bias is None else select_bias.data_ptr(), E, int(top_k), ROUTE_SCORES[score],
+               int(bool(renormalize)), float(scale))
+    r._tensors, r._K = (w, select_bias, norm), K
+    return r
+
+
+def moe_experts(fmt: str, w_gu, s_gu, w_dn, s_dn, E: int, n_shared: int, H: int, I: int, glu: int, b_gu=None, b_dn=None):
+    """A w4_experts descriptor over the repacked weights of E + n_shared experts.  It holds references to its tensors."""
+    n = E + n_shared
+    gu_bytes, dn_bytes = ((w4_glu_repacked_bytes(I, H), w4_repacked_bytes(H, I)) if fmt == "w4"
+                          else (w8_glu_repacked_bytes(I, H), w8_repacked_bytes(H, I)))
+    _check_tensors(w_gu=(w_gu, _U8, (n * gu_bytes,)), s_gu=(s_gu, _F32, (n, 2 * I)), b_gu=(b_gu, _F32, (n, 2 * I)),
+                   w_dn=(w_dn, _U8, (n * dn_bytes,)), s_dn=(s_dn, _F32, (n, H)), b_dn=(b_dn, _F32, (n, H)))
+    e = Experts(EXPERT_FORMATS[fmt], E, n_shared, H, I, glu, w_gu.data_ptr(), s_gu.data_ptr(),
+                None if b_gu is None else b_gu.data_ptr(), w_dn.data_ptr(), s_dn.data_ptr(),
+                None if b_dn is None else b_dn.data_ptr())
+    e._tensors = (w_gu, s_gu, b_gu, w_dn, s_dn, b_dn)
+    return e
+
+
+def w4_moe_route(router, x, ids, weights, qx=None, sx=None, flags: int = 0, stream=None):
+    """ids int32 [M][top_k] and weights float32 [M][top_k] of x [M][K]; qx int8 [M][K] and sx float32 [M] receive the
+    (normalized) tokens' codes and scales, or are both None."""
+    M, K = x.shape
+    if K != router._K:
+        raise ValueError(f"x has {K} columns, the router takes {router._K}")
+    _check_tensors(x=(x, _FLOATS, None), ids=(ids, _I32, (M, router.top_k)), weights=(weights, _F32, (M, router.top_k)),
+                   qx=(qx, _I8, (M, K)), sx=(sx, _F32, (M,)))
+    _check("w4_moe_route", load().w4_moe_route(ctypes.byref(router), _ptr(x), ELEM_TYPES[x.dtype], M, K, _ptr(ids),
+                                               _ptr(weights), _ptr(qx), _ptr(sx), flags, _stream(stream)))
+
+
+def w4_moe_workspace_bytes(experts, M: int, top_k: int) -> int:
+    return int(load().w4_moe_workspace_bytes(ctypes.byref(experts), M, top_k))
+
+
+def w4_moe_experts(experts, qx, sx, ids, weights, y, workspace, residual=None, flags: int = 0, stream=None):
+    """y [M][H] of the experts ids [M][top_k] with weights, on codes qx [M][H], sx [M]."""
+    M, top_k = ids.shape
+    H = experts.H
+    _check_tensors(qx=(qx, _I8, (M, H)), sx=(sx, _F32, (M,)), ids=(ids, _I32, None), weights=(weights, _F32, (M, top_k)),
+                   y=(y, _FLOATS, (M, H)), workspace=(workspace, _U8, None), residual=(residual, _F32, (M, H)))
+    _check("w4_moe_experts", load().w4_moe_experts(ctypes.byref(experts), _ptr(qx), _ptr(sx), _ptr(ids), _ptr(weights), M,
+                                                   top_k, _ptr(residual), _ptr(y), ELEM_TYPES[y.dtype], _ptr(workspace),
+                                                   workspace.numel(), flags, _stream(stream)))
+
+
+def w4_moe_layer(router, experts, x, ids, weights, qx, sx, y, workspace, residual=None, flags: int = 0, stream=None):
+    """w4_moe_route on x [M][H], then w4_moe_experts on its choice, in two launches."""
+    M, H = x.shape
+    if H != router._K or H != experts.H:
+        raise ValueError(f"x has {H} columns, the router takes {router._K}, the experts {experts.H}")
+    _check_tensors(x=(x, _FLOATS, None), ids=(ids, _I32, (M, router.top_k)), weights=(weights, _F32, (M, router.top_k)),
+                   qx=(qx, _I8, (M, H)), sx=(sx, _F32, (M,)), y=(y, _FLOATS, (M, H)), workspace=(workspace, _U8, None),
+                   residual=(residual, _F32, (M, H)))
+    _check("w4_moe_layer", load().w4_moe_layer(ctypes.byref(router), ctypes.byref(experts), _ptr(x), ELEM_TYPES[x.dtype], M,
+                                               _ptr(ids), _ptr(weights), _ptr(qx), _ptr(sx), _ptr(residual), _ptr(y),
+                                               ELEM_TYPES[y.dtype], _ptr(workspace), workspace.numel(), flags,
+                                               _stream(stream)))
 
 
 # ---------------------------------------------------------------- chains

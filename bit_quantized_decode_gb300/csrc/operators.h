@@ -93,4 +93,77 @@ __host__ __device__ inline Gemm8Smem gemm8_smem(int stages, int nt, int splits)
 }
 cudaError_t launch_gemm_w8(Gemm8Args& a, int grid, size_t smem, bool pdl, cudaStream_t s);
 
+// ------------------------------------------------ expert router (moe_route.cu)
+constexpr int kRtThreads = 512;
+constexpr int kRtWarps = kRtThreads / 32;
+constexpr int kRtMaxTok = 4;                    // tokens per cluster at most
+constexpr int kRtMaxCluster = 16;
+
+struct RouteArgs {
+    const void* x;            // [M][K] of xtype
+    const float* gamma;       // RMSNorm weight, or null
+    float eps;
+    const float* w;           // [E][K]
+    const float* sel;         // [E] selection bias (sigmoid), or null
+    int E, top_k;
+    int sigmoid;              // scores: 0 softmax, 1 sigmoid
+    int renorm;
+    float scale;
+    int M, K;
+    int tok;                  // tokens per cluster
+    int cluster;
+    int parts;                // warps per expert
+    int* ids;                 // [M][top_k]
+    float* weights;           // [M][top_k]
+    int8_t* qx;               // [M][K] codes of the (normalized) tokens, or null
+    float* sx;                // [M], or null
+    unsigned* zero;           // words cleared for the experts kernel, or null
+    int n_zero;
+};
+// x as fp32, the partial sums of an expert's warps, the logits (cluster leader), block sums.
+__host__ __device__ inline int route_smem(int tok, int K, int E)
+{
+    return 4 * (tok * K + kRtWarps * kRtMaxTok * 2 + tok * ((E + 3) & ~3) + 2 * kRtWarps * kRtMaxTok);
+}
+cudaError_t launch_moe_route(const RouteArgs& a, int xtype, bool pdl, cudaStream_t s);
+
+// ------------------------------------------ mixture-of-experts kernel (moe_experts.cu)
+constexpr int kMxThreads = 512;
+constexpr int kMxWarps = kMxThreads / 32;
+constexpr int kMxLines = 16;                    // lines (8 rows x 32 weights) per ring slot: one pass of a warp
+constexpr int kMxTok = 8;                       // pairs of one entry (an expert and up to eight of its tokens)
+constexpr int kMxMaxSlots = 20;                 // chosen and shared experts per token
+constexpr int kMxMaxPairs = 16 * kMxMaxSlots;
+constexpr int kMxMaxExperts = 1024;             // routed and shared
+constexpr int kMxSeg = 512;                     // hidden values per quantizing task
+
+struct MoeArgs {
+    const uint8_t* w_gu;      // per expert: gate and up rows paired per tile (w4_repack_glu / w8_repack_glu)
+    const uint8_t* w_dn;      // per expert: w4_repack / w8_repack
+    const float* s_gu;        // [E + S][2 I]
+    const float* b_gu;        // [E + S][2 I] or null
+    const float* s_dn;        // [E + S][H]
+    const float* b_dn;        // [E + S][H] or null
+    const int8_t* qx;         // [M][H]
+    const float* sx;          // [M]
+    const int* ids;           // [M][top_k]
+    const float* weights;     // [M][top_k]
+    const float* residual;    // [M][H] or null
+    void* y;                  // [M][H] of ytype
+    int ytype, glu;
+    int M, H, I, E, S, top_k;
+    int stages;               // ring slots per warp
+    unsigned* ctrl;           // moe_ctrl_words, zero at the start
+    float* h;                 // [pairs][I]
+    int8_t* qh;               // [pairs][I]
+    float* part;              // [pairs][H]
+    unsigned* err;
+};
+// Control words: ticket; per pair: hidden maximum, code sum; per entry: gate/up
+// tiles done, quantizing tasks done; per 8-row output tile: entries done.
+__host__ __device__ inline int moe_ctrl_words(int pairs, int H) { return 4 + 4 * pairs + (H + 7) / 8; }
+cudaError_t launch_moe_experts(int fmt, const MoeArgs& a, int grid, size_t smem, bool pdl, cudaStream_t s);
+size_t moe_experts_smem(int fmt, int stages);
+cudaError_t launch_zero_words(unsigned* p, int n, bool pdl, cudaStream_t s);
+
 }  // namespace w4k

@@ -1,5 +1,5 @@
-// C ABI of the INT8 x INT8 linear (declared in include/w4a8.h): argument
-// checks, launch plan and dispatch.  No entry point allocates memory or
+// C ABI of the INT8 x INT8 linear and the mixture-of-experts layer (declared
+// in include/w4a8.h): argument checks, launch plan and dispatch.  No entry point allocates memory or
 // synchronises.
 #include <cuda_runtime.h>
 
@@ -10,6 +10,8 @@
 
 using namespace w4k;
 
+static_assert(W4_FMT_W8 == FMT_W8F && W4_FMT_W4 == FMT_W4, "public format codes");
+static_assert(W4_MAX_EXPERTS == kMxMaxExperts && W4_MAX_TOP_K + W4_MAX_SHARED == kMxMaxSlots, "public limits");
 static_assert(W4_F32 == T_F32 && W4_F16 == T_F16 && W4_BF16 == T_BF16, "public element types");
 
 namespace {
@@ -86,6 +88,155 @@ w4_status check_w8_operands(const void* w, const float* s_w, const float* bias, 
     return W4_OK;
 }
 
+// ------------------------------------------------------ mixture of experts
+w4_status check_router(const w4_router* r, int M, int K)
+{
+    if (!r || M < 0 || K <= 0) return W4_ERR_INVALID_ARG;
+    if (r->E < 1 || r->top_k < 1 || (r->score != W4_ROUTE_SOFTMAX && r->score != W4_ROUTE_SIGMOID)) return W4_ERR_INVALID_ARG;
+    if (r->select_bias != nullptr && r->score != W4_ROUTE_SIGMOID) return W4_ERR_INVALID_ARG;
+    if (r->norm_weight != nullptr && (!(r->norm_eps > 0.0f) || !(r->norm_eps < 3.0e38f))) return W4_ERR_INVALID_ARG;
+    if (r->top_k > r->E) return W4_ERR_INVALID_ARG;
+    if (r->E > W4_MAX_EXPERTS || r->top_k > W4_MAX_TOP_K || M > W4_MAX_M || K % 32 != 0 || K > W4_MAX_K)
+        return W4_ERR_UNSUPPORTED_SHAPE;
+    return W4_OK;
+}
+
+// Tokens per cluster (as many as fit, up to four), blocks per cluster and
+// warps per expert: up to 16 blocks, so that the logits of a token spread over
+// as many warps as one cluster has.
+bool plan_route(const DeviceFacts& d, RouteArgs& a)
+{
+    a.tok = a.M >= 3 ? 4 : a.M >= 2 ? 2 : 1;
+    while (a.tok > 1 && route_smem(a.tok, a.K, a.E) > d.smem_optin) a.tok /= 2;
+    if (route_smem(a.tok, a.K, a.E) > d.smem_optin) return false;
+    a.cluster = 1;
+    while (a.cluster < kRtMaxCluster && 2 * a.cluster <= a.E) a.cluster *= 2;
+    a.parts = 1;
+    while (a.parts < kRtWarps && kRtWarps / (2 * a.parts) * a.cluster >= a.E) a.parts *= 2;
+    return true;
+}
+
+w4_status run_route(const w4_router* r, const void* x, int x_type, int M, int K, int* ids, float* weights, int8_t* qx,
+                    float* sx, unsigned* zero, int n_zero, bool pdl, cudaStream_t s)
+{
+    DeviceFacts d;
+    if (!device_facts(&d)) return W4_ERR_CUDA;
+    RouteArgs a = {};
+    a.x = x;
+    a.gamma = r->norm_weight;
+    a.eps = r->norm_weight != nullptr ? r->norm_eps : 0.0f;
+    a.w = r->w;
+    a.sel = r->select_bias;
+    a.E = r->E;
+    a.top_k = r->top_k;
+    a.sigmoid = r->score == W4_ROUTE_SIGMOID;
+    a.renorm = r->renormalize != 0;
+    a.scale = r->scale;
+    a.M = M;
+    a.K = K;
+    a.ids = ids;
+    a.weights = weights;
+    a.qx = qx;
+    a.sx = sx;
+    a.zero = zero;
+    a.n_zero = n_zero;
+    if (!plan_route(d, a)) return W4_ERR_UNSUPPORTED_SHAPE;
+    return cuda_status(launch_moe_route(a, x_type, pdl, s));
+}
+
+// Pointers of a router call (after check_router).
+w4_status check_route_pointers(const w4_router* r, const void* x, const int* ids, const float* weights,
+                               const int8_t* qx, const float* sx)
+{
+    if (!r->w || !x || !ids || !weights || (qx == nullptr) != (sx == nullptr)) return W4_ERR_INVALID_ARG;
+    if (!aligned(r->w, 16) || !aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || (qx && !aligned(qx, 16)) ||
+        (sx && !aligned(sx, 4)) || (r->norm_weight && !aligned(r->norm_weight, 16)) ||
+        (r->select_bias && !aligned(r->select_bias, 4)))
+        return W4_ERR_MISALIGNED;
+    return W4_OK;
+}
+
+w4_status check_experts(const w4_experts* e, int M, int top_k)
+{
+    if (!e || M < 0 || top_k < 1 || e->E < 1 || e->n_shared < 0 || e->H <= 0 || e->I <= 0) return W4_ERR_INVALID_ARG;
+    if (e->fmt != W4_FMT_W4 && e->fmt != W4_FMT_W8) return W4_ERR_INVALID_ARG;
+    if (e->glu != W4_GLU_SILU && e->glu != W4_GLU_GELU_TANH) return W4_ERR_INVALID_ARG;
+    if (M > W4_MAX_M || top_k > W4_MAX_TOP_K || e->n_shared > W4_MAX_SHARED || e->E > W4_MAX_EXPERTS - e->n_shared ||
+        e->H % 32 != 0 || e->I % 32 != 0 || e->H > W4_MAX_K || e->I > W4_MAX_K)
+        return W4_ERR_UNSUPPORTED_SHAPE;
+    return W4_OK;
+}
+
+w4_status check_expert_pointers(const w4_experts* e, const float* residual, const void* y, int y_type)
+{
+    if (!e->w_gu || !e->s_gu || !e->w_dn || !e->s_dn || !y) return W4_ERR_INVALID_ARG;
+    if (!aligned(e->w_gu, 16) || !aligned(e->w_dn, 16) || !aligned(e->s_gu, 4) || !aligned(e->s_dn, 4) ||
+        (e->b_gu && !aligned(e->b_gu, 4)) || (e->b_dn && !aligned(e->b_dn, 4)) || (residual && !aligned(residual, 4)) ||
+        !aligned(y, static_cast<size_t>(elem_bytes(y_type))))
+        return W4_ERR_MISALIGNED;
+    return W4_OK;
+}
+
+// Parts of the workspace: control words, h, the codes of h, the slots' outputs.
+struct MoeSpace {
+    size_t h, qh, part, total;
+    int words;
+};
+MoeSpace moe_space(const w4_experts* e, int M, int top_k)
+{
+    const size_t P = static_cast<size_t>(M) * (top_k + e->n_shared);
+    MoeSpace w;
+    w.words = moe_ctrl_words(static_cast<int>(P), e->H);
+    w.h = (static_cast<size_t>(w.words) * 4 + 255) & ~static_cast<size_t>(255);
+    w.qh = w.h + P * e->I * 4;
+    w.part = w.qh + P * e->I;
+    w.total = w.part + P * e->H * 4;
+    return w;
+}
+
+w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, const int* ids, const float* weights, int M,
+                      int top_k, const float* residual, void* y, int y_type, void* ws, cudaStream_t s)
+{
+    DeviceFacts d;
+    if (!device_facts(&d)) return W4_ERR_CUDA;
+    const MoeSpace w = moe_space(e, M, top_k);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    MoeArgs a = {};
+    a.w_gu = static_cast<const uint8_t*>(e->w_gu);
+    a.w_dn = static_cast<const uint8_t*>(e->w_dn);
+    a.s_gu = e->s_gu;
+    a.b_gu = e->b_gu;
+    a.s_dn = e->s_dn;
+    a.b_dn = e->b_dn;
+    a.qx = qx;
+    a.sx = sx;
+    a.ids = ids;
+    a.weights = weights;
+    a.residual = residual;
+    a.y = y;
+    a.ytype = y_type;
+    a.glu = e->glu;
+    a.M = M;
+    a.H = e->H;
+    a.I = e->I;
+    a.E = e->E;
+    a.S = e->n_shared;
+    a.top_k = top_k;
+    a.ctrl = reinterpret_cast<unsigned*>(base);
+    a.h = reinterpret_cast<float*>(base + w.h);
+    a.qh = reinterpret_cast<int8_t*>(base + w.qh);
+    a.part = reinterpret_cast<float*>(base + w.part);
+    a.err = d.err;
+    // about 160 KB of weights in flight per SM (192 KB of INT8), the rest L1 for the codes
+    a.stages = e->fmt == W4_FMT_W4 ? 5 : 3;
+    const size_t smem = moe_experts_smem(e->fmt, a.stages);
+    if (smem > static_cast<size_t>(d.smem_optin)) return W4_ERR_UNSUPPORTED_SHAPE;
+    const long long work = static_cast<long long>(M) * (top_k + e->n_shared) * (e->I / 4 + e->H / 8);
+    const long long blocks = (work + kMxWarps - 1) / kMxWarps;
+    const int grid = blocks < d.sms ? static_cast<int>(blocks) : d.sms;
+    return cuda_status(launch_moe_experts(e->fmt, a, grid, smem, true, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -147,6 +298,66 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
     r = cuda_status(launch_quant_rows(q, x_type, (flags & W4_FLAG_PDL) != 0, s));
     if (r != W4_OK || N == 0) return r;
     return run_gemm8(w, s_w, bias, q.xh, sx, residual, M, N, K, y, y_type, s);
+}
+
+w4_status w4_moe_route(const w4_router* r, const void* x, int x_type, int M, int K, int* ids, float* weights,
+                       int8_t* qx, float* sx, unsigned flags, w4_stream_t s)
+{
+    w4_status st = check_router(r, M, K);
+    if (st != W4_OK) return st;
+    if (!elem_type(x_type) || (flags & ~W4_FLAG_PDL) != 0) return W4_ERR_INVALID_ARG;
+    if (M == 0) return W4_OK;
+    st = check_route_pointers(r, x, ids, weights, qx, sx);
+    if (st != W4_OK) return st;
+    return run_route(r, x, x_type, M, K, ids, weights, qx, sx, nullptr, 0, (flags & W4_FLAG_PDL) != 0,
+                     reinterpret_cast<cudaStream_t>(s));
+}
+
+size_t w4_moe_workspace_bytes(const w4_experts* e, int M, int top_k)
+{
+    if (check_experts(e, M, top_k) != W4_OK || M == 0) return 0;
+    return moe_space(e, M, top_k).total;
+}
+
+w4_status w4_moe_experts(const w4_experts* e, const int8_t* qx, const float* sx, const int* ids,
+                         const float* weights, int M, int top_k, const float* residual, void* y, int y_type,
+                         void* workspace, size_t ws_bytes, unsigned flags, w4_stream_t st)
+{
+    w4_status r = check_experts(e, M, top_k);
+    if (r != W4_OK) return r;
+    if (!elem_type(y_type) || (flags & ~W4_FLAG_PDL) != 0) return W4_ERR_INVALID_ARG;
+    if (M == 0) return W4_OK;
+    r = check_expert_pointers(e, residual, y, y_type);
+    if (r == W4_ERR_INVALID_ARG || !qx || !sx || !ids || !weights || !workspace) return W4_ERR_INVALID_ARG;
+    if (ws_bytes < w4_moe_workspace_bytes(e, M, top_k)) return W4_ERR_UNSUPPORTED_SHAPE;
+    if (r != W4_OK || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 16))
+        return W4_ERR_MISALIGNED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
+    r = cuda_status(launch_zero_words(static_cast<unsigned*>(workspace), moe_space(e, M, top_k).words, (flags & W4_FLAG_PDL) != 0, s));
+    if (r != W4_OK) return r;
+    return run_experts(e, qx, sx, ids, weights, M, top_k, residual, y, y_type, workspace, s);
+}
+
+w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, int x_type, int M, int* ids,
+                       float* weights, int8_t* qx, float* sx, const float* residual, void* y, int y_type,
+                       void* workspace, size_t ws_bytes, unsigned flags, w4_stream_t s)
+{
+    if (!r || !e) return W4_ERR_INVALID_ARG;
+    w4_status st = check_router(r, M, e->H);
+    if (st == W4_OK) st = check_experts(e, M, r->top_k);
+    if (st != W4_OK) return st;
+    if (r->E != e->E || !elem_type(x_type) || !elem_type(y_type) || (flags & ~W4_FLAG_PDL) != 0) return W4_ERR_INVALID_ARG;
+    if (M == 0) return W4_OK;
+    st = check_route_pointers(r, x, ids, weights, qx, sx);
+    const w4_status se = check_expert_pointers(e, residual, y, y_type);
+    if (st == W4_ERR_INVALID_ARG || se == W4_ERR_INVALID_ARG || !qx || !workspace) return W4_ERR_INVALID_ARG;
+    if (ws_bytes < w4_moe_workspace_bytes(e, M, r->top_k)) return W4_ERR_UNSUPPORTED_SHAPE;
+    if (st != W4_OK || se != W4_OK || !aligned(workspace, 16)) return W4_ERR_MISALIGNED;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+    st = run_route(r, x, x_type, M, e->H, ids, weights, qx, sx, static_cast<unsigned*>(workspace),
+                   moe_space(e, M, r->top_k).words, (flags & W4_FLAG_PDL) != 0, cs);
+    if (st != W4_OK) return st;
+    return run_experts(e, qx, sx, ids, weights, M, r->top_k, residual, y, y_type, workspace, cs);
 }
 
 }  // extern "C"

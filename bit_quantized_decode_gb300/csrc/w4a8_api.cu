@@ -908,6 +908,25 @@ w4_status w4_repack_glu(const uint32_t* gate, const uint32_t* up, int I, int K, 
     return cuda_status(launch_w4_repack(st, Nw, K, out, reinterpret_cast<cudaStream_t>(s)));
 }
 
+size_t w8_glu_repacked_bytes(int I, int K)
+{
+    if (I < 0 || I > (1 << 29) || K <= 0 || K % 32 != 0) return 0;
+    return w8_repacked_bytes(8 * ((I + 3) / 4), K);
+}
+
+w4_status w8_repack_glu(const int8_t* gate, const int8_t* up, int I, int K, void* out, size_t out_bytes,
+                        w4_stream_t s)
+{
+    ShardTable st;
+    int Nw = 0;
+    w4_status r = glu_shards(gate, up, I, K, st, Nw);
+    if (r != W4_OK || Nw == 0) return r;
+    if (!out) return W4_ERR_INVALID_ARG;
+    if (out_bytes < w8_glu_repacked_bytes(I, K)) return W4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(out, 16) || !aligned(gate, 16) || !aligned(up, 16)) return W4_ERR_MISALIGNED;
+    return cuda_status(launch_w8_repack(st, Nw, K, out, reinterpret_cast<cudaStream_t>(s)));
+}
+
 w4_status q4_0_repack_glu(const uint8_t* gate, const uint8_t* up, int I, int K, void* out, size_t out_bytes,
                           w4_stream_t s)
 {

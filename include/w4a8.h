@@ -263,10 +263,14 @@ w4_status q6g32_repack(const int8_t* const* shard_q, const uint16_t* const* shar
  * *_linear_fused calls: row tile t holds gate rows 4t..4t+3 and then up rows
  * 4t..4t+3 (8 ceil(I/4) rows in all, padding past I zero), so one thread
  * block sees both halves of every output.  gate and up: canonical [I][..]
- * device arrays (W4: uint32 [I][K/8]; Q4_0: 18-byte blocks [I][K/32]).
+ * device arrays (W4: uint32 [I][K/8]; Q4_0: 18-byte blocks [I][K/32]; per-row
+ * INT8, for the experts of w4_moe_experts: int8 [I][K]).
  * out: *_glu_repacked_bytes(I, K) bytes, 16-byte aligned. */
 size_t w4_glu_repacked_bytes(int I, int K);
 w4_status w4_repack_glu(const uint32_t* gate, const uint32_t* up, int I, int K, void* out, size_t out_bytes,
+                        w4_stream_t s);
+size_t w8_glu_repacked_bytes(int I, int K);
+w4_status w8_repack_glu(const int8_t* gate, const int8_t* up, int I, int K, void* out, size_t out_bytes,
                         w4_stream_t s);
 size_t q4_0_glu_repacked_bytes(int I, int K);
 w4_status q4_0_repack_glu(const uint8_t* gate, const uint8_t* up, int I, int K, void* out, size_t out_bytes,
@@ -459,6 +463,97 @@ w4_status w8a8_matmul(const void* w, const float* s_w, const float* bias, const 
 w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const void* x, int x_type, int M, int N,
                       int K, void* y, int y_type, int8_t* qx, float* sx, const w4_fusion* f, unsigned flags,
                       void* workspace, size_t ws_bytes, w4_stream_t s);
+
+/* ------------------------------------------------------------------------
+ * Mixture-of-experts layer for 1 to 16 tokens: a router and the experts' gated
+ * MLP on per-row INT4 or INT8 weights and INT8 activations.
+ *
+ * w4_moe_route, one launch.  With x' = RMSNorm(x) as in the *_linear_fused
+ * calls (or x, without norm_weight):
+ *   l_e = sum_i x'_i w[e][i], rounded once to fp32 from a compensated sum;
+ *   W4_ROUTE_SOFTMAX: the top_k experts by l; p = softmax(l) over all E;
+ *   W4_ROUTE_SIGMOID: p_e = 1 / (1 + exp(-l_e)) rounded once to fp32, the
+ *     top_k experts by fp32(p_e + select_bias[e]);
+ *   equal keys: the lowest index first.  weights = p of the chosen (divided by
+ *   their sum with renormalize; 0 where that sum is 0) * scale.
+ * ids: int [M][top_k], best first; weights: float [M][top_k]; qx, sx: the
+ * codes and scales of x' (as rms_a8_quantize makes them), or both NULL.
+ * x: [M][K] of x_type, 16-byte aligned; w: float [E][K], 16-byte aligned;
+ * K % 32 == 0, 1 <= top_k <= min(E, 16), E <= 1024; K up to about 50000 (a
+ * token is kept in shared memory as fp32).  A NaN logit is the last choice;
+ * the ids are valid and distinct whatever x holds.
+ *
+ * w4_moe_experts.  For every token m and slot s with expert e = ids[m][s]:
+ *   g, u = linear(qx, sx) by e's gate and up rows, as the W4 / W8A8 linears,
+ *   h    = act(g) u, evaluated to one fp32 rounding,
+ *   d    = linear of h's codes (quantized as a8_quantize does) by e's down rows,
+ *   y[m] = sum over the slots in order of weights[m][s] * d (fp32), then the
+ *          n_shared shared experts with weight 1, then + residual[m], rounded
+ *          to y's type.
+ * An id outside 0 .. E - 1 is an empty slot and contributes nothing; a token
+ * with empty slots only gets the residual (or 0).  An expert may be named
+ * twice.  The experts' weights are read once for all their tokens; results do
+ * not depend on the other tokens of the call, nor on timing.
+ *   experts: E + n_shared of them, the shared ones last, one behind the other:
+ *     w_gu  *_repack_glu of gate and up [I][H] each, *_glu_repacked_bytes(I, H)
+ *           apart;   s_gu (b_gu): float [E + n_shared][2 I], gate rows first;
+ *     w_dn  *_repack of down [H][I], *_repacked_bytes(H, I) apart;
+ *           s_dn (b_dn): float [E + n_shared][H].
+ *     fmt: W4_FMT_W4 or W4_FMT_W8; glu: W4_GLU_SILU or W4_GLU_GELU_TANH;
+ *     H % 32 == 0, I % 32 == 0; E + n_shared <= 1024, n_shared <= 4.
+ *   residual: float [M][H] or NULL (may be y itself where y is W4_F32).
+ *   workspace: w4_moe_workspace_bytes(..) bytes, 16-byte aligned, with no
+ *     contents to keep; calls that share one must not overlap on the GPU.
+ * Two launches (the first clears the workspace's counters).  The kernel waits
+ * on its own blocks' progress with bounded waits (see w4_device_error), but
+ * needs no co-resident grid: calls on several streams, each with its own
+ * workspace, may run at once.
+ *
+ * w4_moe_layer: w4_moe_route, then w4_moe_experts on its choice, in two
+ * launches, the second a programmatic dependent of the first; ids, weights,
+ * qx and sx receive the choice and the codes (none may be NULL).
+ * flags: 0 or W4_FLAG_PDL.  M = 0 is a valid empty call.
+ * ------------------------------------------------------------------------ */
+#define W4_FMT_W8 5 /* per-row INT8 (w8_quantize_rows); w4_experts only */
+#define W4_ROUTE_SOFTMAX 0
+#define W4_ROUTE_SIGMOID 1
+#define W4_MAX_TOP_K 16
+#define W4_MAX_EXPERTS 1024
+#define W4_MAX_SHARED 4
+typedef struct {
+    const float* norm_weight; /* [K] or NULL */
+    float norm_eps;
+    const float* w;           /* [E][K] */
+    const float* select_bias; /* [E] or NULL; W4_ROUTE_SIGMOID only */
+    int E;
+    int top_k;
+    int score;
+    int renormalize;
+    float scale;
+} w4_router;
+typedef struct {
+    int fmt;
+    int E;
+    int n_shared;
+    int H;
+    int I;
+    int glu;
+    const void* w_gu;
+    const float* s_gu;
+    const float* b_gu; /* or NULL */
+    const void* w_dn;
+    const float* s_dn;
+    const float* b_dn; /* or NULL */
+} w4_experts;
+w4_status w4_moe_route(const w4_router* r, const void* x, int x_type, int M, int K, int* ids, float* weights,
+                       int8_t* qx, float* sx, unsigned flags, w4_stream_t s);
+size_t w4_moe_workspace_bytes(const w4_experts* e, int M, int top_k); /* 0 for what the calls refuse */
+w4_status w4_moe_experts(const w4_experts* e, const int8_t* qx, const float* sx, const int* ids,
+                         const float* weights, int M, int top_k, const float* residual, void* y, int y_type,
+                         void* workspace, size_t ws_bytes, unsigned flags, w4_stream_t s);
+w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, int x_type, int M, int* ids,
+                       float* weights, int8_t* qx, float* sx, const float* residual, void* y, int y_type,
+                       void* workspace, size_t ws_bytes, unsigned flags, w4_stream_t s);
 
 /* ------------------------------------------------------------------------
  * A chain of per-row INT4 decode linears in one launch (a decode step's

@@ -35,3 +35,50 @@ def linear(q, s, w, s_w, b=None):
 
 EPS = {"float32": 2.0 ** -24, "float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}   # half a step, relative
 TINY = {"float32": 2.0 ** -149, "float16": 2.0 ** -25, "bfloat16": 2.0 ** -133}
+
+
+def logits(x, w):
+    return one(np.asarray(x, F64) @ np.asarray(w, F64).T)
+
+
+def route(l, top_k, score, bias, renorm, scale):
+    """ids [M][top_k] and weights in 64 bits from the logits l [M][E]."""
+    l = np.asarray(l, F64)
+    if score == "softmax":
+        e = np.exp(l - l.max(axis=1, keepdims=True))
+        p, key = e / e.sum(axis=1, keepdims=True), l
+    else:
+        p = 1.0 / (1.0 + np.exp(-l))
+        key = one(p) if bias is None else one(one(p) + np.asarray(bias, F64))
+    ids = np.argsort(-key, axis=1, kind="stable")[:, :top_k]
+    w = np.take_along_axis(p, ids, axis=1)
+    if renorm:
+        w = w / w.sum(axis=1, keepdims=True)
+    return ids, w * scale
+
+
+def act(kind, g, u):
+    g, u = np.asarray(g, F64), np.asarray(u, F64)
+    with np.errstate(over="ignore"):
+        if kind == "silu":
+            return one(g / (1.0 + np.exp(-g)) * u)
+        return one(g / (1.0 + np.exp(-2.0 * np.sqrt(2.0 / np.pi) * (g + 0.044715 * g ** 3))) * u)
+
+
+def experts(q, s, ids, weights, gu, s_gu, dn, s_dn, kind, n_shared=0, b_gu=None, b_dn=None):
+    """y [M][H] in 64 bits and a bound of its fp32 roundings.  gu [n][2I][H], dn [n][H][I] integer codes."""
+    M, H = q.shape
+    n, I = len(gu), gu[0].shape[0] // 2
+    E = n - n_shared
+    y, room = np.zeros((M, H)), np.zeros((M, H))
+    for m in range(M):
+        slots = [(int(e), float(w)) for e, w in zip(ids[m], weights[m]) if 0 <= e < E] + [(E + j, 1.0) for j in range(n_shared)]
+        for e, w in slots:
+            _, v = linear(q[m:m + 1], s[m:m + 1], gu[e], s_gu[e], None if b_gu is None else b_gu[e])
+            h = act(kind, v[0, :I], v[0, I:])
+            qh, sh = codes(h[None])
+            d, _ = linear(qh, sh, dn[e], s_dn[e], None if b_dn is None else b_dn[e])
+            prod, _ = linear(qh, sh, dn[e], s_dn[e])
+            y[m] += w * d[0]
+            room[m] += abs(w) * (np.abs(prod[0]) + np.abs(d[0])) + (len(slots) + 1) * np.abs(w * d[0])
+    return y, 2.0 ** -24 * room
