@@ -48,17 +48,6 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
-// One lane of a converged warp.  The tensor-core and bulk-copy instructions
-// take uniform registers: under an elected lane the compiler issues them
-// once, where under "lane == 0" it loops over the lanes that might be active
-// (550 against some 60 cycles a stage).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // Wait of a whole warp: a test first, as the phase is usually complete.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
 {

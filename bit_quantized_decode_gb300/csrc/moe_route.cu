@@ -76,8 +76,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
             asm volatile("prefetch.global.L2 [%0];" ::"l"(row + o));
     }
     pdl_wait();
-    if (a.zero != nullptr)
-        for (int i = blockIdx.x * kRtThreads + tid; i < a.n_zero; i += static_cast<int>(gridDim.x) * kRtThreads) a.zero[i] = 0u;
+    moe_fill(a.fill);
 
     // ---- the tokens as fp32 in shared memory, normalized
     float hi[TG], lo[TG];

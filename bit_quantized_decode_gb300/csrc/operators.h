@@ -99,6 +99,18 @@ constexpr int kRtWarps = kRtThreads / 32;
 constexpr int kRtMaxTok = 4;                    // tokens per cluster at most
 constexpr int kRtMaxCluster = 16;
 
+// Words that the experts kernel finds prepared: a zero ticket counter, then
+// values that no result takes (fp32 NaN with all bits set, the code -128), by
+// which a reader sees that a word has not been written yet.
+constexpr int kMxHead = 32;                     // words: the ticket counter and padding
+constexpr unsigned kMxNoValue = 0xffffffffu;
+constexpr unsigned kMxNoCodes = 0x80808080u;
+struct MoeFill {
+    uint4* p;
+    unsigned values;          // 16-byte words of fp32 values behind the head
+    unsigned codes;           // 16-byte words of codes behind those
+};
+
 struct RouteArgs {
     const void* x;            // [M][K] of xtype
     const float* gamma;       // RMSNorm weight, or null
@@ -117,8 +129,7 @@ struct RouteArgs {
     float* weights;           // [M][top_k]
     int8_t* qx;               // [M][K] codes of the (normalized) tokens, or null
     float* sx;                // [M], or null
-    unsigned* zero;           // words cleared for the experts kernel, or null
-    int n_zero;
+    MoeFill fill;             // the experts kernel's workspace, prepared here (words 0: none)
 };
 // x as fp32, the partial sums of an expert's warps, the logits (cluster leader), block sums.
 __host__ __device__ inline int route_smem(int tok, int K, int E)
@@ -128,14 +139,12 @@ __host__ __device__ inline int route_smem(int tok, int K, int E)
 cudaError_t launch_moe_route(const RouteArgs& a, int xtype, bool pdl, cudaStream_t s);
 
 // ------------------------------------------ mixture-of-experts kernel (moe_experts.cu)
-constexpr int kMxThreads = 512;
-constexpr int kMxWarps = kMxThreads / 32;
-constexpr int kMxLines = 16;                    // lines (8 rows x 32 weights) per ring slot: one pass of a warp
-constexpr int kMxTok = 8;                       // pairs of one entry (an expert and up to eight of its tokens)
+constexpr int kMxTok = 8;                       // pairs of one entry at most (an expert and some of its tokens)
 constexpr int kMxMaxSlots = 20;                 // chosen and shared experts per token
 constexpr int kMxMaxPairs = 16 * kMxMaxSlots;
 constexpr int kMxMaxExperts = 1024;             // routed and shared
-constexpr int kMxSeg = 512;                     // hidden values per quantizing task
+constexpr int kMxSeg = 1024;                    // hidden values per quantizing task
+constexpr int kMxAdd = 256;                     // outputs per adding task
 
 struct MoeArgs {
     const uint8_t* w_gu;      // per expert: gate and up rows paired per tile (w4_repack_glu / w8_repack_glu)
@@ -152,18 +161,22 @@ struct MoeArgs {
     void* y;                  // [M][H] of ytype
     int ytype, glu;
     int M, H, I, E, S, top_k;
-    int stages;               // ring slots per warp
-    unsigned* ctrl;           // moe_ctrl_words, zero at the start
-    float* h;                 // [pairs][I]
-    int8_t* qh;               // [pairs][I]
+    int stage_x;              // the tokens' codes are copied into shared memory
+    int batch;                // tickets that a block takes at once
+    float inv_t1, inv_t2, inv_seg, inv_add;   // 1 / (tiles of a gate/up and of a down matrix, quantizing tasks of a
+                              // pair, adding tasks of a token)
+    unsigned* ticket;         // zero at the start
+    float* sh;                // [pairs] scales of the hidden codes            (these four: kMxNoValue /
+    float* h;                 // [pairs][I]                                      kMxNoCodes at the start)
     float* part;              // [pairs][H]
+    int8_t* qh;               // [pairs][Ip]
+    int Ip;                   // I rounded up to 128: no L1 line holds codes of two pairs
     unsigned* err;
 };
-// Control words: ticket; per pair: hidden maximum, code sum; per entry: gate/up
-// tiles done, quantizing tasks done; per 8-row output tile: entries done.
-__host__ __device__ inline int moe_ctrl_words(int pairs, int H) { return 4 + 4 * pairs + (H + 7) / 8; }
-cudaError_t launch_moe_experts(int fmt, const MoeArgs& a, int grid, size_t smem, bool pdl, cudaStream_t s);
-size_t moe_experts_smem(int fmt, int stages);
-cudaError_t launch_zero_words(unsigned* p, int n, bool pdl, cudaStream_t s);
+// `tok`: pairs per entry (1, 2, 4 or 8).  Warps per block and ring slots per warp follow from it.
+int moe_warps(int tok);
+size_t moe_experts_smem(int tok, int staged_bytes);
+cudaError_t launch_moe_experts(int fmt, int tok, const MoeArgs& a, int grid, size_t smem, bool pdl, cudaStream_t s);
+cudaError_t launch_moe_fill(const MoeFill& f, bool pdl, cudaStream_t s);
 
 }  // namespace w4k

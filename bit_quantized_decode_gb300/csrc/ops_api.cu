@@ -117,7 +117,7 @@ bool plan_route(const DeviceFacts& d, RouteArgs& a)
 }
 
 w4_status run_route(const w4_router* r, const void* x, int x_type, int M, int K, int* ids, float* weights, int8_t* qx,
-                    float* sx, unsigned* zero, int n_zero, bool pdl, cudaStream_t s)
+                    float* sx, const MoeFill& fill, bool pdl, cudaStream_t s)
 {
     DeviceFacts d;
     if (!device_facts(&d)) return W4_ERR_CUDA;
@@ -138,8 +138,7 @@ w4_status run_route(const w4_router* r, const void* x, int x_type, int M, int K,
     a.weights = weights;
     a.qx = qx;
     a.sx = sx;
-    a.zero = zero;
-    a.n_zero = n_zero;
+    a.fill = fill;
     if (!plan_route(d, a)) return W4_ERR_UNSUPPORTED_SHAPE;
     return cuda_status(launch_moe_route(a, x_type, pdl, s));
 }
@@ -177,21 +176,26 @@ w4_status check_expert_pointers(const w4_experts* e, const float* residual, cons
     return W4_OK;
 }
 
-// Parts of the workspace: control words, h, the codes of h, the slots' outputs.
+// Parts of the workspace: the ticket counter, then scales, h and the slots'
+// outputs (fp32), then the codes of h.
 struct MoeSpace {
-    size_t h, qh, part, total;
-    int words;
+    size_t h, part, qh, total;
+    int Ip;
 };
 MoeSpace moe_space(const w4_experts* e, int M, int top_k)
 {
     const size_t P = static_cast<size_t>(M) * (top_k + e->n_shared);
     MoeSpace w;
-    w.words = moe_ctrl_words(static_cast<int>(P), e->H);
-    w.h = (static_cast<size_t>(w.words) * 4 + 255) & ~static_cast<size_t>(255);
-    w.qh = w.h + P * e->I * 4;
-    w.part = w.qh + P * e->I;
-    w.total = w.part + P * e->H * 4;
+    w.Ip = (e->I + 127) / 128 * 128;
+    w.h = kMxHead * 4 + (P * 4 + 127) / 128 * 128;
+    w.part = w.h + P * e->I * 4;
+    w.qh = w.part + P * e->H * 4;
+    w.total = w.qh + P * w.Ip;
     return w;
+}
+MoeFill moe_fill_of(const MoeSpace& w, void* ws)
+{
+    return MoeFill{static_cast<uint4*>(ws), static_cast<unsigned>((w.qh - kMxHead * 4) / 16), static_cast<unsigned>((w.total - w.qh) / 16)};
 }
 
 w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, const int* ids, const float* weights, int M,
@@ -222,19 +226,29 @@ w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, co
     a.E = e->E;
     a.S = e->n_shared;
     a.top_k = top_k;
-    a.ctrl = reinterpret_cast<unsigned*>(base);
+    a.ticket = reinterpret_cast<unsigned*>(base);
+    a.sh = reinterpret_cast<float*>(base + kMxHead * 4);
     a.h = reinterpret_cast<float*>(base + w.h);
-    a.qh = reinterpret_cast<int8_t*>(base + w.qh);
     a.part = reinterpret_cast<float*>(base + w.part);
+    a.qh = reinterpret_cast<int8_t*>(base + w.qh);
+    a.Ip = w.Ip;
     a.err = d.err;
-    // about 160 KB of weights in flight per SM (192 KB of INT8), the rest L1 for the codes
-    a.stages = e->fmt == W4_FMT_W4 ? 5 : 3;
-    const size_t smem = moe_experts_smem(e->fmt, a.stages);
+    // entries of as many pairs as there are tokens (a token's experts are distinct, as a rule)
+    const int tok = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : kMxTok;
+    const int warps = moe_warps(tok);
+    a.inv_t1 = 1.0f / static_cast<float>((e->I + 3) / 4);
+    a.inv_t2 = 1.0f / static_cast<float>((e->H + 7) / 8);
+    a.inv_seg = 1.0f / static_cast<float>((e->I + kMxSeg - 1) / kMxSeg);
+    a.inv_add = 1.0f / static_cast<float>((e->H + kMxAdd - 1) / kMxAdd);
+    a.stage_x = moe_experts_smem(tok, M * e->H) <= static_cast<size_t>(d.smem_optin);
+    const size_t smem = moe_experts_smem(tok, a.stage_x ? M * e->H : 0);
     if (smem > static_cast<size_t>(d.smem_optin)) return W4_ERR_UNSUPPORTED_SHAPE;
-    const long long work = static_cast<long long>(M) * (top_k + e->n_shared) * (e->I / 4 + e->H / 8);
-    const long long blocks = (work + kMxWarps - 1) / kMxWarps;
-    const int grid = blocks < d.sms ? static_cast<int>(blocks) : d.sms;
-    return cuda_status(launch_moe_experts(e->fmt, a, grid, smem, true, s));
+    // every SM a share of the gate/up tiles, in one to `warps` tickets at a time
+    const long long work = static_cast<long long>(M) * (top_k + e->n_shared) * ((e->I + 3) / 4);
+    const int grid = work < d.sms ? static_cast<int>(work) : d.sms;
+    const long long share = work / grid;
+    a.batch = share < warps ? static_cast<int>(share) : warps;
+    return cuda_status(launch_moe_experts(e->fmt, tok, a, grid, smem, true, s));
 }
 
 }  // namespace
@@ -309,7 +323,7 @@ w4_status w4_moe_route(const w4_router* r, const void* x, int x_type, int M, int
     if (M == 0) return W4_OK;
     st = check_route_pointers(r, x, ids, weights, qx, sx);
     if (st != W4_OK) return st;
-    return run_route(r, x, x_type, M, K, ids, weights, qx, sx, nullptr, 0, (flags & W4_FLAG_PDL) != 0,
+    return run_route(r, x, x_type, M, K, ids, weights, qx, sx, MoeFill{}, (flags & W4_FLAG_PDL) != 0,
                      reinterpret_cast<cudaStream_t>(s));
 }
 
@@ -330,10 +344,10 @@ w4_status w4_moe_experts(const w4_experts* e, const int8_t* qx, const float* sx,
     r = check_expert_pointers(e, residual, y, y_type);
     if (r == W4_ERR_INVALID_ARG || !qx || !sx || !ids || !weights || !workspace) return W4_ERR_INVALID_ARG;
     if (ws_bytes < w4_moe_workspace_bytes(e, M, top_k)) return W4_ERR_UNSUPPORTED_SHAPE;
-    if (r != W4_OK || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 16))
+    if (r != W4_OK || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 128))
         return W4_ERR_MISALIGNED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
-    r = cuda_status(launch_zero_words(static_cast<unsigned*>(workspace), moe_space(e, M, top_k).words, (flags & W4_FLAG_PDL) != 0, s));
+    r = cuda_status(launch_moe_fill(moe_fill_of(moe_space(e, M, top_k), workspace), (flags & W4_FLAG_PDL) != 0, s));
     if (r != W4_OK) return r;
     return run_experts(e, qx, sx, ids, weights, M, top_k, residual, y, y_type, workspace, s);
 }
@@ -352,10 +366,10 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
     const w4_status se = check_expert_pointers(e, residual, y, y_type);
     if (st == W4_ERR_INVALID_ARG || se == W4_ERR_INVALID_ARG || !qx || !workspace) return W4_ERR_INVALID_ARG;
     if (ws_bytes < w4_moe_workspace_bytes(e, M, r->top_k)) return W4_ERR_UNSUPPORTED_SHAPE;
-    if (st != W4_OK || se != W4_OK || !aligned(workspace, 16)) return W4_ERR_MISALIGNED;
+    if (st != W4_OK || se != W4_OK || !aligned(workspace, 128)) return W4_ERR_MISALIGNED;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-    st = run_route(r, x, x_type, M, e->H, ids, weights, qx, sx, static_cast<unsigned*>(workspace),
-                   moe_space(e, M, r->top_k).words, (flags & W4_FLAG_PDL) != 0, cs);
+    st = run_route(r, x, x_type, M, e->H, ids, weights, qx, sx, moe_fill_of(moe_space(e, M, r->top_k), workspace),
+                   (flags & W4_FLAG_PDL) != 0, cs);
     if (st != W4_OK) return st;
     return run_experts(e, qx, sx, ids, weights, M, r->top_k, residual, y, y_type, workspace, cs);
 }

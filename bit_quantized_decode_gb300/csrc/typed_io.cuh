@@ -11,6 +11,17 @@
 
 namespace w4k {
 
+// One lane of a converged warp.  The tensor-core and bulk-copy instructions
+// take uniform registers: under an elected lane the compiler issues them
+// once, where under "lane == 0" it loops over the lanes that might be active
+// (550 against some 60 cycles for the four to five of a GEMM stage).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void zero8(float (&v)[8])
 {
 #pragma unroll
@@ -63,6 +74,16 @@ __device__ __forceinline__ uint2 quant8(const float (&t)[8], const A8Scale& ks)
     if (all || (ok0 >> 31) == 0u) q.x = a8_pack4_exact(a, ks);
     if (all || (ok1 >> 31) == 0u) q.y = a8_pack4_exact(b, ks);
     return q;
+}
+
+// The experts kernel's workspace (MoeFill), by the whole grid.
+__device__ __forceinline__ void moe_fill(const MoeFill& f)
+{
+    const unsigned head = kMxHead / 4, n = f.p != nullptr ? head + f.values + f.codes : 0u;
+    for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
+        const unsigned v = i < head ? 0u : i < head + f.values ? kMxNoValue : kMxNoCodes;
+        f.p[i] = make_uint4(v, v, v, v);
+    }
 }
 
 // Four int8 -> four fp16, exactly: q + 128 as the low byte of the fp16 number
