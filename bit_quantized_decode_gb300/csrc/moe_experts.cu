@@ -23,11 +23,12 @@
 //     lane / 2 of a 16-line pass, rows 4 (lane & 1) .. + 3, reads permuted
 //     against bank conflicts, a shuffle butterfly at the end of a tile).
 //     More tokens of one expert are further entries.
-//   * No flags, no fences: hidden values, their codes and the slots' outputs
-//     are prepared with values that no result takes (MoeFill), and a reader
-//     looks at the words themselves until every one is there.  (Counters with
-//     release order cost a fence per tile, which waits for all that the warp has
-//     outstanding: 3500 of a tile's 9500 cycles.)
+//   * No fence per tile (it waits for all that the warp has outstanding: it
+//     took 3500 of a tile's 9500 cycles): hidden values and the slots' outputs
+//     are prepared with a value that no result takes (MoeFill), and a reader
+//     looks at the words themselves until every one is there.  Only the few
+//     quantizing tasks publish their codes with release order, which the tiles
+//     that read them through L1 acquire.
 //   * Adding tasks, the last tickets, sum the slots' outputs in order: no
 //     floating-point atomics, so results do not depend on timing.
 #include "exact_act.cuh"
@@ -47,21 +48,22 @@ __host__ __device__ constexpr int mx_unit(int fmt) { return fmt == FMT_W4 ? 16 :
 // sums per weight) the slots are large; with more, more warps.
 __host__ __device__ constexpr int mx_slot(int tok) { return tok <= 2 ? 8192 : 4096; }
 __host__ __device__ constexpr int mx_stages(int) { return 2; }
-__host__ __device__ constexpr int mx_warps(int tok) { return tok <= 2 ? 12 : 16; }
+__host__ __device__ constexpr int mx_warps(int tok) { return tok <= 2 ? 12 : tok <= 4 ? 20 : 16; }
 
 constexpr int kMxBatches = 64;
 
 struct MxSmem {
-    int bars, cnt, off, pair_e, list, tok, ent_e, ent_off, ent_n, of_pos, ready, sh, hs, sx, xsum, misc, base, ring, codes, total;
+    int bars, mask, off, ent0, pair_e, list, tok, ent_e, ent_off, ent_n, of_pos, ready, sh, hs, sx, xsum, misc, base, ring, codes, total;
 };
 __host__ __device__ inline MxSmem mx_smem(int tok, int staged)
 {
     const int warps = mx_warps(tok), stages = mx_stages(tok);
     MxSmem L;
     int o = 0;
-    L.bars = o;    o += warps * stages * 8;
-    L.cnt = o;     o += kMxMaxExperts * 2;             // pairs per expert
+    L.bars = o;    o += (warps * stages + 1) * 8;      // the rings', the staged codes'
+    L.mask = o;    o += kMxMaxExperts * 4;             // tokens of an expert, a bit each (or: pairs per expert)
     L.off = o;     o += kMxMaxExperts * 2;             // first place of an expert's pairs in the list
+    L.ent0 = o;    o += kMxMaxExperts * 2;             // and its first entry
     L.pair_e = o;  o += kMxMaxPairs * 2;               // expert of a pair (0xffff: none)
     L.list = o;    o += kMxMaxPairs * 2;               // pairs ordered by expert
     L.tok = o;     o += kMxMaxPairs;                   // token of a place
@@ -123,11 +125,16 @@ __device__ __forceinline__ void st_value(float* p, float v)
     const uint32_t u = __float_as_uint(v);
     st_relaxed_u32(p, u == kMxNoValue ? 0x7fffffffu : u);
 }
-// Nonzero where a byte of the word is -128.
-__device__ __forceinline__ uint32_t no_code(uint32_t w)
+// A quantizing task's result, ordered behind its codes, and its reader's side.
+__device__ __forceinline__ void st_release_u64(unsigned long long* p, unsigned long long v)
 {
-    const uint32_t t = w ^ kMxNoCodes;
-    return (t - 0x01010101u) & ~t & 0x80808080u;
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long* p)
+{
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ int dp4a_u(uint32_t a, uint32_t b, int c)
@@ -174,12 +181,14 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
 {
     constexpr int NW = mx_warps(TK), NT = 32 * NW;
     constexpr int kUnit = mx_unit(FMT), kSlot = mx_slot(TK), kLines = kSlot / (kRows * kUnit);
+    static_assert(kLines % 16 == 0, "slices of whole passes: every lane steps through the codes alike");
     constexpr bool kPairSums = TK <= 4;            // low and high halves in accumulators of their own
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int S = mx_stages(TK);
     const MxSmem L = mx_smem(TK, 0);
-    uint16_t* cnt_s = reinterpret_cast<uint16_t*>(smem + L.cnt);
+    uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + L.mask);
+    uint16_t* ent0_s = reinterpret_cast<uint16_t*>(smem + L.ent0);
     uint16_t* off_s = reinterpret_cast<uint16_t*>(smem + L.off);
     uint16_t* pair_e = reinterpret_cast<uint16_t*>(smem + L.pair_e);
     uint16_t* list = reinterpret_cast<uint16_t*>(smem + L.list);
@@ -206,21 +215,30 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     const uint32_t bars = smem_u32(smem + L.bars) + static_cast<uint32_t>(warp * S) * 8u;
     if (lane == 0) {
         for (int s = 0; s < S; ++s) mbar_init(bars + 8 * s, 1);
+        if (warp == 1) mbar_init(smem_u32(smem + L.bars) + static_cast<uint32_t>(NW * S) * 8u, 1);
         fence_mbar_init();
     }
+    if (tid > 0 && tid < kMxBatches) base_s[tid] = ~0ull;
+    if (tid == NT - 1) misc[2] = 0;
     const int EE = A.E + A.S;
     if (TK > 1)
-        for (int e = tid; e < EE; e += NT) cnt_s[e] = 0;
+        for (int e = tid; e < EE; e += NT) mask_s[e] = 0u;
     for (int i = tid; i < P; i += NT) ready_s[i] = 0;
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
 
     // ---- the entries, the same in every block: pairs counted by expert in
     // the order of the pairs (warp 0); scales and code sums of the tokens (the others)
-    if (tid == NT - 1) {
-        misc[2] = 0;
-        for (int i = 1; i < kMxBatches; ++i) base_s[i] = ~0ull;
-        base_s[0] = atomicAdd(ticket, static_cast<unsigned>(A.batch));
+    if (tid == NT - 1) base_s[0] = atomicAdd(ticket, static_cast<unsigned>(A.batch));
+    // (the codes before any weights: behind those a load waits for microseconds)
+    const uint32_t xbar = smem_u32(smem + L.bars) + static_cast<uint32_t>(NW * S) * 8u;
+    if (A.stage_x && tid == 32) {
+        mbar_arrive_expect_tx(xbar, static_cast<uint32_t>(A.M * A.H));
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem_u32(smem + L.codes)),
+                     "l"(A.qx), "r"(static_cast<uint32_t>(A.M * A.H)), "r"(xbar)
+                     : "memory");
     }
     auto expert_of = [&](int p) -> int {
         const int m = p / slots, s = p - m * slots;
@@ -245,73 +263,88 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             if (lane == 0) misc[0] = misc[1] = __popc(have);
         }
     } else {
-        for (int p = tid; p < P; p += NT) pair_e[p] = static_cast<uint16_t>(expert_of(p));
-        __syncthreads();
+        static_assert(kMxMaxPairs <= 320 && NT >= 320, "a thread for each pair");
+        const int e = tid < P ? expert_of(tid) : 0xffff;
+        const int m = tid / slots;
+        if (tid < P) pair_e[tid] = static_cast<uint16_t>(e);
+        if (e != 0xffff) atomicOr(mask_s + e, 1u << m);
+        const int valid = __syncthreads_count(e != 0xffff);
         if (warp == 0) {
-            for (int p0 = 0; p0 < P; p0 += 32) {
-                const int p = p0 + lane;
-                const int e = p < P ? pair_e[p] : 0xffff;
-                const unsigned same = __match_any_sync(0xffffffffu, e);
-                const int rank = __popc(same & ((1u << lane) - 1u));
-                const int base = e != 0xffff ? cnt_s[e] : 0;
-                __syncwarp();
-                if (e != 0xffff) {
-                    of_pos[p] = static_cast<uint16_t>(base + rank);         // the pair's rank, for now
-                    if (rank == 0) cnt_s[e] = static_cast<uint16_t>(base + __popc(same));
-                }
-                __syncwarp();
-            }
-            int at = 0, ne = 0;
-            for (int e0 = 0; e0 < EE; e0 += 32) {
-                const int c = e0 + lane < EE ? cnt_s[e0 + lane] : 0;
-                const int k = (c + TK - 1) / TK;
-                int both = c | (k << 16);                                   // two prefix sums in one word
+            // places and entries of the experts: prefix sums of two counts in one word
+            auto scan = [&](auto&& count) -> int {
+                int at = 0, ne = 0;
+                for (int e0 = 0; e0 < EE; e0 += 32) {
+                    const int c = e0 + lane < EE ? count(e0 + lane) : 0;
+                    const int k = (c + TK - 1) / TK;
+                    int both = c | (k << 16);
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, both, o);
-                    if (lane >= o) both += v;
-                }
-                if (c > 0) {
-                    const int a0 = at + (both & 0xffff) - c, n0 = ne + (both >> 16) - k;
-                    off_s[e0 + lane] = static_cast<uint16_t>(a0);
-                    for (int i = 0; i < k; ++i) {
-                        ent_e[n0 + i] = static_cast<uint16_t>(e0 + lane);
-                        ent_off[n0 + i] = static_cast<uint16_t>(a0 + i * TK);
-                        ent_n[n0 + i] = static_cast<uint8_t>(min(TK, c - i * TK));
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int v = __shfl_up_sync(0xffffffffu, both, o);
+                        if (lane >= o) both += v;
                     }
+                    if (c > 0) {
+                        const int a0 = at + (both & 0xffff) - c, n0 = ne + (both >> 16) - k;
+                        off_s[e0 + lane] = static_cast<uint16_t>(a0);
+                        ent0_s[e0 + lane] = static_cast<uint16_t>(n0);
+                        for (int i = 0; i < k; ++i) {
+                            ent_e[n0 + i] = static_cast<uint16_t>(e0 + lane);
+                            ent_off[n0 + i] = static_cast<uint16_t>(a0 + i * TK);
+                            ent_n[n0 + i] = static_cast<uint8_t>(min(TK, c - i * TK));
+                        }
+                    }
+                    both = __shfl_sync(0xffffffffu, both, 31);
+                    at += both & 0xffff;
+                    ne += both >> 16;
                 }
-                both = __shfl_sync(0xffffffffu, both, 31);
-                at += both & 0xffff;
-                ne += both >> 16;
-            }
-            if (lane == 0) {
-                misc[0] = ne;
-                misc[1] = at;
-            }
-            __syncwarp();
-            for (int p = lane; p < P; p += 32)
-                if (pair_e[p] != 0xffff) {
-                    const int pos = off_s[pair_e[p]] + of_pos[p];
-                    list[pos] = static_cast<uint16_t>(p);
-                    tok_s[pos] = static_cast<uint8_t>(p / slots);
+                if (lane == 0) {
+                    misc[0] = ne;
+                    misc[1] = at;
                 }
-            __syncwarp();
-            for (int n = lane; n < ne; n += 32)
-                for (int q = 0; q < ent_n[n]; ++q) of_pos[ent_off[n] + q] = static_cast<uint16_t>(n);
+                return at;
+            };
+            const int at = scan([&](int x) { return __popc(mask_s[x]); });
+            if (at != valid) {
+                // some token names an expert twice: count pair by pair
+                for (int x = lane; x < EE; x += 32) mask_s[x] = 0u;
+                __syncwarp();
+                for (int p0 = 0; p0 < P; p0 += 32) {
+                    const int x = p0 + lane < P ? pair_e[p0 + lane] : 0xffff;
+                    const unsigned same = __match_any_sync(0xffffffffu, x);
+                    const int rank = __popc(same & ((1u << lane) - 1u));
+                    const unsigned base = x != 0xffff ? mask_s[x] : 0u;
+                    __syncwarp();
+                    if (x != 0xffff) {
+                        of_pos[p0 + lane] = static_cast<uint16_t>(base + rank);          // the pair's rank, for now
+                        if (rank == 0) mask_s[x] = base + __popc(same);
+                    }
+                    __syncwarp();
+                }
+                scan([&](int x) { return static_cast<int>(mask_s[x]); });
+            }
+            if (lane == 0) misc[3] = at != valid;
+        }
+        __syncthreads();
+        const int rank = e == 0xffff ? 0 : misc[3] ? of_pos[tid] : __popc(mask_s[e] & ((1u << m) - 1u));
+        if (misc[3]) __syncthreads();
+        if (e != 0xffff) {
+            const int pos = off_s[e] + rank;
+            list[pos] = static_cast<uint16_t>(tid);
+            tok_s[pos] = static_cast<uint8_t>(m);
+            of_pos[pos] = static_cast<uint16_t>(ent0_s[e] + rank / TK);
         }
     }
-    // (before the weights are asked for: behind them a load waits for microseconds)
-    if (A.stage_x) {
-        const uint4* q = reinterpret_cast<const uint4*>(A.qx);
-        for (int i = tid; i < A.M * (A.H >> 4); i += NT) reinterpret_cast<uint4*>(smem + L.codes)[i] = __ldg(q + i);
-    }
-    if (warp > 0)
+    if (warp > 0) {
+        bool ok = true;
+        if (A.stage_x) ok = mbar_wait_bounded(xbar, 0u, kMxWaitNs);
+        if (!ok && A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
+        const int8_t* src = A.stage_x ? reinterpret_cast<const int8_t*>(smem + L.codes) : A.qx;
         for (int m = warp - 1; m < A.M; m += NW - 1) {
             int s = 0;
             if (FMT == FMT_W4) {                                            // for the nibble bias
-                const uint4* q = reinterpret_cast<const uint4*>(A.qx + static_cast<size_t>(m) * A.H);
+                const uint4* q = reinterpret_cast<const uint4*>(src + static_cast<size_t>(m) * A.H);
+#pragma unroll 4
                 for (int i = lane; i < A.H / 16; i += 32) {
-                    const uint4 v = __ldg(q + i);
+                    const uint4 v = q[i];
                     s = __dp4a(static_cast<int>(v.x), 0x01010101, s);
                     s = __dp4a(static_cast<int>(v.y), 0x01010101, s);
                     s = __dp4a(static_cast<int>(v.z), 0x01010101, s);
@@ -324,6 +357,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 sx_s[m] = __ldg(A.sx + m);
             }
         }
+    }
     __syncthreads();
     const int NE = misc[0], PV = misc[1];
     const int nseg = (A.I + kMxSeg - 1) / kMxSeg;
@@ -470,8 +504,9 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
             const A8Scale ks = a8_scale(mx);
             const uint64_t rr = f2_pack(ks.r, ks.r);
-            uint32_t* qp = reinterpret_cast<uint32_t*>(A.qh + static_cast<size_t>(p) * A.Ip);
+            uint32_t* qp = reinterpret_cast<uint32_t*>(A.qh + static_cast<size_t>(p) * A.I);
             const int i1 = min(n4, (tile + 1) * (kMxSeg / 4));
+            int sum = 0;
 #pragma unroll 4
             for (int i = tile * (kMxSeg / 4) + lane; i < i1; i += 32) {
                 const uint4 u = ld_relaxed_v4(hp + 4 * i);
@@ -479,10 +514,15 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 uint32_t good = 0xffffffffu;
                 uint32_t q = a8_pack4_fast2(v, rr, good);
                 if (a8_needs_exact(ks) || (good >> 31) == 0u) q = a8_pack4_exact(v, ks);
-                if (no_code(q) != 0u) q &= 0x7f7f7f7fu;                  // (codes of NaN)
-                st_relaxed_u32(qp + i, q);
+                qp[i] = q;
+                sum = __dp4a(static_cast<int>(q), 0x01010101, sum);
             }
-            if (tile == 0 && lane == 0) st_relaxed_u32(reinterpret_cast<uint32_t*>(A.sh + p), __float_as_uint(ks.s));
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            __syncwarp();
+            // (the sum as a float: exact, and never the bits of "not written")
+            if (lane == 0)
+                st_release_u64(A.qdone + static_cast<size_t>(p) * nseg + tile,
+                               (static_cast<unsigned long long>(__float_as_uint(__int2float_rn(sum))) << 32) | __float_as_uint(ks.s));
             continue;
         }
         if (kind == 3) {
@@ -545,47 +585,25 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
         }
         if (down) {
             if (ready_s[en] == 0) {
-                // every code of the entry, from L2: there, summed up, and then on
-                // its way to L1 for the tiles (rows start at L1 lines, so no line
-                // of a row that is not complete gets there)
+                // the pieces of the entry's pairs: there, and their sums
                 bool ok = true;
-                for (int m = 0; m < cnt && ok; ++m) {
-                    const int p = list[pos0 + m];
-                    const int8_t* qp = A.qh + static_cast<size_t>(p) * A.Ip;
-                    int sum = 0;
-                    for (int i0 = 0; i0 < (A.I >> 4) && ok; i0 += 4 * 32) {
-                        uint4 v[4];
-                        ok = wait_words([&]() {
-                            uint32_t none = 0u;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int i = i0 + 32 * k + lane;
-                                v[k] = i < (A.I >> 4) ? ld_relaxed_v4(qp + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) none |= no_code(v[k].x) | no_code(v[k].y) | no_code(v[k].z) | no_code(v[k].w);
-                            return none == 0u;
-                        });
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            sum = __dp4a(static_cast<int>(v[k].x), 0x01010101, sum);
-                            sum = __dp4a(static_cast<int>(v[k].y), 0x01010101, sum);
-                            sum = __dp4a(static_cast<int>(v[k].z), 0x01010101, sum);
-                            sum = __dp4a(static_cast<int>(v[k].w), 0x01010101, sum);
-                        }
-                    }
-                    uint32_t s = 0u;
-                    ok = ok && wait_words([&]() {
-                        s = ld_relaxed_u32(A.sh + p);
-                        return s != kMxNoValue;
+                int sums = 0;
+                float scale = 0.0f;
+                for (int g = 0; g < nseg && ok; ++g) {
+                    unsigned long long v = 0;
+                    const int p = list[pos0 + min(lane, cnt - 1)];
+                    ok = wait_words([&]() {
+                        v = ld_acquire_u64(A.qdone + static_cast<size_t>(p) * nseg + g);
+                        return static_cast<uint32_t>(v >> 32) != kMxNoValue;
                     });
-                    sum = __reduce_add_sync(0xffffffffu, sum);
-                    if (lane == 0) {
-                        sh_s[pos0 + m] = __uint_as_float(s);
-                        hs_s[pos0 + m] = 8 * sum;
-                    }
+                    sums += __float2int_rn(__uint_as_float(static_cast<uint32_t>(v >> 32)));
+                    scale = __uint_as_float(static_cast<uint32_t>(v));
                 }
                 if (!ok) break;
+                if (lane < cnt) {
+                    sh_s[pos0 + lane] = scale;
+                    hs_s[pos0 + lane] = 8 * sums;
+                }
                 __syncwarp();
                 __threadfence_block();
                 if (lane == 0) ready_s[en] = 1;
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             __threadfence_block();
         }
         uint32_t off[TK];
-        const uint32_t KK = static_cast<uint32_t>(down ? A.Ip : A.H);
+        const uint32_t KK = static_cast<uint32_t>(down ? A.I : A.H);
 #pragma unroll
         for (int m = 0; m < TK; ++m) {
             const int at = pos0 + min(m, cnt - 1);
@@ -760,7 +778,7 @@ cudaError_t launch_moe_experts(int fmt, int tok, const MoeArgs& a, int grid, siz
 
 cudaError_t launch_moe_fill(const MoeFill& f, bool pdl, cudaStream_t s)
 {
-    const unsigned words = kMxHead / 4 + f.values + f.codes;
+    const unsigned words = kMxHead / 4 + f.values;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(words < 256u * 256u ? (words + 255u) / 256u : 256u);
     cfg.blockDim = dim3(256);

@@ -49,6 +49,8 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+constexpr int kRtAhead = 8;                     // float4 of router weights that a lane holds before the wait
+
 template <int XT, int TG>
 __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArgs a)
 {
@@ -63,13 +65,27 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
     float* xs = rsm;                                      // [TG][K]
     float* part_s = xs + TG * K;                          // [warps][TG][2]
     float* key_s = part_s + kRtWarps * kRtMaxTok * 2;     // [TG][Epad], the leader's
-    float* red_s = key_s + TG * Epad;                     // [warps][TG][2]
+    uint32_t* ord_s = reinterpret_cast<uint32_t*>(key_s + TG * Epad);   // [TG][Epad] selection keys, the leader's
+    float* red_s = key_s + 2 * TG * Epad;                 // [TG][warps][2]
 
     pdl_launch_dependents();
     // this block's experts: the slot of warp group g in pass p is (p * groups + g) * cs + rank
     const int groups = kRtWarps / a.parts;
     const int grp = warp / a.parts, sub = warp % a.parts;
-    // the router's weights do not depend on the previous kernel: towards L2
+    const int k0 = static_cast<int>(static_cast<long long>(sub) * K4 / a.parts);
+    const int k1 = static_cast<int>(static_cast<long long>(sub + 1) * K4 / a.parts);
+    // the router's weights do not depend on the previous kernel: the first
+    // pieces of this warp's first expert into registers, the rest towards L2
+    float4 w0[kRtAhead];
+    {
+        const int e = grp * cs + rank;
+        const float4* wr = reinterpret_cast<const float4*>(a.w + static_cast<size_t>(e) * K);
+#pragma unroll
+        for (int u = 0; u < kRtAhead; ++u) {
+            const int i = k0 + lane + 32 * u;
+            w0[u] = e < a.E && i < k1 ? __ldg(wr + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
     for (int e = grp * cs + rank; e < a.E; e += groups * cs) {
         const char* row = reinterpret_cast<const char*>(a.w + static_cast<size_t>(e) * K);
         for (int o = (sub * 32 + lane) * 128; o < 4 * K; o += a.parts * 32 * 128)
@@ -100,16 +116,26 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
         for (int t = 0; t < TG; ++t) {
             warp_pair_sum(hi[t], lo[t]);
             if (lane == 0) {
-                red_s[(warp * TG + t) * 2] = hi[t];
-                red_s[(warp * TG + t) * 2 + 1] = lo[t];
+                red_s[(t * kRtWarps + warp) * 2] = hi[t];
+                red_s[(t * kRtWarps + warp) * 2 + 1] = lo[t];
             }
         }
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < TG; ++t) {
-            float h = red_s[t * 2], l = red_s[t * 2 + 1];
+            // the 16 warps' pairs, by every warp (both halves of it alike)
+            static_assert(kRtWarps == 16, "a half warp holds the block's pairs");
+            float h = red_s[(t * kRtWarps + (lane & 15)) * 2], l = red_s[(t * kRtWarps + (lane & 15)) * 2 + 1];
 #pragma unroll
-            for (int w = 1; w < kRtWarps; ++w) pair_merge(h, l, red_s[(w * TG + t) * 2], red_s[(w * TG + t) * 2 + 1]);
+            for (int off = 8; off > 0; off >>= 1) {
+                const float h2 = __shfl_xor_sync(0xffffffffu, h, off), l2 = __shfl_xor_sync(0xffffffffu, l, off);
+                // (both partners add the same way round: the same result in every lane)
+                const bool up = (lane & off) != 0;
+                float a0 = up ? h2 : h, a1 = up ? l2 : l;
+                pair_merge(a0, a1, up ? h : h2, up ? l : l2);
+                h = a0;
+                l = a1;
+            }
             const float r = rms_scale(h, l, K, a.eps);
             if (t < nt)
                 for (int i = tid; i < K8; i += kRtThreads) {          // the same places as above: no barrier
@@ -123,8 +149,6 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
     __syncthreads();
 
     // ---- logits
-    const int k0 = static_cast<int>(static_cast<long long>(sub) * K4 / a.parts);
-    const int k1 = static_cast<int>(static_cast<long long>(sub + 1) * K4 / a.parts);
     if (cs > 1) cluster_sync();                       // the leader's shared memory is there
     for (int e0 = 0; e0 < a.E; e0 += groups * cs) {
         const int e = e0 + grp * cs + rank;
@@ -135,9 +159,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
             for (int k = 0; k < 4; ++k) ah[t][k] = al[t][k] = 0.0f;
         if (e < a.E) {
             const float4* wr = reinterpret_cast<const float4*>(a.w + static_cast<size_t>(e) * K);
-#pragma unroll 4
-            for (int i = k0 + lane; i < k1; i += 32) {
-                const float4 w = __ldg(wr + i);
+            auto piece = [&](const float4& w, int i) {
 #pragma unroll
                 for (int t = 0; t < TG; ++t) {
                     const float4 x = reinterpret_cast<const float4*>(xs + t * K)[i];
@@ -148,7 +170,14 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
                         dot_acc(x.w, w.w, ah[t][3], al[t][3]);
                     }
                 }
+            };
+            if (e0 == 0) {
+#pragma unroll
+                for (int u = 0; u < kRtAhead; ++u)
+                    if (k0 + lane + 32 * u < k1) piece(w0[u], k0 + lane + 32 * u);
             }
+#pragma unroll 4
+            for (int i = k0 + lane + (e0 == 0 ? 32 * kRtAhead : 0); i < k1; i += 32) piece(__ldg(wr + i), i);
         }
 #pragma unroll
         for (int t = 0; t < TG; ++t) {
@@ -230,11 +259,10 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
         if (small) {
             if (lane < a.E) mine0 = key_of(lane);
             if (lane + 32 < a.E) mine1 = key_of(lane + 32);
-        } else if (a.sigmoid) {
-            for (int e = lane; e < a.E; e += 32) key_of(e);
+        } else {
+            for (int e = lane; e < a.E; e += 32) ord_s[warp * Epad + e] = key_of(e);
         }
         __syncwarp();
-        uint32_t taken = 0u;                              // of this lane's E / 32 <= 32 places
         for (int k = 0; k < a.top_k; ++k) {
             uint32_t best = 0u;
             int at = 0x7fffffff;
@@ -248,11 +276,9 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
                     at = lane + 32;
                 }
             } else {
-                for (int j = 0, e = lane; e < a.E; ++j, e += 32) {
-                    if ((taken >> j) & 1u) continue;
-                    float v = key[e];
-                    if (a.sigmoid && a.sel != nullptr) v = __fadd_rn(v, __ldg(a.sel + e));
-                    const uint32_t u = order_key(v);
+                // (taken ones are 0)
+                for (int e = lane; e < a.E; e += 32) {
+                    const uint32_t u = ord_s[warp * Epad + e];
                     if (u > best) {
                         best = u;
                         at = e;
@@ -262,7 +288,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArg
             const uint32_t win = __reduce_max_sync(0xffffffffu, best);
             const int id = static_cast<int>(__reduce_min_sync(0xffffffffu, best == win ? static_cast<unsigned>(at) : 0x7fffffffu));
             if (at == id) {
-                if (!small) taken |= 1u << (id >> 5);
+                if (!small) ord_s[warp * Epad + id] = 0u;
                 else if (id < 32) mine0 = 0u;
                 else mine1 = 0u;
             }

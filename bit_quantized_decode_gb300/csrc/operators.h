@@ -100,15 +100,13 @@ constexpr int kRtMaxTok = 4;                    // tokens per cluster at most
 constexpr int kRtMaxCluster = 16;
 
 // Words that the experts kernel finds prepared: a zero ticket counter, then
-// values that no result takes (fp32 NaN with all bits set, the code -128), by
-// which a reader sees that a word has not been written yet.
+// a value that no result takes (the fp32 NaN with all bits set), by which a
+// reader sees that a word has not been written yet.
 constexpr int kMxHead = 32;                     // words: the ticket counter and padding
 constexpr unsigned kMxNoValue = 0xffffffffu;
-constexpr unsigned kMxNoCodes = 0x80808080u;
 struct MoeFill {
     uint4* p;
-    unsigned values;          // 16-byte words of fp32 values behind the head
-    unsigned codes;           // 16-byte words of codes behind those
+    unsigned values;          // 16-byte words of values behind the head
 };
 
 struct RouteArgs {
@@ -131,10 +129,10 @@ struct RouteArgs {
     float* sx;                // [M], or null
     MoeFill fill;             // the experts kernel's workspace, prepared here (words 0: none)
 };
-// x as fp32, the partial sums of an expert's warps, the logits (cluster leader), block sums.
+// x as fp32, the partial sums of an expert's warps, logits and selection keys (cluster leader), block sums.
 __host__ __device__ inline int route_smem(int tok, int K, int E)
 {
-    return 4 * (tok * K + kRtWarps * kRtMaxTok * 2 + tok * ((E + 3) & ~3) + 2 * kRtWarps * kRtMaxTok);
+    return 4 * (tok * K + kRtWarps * kRtMaxTok * 2 + 2 * tok * ((E + 3) & ~3) + 2 * kRtWarps * kRtMaxTok);
 }
 cudaError_t launch_moe_route(const RouteArgs& a, int xtype, bool pdl, cudaStream_t s);
 
@@ -166,11 +164,10 @@ struct MoeArgs {
     float inv_t1, inv_t2, inv_seg, inv_add;   // 1 / (tiles of a gate/up and of a down matrix, quantizing tasks of a
                               // pair, adding tasks of a token)
     unsigned* ticket;         // zero at the start
-    float* sh;                // [pairs] scales of the hidden codes            (these four: kMxNoValue /
-    float* h;                 // [pairs][I]                                      kMxNoCodes at the start)
+    float* h;                 // [pairs][I], kMxNoValue at the start, and so
     float* part;              // [pairs][H]
-    int8_t* qh;               // [pairs][Ip]
-    int Ip;                   // I rounded up to 128: no L1 line holds codes of two pairs
+    unsigned long long* qdone;   // [pairs][quantizing tasks]: scale and code sum of a finished piece
+    int8_t* qh;               // [pairs][I] codes
     unsigned* err;
 };
 // `tok`: pairs per entry (1, 2, 4 or 8).  Warps per block and ring slots per warp follow from it.

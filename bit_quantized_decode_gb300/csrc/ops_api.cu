@@ -3,6 +3,7 @@
 // synchronises.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/w4a8.h"
@@ -101,16 +102,20 @@ w4_status check_router(const w4_router* r, int M, int K)
     return W4_OK;
 }
 
-// Tokens per cluster (as many as fit, up to four), blocks per cluster and
-// warps per expert: up to 16 blocks, so that the logits of a token spread over
-// as many warps as one cluster has.
+// Blocks per cluster, tokens per cluster and warps per expert.  Up to four
+// tokens spread their logits over clusters of 16 blocks; more tokens take the
+// portable 8 (a cluster of 16 fills most of a GPC, and few of them run at once:
+// 16 tokens over 256 experts took 25 us so).  As few tokens to a cluster as the
+// SMs allow.
 bool plan_route(const DeviceFacts& d, RouteArgs& a)
 {
-    a.tok = a.M >= 3 ? 4 : a.M >= 2 ? 2 : 1;
+    const int most = a.M <= 4 ? kRtMaxCluster : 8;
+    a.cluster = 1;
+    while (a.cluster < most && 2 * a.cluster <= a.E) a.cluster *= 2;
+    a.tok = 1;
+    while (a.tok < kRtMaxTok && (a.M + a.tok - 1) / a.tok * a.cluster > d.sms) a.tok *= 2;
     while (a.tok > 1 && route_smem(a.tok, a.K, a.E) > d.smem_optin) a.tok /= 2;
     if (route_smem(a.tok, a.K, a.E) > d.smem_optin) return false;
-    a.cluster = 1;
-    while (a.cluster < kRtMaxCluster && 2 * a.cluster <= a.E) a.cluster *= 2;
     a.parts = 1;
     while (a.parts < kRtWarps && kRtWarps / (2 * a.parts) * a.cluster >= a.E) a.parts *= 2;
     return true;
@@ -176,26 +181,38 @@ w4_status check_expert_pointers(const w4_experts* e, const float* residual, cons
     return W4_OK;
 }
 
-// Parts of the workspace: the ticket counter, then scales, h and the slots'
-// outputs (fp32), then the codes of h.
+// Parts of the workspace: the ticket counter, then (prepared) h, the slots'
+// outputs and the quantizing tasks' results, then the codes of h.
 struct MoeSpace {
-    size_t h, part, qh, total;
-    int Ip;
+    size_t h, part, qdone, qh, total;
 };
 MoeSpace moe_space(const w4_experts* e, int M, int top_k)
 {
     const size_t P = static_cast<size_t>(M) * (top_k + e->n_shared);
+    const size_t nseg = static_cast<size_t>((e->I + kMxSeg - 1) / kMxSeg);
     MoeSpace w;
-    w.Ip = (e->I + 127) / 128 * 128;
-    w.h = kMxHead * 4 + (P * 4 + 127) / 128 * 128;
+    w.h = kMxHead * 4;
     w.part = w.h + P * e->I * 4;
-    w.qh = w.part + P * e->H * 4;
-    w.total = w.qh + P * w.Ip;
+    w.qdone = w.part + P * e->H * 4;
+    w.qh = w.qdone + (P * nseg * 8 + 127) / 128 * 128;
+    w.total = w.qh + P * e->I;
     return w;
 }
 MoeFill moe_fill_of(const MoeSpace& w, void* ws)
 {
-    return MoeFill{static_cast<uint4*>(ws), static_cast<unsigned>((w.qh - kMxHead * 4) / 16), static_cast<unsigned>((w.total - w.qh) / 16)};
+    return MoeFill{static_cast<uint4*>(ws), static_cast<unsigned>((w.qh - kMxHead * 4) / 16)};
+}
+
+// Pairs per entry (an expert and some of its tokens, whose weights are read
+// once): no more than there are tokens, and no more than an expert has as a
+// rule.  Four leave registers for 20 warps per SM instead of 16, and a further
+// entry reads its weights from L2.
+int moe_entry_pairs(int M, int top_k, int E, int n_shared)
+{
+    if (M <= 2) return M < 1 ? 1 : M;
+    const double reached = 1.0 - pow(1.0 - static_cast<double>(top_k < E ? top_k : E) / E, M);   // share of the experts
+    const double each = static_cast<double>(M) * top_k / (E * reached);
+    return M <= 4 || (n_shared == 0 && each <= 3.0) ? 4 : kMxTok;
 }
 
 w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, const int* ids, const float* weights, int M,
@@ -227,14 +244,12 @@ w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, co
     a.S = e->n_shared;
     a.top_k = top_k;
     a.ticket = reinterpret_cast<unsigned*>(base);
-    a.sh = reinterpret_cast<float*>(base + kMxHead * 4);
     a.h = reinterpret_cast<float*>(base + w.h);
     a.part = reinterpret_cast<float*>(base + w.part);
+    a.qdone = reinterpret_cast<unsigned long long*>(base + w.qdone);
     a.qh = reinterpret_cast<int8_t*>(base + w.qh);
-    a.Ip = w.Ip;
     a.err = d.err;
-    // entries of as many pairs as there are tokens (a token's experts are distinct, as a rule)
-    const int tok = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : kMxTok;
+    const int tok = moe_entry_pairs(M, top_k, e->E, e->n_shared);
     const int warps = moe_warps(tok);
     a.inv_t1 = 1.0f / static_cast<float>((e->I + 3) / 4);
     a.inv_t2 = 1.0f / static_cast<float>((e->H + 7) / 8);
@@ -344,7 +359,7 @@ w4_status w4_moe_experts(const w4_experts* e, const int8_t* qx, const float* sx,
     r = check_expert_pointers(e, residual, y, y_type);
     if (r == W4_ERR_INVALID_ARG || !qx || !sx || !ids || !weights || !workspace) return W4_ERR_INVALID_ARG;
     if (ws_bytes < w4_moe_workspace_bytes(e, M, top_k)) return W4_ERR_UNSUPPORTED_SHAPE;
-    if (r != W4_OK || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 128))
+    if (r != W4_OK || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 16))
         return W4_ERR_MISALIGNED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
     r = cuda_status(launch_moe_fill(moe_fill_of(moe_space(e, M, top_k), workspace), (flags & W4_FLAG_PDL) != 0, s));
@@ -366,7 +381,7 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
     const w4_status se = check_expert_pointers(e, residual, y, y_type);
     if (st == W4_ERR_INVALID_ARG || se == W4_ERR_INVALID_ARG || !qx || !workspace) return W4_ERR_INVALID_ARG;
     if (ws_bytes < w4_moe_workspace_bytes(e, M, r->top_k)) return W4_ERR_UNSUPPORTED_SHAPE;
-    if (st != W4_OK || se != W4_OK || !aligned(workspace, 128)) return W4_ERR_MISALIGNED;
+    if (st != W4_OK || se != W4_OK || !aligned(workspace, 16)) return W4_ERR_MISALIGNED;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
     st = run_route(r, x, x_type, M, e->H, ids, weights, qx, sx, moe_fill_of(moe_space(e, M, r->top_k), workspace),
                    (flags & W4_FLAG_PDL) != 0, cs);

@@ -79,9 +79,9 @@ __device__ __forceinline__ uint2 quant8(const float (&t)[8], const A8Scale& ks)
 // The experts kernel's workspace (MoeFill), by the whole grid.
 __device__ __forceinline__ void moe_fill(const MoeFill& f)
 {
-    const unsigned head = kMxHead / 4, n = f.p != nullptr ? head + f.values + f.codes : 0u;
+    const unsigned head = kMxHead / 4, n = f.p != nullptr ? head + f.values : 0u;
     for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
-        const unsigned v = i < head ? 0u : i < head + f.values ? kMxNoValue : kMxNoCodes;
+        const unsigned v = i < head ? 0u : kMxNoValue;
         f.p[i] = make_uint4(v, v, v, v);
     }
 }

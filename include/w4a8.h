@@ -502,7 +502,7 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
  *     fmt: W4_FMT_W4 or W4_FMT_W8; glu: W4_GLU_SILU or W4_GLU_GELU_TANH;
  *     H % 32 == 0, I % 32 == 0; E + n_shared <= 1024, n_shared <= 4.
  *   residual: float [M][H] or NULL (may be y itself where y is W4_F32).
- *   workspace: w4_moe_workspace_bytes(..) bytes, 128-byte aligned, with no
+ *   workspace: w4_moe_workspace_bytes(..) bytes, 16-byte aligned, with no
  *     contents to keep; calls that share one must not overlap on the GPU.
  * Two launches (the first prepares the workspace).  The kernel waits
  * on its own blocks' progress with bounded waits (see w4_device_error), but
