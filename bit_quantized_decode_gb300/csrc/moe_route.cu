@@ -49,10 +49,10 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kRtAhead = 8;                     // float4 of router weights that a lane holds before the wait
+constexpr int kRtAhead = 4;                     // float4 of router weights that a lane holds before the wait
 
 template <int XT, int TG>
-__global__ void __launch_bounds__(kRtThreads, 1) moe_route_kernel(const RouteArgs a)
+__global__ void __launch_bounds__(kRtThreads, 2) moe_route_kernel(const RouteArgs a)
 {
     extern __shared__ __align__(16) float rsm[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

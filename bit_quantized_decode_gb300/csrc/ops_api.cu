@@ -102,18 +102,18 @@ w4_status check_router(const w4_router* r, int M, int K)
     return W4_OK;
 }
 
-// Blocks per cluster, tokens per cluster and warps per expert.  Up to four
-// tokens spread their logits over clusters of 16 blocks; more tokens take the
-// portable 8 (a cluster of 16 fills most of a GPC, and few of them run at once:
-// 16 tokens over 256 experts took 25 us so).  As few tokens to a cluster as the
-// SMs allow.
+// Blocks per cluster, tokens per cluster and warps per expert.  A token's
+// logits spread over a cluster of 16 blocks while all clusters run at once, up
+// to eight tokens (8 tokens, 256 experts of 1536: 10.5 us, with clusters of 8
+// 13.5 us); more tokens take clusters of 8 (16 tokens: 14.9 against 17.9 us).
+// As few tokens to a cluster as two blocks per SM allow.
 bool plan_route(const DeviceFacts& d, RouteArgs& a)
 {
-    const int most = a.M <= 4 ? kRtMaxCluster : 8;
+    const int most = a.M <= 8 ? kRtMaxCluster : 8;
     a.cluster = 1;
     while (a.cluster < most && 2 * a.cluster <= a.E) a.cluster *= 2;
     a.tok = 1;
-    while (a.tok < kRtMaxTok && (a.M + a.tok - 1) / a.tok * a.cluster > d.sms) a.tok *= 2;
+    while (a.tok < kRtMaxTok && (a.M + a.tok - 1) / a.tok * a.cluster > 2 * d.sms) a.tok *= 2;
     while (a.tok > 1 && route_smem(a.tok, a.K, a.E) > d.smem_optin) a.tok /= 2;
     if (route_smem(a.tok, a.K, a.E) > d.smem_optin) return false;
     a.parts = 1;
