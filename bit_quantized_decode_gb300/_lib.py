@@ -606,18 +606,16 @@ def w8a32_gemv(w, s_w, bias, x, y, flags: int = 0, stream=None):
 
 
 # -------------------------------------------- INT8 x INT8, any number of tokens
-def _check_tensors(**specs):
-    """Each keyword: (tensor or None, dtypes, shape or None).  Contiguous, of one of the dtypes, of the shape, on the
+def _check_tensors(*specs):
+    """Each spec: (name, tensor or None, dtypes, shape or None).  Contiguous, of one of the dtypes, of the shape, on the
     current CUDA device."""
-    cur = None
-    for name, (t, dtypes, shape) in specs.items():
+    cur = torch.cuda.current_device()
+    for name, t, dtypes, shape in specs:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{name}: tensor must live on a CUDA device")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.device.index != cur:
+        if t.get_device() != cur:
+            if not t.is_cuda:
+                raise ValueError(f"{name}: tensor must live on a CUDA device")
             raise ValueError(f"{name}: tensor lives on {t.device}, the current device is cuda:{cur}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: tensor must be contiguous")
@@ -625,6 +623,16 @@ def _check_tensors(**specs):
             raise ValueError(f"{name}: dtype {t.dtype} is not one of {[str(d) for d in dtypes]}")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
+    return cur
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    """The stream's handle: the given one's, or the current one's of `device`."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 _F32 = (torch.float32,)
@@ -647,11 +655,12 @@ def w8a8_matmul(w, s_w, bias, qx, sx, y, workspace, stream=None):
     """y [M][N] (fp32, fp16 or bf16) from per-row INT8 weights (w8_repack) and int8 codes qx [M][K], sx [M]."""
     M, K = qx.shape
     N = y.shape[1]
-    _check_tensors(w=(w, _U8, None), s_w=(s_w, _F32, (N,)), bias=(bias, _F32, (N,)), qx=(qx, _I8, None),
-                   sx=(sx, _F32, (M,)), y=(y, _FLOATS, (M, N)), workspace=(workspace, _U8, None))
+    dev = _check_tensors(("w", w, _U8, None), ("s_w", s_w, _F32, (N,)), ("bias", bias, _F32, (N,)),
+                         ("qx", qx, _I8, None), ("sx", sx, _F32, (M,)), ("y", y, _FLOATS, (M, N)),
+                         ("workspace", workspace, _U8, None))
     _w8_sizes(w, N, K)
-    _check("w8a8_matmul", load().w8a8_matmul(_ptr(w), _ptr(s_w), _ptr(bias), _ptr(qx), _ptr(sx), M, N, K, _ptr(y),
-                                             ELEM_TYPES[y.dtype], _ptr(workspace), workspace.numel(), _stream(stream)))
+    _check("w8a8_matmul", load().w8a8_matmul(_addr(w), _addr(s_w), _addr(bias), _addr(qx), _addr(sx), M, N, K, _addr(y),
+                                             ELEM_TYPES[y.dtype], _addr(workspace), workspace.numel(), _raw_stream(stream, dev)))
 
 
 def w8a8_linear(w, s_w, bias, x, y, qx, sx, workspace, norm=None, eps: float = 0.0, residual=None, flags: int = 0,
@@ -661,17 +670,18 @@ def w8a8_linear(w, s_w, bias, x, y, qx, sx, workspace, norm=None, eps: float = 0
     qx: int8 [M][K] to receive the codes, or None."""
     M, K = x.shape
     N = y.shape[1]
-    _check_tensors(w=(w, _U8, None), s_w=(s_w, _F32, (N,)), bias=(bias, _F32, (N,)), x=(x, _FLOATS, None),
-                   y=(y, _FLOATS, (M, N)), qx=(qx, _I8, (M, K)), sx=(sx, _F32, (M,)), workspace=(workspace, _U8, None),
-                   norm=(norm, _F32, (K,)), residual=(residual, _F32, (M, N)))
+    dev = _check_tensors(("w", w, _U8, None), ("s_w", s_w, _F32, (N,)), ("bias", bias, _F32, (N,)),
+                         ("x", x, _FLOATS, None), ("y", y, _FLOATS, (M, N)), ("qx", qx, _I8, (M, K)),
+                         ("sx", sx, _F32, (M,)), ("workspace", workspace, _U8, None), ("norm", norm, _F32, (K,)),
+                         ("residual", residual, _F32, (M, N)))
     _w8_sizes(w, N, K)
     fz = None
     if norm is not None or residual is not None:
         fz = ctypes.byref(Fusion(None if norm is None else norm.data_ptr(), float(eps), W4_GLU_NONE,
                                  None if residual is None else residual.data_ptr()))
-    _check("w8a8_linear", load().w8a8_linear(_ptr(w), _ptr(s_w), _ptr(bias), _ptr(x), ELEM_TYPES[x.dtype], M, N, K,
-                                             _ptr(y), ELEM_TYPES[y.dtype], _ptr(qx), _ptr(sx), fz, flags,
-                                             _ptr(workspace), workspace.numel(), _stream(stream)))
+    _check("w8a8_linear", load().w8a8_linear(_addr(w), _addr(s_w), _addr(bias), _addr(x), ELEM_TYPES[x.dtype], M, N, K,
+                                             _addr(y), ELEM_TYPES[y.dtype], _addr(qx), _addr(sx), fz, flags,
+                                             _addr(workspace), workspace.numel(), _raw_stream(stream, dev)))
 
 
 # ------------------------------------------------- mixture of experts, few tokens
@@ -681,9 +691,9 @@ def w8_glu_repacked_bytes(I: int, K: int) -> int:
 
 def w8_repack_glu(gate, up, K, out, stream=None):
     """int8 codes of gate and up [I][K] -> the paired device layout (the experts of w4_moe_experts)."""
-    _check_tensors(gate=(gate, _I8, None), up=(up, _I8, gate.shape), out=(out, _U8, None))
-    _check("w8_repack_glu", load().w8_repack_glu(_ptr(gate), _ptr(up), gate.shape[0], K, _ptr(out), out.numel(),
-                                                 _stream(stream)))
+    dev = _check_tensors(("gate", gate, _I8, None), ("up", up, _I8, gate.shape), ("out", out, _U8, None))
+    _check("w8_repack_glu", load().w8_repack_glu(_addr(gate), _addr(up), gate.shape[0], K, _addr(out), out.numel(),
+                                                 _raw_stream(stream, dev)))
 
 
 _I32 = (torch.int32,)
@@ -693,7 +703,7 @@ def moe_router(w, top_k: int, select_bias=None, score: str = "softmax", renormal
                norm=None, eps: float = 1e-6):
     """A w4_router descriptor: w float32 [E][K].  It holds references to its tensors."""
     E, K = w.shape
-    _check_tensors(w=(w, _F32, None), select_bias=(select_bias, _F32, (E,)), norm=(norm, _F32, (K,)))
+    _check_tensors(("w", w, _F32, None), ("select_bias", select_bias, _F32, (E,)), ("norm", norm, _F32, (K,)))
     r = Router(None if norm is None else norm.data_ptr(), float(eps), w.data_ptr(),
                None if select_bias is None else select_bias.data_ptr(), E, int(top_k), ROUTE_SCORES[score],
                int(bool(renormalize)), float(scale))
@@ -706,8 +716,9 @@ def moe_experts(fmt: str, w_gu, s_gu, w_dn, s_dn, E: int, n_shared: int, H: int,
     n = E + n_shared
     gu_bytes, dn_bytes = ((w4_glu_repacked_bytes(I, H), w4_repacked_bytes(H, I)) if fmt == "w4"
                           else (w8_glu_repacked_bytes(I, H), w8_repacked_bytes(H, I)))
-    _check_tensors(w_gu=(w_gu, _U8, (n * gu_bytes,)), s_gu=(s_gu, _F32, (n, 2 * I)), b_gu=(b_gu, _F32, (n, 2 * I)),
-                   w_dn=(w_dn, _U8, (n * dn_bytes,)), s_dn=(s_dn, _F32, (n, H)), b_dn=(b_dn, _F32, (n, H)))
+    dev = _check_tensors(("w_gu", w_gu, _U8, (n * gu_bytes,)), ("s_gu", s_gu, _F32, (n, 2 * I)),
+                         ("b_gu", b_gu, _F32, (n, 2 * I)), ("w_dn", w_dn, _U8, (n * dn_bytes,)),
+                         ("s_dn", s_dn, _F32, (n, H)), ("b_dn", b_dn, _F32, (n, H)))
     e = Experts(EXPERT_FORMATS[fmt], E, n_shared, H, I, glu, w_gu.data_ptr(), s_gu.data_ptr(),
                 None if b_gu is None else b_gu.data_ptr(), w_dn.data_ptr(), s_dn.data_ptr(),
                 None if b_dn is None else b_dn.data_ptr())
@@ -721,10 +732,11 @@ def w4_moe_route(router, x, ids, weights, qx=None, sx=None, flags: int = 0, stre
     M, K = x.shape
     if K != router._K:
         raise ValueError(f"x has {K} columns, the router takes {router._K}")
-    _check_tensors(x=(x, _FLOATS, None), ids=(ids, _I32, (M, router.top_k)), weights=(weights, _F32, (M, router.top_k)),
-                   qx=(qx, _I8, (M, K)), sx=(sx, _F32, (M,)))
-    _check("w4_moe_route", load().w4_moe_route(ctypes.byref(router), _ptr(x), ELEM_TYPES[x.dtype], M, K, _ptr(ids),
-                                               _ptr(weights), _ptr(qx), _ptr(sx), flags, _stream(stream)))
+    dev = _check_tensors(("x", x, _FLOATS, None), ("ids", ids, _I32, (M, router.top_k)),
+                         ("weights", weights, _F32, (M, router.top_k)), ("qx", qx, _I8, (M, K)),
+                         ("sx", sx, _F32, (M,)))
+    _check("w4_moe_route", load().w4_moe_route(ctypes.byref(router), _addr(x), ELEM_TYPES[x.dtype], M, K, _addr(ids),
+                                               _addr(weights), _addr(qx), _addr(sx), flags, _raw_stream(stream, dev)))
 
 
 def w4_moe_workspace_bytes(experts, M: int, top_k: int) -> int:
@@ -735,11 +747,12 @@ def w4_moe_experts(experts, qx, sx, ids, weights, y, workspace, residual=None, f
     """y [M][H] of the experts ids [M][top_k] with weights, on codes qx [M][H], sx [M]."""
     M, top_k = ids.shape
     H = experts.H
-    _check_tensors(qx=(qx, _I8, (M, H)), sx=(sx, _F32, (M,)), ids=(ids, _I32, None), weights=(weights, _F32, (M, top_k)),
-                   y=(y, _FLOATS, (M, H)), workspace=(workspace, _U8, None), residual=(residual, _F32, (M, H)))
-    _check("w4_moe_experts", load().w4_moe_experts(ctypes.byref(experts), _ptr(qx), _ptr(sx), _ptr(ids), _ptr(weights), M,
-                                                   top_k, _ptr(residual), _ptr(y), ELEM_TYPES[y.dtype], _ptr(workspace),
-                                                   workspace.numel(), flags, _stream(stream)))
+    dev = _check_tensors(("qx", qx, _I8, (M, H)), ("sx", sx, _F32, (M,)), ("ids", ids, _I32, None),
+                         ("weights", weights, _F32, (M, top_k)), ("y", y, _FLOATS, (M, H)),
+                         ("workspace", workspace, _U8, None), ("residual", residual, _F32, (M, H)))
+    _check("w4_moe_experts", load().w4_moe_experts(ctypes.byref(experts), _addr(qx), _addr(sx), _addr(ids), _addr(weights), M,
+                                                   top_k, _addr(residual), _addr(y), ELEM_TYPES[y.dtype], _addr(workspace),
+                                                   workspace.numel(), flags, _raw_stream(stream, dev)))
 
 
 def w4_moe_layer(router, experts, x, ids, weights, qx, sx, y, workspace, residual=None, flags: int = 0, stream=None):
@@ -747,13 +760,14 @@ def w4_moe_layer(router, experts, x, ids, weights, qx, sx, y, workspace, residua
     M, H = x.shape
     if H != router._K or H != experts.H:
         raise ValueError(f"x has {H} columns, the router takes {router._K}, the experts {experts.H}")
-    _check_tensors(x=(x, _FLOATS, None), ids=(ids, _I32, (M, router.top_k)), weights=(weights, _F32, (M, router.top_k)),
-                   qx=(qx, _I8, (M, H)), sx=(sx, _F32, (M,)), y=(y, _FLOATS, (M, H)), workspace=(workspace, _U8, None),
-                   residual=(residual, _F32, (M, H)))
-    _check("w4_moe_layer", load().w4_moe_layer(ctypes.byref(router), ctypes.byref(experts), _ptr(x), ELEM_TYPES[x.dtype], M,
-                                               _ptr(ids), _ptr(weights), _ptr(qx), _ptr(sx), _ptr(residual), _ptr(y),
-                                               ELEM_TYPES[y.dtype], _ptr(workspace), workspace.numel(), flags,
-                                               _stream(stream)))
+    dev = _check_tensors(("x", x, _FLOATS, None), ("ids", ids, _I32, (M, router.top_k)),
+                         ("weights", weights, _F32, (M, router.top_k)), ("qx", qx, _I8, (M, H)),
+                         ("sx", sx, _F32, (M,)), ("y", y, _FLOATS, (M, H)), ("workspace", workspace, _U8, None),
+                         ("residual", residual, _F32, (M, H)))
+    _check("w4_moe_layer", load().w4_moe_layer(ctypes.byref(router), ctypes.byref(experts), _addr(x), ELEM_TYPES[x.dtype], M,
+                                               _addr(ids), _addr(weights), _addr(qx), _addr(sx), _addr(residual), _addr(y),
+                                               ELEM_TYPES[y.dtype], _addr(workspace), workspace.numel(), flags,
+                                               _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- chains
