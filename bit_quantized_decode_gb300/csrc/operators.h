@@ -93,6 +93,40 @@ __host__ __device__ inline Gemm8Smem gemm8_smem(int stages, int nt, int splits)
 }
 cudaError_t launch_gemm_w8(Gemm8Args& a, int grid, size_t smem, bool pdl, cudaStream_t s);
 
+// ------------------------------- INT8 x INT8 product of up to eight tokens (gemv_w8.cu)
+constexpr int kV8Warps = 12;
+constexpr int kV8Threads = kV8Warps * 32;
+constexpr int kV8MaxTok = 8;
+constexpr int kV8FusedTok = 2;                  // tokens that the kernel quantizes itself, at most,
+constexpr int kV8FusedValues = 16384;           // and activations (two tokens of 3584: 6.7 us, of 18944: 18.8 against 15.3 us)
+
+struct Gemv8Args {
+    const uint8_t* w;         // w8_repack units
+    const float* s_w;         // [N]
+    const float* bias;        // [N] or null
+    const void* x;            // [M][K] of xtype (fused), else null
+    int xtype;
+    const float* gamma;       // RMSNorm weight (fused), or null
+    float eps;
+    const int8_t* qx_in;      // [M][K] codes (not fused)
+    const float* sx_in;       // [M]
+    int8_t* qx_out;           // fused: block 0 writes the codes here, or null
+    float* sx_out;            // fused: and the scales
+    const float* residual;    // [M][N] or null
+    void* y;
+    int ytype;
+    int M, N, K;
+    int share;                // warps per row tile (1, 2 or 4): each a share of K
+    int slot;                 // bytes of a ring slot
+    unsigned* err;
+};
+// Ring of two slots per warp, the codes, partial sums, scales, block sums, barriers.
+__host__ __device__ inline int gemv8_smem(int slot, int M, int K)
+{
+    return kV8Warps * 2 * slot + M * K + kV8Warps * 8 * kV8MaxTok * 4 + 16 * kV8MaxTok + 4 * 4 * kV8Warps + (2 * kV8Warps + 1) * 8 + 64;
+}
+cudaError_t launch_gemv_w8(const Gemv8Args& a, int grid, size_t smem, bool pdl, cudaStream_t s);
+
 // ------------------------------------------------ expert router (moe_route.cu)
 constexpr int kRtThreads = 512;
 constexpr int kRtWarps = kRtThreads / 32;

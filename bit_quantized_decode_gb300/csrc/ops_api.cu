@@ -56,6 +56,24 @@ bool plan_gemm8(const DeviceFacts& d, Gemm8Args& a, int& grid, size_t& smem)
     return smem <= static_cast<size_t>(d.smem_optin);
 }
 
+// A product of up to eight tokens that the DP4A kernel takes; false where the
+// codes leave no room for its rings.
+bool plan_gemv8(const DeviceFacts& d, Gemv8Args& a, int& grid, size_t& smem)
+{
+    if (a.M > kV8MaxTok) return false;
+    a.slot = 8192;
+    while (a.slot > 4096 && gemv8_smem(a.slot, a.M, a.K) > d.smem_optin) a.slot /= 2;
+    smem = static_cast<size_t>(gemv8_smem(a.slot, a.M, a.K));
+    if (smem > static_cast<size_t>(d.smem_optin)) return false;
+    // warps to a tile: as many as there are warps for, each with 1024 K or more
+    const int T = (a.N + 7) / 8, C = a.K / 32;
+    a.share = 1;
+    while (a.share < 4 && 2 * a.share * static_cast<long long>(T) <= static_cast<long long>(d.sms) * kV8Warps && C >= 64 * a.share)
+        a.share *= 2;
+    grid = T < d.sms ? T : d.sms;
+    return true;
+}
+
 w4_status run_gemm8(const void* w, const float* s_w, const float* bias, const uint4* xh, const float* sx,
                     const float* residual, int M, int N, int K, void* y, int y_type, cudaStream_t s)
 {
@@ -288,6 +306,25 @@ w4_status w8a8_matmul(const void* w, const float* s_w, const float* bias, const 
     if (ws_bytes < w8a8_workspace_bytes(M, N, K)) return W4_ERR_UNSUPPORTED_SHAPE;
     if (r != W4_OK || !aligned(qx, 16) || !aligned(sx, 4) || !aligned(workspace, 16)) return W4_ERR_MISALIGNED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
+    DeviceFacts d;
+    if (!device_facts(&d)) return W4_ERR_CUDA;
+    int grid = 0;
+    size_t smem = 0;
+    Gemv8Args v = {};
+    v.M = M;
+    v.N = N;
+    v.K = K;
+    if (plan_gemv8(d, v, grid, smem)) {
+        v.w = static_cast<const uint8_t*>(w);
+        v.s_w = s_w;
+        v.bias = bias;
+        v.qx_in = qx;
+        v.sx_in = sx;
+        v.y = y;
+        v.ytype = y_type;
+        v.err = d.err;
+        return cuda_status(launch_gemv_w8(v, grid, smem, false, s));
+    }
     uint4* xh = static_cast<uint4*>(workspace);
     r = cuda_status(launch_expand_codes(qx, M, K, xh, tile_tokens(M), false, s));
     if (r != W4_OK) return r;
@@ -314,18 +351,49 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
         (gamma && !aligned(gamma, 16)) || (residual && !aligned(residual, 4)))
         return W4_ERR_MISALIGNED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(st);
+    const bool pdl = (flags & W4_FLAG_PDL) != 0;
+    DeviceFacts d;
+    if (!device_facts(&d)) return W4_ERR_CUDA;
+    int grid = 0;
+    size_t smem = 0;
+    Gemv8Args v = {};
+    v.M = M;
+    v.N = N;
+    v.K = K;
+    const bool few = N > 0 && plan_gemv8(d, v, grid, smem);
+    if (few) {
+        v.w = static_cast<const uint8_t*>(w);
+        v.s_w = s_w;
+        v.bias = bias;
+        v.residual = residual;
+        v.y = y;
+        v.ytype = y_type;
+        v.err = d.err;
+        if (M == 1 || (M <= kV8FusedTok && M * K <= kV8FusedValues)) {
+            v.x = x;
+            v.xtype = x_type;
+            v.gamma = gamma;
+            v.eps = gamma != nullptr ? f->norm_eps : 0.0f;
+            v.qx_out = qx;
+            v.sx_out = sx;
+            return cuda_status(launch_gemv_w8(v, grid, smem, pdl, s));
+        }
+        v.qx_in = qx != nullptr ? qx : static_cast<int8_t*>(workspace);
+        v.sx_in = sx;
+    }
     QuantRowsArgs q = {};
     q.x = x;
     q.gamma = gamma;
     q.eps = gamma != nullptr ? f->norm_eps : 0.0f;
     q.M = M;
     q.K = K;
-    q.qx = qx;
+    q.qx = few ? const_cast<int8_t*>(v.qx_in) : qx;
     q.sx = sx;
-    q.xh = N > 0 ? static_cast<uint4*>(workspace) : nullptr;
+    q.xh = N > 0 && !few ? static_cast<uint4*>(workspace) : nullptr;
     q.nt = tile_tokens(M);
-    r = cuda_status(launch_quant_rows(q, x_type, (flags & W4_FLAG_PDL) != 0, s));
+    r = cuda_status(launch_quant_rows(q, x_type, pdl, s));
     if (r != W4_OK || N == 0) return r;
+    if (few) return cuda_status(launch_gemv_w8(v, grid, smem, true, s));
     return run_gemm8(w, s_w, bias, q.xh, sx, residual, M, N, K, y, y_type, s);
 }
 
