@@ -35,9 +35,11 @@ namespace w4k {
 namespace {
 
 constexpr uint64_t kG8WaitNs = 250ull * 1000ull * 1000ull;
-constexpr int kWarpMma = 1, kWarpConv = 4, kWarpEpi = 12;
+constexpr int kWarpMma = 1, kWarpConv = 2, kWarpEpi = 10;
 
-// One kind::f16 MMA (A in tensor memory, B from a shared-memory descriptor).
+// kind::f16 MMAs of one stage's K slices (A in tensor memory, eight columns to
+// a slice; B from shared-memory descriptors `bstep` apart in the address
+// field): eight in one statement, or one.
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate)
 {
@@ -47,21 +49,29 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+__device__ __forceinline__ void tc_mma_f16_ts_x8(uint32_t d, uint32_t a, uint64_t b, uint64_t bstep, uint32_t idesc,
+                                                 uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 q, %5, %5;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "add.u32 a1, a1, 8;\n\tadd.u64 b1, b1, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "add.u32 a1, a1, 8;\n\tadd.u64 b1, b1, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "add.u32 a1, a1, 8;\n\tadd.u64 b1, b1, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "add.u32 a1, a1, 8;\n\tadd.u64 b1, b1, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "add.u32 a1, a1, 8;\n\tadd.u64 b1, b1, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "add.u32 a1, a1, 8;\n\tadd.u64 b1, b1, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "l"(bstep), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 
 // Wait of a whole warp: a test first, as the phase is usually complete.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
 {
     bool ok = mbar_test_wait(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) ok = mbar_wait_bounded(bar, parity, kG8WaitNs);
-    return __all_sync(0xffffffffu, ok);
-}
-
-// The same for two barriers of equal phase.
-__device__ __forceinline__ bool warp_wait2(uint32_t bar, uint32_t bar2, uint32_t parity)
-{
-    bool ok = mbar_test_wait(bar, parity) & mbar_test_wait(bar2, parity);
-    if (!__all_sync(0xffffffffu, ok))
-        ok = mbar_wait_bounded(bar, parity, kG8WaitNs) && mbar_wait_bounded(bar2, parity, kG8WaitNs);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -239,30 +249,34 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         int it = 0, ac = 0, slot = 0;
         uint32_t sph = 0u;
         bool ok = true;
+        // core matrices of 8 tokens x 8 K (128 B): token groups 128 B apart, K groups nt * 16 B
+        const uint64_t bdesc0 = smem_desc_noswizzle(smem_u32(smem + L.ring) + kG8WBytes, static_cast<uint32_t>(nt * 16), 128u);
+        const uint64_t bstep = static_cast<uint64_t>(2 * nt);          // 16 K in the descriptor's address field
+        const uint64_t bslot = static_cast<uint64_t>(slot_bytes >> 4);
+        uint64_t bdesc = bdesc0;
+        uint32_t acol = tbase + col_a;
         for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
             int run = 0;                 // stages in the current accumulator
             for (int st = st0; st < st1; ++st, ++it) {
-                const int k16 = 2 * min(kG8StageChunks, A.C - st * kG8StageChunks);
                 const bool last = st + 1 == st1 || run == kG8AccStages - 1;
                 const uint32_t dcol = tbase + static_cast<uint32_t>((ac & 1) * nt);
                 if (run == 0 && ac >= 2) ok = warp_wait(acce_b + 8 * (ac & 1), static_cast<uint32_t>((ac >> 1) - 1) & 1u);
-                ok = ok && warp_wait2(full_b + 8 * slot, ready_b + 8 * slot, sph);
+                // converted, so landed: the converting warps saw the codes land with the weights
+                ok = ok && warp_wait(ready_b + 8 * slot, sph);
                 if (!ok) {
                     if (lane == 0) fail();
                     break;
                 }
                 tc_fence_after();
-                // core matrices of 8 tokens x 8 K (128 B): token groups 128 B apart, K groups nt * 16 B
-                const uint64_t bdesc = smem_desc_noswizzle(
-                    smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
-                    static_cast<uint32_t>(nt * 16), 128u);
-                const uint32_t acol = tbase + col_a + static_cast<uint32_t>(kG8ACols * slot);
                 if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < 2 * kG8StageChunks; ++kk)
-                        if (kk < k16)
-                            tc_mma_f16_ts(dcol, acol + 8 * kk, bdesc + static_cast<uint64_t>(kk * 2 * nt), idesc,
-                                          run == 0 && kk == 0 ? 0u : 1u);
+                    const uint32_t more = run == 0 ? 0u : 1u;
+                    if ((st + 1) * kG8StageChunks <= A.C) {
+                        tc_mma_f16_ts_x8(dcol, acol, bdesc, bstep, idesc, more);
+                    } else {
+                        const int k16 = 2 * (A.C - st * kG8StageChunks);
+                        for (int kk = 0; kk < k16; ++kk)
+                            tc_mma_f16_ts(dcol, acol + 8 * kk, bdesc + static_cast<uint64_t>(kk) * bstep, idesc, kk == 0 ? more : 1u);
+                    }
                     tc_commit(empty_b + 8 * slot);
                     if (last) tc_commit(accf_b + 8 * (ac & 1));
                 }
@@ -272,9 +286,13 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                     ++ac;
                     run = 0;
                 }
+                bdesc += bslot;
+                acol += kG8ACols;
                 if (++slot == S) {
                     slot = 0;
                     sph ^= 1u;
+                    bdesc = bdesc0;
+                    acol = tbase + col_a;
                 }
             }
         }
