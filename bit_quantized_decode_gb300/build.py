@@ -31,7 +31,7 @@ NVCC_FLAGS = [
     "-I", INCLUDE,
 ]
 SOURCES = ["gemv_w4.cu", "gemv_q4_0.cu", "gemv_q6g32.cu", "gemv_i8g32.cu", "gemv_a32.cu", "w4a8_api.cu",
-           "prep_kernels.cu", "gemv_tc.cu", "gemv_chain.cu", "hbm_read.cu", "quant_rows.cu", "gemm_w8.cu", "gemv_w8.cu", "moe_route.cu",
+           "prep_kernels.cu", "gemv_tc.cu", "gemv_chain.cu", "hbm_read.cu", "quant_rows.cu", "gemm_w8.cu", "gemm_w8_pair.cu", "gemv_w8.cu", "moe_route.cu",
            "moe_experts.cu", "ops_api.cu",
            "host_quant.cpp"]
 # host-only C++ (the host quantizers): IEEE arithmetic as written, no FMA contraction

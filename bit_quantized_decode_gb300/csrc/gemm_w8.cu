@@ -27,14 +27,11 @@
 
 #include <atomic>
 
-#include "operators.h"
-#include "ptx.cuh"
-#include "typed_io.cuh"
+#include "gemm_w8.cuh"
 
 namespace w4k {
 namespace {
 
-constexpr uint64_t kG8WaitNs = 250ull * 1000ull * 1000ull;
 constexpr int kWarpMma = 1, kWarpConv = 2, kWarpEpi = 10;
 
 // kind::f16 MMAs of one stage's K slices (A in tensor memory, eight columns to
@@ -65,32 +62,6 @@ __device__ __forceinline__ void tc_mma_f16_ts_x8(uint32_t d, uint32_t a, uint64_
         "add.u32 a1, a1, 8;\n\tadd.u64 b1, b1, %3;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "l"(bstep), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// Wait of a whole warp: a test first, as the phase is usually complete.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
-{
-    bool ok = mbar_test_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) ok = mbar_wait_bounded(bar, parity, kG8WaitNs);
-    return __all_sync(0xffffffffu, ok);
-}
-
-// Box of a 2-D tensor map -> shared memory.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t pol)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
-        "%3}], [%4], %5;" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar), "l"(pol)
-        : "memory");
-}
-
-// L2 policy for the activation codes, which every row group reads again.
-__device__ __forceinline__ uint64_t l2_policy_evict_last()
-{
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-    return p;
 }
 
 // Scales of a warp's tokens m + 32 b + i (b < 2, i < 16), token 16 b + i in lane 16 b + i.
@@ -331,16 +302,8 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < kG8StageChunks; ++e) {
                         if (e < nch) {
-                            const uint4 lo = hsel ? b[e] : a[e], hi = hsel ? a[e] : b[e];
                             uint32_t h[16];
-                            i8_to_f16(lo.x, h[0], h[1]);
-                            i8_to_f16(lo.y, h[2], h[3]);
-                            i8_to_f16(lo.z, h[4], h[5]);
-                            i8_to_f16(lo.w, h[6], h[7]);
-                            i8_to_f16(hi.x, h[8], h[9]);
-                            i8_to_f16(hi.y, h[10], h[11]);
-                            i8_to_f16(hi.z, h[12], h[13]);
-                            i8_to_f16(hi.w, h[14], h[15]);
+                            unit_f16(a[e], b[e], hsel, h);
                             tmem_st16(tbase + tlane + col_a + static_cast<uint32_t>(kG8ACols * slot + 16 * e), h);
                         }
                     }
@@ -454,10 +417,9 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
 
 }  // namespace
 
-namespace {
 // The weights as a 2-D array of 8-byte elements: a row per 8-row tile (C
 // chunks of 256 bytes), a box of 16 tiles x one stage.
-cudaError_t encode_wmap(Gemm8Args& a)
+cudaError_t encode_w8_map(Gemm8Args& a)
 {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -481,14 +443,13 @@ cudaError_t encode_wmap(Gemm8Args& a)
         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-}  // namespace
 
 cudaError_t launch_gemm_w8(Gemm8Args& a, int grid, size_t smem, bool pdl, cudaStream_t s)
 {
     auto kern = gemm_w8_kernel;
     static SmemLimit limit;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, smem);
-    if (e == cudaSuccess) e = encode_wmap(a);
+    if (e == cudaSuccess) e = encode_w8_map(a);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));

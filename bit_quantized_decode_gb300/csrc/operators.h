@@ -91,6 +91,29 @@ __host__ __device__ inline Gemm8Smem gemm8_smem(int stages, int nt, int splits)
     L.total = o;
     return L;
 }
+// The same product with pairs of blocks (cta_group::2) on tiles of 256 rows by
+// up to 192 tokens (gemm_w8_pair.cu); nt is then the tokens of one block, half
+// a tile.
+constexpr int kP8MaxTok = 192;
+constexpr int kP8Threads = 640;
+constexpr int kP8ABufs = 4;                     // converted half stages (64 K) in tensor memory
+constexpr int kP8ACols = 32;
+constexpr int kP8MaxStages = 8;
+struct Pair8Smem {
+    int ring, bars, tmem, total;
+};
+__host__ __device__ inline Pair8Smem pair8_smem(int stages, int nt)
+{
+    Pair8Smem L;
+    int o = 0;
+    L.ring = o;  o += stages * (kG8WBytes + nt * 64 * kG8StageChunks);
+    L.bars = o;  o += (2 * kP8MaxStages + 2 * kP8ABufs + 4) * 8;
+    L.tmem = o;  o += 16;
+    L.total = o;
+    return L;
+}
+cudaError_t launch_gemm_w8_pair(Gemm8Args& a, int grid, size_t smem, bool pdl, cudaStream_t s);
+cudaError_t encode_w8_map(Gemm8Args& a);
 cudaError_t launch_gemm_w8(Gemm8Args& a, int grid, size_t smem, bool pdl, cudaStream_t s);
 
 // ------------------------------- INT8 x INT8 product of up to eight tokens (gemv_w8.cu)

@@ -21,12 +21,10 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 inline w4_status cuda_status(cudaError_t e) { return e == cudaSuccess ? W4_OK : W4_ERR_CUDA; }
 inline bool elem_type(int t) { return t == W4_F32 || t == W4_F16 || t == W4_BF16; }
 
-// Token tiles of a call: as few as hold M, evenly filled, in sixteens.
-inline int token_tiles(int M) { return (M + kG8MaxTok - 1) / kG8MaxTok; }
-inline int tile_tokens(int M)
+// Tokens that the fp16 codes of a call may take: M, and up to a tile's padding.
+inline size_t padded_tokens(int M)
 {
-    const int n = token_tiles(M);
-    return n > 0 ? ((M + n - 1) / n + 15) / 16 * 16 : 16;
+    return M <= 16 ? 16 : static_cast<size_t>(M) + kP8MaxTok;
 }
 
 w4_status check_w8_shape(int M, int N, int K)
@@ -37,24 +35,62 @@ w4_status check_w8_shape(int M, int N, int K)
     return tiles > (1 << 30) ? W4_ERR_UNSUPPORTED_SHAPE : W4_OK;
 }
 
-// Tiles and K splits of an M x N x K product on a device of `sms` SMs.
-bool plan_gemm8(const DeviceFacts& d, Gemm8Args& a, int& grid, size_t& smem)
+// Tiles of an M x N x K product: 128 rows by up to 128 tokens to a block, with
+// K splits where tiles are few, or 256 rows by up to 192 tokens to a pair of
+// blocks.  A stage of either takes about the same time (4096 tokens, 37888 x
+// 3584: 870 us with blocks, 690 with pairs), so the one with fewer rounds of
+// tiles over the SMs is taken.
+bool plan_gemm8(const DeviceFacts& d, Gemm8Args& a, bool& pairs, int& grid, size_t& smem)
 {
+    auto tile = [&](int most, int step) {
+        const int n = (a.M + most - 1) / most;
+        return ((a.M + n - 1) / n + step - 1) / step * step;
+    };
     a.C = a.K / 32;
     a.T = (a.N + kRows - 1) / kRows;
-    a.n_g = (a.N + kG8Rows - 1) / kG8Rows;
-    a.n_tt = token_tiles(a.M);
-    a.nt = tile_tokens(a.M);
-    const int tiles = a.n_g * a.n_tt;
     const int nst = (a.C + kG8StageChunks - 1) / kG8StageChunks;
+    const int nt1 = tile(kG8MaxTok, 16), nt2 = tile(kP8MaxTok, 32);
+    const long long tiles1 = static_cast<long long>((a.N + kG8Rows - 1) / kG8Rows) * ((a.M + nt1 - 1) / nt1);
+    const long long tiles2 = static_cast<long long>((a.N + 2 * kG8Rows - 1) / (2 * kG8Rows)) * ((a.M + nt2 - 1) / nt2);
+    const int npairs = d.sms / 2;
+    pairs = a.M > kG8MaxTok && npairs > 0 && (tiles2 + npairs - 1) / npairs < (tiles1 + d.sms - 1) / d.sms;
     a.splits = 1;
-    while (a.splits < kG8MaxSplit && tiles * 2 * a.splits <= d.sms && nst >= 4 * a.splits) a.splits *= 2;
-    a.stages = gemm8_max_stages(a.nt) < kG8MaxStages ? gemm8_max_stages(a.nt) : kG8MaxStages;
-    while (a.stages > 2 && gemm8_smem(a.stages, a.nt, a.splits).total > d.smem_optin) --a.stages;
-    smem = static_cast<size_t>(gemm8_smem(a.stages, a.nt, a.splits).total);
-    grid = a.splits > 1 ? tiles * a.splits : (tiles < d.sms ? tiles : d.sms);
+    if (pairs) {
+        a.nt = nt2 / 2;
+        a.n_g = (a.N + 2 * kG8Rows - 1) / (2 * kG8Rows);
+        a.n_tt = (a.M + nt2 - 1) / nt2;
+        a.stages = kP8MaxStages;
+        while (a.stages > 2 && pair8_smem(a.stages, a.nt).total > d.smem_optin) --a.stages;
+        smem = static_cast<size_t>(pair8_smem(a.stages, a.nt).total);
+        grid = 2 * (tiles2 < npairs ? static_cast<int>(tiles2) : npairs);
+    } else {
+        a.nt = nt1;
+        a.n_g = (a.N + kG8Rows - 1) / kG8Rows;
+        a.n_tt = (a.M + nt1 - 1) / nt1;
+        while (a.splits < kG8MaxSplit && tiles1 * 2 * a.splits <= d.sms && nst >= 4 * a.splits) a.splits *= 2;
+        a.stages = gemm8_max_stages(a.nt) < kG8MaxStages ? gemm8_max_stages(a.nt) : kG8MaxStages;
+        while (a.stages > 2 && gemm8_smem(a.stages, a.nt, a.splits).total > d.smem_optin) --a.stages;
+        smem = static_cast<size_t>(gemm8_smem(a.stages, a.nt, a.splits).total);
+        grid = a.splits > 1 ? static_cast<int>(tiles1) * a.splits : tiles1 < d.sms ? static_cast<int>(tiles1) : d.sms;
+    }
     return smem <= static_cast<size_t>(d.smem_optin);
 }
+
+// The plan of a product: its tile arguments are needed before the codes are laid out.
+struct Gemm8Plan {
+    Gemm8Args a = {};
+    bool pairs = false;
+    int grid = 0;
+    size_t smem = 0;
+    bool make(const DeviceFacts& d, int M, int N, int K)
+    {
+        a.M = M;
+        a.N = N;
+        a.K = K;
+        a.err = d.err;
+        return plan_gemm8(d, a, pairs, grid, smem);
+    }
+};
 
 // A product of up to eight tokens that the DP4A kernel takes; false where the
 // codes leave no room for its rings.
@@ -74,28 +110,18 @@ bool plan_gemv8(const DeviceFacts& d, Gemv8Args& a, int& grid, size_t& smem)
     return true;
 }
 
-w4_status run_gemm8(const void* w, const float* s_w, const float* bias, const uint4* xh, const float* sx,
-                    const float* residual, int M, int N, int K, void* y, int y_type, cudaStream_t s)
+w4_status run_gemm8(Gemm8Plan& p, const void* w, const float* s_w, const float* bias, const uint4* xh, const float* sx,
+                    const float* residual, void* y, int y_type, cudaStream_t s)
 {
-    DeviceFacts d;
-    if (!device_facts(&d)) return W4_ERR_CUDA;
-    Gemm8Args a = {};
-    a.w = static_cast<const uint8_t*>(w);
-    a.s_w = s_w;
-    a.bias = bias;
-    a.xh = xh;
-    a.sx = sx;
-    a.residual = residual;
-    a.y = y;
-    a.ytype = y_type;
-    a.M = M;
-    a.N = N;
-    a.K = K;
-    a.err = d.err;
-    int grid = 0;
-    size_t smem = 0;
-    if (!plan_gemm8(d, a, grid, smem)) return W4_ERR_UNSUPPORTED_SHAPE;
-    return cuda_status(launch_gemm_w8(a, grid, smem, true, s));
+    p.a.w = static_cast<const uint8_t*>(w);
+    p.a.s_w = s_w;
+    p.a.bias = bias;
+    p.a.xh = xh;
+    p.a.sx = sx;
+    p.a.residual = residual;
+    p.a.y = y;
+    p.a.ytype = y_type;
+    return cuda_status(p.pairs ? launch_gemm_w8_pair(p.a, p.grid, p.smem, true, s) : launch_gemm_w8(p.a, p.grid, p.smem, true, s));
 }
 
 w4_status check_w8_operands(const void* w, const float* s_w, const float* bias, const void* y, int y_type)
@@ -291,7 +317,7 @@ extern "C" {
 size_t w8a8_workspace_bytes(int M, int N, int K)
 {
     if (check_w8_shape(M, N, K) != W4_OK) return 0;
-    return static_cast<size_t>(token_tiles(M)) * tile_tokens(M) * K * 2;
+    return M > 0 ? padded_tokens(M) * K * 2 : 0;
 }
 
 w4_status w8a8_matmul(const void* w, const float* s_w, const float* bias, const int8_t* qx, const float* sx, int M,
@@ -326,9 +352,11 @@ w4_status w8a8_matmul(const void* w, const float* s_w, const float* bias, const 
         return cuda_status(launch_gemv_w8(v, grid, smem, false, s));
     }
     uint4* xh = static_cast<uint4*>(workspace);
-    r = cuda_status(launch_expand_codes(qx, M, K, xh, tile_tokens(M), false, s));
+    Gemm8Plan p;
+    if (!p.make(d, M, N, K)) return W4_ERR_UNSUPPORTED_SHAPE;
+    r = cuda_status(launch_expand_codes(qx, M, K, xh, p.a.nt, false, s));
     if (r != W4_OK) return r;
-    return run_gemm8(w, s_w, bias, xh, sx, nullptr, M, N, K, y, y_type, s);
+    return run_gemm8(p, w, s_w, bias, xh, sx, nullptr, y, y_type, s);
 }
 
 w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const void* x, int x_type, int M, int N,
@@ -390,11 +418,13 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
     q.qx = few ? const_cast<int8_t*>(v.qx_in) : qx;
     q.sx = sx;
     q.xh = N > 0 && !few ? static_cast<uint4*>(workspace) : nullptr;
-    q.nt = tile_tokens(M);
+    Gemm8Plan p;
+    if (q.xh != nullptr && !p.make(d, M, N, K)) return W4_ERR_UNSUPPORTED_SHAPE;
+    q.nt = p.a.nt;
     r = cuda_status(launch_quant_rows(q, x_type, pdl, s));
     if (r != W4_OK || N == 0) return r;
     if (few) return cuda_status(launch_gemv_w8(v, grid, smem, true, s));
-    return run_gemm8(w, s_w, bias, q.xh, sx, residual, M, N, K, y, y_type, s);
+    return run_gemm8(p, w, s_w, bias, q.xh, sx, residual, y, y_type, s);
 }
 
 w4_status w4_moe_route(const w4_router* r, const void* x, int x_type, int M, int K, int* ids, float* weights,

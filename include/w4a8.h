@@ -448,7 +448,7 @@ w4_status w8a32_gemv(const void* w, const float* s_w, const float* bias, const f
  * W4_F32).  x must not overlap y.  f may be NULL; a GLU is refused.
  * 0 <= M <= W4_MAX_TOKENS, K % 32 == 0, any N.
  * workspace: device memory of w8a8_workspace_bytes(M, N, K) bytes (2 K for each
- * token and a few of padding), 16-byte aligned, with no contents to keep; calls that
+ * token and up to 192 of padding), 16-byte aligned, with no contents to keep; calls that
  * share one must not overlap on the GPU.  W4_FLAG_PDL as above: the weights
  * are fetched before the dependency wait.
  * Results do not depend on M: a token's row is the same in every batch.

@@ -54,6 +54,8 @@ SHAPES = [  # M, N, K
     (15, 129, 2080), (16, 1000, 512), (17, 300, 1536), (31, 8, 160), (33, 640, 1088), (64, 384, 18944), (100, 257, 2016),
     (127, 136, 992), (128, 256, 2048), (129, 255, 1536), (130, 1, 3584), (257, 1000, 480), (300, 392, 1120),
     (513, 4000, 1536), (1000, 2560, 1536),
+    # more tiles than SMs: pairs of blocks, with ragged tokens, rows and K, several rounds of tiles
+    (1100, 2500, 96), (770, 5000, 1056), (2000, 4608, 544), (4001, 3333, 32), (200, 40000, 160),
 ]
 
 
