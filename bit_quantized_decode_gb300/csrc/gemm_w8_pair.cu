@@ -185,6 +185,21 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
         if (warp == 0) {
             // --------------------------------------------------- copy warp
             const uint64_t pol = l2_policy_evict_first(), pol_b = l2_policy_evict_last();
+            auto copy_w = [&](int row_tile, int st, int slot) {
+                if (elect_one()) {
+                    const uint32_t bar = full_b + 8 * slot;
+                    const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kG8WBytes + k8 * nt * 16));
+                    tma_load_2d(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes), &A.wmap,
+                                st * kG8StageChunks * 32, row_tile, bar, pol);
+                }
+                __syncwarp();
+            };
+            // the first tile's weights do not depend on the previous kernel
+            int ahead = 0;
+            if (pair < ntiles)
+                for (; ahead < S && ahead < nst; ++ahead)
+                    copy_w((2 * (pair / A.n_tt) + static_cast<int>(rank)) * (kG8Rows / kRows), ahead, ahead);
             pdl_wait();
             int it = 0, slot = 0;
             uint32_t ph = 1u;
@@ -201,14 +216,12 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
                             break;
                         }
                     }
+                    if (it >= ahead) copy_w(row_tile, st, slot);
                     if (elect_one()) {
-                        const uint32_t bar = full_b + 8 * slot;
-                        const uint32_t dst = smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes);
                         const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
-                        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(kG8WBytes + k8 * nt * 16));
-                        tma_load_2d(dst, &A.wmap, st * kG8StageChunks * 32, row_tile, bar, pol);
-                        bulk_g2s(dst + kG8WBytes, codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt,
-                                 static_cast<uint32_t>(k8 * nt * 16), bar, pol_b);
+                        bulk_g2s(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
+                                 codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt, static_cast<uint32_t>(k8 * nt * 16),
+                                 full_b + 8 * slot, pol_b);
                     }
                     __syncwarp();
                     if (++slot == S) {

@@ -34,6 +34,7 @@ struct QuantRowsArgs {
     float* sx;            // [M]
     uint4* xh;            // the codes as fp16 in token tiles (f16_word), or null
     int nt;               // tokens per tile of xh
+    int cluster;          // blocks per token (set by the launch)
 };
 // fp16 codes: 16-byte words of eight K values; a token tile's words of one K
 // group follow each other, so (tile, K range) is one contiguous run.

@@ -49,7 +49,15 @@ bool plan_gemm8(const DeviceFacts& d, Gemm8Args& a, bool& pairs, int& grid, size
     a.C = a.K / 32;
     a.T = (a.N + kRows - 1) / kRows;
     const int nst = (a.C + kG8StageChunks - 1) / kG8StageChunks;
-    const int nt1 = tile(kG8MaxTok, 16), nt2 = tile(kP8MaxTok, 32);
+    int nt1 = tile(kG8MaxTok, 16);
+    const int nt2 = tile(kP8MaxTok, 32);
+    // several token tiles in one round: as many as there are SMs for
+    const int n_g = (a.N + kG8Rows - 1) / kG8Rows;
+    if (a.M > kG8MaxTok && n_g * ((a.M + nt1 - 1) / nt1) <= d.sms) {
+        const int n = d.sms / n_g;
+        const int nt = ((a.M + n - 1) / n + 15) / 16 * 16;
+        if (nt >= 32 && nt < nt1) nt1 = nt;
+    }
     const long long tiles1 = static_cast<long long>((a.N + kG8Rows - 1) / kG8Rows) * ((a.M + nt1 - 1) / nt1);
     const long long tiles2 = static_cast<long long>((a.N + 2 * kG8Rows - 1) / (2 * kG8Rows)) * ((a.M + nt2 - 1) / nt2);
     const int npairs = d.sms / 2;

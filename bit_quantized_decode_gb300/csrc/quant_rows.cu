@@ -3,8 +3,11 @@
 // of a8_quantize / rms_a8_quantize (every step an IEEE fp32 operation on the
 // activations widened to fp32, see quant_a8.cuh and fusion.cuh).
 //
-// One block per token; the row stays in registers between the norm, the
-// maximum and the rounding (K <= 20480; longer rows are read again).  Besides
+// One block per token, or a cluster of up to eight where tokens are few and
+// long: each block then has a part of the row, and they exchange their sums and
+// maxima through distributed shared memory (64 tokens of 18944: 6.5 -> 4 us).
+// The row stays in registers between the norm, the maximum and the rounding
+// (up to 20480 values a block; longer ones are read again).  Besides
 // the int8 codes it writes them as fp16 in the layout that the tensor-core
 // product copies tiles of (f16_word): a stage of a token tile is one
 // contiguous run in the MMA's core-matrix order.  It moves the activations once and the codes once (2 bytes each); its
@@ -23,18 +26,24 @@ namespace {
 
 constexpr int kQrThreads = 256;
 constexpr int kQrWarps = kQrThreads / 32;
+constexpr int kQrMaxCluster = 8;
 
 template <int XT, int NIT, bool kNorm>
 __global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsArgs a)
 {
     __shared__ float red_s[2 * kQrWarps];
+    __shared__ float all_s[3 * kQrMaxCluster];                  // the cluster's blocks: sums (hi, lo), maxima
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int m = blockIdx.x;
-    const int K8 = a.K >> 3;
+    const int cs = a.cluster;
+    const int rank = cs > 1 ? static_cast<int>(blockIdx.x) % cs : 0;
+    const int m = static_cast<int>(blockIdx.x) / cs;
+    const int K8_all = a.K >> 3;
+    const int k0 = static_cast<int>(static_cast<long long>(rank) * K8_all / cs);
+    const int K8 = static_cast<int>(static_cast<long long>(rank + 1) * K8_all / cs) - k0;    // this block's groups of eight
     constexpr int kN = NIT > 0 ? NIT : 1;
     pdl_launch_dependents();
     pdl_wait();
-    const size_t row = static_cast<size_t>(m) * a.K;
+    const size_t row = static_cast<size_t>(m) * a.K + 8 * static_cast<size_t>(k0);
     float v[kN][8];
     if constexpr (NIT > 0) {
 #pragma unroll
@@ -62,7 +71,7 @@ __global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsA
     auto normed = [&](int i, float (&t)[8]) {
         if constexpr (kNorm) {
             float g[8];
-            load8<T_F32>(a.gamma, 8 * static_cast<size_t>(i), g);
+            load8<T_F32>(a.gamma, 8 * static_cast<size_t>(k0 + i), g);
 #pragma unroll
             for (int k = 0; k < 8; ++k) t[k] = __fmul_rn(__fmul_rn(t[k], r), g[k]);
         }
@@ -83,6 +92,16 @@ __global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsA
         lo = red_s[1];
 #pragma unroll
         for (int w = 1; w < kQrWarps; ++w) pair_merge(hi, lo, red_s[2 * w], red_s[2 * w + 1]);
+        if (cs > 1) {
+            if (tid < cs) {
+                st_cluster_u32(mapa_shared(smem_u32(all_s + 2 * rank), static_cast<uint32_t>(tid)), __float_as_uint(hi));
+                st_cluster_u32(mapa_shared(smem_u32(all_s + 2 * rank + 1), static_cast<uint32_t>(tid)), __float_as_uint(lo));
+            }
+            cluster_sync();
+            hi = all_s[0];
+            lo = all_s[1];
+            for (int b = 1; b < cs; ++b) pair_merge(hi, lo, all_s[2 * b], all_s[2 * b + 1]);
+        }
         r = rms_scale(hi, lo, a.K, a.eps);
         __syncthreads();
     }
@@ -99,14 +118,20 @@ __global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsA
     float amax = red_s[0];
 #pragma unroll
     for (int w = 1; w < kQrWarps; ++w) amax = fmaxf(amax, red_s[w]);
+    if (cs > 1) {
+        float* max_s = all_s + 2 * kQrMaxCluster;
+        if (tid < cs) st_cluster_u32(mapa_shared(smem_u32(max_s + rank), static_cast<uint32_t>(tid)), __float_as_uint(amax));
+        cluster_sync();
+        for (int b = 0; b < cs; ++b) amax = fmaxf(amax, max_s[b]);
+    }
     const A8Scale ks = a8_scale(amax);
-    if (tid == 0) a.sx[m] = ks.s;
+    if (tid == 0 && rank == 0) a.sx[m] = ks.s;
     uint2* q8 = a.qx != nullptr ? reinterpret_cast<uint2*>(a.qx + row) : nullptr;
     each([&](int i, float (&t)[8]) {
         if constexpr (NIT == 0) normed(i, t);
         const uint2 q = quant8(t, ks);
         if (q8 != nullptr) q8[i] = q;
-        if (a.xh != nullptr) a.xh[f16_word(m, i, K8, a.nt)] = codes_f16(q);
+        if (a.xh != nullptr) a.xh[f16_word(m, k0 + i, K8_all, a.nt)] = codes_f16(q);
     });
 }
 
@@ -136,7 +161,7 @@ cudaLaunchConfig_t row_launch(int blocks, int threads, bool pdl, cudaStream_t s,
 template <int XT, bool kNorm>
 cudaError_t launch_rows(const QuantRowsArgs& a, const cudaLaunchConfig_t& cfg)
 {
-    const int nit = (a.K / 8 + kQrThreads - 1) / kQrThreads;
+    const int nit = ((a.K / 8 + a.cluster - 1) / a.cluster + kQrThreads - 1) / kQrThreads;
     if (nit <= 2) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 2, kNorm>, a);
     if (nit <= 4) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 4, kNorm>, a);
     if (nit <= 10) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 10, kNorm>, a);
@@ -151,10 +176,22 @@ cudaError_t launch_typed(const QuantRowsArgs& a, const cudaLaunchConfig_t& cfg)
 
 }  // namespace
 
-cudaError_t launch_quant_rows(const QuantRowsArgs& a, int xtype, bool pdl, cudaStream_t s)
+cudaError_t launch_quant_rows(const QuantRowsArgs& args, int xtype, bool pdl, cudaStream_t s)
 {
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = row_launch(a.M, kQrThreads, pdl, s, attr);
+    // a block for about 4096 values, while there are few blocks
+    QuantRowsArgs a = args;
+    a.cluster = 1;
+    while (a.cluster < kQrMaxCluster && a.K >= 8192 * a.cluster && a.M * a.cluster <= 256) a.cluster *= 2;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = row_launch(a.M * a.cluster, kQrThreads, pdl, s, attr);
+    if (a.cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+        cfg.attrs = attr;
+    }
     if (xtype == T_F32) return launch_typed<T_F32>(a, cfg);
     if (xtype == T_F16) return launch_typed<T_F16>(a, cfg);
     return launch_typed<T_BF16>(a, cfg);
