@@ -32,7 +32,7 @@
 namespace w4k {
 namespace {
 
-constexpr int kWarpMma = 1, kWarpConv = 2, kWarpEpi = 10, kWarpCodes = 18;
+constexpr int kWarpMma = 1, kWarpConv = 2, kWarpEpi = 10;
 
 // kind::f16 MMAs of one stage's K slices (A in tensor memory, eight columns to
 // a slice; B from shared-memory descriptors `bstep` apart in the address
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
     };
     if (warp == 0) {
         // ------------------------------------------------------- copy warp
-        const uint64_t pol = l2_policy_evict_first();
+        const uint64_t pol = l2_policy_evict_first(), pol_b = l2_policy_evict_last();
         auto copy_w = [&](int row_tile, int st, int slot) {
             if (elect_one()) {
                 const uint32_t bar = full_b + 8 * slot;
@@ -170,18 +170,28 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 tma_load_2d(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes), &A.wmap,
                             st * kG8StageChunks * 32, row_tile, bar, pol);
             }
-            __syncwarp();
+        };
+        auto copy_b = [&](const uint4* codes, int st, int slot) {
+            if (elect_one()) {
+                const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
+                bulk_g2s(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
+                         codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt, static_cast<uint32_t>(k8 * nt * 16),
+                         full_b + 8 * slot, pol_b);
+            }
         };
         // the first tile's weights do not depend on the previous kernel
         int ahead = 0;
         if (tile_first < ntiles)
             for (; ahead < S && st0 + ahead < st1; ++ahead)
                 copy_w((tile_first / A.n_tt) * (kG8Rows / kRows), st0 + ahead, ahead);
+        pdl_wait();
         int it = 0, slot = 0;
         uint32_t ph = 1u;                // parity of the slot's previous release
         bool ok = true;
         for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
-            const int row_tile = tile / A.n_tt * (kG8Rows / kRows);
+            const int g = tile / A.n_tt;
+            const int row_tile = g * (kG8Rows / kRows);
+            const uint4* codes = A.xh + static_cast<size_t>(tile - g * A.n_tt) * (A.K >> 3) * nt;
             for (int st = st0; st < st1; ++st, ++it) {
                 if (it >= ahead) {
                     if (it >= S) {
@@ -193,6 +203,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                     }
                     copy_w(row_tile, st, slot);
                 }
+                copy_b(codes, st, slot);
                 if (++slot == S) {
                     slot = 0;
                     ph ^= 1u;
@@ -203,38 +214,6 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         for (int k = max(0, it - S); k < it; ++k)
             if (!mbar_wait_bounded(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u, kG8WaitNs)) break;
         __syncwarp();
-    } else if (warp == kWarpCodes) {
-        // ------------------------------------- copy warp of the codes: a
-        // copy takes its warp some 150 to 200 cycles, two of them bound the loop
-        const uint64_t pol = l2_policy_evict_last();
-        pdl_wait();
-        int it = 0, slot = 0;
-        uint32_t ph = 1u;
-        bool ok = true;
-        for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
-            const uint4* codes = A.xh + static_cast<size_t>(tile % A.n_tt) * (A.K >> 3) * nt;
-            for (int st = st0; st < st1; ++st, ++it) {
-                if (it >= S) {
-                    ok = warp_wait(empty_b + 8 * slot, ph);
-                    if (!ok) {
-                        if (lane == 0) fail();
-                        break;
-                    }
-                }
-                if (elect_one()) {
-                    // (the byte count of both copies is the other warp's: it may come after these bytes)
-                    const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
-                    bulk_g2s(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
-                             codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt, static_cast<uint32_t>(k8 * nt * 16),
-                             full_b + 8 * slot, pol);
-                }
-                __syncwarp();
-                if (++slot == S) {
-                    slot = 0;
-                    ph ^= 1u;
-                }
-            }
-        }
     } else if (warp == kWarpMma) {
         // -------------------------------------------------------- MMA warp
         const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(kG8Rows >> 4) << 24);
@@ -328,6 +307,8 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                             tmem_st16(tbase + tlane + col_a + static_cast<uint32_t>(kG8ACols * slot + 16 * e), h);
                         }
                     }
+                    // (the reads of the slot are ordered before the copy that refills it)
+                    fence_proxy_async_smem();
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -339,7 +320,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 }
             }
         }
-    } else if (warp >= kWarpEpi && warp < kWarpCodes) {
+    } else if (warp >= kWarpEpi) {
         // -------------------------------------------------- epilogue warps
         const int half = (warp - kWarpEpi) >> 2;
         const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;

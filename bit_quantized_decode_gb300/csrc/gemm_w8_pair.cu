@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
             // --------------------------------------------------- copy warp
-            const uint64_t pol = l2_policy_evict_first();
+            const uint64_t pol = l2_policy_evict_first(), pol_b = l2_policy_evict_last();
             auto copy_w = [&](int row_tile, int st, int slot) {
                 if (elect_one()) {
                     const uint32_t bar = full_b + 8 * slot;
@@ -200,22 +200,30 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
             if (pair < ntiles)
                 for (; ahead < S && ahead < nst; ++ahead)
                     copy_w((2 * (pair / A.n_tt) + static_cast<int>(rank)) * (kG8Rows / kRows), ahead, ahead);
+            pdl_wait();
             int it = 0, slot = 0;
             uint32_t ph = 1u;
             bool ok = true;
             for (int tile = pair; tile < ntiles && ok; tile += pairs) {
-                const int row_tile = (2 * (tile / A.n_tt) + static_cast<int>(rank)) * (kG8Rows / kRows);
+                const int g = tile / A.n_tt;
+                const int row_tile = (2 * g + static_cast<int>(rank)) * (kG8Rows / kRows);
+                const uint4* codes = A.xh + static_cast<size_t>(2 * (tile - g * A.n_tt) + static_cast<int>(rank)) * (A.K >> 3) * nt;
                 for (int st = 0; st < nst; ++st, ++it) {
-                    if (it >= ahead) {
-                        if (it >= S) {
-                            ok = pair_wait(empty_b + 8 * slot, ph);
-                            if (!ok) {
-                                fail();
-                                break;
-                            }
+                    if (it >= S) {
+                        ok = pair_wait(empty_b + 8 * slot, ph);
+                        if (!ok) {
+                            fail();
+                            break;
                         }
-                        copy_w(row_tile, st, slot);
                     }
+                    if (it >= ahead) copy_w(row_tile, st, slot);
+                    if (elect_one()) {
+                        const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
+                        bulk_g2s(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
+                                 codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt, static_cast<uint32_t>(k8 * nt * 16),
+                                 full_b + 8 * slot, pol_b);
+                    }
+                    __syncwarp();
                     if (++slot == S) {
                         slot = 0;
                         ph ^= 1u;
@@ -226,38 +234,6 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
             for (int k = max(0, it - S); k < it; ++k)
                 if (!mbar_wait_bounded(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u, kG8WaitNs)) break;
             __syncwarp();
-        } else if (warp == 2) {
-            // --------------------------------- copy warp of the codes: a
-            // copy takes its warp some 150 to 200 cycles
-            const uint64_t pol = l2_policy_evict_last();
-            pdl_wait();
-            int it = 0, slot = 0;
-            uint32_t ph = 1u;
-            bool ok = true;
-            for (int tile = pair; tile < ntiles && ok; tile += pairs) {
-                const uint4* codes = A.xh + static_cast<size_t>(2 * (tile % A.n_tt) + static_cast<int>(rank)) * (A.K >> 3) * nt;
-                for (int st = 0; st < nst; ++st, ++it) {
-                    if (it >= S) {
-                        ok = pair_wait(empty_b + 8 * slot, ph);
-                        if (!ok) {
-                            fail();
-                            break;
-                        }
-                    }
-                    if (elect_one()) {
-                        // (the byte count of both copies is the other warp's: it may come after these bytes)
-                        const int k8 = 4 * min(kG8StageChunks, A.C - st * kG8StageChunks);
-                        bulk_g2s(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes + kG8WBytes),
-                                 codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt, static_cast<uint32_t>(k8 * nt * 16),
-                                 full_b + 8 * slot, pol);
-                    }
-                    __syncwarp();
-                    if (++slot == S) {
-                        slot = 0;
-                        ph ^= 1u;
-                    }
-                }
-            }
         } else if (warp == 1 && rank == 0) {
             // ---------------------------------------------------- MMA warp
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(2 * nt >> 3) << 17) | (16u << 24);   // M = 256

@@ -56,7 +56,7 @@ constexpr int kG8TmemCols = 512;
 constexpr int kG8ACols = 16 * kG8StageChunks;   // tensor-memory columns of one converted stage
 constexpr int kG8MaxStages = 7;
 constexpr int kG8MaxSplit = 8;
-constexpr int kG8Threads = 608;
+constexpr int kG8Threads = 576;
 
 struct Gemm8Args {
     CUtensorMap wmap;         // the weights as [T row tiles][C chunks x 256 bytes]
