@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         fence_mbar_init();
         *dead_s = 0u;
     }
+    __syncwarp();
     if (warp == kWarpMma) {
         tmem_alloc(smem_u32(tmem_slot), kG8TmemCols);
         tmem_relinquish();
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 tma_load_2d(smem_u32(smem + L.ring) + static_cast<uint32_t>(slot * slot_bytes), &A.wmap,
                             st * kG8StageChunks * 32, row_tile, bar, pol);
             }
+            __syncwarp();
         };
         auto copy_b = [&](const uint4* codes, int st, int slot) {
             if (elect_one()) {
@@ -178,6 +180,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                          codes + static_cast<size_t>(st * kG8StageChunks * 4) * nt, static_cast<uint32_t>(k8 * nt * 16),
                          full_b + 8 * slot, pol_b);
             }
+            __syncwarp();
         };
         // the first tile's weights do not depend on the previous kernel
         int ahead = 0;
@@ -212,8 +215,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         }
         // every copy has landed before the block ends (also after a failure)
         for (int k = max(0, it - S); k < it; ++k)
-            if (!mbar_wait_bounded(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u, kG8WaitNs)) break;
-        __syncwarp();
+            if (!warp_wait(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u)) break;
     } else if (warp == kWarpMma) {
         // -------------------------------------------------------- MMA warp
         const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(nt >> 3) << 17) | (static_cast<uint32_t>(kG8Rows >> 4) << 24);
@@ -232,8 +234,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 const bool last = st + 1 == st1 || run == kG8AccStages - 1;
                 const uint32_t dcol = tbase + static_cast<uint32_t>((ac & 1) * nt);
                 if (run == 0 && ac >= 2) ok = warp_wait(acce_b + 8 * (ac & 1), static_cast<uint32_t>((ac >> 1) - 1) & 1u);
-                // converted, so landed: the converting warps saw the codes land with the weights
-                ok = ok && warp_wait(ready_b + 8 * slot, sph);
+                ok = ok && warp_wait(ready_b + 8 * slot, sph) && warp_wait(full_b + 8 * slot, sph);
                 if (!ok) {
                     if (lane == 0) fail();
                     break;
@@ -268,9 +269,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
             }
         }
         // every MMA has completed before the tensor memory is freed
-        if (it > 0)
-            mbar_wait_bounded(empty_b + 8 * ((it - 1) % S), static_cast<uint32_t>((it - 1) / S) & 1u, kG8WaitNs);
-        __syncwarp();
+        if (it > 0) warp_wait(empty_b + 8 * ((it - 1) % S), static_cast<uint32_t>((it - 1) / S) & 1u);
     } else if (warp >= kWarpConv && warp < kWarpEpi) {
         // ------------------------------------------------ converting warps
         const int grp = (warp - kWarpConv) >> 2;
@@ -313,6 +312,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ready_b + 8 * slot);
+                    __syncwarp();
                 }
                 if (++slot == S) {
                     slot = 0;
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(acce_b + 8 * (ac & 1));
+                __syncwarp();
             }
             if (ks > 1 || !ok) break;
             const int m0 = (tile - g * A.n_tt) * nt + 16 * half;
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     if (warp == kWarpMma) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tbase, kG8TmemCols);
     }

@@ -11,12 +11,27 @@ namespace w4k {
 
 constexpr uint64_t kG8WaitNs = 250ull * 1000ull * 1000ull;
 
-// Wait of a whole warp: a test first, as the phase is usually complete.
+// Wait of a whole warp: a test first, as the phase is usually complete.  The
+// lanes vote on every try and leave together: what follows are .aligned
+// tensor-memory instructions, which a warp whose lanes come one after another
+// (each out of a loop of its own) must not reach.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
 {
-    bool ok = mbar_test_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) ok = mbar_wait_bounded(bar, parity, kG8WaitNs);
-    return __all_sync(0xffffffffu, ok);
+    bool ok = __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+    if (!ok) {
+        uint64_t t0 = 0;
+#pragma unroll 1
+        for (uint32_t i = 1; !ok; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+            if (!ok && (i & 31u) == 0u) {          // the timer is slow to read
+                const uint64_t now = globaltimer_ns();
+                if (i == 32u) t0 = now;
+                else if (__any_sync(0xffffffffu, now - t0 > kG8WaitNs)) break;
+            }
+        }
+    }
+    __syncwarp();
+    return ok;
 }
 
 // Box of a 2-D tensor map -> shared memory.

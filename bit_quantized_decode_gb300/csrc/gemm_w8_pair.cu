@@ -69,8 +69,8 @@ __device__ __forceinline__ void pair_arrive(uint32_t addr)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// Wait of a whole warp for arrivals that may come from the other block: tries
-// first, the timer (slow to read) only when they have run out.
+// Wait of a whole warp for arrivals that may come from the other block; the
+// lanes leave together, as in warp_wait.
 __device__ __forceinline__ bool pair_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -84,11 +84,21 @@ __device__ __forceinline__ bool pair_try(uint32_t bar, uint32_t parity)
 }
 __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity)
 {
-    bool ok = pair_try(bar, parity);
+    bool ok = __all_sync(0xffffffffu, pair_try(bar, parity));
+    if (!ok) {
+        uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64 && !ok; ++i) ok = pair_try(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) ok = mbar_wait_cluster_bounded(bar, parity, kG8WaitNs);
-    return __all_sync(0xffffffffu, ok);
+        for (uint32_t i = 1; !ok; ++i) {
+            ok = __all_sync(0xffffffffu, pair_try(bar, parity));
+            if (!ok && (i & 31u) == 0u) {
+                const uint64_t now = globaltimer_ns();
+                if (i == 32u) t0 = now;
+                else if (__any_sync(0xffffffffu, now - t0 > kG8WaitNs)) break;
+            }
+        }
+    }
+    __syncwarp();
+    return ok;
 }
 
 // Outputs of one weight row and the tokens m0 + 16 b + i (16 b < cols); clears acc.
@@ -167,6 +177,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
         }
         fence_mbar_init();
     }
+    __syncwarp();
     if (warp == 1) pair_alloc(smem_u32(tmem_slot), kG8TmemCols);
     tc_fence_before();
     __syncthreads();
@@ -232,8 +243,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
             }
             // every copy has landed before the block ends (also after a failure)
             for (int k = max(0, it - S); k < it; ++k)
-                if (!mbar_wait_bounded(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u, kG8WaitNs)) break;
-            __syncwarp();
+                if (!warp_wait(full_b + 8 * (k % S), static_cast<uint32_t>(k / S) & 1u)) break;
         } else if (warp == 1 && rank == 0) {
             // ---------------------------------------------------- MMA warp
             const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(2 * nt >> 3) << 17) | (16u << 24);   // M = 256
@@ -336,6 +346,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) pair_arrive(ready0 + 8 * j);
+                __syncwarp();
                 if (++slot == S) {
                     slot = 0;
                     sph ^= 1u;
@@ -384,6 +395,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) pair_arrive(acce0 + 8 * (ac & 1));
+                __syncwarp();
             }
             if (!ok) break;
             if (A.ytype == T_F32) pair_emit<T_F32>(A, acc, m0, nt, row, sw, bv, sx);
@@ -391,10 +403,12 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
             else pair_emit<T_BF16>(A, acc, m0, nt, row, sw, bv, sx);
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_sync();                                                // no arrival comes to a block that has left
     if (warp == 1) {
+        __syncwarp();
         tc_fence_after();
         pair_dealloc(tbase, kG8TmemCols);
     }
