@@ -9,6 +9,7 @@ it.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -609,13 +610,16 @@ def w8a32_gemv(w, s_w, bias, x, y, flags: int = 0, stream=None):
 def _check_tensors(*specs):
     """Each spec: (name, tensor or None, dtypes, shape or None).  Contiguous, of one of the dtypes, of the shape, on the
     current CUDA device."""
-    cur = torch.cuda.current_device()
+    cur = None
     for name, t, dtypes, shape in specs:
         if t is None:
             continue
-        if t.get_device() != cur:
-            if not t.is_cuda:
-                raise ValueError(f"{name}: tensor must live on a CUDA device")
+        at = t.get_device()
+        if at < 0:
+            raise ValueError(f"{name}: tensor must live on a CUDA device")
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if at != cur:
             raise ValueError(f"{name}: tensor lives on {t.device}, the current device is cuda:{cur}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: tensor must be contiguous")
@@ -633,6 +637,12 @@ def _addr(t):
 def _raw_stream(stream, device):
     """The stream's handle: the given one's, or the current one's of `device`."""
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+
+
+def allocating_on(stream):
+    """Context in which a call on `stream` (None: the current one) makes its tensors, so that the allocator orders their
+    memory with that stream's work."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 _F32 = (torch.float32,)
@@ -703,16 +713,20 @@ def moe_router(w, top_k: int, select_bias=None, score: str = "softmax", renormal
                norm=None, eps: float = 1e-6):
     """A w4_router descriptor: w float32 [E][K].  It holds references to its tensors."""
     E, K = w.shape
-    _check_tensors(("w", w, _F32, None), ("select_bias", select_bias, _F32, (E,)), ("norm", norm, _F32, (K,)))
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
+    dev = _check_tensors(("w", w, _F32, None), ("select_bias", select_bias, _F32, (E,)), ("norm", norm, _F32, (K,)))
     r = Router(None if norm is None else norm.data_ptr(), float(eps), w.data_ptr(),
                None if select_bias is None else select_bias.data_ptr(), E, int(top_k), ROUTE_SCORES[score],
                int(bool(renormalize)), float(scale))
-    r._tensors, r._K = (w, select_bias, norm), K
+    r._tensors, r._K, r._device = (w, select_bias, norm), K, dev
     return r
 
 
 def moe_experts(fmt: str, w_gu, s_gu, w_dn, s_dn, E: int, n_shared: int, H: int, I: int, glu: int, b_gu=None, b_dn=None):
     """A w4_experts descriptor over the repacked weights of E + n_shared experts.  It holds references to its tensors."""
+    if fmt not in EXPERT_FORMATS:
+        raise ValueError(f"experts are {sorted(EXPERT_FORMATS)}, not {fmt!r}")
     n = E + n_shared
     gu_bytes, dn_bytes = ((w4_glu_repacked_bytes(I, H), w4_repacked_bytes(H, I)) if fmt == "w4"
                           else (w8_glu_repacked_bytes(I, H), w8_repacked_bytes(H, I)))
@@ -722,8 +736,14 @@ def moe_experts(fmt: str, w_gu, s_gu, w_dn, s_dn, E: int, n_shared: int, H: int,
     e = Experts(EXPERT_FORMATS[fmt], E, n_shared, H, I, glu, w_gu.data_ptr(), s_gu.data_ptr(),
                 None if b_gu is None else b_gu.data_ptr(), w_dn.data_ptr(), s_dn.data_ptr(),
                 None if b_dn is None else b_dn.data_ptr())
-    e._tensors = (w_gu, s_gu, b_gu, w_dn, s_dn, b_dn)
+    e._tensors, e._device = (w_gu, s_gu, b_gu, w_dn, s_dn, b_dn), dev
     return e
+
+
+def _check_home(dev, *descs):
+    for d in descs:
+        if d._device != dev:
+            raise ValueError(f"the descriptor's tensors live on cuda:{d._device}, the current device is cuda:{dev}")
 
 
 def w4_moe_route(router, x, ids, weights, qx=None, sx=None, flags: int = 0, stream=None):
@@ -735,6 +755,7 @@ def w4_moe_route(router, x, ids, weights, qx=None, sx=None, flags: int = 0, stre
     dev = _check_tensors(("x", x, _FLOATS, None), ("ids", ids, _I32, (M, router.top_k)),
                          ("weights", weights, _F32, (M, router.top_k)), ("qx", qx, _I8, (M, K)),
                          ("sx", sx, _F32, (M,)))
+    _check_home(dev, router)
     _check("w4_moe_route", load().w4_moe_route(ctypes.byref(router), _addr(x), ELEM_TYPES[x.dtype], M, K, _addr(ids),
                                                _addr(weights), _addr(qx), _addr(sx), flags, _raw_stream(stream, dev)))
 
@@ -750,6 +771,7 @@ def w4_moe_experts(experts, qx, sx, ids, weights, y, workspace, residual=None, f
     dev = _check_tensors(("qx", qx, _I8, (M, H)), ("sx", sx, _F32, (M,)), ("ids", ids, _I32, None),
                          ("weights", weights, _F32, (M, top_k)), ("y", y, _FLOATS, (M, H)),
                          ("workspace", workspace, _U8, None), ("residual", residual, _F32, (M, H)))
+    _check_home(dev, experts)
     _check("w4_moe_experts", load().w4_moe_experts(ctypes.byref(experts), _addr(qx), _addr(sx), _addr(ids), _addr(weights), M,
                                                    top_k, _addr(residual), _addr(y), ELEM_TYPES[y.dtype], _addr(workspace),
                                                    workspace.numel(), flags, _raw_stream(stream, dev)))
@@ -764,6 +786,7 @@ def w4_moe_layer(router, experts, x, ids, weights, qx, sx, y, workspace, residua
                          ("weights", weights, _F32, (M, router.top_k)), ("qx", qx, _I8, (M, H)),
                          ("sx", sx, _F32, (M,)), ("y", y, _FLOATS, (M, H)), ("workspace", workspace, _U8, None),
                          ("residual", residual, _F32, (M, H)))
+    _check_home(dev, router, experts)
     _check("w4_moe_layer", load().w4_moe_layer(ctypes.byref(router), ctypes.byref(experts), _addr(x), ELEM_TYPES[x.dtype], M,
                                                _addr(ids), _addr(weights), _addr(qx), _addr(sx), _addr(residual), _addr(y),
                                                ELEM_TYPES[y.dtype], _addr(workspace), workspace.numel(), flags,

@@ -148,12 +148,13 @@ class QuantLinear:
         M, K = x.shape
         if K != self.K:
             raise ValueError(f"x has {K} columns, the linear takes {self.K}")
-        if y is None:
-            y = torch.empty((M, self.N), dtype=x.dtype if residual is None else torch.float32, device=x.device)
-        if sx is None:
-            sx = torch.empty(M, dtype=torch.float32, device=x.device)
-        if workspace is None:
-            workspace = self.workspace(M)
+        with _lib.allocating_on(stream):
+            if y is None:
+                y = torch.empty((M, self.N), dtype=x.dtype if residual is None else torch.float32, device=x.device)
+            if sx is None:
+                sx = torch.empty(M, dtype=torch.float32, device=x.device)
+            if workspace is None:
+                workspace = self.workspace(M)
         _lib.w8a8_linear(self.w, self.s_w, self.bias, x, y, qx, sx, workspace, norm, eps, residual, flags, stream)
         return y
 
@@ -201,7 +202,9 @@ class QuantLinear:
     def gemv(self, qx, sx, y, stream=None):
         """GEMV on already-quantized activations."""
         if self.fmt == "w8":
-            _lib.w8a8_matmul(self.w, self.s_w, self.bias, qx, sx, y, self.workspace(qx.shape[0]), stream)
+            with _lib.allocating_on(stream):
+                workspace = self.workspace(qx.shape[0])
+            _lib.w8a8_matmul(self.w, self.s_w, self.bias, qx, sx, y, workspace, stream)
         elif self.fmt == "w4":
             _lib.w4a8_gemv(self.w, self.s_w, self.bias, qx, sx, y, stream)
         elif self.fmt == "q4_0":

@@ -39,8 +39,6 @@ class MoeRouter:
 
     def __init__(self, w, top_k: int, select_bias=None, score: str = "softmax", renormalize: bool = True,
                  scale: float = 1.0, norm=None, eps: float = 1e-6):
-        if score not in _lib.ROUTE_SCORES:
-            raise ValueError(f"score {score!r} is not one of {sorted(_lib.ROUTE_SCORES)}")
         self.E, self.K = w.shape
         self.top_k = int(top_k)
         self.desc = _lib.moe_router(w, top_k, select_bias, score, renormalize, scale, norm, eps)
@@ -52,7 +50,10 @@ class MoeRouter:
 
     def __call__(self, x, buffers: RouteBuffers = None, qx=None, sx=None, flags: int = 0, stream=None):
         """ids and weights of x [M][K] (fp32, fp16 or bf16); qx, sx: receive the (normalized) tokens' codes."""
-        b = buffers if buffers is not None else self.buffers(x.shape[0])
+        b = buffers
+        if b is None:
+            with _lib.allocating_on(stream):
+                b = self.buffers(x.shape[0])
         _lib.w4_moe_route(self.desc, x, b.ids, b.weights, qx, sx, flags, stream)
         return b.ids, b.weights
 
@@ -68,6 +69,8 @@ class MoeLayer:
                    b_dn=None) -> "MoeLayer":
         """gate_up: float32 CUDA tensors [2 I][H] (gate rows first), down: [H][I], one per expert, the n_shared shared
         experts last (each is quantized as it is reached, so they may come from a generator); biases [experts][..]."""
+        if fmt not in _lib.EXPERT_FORMATS:
+            raise ValueError(f"experts are {sorted(_lib.EXPERT_FORMATS)}, not {fmt!r}")
         q = _lib.w4_quantize_rows if fmt == "w4" else _lib.w8_quantize_rows
 
         def quantized(W):
@@ -129,7 +132,8 @@ class MoeLayer:
         (float32 [M][H]).  Without buffers y has x's type, or float32 with a residual."""
         b = buffers
         if b is None:
-            b = self.buffers(x.shape[0], x.dtype if residual is None else torch.float32)
+            with _lib.allocating_on(stream):
+                b = self.buffers(x.shape[0], x.dtype if residual is None else torch.float32)
         _lib.w4_moe_layer(self.router.desc, self.desc, x, b.ids, b.weights, b.qx, b.sx, b.y, b.workspace, residual, flags,
                           stream)
         return b.y
@@ -137,7 +141,8 @@ class MoeLayer:
     def experts(self, qx, sx, ids, weights, y, workspace=None, residual=None, flags: int = 0, stream=None):
         """The experts alone on int8 codes and a choice made elsewhere (an id outside 0 .. E - 1 is an empty slot)."""
         if workspace is None:
-            workspace = torch.empty(_lib.w4_moe_workspace_bytes(self.desc, ids.shape[0], ids.shape[1]), dtype=torch.uint8,
-                                    device=y.device)
+            with _lib.allocating_on(stream):
+                workspace = torch.empty(_lib.w4_moe_workspace_bytes(self.desc, ids.shape[0], ids.shape[1]),
+                                        dtype=torch.uint8, device=y.device)
         _lib.w4_moe_experts(self.desc, qx, sx, ids, weights, y, workspace, residual, flags, stream)
         return y
