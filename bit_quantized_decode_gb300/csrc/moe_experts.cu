@@ -18,11 +18,25 @@
 //     on their way.  A warp waits only for tickets handed out before its own,
 //     which running warps hold and finish without waiting on later ones: the
 //     kernel needs no co-resident grid and two of them may share the GPU.
-//   * An entry is an expert and up to eight of its tokens; a lane holds four
-//     rows by eight tokens of integer sums (DP4A, as the decode GEMV: line
-//     lane / 2 of a 16-line pass, rows 4 (lane & 1) .. + 3, reads permuted
-//     against bank conflicts, a shuffle butterfly at the end of a tile).
-//     More tokens of one expert are further entries.
+//   * An entry is an expert and some of its tokens; more of them are further
+//     entries.  Up to two tokens (INT8: four): a lane holds four rows by the
+//     tokens of integer sums (DP4A, as the decode GEMV: line lane / 2 of a
+//     16-line pass, rows 4 (lane & 1) .. + 3, reads permuted against bank
+//     conflicts, a shuffle butterfly at the end of a tile).
+//   * Up to eight tokens: mma.sync on two tiles at a time, the weights as the 16
+//     rows of A, the tokens as the eight columns of B.  So few columns leave
+//     tcgen05 nothing to gain (its smallest tile has 64 or 128 rows, and A would
+//     go through tensor memory once more); here a lane loads its K of a row from
+//     the ring as it lies.  INT4 needs no conversion at all: a nibble w + 8 at
+//     bit 0 or 16 of a word is the fp16 number (w + 8) 2^-24, subnormal and
+//     exact, so a mask makes an operand pair; the codes wait as fp16 in shared
+//     memory.  (e4m3 operands would take half the products, but are converted to
+//     fp16 by instructions of their own: 162 instead of 106 million.)  INT8 runs
+//     on the integer product, 15 cycles for 16 x 32 x 8 (fp16: 4.2), which two
+//     INT8 tiles just afford and INT4 ones would not.
+//     A slice of 16 lines takes a warp some 1600 cycles and its copies and
+//     bookkeeping another 1300; waits for memory are 5%.  16 tokens over 64
+//     experts of 2368 x 3584 (722 MB of INT4): 177 us with the router; DP4A 202.
 //   * No fence per tile (it waits for all that the warp has outstanding: it
 //     took 3500 of a tile's 9500 cycles): hidden values and the slots' outputs
 //     are prepared with a value that no result takes (MoeFill), and a reader
@@ -31,6 +45,8 @@
 //     that read them through L1 acquire.
 //   * Adding tasks, the last tickets, sum the slots' outputs in order: no
 //     floating-point atomics, so results do not depend on timing.
+#include <type_traits>
+
 #include "exact_act.cuh"
 #include "operators.h"
 #include "ptx.cuh"
@@ -45,19 +61,31 @@ constexpr uint64_t kMxWaitNs = 250ull * 1000ull * 1000ull;
 __host__ __device__ constexpr int mx_unit(int fmt) { return fmt == FMT_W4 ? 16 : 32; }
 // Ring slots: bytes, slots per warp and warps per block.  A slot costs a wait
 // and a copy however large it is, so where an entry has one or two tokens (few
-// sums per weight) the slots are large; with more, more warps.
+// sums per weight) the slots are large; with more, more warps.  On the tensor
+// cores as many of the warps as fit beside the tokens' codes (8 tokens of 3584:
+// 16 warps 121 us, 12 warps 135).
 __host__ __device__ constexpr int mx_slot(int tok) { return tok <= 2 ? 8192 : 4096; }
 __host__ __device__ constexpr int mx_stages(int) { return 2; }
 __host__ __device__ constexpr int mx_warps(int tok) { return tok <= 2 ? 12 : tok <= 4 ? 20 : 16; }
+constexpr int kMxFewestWarps = 10;                 // a thread for each pair
+// Entries of more than four tokens multiply on the tensor cores, two tiles at a time.
+__host__ __device__ constexpr bool mx_mma(int tok) { return tok > 4; }
+// Bytes of a code as a kernel reads it (INT4 on the tensor cores: fp16), and the stride of the tokens' staged codes: what a read takes of
+// several tokens lies in banks of their own.
+__host__ __device__ constexpr int mx_code(int fmt, int tok) { return mx_mma(tok) && fmt == FMT_W4 ? 2 : 1; }
+__host__ __device__ constexpr int mx_stride(int fmt, int tok, int H)
+{
+    return !mx_mma(tok) ? H : fmt == FMT_W4 ? 2 * H + (192 - 2 * H % 128) % 128 : H + (160 - H % 128) % 128;
+}
 
 constexpr int kMxBatches = 64;
 
 struct MxSmem {
     int bars, mask, off, ent0, pair_e, list, tok, ent_e, ent_off, ent_n, of_pos, ready, sh, hs, sx, xsum, misc, base, ring, codes, total;
 };
-__host__ __device__ inline MxSmem mx_smem(int tok, int staged)
+__host__ __device__ inline MxSmem mx_smem(int tok, int warps, int staged)
 {
-    const int warps = mx_warps(tok), stages = mx_stages(tok);
+    const int stages = mx_stages(tok);
     MxSmem L;
     int o = 0;
     L.bars = o;    o += (warps * stages + 1) * 8;      // the rings', the staged codes'
@@ -176,17 +204,47 @@ __device__ __forceinline__ void line_dot(const uint4 (&w0)[4], const uint4 (&w1)
     }
 }
 
+// Eight INT8 codes (K 0 .. 3, 4 .. 7) as the fp16 pairs K 0 2, 1 3 and, divided
+// by 16, 4 6, 5 7: (1024 + (x + 128)) - 1152 and its sixteenth, all exact.
+__device__ __forceinline__ uint4 codes_half(uint32_t lo, uint32_t hi)
+{
+    lo ^= 0x80808080u;
+    hi ^= 0x80808080u;
+    uint4 h;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h.x) : "r"(__byte_perm(lo, 0x64646464u, 0x4240)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h.y) : "r"(__byte_perm(lo, 0x64646464u, 0x4341)), "r"(0x64806480u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h.z) : "r"(__byte_perm(hi, 0x64646464u, 0x4240)), "r"(0x2c002c00u), "r"(0xd480d480u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h.w) : "r"(__byte_perm(hi, 0x64646464u, 0x4341)), "r"(0x2c002c00u), "r"(0xd480d480u));
+    return h;
+}
+// D += A B: 16 rows by 16 or 32 K of A, as many K by 8 columns of B.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 template <int FMT, int TK>
 __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const __grid_constant__ MoeArgs A)
 {
-    constexpr int NW = mx_warps(TK), NT = 32 * NW;
-    constexpr int kUnit = mx_unit(FMT), kSlot = mx_slot(TK), kLines = kSlot / (kRows * kUnit);
-    static_assert(kLines % 16 == 0, "slices of whole passes: every lane steps through the codes alike");
-    constexpr bool kPairSums = TK <= 4;            // low and high halves in accumulators of their own
+    constexpr bool kMma = mx_mma(TK);
+    const int NW = kMma ? static_cast<int>(blockDim.x) >> 5 : mx_warps(TK), NT = 32 * NW;
+    constexpr int kTiles = kMma ? 2 : 1;           // tiles of a ticket, each with its part of a ring slot
+    constexpr int kUnit = mx_unit(FMT), kSlot = mx_slot(TK), kLines = kSlot / (kTiles * kRows * kUnit);
+    static_assert(kMma || kLines % 16 == 0, "slices of whole passes: every lane steps through the codes alike");
+    static_assert(!kMma || FMT != FMT_W4 || kLines * 32 * 15 * 128 <= (1 << 24), "a slice's sums are exact in fp32");
+    constexpr bool kSplit = mx_code(FMT, TK) == 2;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int S = mx_stages(TK);
-    const MxSmem L = mx_smem(TK, 0);
+    const MxSmem L = mx_smem(TK, NW, 0);
     uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + L.mask);
     uint16_t* ent0_s = reinterpret_cast<uint16_t*>(smem + L.ent0);
     uint16_t* off_s = reinterpret_cast<uint16_t*>(smem + L.off);
@@ -209,6 +267,8 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     const int P = A.M * slots;
     const int C1 = A.H >> 5, C2 = A.I >> 5;
     const int T1 = (A.I + 3) >> 2, T2 = (A.H + 7) >> 3;
+    const int U1 = (T1 + kTiles - 1) / kTiles, U2 = (T2 + kTiles - 1) / kTiles;      // tickets of a matrix
+    const int HS = mx_stride(FMT, TK, A.H);
     unsigned* ticket = A.ticket;
 
     uint8_t* ring = smem + L.ring + static_cast<size_t>(warp) * S * kSlot;
@@ -218,8 +278,9 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
         if (warp == 1) mbar_init(smem_u32(smem + L.bars) + static_cast<uint32_t>(NW * S) * 8u, 1);
         fence_mbar_init();
     }
-    if (tid > 0 && tid < kMxBatches) base_s[tid] = ~0ull;
+    if (tid > 1 && tid < kMxBatches) base_s[tid] = ~0ull;
     if (tid == NT - 1) misc[2] = 0;
+    if (tid >= 64 && tid < 80) xsum_s[tid - 64] = 0;
     const int EE = A.E + A.S;
     if (TK > 1)
         for (int e = tid; e < EE; e += NT) mask_s[e] = 0u;
@@ -230,21 +291,66 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
 
     // ---- the entries, the same in every block: pairs counted by expert in
     // the order of the pairs (warp 0); scales and code sums of the tokens (the others)
-    if (tid == NT - 1) base_s[0] = atomicAdd(ticket, static_cast<unsigned>(A.batch));
+    if (tid == NT - 1) {
+        base_s[0] = atomicAdd(ticket, static_cast<unsigned>(A.batch0));
+        base_s[1] = (1ull << 32) | atomicAdd(ticket, static_cast<unsigned>(A.batch));
+    }
     // (the codes before any weights: behind those a load waits for microseconds)
     const uint32_t xbar = smem_u32(smem + L.bars) + static_cast<uint32_t>(NW * S) * 8u;
-    if (A.stage_x && tid == 32) {
+    if (A.stage_x && !kSplit && tid == 32) {
         mbar_arrive_expect_tx(xbar, static_cast<uint32_t>(A.M * A.H));
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         smem_u32(smem + L.codes)),
-                     "l"(A.qx), "r"(static_cast<uint32_t>(A.M * A.H)), "r"(xbar)
-                     : "memory");
+        const int n = kMma ? A.M : 1, bytes = kMma ? A.H : A.M * A.H;
+        for (int m = 0; m < n; ++m)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(smem + L.codes) + static_cast<uint32_t>(m * HS)),
+                         "l"(A.qx + static_cast<size_t>(m) * A.H), "r"(static_cast<uint32_t>(bytes)), "r"(xbar)
+                         : "memory");
     }
     auto expert_of = [&](int p) -> int {
         const int m = p / slots, s = p - m * slots;
         if (s >= A.top_k) return A.E + s - A.top_k;
         const int e = __ldg(A.ids + m * A.top_k + s);
         return e < 0 || e >= A.E ? 0xffff : e;
+    };
+    // (every warp but the first)
+    auto stage_split = [&]() {
+        const int WT = NT - 32;
+        const int wt = tid - 32;
+        // the split codes of every token, eight reads of 16 codes to a thread at a time
+        if (wt < A.M) sx_s[wt] = __ldg(A.sx + wt);
+        const int per = A.H >> 4, n = A.M * per;
+        const uint4* q = reinterpret_cast<const uint4*>(A.qx);
+        for (int i0 = 0; i0 < n; i0 += 8 * WT) {
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * WT + wt;
+                v[k] = i < n ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int i = i0 + k * WT + wt;
+                if (i0 + k * WT >= n) break;
+                int at = 0, s = 0;
+                const int m = i < n ? div_by(i, per, A.inv_x16, at) : A.M - 1;
+                if (i < n) {
+                    uint4* to = reinterpret_cast<uint4*>(smem + L.codes + m * HS) + 2 * at;
+                    to[0] = codes_half(v[k].x, v[k].y);
+                    to[1] = codes_half(v[k].z, v[k].w);
+                    s = __dp4a(static_cast<int>(v[k].x), 0x01010101, s);
+                    s = __dp4a(static_cast<int>(v[k].y), 0x01010101, s);
+                    s = __dp4a(static_cast<int>(v[k].z), 0x01010101, s);
+                    s = __dp4a(static_cast<int>(v[k].w), 0x01010101, s);
+                }
+                // for the nibble bias
+                if (__all_sync(0xffffffffu, m == __shfl_sync(0xffffffffu, m, 0))) {
+                    s = __reduce_add_sync(0xffffffffu, s);
+                    if (lane == 0) atomicAdd(xsum_s + m, 8 * s);
+                } else {
+                    atomicAdd(xsum_s + m, 8 * s);
+                }
+            }
+        }
     };
     if (TK == 1) {
         // one token: every pair is an entry (at most kMxMaxSlots <= 32 of them)
@@ -263,7 +369,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             if (lane == 0) misc[0] = misc[1] = __popc(have);
         }
     } else {
-        static_assert(kMxMaxPairs <= 320 && NT >= 320, "a thread for each pair");
+        static_assert(kMxMaxPairs <= 32 * kMxFewestWarps && mx_warps(TK) >= kMxFewestWarps, "a thread for each pair");
         const int e = tid < P ? expert_of(tid) : 0xffff;
         const int m = tid / slots;
         if (tid < P) pair_e[tid] = static_cast<uint16_t>(e);
@@ -322,6 +428,8 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 scan([&](int x) { return static_cast<int>(mask_s[x]); });
             }
             if (lane == 0) misc[3] = at != valid;
+        } else if (kSplit) {
+            stage_split();
         }
         __syncthreads();
         const int rank = e == 0xffff ? 0 : misc[3] ? of_pos[tid] : __popc(mask_s[e] & ((1u << m) - 1u));
@@ -333,7 +441,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             of_pos[pos] = static_cast<uint16_t>(ent0_s[e] + rank / TK);
         }
     }
-    if (warp > 0) {
+    if (!kSplit && warp > 0) {
         bool ok = true;
         if (A.stage_x) ok = mbar_wait_bounded(xbar, 0u, kMxWaitNs);
         if (!ok && A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
@@ -341,7 +449,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
         for (int m = warp - 1; m < A.M; m += NW - 1) {
             int s = 0;
             if (FMT == FMT_W4) {                                            // for the nibble bias
-                const uint4* q = reinterpret_cast<const uint4*>(src + static_cast<size_t>(m) * A.H);
+                const uint4* q = reinterpret_cast<const uint4*>(src + static_cast<size_t>(m) * (A.stage_x ? HS : A.H));
 #pragma unroll 4
                 for (int i = lane; i < A.H / 16; i += 32) {
                     const uint4 v = q[i];
@@ -362,12 +470,12 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     const int NE = misc[0], PV = misc[1];
     const int nseg = (A.I + kMxSeg - 1) / kMxSeg;
     const int nadd = (A.H + kMxAdd - 1) / kMxAdd;
-    const int n1 = NE * T1, nq = n1 + PV * nseg, n2 = nq + NE * T2, total = n2 + A.M * nadd;
+    const int n1 = NE * U1, nq = n1 + PV * nseg, n2 = nq + NE * U2, total = n2 + A.M * nadd;
 
     // ---- tickets.  A block takes them from the global counter a batch at a
     // time (thousands of warps on one counter would wait for it: some 2 ns
     // each), its warps from a counter of their own; the warp that opens a batch
-    // fetches the next.  Claimed tickets wait in the lanes of `fifo` until
+    // fetches the one after the next.  Claimed tickets wait in the lanes of `fifo` until
     // their weights are consumed, as kind (0 gate/up, 1 quantize, 2 down,
     // 3 add), entry, place or token, and tile or segment.
     const uint64_t pol = l2_policy_evict_first();
@@ -379,30 +487,39 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     // the ticket whose slices are being issued
     const uint8_t* isrc = nullptr;
     int ileft = 0;                        // lines left of it
+    uint32_t isecond = 0;                 // bytes from its tile to the next one, 0 where there is none
     bool more = true;
     const float inv_batch = 1.0f / static_cast<float>(A.batch);
+    // First ticket of the block's batch b, from the warp that opened the batch before the last.
+    auto base_of = [&](int b) -> int {
+        unsigned long long v = base_s[b % kMxBatches];
+        if (static_cast<int>(v >> 32) != b) {
+            const uint64_t t0 = globaltimer_ns();
+            while (static_cast<int>((v = base_s[b % kMxBatches]) >> 32) != b) {
+                if (globaltimer_ns() - t0 > kMxWaitNs) {
+                    if (A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
+                    return 0x7fffffff;
+                }
+            }
+        }
+        return static_cast<int>(static_cast<uint32_t>(v));
+    };
     // The next ticket, or one past the last.
     auto claim = [&]() -> int {
         int next = 0;
         if (lane == 0) {
             int i;
             const int l = atomicAdd(const_cast<int*>(misc + 2), 1);
-            const int b = div_by(l, A.batch, inv_batch, i);
+            const int b = l < A.batch0 ? 0 : 1 + div_by(l - A.batch0, A.batch, inv_batch, i);
+            if (b == 0) i = l;
             if (i == 0) {
-                const unsigned long long got = atomicAdd(ticket, static_cast<unsigned>(A.batch));
-                base_s[(b + 1) % kMxBatches] = (static_cast<unsigned long long>(b + 1) << 32) | got;
+                // only once the batch in between is known: batches of a block come in the order of their tickets
+                const int last = base_of(b + 1);
+                const unsigned got = last >= total ? static_cast<unsigned>(last) : atomicAdd(ticket, static_cast<unsigned>(A.batch));
+                base_s[(b + 2) % kMxBatches] = (static_cast<unsigned long long>(b + 2) << 32) | got;
             }
-            unsigned long long v = base_s[b % kMxBatches];
-            if (static_cast<int>(v >> 32) != b) {
-                const uint64_t t0 = globaltimer_ns();
-                while (static_cast<int>((v = base_s[b % kMxBatches]) >> 32) != b) {
-                    if (globaltimer_ns() - t0 > kMxWaitNs) {
-                        if (A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
-                        break;
-                    }
-                }
-            }
-            next = static_cast<int>(v >> 32) == b ? static_cast<int>(static_cast<uint32_t>(v)) + i : 0x7fffffff;
+            const int base = base_of(b);
+            next = base >= total ? 0x7fffffff : base + i;
         }
         return __shfl_sync(0xffffffffu, next, 0);
     };
@@ -417,7 +534,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 return;
             }
             const int kind = next < n1 ? 0 : next < nq ? 1 : next < n2 ? 2 : 3;
-            const int TT = kind == 0 ? T1 : kind == 1 ? nseg : kind == 2 ? T2 : nadd;
+            const int TT = kind == 0 ? U1 : kind == 1 ? nseg : kind == 2 ? U2 : nadd;
             int sub;
             const int en = div_by(next - (kind == 0 ? 0 : kind == 1 ? n1 : kind == 2 ? nq : n2), TT,
                                   kind == 0 ? A.inv_t1 : kind == 1 ? A.inv_seg : kind == 2 ? A.inv_t2 : A.inv_add, sub);
@@ -425,19 +542,22 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 fifo = (static_cast<uint32_t>(kind) << 30) | (static_cast<uint32_t>(en) << 16) | static_cast<uint32_t>(sub);
             ++tail;
             if (!(kind & 1)) {
-                const int C = kind == 0 ? C1 : C2;
+                const int C = kind == 0 ? C1 : C2, T = kind == 0 ? T1 : T2;
                 isrc = (kind == 0 ? A.w_gu : A.w_dn) +
-                       static_cast<size_t>(static_cast<uint32_t>(ent_e[en]) * static_cast<uint32_t>(TT) + static_cast<uint32_t>(sub)) *
+                       static_cast<size_t>(static_cast<uint32_t>(ent_e[en]) * static_cast<uint32_t>(T) + static_cast<uint32_t>(kTiles * sub)) *
                            static_cast<uint32_t>(C * kRows * kUnit);
                 ileft = C;
+                if (kMma) isecond = 2 * sub + 1 < T ? static_cast<uint32_t>(C * kRows * kUnit) : 0u;
             }
         }
         const uint32_t n = static_cast<uint32_t>(min(ileft, kLines));
         // (the slot's reads are complete: their values have been used)
         if (elect_one()) {
             const uint32_t bar = bars + 8 * islot;
-            mbar_arrive_expect_tx(bar, n * (kRows * kUnit));
-            bulk_g2s(ring_u + static_cast<uint32_t>(islot * kSlot), isrc, n * (kRows * kUnit), bar, pol);
+            const uint32_t dst = ring_u + static_cast<uint32_t>(islot * kSlot);
+            mbar_arrive_expect_tx(bar, (kMma && isecond != 0u ? 2u : 1u) * n * (kRows * kUnit));
+            bulk_g2s(dst, isrc, n * (kRows * kUnit), bar, pol);
+            if (kMma && isecond != 0u) bulk_g2s(dst + kSlot / 2, isrc + isecond, n * (kRows * kUnit), bar, pol);
         }
         __syncwarp();
         isrc += n * (kRows * kUnit);
@@ -504,7 +624,15 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
             const A8Scale ks = a8_scale(mx);
             const uint64_t rr = f2_pack(ks.r, ks.r);
+            // a row of codes for each pair, or (tensor cores) the entry's tokens line by line, 32 codes of each
             uint32_t* qp = reinterpret_cast<uint32_t*>(A.qh + static_cast<size_t>(p) * A.I);
+            int qstep = 8;
+            if constexpr (kMma) {
+                const int at = static_cast<int>((t >> 16) & 0x3fffu), en = of_pos[at];
+                qstep = 8 * mx_code(FMT, TK) * ent_n[en];
+                qp = reinterpret_cast<uint32_t*>(A.qh + static_cast<size_t>(ent_off[en]) * A.I * mx_code(FMT, TK)) +
+                     8 * mx_code(FMT, TK) * (at - ent_off[en]);
+            }
             const int i1 = min(n4, (tile + 1) * (kMxSeg / 4));
             int sum = 0;
 #pragma unroll 4
@@ -514,7 +642,15 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 uint32_t good = 0xffffffffu;
                 uint32_t q = a8_pack4_fast2(v, rr, good);
                 if (a8_needs_exact(ks) || (good >> 31) == 0u) q = a8_pack4_exact(v, ks);
-                qp[i] = q;
+                if constexpr (kSplit) {
+                    // (words of K 0 .. 3 and 4 .. 7 in turn)
+                    const uint4 h2 = codes_half(q, q);
+                    *reinterpret_cast<uint2*>(qp + (i >> 3) * qstep + ((i & 7) << 1)) = i & 1 ? make_uint2(h2.z, h2.w) : make_uint2(h2.x, h2.y);
+                } else if constexpr (kMma) {
+                    qp[(i >> 3) * qstep + (i & 7)] = q;
+                } else {
+                    qp[i] = q;
+                }
                 sum = __dp4a(static_cast<int>(q), 0x01010101, sum);
             }
             sum = __reduce_add_sync(0xffffffffu, sum);
@@ -571,35 +707,40 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
         const int e = ent_e[en], pos0 = ent_off[en];
         const int cnt = TK == 1 ? 1 : ent_n[en];
         const int C = down ? C2 : C1;
-        const int8_t* codes = (down ? A.qh : A.stage_x ? reinterpret_cast<const int8_t*>(smem + L.codes) : A.qx) + pl * 32;
         // this lane's row parameters, wanted at the tile's end
-        float sw = 0.0f, bv = 0.0f;
-        {
-            const int row = down ? (8 * tile + my_row < A.H ? 8 * tile + my_row : -1) : glu_param_row(8 * tile + my_row, A.I);
+        auto row_params = [&](int row8, float& sw, float& bv) {      // row8: row counted in tiles of eight
+            const int row = down ? (row8 < A.H ? row8 : -1) : glu_param_row(row8, A.I);
             const uint32_t at = static_cast<uint32_t>(e) * static_cast<uint32_t>(down ? A.H : 2 * A.I) + static_cast<uint32_t>(row);
             const float* bias = down ? A.b_dn : A.b_gu;
+            sw = bv = 0.0f;
             if (row >= 0) {
                 sw = __ldg((down ? A.s_dn : A.s_gu) + at);
                 if (bias != nullptr) bv = __ldg(bias + at);
             }
-        }
+        };
+        float sw[kTiles], bv[kTiles];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) row_params(8 * (kTiles * tile + i) + (kMma ? lane >> 2 : my_row), sw[i], bv[i]);
         if (down) {
             if (ready_s[en] == 0) {
-                // the pieces of the entry's pairs: there, and their sums
+                // the pieces of the entry's pairs: there, and their sums (four pieces of eight pairs at a time)
                 bool ok = true;
                 int sums = 0;
                 float scale = 0.0f;
-                for (int g = 0; g < nseg && ok; ++g) {
+                const unsigned long long* done = A.qdone + static_cast<size_t>(list[pos0 + min(lane & 7, cnt - 1)]) * nseg;
+                for (int g0 = 0; g0 < nseg && ok; g0 += 4) {
                     unsigned long long v = 0;
-                    const int p = list[pos0 + min(lane, cnt - 1)];
+                    const int g = g0 + (lane >> 3);
                     ok = wait_words([&]() {
-                        v = ld_acquire_u64(A.qdone + static_cast<size_t>(p) * nseg + g);
+                        v = ld_acquire_u64(done + min(g, nseg - 1));
                         return static_cast<uint32_t>(v >> 32) != kMxNoValue;
                     });
-                    sums += __float2int_rn(__uint_as_float(static_cast<uint32_t>(v >> 32)));
+                    if (g < nseg) sums += __float2int_rn(__uint_as_float(static_cast<uint32_t>(v >> 32)));
                     scale = __uint_as_float(static_cast<uint32_t>(v));
                 }
                 if (!ok) break;
+                sums += __shfl_xor_sync(0xffffffffu, sums, 8);
+                sums += __shfl_xor_sync(0xffffffffu, sums, 16);
                 if (lane < cnt) {
                     sh_s[pos0 + lane] = scale;
                     hs_s[pos0 + lane] = 8 * sums;
@@ -610,30 +751,181 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             }
             __threadfence_block();
         }
-        uint32_t off[TK];
         const uint32_t KK = static_cast<uint32_t>(down ? A.I : A.H);
-#pragma unroll
-        for (int m = 0; m < TK; ++m) {
-            const int at = pos0 + min(m, cnt - 1);
-            off[m] = static_cast<uint32_t>(down ? list[at] : tok_s[at]) * KK;
-        }
-        int acc[TK][4], acch[kPairSums ? TK : 1][4];
-#pragma unroll
-        for (int m = 0; m < TK; ++m)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[m][j] = 0;
-                if (kPairSums) acch[m][j] = 0;
-            }
-        for (int c = 0; c < C; c += kLines) {
+        // Waits for the tile's next slice; false after a wait that ran out.
+        auto slice_landed = [&]() {
             const uint32_t bar = bars + 8 * cslot;
             bool ok = __all_sync(0xffffffffu, mbar_test_wait(bar, cph));
             if (!ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, cph, kMxWaitNs));
             if (!ok) {
                 dead = true;
                 if (lane == 0 && A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
-                break;
             }
+            __syncwarp();
+            return ok;
+        };
+        auto slice_read = [&]() {
+            if (++cslot == S) {
+                cslot = 0;
+                cph ^= 1u;
+            }
+            ++consumed;
+            __syncwarp();
+            issue_one();
+        };
+        if constexpr (kMma) {
+            constexpr int kCode = mx_code(FMT, TK);
+            const int g = lane >> 2, tq = lane & 3, gm = min(g, cnt - 1);
+            const uint8_t* xp = down ? reinterpret_cast<const uint8_t*>(A.qh) + static_cast<size_t>(pos0) * A.I * kCode + gm * 32 * kCode
+                                     : smem + L.codes + tok_s[pos0 + gm] * HS;
+            const int xstep = down ? 32 * kCode * cnt : 32 * kCode;
+            xp += 8 * kCode * tq;
+            int acc[4] = {0, 0, 0, 0};       // rows g of both tiles by tokens 2 tq, 2 tq + 1
+            for (int c = 0; c < C; c += kLines) {
+                if (!slice_landed()) break;
+                const uint8_t* ub = ring + cslot * kSlot + g * kUnit + tq * (kUnit / 4);
+                const int n = min(kLines, C - c);
+                if constexpr (FMT == FMT_W4) {
+                    // nibble w + 8 at bit 0 or 16 of a pair's half is, as it stands, the fp16 number (w + 8) 2^-24, at
+                    // bit 4 16 times that: the sums are multiples of 2^-24 below 1, exact in fp32
+                    // (four chains: a product's result takes some 35 cycles)
+                    float d[4][4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[k][i] = 0.0f;
+                    struct Lines {
+                        uint32_t w0[4], w1[4];
+                        uint4 x[4];
+                    };
+                    auto load = [&](Lines& v, int l0, int count) {
+#pragma unroll
+                        for (int l = 0; l < 4; ++l) {
+                            if (l < count) {
+                                v.w0[l] = *reinterpret_cast<const uint32_t*>(ub + (l0 + l) * (kRows * kUnit));
+                                v.w1[l] = *reinterpret_cast<const uint32_t*>(ub + (l0 + l) * (kRows * kUnit) + kSlot / 2);
+                                v.x[l] = *reinterpret_cast<const uint4*>(xp + (l0 + l) * xstep);
+                            }
+                        }
+                    };
+                    auto multiply = [&](const Lines& v, int count) {
+#pragma unroll
+                        for (int l = 0; l < 4; ++l) {
+                            if (l < count) {
+                                const uint32_t u0 = v.w0[l] >> 8, u1 = v.w1[l] >> 8;
+                                mma_f16(d[2 * (l & 1)], v.w0[l] & 0x000f000fu, v.w1[l] & 0x000f000fu, v.w0[l] & 0x00f000f0u,
+                                        v.w1[l] & 0x00f000f0u, v.x[l].x, v.x[l].z);
+                                mma_f16(d[2 * (l & 1) + 1], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
+                                        v.x[l].y, v.x[l].w);
+                            }
+                        }
+                    };
+                    Lines v[2];
+                    if (n == kLines) {
+                        load(v[0], 0, 4);
+#pragma unroll
+                        for (int l = 0; l < kLines; l += 4) {
+                            if (l + 4 < kLines) load(v[(l / 4 + 1) & 1], l + 4, 4);
+                            multiply(v[(l / 4) & 1], 4);
+                        }
+                    } else {
+                        int l = 0;
+#pragma unroll 1
+                        for (; l + 4 <= n; l += 4) {
+                            load(v[0], l, 4);
+                            multiply(v[0], 4);
+                        }
+#pragma unroll 1
+                        for (; l < n; ++l) {
+                            load(v[0], l, 1);
+                            multiply(v[0], 1);
+                        }
+                    }
+                    xp += n * xstep;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[i] += __float2int_rn(__fmul_rn(__fadd_rn(__fadd_rn(d[0][i], d[1][i]), __fadd_rn(d[2][i], d[3][i])), 16777216.0f));
+                } else {
+                    auto lines = [&](auto count) {
+                        constexpr int kN = decltype(count)::value;
+                        uint2 w0[kN], w1[kN], x[kN];
+#pragma unroll
+                        for (int l = 0; l < kN; ++l) {
+                            w0[l] = *reinterpret_cast<const uint2*>(ub + l * (kRows * kUnit));
+                            w1[l] = *reinterpret_cast<const uint2*>(ub + l * (kRows * kUnit) + kSlot / 2);
+                            x[l] = *reinterpret_cast<const uint2*>(xp + l * xstep);
+                        }
+#pragma unroll
+                        for (int l = 0; l < kN; ++l) mma_s8(acc, w0[l].x, w1[l].x, w0[l].y, w1[l].y, x[l].x, x[l].y);
+                        ub += kN * (kRows * kUnit);
+                        xp += kN * xstep;
+                    };
+                    if (n == kLines) lines(std::integral_constant<int, kLines>());
+                    else
+#pragma unroll 1
+                        for (int l = 0; l < n; ++l) lines(std::integral_constant<int, 1>());
+                }
+                slice_read();
+            }
+            if (dead) break;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = pos0 + min(2 * tq + (i & 1), cnt - 1), tok = tok_s[at];
+                const int a = FMT == FMT_W4 ? acc[i] - (down ? hs_s[at] : xsum_s[tok]) : acc[i];
+                v[i] = __fmaf_rn(__fmul_rn(sw[i >> 1], down ? sh_s[at] : sx_s[tok]), __int2float_rn(a), bv[i >> 1]);
+            }
+            if (down) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = 2 * tq + (i & 1), row = 8 * (2 * tile + (i >> 1)) + g;
+                    if (m < cnt && row < A.H) st_value(A.part + static_cast<size_t>(list[pos0 + min(m, cnt - 1)]) * A.H + row, v[i]);
+                }
+                continue;
+            }
+            // Rows 0 .. 3 are gates, 4 .. 7 their ups: the lanes of gates take the first tile's values, the others the
+            // second's.  Lanes have tokens 2 tq and 2 tq + 1, or (up to four) token tq: one activation instead of two.
+            float gt[2], up[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float got = __shfl_xor_sync(0xffffffffu, g < 4 ? v[2 + i] : v[i], 16);
+                gt[i] = g < 4 ? v[i] : got;
+                up[i] = g < 4 ? got : v[2 + i];
+            }
+            const int j = 4 * (2 * tile + (g >> 2)) + (g & 3);
+            const bool spread = cnt <= 4;
+            if (spread) {
+                const int from = (lane & 28) | (tq >> 1);
+                const float g0 = __shfl_sync(0xffffffffu, gt[0], from), g1 = __shfl_sync(0xffffffffu, gt[1], from);
+                const float u0 = __shfl_sync(0xffffffffu, up[0], from), u1 = __shfl_sync(0xffffffffu, up[1], from);
+                gt[0] = tq & 1 ? g1 : g0;
+                up[0] = tq & 1 ? u1 : u0;
+            }
+#pragma unroll 1
+            for (int i = 0; i < (spread ? 1 : 2); ++i) {
+                const int m = spread ? tq : 2 * tq + i;
+                if (m < cnt && j < A.I)
+                    st_value(A.h + static_cast<size_t>(list[pos0 + m]) * A.I + j, xa_glu(A.glu, i == 0 ? gt[0] : gt[1], i == 0 ? up[0] : up[1]));
+            }
+            continue;
+        } else {
+        const int8_t* codes = (down ? A.qh : A.stage_x ? reinterpret_cast<const int8_t*>(smem + L.codes) : A.qx) + pl * 32;
+        uint32_t off[TK];
+#pragma unroll
+        for (int m = 0; m < TK; ++m) {
+            const int at = pos0 + min(m, cnt - 1);
+            off[m] = static_cast<uint32_t>(down ? list[at] : tok_s[at]) * KK;
+        }
+        int acc[TK][4], acch[TK][4];             // low and high halves in accumulators of their own
+#pragma unroll
+        for (int m = 0; m < TK; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[m][j] = 0;
+                acch[m][j] = 0;
+            }
+        for (int c = 0; c < C; c += kLines) {
+            if (!slice_landed()) break;
             const uint8_t* ub = ring + cslot * kSlot + (pl * kRows + 4 * hb) * kUnit;
             const int n = min(kLines, C - c) - pl;          // this lane's lines: 0, 16, .. < n
 #pragma unroll 2
@@ -656,26 +948,13 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                     if (m == 0 || m < cnt) {
                         const uint4* xp = reinterpret_cast<const uint4*>(codes + off[m]);
                         const uint4 x0 = xp[0], x1 = xp[1];
-                        if constexpr (kPairSums) {
-                            line_dot<FMT>(w0, w1, x0, x1, acc[m], acch[m]);
-                        } else {
-                            int hi[4] = {0, 0, 0, 0};
-                            line_dot<FMT>(w0, w1, x0, x1, acc[m], hi);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[m][j] += FMT == FMT_W4 ? hi[j] >> 4 : hi[j];
-                        }
+                        line_dot<FMT>(w0, w1, x0, x1, acc[m], acch[m]);
                     }
                 }
                 ub += 16 * kRows * kUnit;
                 codes += 16 * 32;
             }
-            if (++cslot == S) {
-                cslot = 0;
-                cph ^= 1u;
-            }
-            ++consumed;
-            __syncwarp();
-            issue_one();
+            slice_read();
         }
         if (dead) break;
         // lanes of equal (hb, pp) add up, then the read permutation is undone:
@@ -685,7 +964,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             if (m < cnt) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (kPairSums) acc[m][j] += FMT == FMT_W4 ? acch[m][j] >> 4 : acch[m][j];
+                    acc[m][j] += FMT == FMT_W4 ? acch[m][j] >> 4 : acch[m][j];
                     acc[m][j] += __shfl_xor_sync(0xffffffffu, acc[m][j], 8);
                     acc[m][j] += __shfl_xor_sync(0xffffffffu, acc[m][j], 16);
                 }
@@ -709,15 +988,16 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 if (FMT == FMT_W4) a -= hs_s[at];
                 const int row = 8 * tile + my_row;
                 if (have && row < A.H)
-                    st_value(A.part + static_cast<size_t>(p) * A.H + row, __fmaf_rn(__fmul_rn(sw, sh_s[at]), __int2float_rn(a), bv));
+                    st_value(A.part + static_cast<size_t>(p) * A.H + row, __fmaf_rn(__fmul_rn(sw[0], sh_s[at]), __int2float_rn(a), bv[0]));
             } else {
                 const int tok = tok_s[at];
                 if (FMT == FMT_W4) a -= xsum_s[tok];
-                const float v = __fmaf_rn(__fmul_rn(sw, sx_s[tok]), __int2float_rn(a), bv);
+                const float v = __fmaf_rn(__fmul_rn(sw[0], sx_s[tok]), __int2float_rn(a), bv[0]);
                 const float u = __shfl_xor_sync(0xffffffffu, v, 1);      // gate lanes are even, up lanes odd
                 const int j = 4 * tile + pp;
                 if (have && hb == 0 && j < A.I) st_value(A.h + static_cast<size_t>(p) * A.I + j, xa_glu(A.glu, v, u));
             }
+        }
         }
     }
     // after a wait that ran out: the copies in flight land before the block ends
@@ -734,7 +1014,7 @@ __global__ void __launch_bounds__(256) moe_fill_kernel(const MoeFill f)
 }
 
 template <int FMT, int TK>
-cudaError_t launch_experts_t(const MoeArgs& a, int grid, size_t smem, bool pdl, cudaStream_t s)
+cudaError_t launch_experts_t(const MoeArgs& a, int grid, int warps, size_t smem, bool pdl, cudaStream_t s)
 {
     auto kern = moe_experts_kernel<FMT, TK>;
     static SmemLimit limit;
@@ -742,7 +1022,7 @@ cudaError_t launch_experts_t(const MoeArgs& a, int grid, size_t smem, bool pdl, 
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(32 * mx_warps(TK));
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -754,26 +1034,35 @@ cudaError_t launch_experts_t(const MoeArgs& a, int grid, size_t smem, bool pdl, 
 }
 
 template <int FMT>
-cudaError_t launch_experts_f(int tok, const MoeArgs& a, int grid, size_t smem, bool pdl, cudaStream_t s)
+cudaError_t launch_experts_f(int tok, const MoeArgs& a, int grid, int warps, size_t smem, bool pdl, cudaStream_t s)
 {
-    if (tok <= 1) return launch_experts_t<FMT, 1>(a, grid, smem, pdl, s);
-    if (tok <= 2) return launch_experts_t<FMT, 2>(a, grid, smem, pdl, s);
-    if (tok <= 4) return launch_experts_t<FMT, 4>(a, grid, smem, pdl, s);
-    return launch_experts_t<FMT, 8>(a, grid, smem, pdl, s);
+    if (tok <= 1) return launch_experts_t<FMT, 1>(a, grid, warps, smem, pdl, s);
+    if (tok <= 2) return launch_experts_t<FMT, 2>(a, grid, warps, smem, pdl, s);
+    if constexpr (FMT != FMT_W4)
+        if (tok <= 4) return launch_experts_t<FMT, 4>(a, grid, warps, smem, pdl, s);
+    return launch_experts_t<FMT, 8>(a, grid, warps, smem, pdl, s);
 }
 
 }  // namespace
 
-int moe_warps(int tok) { return mx_warps(tok); }
-size_t moe_experts_smem(int tok, int staged_bytes)
+MoePlan moe_plan(int fmt, int tok, int M, int H, size_t most)
 {
-    return static_cast<size_t>(mx_smem(tok, staged_bytes).total);
+    MoePlan p;
+    p.tiles = mx_mma(tok) ? 2 : 1;
+    p.warps = mx_warps(tok);
+    const size_t staged = static_cast<size_t>(M) * static_cast<size_t>(mx_stride(fmt, tok, H));
+    auto total = [&](size_t codes) { return static_cast<size_t>(mx_smem(tok, p.warps, 0).total) + codes; };
+    while (mx_mma(tok) && p.warps > kMxFewestWarps && total(staged) > most) --p.warps;
+    p.staged = total(staged) <= most;
+    p.smem = total(p.staged ? staged : 0);
+    p.fits = p.smem <= most && (p.staged || !mx_mma(tok));
+    return p;
 }
 
-cudaError_t launch_moe_experts(int fmt, int tok, const MoeArgs& a, int grid, size_t smem, bool pdl, cudaStream_t s)
+cudaError_t launch_moe_experts(int fmt, int tok, const MoeArgs& a, int grid, int warps, size_t smem, bool pdl, cudaStream_t s)
 {
-    return fmt == FMT_W4 ? launch_experts_f<FMT_W4>(tok, a, grid, smem, pdl, s)
-                         : launch_experts_f<FMT_W8F>(tok, a, grid, smem, pdl, s);
+    return fmt == FMT_W4 ? launch_experts_f<FMT_W4>(tok, a, grid, warps, smem, pdl, s)
+                         : launch_experts_f<FMT_W8F>(tok, a, grid, warps, smem, pdl, s);
 }
 
 cudaError_t launch_moe_fill(const MoeFill& f, bool pdl, cudaStream_t s)

@@ -218,8 +218,9 @@ struct MoeArgs {
     int ytype, glu;
     int M, H, I, E, S, top_k;
     int stage_x;              // the tokens' codes are copied into shared memory
-    int batch;                // tickets that a block takes at once
-    float inv_t1, inv_t2, inv_seg, inv_add;   // 1 / (tiles of a gate/up and of a down matrix, quantizing tasks of a
+    int batch0, batch;        // tickets that a block takes at once: at its start, later
+    float inv_x16;            // 16 / H
+    float inv_t1, inv_t2, inv_seg, inv_add;   // 1 / (tickets of a gate/up and of a down matrix, quantizing tasks of a
                               // pair, adding tasks of a token)
     unsigned* ticket;         // zero at the start
     float* h;                 // [pairs][I], kMxNoValue at the start, and so
@@ -228,10 +229,15 @@ struct MoeArgs {
     int8_t* qh;               // [pairs][I] codes
     unsigned* err;
 };
-// `tok`: pairs per entry (1, 2, 4 or 8).  Warps per block and ring slots per warp follow from it.
-int moe_warps(int tok);
-size_t moe_experts_smem(int tok, int staged_bytes);
-cudaError_t launch_moe_experts(int fmt, int tok, const MoeArgs& a, int grid, size_t smem, bool pdl, cudaStream_t s);
+// Launch shape for `tok` pairs per entry (1, 2, 4 or 8) on `most` bytes of shared memory.
+struct MoePlan {
+    int warps, tiles;         // per block; weight tiles to a ticket
+    bool staged;              // the tokens' codes go into shared memory
+    bool fits;
+    size_t smem;
+};
+MoePlan moe_plan(int fmt, int tok, int M, int H, size_t most);
+cudaError_t launch_moe_experts(int fmt, int tok, const MoeArgs& a, int grid, int warps, size_t smem, bool pdl, cudaStream_t s);
 cudaError_t launch_moe_fill(const MoeFill& f, bool pdl, cudaStream_t s);
 
 }  // namespace w4k

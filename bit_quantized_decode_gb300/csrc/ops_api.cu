@@ -247,7 +247,7 @@ MoeSpace moe_space(const w4_experts* e, int M, int top_k)
     w.part = w.h + P * e->I * 4;
     w.qdone = w.part + P * e->H * 4;
     w.qh = w.qdone + (P * nseg * 8 + 127) / 128 * 128;
-    w.total = w.qh + P * e->I;
+    w.total = w.qh + P * e->I * (e->fmt == W4_FMT_W4 ? 2 : 1);       // (INT4 on the tensor cores: as fp16)
     return w;
 }
 MoeFill moe_fill_of(const MoeSpace& w, void* ws)
@@ -256,15 +256,25 @@ MoeFill moe_fill_of(const MoeSpace& w, void* ws)
 }
 
 // Pairs per entry (an expert and some of its tokens, whose weights are read
-// once): no more than there are tokens, and no more than an expert has as a
-// rule.  Four leave registers for 20 warps per SM instead of 16, and a further
-// entry reads its weights from L2.
-int moe_entry_pairs(int M, int top_k, int E, int n_shared)
+// once).  Where an expert that is reached at all has one token as a rule, the
+// DP4A entries of two tokens (INT4) or four (INT8) are ahead, elsewhere the
+// tensor cores' eight.  64 experts of 2368 x 3584 in INT4, top 8: 6 tokens (1.36
+// tokens per expert) 105 us by two, 108 by eight; 8 tokens (1.52) 129 and 123, 16
+// tokens 213 and 177.  128 experts of 768 x 1536 and a shared one in INT8, top 6:
+// 5 tokens 42.4 us by four, 47.5 by eight; 10 tokens (1.41) 58 and 55.
+int moe_entry_pairs(const DeviceFacts& d, const w4_experts* e, int M, int top_k, MoePlan& p)
 {
-    if (M <= 2) return M < 1 ? 1 : M;
-    const double reached = 1.0 - pow(1.0 - static_cast<double>(top_k < E ? top_k : E) / E, M);   // share of the experts
-    const double each = static_cast<double>(M) * top_k / (E * reached);
-    return M <= 4 || (n_shared == 0 && each <= 3.0) ? 4 : kMxTok;
+    const size_t most = static_cast<size_t>(d.smem_optin);
+    if (M > 2) {
+        const double reached = e->E * (1.0 - pow(1.0 - static_cast<double>(top_k < e->E ? top_k : e->E) / e->E, M)) + e->n_shared;
+        if (static_cast<double>(M) * (top_k + e->n_shared) > 1.4 * reached) {
+            p = moe_plan(e->fmt, kMxTok, M, e->H, most);
+            if (p.fits) return kMxTok;
+        }
+    }
+    const int tok = M <= 1 ? 1 : M == 2 || e->fmt == W4_FMT_W4 ? 2 : 4;
+    p = moe_plan(e->fmt, tok, M, e->H, most);
+    return tok;
 }
 
 w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, const int* ids, const float* weights, int M,
@@ -301,21 +311,26 @@ w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, co
     a.qdone = reinterpret_cast<unsigned long long*>(base + w.qdone);
     a.qh = reinterpret_cast<int8_t*>(base + w.qh);
     a.err = d.err;
-    const int tok = moe_entry_pairs(M, top_k, e->E, e->n_shared);
-    const int warps = moe_warps(tok);
-    a.inv_t1 = 1.0f / static_cast<float>((e->I + 3) / 4);
-    a.inv_t2 = 1.0f / static_cast<float>((e->H + 7) / 8);
+    MoePlan plan;
+    const int tok = moe_entry_pairs(d, e, M, top_k, plan);
+    if (!plan.fits) return W4_ERR_UNSUPPORTED_SHAPE;
+    a.inv_x16 = 16.0f / static_cast<float>(e->H);
+    const int u = plan.tiles;
+    const int u1 = ((e->I + 3) / 4 + u - 1) / u, u2 = ((e->H + 7) / 8 + u - 1) / u;
+    a.inv_t1 = 1.0f / static_cast<float>(u1);
+    a.inv_t2 = 1.0f / static_cast<float>(u2);
     a.inv_seg = 1.0f / static_cast<float>((e->I + kMxSeg - 1) / kMxSeg);
     a.inv_add = 1.0f / static_cast<float>((e->H + kMxAdd - 1) / kMxAdd);
-    a.stage_x = moe_experts_smem(tok, M * e->H) <= static_cast<size_t>(d.smem_optin);
-    const size_t smem = moe_experts_smem(tok, a.stage_x ? M * e->H : 0);
-    if (smem > static_cast<size_t>(d.smem_optin)) return W4_ERR_UNSUPPORTED_SHAPE;
-    // every SM a share of the gate/up tiles, in one to `warps` tickets at a time
-    const long long work = static_cast<long long>(M) * (top_k + e->n_shared) * ((e->I + 3) / 4);
+    a.stage_x = plan.staged;
+    // every SM a share of the gate/up tiles: a ticket for each warp at the start
+    // (or fewer), then a few at a time, two batches ahead (a batch takes a
+    // microsecond to fetch, a ticket some ten to work off)
+    const long long work = static_cast<long long>(M) * (top_k + e->n_shared) * u1;
     const int grid = work < d.sms ? static_cast<int>(work) : d.sms;
     const long long share = work / grid;
-    a.batch = share < warps ? static_cast<int>(share) : warps;
-    return cuda_status(launch_moe_experts(e->fmt, tok, a, grid, smem, true, s));
+    a.batch0 = share < plan.warps ? static_cast<int>(share) : plan.warps;
+    a.batch = share >= 8 ? 4 : share >= 4 ? 2 : 1;
+    return cuda_status(launch_moe_experts(e->fmt, tok, a, grid, plan.warps, plan.smem, true, s));
 }
 
 }  // namespace

@@ -108,3 +108,36 @@ def test_dependent_launches_share_buffers_and_workspaces(bq):
         torch.cuda.synchronize()
         for got, w in zip(ys + zs, want + wmoe):
             assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("fmt", ["w4", "w8"])
+def test_many_small_expert_calls_all_finish(bq, fmt):
+    """Blocks that take their tickets one at a time get them in order: thousands of small calls, each of them complete."""
+    import torch
+    g = wl.rng(9)
+    H = 512
+    layer = _moe(bq, fmt, g, H, 256, 12, 3)
+    for M, calls in ((1, 6000), (2, 2000), (7, 1000)):
+        x = dev(wl.residual_stream(g, M, H))
+        want = layer(x, residual=x).clone()
+        b = layer.buffers(M)
+        wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+        for _ in range(calls):
+            b.y.fill_(float("nan"))
+            layer(x, b, residual=x)
+            wrong += (b.y != want).any()
+        assert int(wrong) == 0 and bq._lib.device_error() == 0
+
+
+@pytest.mark.parametrize("fmt,M,H,I,E,k", [("w4", 16, 8192, 64, 4, 2), ("w8", 16, 16384, 64, 4, 2), ("w4", 9, 96, 4160, 3, 2),
+                                           ("w8", 16, 2080, 2976, 3, 3), ("w4", 16, 2080, 2976, 3, 3), ("w4", 16, 32, 32, 2, 1)])
+def test_batches_equal_single_tokens(bq, fmt, M, H, I, E, k):
+    """Every way to batch an expert's tokens gives each of them the bits that it has alone: codes that do not fit shared
+    memory, several entries to an expert, odd numbers of tiles, slices that end early, one line."""
+    import torch
+    g = wl.rng(M + H)
+    layer = _moe(bq, fmt, g, H, I, E, k)
+    x = dev(wl.residual_stream(g, M, H))
+    y = layer(x).clone()
+    for m in range(M):
+        assert torch.equal(layer(x[m:m + 1].contiguous()), y[m:m + 1])
