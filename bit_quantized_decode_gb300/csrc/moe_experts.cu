@@ -19,10 +19,11 @@
 //     which running warps hold and finish without waiting on later ones: the
 //     kernel needs no co-resident grid and two of them may share the GPU.
 //   * An entry is an expert and some of its tokens; more of them are further
-//     entries.  Up to two tokens (INT8: four): a lane holds four rows by the
-//     tokens of integer sums (DP4A, as the decode GEMV: line lane / 2 of a
-//     16-line pass, rows 4 (lane & 1) .. + 3, reads permuted against bank
-//     conflicts, a shuffle butterfly at the end of a tile).
+//     entries.  Up to two tokens: a lane holds four rows by the tokens of
+//     integer sums (DP4A, as the decode GEMV: line lane / 2 of a 16-line pass,
+//     rows 4 (lane & 1) .. + 3, reads permuted against bank conflicts, a shuffle
+//     butterfly at the end of a tile).  One token, eight of 64 experts of 2368 x
+//     3584 (102 MB of INT4): 36 us with the router.
 //   * Up to eight tokens: mma.sync on two tiles at a time, the weights as the 16
 //     rows of A, the tokens as the eight columns of B.  So few columns leave
 //     tcgen05 nothing to gain (its smallest tile has 64 or 128 rows, and A would
@@ -36,7 +37,7 @@
 //     INT8 tiles just afford and INT4 ones would not.
 //     A slice of 16 lines takes a warp some 1600 cycles and its copies and
 //     bookkeeping another 1300; waits for memory are 5%.  16 tokens over 64
-//     experts of 2368 x 3584 (722 MB of INT4): 177 us with the router; DP4A 202.
+//     experts of 2368 x 3584 (722 MB of INT4): 178 us with the router; DP4A 202.
 //   * No fence per tile (it waits for all that the warp has outstanding: it
 //     took 3500 of a tile's 9500 cycles): hidden values and the slots' outputs
 //     are prepared with a value that no result takes (MoeFill), and a reader
@@ -61,15 +62,15 @@ constexpr uint64_t kMxWaitNs = 250ull * 1000ull * 1000ull;
 __host__ __device__ constexpr int mx_unit(int fmt) { return fmt == FMT_W4 ? 16 : 32; }
 // Ring slots: bytes, slots per warp and warps per block.  A slot costs a wait
 // and a copy however large it is, so where an entry has one or two tokens (few
-// sums per weight) the slots are large; with more, more warps.  On the tensor
-// cores as many of the warps as fit beside the tokens' codes (8 tokens of 3584:
-// 16 warps 121 us, 12 warps 135).
+// sums per weight) the slots are large.  On the tensor cores more warps, as many
+// as fit beside the tokens' codes (8 tokens of 3584: 16 warps 121 us, 12 warps
+// 135).
 __host__ __device__ constexpr int mx_slot(int tok) { return tok <= 2 ? 8192 : 4096; }
 __host__ __device__ constexpr int mx_stages(int) { return 2; }
-__host__ __device__ constexpr int mx_warps(int tok) { return tok <= 2 ? 12 : tok <= 4 ? 20 : 16; }
+__host__ __device__ constexpr int mx_warps(int tok) { return tok <= 2 ? 12 : 16; }
 constexpr int kMxFewestWarps = 10;                 // a thread for each pair
-// Entries of more than four tokens multiply on the tensor cores, two tiles at a time.
-__host__ __device__ constexpr bool mx_mma(int tok) { return tok > 4; }
+// Entries of more than two tokens multiply on the tensor cores, two tiles at a time.
+__host__ __device__ constexpr bool mx_mma(int tok) { return tok > 2; }
 // Bytes of a code as a kernel reads it (INT4 on the tensor cores: fp16), and the stride of the tokens' staged codes: what a read takes of
 // several tokens lies in banks of their own.
 __host__ __device__ constexpr int mx_code(int fmt, int tok) { return mx_mma(tok) && fmt == FMT_W4 ? 2 : 1; }
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     constexpr bool kMma = mx_mma(TK);
     const int NW = kMma ? static_cast<int>(blockDim.x) >> 5 : mx_warps(TK), NT = 32 * NW;
     constexpr int kTiles = kMma ? 2 : 1;           // tiles of a ticket, each with its part of a ring slot
+    constexpr int kAdd = mx_add(TK);
     constexpr int kUnit = mx_unit(FMT), kSlot = mx_slot(TK), kLines = kSlot / (kTiles * kRows * kUnit);
     static_assert(kMma || kLines % 16 == 0, "slices of whole passes: every lane steps through the codes alike");
     static_assert(!kMma || FMT != FMT_W4 || kLines * 32 * 15 * 128 <= (1 << 24), "a slice's sums are exact in fp32");
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     __syncthreads();
     const int NE = misc[0], PV = misc[1];
     const int nseg = (A.I + kMxSeg - 1) / kMxSeg;
-    const int nadd = (A.H + kMxAdd - 1) / kMxAdd;
+    const int nadd = (A.H + kAdd - 1) / kAdd;
     const int n1 = NE * U1, nq = n1 + PV * nseg, n2 = nq + NE * U2, total = n2 + A.M * nadd;
 
     // ---- tickets.  A block takes them from the global counter a batch at a
@@ -489,6 +491,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     int ileft = 0;                        // lines left of it
     uint32_t isecond = 0;                 // bytes from its tile to the next one, 0 where there is none
     bool more = true;
+    bool task = false;                    // a quantizing or adding task is claimed and not done
     const float inv_batch = 1.0f / static_cast<float>(A.batch);
     // First ticket of the block's batch b, from the warp that opened the batch before the last.
     auto base_of = [&](int b) -> int {
@@ -503,6 +506,13 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             }
         }
         return static_cast<int>(static_cast<uint32_t>(v));
+    };
+    // Whether the block's next ticket is known by now (another warp may be faster).
+    auto known = [&]() -> bool {
+        const int l = misc[2];
+        int i;
+        const int b = l < A.batch0 ? 0 : 1 + div_by(l - A.batch0, A.batch, inv_batch, i);
+        return static_cast<int>(base_s[b % kMxBatches] >> 32) == b;
     };
     // The next ticket, or one past the last.
     auto claim = [&]() -> int {
@@ -527,7 +537,9 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     auto issue_one = [&]() {
         // claim tickets until one has slices (or none is left)
         while (ileft == 0) {
-            if (!more || tail - head >= 32u) return;
+            // (a warp takes one task at a time and leaves further tickets to others; with work at hand it waits for none)
+            if (!more || task || tail - head >= 32u) return;
+            if (head != tail && !__shfl_sync(0xffffffffu, static_cast<int>(lane != 0 || known()), 0)) return;
             const int next = claim();
             if (next >= total) {
                 more = false;
@@ -541,7 +553,9 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             if (lane == static_cast<int>(tail & 31u))
                 fifo = (static_cast<uint32_t>(kind) << 30) | (static_cast<uint32_t>(en) << 16) | static_cast<uint32_t>(sub);
             ++tail;
-            if (!(kind & 1)) {
+            if (kind & 1) {
+                task = true;
+            } else {
                 const int C = kind == 0 ? C1 : C2, T = kind == 0 ? T1 : T2;
                 isrc = (kind == 0 ? A.w_gu : A.w_dn) +
                        static_cast<size_t>(static_cast<uint32_t>(ent_e[en]) * static_cast<uint32_t>(T) + static_cast<uint32_t>(kTiles * sub)) *
@@ -565,7 +579,16 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
         ++issued;
         if (++islot == S) islot = 0;
     };
-    for (int s = 0; s < S; ++s) issue_one();
+    // As many slices in flight as the ring holds, or as there is work known for.
+    auto issue = [&]() {
+#pragma unroll 1
+        while (issued - consumed < S) {
+            const int before = issued;
+            issue_one();
+            if (issued == before) break;
+        }
+    };
+    issue();
 
     // Looks at words until `there` holds for the whole warp, for a bounded time.
     auto wait_words = [&](auto&& there) {
@@ -589,7 +612,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
     for (int j = 0; j < 4; ++j) perm[j] = (j ^ pp) * kUnit + (FMT == FMT_W4 ? 0 : hb << 4);
 
     while (!dead) {
-        if (head == tail) issue_one();
+        if (head == tail) issue();
         if (head == tail) break;
         const uint32_t t = __shfl_sync(0xffffffffu, fifo, static_cast<int>(head & 31u));
         ++head;
@@ -599,24 +622,27 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             const int p = list[(t >> 16) & 0x3fffu];
             const float* hp = A.h + static_cast<size_t>(p) * A.I;
             const int n4 = A.I >> 2;
+            constexpr int kPiece = kMxSeg / 4, kEach = kPiece / 32;      // float4 of a piece, and of a lane
             float mx = 0.0f;
             bool ok = true;
-            for (int i0 = 0; i0 < n4 && ok; i0 += 8 * 32) {
-                uint4 v[8];
+            // the largest value of all pieces, the own one last: it stays in registers
+            uint4 v[kEach];
+            for (int g = 0; g < nseg && ok; ++g) {
+                const int i0 = (g + 1 == nseg ? tile : g < tile ? g : g + 1) * kPiece;
                 ok = wait_words([&]() {
                     bool all = true;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < kEach; ++k) {
                         const int i = i0 + 32 * k + lane;
                         v[k] = i < n4 ? ld_relaxed_v4(hp + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
+                    for (int k = 0; k < kEach; ++k)
                         all = all && v[k].x != kMxNoValue && v[k].y != kMxNoValue && v[k].z != kMxNoValue && v[k].w != kMxNoValue;
                     return all;
                 });
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < kEach; ++k)
                     mx = fmaxf(fmaxf(mx, fmaxf(fabsf(__uint_as_float(v[k].x)), fabsf(__uint_as_float(v[k].y)))),
                                fmaxf(fabsf(__uint_as_float(v[k].z)), fabsf(__uint_as_float(v[k].w))));
             }
@@ -633,15 +659,12 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 qp = reinterpret_cast<uint32_t*>(A.qh + static_cast<size_t>(ent_off[en]) * A.I * mx_code(FMT, TK)) +
                      8 * mx_code(FMT, TK) * (at - ent_off[en]);
             }
-            const int i1 = min(n4, (tile + 1) * (kMxSeg / 4));
             int sum = 0;
-#pragma unroll 4
-            for (int i = tile * (kMxSeg / 4) + lane; i < i1; i += 32) {
-                const uint4 u = ld_relaxed_v4(hp + 4 * i);
-                const float4 v = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+            auto quantize = [&](const uint4& u, int i) {
+                const float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
                 uint32_t good = 0xffffffffu;
-                uint32_t q = a8_pack4_fast2(v, rr, good);
-                if (a8_needs_exact(ks) || (good >> 31) == 0u) q = a8_pack4_exact(v, ks);
+                uint32_t q = a8_pack4_fast2(f, rr, good);
+                if (a8_needs_exact(ks) || (good >> 31) == 0u) q = a8_pack4_exact(f, ks);
                 if constexpr (kSplit) {
                     // (words of K 0 .. 3 and 4 .. 7 in turn)
                     const uint4 h2 = codes_half(q, q);
@@ -652,6 +675,18 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                     qp[i] = q;
                 }
                 sum = __dp4a(static_cast<int>(q), 0x01010101, sum);
+            };
+            if constexpr (kMma) {
+                // (read again: the code for eight at once is long, and other warps run other code meanwhile)
+                const int i1 = min(n4, (tile + 1) * kPiece);
+#pragma unroll 4
+                for (int i = tile * kPiece + lane; i < i1; i += 32) quantize(ld_relaxed_v4(hp + 4 * i), i);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const int i = tile * kPiece + 32 * k + lane;
+                    if (i < n4) quantize(v[k], i);
+                }
             }
             sum = __reduce_add_sync(0xffffffffu, sum);
             __syncwarp();
@@ -659,39 +694,51 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             if (lane == 0)
                 st_release_u64(A.qdone + static_cast<size_t>(p) * nseg + tile,
                                (static_cast<unsigned long long>(__float_as_uint(__int2float_rn(sum))) << 32) | __float_as_uint(ks.s));
+            task = false;
             continue;
         }
         if (kind == 3) {
-            // ------------------------------ add the slots of 256 outputs
+            // ------------------------------ add the slots of kAdd outputs
+            constexpr int kAddSlots = TK <= 2 ? 8 : 1;       // looked at together (as registers allow)
             const int m = static_cast<int>((t >> 16) & 0x3fffu);
-            float acc[kMxAdd / 32];
+            float acc[kAdd / 32];
 #pragma unroll
-            for (int k = 0; k < kMxAdd / 32; ++k) acc[k] = 0.0f;
+            for (int k = 0; k < kAdd / 32; ++k) acc[k] = 0.0f;
             bool ok = true;
-            for (int s = 0; s < slots && ok; ++s) {
-                const int p = m * slots + s;
-                if (pair_e[p] == 0xffff) continue;
-                const float w = s < A.top_k ? __ldg(A.weights + m * A.top_k + s) : 1.0f;
-                const float* pp_ = A.part + static_cast<size_t>(p) * A.H;
-                uint32_t v[kMxAdd / 32];
+            for (int s0 = 0; s0 < slots && ok; s0 += kAddSlots) {
+                // (a slot's values take a trip to L2: several slots at once)
+                uint32_t v[kAddSlots][kAdd / 32];
                 ok = wait_words([&]() {
                     bool all = true;
 #pragma unroll
-                    for (int k = 0; k < kMxAdd / 32; ++k) {
-                        const int row = kMxAdd * tile + 32 * k + lane;
-                        v[k] = row < A.H ? ld_relaxed_u32(pp_ + row) : 0u;
+                    for (int j = 0; j < kAddSlots; ++j) {
+                        const int p = m * slots + min(s0 + j, slots - 1);
+                        const bool have = s0 + j < slots && pair_e[p] != 0xffff;
+#pragma unroll
+                        for (int k = 0; k < kAdd / 32; ++k) {
+                            const int row = kAdd * tile + 32 * k + lane;
+                            v[j][k] = have && row < A.H ? ld_relaxed_u32(A.part + static_cast<size_t>(p) * A.H + row) : 0u;
+                        }
                     }
 #pragma unroll
-                    for (int k = 0; k < kMxAdd / 32; ++k) all = all && v[k] != kMxNoValue;
+                    for (int j = 0; j < kAddSlots; ++j)
+#pragma unroll
+                        for (int k = 0; k < kAdd / 32; ++k) all = all && v[j][k] != kMxNoValue;
                     return all;
                 });
 #pragma unroll
-                for (int k = 0; k < kMxAdd / 32; ++k) acc[k] = __fmaf_rn(w, __uint_as_float(v[k]), acc[k]);
+                for (int j = 0; j < kAddSlots; ++j) {
+                    const int s = s0 + j;
+                    if (s >= slots || pair_e[m * slots + s] == 0xffff) continue;
+                    const float w = s < A.top_k ? __ldg(A.weights + m * A.top_k + s) : 1.0f;
+#pragma unroll
+                    for (int k = 0; k < kAdd / 32; ++k) acc[k] = __fmaf_rn(w, __uint_as_float(v[j][k]), acc[k]);
+                }
             }
             if (!ok) break;
 #pragma unroll
-            for (int k = 0; k < kMxAdd / 32; ++k) {
-                const int row = kMxAdd * tile + 32 * k + lane;
+            for (int k = 0; k < kAdd / 32; ++k) {
+                const int row = kAdd * tile + 32 * k + lane;
                 if (row < A.H) {
                     const size_t o = static_cast<size_t>(m) * A.H + row;
                     float v = acc[k];
@@ -699,6 +746,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                     store_typed(A.y, A.ytype, o, v);
                 }
             }
+            task = false;
             continue;
         }
         // ------------------------------------------------ a tile of weights
@@ -771,7 +819,7 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
             }
             ++consumed;
             __syncwarp();
-            issue_one();
+            issue();
         };
         if constexpr (kMma) {
             constexpr int kCode = mx_code(FMT, TK);
@@ -788,63 +836,33 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
                 if constexpr (FMT == FMT_W4) {
                     // nibble w + 8 at bit 0 or 16 of a pair's half is, as it stands, the fp16 number (w + 8) 2^-24, at
                     // bit 4 16 times that: the sums are multiples of 2^-24 below 1, exact in fp32
-                    // (four chains: a product's result takes some 35 cycles)
-                    float d[4][4];
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    auto lines = [&](auto count) {
+                        constexpr int kN = decltype(count)::value;
+                        uint32_t w0[kN], w1[kN];
+                        uint4 x[kN];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) d[k][i] = 0.0f;
-                    struct Lines {
-                        uint32_t w0[4], w1[4];
-                        uint4 x[4];
-                    };
-                    auto load = [&](Lines& v, int l0, int count) {
-#pragma unroll
-                        for (int l = 0; l < 4; ++l) {
-                            if (l < count) {
-                                v.w0[l] = *reinterpret_cast<const uint32_t*>(ub + (l0 + l) * (kRows * kUnit));
-                                v.w1[l] = *reinterpret_cast<const uint32_t*>(ub + (l0 + l) * (kRows * kUnit) + kSlot / 2);
-                                v.x[l] = *reinterpret_cast<const uint4*>(xp + (l0 + l) * xstep);
-                            }
+                        for (int l = 0; l < kN; ++l) {
+                            w0[l] = *reinterpret_cast<const uint32_t*>(ub + l * (kRows * kUnit));
+                            w1[l] = *reinterpret_cast<const uint32_t*>(ub + l * (kRows * kUnit) + kSlot / 2);
+                            x[l] = *reinterpret_cast<const uint4*>(xp + l * xstep);
                         }
-                    };
-                    auto multiply = [&](const Lines& v, int count) {
 #pragma unroll
-                        for (int l = 0; l < 4; ++l) {
-                            if (l < count) {
-                                const uint32_t u0 = v.w0[l] >> 8, u1 = v.w1[l] >> 8;
-                                mma_f16(d[2 * (l & 1)], v.w0[l] & 0x000f000fu, v.w1[l] & 0x000f000fu, v.w0[l] & 0x00f000f0u,
-                                        v.w1[l] & 0x00f000f0u, v.x[l].x, v.x[l].z);
-                                mma_f16(d[2 * (l & 1) + 1], u0 & 0x000f000fu, u1 & 0x000f000fu, u0 & 0x00f000f0u, u1 & 0x00f000f0u,
-                                        v.x[l].y, v.x[l].w);
-                            }
+                        for (int l = 0; l < kN; ++l) {
+                            mma_f16(d, w0[l] & 0x000f000fu, w1[l] & 0x000f000fu, w0[l] & 0x00f000f0u, w1[l] & 0x00f000f0u, x[l].x, x[l].z);
+                            const uint32_t v0 = w0[l] >> 8, v1 = w1[l] >> 8;
+                            mma_f16(d2, v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x00f000f0u, x[l].y, x[l].w);
                         }
+                        ub += kN * (kRows * kUnit);
+                        xp += kN * xstep;
                     };
-                    Lines v[2];
-                    if (n == kLines) {
-                        load(v[0], 0, 4);
-#pragma unroll
-                        for (int l = 0; l < kLines; l += 4) {
-                            if (l + 4 < kLines) load(v[(l / 4 + 1) & 1], l + 4, 4);
-                            multiply(v[(l / 4) & 1], 4);
-                        }
-                    } else {
-                        int l = 0;
+                    int l = 0;
 #pragma unroll 1
-                        for (; l + 4 <= n; l += 4) {
-                            load(v[0], l, 4);
-                            multiply(v[0], 4);
-                        }
+                    for (; l + 8 <= n; l += 8) lines(std::integral_constant<int, 8>());
 #pragma unroll 1
-                        for (; l < n; ++l) {
-                            load(v[0], l, 1);
-                            multiply(v[0], 1);
-                        }
-                    }
-                    xp += n * xstep;
+                    for (; l < n; ++l) lines(std::integral_constant<int, 1>());
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[i] += __float2int_rn(__fmul_rn(__fadd_rn(__fadd_rn(d[0][i], d[1][i]), __fadd_rn(d[2][i], d[3][i])), 16777216.0f));
+                    for (int i = 0; i < 4; ++i) acc[i] += __float2int_rn(__fmul_rn(__fadd_rn(d[i], d2[i]), 16777216.0f));
                 } else {
                     auto lines = [&](auto count) {
                         constexpr int kN = decltype(count)::value;
@@ -1038,8 +1056,6 @@ cudaError_t launch_experts_f(int tok, const MoeArgs& a, int grid, int warps, siz
 {
     if (tok <= 1) return launch_experts_t<FMT, 1>(a, grid, warps, smem, pdl, s);
     if (tok <= 2) return launch_experts_t<FMT, 2>(a, grid, warps, smem, pdl, s);
-    if constexpr (FMT != FMT_W4)
-        if (tok <= 4) return launch_experts_t<FMT, 4>(a, grid, warps, smem, pdl, s);
     return launch_experts_t<FMT, 8>(a, grid, warps, smem, pdl, s);
 }
 

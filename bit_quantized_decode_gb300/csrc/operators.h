@@ -200,7 +200,7 @@ constexpr int kMxMaxSlots = 20;                 // chosen and shared experts per
 constexpr int kMxMaxPairs = 16 * kMxMaxSlots;
 constexpr int kMxMaxExperts = 1024;             // routed and shared
 constexpr int kMxSeg = 1024;                    // hidden values per quantizing task
-constexpr int kMxAdd = 256;                     // outputs per adding task
+__host__ __device__ constexpr int mx_add(int tok) { return tok <= 2 ? 128 : 256; }   // outputs per adding task
 
 struct MoeArgs {
     const uint8_t* w_gu;      // per expert: gate and up rows paired per tile (w4_repack_glu / w8_repack_glu)
@@ -229,7 +229,7 @@ struct MoeArgs {
     int8_t* qh;               // [pairs][I] codes
     unsigned* err;
 };
-// Launch shape for `tok` pairs per entry (1, 2, 4 or 8) on `most` bytes of shared memory.
+// Launch shape for `tok` pairs per entry (1, 2 or 8) on `most` bytes of shared memory.
 struct MoePlan {
     int warps, tiles;         // per block; weight tiles to a ticket
     bool staged;              // the tokens' codes go into shared memory

@@ -257,11 +257,11 @@ MoeFill moe_fill_of(const MoeSpace& w, void* ws)
 
 // Pairs per entry (an expert and some of its tokens, whose weights are read
 // once).  Where an expert that is reached at all has one token as a rule, the
-// DP4A entries of two tokens (INT4) or four (INT8) are ahead, elsewhere the
-// tensor cores' eight.  64 experts of 2368 x 3584 in INT4, top 8: 6 tokens (1.36
-// tokens per expert) 105 us by two, 108 by eight; 8 tokens (1.52) 129 and 123, 16
-// tokens 213 and 177.  128 experts of 768 x 1536 and a shared one in INT8, top 6:
-// 5 tokens 42.4 us by four, 47.5 by eight; 10 tokens (1.41) 58 and 55.
+// DP4A entries of two are ahead, elsewhere the tensor cores' eight.  64 experts
+// of 2368 x 3584 in INT4, top 8: 6 tokens (1.36 tokens per expert) 101 us by
+// two, 108 by eight; 8 tokens (1.52) 129 and 123, 16 tokens 213 and 178.  128
+// experts of 768 x 1536 and a shared one in INT8, top 6: 5 tokens (1.25) 38 us
+// by two, 47 by eight; 12 tokens (1.47) 63 and 55.
 int moe_entry_pairs(const DeviceFacts& d, const w4_experts* e, int M, int top_k, MoePlan& p)
 {
     const size_t most = static_cast<size_t>(d.smem_optin);
@@ -272,7 +272,7 @@ int moe_entry_pairs(const DeviceFacts& d, const w4_experts* e, int M, int top_k,
             if (p.fits) return kMxTok;
         }
     }
-    const int tok = M <= 1 ? 1 : M == 2 || e->fmt == W4_FMT_W4 ? 2 : 4;
+    const int tok = M <= 1 ? 1 : 2;
     p = moe_plan(e->fmt, tok, M, e->H, most);
     return tok;
 }
@@ -320,7 +320,7 @@ w4_status run_experts(const w4_experts* e, const int8_t* qx, const float* sx, co
     a.inv_t1 = 1.0f / static_cast<float>(u1);
     a.inv_t2 = 1.0f / static_cast<float>(u2);
     a.inv_seg = 1.0f / static_cast<float>((e->I + kMxSeg - 1) / kMxSeg);
-    a.inv_add = 1.0f / static_cast<float>((e->H + kMxAdd - 1) / kMxAdd);
+    a.inv_add = 1.0f / static_cast<float>((e->H + mx_add(tok) - 1) / mx_add(tok));
     a.stage_x = plan.staged;
     // every SM a share of the gate/up tiles: a ticket for each warp at the start
     // (or fewer), then a few at a time, two batches ahead (a batch takes a
