@@ -18,7 +18,7 @@
 //     run, copied by a 1-D bulk copy into the core-matrix layout without
 //     swizzle.
 //   * Persistent blocks, one per SM: a copy warp, an MMA warp, eight
-//     converting warps (two groups on alternate 128-K stages) and eight
+//     converting warps (two groups on alternate slots of 128 K) and eight
 //     epilogue warps, joined by mbarriers only.
 //   * Few tiles: K is split over a thread-block cluster; the splits exchange
 //     their integer sums through distributed shared memory (split r owns the
@@ -234,7 +234,9 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                 const bool last = st + 1 == st1 || run == kG8AccStages - 1;
                 const uint32_t dcol = tbase + static_cast<uint32_t>((ac & 1) * nt);
                 if (run == 0 && ac >= 2) ok = warp_wait(acce_b + 8 * (ac & 1), static_cast<uint32_t>((ac >> 1) - 1) & 1u);
-                ok = ok && warp_wait(ready_b + 8 * slot, sph) && warp_wait(full_b + 8 * slot, sph);
+                // converted, so landed: the converting warps saw the codes land with the weights (a wait of this warp for
+                // them as well took 8% of the 16-token lm_head)
+                ok = ok && warp_wait(ready_b + 8 * slot, sph);
                 if (!ok) {
                     if (lane == 0) fail();
                     break;
@@ -281,7 +283,10 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         bool ok = true;
         for (int tile = tile_first; tile < ntiles && ok; tile += tile_step) {
             for (int st = st0; st < st1; ++st, ++it) {
-                if ((it & 1) == grp) {
+                // A group has its slots to itself (not every other stage: with an odd number of slots the groups would
+                // take turns on a slot, and the one that is ahead could take a landing of the turn before last, whose
+                // parity is the same, for its own)
+                if ((slot & 1) == grp) {
                     // the slot's refill follows the MMAs that read its last converted
                     // stage, so a landed stage also has its tensor-memory columns free
                     const int nch = min(kG8StageChunks, A.C - st * kG8StageChunks);

@@ -141,3 +141,35 @@ def test_batches_equal_single_tokens(bq, fmt, M, H, I, E, k):
     y = layer(x).clone()
     for m in range(M):
         assert torch.equal(layer(x[m:m + 1].contiguous()), y[m:m + 1])
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 20000, 3584), (12, 19999, 1056), (40, 20500, 544), (9, 41000, 32), (100, 19600, 1120)])
+def test_many_rows_equal_few_token_calls(bq, M, N, K):
+    """Several tiles to a block: the codes that stay in shared memory serve all of them."""
+    import torch
+    g = wl.rng(M + K)
+    lin = bq.QuantLinear.from_float("w8", [dev(wl.weights(g, N, K))])
+    x = dev(wl.activations(g, M, K))
+    for _ in range(2):
+        y = lin(x)
+        for m in range(0, M, 4):
+            assert torch.equal(lin(x[m:m + 4].contiguous()), y[m:m + 4])
+
+
+@pytest.mark.parametrize("M,N,K,calls", [(128, 3584, 18944, 6000), (100, 640, 7168, 4000), (16, 40000, 1024, 4000), (48, 5000, 3584, 4000)])
+def test_long_runs_of_the_linear_repeat_every_bit(bq, M, N, K, calls):
+    """Thousands of calls, whatever the order in which copies land: odd and even numbers of stages, split K or not."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    lin = bq.QuantLinear.from_float("w8", [torch.randn(N, K, device="cuda", generator=g)])
+    x = torch.randn(M, K, device="cuda", generator=g)
+    want = torch.cat([lin(x[m:m + 4].contiguous()) for m in range(0, M, 4)])
+    ws, sx = lin.workspace(M), torch.empty(M, device="cuda")
+    ys = [torch.empty((M, N), device="cuda") for _ in range(8)]
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(calls // len(ys)):
+        for y in ys:
+            lin(x, y, None, sx, workspace=ws, flags=bq.W4_FLAG_PDL)
+        for y in ys:
+            wrong += (y != want).any()
+    assert int(wrong) == 0 and bq._lib.device_error() == 0
