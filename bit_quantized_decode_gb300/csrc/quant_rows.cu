@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsA
     const int K8 = static_cast<int>(static_cast<long long>(rank + 1) * K8_all / cs) - k0;    // this block's groups of eight
     constexpr int kN = NIT > 0 ? NIT : 1;
     pdl_launch_dependents();
+    if (cs > 1) cluster_arrive_release();                       // waited for before the first store to another block
     pdl_wait();
     const size_t row = static_cast<size_t>(m) * a.K + 8 * static_cast<size_t>(k0);
     float v[kN][8];
@@ -93,6 +94,7 @@ __global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsA
 #pragma unroll
         for (int w = 1; w < kQrWarps; ++w) pair_merge(hi, lo, red_s[2 * w], red_s[2 * w + 1]);
         if (cs > 1) {
+            cluster_wait_acquire();
             if (tid < cs) {
                 st_cluster_u32(mapa_shared(smem_u32(all_s + 2 * rank), static_cast<uint32_t>(tid)), __float_as_uint(hi));
                 st_cluster_u32(mapa_shared(smem_u32(all_s + 2 * rank + 1), static_cast<uint32_t>(tid)), __float_as_uint(lo));
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsA
     for (int w = 1; w < kQrWarps; ++w) amax = fmaxf(amax, red_s[w]);
     if (cs > 1) {
         float* max_s = all_s + 2 * kQrMaxCluster;
+        if (!kNorm) cluster_wait_acquire();
         if (tid < cs) st_cluster_u32(mapa_shared(smem_u32(max_s + rank), static_cast<uint32_t>(tid)), __float_as_uint(amax));
         cluster_sync();
         for (int b = 0; b < cs; ++b) amax = fmaxf(amax, max_s[b]);
