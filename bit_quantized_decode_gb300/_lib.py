@@ -655,21 +655,27 @@ def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(load().w8a8_workspace_bytes(M, N, K))
 
 
-def _w8_sizes(w, N, K):
-    need = w8_repacked_bytes(N, K)
-    if w.numel() < need:
-        raise ValueError(f"w: {w.numel()} bytes, {need} are needed")
+class W8Weights:
+    """Checked weights of the INT8 x INT8 linear (w8_repack), for callers that use them again and again."""
+    __slots__ = ("w", "s_w", "bias", "N", "K", "device", "addr")
+
+    def __init__(self, w, s_w, bias, N: int, K: int):
+        self.device = _check_tensors(("w", w, _U8, None), ("s_w", s_w, _F32, (N,)), ("bias", bias, _F32, (N,)))
+        need = w8_repacked_bytes(N, K)
+        if w.numel() < need:
+            raise ValueError(f"w: {w.numel()} bytes, {need} are needed")
+        self.w, self.s_w, self.bias, self.N, self.K = w, s_w, bias, N, K
+        self.addr = (_addr(w), _addr(s_w), _addr(bias))
 
 
 def w8a8_matmul(w, s_w, bias, qx, sx, y, workspace, stream=None):
     """y [M][N] (fp32, fp16 or bf16) from per-row INT8 weights (w8_repack) and int8 codes qx [M][K], sx [M]."""
     M, K = qx.shape
     N = y.shape[1]
-    dev = _check_tensors(("w", w, _U8, None), ("s_w", s_w, _F32, (N,)), ("bias", bias, _F32, (N,)),
-                         ("qx", qx, _I8, None), ("sx", sx, _F32, (M,)), ("y", y, _FLOATS, (M, N)),
+    weights = W8Weights(w, s_w, bias, N, K)
+    dev = _check_tensors(("qx", qx, _I8, None), ("sx", sx, _F32, (M,)), ("y", y, _FLOATS, (M, N)),
                          ("workspace", workspace, _U8, None))
-    _w8_sizes(w, N, K)
-    _check("w8a8_matmul", load().w8a8_matmul(_addr(w), _addr(s_w), _addr(bias), _addr(qx), _addr(sx), M, N, K, _addr(y),
+    _check("w8a8_matmul", load().w8a8_matmul(*weights.addr, _addr(qx), _addr(sx), M, N, K, _addr(y),
                                              ELEM_TYPES[y.dtype], _addr(workspace), workspace.numel(), _raw_stream(stream, dev)))
 
 
@@ -678,18 +684,25 @@ def w8a8_linear(w, s_w, bias, x, y, qx, sx, workspace, norm=None, eps: float = 0
     """Quantize x [M][K] (fp32, fp16 or bf16; RMSNorm first with norm) and form y [M][N] (any of the three types)
     from per-row INT8 weights, for any number of tokens; residual float32 [M][N] is added before the rounding.
     qx: int8 [M][K] to receive the codes, or None."""
+    w8a8_linear_on(W8Weights(w, s_w, bias, y.shape[1], x.shape[1]), x, y, qx, sx, workspace, norm, eps, residual, flags, stream)
+
+
+def w8a8_linear_on(weights: W8Weights, x, y, qx, sx, workspace, norm=None, eps: float = 0.0, residual=None, flags: int = 0,
+                   stream=None):
+    """w8a8_linear on weights that were checked before."""
     M, K = x.shape
-    N = y.shape[1]
-    dev = _check_tensors(("w", w, _U8, None), ("s_w", s_w, _F32, (N,)), ("bias", bias, _F32, (N,)),
-                         ("x", x, _FLOATS, None), ("y", y, _FLOATS, (M, N)), ("qx", qx, _I8, (M, K)),
-                         ("sx", sx, _F32, (M,)), ("workspace", workspace, _U8, None), ("norm", norm, _F32, (K,)),
-                         ("residual", residual, _F32, (M, N)))
-    _w8_sizes(w, N, K)
+    N = weights.N
+    if K != weights.K:
+        raise ValueError(f"x has {K} columns, the linear takes {weights.K}")
+    dev = _check_tensors(("x", x, _FLOATS, None), ("y", y, _FLOATS, (M, N)), ("qx", qx, _I8, (M, K)), ("sx", sx, _F32, (M,)),
+                         ("workspace", workspace, _U8, None), ("norm", norm, _F32, (K,)), ("residual", residual, _F32, (M, N)))
+    if weights.device != dev:
+        raise ValueError(f"the weights live on cuda:{weights.device}, the current device is cuda:{dev}")
     fz = None
     if norm is not None or residual is not None:
         fz = ctypes.byref(Fusion(None if norm is None else norm.data_ptr(), float(eps), W4_GLU_NONE,
                                  None if residual is None else residual.data_ptr()))
-    _check("w8a8_linear", load().w8a8_linear(_addr(w), _addr(s_w), _addr(bias), _addr(x), ELEM_TYPES[x.dtype], M, N, K,
+    _check("w8a8_linear", load().w8a8_linear(*weights.addr, _addr(x), ELEM_TYPES[x.dtype], M, N, K,
                                              _addr(y), ELEM_TYPES[y.dtype], _addr(qx), _addr(sx), fz, flags,
                                              _addr(workspace), workspace.numel(), _raw_stream(stream, dev)))
 

@@ -31,6 +31,7 @@ class QuantLinear:
         self.s_w = s_w              # float32 [N] (per-row formats)
         self.bias = bias            # float32 [N] or None
         self.canonical = canonical  # per-shard canonical tensors, if kept
+        self._w8 = None             # "w8": the checked weights of the last call
 
     # ------------------------------------------------------------- building
     @classmethod
@@ -148,14 +149,18 @@ class QuantLinear:
         M, K = x.shape
         if K != self.K:
             raise ValueError(f"x has {K} columns, the linear takes {self.K}")
-        with _lib.allocating_on(stream):
-            if y is None:
-                y = torch.empty((M, self.N), dtype=x.dtype if residual is None else torch.float32, device=x.device)
-            if sx is None:
-                sx = torch.empty(M, dtype=torch.float32, device=x.device)
-            if workspace is None:
-                workspace = self.workspace(M)
-        _lib.w8a8_linear(self.w, self.s_w, self.bias, x, y, qx, sx, workspace, norm, eps, residual, flags, stream)
+        weights = self._w8
+        if weights is None or weights.w is not self.w or weights.s_w is not self.s_w or weights.bias is not self.bias:
+            weights = self._w8 = _lib.W8Weights(self.w, self.s_w, self.bias, self.N, self.K)
+        if y is None or sx is None or workspace is None:
+            with _lib.allocating_on(stream):
+                if y is None:
+                    y = torch.empty((M, self.N), dtype=x.dtype if residual is None else torch.float32, device=x.device)
+                if sx is None:
+                    sx = torch.empty(M, dtype=torch.float32, device=x.device)
+                if workspace is None:
+                    workspace = self.workspace(M)
+        _lib.w8a8_linear_on(weights, x, y, qx, sx, workspace, norm, eps, residual, flags, stream)
         return y
 
     def __call__(self, x, y=None, qx=None, sx=None, flags: int = 0, stream=None, norm=None, eps: float = 1e-6,
