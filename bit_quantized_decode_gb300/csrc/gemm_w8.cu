@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         }
         if (ks > 1) {
             // token column c of the tile belongs to split c % ks: its sums go there
-            const int per = nt / ks;
+            const int lg = 31 - __clz(ks), per = nt >> lg;              // (a power of two)
             const uint32_t red_u = smem_u32(smem + L.red);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int c = 32 * b + 16 * half + i;
-                        const int o = (rank * per + c / ks) * kG8Rows + (warp & 3) * 32 + lane;
-                        st_cluster_u32(mapa_shared(red_u + 4u * static_cast<uint32_t>(o), static_cast<uint32_t>(c % ks)),
+                        const int o = (rank * per + (c >> lg)) * kG8Rows + (warp & 3) * 32 + lane;
+                        st_cluster_u32(mapa_shared(red_u + 4u * static_cast<uint32_t>(o), static_cast<uint32_t>(c & (ks - 1))),
                                        static_cast<uint32_t>(acc[b][i]));
                     }
                 }
@@ -394,19 +394,24 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
     if (ks > 1) {
         const int per = nt / ks;
         const int* red = reinterpret_cast<const int*>(smem + L.red);
-        cluster_sync();
+        // a row and every fourth of the columns to a thread
+        static_assert(kG8Rows == 128 && kG8Threads >= 512, "threads for the exchange");
+        const int r = tid & (kG8Rows - 1), c0 = tid >> 7;
+        const int row = (tile_first / A.n_tt) * kG8Rows + r;
+        const int m0 = (tile_first % A.n_tt) * nt + rank;
+        const bool mine = tid < 512 && row < A.N;
         pdl_wait();
-        const int m0 = (tile_first % A.n_tt) * nt;
+        const float sw = mine ? __ldg(A.s_w + row) : 0.0f;
+        const float bv = mine && A.bias != nullptr ? __ldg(A.bias + row) : 0.0f;
+        cluster_sync();
         const bool dead = *dead_s != 0u;
-        for (int idx = tid; idx < per * kG8Rows; idx += kG8Threads) {
-            const int r = idx % kG8Rows, c = idx / kG8Rows;
-            const int row = (tile_first / A.n_tt) * kG8Rows + r;
-            const int m = m0 + c * ks + rank;
-            if (row < A.N && m < A.M && !dead) {
+#pragma unroll 4
+        for (int c = c0; c < per; c += 4) {
+            const int m = m0 + c * ks;
+            if (mine && m < A.M && !dead) {
                 int s = 0;
                 for (int q = 0; q < ks; ++q) s += red[(q * per + c) * kG8Rows + r];
-                float v = __fmaf_rn(__fmul_rn(__ldg(A.s_w + row), __ldg(A.sx + m)), __int2float_rn(s),
-                                    A.bias != nullptr ? __ldg(A.bias + row) : 0.0f);
+                float v = __fmaf_rn(__fmul_rn(sw, __ldg(A.sx + m)), __int2float_rn(s), bv);
                 const size_t o = static_cast<size_t>(m) * A.N + row;
                 if (A.residual != nullptr) v = __fadd_rn(A.residual[o], v);
                 store_typed(A.y, A.ytype, o, v);

@@ -29,7 +29,7 @@ constexpr int kQrWarps = kQrThreads / 32;
 constexpr int kQrMaxCluster = 8;
 
 template <int XT, int NIT, bool kNorm>
-__global__ void __launch_bounds__(kQrThreads) quant_rows_kernel(const QuantRowsArgs a)
+__global__ void __launch_bounds__(kQrThreads, NIT == 1 ? 7 : NIT == 2 ? 5 : 1) quant_rows_kernel(const QuantRowsArgs a)
 {
     __shared__ float red_s[2 * kQrWarps];
     __shared__ float all_s[3 * kQrMaxCluster];                  // the cluster's blocks: sums (hi, lo), maxima
@@ -165,6 +165,7 @@ template <int XT, bool kNorm>
 cudaError_t launch_rows(const QuantRowsArgs& a, const cudaLaunchConfig_t& cfg)
 {
     const int nit = ((a.K / 8 + a.cluster - 1) / a.cluster + kQrThreads - 1) / kQrThreads;
+    if (nit <= 1) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 1, kNorm>, a);
     if (nit <= 2) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 2, kNorm>, a);
     if (nit <= 4) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 4, kNorm>, a);
     if (nit <= 10) return cudaLaunchKernelEx(&cfg, quant_rows_kernel<XT, 10, kNorm>, a);
