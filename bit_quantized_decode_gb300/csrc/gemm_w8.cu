@@ -23,6 +23,10 @@
 //   * Few tiles: K is split over a thread-block cluster; the splits exchange
 //     their integer sums through distributed shared memory (split r owns the
 //     tokens c with c % splits = r), so every block writes a share of y.
+// A stage of 128 K takes some 400 ns whatever the tokens of the tile: eight MMAs
+// whose A comes from tensor memory.  16 tokens, 152064 x 3584: 93 us (5.97 TB/s,
+// measured copy rate 6.79); 64 tokens, 3584 x 18944: 26.7 us with the quantizer;
+// 333 tokens, 3584 x 3584: 23.3 us with it.
 #include <cuda_fp16.h>
 
 #include <atomic>

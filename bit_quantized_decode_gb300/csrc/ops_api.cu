@@ -38,7 +38,7 @@ w4_status check_w8_shape(int M, int N, int K)
 // Tiles of an M x N x K product: 128 rows by up to 128 tokens to a block, with
 // K splits where tiles are few, or 256 rows by up to 192 tokens to a pair of
 // blocks.  A stage of either takes about the same time (4096 tokens, 37888 x
-// 3584: 870 us with blocks, 690 with pairs), so the one with fewer rounds of
+// 3584: 868 us with blocks, 730 with pairs), so the one with fewer rounds of
 // tiles over the SMs is taken.
 bool plan_gemm8(const DeviceFacts& d, Gemm8Args& a, bool& pairs, int& grid, size_t& smem)
 {

@@ -12,6 +12,8 @@
 // product copies tiles of (f16_word): a stage of a token tile is one
 // contiguous run in the MMA's core-matrix order.  It moves the activations once and the codes once (2 bytes each); its
 // time is HBM traffic for long prompts and one launch's latency for few tokens.
+// Short rows on as many blocks per SM as registers allow: 1000 tokens of 1536 in
+// one wave of blocks instead of two (22.5 -> 22.0 us with their product).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
