@@ -23,10 +23,12 @@
 //   * Few tiles: K is split over a thread-block cluster; the splits exchange
 //     their integer sums through distributed shared memory (split r owns the
 //     tokens c with c % splits = r), so every block writes a share of y.
-// A stage of 128 K takes some 400 ns whatever the tokens of the tile: eight MMAs
-// whose A comes from tensor memory.  16 tokens, 152064 x 3584: 93 us (5.97 TB/s,
-// measured copy rate 6.79); 64 tokens, 3584 x 18944: 26.7 us with the quantizer;
-// 333 tokens, 3584 x 3584: 23.3 us with it.
+// A stage of 128 K takes some 400 ns whatever the tokens of the tile: a group's
+// way from the landing over the conversion to the arrival, twice as long, more
+// than the MMAs (with one MMA instead of eight 16 tokens would take 92 us, without the
+// conversion's arithmetic 85).  16 tokens, 152064 x 3584: 92 us (6.03 TB/s, measured
+// copy rate 6.79); 64 tokens, 3584 x 18944: 26.1 us with the quantizer; 333
+// tokens, 3584 x 3584: 23.0 us with it.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -280,7 +282,6 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
         // ------------------------------------------------ converting warps
         const int grp = (warp - kWarpConv) >> 2;
         const int row = (warp & 3) * 32 + lane;                    // tensor-memory lane and weight row of the tile
-        const int hsel = (row >> 2) & 1;                           // reading order of a unit's halves (bank spread)
         const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
         int it = 0, slot = 0;
         uint32_t sph = 0u;
@@ -304,14 +305,16 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
                     uint4 a[kG8StageChunks], b[kG8StageChunks];
 #pragma unroll
                     for (int e = 0; e < kG8StageChunks; ++e) {
-                        a[e] = *reinterpret_cast<const uint4*>(u + e * 256 + (hsel << 4));
-                        b[e] = *reinterpret_cast<const uint4*>(u + e * 256 + ((hsel ^ 1) << 4));
+                        // (two lanes to a bank; reading every other row's halves the other way round would spread them, but the
+                        // selects that put the halves back took more: 16-token lm_head 93.6 against 91.5 us)
+                        a[e] = *reinterpret_cast<const uint4*>(u + e * 256);
+                        b[e] = *reinterpret_cast<const uint4*>(u + e * 256 + 16);
                     }
 #pragma unroll
                     for (int e = 0; e < kG8StageChunks; ++e) {
                         if (e < nch) {
                             uint32_t h[16];
-                            unit_f16(a[e], b[e], hsel, h);
+                            unit_f16(a[e], b[e], h);
                             tmem_st16(tbase + tlane + col_a + static_cast<uint32_t>(kG8ACols * slot + 16 * e), h);
                         }
                     }

@@ -52,11 +52,9 @@ __device__ __forceinline__ uint64_t l2_policy_evict_last()
     return p;
 }
 
-// 32 int8 weights of a row (halves in the order that `swapped` says) as 16
-// words of fp16 pairs.
-__device__ __forceinline__ void unit_f16(const uint4& first, const uint4& second, int swapped, uint32_t (&h)[16])
+// 32 int8 weights of a row as 16 words of fp16 pairs.
+__device__ __forceinline__ void unit_f16(const uint4& lo, const uint4& hi, uint32_t (&h)[16])
 {
-    const uint4 lo = swapped ? second : first, hi = swapped ? first : second;
     i8_to_f16(lo.x, h[0], h[1]);
     i8_to_f16(lo.y, h[2], h[3]);
     i8_to_f16(lo.z, h[4], h[5]);

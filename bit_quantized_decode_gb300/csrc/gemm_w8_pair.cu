@@ -17,7 +17,7 @@
 //   * The epilogue's two warpgroups hold 96 columns of int32 each; registers are
 //     moved to them from the others (setmaxnreg; 5 x 128 threads start with 96,
 //     then 40 + 72 + 72 + 144 + 144 of 480).
-// 4096 tokens, 37888 x 3584 in bf16: 730 us with the quantizer, 1.52 PFLOP/s (the
+// 4096 tokens, 37888 x 3584 in bf16: 725 us with the quantizer, 1.53 PFLOP/s (the
 // library's bf16 product sustains 1.73 on this chip); the tensor pipe is active
 // for two thirds of the time.
 #include "gemm_w8.cuh"
@@ -312,7 +312,6 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int grp = (warp - kP8Conv) >> 2;
         const int row = (warp & 3) * 32 + lane;                    // tensor-memory lane and weight row of the block
-        const int hsel = (row >> 2) & 1;                           // reading order of a unit's halves (bank spread)
         const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint8_t* units = smem + L.ring + (row >> 3) * (256 * kG8StageChunks) + (row & 7) * 32 + grp * 512;
         const uint32_t ready0 = mapa_shared(ready_b, 0);
@@ -334,14 +333,14 @@ __global__ void __launch_bounds__(kP8Threads, 1) gemm_w8_pair_kernel(const __gri
                 uint4 a[2], b[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    a[e] = *reinterpret_cast<const uint4*>(u + e * 256 + (hsel << 4));
-                    b[e] = *reinterpret_cast<const uint4*>(u + e * 256 + ((hsel ^ 1) << 4));
+                    a[e] = *reinterpret_cast<const uint4*>(u + e * 256);          // (two lanes to a bank, as in gemm_w8.cu)
+                    b[e] = *reinterpret_cast<const uint4*>(u + e * 256 + 16);
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (e < nch) {
                         uint32_t h[16];
-                        unit_f16(a[e], b[e], hsel, h);
+                        unit_f16(a[e], b[e], h);
                         tmem_st16(tbase + tlane + col_a + static_cast<uint32_t>(kP8ACols * j + 16 * e), h);
                     }
                 }
