@@ -71,8 +71,9 @@ __host__ __device__ constexpr int mx_warps(int tok) { return tok <= 2 ? 12 : 16;
 constexpr int kMxFewestWarps = 10;                 // a thread for each pair
 // Entries of more than two tokens multiply on the tensor cores, two tiles at a time.
 __host__ __device__ constexpr bool mx_mma(int tok) { return tok > 2; }
-// Bytes of a code as a kernel reads it (INT4 on the tensor cores: fp16), and the stride of the tokens' staged codes: what a read takes of
-// several tokens lies in banks of their own.
+// Bytes of a code as a kernel reads it (INT4 on the tensor cores: fp16), and the
+// stride of the tokens' staged codes: what a read takes of several tokens lies in
+// banks of their own.
 __host__ __device__ constexpr int mx_code(int fmt, int tok) { return mx_mma(tok) && fmt == FMT_W4 ? 2 : 1; }
 __host__ __device__ constexpr int mx_stride(int fmt, int tok, int H)
 {
