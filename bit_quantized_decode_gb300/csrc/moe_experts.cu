@@ -771,7 +771,9 @@ __global__ void __launch_bounds__(32 * mx_warps(TK), 1) moe_experts_kernel(const
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) row_params(8 * (kTiles * tile + i) + (kMma ? lane >> 2 : my_row), sw[i], bv[i]);
         if (down) {
-            if (ready_s[en] == 0) {
+            // One answer for the warp: another warp may set the byte between two lanes' loads of it, and the code behind the
+            // branch votes with all of them.  (Looking twice at finished pieces changes nothing.)
+            if (!__all_sync(0xffffffffu, ready_s[en] != 0)) {
                 // the pieces of the entry's pairs: there, and their sums (four pieces of eight pairs at a time)
                 bool ok = true;
                 int sums = 0;
