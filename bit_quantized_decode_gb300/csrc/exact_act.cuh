@@ -82,8 +82,9 @@ __host__ __device__ inline F2 xa_exp_neg(F2 t)
     const float d = xa_fma(-N, 0x1.63p-6f, t.h);                     // exact
     const F2 p = xa_prod(N, -0x1.bd0106p-18f);
     const F2 s = xa_sum(d, -p.h);
-    const float qh = -s.h;                                           // -r
-    const float ql = -xa_fma(-N, 0x1.cf79acp-45f, xa_add(xa_add(s.l, -p.l), t.l));
+    const F2 r = xa_sum(s.h, xa_add(xa_add(s.l, -p.l), t.l));        // (t.l may pass s.h; the series wants a small low part)
+    const float qh = -r.h;
+    const float ql = -xa_fma(-N, 0x1.cf79acp-45f, r.l);
     const F2 q2 = xa_prod(qh, qh);
     const float q3 = xa_mul(xa_mul(q2.h, qh), xa_fma(qh, xa_fma(qh, 0x1.111112p-7f, 0x1.555556p-5f), 0x1.555556p-3f));
     const F2 a = xa_fast(qh, xa_mul(0.5f, q2.h));
