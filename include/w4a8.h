@@ -472,8 +472,9 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
  * calls (or x, without norm_weight):
  *   l_e = sum_i x'_i w[e][i], rounded once to fp32 from a compensated sum;
  *   W4_ROUTE_SOFTMAX: the top_k experts by l; p = softmax(l) over all E;
- *   W4_ROUTE_SIGMOID: p_e = 1 / (1 + exp(-l_e)) rounded once to fp32, the
- *     top_k experts by fp32(p_e + select_bias[e]);
+ *   W4_ROUTE_SIGMOID: p_e = 1 / (1 + exp(-l_e)) rounded once to fp32 (subnormal
+ *     values to half a step and 2^-24 of the value), the top_k experts by
+ *     fp32(p_e + select_bias[e]);
  *   equal keys: the lowest index first.  weights = p of the chosen (divided by
  *   their sum with renormalize; 0 where that sum is 0) * scale.
  * ids: int [M][top_k], best first; weights: float [M][top_k]; qx, sx: the
@@ -485,7 +486,8 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
  *
  * w4_moe_experts.  For every token m and slot s with expert e = ids[m][s]:
  *   g, u = linear(qx, sx) by e's gate and up rows, as the W4 / W8A8 linears,
- *   h    = act(g) u, evaluated to one fp32 rounding,
+ *   h    = act(g) u, evaluated to one fp32 rounding over the whole range of g
+ *          and u (subnormal values to half a step and 2^-24 of the value),
  *   d    = linear of h's codes (quantized as a8_quantize does) by e's down rows,
  *   y[m] = sum over the slots in order of weights[m][s] * d (fp32), then the
  *          n_shared shared experts with weight 1, then + residual[m], rounded

@@ -92,9 +92,46 @@ def _values(n, seed, low, high):
 
 
 @pytest.mark.parametrize("kind", [SILU, GELU])
-@pytest.mark.parametrize("g_range,u_range", [((1, 2.2), (-10, 10))])
+@pytest.mark.parametrize("g_range,u_range", [((1, 2.2), (-10, 10)), ((-20, 3), (-10, 10)), ((3, 7.5), (-10, 10)), ((4, 8), (90, 127)), ((-149, -20), (-149, 127)),
+                                             ((40, 127), (-149, 127)), ((-149, 127), (-149, 127))])
 def test_gated_activations_round_once(lib, kind, g_range, u_range):
     n = 200000
     g, u = _values(n, 11, *g_range), _values(n, 12, *u_range)
     t = np.minimum(np.abs(_argument(kind, g)), 400.0)
     _check(_glu(lib, kind, g, u), _want(kind, g, u), 2.0 ** -17 + (t * 2.0 ** -19.5 if kind == GELU else 0.0))
+
+
+@pytest.mark.parametrize("kind,g,u", [(SILU, -88, 1), (SILU, -88, 1000), (SILU, -50, 1e37), (SILU, 1e20, 1e20), (SILU, -110, 1e38),
+                                      (SILU, -180, 3e38), (SILU, 1e30, -1e30), (SILU, 2.0, 2.5e38), (SILU, 1e-30, 1e-10),
+                                      (SILU, 1e-40, 1e20), (GELU, -10.2, 1000), (GELU, -10.2, 1), (GELU, 1e20, 1), (GELU, 1e20, 1e20),
+                                      (GELU, -13, 3e38), (GELU, -1e20, 1e38), (GELU, 3e-39, 1e30), (GELU, 5.0, 3.4e38)])
+def test_the_ends_of_the_range(lib, kind, g, u):
+    g, u = np.array([g], F32), np.array([u], F32)
+    t = np.minimum(np.abs(_argument(kind, g)), 400.0)
+    _check(_glu(lib, kind, g, u), _want(kind, g, u), 2.0 ** -17 + t * 2.0 ** -19.5)
+
+
+@pytest.mark.parametrize("kind", [SILU, GELU])
+def test_zeros_infinities_and_nan(lib, kind):
+    inf, nan = np.inf, np.nan
+    rows = [(0.0, 5.0, 0.0), (-0.0, 5.0, -0.0), (3.0, 0.0, 0.0), (-3.0, 0.0, -0.0), (200.0, 1.0, 200.0), (-1000.0, 1.0, 0.0),
+            (inf, 2.0, inf), (inf, -2.0, -inf), (1.0, inf, inf), (-1.0, inf, -inf), (1.0, -inf, -inf),
+            (nan, 1.0, nan), (1.0, nan, nan), (inf, 0.0, nan), (0.0, inf, nan), (nan, 0.0, nan), (-inf, 1.0, nan)]
+    y = _glu(lib, kind, [r[0] for r in rows], [r[1] for r in rows])
+    assert np.array_equal(y, np.array([r[2] for r in rows], F32), equal_nan=True), y
+
+
+def test_logistic_rounds_once_to_the_smallest_values(lib):
+    v = np.concatenate([_values(400000, 3, -30, 7.5), np.linspace(-104, -86, 40001, dtype=F32), np.linspace(-88, 88, 200001, dtype=F32)])
+    want = 1.0 / (1.0 + np.exp(-v.astype(F64)))
+    _check(_logistic(lib, v), want, 2.0 ** -17)
+    y = _logistic(lib, [np.inf, -np.inf, 0.0, np.nan, 1000.0, -1000.0])
+    assert np.array_equal(y, np.array([1.0, 0.0, 0.5, np.nan, 1.0, 0.0], F32), equal_nan=True)
+
+
+def test_far_logits_keep_their_order(lib):
+    """Scores below 2^-126 are numbers like others: a larger logit has no smaller score, and those apart differ."""
+    v = np.linspace(-103, -86, 2000, dtype=F32)
+    y = _logistic(lib, v)
+    assert (np.diff(y.astype(F64)) >= 0).all() and y[0] > 0
+    assert _logistic(lib, [-88.0])[0] > _logistic(lib, [-90.0])[0] > _logistic(lib, [-100.0])[0] > 0

@@ -1,0 +1,73 @@
+"""Ends of the ranges of the expert router and the expert layer: scores and gates far out, infinities, the largest codes."""
+import numpy as np
+import pytest
+
+import ops_reference as ref
+from bit_quantized_decode_gb300 import workloads as wl
+from helpers import cuda_ok, dev, host
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def bq():
+    import bit_quantized_decode_gb300 as pkg
+    pkg._lib.load()
+    pkg._lib.clear_device_error()
+    yield pkg
+    assert pkg._lib.device_error() == 0
+
+
+def _stored(fmt, q):
+    import oracle
+    return dev(oracle.pack_int4(q).view(np.int32)) if fmt == "w4" else dev(q)
+
+
+@pytest.mark.parametrize("E", [6, 70])
+def test_sigmoid_scores_far_below_one_keep_their_order(bq, E):
+    """Logits below -87, whose scores are subnormal: a larger one comes first, and its weight is the larger."""
+    K, k = 64, 4
+    l = -100.0 + 12.5 * np.linspace(0.0, 1.0, E)                   # the last expert leads
+    x = np.zeros((2, K), np.float32)
+    x[:, 3] = 1.0
+    w = np.zeros((E, K), np.float32)
+    w[:, 3] = l
+    ids, weights = bq.MoeRouter(dev(w), k, score="sigmoid", renormalize=False)(dev(x))
+    want, ww = ref.route(ref.logits(x, w), k, "sigmoid", None, False, 1.0)
+    assert np.array_equal(host(ids), want) and host(ids)[0].tolist() == list(range(E - 1, E - 1 - k, -1))
+    # one rounding of the value, to a subnormal's step and 24 bits; the product with 1 adds none
+    assert (np.abs(host(weights).astype(np.float64) - ww) <= 2.0 ** -150 + U * ww).all()
+
+
+@pytest.mark.parametrize("fmt", ["w4", "w8"])
+@pytest.mark.parametrize("act,gate,up", [("silu", (-60.0, -50.0), 1e37), ("silu", (-92.0, -88.0), 1e3), ("silu", (1e18, 4e18), 5e18),
+                                         ("gelu_tanh", (-10.6, -10.2), 1e4), ("gelu_tanh", (-12.2, -11.8), 1e37), ("silu", (1e-30, 4e-30), 1e-5)])
+@pytest.mark.parametrize("M", [1, 2, 9])
+def test_far_gates(bq, fmt, act, gate, up, M):
+    """Gates whose activation is tiny beside a large up value, or whose product passes fp32 before the sigmoid: the layer's y
+    is the definition's."""
+    import torch
+    H = I = 64
+    top = 7 if fmt == "w4" else 127
+    g = wl.rng(M)
+    gu = np.zeros((2 * I, H), np.int8)
+    gu[:I, 0] = top if gate[0] > 0 else -top
+    gu[I:, 0] = g.choice([-top, top], I)
+    size = np.concatenate([g.uniform(abs(gate[0]), abs(gate[1]), I) if gate[0] > 0 else g.uniform(abs(gate[1]), abs(gate[0]), I),
+                           up * g.uniform(1.0, 2.0, I)])
+    s_gu = (size / top).astype(np.float32)
+    dn = wl.int_codes(g, (H, I), -top, top)
+    s_dn = wl.positive_scales(g, H, 1e-3, 1e-2)
+    x = np.zeros((M, H), np.float32)
+    x[:, 0] = 1.0                                                   # code 127, scale 1 / 127
+    q, s = ref.codes(x)
+    ids, w = np.zeros((M, 1), np.int32), np.ones((M, 1), np.float32)
+    layer = bq.MoeLayer.from_canonical(fmt, bq.MoeRouter(torch.zeros(1, H, device="cuda"), 1), [_stored(fmt, gu)], dev(s_gu[None]),
+                                       [_stored(fmt, dn)], dev(s_dn[None]), act)
+    y = torch.empty((M, H), device="cuda")
+    layer.experts(dev(q.astype(np.int8)), dev(s.astype(np.float32)), dev(ids), dev(w), y)
+    want, room = ref.experts(q, s, ids, w, [gu], s_gu[None], [dn], s_dn[None], act)
+    assert np.isfinite(want).all() and (np.abs(want).max(axis=1) > 0).all()
+    bound = 1.05 * (room + U * np.abs(want)) + 2.0 ** -148
+    assert (np.abs(host(y).astype(np.float64) - want) <= bound).all()
