@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kRtThreads, 2) moe_route_kernel(const RouteArg
                 const float* p = part_s + (g * a.parts * TG + t) * 2;
                 float h = p[0], l = p[1];
                 for (int s = 1; s < a.parts; ++s) pair_merge(h, l, p[s * TG * 2], p[s * TG * 2 + 1]);
-                const float logit = __fadd_rn(h, l);
+                // (past fp32 the errors of the sum are NaN)
+                const float logit = fabsf(h) <= 0x1.fffffep+127f ? __fadd_rn(h, l) : h;
                 if (cs > 1) st_cluster_u32(mapa_shared(smem_u32(key_s + t * Epad + ee), 0u), __float_as_uint(logit));
                 else key_s[t * Epad + ee] = logit;
             }

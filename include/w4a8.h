@@ -481,7 +481,8 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
  * codes and scales of x' (as rms_a8_quantize makes them), or both NULL.
  * x: [M][K] of x_type, 16-byte aligned; w: float [E][K], 16-byte aligned;
  * K % 32 == 0, 1 <= top_k <= min(E, 16), E <= 1024; K up to about 50000 (a
- * token is kept in shared memory as fp32).  A NaN logit is the last choice;
+ * token is kept in shared memory as fp32).  A logit past fp32 is an infinity
+ * of its sign (softmax then has NaN weights); a NaN logit is the last choice;
  * the ids are valid and distinct whatever x holds.
  *
  * w4_moe_experts.  For every token m and slot s with expert e = ids[m][s]:

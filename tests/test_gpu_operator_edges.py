@@ -71,3 +71,30 @@ def test_far_gates(bq, fmt, act, gate, up, M):
     assert np.isfinite(want).all() and (np.abs(want).max(axis=1) > 0).all()
     bound = 1.05 * (room + U * np.abs(want)) + 2.0 ** -148
     assert (np.abs(host(y).astype(np.float64) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("E,k", [(6, 3), (70, 9), (300, 16)])
+def test_infinite_logits_lead_or_trail(bq, E, k):
+    """A logit that passes fp32 is an infinity of its sign, not a NaN: it is the first choice, or (negative) comes after every
+    finite one, and its sigmoid score is 1 or 0."""
+    K = 96
+    g = wl.rng(E)
+    w = (g.standard_normal((E, K)) * 0.05).astype(np.float32)
+    w[:, 5] = np.where(np.arange(E) % 3 == 0, -3.0, 2.0)
+    w[E - 1, 5] = 5.0
+    x = wl.activations(g, 5, K)
+    x[0, 5], x[1, 5] = np.inf, -np.inf                      # infinite for every expert
+    x[2, 5] = 1e38                                          # past fp32 for the last expert only
+    x[3, 5] = -1.2e38                                       # past fp32 for the last (negative) and for every third
+    with np.errstate(over="ignore"):
+        l = ref.logits(x, w)
+    assert np.isinf(l[:2]).all() and np.isposinf(l[2, -1]) and np.isneginf(l[3, -1]) and np.isposinf(l[3, 0]) and np.isfinite(l[4]).all()
+    for score in ("softmax", "sigmoid"):
+        ids, weights = bq.MoeRouter(dev(w), k, score=score, renormalize=False)(dev(x))
+        with np.errstate(over="ignore", invalid="ignore"):
+            want, ww = ref.route(l, k, score, None, False, 1.0)
+        assert np.array_equal(host(ids), want), (host(ids), want)
+        if score == "sigmoid":
+            assert (np.abs(host(weights).astype(np.float64) - ww) <= U * ww + 2.0 ** -150).all()
+        else:                                               # an infinite logit has no softmax
+            assert np.isfinite(host(weights)[4]).all()
