@@ -660,12 +660,23 @@ class W8Weights:
     __slots__ = ("w", "s_w", "bias", "N", "K", "device", "addr")
 
     def __init__(self, w, s_w, bias, N: int, K: int):
-        self.device = _check_tensors(("w", w, _U8, None), ("s_w", s_w, _F32, (N,)), ("bias", bias, _F32, (N,)))
-        need = w8_repacked_bytes(N, K)
-        if w.numel() < need:
-            raise ValueError(f"w: {w.numel()} bytes, {need} are needed")
         self.w, self.s_w, self.bias, self.N, self.K = w, s_w, bias, N, K
-        self.addr = (_addr(w), _addr(s_w), _addr(bias))
+        self._settle()
+
+    def _settle(self):
+        N = self.N
+        self.device = _check_tensors(("w", self.w, _U8, None), ("s_w", self.s_w, _F32, (N,)), ("bias", self.bias, _F32, (N,)))
+        need = w8_repacked_bytes(N, self.K)
+        if self.w.numel() < need:
+            raise ValueError(f"w: {self.w.numel()} bytes, {need} are needed")
+        self.addr = (_addr(self.w), _addr(self.s_w), _addr(self.bias))
+
+    def addresses(self):
+        """Where the weights are now: a tensor may have got other memory since the last call, which is checked then."""
+        bias = self.bias
+        if (self.w.data_ptr(), self.s_w.data_ptr(), None if bias is None else bias.data_ptr()) != self.addr:
+            self._settle()
+        return self.addr
 
 
 def w8a8_matmul(w, s_w, bias, qx, sx, y, workspace, stream=None):
@@ -696,13 +707,14 @@ def w8a8_linear_on(weights: W8Weights, x, y, qx, sx, workspace, norm=None, eps: 
         raise ValueError(f"x has {K} columns, the linear takes {weights.K}")
     dev = _check_tensors(("x", x, _FLOATS, None), ("y", y, _FLOATS, (M, N)), ("qx", qx, _I8, (M, K)), ("sx", sx, _F32, (M,)),
                          ("workspace", workspace, _U8, None), ("norm", norm, _F32, (K,)), ("residual", residual, _F32, (M, N)))
+    addr = weights.addresses()
     if weights.device != dev:
         raise ValueError(f"the weights live on cuda:{weights.device}, the current device is cuda:{dev}")
     fz = None
     if norm is not None or residual is not None:
         fz = ctypes.byref(Fusion(None if norm is None else norm.data_ptr(), float(eps), W4_GLU_NONE,
                                  None if residual is None else residual.data_ptr()))
-    _check("w8a8_linear", load().w8a8_linear(*weights.addr, _addr(x), ELEM_TYPES[x.dtype], M, N, K,
+    _check("w8a8_linear", load().w8a8_linear(*addr, _addr(x), ELEM_TYPES[x.dtype], M, N, K,
                                              _addr(y), ELEM_TYPES[y.dtype], _addr(qx), _addr(sx), fz, flags,
                                              _addr(workspace), workspace.numel(), _raw_stream(stream, dev)))
 
@@ -722,18 +734,27 @@ def w8_repack_glu(gate, up, K, out, stream=None):
 _I32 = (torch.int32,)
 
 
+def _settle(desc):
+    """Checks a descriptor's tensors and takes their addresses."""
+    desc._device = _check_tensors(*((name, t, dtypes, shape) for (_, name, dtypes, shape), t in zip(desc._specs, desc._tensors)))
+    for (field, *_), t in zip(desc._specs, desc._tensors):
+        setattr(desc, field, _addr(t))
+    desc._held = tuple(t for t in desc._tensors if t is not None)
+    desc._addrs = [t.data_ptr() for t in desc._held]
+    return desc
+
+
 def moe_router(w, top_k: int, select_bias=None, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
                norm=None, eps: float = 1e-6):
     """A w4_router descriptor: w float32 [E][K].  It holds references to its tensors."""
     E, K = w.shape
     if score not in ROUTE_SCORES:
         raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
-    dev = _check_tensors(("w", w, _F32, None), ("select_bias", select_bias, _F32, (E,)), ("norm", norm, _F32, (K,)))
-    r = Router(None if norm is None else norm.data_ptr(), float(eps), w.data_ptr(),
-               None if select_bias is None else select_bias.data_ptr(), E, int(top_k), ROUTE_SCORES[score],
-               int(bool(renormalize)), float(scale))
-    r._tensors, r._K, r._device = (w, select_bias, norm), K, dev
-    return r
+    r = Router(norm_eps=float(eps), E=E, top_k=int(top_k), score=ROUTE_SCORES[score], renormalize=int(bool(renormalize)),
+               scale=float(scale))
+    r._tensors, r._K = (w, select_bias, norm), K
+    r._specs = (("w", "w", _F32, (E, K)), ("select_bias", "select_bias", _F32, (E,)), ("norm_weight", "norm", _F32, (K,)))
+    return _settle(r)
 
 
 def moe_experts(fmt: str, w_gu, s_gu, w_dn, s_dn, E: int, n_shared: int, H: int, I: int, glu: int, b_gu=None, b_dn=None):
@@ -743,18 +764,18 @@ def moe_experts(fmt: str, w_gu, s_gu, w_dn, s_dn, E: int, n_shared: int, H: int,
     n = E + n_shared
     gu_bytes, dn_bytes = ((w4_glu_repacked_bytes(I, H), w4_repacked_bytes(H, I)) if fmt == "w4"
                           else (w8_glu_repacked_bytes(I, H), w8_repacked_bytes(H, I)))
-    dev = _check_tensors(("w_gu", w_gu, _U8, (n * gu_bytes,)), ("s_gu", s_gu, _F32, (n, 2 * I)),
-                         ("b_gu", b_gu, _F32, (n, 2 * I)), ("w_dn", w_dn, _U8, (n * dn_bytes,)),
-                         ("s_dn", s_dn, _F32, (n, H)), ("b_dn", b_dn, _F32, (n, H)))
-    e = Experts(EXPERT_FORMATS[fmt], E, n_shared, H, I, glu, w_gu.data_ptr(), s_gu.data_ptr(),
-                None if b_gu is None else b_gu.data_ptr(), w_dn.data_ptr(), s_dn.data_ptr(),
-                None if b_dn is None else b_dn.data_ptr())
-    e._tensors, e._device = (w_gu, s_gu, b_gu, w_dn, s_dn, b_dn), dev
-    return e
+    e = Experts(fmt=EXPERT_FORMATS[fmt], E=E, n_shared=n_shared, H=H, I=I, glu=glu)
+    e._tensors = (w_gu, s_gu, b_gu, w_dn, s_dn, b_dn)
+    e._specs = (("w_gu", "w_gu", _U8, (n * gu_bytes,)), ("s_gu", "s_gu", _F32, (n, 2 * I)), ("b_gu", "b_gu", _F32, (n, 2 * I)),
+                ("w_dn", "w_dn", _U8, (n * dn_bytes,)), ("s_dn", "s_dn", _F32, (n, H)), ("b_dn", "b_dn", _F32, (n, H)))
+    return _settle(e)
 
 
 def _check_home(dev, *descs):
+    """The descriptors' tensors, wherever their memory is now, are on the current device."""
     for d in descs:
+        if [t.data_ptr() for t in d._held] != d._addrs:
+            _settle(d)
         if d._device != dev:
             raise ValueError(f"the descriptor's tensors live on cuda:{d._device}, the current device is cuda:{dev}")
 

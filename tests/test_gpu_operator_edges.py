@@ -98,3 +98,23 @@ def test_infinite_logits_lead_or_trail(bq, E, k):
             assert (np.abs(host(weights).astype(np.float64) - ww) <= U * ww + 2.0 ** -150).all()
         else:                                               # an infinite logit has no softmax
             assert np.isfinite(host(weights)[4]).all()
+
+
+def test_weights_that_moved_are_found(bq):
+    """New storage behind the same tensors (a reload, an update by swapping .data): the next call reads the new one."""
+    import torch
+    g = wl.rng(2)
+    N, K, H, I, E = 72, 128, 64, 32, 3
+    a, b = (bq.QuantLinear.from_float("w8", [dev(wl.weights(g, N, K))]) for _ in range(2))
+    layers = [bq.MoeLayer.from_float("w4", bq.MoeRouter(dev(wl.weights(g, E, H)), 2), [dev(wl.weights(g, 2 * I, H)) for _ in range(E)],
+                                     [dev(wl.weights(g, H, I)) for _ in range(E)]) for _ in range(2)]
+    x, t = dev(wl.activations(g, 3, K)), dev(wl.activations(g, 2, H))
+    wants = [q(x).clone() for q in (a, b)], [m(t).clone() for m in layers]
+    assert not torch.equal(*wants[0]) and not torch.equal(*wants[1])
+    tensors = [(a.w, b.w), (a.s_w, b.s_w)]
+    for d0, d1 in ((layers[0].desc, layers[1].desc), (layers[0].router.desc, layers[1].router.desc)):
+        tensors += [(p, q) for p, q in zip(d0._tensors, d1._tensors) if p is not None]
+    for p, q in tensors:
+        p.data, q.data = q.data, p.data
+    assert torch.equal(a(x), wants[0][1]) and torch.equal(b(x), wants[0][0])
+    assert torch.equal(layers[0](t), wants[1][1]) and torch.equal(layers[1](t), wants[1][0])
