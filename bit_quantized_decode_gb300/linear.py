@@ -238,6 +238,9 @@ class LinearChain:
             raise ValueError("empty chain")
         if len(items) > _lib.W4_MAX_CHAIN:
             raise ValueError(f"at most {_lib.W4_MAX_CHAIN} linears per chain")
+        other = sorted({ql.fmt for ql, *_ in items} - {"w4", "w4a32"})
+        if other:
+            raise ValueError(f"a chain takes per-row INT4 weights, not {', '.join(other)}")
         dev = items[0][0].w.device
         self.M = M
         self.items = list(items)

@@ -107,3 +107,14 @@ def test_descriptors_take_the_addresses_of_the_call(calls):
         t.data = old
     assert len(calls) == n
     right(*layer())
+
+
+@pytest.mark.parametrize("fmt", ["w8", "w8a32", "q4_0"])
+def test_a_chain_takes_int4_rows_only(calls, fmt):
+    """A chain reads its weights as per-row INT4: the INT8 linear's bytes would be taken for twice as many of them."""
+    from bit_quantized_decode_gb300 import LinearChain
+    N, K = 8, 64
+    lin = QuantLinear(fmt, N, K, torch.zeros(_lib.w8_repacked_bytes(N, K), dtype=torch.uint8), torch.zeros(N), None, None)
+    x, y = torch.zeros(1, K), torch.zeros(1, N)
+    with pytest.raises(ValueError, match="per-row INT4"):
+        LinearChain([(lin, x, y, torch.zeros((1, K), dtype=torch.int8), torch.zeros(1))], 1)
