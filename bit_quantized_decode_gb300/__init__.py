@@ -19,6 +19,7 @@ from .moe import MoeLayer, MoeRouter
 __all__ = [
     "W4_FLAG_PDL", "W4Error", "LinearChain", "MoeLayer", "MoeRouter", "QuantLinear", "a8_quantize", "clear_device_error", "device_error",
     "i8g32_gemv", "i8g32_linear", "i8g32_quantize", "i8g32_repack", "i8g32_repacked_bytes", "q4_0_gemv",
-    "q4_0_linear", "q4_0_quantize", "q4_0_repack", "q4_0_repacked_bytes", "w4_concat_f32", "w4_quantize_rows",
-    "w4_repack", "w4_repacked_bytes", "w4a8_gemv", "w4a8_linear",
+    "q4_0_linear", "q4_0_quantize", "q4_0_repack", "q4_0_repacked_bytes", "w4_concat_f32", "w4_moe_experts", "w4_moe_layer",
+    "w4_moe_route", "w4_quantize_rows", "w4_repack", "w4_repacked_bytes", "w4a8_gemv", "w4a8_linear", "w8_repack_glu",
+    "w8a8_linear", "w8a8_matmul",
 ]

@@ -118,3 +118,9 @@ def test_a_chain_takes_int4_rows_only(calls, fmt):
     x, y = torch.zeros(1, K), torch.zeros(1, N)
     with pytest.raises(ValueError, match="per-row INT4"):
         LinearChain([(lin, x, y, torch.zeros((1, K), dtype=torch.int8), torch.zeros(1))], 1)
+
+
+def test_every_imported_function_is_public():
+    import bit_quantized_decode_gb300 as bq
+    names = {n for n, v in vars(bq).items() if not n.startswith("_") and not isinstance(v, types.ModuleType)}
+    assert names - {"annotations"} == set(bq.__all__)
