@@ -118,3 +118,88 @@ def test_weights_that_moved_are_found(bq):
         p.data, q.data = q.data, p.data
     assert torch.equal(a(x), wants[0][1]) and torch.equal(b(x), wants[0][0])
     assert torch.equal(layers[0](t), wants[1][1]) and torch.equal(layers[1](t), wants[1][0])
+
+
+def _streams_of(tensors):
+    """The stream whose pool holds each tensor's memory, as the allocator keeps it."""
+    import torch
+    segments = torch.cuda.memory_snapshot()
+
+    def of(t):
+        return next(s["stream"] for s in segments if s["address"] <= t.data_ptr() < s["address"] + s["total_size"])
+    return [of(t) for t in tensors]
+
+
+def test_a_call_on_a_stream_takes_its_memory_from_that_streams_pool(bq, monkeypatch):
+    """Every tensor that a call makes itself, outputs and temporaries: memory that the allocator orders with the given stream."""
+    import torch
+    g = wl.rng(12)
+    N, K, H, I, E, k = 520, 2048, 64, 32, 6, 2
+    lin = bq.QuantLinear.from_float("w8", [dev(wl.weights(g, N, K))])
+    router = bq.MoeRouter(dev(wl.weights(g, E, H)), k)
+    layer = bq.MoeLayer.from_float("w4", router, [dev(wl.weights(g, 2 * I, H)) for _ in range(E)], [dev(wl.weights(g, H, I)) for _ in range(E)])
+    made, empty = [], torch.empty
+
+    def recording(*args, **kw):
+        t = empty(*args, **kw)
+        if t.is_cuda:
+            made.append(t)
+        return t
+
+    side = torch.cuda.Stream()
+    xs = {M: dev(wl.activations(g, M, K)) for M in (1, 12, 300)}
+    codes = {M: (torch.ones((M, K), dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda"), torch.zeros((M, N), device="cuda")) for M in (1, 12, 300)}
+    t = dev(wl.residual_stream(g, 5, H))
+    b, y = layer.buffers(5), torch.zeros((5, H), device="cuda")
+    router(t, bq.moe.RouteBuffers(b.ids, b.weights), b.qx, b.sx)
+    calls = [(lambda s, x=x: lin(x, stream=s), 3) for x in xs.values()]
+    calls += [(lambda s, c=c: lin.gemv(*c, stream=s), 1) for c in codes.values()]
+    calls += [(lambda s: router(t, stream=s), 2), (lambda s: layer(t, stream=s), 6),
+              (lambda s: layer.experts(b.qx, b.sx, b.ids, b.weights, y, stream=s), 1)]
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", recording)
+    for stream, handle in ((side, side.cuda_stream), (None, torch.cuda.current_stream().cuda_stream)):
+        for call, count in calls:
+            made.clear()
+            call(stream)
+            assert len(made) == count and _streams_of(made) == [handle] * count
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["w4", "w8"])
+@pytest.mark.parametrize("M,H,I", [(1, 3584, 2976), (2, 3584, 2976), (16, 3584, 2976), (16, 1056, 4128)])
+def test_largest_magnitudes_of_the_experts(bq, fmt, M, H, I):
+    """Codes of +-127 against weights at both ends of their range, in both halves of the layer: each integer sum at its largest
+    or cancelling to the last bit, one rounding in the epilogue."""
+    import torch
+    lo, top = (-8, 7) if fmt == "w4" else (-128, 127)
+
+    def rows(n, K):
+        w = np.full((n, K), lo, np.int8)
+        w[1::4] = top
+        w[2::4, ::2] = top                                         # sums that nearly cancel
+        w[3::4, 1::2] = top
+        w[:, 17] = np.arange(n) % (top - lo + 1) + lo              # and differ in one weight
+        return w
+
+    # gates at the top, ups at both ends with scales that make them alike: every code of h is +-127
+    gu, dn = [np.full((2 * I, H), top, np.int8) for _ in range(2)], [rows(H, I) for _ in range(2)]
+    for w in gu:
+        w[I::2] = lo
+    q = np.full((M, H), 127, np.int8)
+    q[1::3] = -127
+    q[2::3, ::2] = -126
+    s = np.full(M, 2.0 ** -7)
+    s_gu = np.full((2, 2 * I), 2.0 ** -2 / (H * top), np.float32)
+    s_gu[:, I::2] = 2.0 ** -2 / (H * -lo)
+    s_dn = np.full((2, H), 2.0 ** -9, np.float32)
+    h = ref.act("silu", *np.split(ref.linear(q[:2], s[:2], gu[1], s_gu[1])[1], 2, axis=1))
+    assert (np.abs(ref.codes(h)[0]) == 127).all()
+    layer = bq.MoeLayer.from_canonical(fmt, bq.MoeRouter(torch.zeros(2, H, device="cuda"), 1), [_stored(fmt, w) for w in gu], dev(s_gu),
+                                       [_stored(fmt, w) for w in dn], dev(s_dn))
+    ids, w = np.ones((M, 1), np.int32), np.ones((M, 1), np.float32)
+    y = torch.empty((M, H), device="cuda")
+    layer.experts(dev(q), dev(s.astype(np.float32)), dev(ids), dev(w), y)
+    want, room = ref.experts(q, s, ids, w, gu, s_gu, dn, s_dn, "silu")
+    assert (np.abs(want).max(axis=1) > 0).all()
+    assert (np.abs(host(y).astype(np.float64) - want) <= 1.05 * (room + U * np.abs(want))).all()
