@@ -25,10 +25,9 @@
 //     tokens c with c % splits = r), so every block writes a share of y.
 // A stage of 128 K takes some 400 ns whatever the tokens of the tile: a group's
 // way from the landing over the conversion to the arrival, twice as long, more
-// than the MMAs (with one MMA instead of eight 16 tokens would take 92 us, without the
-// conversion's arithmetic 85).  16 tokens, 152064 x 3584: 92 us (6.03 TB/s, measured
-// copy rate 6.79); 64 tokens, 3584 x 18944: 26.1 us with the quantizer; 333
-// tokens, 3584 x 3584: 23.0 us with it.
+// than the MMAs.  16 tokens, 152064 x 3584: 92 us (6.03 TB/s, measured copy rate
+// 6.79); 64 tokens, 3584 x 18944: 26.1 us with the quantizer; 333 tokens, 3584 x
+// 3584: 22.9 us with it.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -157,7 +156,9 @@ __global__ void __launch_bounds__(kG8Threads, 1) gemm_w8_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // the next kernel's blocks may come only once this one holds its tensor memory
+    // The next kernel's blocks may come only once this one holds its tensor memory.  (All of it: blocks that wait for tensor
+    // memory on an SM wait for this one to end.  None of the library's is beside it there: 143 KB of shared memory at
+    // least here, 106 KB at least in gemv_tc.cu, of 228 KB.)
     pdl_launch_dependents();
     if (ks > 1) cluster_sync();          // the other splits' shared memory is there
     const uint32_t tbase = *tmem_slot;

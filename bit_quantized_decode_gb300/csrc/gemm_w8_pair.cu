@@ -17,9 +17,10 @@
 //   * The epilogue's two warpgroups hold 96 columns of int32 each; registers are
 //     moved to them from the others (setmaxnreg; 5 x 128 threads start with 96,
 //     then 40 + 72 + 72 + 144 + 144 of 480).
-// 4096 tokens, 37888 x 3584 in bf16: 725 us with the quantizer, 1.53 PFLOP/s (the
-// library's bf16 product sustains 1.73 on this chip); the tensor pipe is active
-// for two thirds of the time.
+// 4096 tokens, 37888 x 3584 in bf16, with the quantizer: 728 to 734 us in graph
+// replays, 1.52 PFLOP/s (the library's bf16 product sustains 1.73 on this chip),
+// 760 us as single calls on changing inputs; the tensor pipe is active for two
+// thirds of the time.
 #include "gemm_w8.cuh"
 
 namespace w4k {

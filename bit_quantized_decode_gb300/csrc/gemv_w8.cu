@@ -10,11 +10,14 @@
 //     K, and add their integer sums in shared memory.
 //   * One or two tokens: every block normalizes and quantizes them itself (a
 //     launch less); more come as codes from the row quantizer.
-//   * A weight word meets four codes in one DP4A, with no unpacking, so up to
-//     eight tokens the products keep up with HBM; past that the tensor cores'
-//     product (gemm_w8.cu) takes over.  Both are exact, so the results agree
-//     bit for bit.
-// One token: 152064 x 3584 at 7.05 TB/s, 4608 x 3584 with its norm 6.2 us.
+//   * A weight word meets four codes in one DP4A, with no unpacking; past eight
+//     tokens the tensor cores' product (gemm_w8.cu) takes over.  Both are exact,
+//     so the results agree bit for bit.  us in graph replays, quantizer included
+//     (the tensor cores' product at the same tokens), 152064 x 3584: one token
+//     80.7 (6.77 TB/s), two 83.6 (91.5), four 87.5 (91.0), seven 90.4 (92.1),
+//     eight 95.5 (92.0); 4608 x 3584: two 6.6 (11.3), eight 9.6 (11.4).  At eight
+//     a long matrix would gain from changing over and a short one would lose more.
+// 4608 x 3584 with its norm, one token: 6.3 us.
 #include "fusion.cuh"
 #include "operators.h"
 #include "ptx.cuh"

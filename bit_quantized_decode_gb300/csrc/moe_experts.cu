@@ -37,7 +37,7 @@
 //     INT8 tiles just afford and INT4 ones would not.
 //     A slice of 16 lines takes a warp some 1600 cycles and its copies and
 //     bookkeeping another 1300; waits for memory are 5%.  16 tokens over 64
-//     experts of 2368 x 3584 (722 MB of INT4): 178 us with the router; DP4A 202.
+//     experts of 2368 x 3584 (722 MB of INT4): 178 to 181 us with the router; DP4A 202.
 //   * No fence per tile (it waits for all that the warp has outstanding: it
 //     took 3500 of a tile's 9500 cycles): hidden values and the slots' outputs
 //     are prepared with a value that no result takes (MoeFill), and a reader

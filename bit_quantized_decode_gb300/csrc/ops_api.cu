@@ -155,10 +155,11 @@ w4_status check_router(const w4_router* r, int M, int K)
 }
 
 // Blocks per cluster, tokens per cluster and warps per expert.  A token's
-// logits spread over a cluster of 16 blocks while all clusters run at once, up
-// to eight tokens (8 tokens, 256 experts of 1536: 10.5 us, with clusters of 8
-// 13.5 us); more tokens take clusters of 8 (16 tokens: 14.9 against 17.9 us).
-// As few tokens to a cluster as two blocks per SM allow.
+// logits spread over a cluster of 16 blocks up to eight tokens; more tokens take
+// clusters of 8, all of which run at once.  256 experts of 1536, softmax scores,
+// us in graph replays: 9 tokens 13.4 (clusters of 16: 10.3), 12 tokens 13.5
+// (10.4), 16 tokens 14.4 (17.4); 64 experts of 3584: 9 tokens 9.9 (9.6), 16
+// tokens 10.7 (14.6).  As few tokens to a cluster as two blocks per SM allow.
 bool plan_route(const DeviceFacts& d, RouteArgs& a)
 {
     const int most = a.M <= 8 ? kRtMaxCluster : 8;

@@ -451,7 +451,11 @@ w4_status w8a32_gemv(const void* w, const float* s_w, const float* bias, const f
  * token and up to 192 of padding), 16-byte aligned, with no contents to keep; calls that
  * share one must not overlap on the GPU.  W4_FLAG_PDL as above: the weights
  * are fetched before the dependency wait.
- * Results do not depend on M: a token's row is the same in every batch.
+ * The codes and the scale of a token given, its row is the same in every batch,
+ * and so are the codes of an x that is not normalized.  With norm_weight the sum
+ * of squares is added in an order that depends on M, to 2^-45 of it, and rounded
+ * once: for a sum that close to a rounding boundary (one random token in some 10
+ * million) r, and with it a few codes, may be a step off another batch's.
  * ------------------------------------------------------------------------ */
 #define W4_F32 0
 #define W4_F16 1
@@ -483,7 +487,9 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
  * K % 32 == 0, 1 <= top_k <= min(E, 16), E <= 1024; K up to about 50000 (a
  * token is kept in shared memory as fp32).  A logit past fp32 is an infinity
  * of its sign (softmax then has NaN weights); a NaN logit is the last choice;
- * the ids are valid and distinct whatever x holds.
+ * the ids are valid and distinct whatever x holds.  The order of the sums
+ * depends on M: a logit within 2^-44 of its terms' magnitudes of a rounding
+ * boundary may be a step off another batch's (and r, as for w8a8_linear).
  *
  * w4_moe_experts.  For every token m and slot s with expert e = ids[m][s]:
  *   g, u = linear(qx, sx) by e's gate and up rows, as the W4 / W8A8 linears,
@@ -495,8 +501,9 @@ w4_status w8a8_linear(const void* w, const float* s_w, const float* bias, const 
  *          to y's type.
  * An id outside 0 .. E - 1 is an empty slot and contributes nothing; a token
  * with empty slots only gets the residual (or 0).  An expert may be named
- * twice.  The experts' weights are read once for all their tokens; results do
- * not depend on the other tokens of the call, nor on timing.
+ * twice.  The experts' weights are read once for all their tokens; for given
+ * codes, ids and weights the results do not depend on the other tokens of the
+ * call, nor on timing.
  *   experts: E + n_shared of them, the shared ones last, one behind the other:
  *     w_gu  *_repack_glu of gate and up [I][H] each, *_glu_repacked_bytes(I, H)
  *           apart;   s_gu (b_gu): float [E + n_shared][2 I], gate rows first;
