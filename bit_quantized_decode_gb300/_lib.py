@@ -655,9 +655,14 @@ def w8a8_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(load().w8a8_workspace_bytes(M, N, K))
 
 
+def _places(tensors):
+    """Address and bytes of each tensor: as long as they stay, what was checked of its memory holds."""
+    return [(t.data_ptr(), t.nbytes) for t in tensors]
+
+
 class W8Weights:
     """Checked weights of the INT8 x INT8 linear (w8_repack), for callers that use them again and again."""
-    __slots__ = ("w", "s_w", "bias", "N", "K", "device", "addr")
+    __slots__ = ("w", "s_w", "bias", "N", "K", "device", "addr", "held", "places")
 
     def __init__(self, w, s_w, bias, N: int, K: int):
         self.w, self.s_w, self.bias, self.N, self.K = w, s_w, bias, N, K
@@ -670,11 +675,12 @@ class W8Weights:
         if self.w.numel() < need:
             raise ValueError(f"w: {self.w.numel()} bytes, {need} are needed")
         self.addr = (_addr(self.w), _addr(self.s_w), _addr(self.bias))
+        self.held = tuple(t for t in (self.w, self.s_w, self.bias) if t is not None)
+        self.places = _places(self.held)
 
     def addresses(self):
         """Where the weights are now: a tensor may have got other memory since the last call, which is checked then."""
-        bias = self.bias
-        if (self.w.data_ptr(), self.s_w.data_ptr(), None if bias is None else bias.data_ptr()) != self.addr:
+        if _places(self.held) != self.places:
             self._settle()
         return self.addr
 
@@ -714,9 +720,9 @@ def w8a8_linear_on(weights: W8Weights, x, y, qx, sx, workspace, norm=None, eps: 
     if norm is not None or residual is not None:
         fz = ctypes.byref(Fusion(None if norm is None else norm.data_ptr(), float(eps), W4_GLU_NONE,
                                  None if residual is None else residual.data_ptr()))
-    _check("w8a8_linear", load().w8a8_linear(*addr, _addr(x), ELEM_TYPES[x.dtype], M, N, K,
-                                             _addr(y), ELEM_TYPES[y.dtype], _addr(qx), _addr(sx), fz, flags,
-                                             _addr(workspace), workspace.numel(), _raw_stream(stream, dev)))
+    _check("w8a8_linear", load().w8a8_linear(*addr, x.data_ptr(), ELEM_TYPES[x.dtype], M, N, K,
+                                             y.data_ptr(), ELEM_TYPES[y.dtype], _addr(qx), _addr(sx), fz, flags,
+                                             workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)))
 
 
 # ------------------------------------------------- mixture of experts, few tokens
@@ -740,7 +746,7 @@ def _settle(desc):
     for (field, *_), t in zip(desc._specs, desc._tensors):
         setattr(desc, field, _addr(t))
     desc._held = tuple(t for t in desc._tensors if t is not None)
-    desc._addrs = [t.data_ptr() for t in desc._held]
+    desc._places = _places(desc._held)
     return desc
 
 
@@ -774,7 +780,7 @@ def moe_experts(fmt: str, w_gu, s_gu, w_dn, s_dn, E: int, n_shared: int, H: int,
 def _check_home(dev, *descs):
     """The descriptors' tensors, wherever their memory is now, are on the current device."""
     for d in descs:
-        if [t.data_ptr() for t in d._held] != d._addrs:
+        if _places(d._held) != d._places:
             _settle(d)
         if d._device != dev:
             raise ValueError(f"the descriptor's tensors live on cuda:{d._device}, the current device is cuda:{dev}")

@@ -124,3 +124,27 @@ def test_every_imported_function_is_public():
     import bit_quantized_decode_gb300 as bq
     names = {n for n, v in vars(bq).items() if not n.startswith("_") and not isinstance(v, types.ModuleType)}
     assert names - {"annotations"} == set(bq.__all__)
+
+
+def test_a_smaller_tensor_at_the_same_address_is_checked(calls):
+    """A part of the old storage, or another type in it: the address alone does not show it."""
+    N, K, M, E, H, I = 8, 64, 3, 4, 64, 32
+    lin = QuantLinear("w8", N, K, torch.zeros(_lib.w8_repacked_bytes(N, K), dtype=torch.uint8), torch.zeros(N), torch.zeros(N), None)
+    r, e = _lib.moe_router(torch.zeros(E, H), 2, torch.zeros(E), "sigmoid", norm=torch.zeros(H)), _experts(E, H, I)
+    x, y, sx, ws = torch.zeros(M, K), torch.zeros(M, N), torch.zeros(M), torch.zeros(1 << 16, dtype=torch.uint8)
+    ids, w, qx, z = torch.zeros(M, 2, dtype=torch.int32), torch.zeros(M, 2), torch.zeros(M, H, dtype=torch.int8), torch.zeros(M, H)
+    linear = lambda: lin(x, y, None, sx, workspace=ws)                          # noqa: E731
+    layer = lambda: _lib.w4_moe_layer(r, e, x, ids, w, qx, sx, z, ws)           # noqa: E731
+    for call, tensors in ((linear, (lin.w, lin.s_w, lin.bias)), (layer, (*r._tensors, *e._tensors))):
+        call()
+        for t in tensors:
+            whole = t.data
+            for part in (whole[:-1], whole.view(torch.int8)[..., : whole.shape[-1]] if whole.element_size() > 1 else whole[: 1]):
+                assert part.data_ptr() == whole.data_ptr()
+                t.data = part
+                n = len(calls)
+                with pytest.raises(ValueError):
+                    call()
+                assert len(calls) == n
+                t.data = whole
+            call()
