@@ -171,6 +171,42 @@ ELEM_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # W4_F32,
 W4_MAX_TOKENS = 1 << 20
 W4_MAX_CHAIN = 128
 
+
+class KVCacheDesc(ctypes.Structure):
+    """w4_kv_cache of include/w4a8.h."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("type", _I), ("pages", _I), ("page_size", _I),
+                ("Hkv", _I), ("D", _I)]
+
+
+class KVBatchDesc(ctypes.Structure):
+    """w4_kv_batch of include/w4a8.h."""
+    _fields_ = [("table", _P), ("ctx", _P), ("q_start", _P), ("B", _I), ("max_pages", _I), ("max_tokens", _I)]
+
+
+class RopeDesc(ctypes.Structure):
+    """w4_rope of include/w4a8.h."""
+    _fields_ = [("turns", _P), ("positions", _I), ("rot", _I), ("layout", _I)]
+
+
+class LogitRulesDesc(ctypes.Structure):
+    """w4_logit_rules of include/w4a8.h."""
+    _fields_ = [("V", _I), ("S", _I), ("ids", _P), ("cap", _I), ("length", _P), ("prompt", _P), ("repetition", _P),
+                ("frequency", _P), ("presence", _P), ("bias_ids", _P), ("bias", _P), ("n_bias", _I)]
+
+
+_PC = ctypes.POINTER(KVCacheDesc)
+_PB = ctypes.POINTER(KVBatchDesc)
+SIGNATURES["w4_rope_table"] = ([_P, ctypes.c_double, ctypes.c_double, _I, _I, _P, _P], _I)
+SIGNATURES["w4_kv_append"] = ([_PC, _PB, ctypes.POINTER(RopeDesc), _P, _I, _LL, _I, _I, _P, _P, _P, _F, _P, _I, _U, _P], _I)
+SIGNATURES["w4_tree_attention_workspace_bytes"] = ([_PC, _PB, _I, _I], _SZ)
+SIGNATURES["w4_tree_attention"] = ([_PC, _PB, _P, _I, _I, _I, _P, _F, _P, _I, _P, _SZ, _U, _P], _I)
+SIGNATURES["w4_logits_adjust"] = ([ctypes.POINTER(LogitRulesDesc), _P, _I, _LL, _I, _P, _P, _P, _P, _P, _LL, _U, _P], _I)
+CACHE_TYPES = {torch.float16: 1, torch.bfloat16: 2, torch.int8: 3}     # W4_F16, W4_BF16, W4_I8
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+W4_MAX_SEQUENCES = 1024
+W4_MAX_DRAFTS = 64
+W4_MAX_BIASES = 1024
+
 _lib = None
 
 
@@ -831,6 +867,165 @@ def w4_moe_layer(router, experts, x, ids, weights, qx, sx, y, workspace, residua
                                                _addr(ids), _addr(weights), _addr(qx), _addr(sx), _addr(residual), _addr(y),
                                                ELEM_TYPES[y.dtype], _addr(workspace), workspace.numel(), flags,
                                                _raw_stream(stream, dev)))
+
+
+# --------------------------------------- attention over a paged cache, and logits
+_CACHES = tuple(CACHE_TYPES)
+_HALVES = (torch.float16, torch.bfloat16)
+_I64 = (torch.int64,)
+_F64 = (torch.float64,)
+
+
+def _check_rows(name, t, dtypes, width=None):
+    """A 2-D tensor whose rows are contiguous (they may be apart): the current CUDA device and the rows' distance."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name}: tensor must live on a CUDA device")
+    if at != torch.cuda.current_device():
+        raise ValueError(f"{name}: tensor lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype} is not one of {[str(d) for d in dtypes]}")
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is not rows of {width}")
+    n, w = t.shape
+    if w > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    if n > 1 and t.stride(0) < w:
+        raise ValueError(f"{name}: rows overlap")
+    return at, t.stride(0) if n > 1 else w
+
+
+def kv_cache(k, v, k_scale=None, v_scale=None):
+    """A w4_kv_cache descriptor: k and v [pages][Hkv][page_size][D] of fp16, bf16 or int8 codes with scales float32
+    [pages][Hkv][page_size].  It holds references to its tensors."""
+    if k.dim() != 4:
+        raise ValueError(f"k: shape {tuple(k.shape)} is not [pages][heads][page_size][head_dim]")
+    if (k.dtype == torch.int8) != (k_scale is not None) or (k.dtype == torch.int8) != (v_scale is not None):
+        raise ValueError("an int8 cache has scales for keys and values, a 16-bit cache has none")
+    pages, heads, page_size, D = k.shape
+    c = KVCacheDesc(type=CACHE_TYPES.get(k.dtype, -1), pages=pages, page_size=page_size, Hkv=heads, D=D)
+    c._tensors = (k, v, k_scale, v_scale)
+    c._specs = (("k", "k", _CACHES, k.shape), ("v", "v", (k.dtype,), k.shape), ("k_scale", "k_scale", _F32, k.shape[:3]),
+                ("v_scale", "v_scale", _F32, k.shape[:3]))
+    return _settle(c)
+
+
+def kv_batch(table, ctx, q_start, max_tokens: int):
+    """A w4_kv_batch descriptor: table int32 [B][max_pages], ctx int32 [B], q_start int32 [B + 1], all on the device.  It
+    holds references to its tensors."""
+    if table.dim() != 2:
+        raise ValueError(f"table: shape {tuple(table.shape)} is not [sequences][pages]")
+    B, max_pages = table.shape
+    b = KVBatchDesc(B=B, max_pages=max_pages, max_tokens=int(max_tokens))
+    b._tensors = (table, ctx, q_start)
+    b._specs = (("table", "table", _I32, (B, max_pages)), ("ctx", "ctx", _I32, (B,)), ("q_start", "q_start", _I32, (B + 1,)))
+    return _settle(b)
+
+
+def rope_desc(turns, layout: str = "half"):
+    """A w4_rope descriptor over turns float32 [positions][rot / 2][2].  It holds a reference to its tensor."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout {layout!r} is not one of {sorted(ROPE_LAYOUTS)}")
+    if turns.dim() != 3 or turns.shape[2] != 2:
+        raise ValueError(f"turns: shape {tuple(turns.shape)} is not [positions][rot / 2][2]")
+    r = RopeDesc(positions=turns.shape[0], rot=2 * turns.shape[1], layout=ROPE_LAYOUTS[layout])
+    r._tensors, r._specs = (turns,), (("turns", "turns", _F32, tuple(turns.shape)),)
+    return _settle(r)
+
+
+def w4_rope_table(inv_freq, turns, factor: float = 1.0, scale: float = 1.0, stream=None):
+    """turns float32 [positions][rot / 2][2]: (cos, sin) of position * factor * inv_freq (float64 [rot / 2]), times scale."""
+    positions, half, _ = turns.shape
+    dev = _check_tensors(("inv_freq", inv_freq, _F64, (half,)), ("turns", turns, _F32, (positions, half, 2)))
+    _check("w4_rope_table", load().w4_rope_table(_addr(inv_freq), float(factor), float(scale), positions, 2 * half, _addr(turns),
+                                                 _raw_stream(stream, dev)))
+
+
+def w4_kv_append(cache, batch, rope, qkv, q, positions=None, q_norm=None, k_norm=None, eps: float = 1e-6, flags: int = 0,
+                 stream=None):
+    """Rows qkv [T][(Hq + 2 Hkv) D] (fp32, fp16 or bf16; rows may be apart): norms and rotation of q [T][Hq][D] (fp16 or
+    bf16) and of the keys, which go to the cache with the values.  positions: int32 [T] or None."""
+    D = cache.D
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q: shape {tuple(q.shape)} is not [rows][heads][{D}]")
+    T, Hq, _ = q.shape
+    _, ld = _check_rows("qkv", qkv, _FLOATS, (Hq + 2 * cache.Hkv) * D)
+    dev = _check_tensors(("q", q, _HALVES, (qkv.shape[0], Hq, D)), ("positions", positions, _I32, (T,)),
+                         ("q_norm", q_norm, _F32, (D,)), ("k_norm", k_norm, _F32, (D,)))
+    if rope is None:
+        _check_home(dev, cache, batch)
+    else:
+        _check_home(dev, cache, batch, rope)
+    _check("w4_kv_append", load().w4_kv_append(ctypes.byref(cache), ctypes.byref(batch), None if rope is None else ctypes.byref(rope),
+                                               qkv.data_ptr(), ELEM_TYPES[qkv.dtype], ld, T, Hq, _addr(positions), _addr(q_norm),
+                                               _addr(k_norm), float(eps), q.data_ptr(), ELEM_TYPES[q.dtype], flags,
+                                               _raw_stream(stream, dev)))
+
+
+def w4_tree_attention_workspace_bytes(cache, batch, T: int, Hq: int) -> int:
+    return int(load().w4_tree_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(batch), T, Hq))
+
+
+def w4_tree_attention(cache, batch, q, y, workspace, mask=None, scale: float = None, flags: int = 0, stream=None):
+    """y [T][Hq][D] (fp32, fp16 or bf16) of q [T][Hq][D] over the cache; mask int64 [T]: bit j is the sequence's row j
+    (None: a row sees the rows up to itself); scale: 1 / sqrt(D) if None."""
+    D = cache.D
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q: shape {tuple(q.shape)} is not [rows][heads][{D}]")
+    T, Hq, _ = q.shape
+    dev = _check_tensors(("q", q, _HALVES, None), ("y", y, _FLOATS, q.shape), ("mask", mask, _I64, (T,)),
+                         ("workspace", workspace, _U8, None))
+    _check_home(dev, cache, batch)
+    _check("w4_tree_attention", load().w4_tree_attention(ctypes.byref(cache), ctypes.byref(batch), q.data_ptr(), ELEM_TYPES[q.dtype],
+                                                         T, Hq, _addr(mask), D ** -0.5 if scale is None else float(scale),
+                                                         y.data_ptr(), ELEM_TYPES[y.dtype], workspace.data_ptr(),
+                                                         workspace.numel(), flags, _raw_stream(stream, dev)))
+
+
+def logit_rules(vocab: int, ids=None, length=None, prompt=None, repetition=None, frequency=None, presence=None, bias_ids=None,
+                bias=None, sequences: int = None):
+    """A w4_logit_rules descriptor: ids int32 [S][cap], length and prompt int32 [S], factors float32 [S], bias_ids int32 and
+    bias float32 [S][n_bias].  It holds references to its tensors."""
+    if (ids is None) != (length is None) or (ids is None and prompt is not None):
+        raise ValueError("ids and length come together, prompt with them")
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias come together")
+    S, cap, nb = sequences, 0, 0
+    for t in (ids, repetition, frequency, presence, bias_ids):
+        if t is not None and S is None:
+            S = t.shape[0]
+    if S is None:
+        raise ValueError("the number of sequences is not known: give sequences")
+    if ids is not None:
+        cap = ids.shape[1] if ids.dim() == 2 else -1
+    if bias_ids is not None:
+        nb = bias_ids.shape[1] if bias_ids.dim() == 2 else -1
+    if cap < 0 or nb < 0:
+        raise ValueError("ids and bias_ids are [sequences][entries]")
+    u = LogitRulesDesc(V=int(vocab), S=S, cap=cap, n_bias=nb)
+    u._tensors = (ids, length, prompt, repetition, frequency, presence, bias_ids, bias)
+    u._specs = (("ids", "ids", _I32, (S, cap)), ("length", "length", _I32, (S,)), ("prompt", "prompt", _I32, (S,)),
+                ("repetition", "repetition", _F32, (S,)), ("frequency", "frequency", _F32, (S,)),
+                ("presence", "presence", _F32, (S,)), ("bias_ids", "bias_ids", _I32, (S, nb)), ("bias", "bias", _F32, (S, nb)))
+    return _settle(u)
+
+
+def w4_logits_adjust(rules, logits, out, row_start=None, drafts=None, mask=None, allowed=None, flags: int = 0, stream=None):
+    """out [R][V] = logits [R][V] (fp32, fp16 or bf16; rows may be apart) after penalties, biases and the grammar's mask:
+    allowed int32 [R][ceil(V / 32)]; row_start int32 [S + 1], drafts int32 [R] and mask int64 [R] for drafted trees."""
+    V = rules.V
+    dev, ld = _check_rows("logits", logits, _FLOATS, V)
+    _, ld_out = _check_rows("out", out, (logits.dtype,), V)
+    R = logits.shape[0]
+    if out.shape[0] != R:
+        raise ValueError(f"out: {out.shape[0]} rows, logits have {R}")
+    _check_tensors(("row_start", row_start, _I32, (rules.S + 1,)), ("drafts", drafts, _I32, (R,)), ("mask", mask, _I64, (R,)),
+                   ("allowed", allowed, _I32, (R, (V + 31) // 32)))
+    if rules._held:
+        _check_home(dev, rules)
+    _check("w4_logits_adjust", load().w4_logits_adjust(ctypes.byref(rules), logits.data_ptr(), ELEM_TYPES[logits.dtype], ld, R,
+                                                       _addr(row_start), _addr(drafts), _addr(mask), _addr(allowed),
+                                                       out.data_ptr(), ld_out, flags, _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- chains

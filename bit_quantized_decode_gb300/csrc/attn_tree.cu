@@ -1,0 +1,708 @@
+// Attention of a few drafted tokens over a paged cache:
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - max),
+// over the places t < ctx of a sequence and the drafts j whose bit the row's
+// mask has.
+//
+// The rows of a tile are (token, head of a key head's group) pairs, 16 of them:
+// one m16 tile of mma.sync, so every key and value is read once for all of
+// them.  Work is counted in units of 16 cached tokens over all (sequence, key
+// head, tile) segments and dealt to the blocks in equal shares, whatever the
+// sequences' lengths; a block walks its share segment by segment.  In a
+// block, each warp takes every eighth unit with a ring of its own: a lane
+// orders the unit's keys and values from the tensor map (16 tokens are always
+// in one page), two to five units ahead, and the warp multiplies, takes
+// the softmax with a running maximum and sum, and multiplies again, without a
+// barrier to other warps until the segment ends.  Then the warps' results are
+// joined in shared memory; a segment that several blocks share is joined by
+// the second launch (attn_join_kernel) in the order of its pieces, so no
+// result depends on timing.
+//
+// Precision: products of 16-bit numbers in fp32 sums; probabilities enter the
+// second product in 16 bits, as two numbers (high and low part) where the
+// output is fp32.  INT8 codes are exact in 16 bits; a key's scale multiplies its
+// score, a value's scale its probability (bf16: no range of the scales is lost).
+#include <atomic>
+
+#include "attn_tree.cuh"
+
+namespace w4k {
+namespace {
+
+template <int D, int CT>
+struct At {
+    static constexpr int kEb = CT == T_I8 ? 1 : 2;
+    static constexpr int kRow = D * kEb;                      // bytes of a token
+    static constexpr int kBox = kRow < 128 ? kRow : 128;      // bytes of a box row
+    static constexpr int kBoxes = kRow / kBox;
+    static constexpr int kHalf = kAtUnit * kRow;              // a unit's keys (or values)
+    static constexpr int kSlot = 2 * kHalf;
+    static constexpr int kWarps = D == 256 ? 4 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kRing = 192 * 1024 / (kWarps * kSlot);
+    static constexpr int kSlots = kRing > 6 ? 6 : kRing;      // units ahead of a warp
+    static constexpr int kParts = kWarps / 4;                 // joined row blocks: four warps take turns on one
+    static constexpr int kPad = D + 8;                        // floats of a joined row: rows spread over the banks
+    // shared memory
+    static constexpr int oRing = 0;
+    static constexpr int oJoin = kWarps * kSlots * kSlot;                              // [kParts][16][kPad]
+    static constexpr int oScale = oJoin + kParts * kAtRows * kPad * 4;             // [warps][slots][2][16]
+    static constexpr int oMl = oScale + (CT == T_I8 ? kWarps * kSlots * 2 * kAtUnit * 4 : 0);   // [warps][2][16]
+    static constexpr int oFin = oMl + kWarps * 2 * kAtRows * 4;                        // [2][16]
+    static constexpr int oBars = oFin + 2 * kAtRows * 4;
+    static constexpr int oOk = oBars + kWarps * kSlots * 8;                            // [warps][slots]: the page is there
+    static constexpr int oWarpSum = (oOk + kWarps * kSlots * 4 + 7) / 8 * 8;
+    static constexpr int oPre = oWarpSum + kWarps * 8;
+    static constexpr int smem(int B) { return oPre + (B + 1) * 8 + 1024; }              // and the alignment of the ring
+    static_assert(kSlots >= 2, "two units per warp");
+    static_assert(oPre + (kAtMaxSeq + 1) * 8 + 1024 <= 232448, "shared memory of a block");
+};
+
+// The byte at column x of token t in a half slot, as the copies with a swizzle lay it.
+template <int D, int CT>
+__device__ __forceinline__ uint32_t place_of(int t, int x)
+{
+    using C = At<D, CT>;
+    if constexpr (C::kBox == 128) {
+        const int o = t * 128 + (x & 127);
+        return static_cast<uint32_t>((x >> 7) * (kAtUnit * 128) + (o ^ ((t & 7) << 4)));
+    } else {                                                  // 64-byte rows: two tokens to 128 bytes
+        const int o = t * 64 + x;
+        return static_cast<uint32_t>(o ^ ((o >> 7 & 3) << 4));
+    }
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// c += a b, 16 x 8 x 16, fp16 or bf16 operands.
+template <int T>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (T == T_F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two fp32 as a pair of 16-bit numbers (the first in the low half).
+template <int T>
+__device__ __forceinline__ uint32_t pair16(float a, float b)
+{
+    if constexpr (T == T_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <int T>
+__device__ __forceinline__ float2 unpair16(uint32_t u)
+{
+    if constexpr (T == T_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Four int8 -> four bf16, exactly: the low seven bits on 128.0 (whose last place is 1), less 128 or, for a negative code,
+// 256.
+__device__ __forceinline__ void i8_to_bf16(uint32_t c, uint32_t& h01, uint32_t& h23)
+{
+    const uint32_t m = c & 0x7f7f7f7fu, n = c & 0x80808080u;
+    const uint32_t a = __byte_perm(m, 0x43434343u, 0x4140), b = __byte_perm(m, 0x43434343u, 0x4342);
+    const uint32_t s = __byte_perm(n, 0x43434343u, 0x4140), t = __byte_perm(n, 0x43434343u, 0x4342);
+    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&t));
+    h01 = *reinterpret_cast<const uint32_t*>(&x);
+    h23 = *reinterpret_cast<const uint32_t*>(&y);
+}
+template <int T>
+__device__ __forceinline__ void codes16(uint32_t c, uint32_t& h01, uint32_t& h23)
+{
+    if constexpr (T == T_F16) i8_to_f16(c, h01, h23);
+    else i8_to_bf16(c, h01, h23);
+}
+
+template <int D, int CT, int QT, bool kWide>
+__global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const __grid_constant__ AttnArgs A)
+{
+    using C = At<D, CT>;
+    constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
+    constexpr int W = C::kWarps;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    float* join_s = reinterpret_cast<float*>(smem + C::oJoin);
+    float* ml_s = reinterpret_cast<float*>(smem + C::oMl);
+    float* fin_s = reinterpret_cast<float*>(smem + C::oFin);
+    volatile int* ok_s = reinterpret_cast<volatile int*>(smem + C::oOk) + warp * C::kSlots;
+    long long* pre_s = reinterpret_cast<long long*>(smem + C::oPre);
+    const uint32_t bars = smem_u32(smem + C::oBars) + static_cast<uint32_t>(warp * C::kSlots * 8);
+    uint8_t* ring = smem + C::oRing + warp * C::kSlots * C::kSlot;
+    const uint32_t ring_a = smem_u32(ring);
+    float* scale_s = reinterpret_cast<float*>(smem + C::oScale) + warp * C::kSlots * 2 * kAtUnit;
+
+    if (lane == 0) {
+        for (int k = 0; k < C::kSlots; ++k) mbar_init(bars + 8 * k, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    pdl_launch_dependents();
+    pdl_wait();
+    seq_prefix<C::kThreads>(A, kAtRows, kAtUnit, pre_s, reinterpret_cast<long long*>(smem + C::oWarpSum));
+    const long long total = pre_s[A.b.B];
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < W) share = W;                   // a unit for each warp
+    if (blockIdx.x == 0) {                      // for the joining launch
+        if (tid == 0) A.head[0] = share;
+        for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[1 + b] = pre_s[b];
+    }
+    const long long us = min(static_cast<long long>(blockIdx.x) * share, total), ue = min(us + share, total);
+    if (us >= ue) return;
+
+    // ------------------------------------------------- copies, units ahead
+    // The warp's units of a piece are its begin + warp, + W, ..; pieces follow each other.
+    Segment ps = find_segment(A, pre_s, us, kAtRows, kAtUnit);
+    long long pend = min(ps.u0 + ps.units, ue), pu = us + warp;
+    int page_ahead = -1;
+    auto settle = [&]() {                       // pu: the next unit to order (or none: pu >= ue); its page
+        while (pu >= pend && pend < ue) {
+            const long long begin = pend;
+            ps = find_segment(A, pre_s, begin, kAtRows, kAtUnit);
+            pend = min(ps.u0 + ps.units, ue);
+            pu = begin + warp;
+        }
+        if (pu < pend) {
+            const int t = static_cast<int>(pu - ps.u0) * kAtUnit;
+            page_ahead = __ldg(A.b.table + static_cast<size_t>(ps.b) * A.b.max_pages + (t >> A.c.lg));
+        }
+    };
+    settle();
+    int issued = 0;
+    auto order = [&](int slot) {
+        if (pu >= pend) return;
+        const uint32_t bar = bars + 8 * slot;
+        const bool there = page_ahead >= 0 && page_ahead < A.c.pages;
+        if (lane == 0) {
+            ok_s[slot] = there;
+            if (there) {
+                const int y = static_cast<int>(pu - ps.u0) * kAtUnit & (A.c.page - 1);
+                const int z = page_ahead * A.c.Hkv + ps.h;
+                mbar_arrive_expect_tx(bar, C::kSlot + (CT == T_I8 ? 2 * kAtUnit * 4 : 0));
+                const uint32_t dst = ring_a + slot * C::kSlot;
+#pragma unroll
+                for (int x = 0; x < C::kBoxes; ++x) {
+                    tma_load_3d(dst + x * kAtUnit * C::kBox, &A.kmap, x * C::kBox / C::kEb, y, z, bar);
+                    tma_load_3d(dst + C::kHalf + x * kAtUnit * C::kBox, &A.vmap, x * C::kBox / C::kEb, y, z, bar);
+                }
+                if constexpr (CT == T_I8) {
+                    const size_t at = static_cast<size_t>(z) * A.c.page + y;
+                    bulk_copy(smem_u32(scale_s + slot * 2 * kAtUnit), A.c.ks + at, kAtUnit * 4, bar);
+                    bulk_copy(smem_u32(scale_s + slot * 2 * kAtUnit + kAtUnit), A.c.vs + at, kAtUnit * 4, bar);
+                }
+            } else {
+                mbar_arrive(bar);
+            }
+        }
+        __syncwarp();
+        ++issued;
+        pu += W;
+        settle();
+    };
+#pragma unroll 1
+    for (int k = 0; k < C::kSlots; ++k) order(k);
+
+    // ------------------------------------------------------------ segments
+    int slot = 0, seen = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+#pragma unroll 1
+    for (long long begin = us; begin < ue;) {
+        const Segment sg = find_segment(A, pre_s, begin, kAtRows, kAtUnit);
+        const long long end = min(sg.u0 + sg.units, ue);
+        const int rows = min(kAtRows, sg.f.n * A.G - sg.tile * kAtRows);
+        // this lane's rows g and g + 8: queries, masks
+        uint32_t qa[D / 16][4];
+        unsigned long long see[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = g + 8 * e;
+            const bool have = r < rows;
+            const int rr = sg.tile * kAtRows + (have ? r : 0);
+            const int tok = rr / A.G, t = sg.f.q0 + tok;
+            see[e] = A.mask != nullptr ? __ldg(A.mask + t) : (2ull << tok) - 1ull;
+            const uint16_t* q = static_cast<const uint16_t*>(A.q) + (static_cast<size_t>(t) * A.Hq + sg.h * A.G + (rr - tok * A.G)) * D;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint2 v;
+                if constexpr (CT == T_I8) {     // a lane's K values of a step are four codes in a row
+                    v = __ldg(reinterpret_cast<const uint2*>(q + 16 * j + 4 * c));
+                } else {
+                    v.x = __ldg(reinterpret_cast<const unsigned*>(q + 16 * j + 2 * c));
+                    v.y = __ldg(reinterpret_cast<const unsigned*>(q + 16 * j + 8 + 2 * c));
+                }
+                qa[j][e] = have ? v.x : 0u;
+                qa[j][2 + e] = have ? v.y : 0u;
+            }
+        }
+        float o[D / 8][4];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+        float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.0f, 0.0f};
+
+#pragma unroll 1
+        for (long long u = begin + warp; u < end; u += W) {
+            if (!dead) {
+                const bool ok = mbar_wait_bounded(bars + 8 * slot, phase, kAtWaitNs);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    dead = true;
+                    if (lane == 0 && A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
+                }
+            }
+            if (dead) continue;
+            ++seen;
+            uint8_t* ks = ring + slot * C::kSlot;
+            uint8_t* vs = ks + C::kHalf;
+            const uint32_t ka = ring_a + slot * C::kSlot, va = ka + C::kHalf;
+            const int t0 = static_cast<int>(u - sg.u0) * kAtUnit;
+            if (ok_s[slot] != 0) {
+                // scores: tokens 2c, 2c + 1, 8 + 2c, 9 + 2c of rows g, g + 8
+                float s[2][4] = {};
+                if constexpr (CT == T_I8) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + place_of<D, CT>(g + 8 * h, 16 * j + 4 * c));
+                            uint32_t b0, b1;
+                            codes16<QT>(w, b0, b1);
+                            mma16<QT>(s[h], qa[j], b0, b1);
+                        }
+                } else {
+                    // four 8 x 8 matrices: tokens 0-7 and 8-15, each the two halves of 16 columns
+                    const int t = (lane & 7) + ((lane >> 4) << 3), x = (lane >> 3 & 1) * 16;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t b[4];
+                        ldsm_x4(ka + place_of<D, CT>(t, 32 * j + x), b);
+                        mma16<QT>(s[0], qa[j], b[0], b[1]);
+                        mma16<QT>(s[1], qa[j], b[2], b[3]);
+                    }
+                }
+                float vsc[4];
+                if constexpr (CT == T_I8) {
+                    const float* sc = scale_s + slot * 2 * kAtUnit;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 kk = *reinterpret_cast<const float2*>(sc + 8 * h + 2 * c);
+                        const float2 vv = *reinterpret_cast<const float2*>(sc + kAtUnit + 8 * h + 2 * c);
+                        s[h][0] *= kk.x * A.scale; s[h][2] *= kk.x * A.scale;
+                        s[h][1] *= kk.y * A.scale; s[h][3] *= kk.y * A.scale;
+                        vsc[2 * h] = vv.x;
+                        vsc[2 * h + 1] = vv.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) s[h][k] *= A.scale;
+                }
+                // drafts: a row sees those of its mask; places behind the last do not count
+                const bool drafts = t0 + kAtUnit > sg.f.ctx;
+                unsigned hidden = 0;
+                if (drafts) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = t0 + 8 * h + 2 * c + (k & 1), j = t - sg.f.ctx;
+                            if (j >= 0 && (t >= sg.f.len || ((see[k >> 1] >> j) & 1ull) == 0ull)) {
+                                s[h][k] = neg_inf();
+                                hidden |= 1u << (4 * h + k);
+                            }
+                        }
+                }
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    if (__any_sync(0xffffffffu, top > m[e])) {
+                        const float was = m[e];
+                        m[e] = fmaxf(was, top);
+                        const float f = was == neg_inf() ? 0.0f : exp2_fast(was - m[e]);
+                        l[e] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            o[j][2 * e] *= f;
+                            o[j][2 * e + 1] *= f;
+                        }
+                    }
+                    const float base = m[e] == neg_inf() ? 0.0f : m[e];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 2 * e; k < 2 * e + 2; ++k) {
+                            const float p = exp2_fast(s[h][k] - base);
+                            l[e] += p;
+                            if constexpr (CT == T_I8) s[h][k] = (hidden >> (4 * h + k)) & 1u ? 0.0f : p * vsc[2 * h + (k & 1)];
+                            else s[h][k] = p;
+                        }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t p = pair16<PT>(s[h][2 * e], s[h][2 * e + 1]);
+                        hi[2 * h + e] = p;
+                        if constexpr (kWide) {
+                            const float2 r = unpair16<PT>(p);
+                            lo[2 * h + e] = pair16<PT>(s[h][2 * e] - r.x, s[h][2 * e + 1] - r.y);
+                        }
+                    }
+                if constexpr (CT == T_I8) {
+                    // four tokens' words of four columns, transposed: columns 4 (g + 8 jj) + i of tokens 2c, 2c + 1, 8 + 2c, 9 + 2c
+#pragma unroll
+                    for (int jj = 0; jj < D / 32; ++jj) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = *reinterpret_cast<const uint32_t*>(vs + place_of<D, CT>(2 * c + (k & 1) + 8 * (k >> 1), 4 * (g + 8 * jj)));
+                        const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+                        const uint32_t d = __byte_perm(w[0], w[1], 0x7362), e = __byte_perm(w[2], w[3], 0x7362);
+                        const uint32_t col[4] = {__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632),
+                                                 __byte_perm(d, e, 0x5410), __byte_perm(d, e, 0x7632)};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t b0, b1;
+                            i8_to_bf16(col[i], b0, b1);
+                            mma16<PT>(o[4 * jj + i], hi, b0, b1);
+                            if constexpr (kWide) mma16<PT>(o[4 * jj + i], lo, b0, b1);
+                        }
+                    }
+                } else {
+                    bool plain = false;
+                    if (drafts) {
+                        // Places behind the last hold anything: zeros in their stead.  A draft's infinities and NaN would
+                        // reach the rows that do not see it (0 times them): such a unit is summed without the tensor cores.
+                        bool odd = false;
+                        for (int k = lane; k < kAtUnit * D / 2; k += 32) {
+                            const int t = k / (D / 2);
+                            uint32_t* w = reinterpret_cast<uint32_t*>(vs + place_of<D, CT>(t, 4 * (k % (D / 2))));
+                            const uint32_t top = CT == T_F16 ? 0x7c00u : 0x7f80u;
+                            if (t0 + t >= sg.f.len) *w = 0u;
+                            else if (t0 + t >= sg.f.ctx) odd |= (*w & top) == top || (*w >> 16 & top) == top;
+                        }
+                        plain = __any_sync(0xffffffffu, odd);
+                        __syncwarp();
+                    }
+                    if (!plain) {
+                        const int t = lane & 15, x = (lane >> 4) * 16;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            uint32_t b[4];
+                            ldsm_x4_t(va + place_of<D, CT>(t, 32 * j + x), b);
+                            mma16<PT>(o[2 * j], hi, b[0], b[1]);
+                            mma16<PT>(o[2 * j + 1], hi, b[2], b[3]);
+                            if constexpr (kWide) {
+                                mma16<PT>(o[2 * j], lo, b[0], b[1]);
+                                mma16<PT>(o[2 * j + 1], lo, b[2], b[3]);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int t = 0; t < kAtUnit; ++t) {
+                            const int from = (lane & 28) | ((t & 7) >> 1);
+                            float p[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float p0 = __shfl_sync(0xffffffffu, t & 8 ? s[1][2 * e] : s[0][2 * e], from);
+                                const float p1 = __shfl_sync(0xffffffffu, t & 8 ? s[1][2 * e + 1] : s[0][2 * e + 1], from);
+                                p[e] = t & 1 ? p1 : p0;
+                                const int j = t0 + t - sg.f.ctx;
+                                if (j >= 0 && (t0 + t >= sg.f.len || ((see[e] >> j) & 1ull) == 0ull)) p[e] = -1.0f;
+                            }
+#pragma unroll
+                            for (int j = 0; j < D / 8; ++j) {
+                                const float2 v = unpair16<PT>(*reinterpret_cast<const uint32_t*>(vs + place_of<D, CT>(t, 2 * (8 * j + 2 * c))));
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (p[e] >= 0.0f) {
+                                        o[j][2 * e] += p[e] * v.x;
+                                        o[j][2 * e + 1] += p[e] * v.y;
+                                    }
+                            }
+                        }
+                    }
+                    if (drafts) fence_proxy_async_smem();     // (zeros were written where the next copy lands)
+                }
+            }
+            __syncwarp();
+            order(slot);
+            if (++slot == C::kSlots) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+
+        // -------------------------------------------- the warps' results joined
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+            if (c == 0) {
+                ml_s[(warp * 2) * kAtRows + g + 8 * e] = m[e];
+                ml_s[(warp * 2 + 1) * kAtRows + g + 8 * e] = l[e];
+            }
+        }
+        __syncthreads();
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = g + 8 * e;
+            float top = neg_inf(), sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) top = fmaxf(top, ml_s[w * 2 * kAtRows + r]);
+            const float base = top == neg_inf() ? 0.0f : top;
+#pragma unroll
+            for (int w = 0; w < W; ++w) sum += ml_s[(w * 2 + 1) * kAtRows + r] * exp2_fast(ml_s[w * 2 * kAtRows + r] - base);
+            f[e] = exp2_fast(m[e] - base);
+            if (warp == 0 && c == 0) {
+                fin_s[r] = top;
+                fin_s[kAtRows + r] = sum;
+            }
+        }
+        auto at = [&](int e, int j, int k) {                  // accumulator (row g + 8 e, tile j, column k) -> place in a joined row block
+            const int d = CT == T_I8 ? 4 * (2 * c + k + 8 * (j >> 2)) + (j & 3) : 8 * j + 2 * c + k;
+            return (g + 8 * e) * C::kPad + d;
+        };
+        float* mine = join_s + (warp % C::kParts) * kAtRows * C::kPad;
+#pragma unroll 1
+        for (int turn = 0; turn < 4; ++turn) {
+            if (warp / C::kParts == turn) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (g + 8 * e < rows)
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float& v = mine[at(e, j, k)];
+                                v = turn == 0 ? o[j][2 * e + k] * f[e] : v + o[j][2 * e + k] * f[e];
+                            }
+            }
+            __syncthreads();
+        }
+        const bool whole = begin == sg.u0 && end == sg.u0 + sg.units;
+        float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(kAtRows, D);
+        if (!whole && tid < rows) {
+            part[tid] = fin_s[tid];
+            part[kAtRows + tid] = fin_s[kAtRows + tid];
+        }
+        for (int k = tid; k < rows * (D / 4); k += C::kThreads) {
+            const int r = k / (D / 4), d = k % (D / 4) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < C::kParts; ++w) {
+                const float4 t = *reinterpret_cast<const float4*>(join_s + (w * kAtRows + r) * C::kPad + d);
+                v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+            }
+            if (!whole) {
+                *reinterpret_cast<float4*>(part + 2 * kAtRows + r * D + d) = v;
+            } else {
+                const float sum = fin_s[kAtRows + r], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const int rr = sg.tile * kAtRows + r, tok = rr / A.G;
+                const size_t y = (static_cast<size_t>(sg.f.q0 + tok) * A.Hq + sg.h * A.G + (rr - tok * A.G)) * D + d;
+                const float w[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+                if (A.ytype == T_F32) *reinterpret_cast<float4*>(static_cast<float*>(A.y) + y) = make_float4(w[0], w[1], w[2], w[3]);
+                else if (A.ytype == T_F16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + y) = make_uint2(pair16<T_F16>(w[0], w[1]), pair16<T_F16>(w[2], w[3]));
+                else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + y) = make_uint2(pair16<T_BF16>(w[0], w[1]), pair16<T_BF16>(w[2], w[3]));
+            }
+        }
+        __syncthreads();
+        begin = end;
+    }
+    // after a timeout: this warp's copies in flight land before the block ends
+    if (dead)
+        for (int k = seen; k < issued; ++k)
+            if (!mbar_wait_bounded(bars + 8 * (k % C::kSlots), static_cast<uint32_t>(k / C::kSlots) & 1u, kAtWaitNs)) break;
+}
+
+// Rows of segments that several blocks share: the pieces' results weighted by
+// 2^(maximum - the largest) and added in the pieces' order, one block per row.
+constexpr int kJoinThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs A, int tile_rows, int unit)
+{
+    __shared__ float w_s[kAtMaxBlocks];
+    __shared__ float red_s[kJoinThreads / 32][D];
+    __shared__ float sum_s[kJoinThreads / 32], top_s[kJoinThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int t = static_cast<int>(blockIdx.x) / A.Hq, head = static_cast<int>(blockIdx.x) - t * A.Hq;
+    const int b = row_sequence(A.b.q_start, A.b.B, t, lane);
+    if (b >= A.b.B) return;
+    const SeqFacts f = seq_facts(A, b);
+    const int i = t - f.q0;
+    if (i < 0 || i >= f.n) return;
+    const int h = head / A.G, r = i * A.G + (head - h * A.G), tile = r / tile_rows, row = r - tile * tile_rows;
+    const int units = seq_units(f, unit);
+    const long long u0 = A.head[1 + b] + (static_cast<long long>(h) * seq_tiles(A, f, tile_rows) + tile) * units;
+    const long long share = A.head[0];
+    const int j0 = static_cast<int>(u0 / share), j1 = static_cast<int>((u0 + units - 1) / share);
+    if (j0 == j1) return;                       // one block's: written
+    const int pieces = j1 - j0 + 1;
+    const size_t pf = attn_part_floats(tile_rows, D);
+    // (a block's first piece is in its first place; a piece that begins within the block in the second)
+    auto part = [&](int k) {
+        const int j = j0 + k;
+        return A.part + (static_cast<size_t>(j) * 2 + (j * share < u0 ? 1 : 0)) * pf;
+    };
+    float top = neg_inf();
+    for (int k = tid; k < pieces; k += kJoinThreads) {
+        w_s[k] = part(k)[row];
+        top = fmaxf(top, w_s[k]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (lane == 0) top_s[warp] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
+    const float base = top == neg_inf() ? 0.0f : top;
+    float sum = 0.0f;
+    for (int k = tid; k < pieces; k += kJoinThreads) {
+        const float w = exp2_fast(w_s[k] - base);
+        w_s[k] = w;
+        sum += w * part(k)[tile_rows + row];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+    constexpr int kV = D / 32;
+    float acc[kV] = {};
+#pragma unroll 4
+    for (int k = warp; k < pieces; k += kJoinThreads / 32) {
+        const float* p = part(k) + 2 * tile_rows + static_cast<size_t>(row) * D;
+        const float w = w_s[k];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) acc[v] += w * __ldcg(p + 32 * v + lane);
+    }
+#pragma unroll
+    for (int v = 0; v < kV; ++v) red_s[warp][32 * v + lane] = acc[v];
+    __syncthreads();
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int d = tid; d < D; d += kJoinThreads) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) v += red_s[w][d];
+        store_typed(A.y, A.ytype, (static_cast<size_t>(t) * A.Hq + head) * D + d, v * inv);
+    }
+}
+
+cudaError_t encode_kv_map(CUtensorMap* map, const AttnArgs& a, const void* base, int box_bytes, int box_rows)
+{
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<void*> cached{nullptr};
+    void* fn = cached.load(std::memory_order_acquire);
+    if (fn == nullptr) {
+        cudaDriverEntryPointQueryResult got;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got);
+        if (e != cudaSuccess) return e;
+        if (got != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+        cached.store(fn, std::memory_order_release);
+    }
+    const cuuint64_t eb = a.c.type == T_I8 ? 1 : 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.D), static_cast<cuuint64_t>(a.c.page),
+                                static_cast<cuuint64_t>(a.c.pages) * a.c.Hkv};
+    const cuuint64_t strides[2] = {a.c.D * eb, a.c.D * eb * a.c.page};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / eb), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r = reinterpret_cast<Encode>(fn)(
+        map, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides,
+        box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, bool pdl)
+{
+    if (!pdl) return;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+}
+
+template <int D, int CT, int QT, bool kWide>
+cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+{
+    using C = At<D, CT>;
+    auto kern = attn_tree_kernel<D, CT, QT, kWide>;
+    static SmemLimit limit;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, C::smem(kAtMaxSeq));
+    if (e == cudaSuccess) e = encode_kv_map(&a.kmap, a, a.c.k, C::kBox, kAtUnit);
+    if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, C::kBox, kAtUnit);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::smem(a.b.B);
+    cfg.stream = s;
+    dependent(cfg, attr, pdl);
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess || grid == 1) return e;
+    cudaLaunchConfig_t join = {};
+    join.gridDim = dim3(static_cast<unsigned>(a.T) * static_cast<unsigned>(a.Hq));
+    join.blockDim = dim3(kJoinThreads);
+    join.stream = s;
+    dependent(join, attr, true);
+    return cudaLaunchKernelEx(&join, attn_join_kernel<D>, a, kAtRows, kAtUnit);
+}
+
+template <int D, int CT, int QT>
+cudaError_t launch_w(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+{
+    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, pdl, s) : launch<D, CT, QT, false>(a, grid, pdl, s);
+}
+
+template <int D>
+cudaError_t launch_d(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+{
+    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, pdl, s);
+    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, pdl, s);
+    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, pdl, s) : launch_w<D, T_I8, T_BF16>(a, grid, pdl, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+{
+    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, pdl, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, pdl, s)
+                                                                            : launch_d<256>(a, qtype, grid, pdl, s);
+}
+
+}  // namespace w4k

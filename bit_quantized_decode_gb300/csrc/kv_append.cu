@@ -1,0 +1,244 @@
+// Cache append: RMSNorm of each query and key head, their rotation by
+// position, and the way of keys and values into a paged cache, in one pass
+// over the q/k/v projection's output.
+//
+//   x' = (x r) g, r = 1 / sqrt(fp32(sum x^2) / D + eps)         (q and k, optional)
+//   a' = a c - b s, b' = b c + a s   over pairs of the first `rot` values
+//   16-bit cache: rounded once; INT8: s = max|x'| / 127, q = clip(rint(x' / s)).
+//
+// D / 8 lanes take a head, eight values to a lane: a lane of the half layout
+// holds four values and their four partners, so a rotation needs no exchange,
+// and a pair's (cos, sin) is read once.  A warp takes 4, 2 or 1 heads of a
+// token (D 64, 128, 256).  An INT8 code hangs on the last bit of a value, so a
+// key for an INT8 cache is rotated with exact products and a compensated sum
+// (rounded once), and the squares are summed in compensated pairs as in the
+// other fused norms.  Memory bound for prompts; for a few tokens the chain of
+// loads (row's sequence, its length, the page) is.
+#include "attention.h"
+#include "fusion.cuh"
+#include "ptx.cuh"
+#include "typed_io.cuh"
+
+namespace w4k {
+namespace {
+
+template <int T>
+__device__ __forceinline__ void load4(const void* base, size_t at, float* v)
+{
+    if constexpr (T == T_F32) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + at));
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at));
+        const uint32_t w[2] = {u.x, u.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if constexpr (T == T_F16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                v[2 * k] = f.x;
+                v[2 * k + 1] = f.y;
+            } else {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack16(int type, float a, float b)
+{
+    if (type == T_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// a c + b d rounded once (but for sums within some 2^-46 of a rounding boundary).
+__device__ __forceinline__ float dot2_once(float a, float c, float b, float d)
+{
+    const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
+    const float q = __fmul_rn(b, d), qe = __fmaf_rn(b, d, -q);
+    float s, e;
+    two_sum(p, q, s, e);
+    return __fadd_rn(s, __fadd_rn(e, __fadd_rn(pe, qe)));
+}
+
+template <int XT, int D>
+__global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs A)
+{
+    constexpr int kLanes = D / 8;               // lanes of a head
+    constexpr int kHeads = 32 / kLanes;         // heads of a warp
+    const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int H = A.Hq + 2 * A.c.Hkv;
+    const int groups = (H + kHeads - 1) / kHeads;
+    const long long task = (static_cast<long long>(blockIdx.x) * kKaThreads + threadIdx.x) >> 5;
+    if (task >= static_cast<long long>(A.T) * groups) return;
+    const int t = static_cast<int>(task / groups);
+    const int head = static_cast<int>(task - static_cast<long long>(t) * groups) * kHeads + lane / kLanes;
+    const int u = lane % kLanes;                // eight values of the head
+
+    // the values, as they lie: of a rotated half-layout unit 4u.. and rot/2 + 4u.., else 8u..
+    const bool turned = 8 * u < A.rot && head < A.Hq + A.c.Hkv;
+    const bool split = turned && !A.interleaved;
+    const int at0 = split ? 4 * u : 8 * u, at1 = split ? A.rot / 2 + 4 * u : 8 * u + 4;
+    float x[8];
+    const bool have = head < H;
+    const size_t base = static_cast<size_t>(t) * A.ld + static_cast<size_t>(have ? head : 0) * D;
+    load4<XT>(A.x, base + at0, x);
+    load4<XT>(A.x, base + at1, x + 4);
+
+    const int b = row_sequence(A.b.q_start, A.b.B, t, lane);
+    if (b >= A.b.B) return;                     // behind the last sequence
+    const int i = t - __ldg(A.b.q_start + b);
+    if (i < 0) return;
+    const long long place = static_cast<long long>(max(__ldg(A.b.ctx + b), 0)) + i;
+
+    const bool is_q = head < A.Hq, is_k = !is_q && head < A.Hq + A.c.Hkv;
+    const bool i8 = A.c.type == T_I8;
+    const float* g = is_q ? A.q_norm : is_k ? A.k_norm : nullptr;
+    if (A.q_norm != nullptr || A.k_norm != nullptr) {
+        float hi = 0.0f, lo = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sq_acc(x[k], hi, lo);
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) {
+            const float h2 = __shfl_xor_sync(0xffffffffu, hi, off), l2 = __shfl_xor_sync(0xffffffffu, lo, off);
+            pair_merge(hi, lo, h2, l2);
+        }
+        hi = __shfl_sync(0xffffffffu, hi, lane - u);          // (the same sum in every lane of the head)
+        lo = __shfl_sync(0xffffffffu, lo, lane - u);
+        if (g != nullptr) {
+            const float r = rms_scale(hi, lo, D, A.eps);
+            float w[8];
+            load4<T_F32>(g, at0, w);
+            load4<T_F32>(g, at1, w + 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(__fmul_rn(x[k], r), w[k]);
+        }
+    }
+    bool lost = false;                          // a position that the table does not have
+    if (A.rot > 0) {
+        const long long p = A.pos != nullptr ? __ldg(A.pos + t) : place;
+        lost = p < 0 || p >= A.positions;
+        if (turned) {
+            float cs[8], pa[4], pb[4];          // (cos, sin) of pairs 4u .. 4u + 3; the pairs
+            load4<T_F32>(A.turns, static_cast<size_t>(lost ? 0 : p) * A.rot + 8 * u, cs);
+            load4<T_F32>(A.turns, static_cast<size_t>(lost ? 0 : p) * A.rot + 8 * u + 4, cs + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pa[k] = split ? x[k] : x[2 * k], pb[k] = split ? x[4 + k] : x[2 * k + 1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float c = lost ? __int_as_float(0x7fc00000) : cs[2 * k], s = cs[2 * k + 1];
+                const float a = pa[k], v = pb[k];
+                if (i8 && is_k) {
+                    pa[k] = dot2_once(a, c, -v, s);
+                    pb[k] = dot2_once(v, c, a, s);
+                } else {
+                    pa[k] = __fmaf_rn(a, c, -__fmul_rn(v, s));
+                    pb[k] = __fmaf_rn(v, c, __fmul_rn(a, s));
+                }
+            }
+            x[0] = pa[0];
+            x[1] = split ? pa[1] : pb[0];
+            x[2] = split ? pa[2] : pa[1];
+            x[3] = split ? pa[3] : pb[1];
+            x[4] = split ? pb[0] : pa[2];
+            x[5] = split ? pb[1] : pb[2];
+            x[6] = split ? pb[2] : pa[3];
+            x[7] = pb[3];
+        }
+    }
+    if (is_q && have) {
+        uint16_t* q = static_cast<uint16_t*>(A.q) + (static_cast<size_t>(t) * A.Hq + head) * D;
+        *reinterpret_cast<uint2*>(q + at0) = make_uint2(pack16(A.qtype, x[0], x[1]), pack16(A.qtype, x[2], x[3]));
+        *reinterpret_cast<uint2*>(q + at1) = make_uint2(pack16(A.qtype, x[4], x[5]), pack16(A.qtype, x[6], x[7]));
+    }
+    // the page; a place past the table, or a page that the cache does not have, is not written
+    const long long pi = place >> A.c.lg;
+    const int page = pi < A.b.max_pages ? __ldg(A.b.table + static_cast<size_t>(b) * A.b.max_pages + pi) : -1;
+    const bool store = have && !is_q && page >= 0 && page < A.c.pages;
+    const int hk = is_k ? head - A.Hq : head - A.Hq - A.c.Hkv;
+    const size_t slot = (static_cast<size_t>(store ? page : 0) * A.c.Hkv + (store ? hk : 0)) * A.c.page +
+                        static_cast<size_t>(place & (A.c.page - 1));
+    if (!i8) {
+        if (store) {
+            uint16_t* d = static_cast<uint16_t*>(is_k ? A.c.k : A.c.v) + slot * D;
+            *reinterpret_cast<uint2*>(d + at0) = make_uint2(pack16(A.c.type, x[0], x[1]), pack16(A.c.type, x[2], x[3]));
+            *reinterpret_cast<uint2*>(d + at1) = make_uint2(pack16(A.c.type, x[4], x[5]), pack16(A.c.type, x[6], x[7]));
+        }
+        return;
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (!store) return;
+    const A8Scale ks = a8_scale(top);
+    uint2 q = quant8(x, ks);
+    lost = lost && is_k;
+    if (lost) q = make_uint2(0u, 0u);
+    int8_t* d = static_cast<int8_t*>(is_k ? A.c.k : A.c.v) + slot * D;
+    *reinterpret_cast<uint32_t*>(d + at0) = q.x;
+    *reinterpret_cast<uint32_t*>(d + at1) = q.y;
+    if (u == 0) (is_k ? A.c.ks : A.c.vs)[slot] = lost ? __int_as_float(0x7fc00000) : ks.s;
+}
+
+template <int XT, int D>
+cudaError_t launch(const AppendArgs& a, bool pdl, cudaStream_t s)
+{
+    constexpr int kHeads = 32 / (D / 8);
+    const long long tasks = static_cast<long long>(a.T) * ((a.Hq + 2 * a.c.Hkv + kHeads - 1) / kHeads);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((tasks * 32 + kKaThreads - 1) / kKaThreads));
+    cfg.blockDim = dim3(kKaThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kv_append_kernel<XT, D>, a);
+}
+
+template <int XT>
+cudaError_t launch_d(const AppendArgs& a, bool pdl, cudaStream_t s)
+{
+    return a.c.D == 64 ? launch<XT, 64>(a, pdl, s) : a.c.D == 128 ? launch<XT, 128>(a, pdl, s) : launch<XT, 256>(a, pdl, s);
+}
+
+// (cos, sin) of position * factor * inv_freq, times scale: angles of far positions
+// need the product and its reduction in 64 bits; each number is rounded once.
+__global__ void rope_table_kernel(const double* inv_freq, double factor, double scale, long long n, int half, float2* turns)
+{
+    const long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (e >= n) return;
+    const long long p = e / half;
+    double s, c;
+    sincos(static_cast<double>(p) * factor * inv_freq[e - p * half], &s, &c);
+    turns[e] = make_float2(static_cast<float>(c * scale), static_cast<float>(s * scale));
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendArgs& a, int xtype, bool pdl, cudaStream_t s)
+{
+    return xtype == T_F32 ? launch_d<T_F32>(a, pdl, s) : xtype == T_F16 ? launch_d<T_F16>(a, pdl, s) : launch_d<T_BF16>(a, pdl, s);
+}
+
+cudaError_t launch_rope_table(const double* inv_freq, double factor, double scale, int positions, int half, float* turns,
+                              cudaStream_t s)
+{
+    const long long n = static_cast<long long>(positions) * half;
+    rope_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(inv_freq, factor, scale, n, half,
+                                                                            reinterpret_cast<float2*>(turns));
+    return cudaGetLastError();
+}
+
+}  // namespace w4k

@@ -566,6 +566,140 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
                        void* workspace, size_t ws_bytes, unsigned flags, w4_stream_t s);
 
 /* ------------------------------------------------------------------------
+ * Attention over a paged cache, for a decode step or the verification of a
+ * tree of drafted tokens: the operators between the q/k/v and the output
+ * projection.
+ *
+ * w4_kv_cache: one layer's cache, k and v [pages][Hkv][page_size][D] of
+ *   W4_F16, W4_BF16 or W4_I8, 16-byte aligned.  INT8 codes have a scale for
+ *   each token and head, k_scale and v_scale [pages][Hkv][page_size], 16-byte
+ *   aligned (NULL for the 16-bit types).  D is 64, 128 or 256, page_size a
+ *   power of two from 16 to 256.
+ * w4_kv_batch: which rows of a call are whose.  Sequence b < B (at most
+ *   W4_MAX_SEQUENCES) has rows q_start[b] .. q_start[b + 1] - 1 (q_start int
+ *   [B + 1], ascending from 0) and ctx[b] places before them.  Row i of a
+ *   sequence has place ctx[b] + i: entry (place % page_size) of page
+ *   table[b][place / page_size] (table int [B][max_pages]).  Rows behind the
+ *   last sequence are left as they are.  A page outside 0 .. pages - 1, or a
+ *   place past the table, holds nothing: it is not written, and no row sees
+ *   it.  The arrays live on the device, so a captured call follows them.
+ *   max_tokens: the most rows of a sequence (rows past it get no attention);
+ *   at most W4_MAX_DRAFTS for w4_tree_attention, any number for w4_kv_append.
+ *
+ * w4_rope_table: turns float [positions][rot / 2][2], 16-byte aligned,
+ *   (cos, sin)(p * factor * inv_freq[i]) * scale: angles in 64 bits, each
+ *   number rounded once; rot % 8 == 0, at most 256.  inv_freq: double
+ *   [rot / 2] on the device.
+ * w4_kv_append, one launch: rows qkv [T] of ld values of x_type (16-byte
+ *   aligned, so is ld), Hq query heads, then Hkv key and Hkv value heads of D.
+ *   RMSNorm of each query (q_norm float [D]) and key head (k_norm), either
+ *   may be NULL; rotation of the first rot values of each query and key head
+ *   (rope NULL: none) by row positions[t] of the table (NULL: the row's
+ *   place), in pairs (i, i + rot / 2) (W4_ROPE_HALF) or (2 i, 2 i + 1)
+ *   (W4_ROPE_INTERLEAVED): a' = a c - b s, b' = b c + a s.  A position that
+ *   the table does not have gives NaN (in an INT8 cache: the scale).  q [T][Hq][D] of q_type
+ *   (W4_F16 or W4_BF16), 16-byte aligned; k and v go to the cache, rounded
+ *   once, or as the codes and scale that a8_quantize gives for a head's
+ *   values (the norm's steps as in rms_a8_quantize; a rotated value of a key
+ *   rounded once to fp32).  Two rows with the same place race.
+ * w4_tree_attention: y[t][h] = sum p v / sum p, p = exp(scale q.k), over the
+ *   places below ctx and the drafts of the row's own sequence (the rows of
+ *   this call, already appended) whose bit the row's mask has: bit j of
+ *   mask[t] (uint64, device) is row j of the sequence.  mask NULL: row i sees
+ *   rows 0 .. i.  A row that sees nothing gets 0.  What a row does not see
+ *   does not reach it, infinities and NaN included.  q [T][Hq][D] of the
+ *   cache's type (either 16-bit type for W4_I8), y [T][Hq][D] of y_type, both
+ *   16-byte aligned; query head h reads key head h / (Hq / Hkv).
+ *   Sums in fp32; probabilities in the second product are rounded to 16 bits
+ *   for a 16-bit y, and are held in two 16-bit parts for W4_F32.
+ *   workspace: w4_tree_attention_workspace_bytes(..) bytes, 16-byte aligned,
+ *   with no contents to keep; calls that share one must not overlap on the
+ *   GPU.  Two launches.  For given inputs the result is the same in every
+ *   call, but it depends on the other sequences of the call in its last bits
+ *   (how a sequence is split).
+ * flags: 0 or W4_FLAG_PDL.  T = 0 or B = 0 is a valid empty call.
+ * ------------------------------------------------------------------------ */
+#define W4_I8 3
+#define W4_ROPE_HALF 0
+#define W4_ROPE_INTERLEAVED 1
+#define W4_MAX_SEQUENCES 1024
+#define W4_MAX_DRAFTS 64
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int type;
+    int pages;
+    int page_size;
+    int Hkv;
+    int D;
+} w4_kv_cache;
+typedef struct {
+    const int* table;
+    const int* ctx;
+    const int* q_start;
+    int B;
+    int max_pages;
+    int max_tokens;
+} w4_kv_batch;
+typedef struct {
+    const float* turns;
+    int positions;
+    int rot;
+    int layout;
+} w4_rope;
+w4_status w4_rope_table(const double* inv_freq, double factor, double scale, int positions, int rot, float* turns,
+                        w4_stream_t s);
+w4_status w4_kv_append(const w4_kv_cache* c, const w4_kv_batch* b, const w4_rope* rope, const void* qkv, int x_type,
+                       long long ld, int T, int Hq, const int* positions, const float* q_norm, const float* k_norm,
+                       float eps, void* q, int q_type, unsigned flags, w4_stream_t s);
+size_t w4_tree_attention_workspace_bytes(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq); /* 0: refused or empty */
+w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const void* q, int q_type, int T, int Hq,
+                            const unsigned long long* mask, float scale, void* y, int y_type, void* workspace,
+                            size_t ws_bytes, unsigned flags, w4_stream_t s);
+
+/* ------------------------------------------------------------------------
+ * w4_logits_adjust, one launch: penalties for repeated tokens, biases and a
+ * grammar's mask on rows of logits, behind the vocabulary projection.
+ *   Sequence s < S has length[s] tokens ids[s][..] (ids int [S][cap]), the
+ *   first prompt[s] of them the prompt (prompt NULL: none), the others
+ *   generated.  Row r is sequence r's, or with row_start (int [S + 1],
+ *   ascending from 0) row row_start[s] + i is sequence s's i-th; rows behind
+ *   the last sequence are left as they are.  drafts int [R]: the token of each row in a
+ *   drafted tree; row r's path (bit j of mask[r]: row j of its sequence, j <
+ *   64; mask NULL: rows 0 .. i) counts as generated, r's own token with its own bit.
+ *   For token v with n occurrences among the generated ones:
+ *     l = l > 0 ? l / repetition[s] : l * repetition[s]   if n > 0 or v is in the prompt,
+ *     l = l - frequency[s] * n - presence[s]              if n > 0,
+ *     l = l + the biases of v, added in their order (bias_ids int [S][n_bias], bias float),
+ *     l = -inf                                            if bit v % 32 of allowed[r][v / 32] is 0,
+ *   each step an fp32 operation, rounded to the logits' type.  The arrays of
+ *   factors float [S] may be NULL (1, 0 and 0), so may allowed (uint32 [R][ceil(V / 32)]).
+ *   Ids outside 0 .. V - 1 are passed over.  logits: [R] rows of ld values of
+ *   `type`, out the same with ld_out (it may be logits itself).  V <= 2^24,
+ *   n_bias <= W4_MAX_BIASES.  flags: 0 or W4_FLAG_PDL.
+ * ------------------------------------------------------------------------ */
+#define W4_MAX_BIASES 1024
+typedef struct {
+    int V;
+    int S;
+    const int* ids;          /* [S][cap], or NULL with cap 0 */
+    int cap;
+    const int* length;       /* [S] */
+    const int* prompt;       /* [S] or NULL */
+    const float* repetition; /* [S] or NULL */
+    const float* frequency;  /* [S] or NULL */
+    const float* presence;   /* [S] or NULL */
+    const int* bias_ids;     /* [S][n_bias], or NULL with n_bias 0 */
+    const float* bias;
+    int n_bias;
+} w4_logit_rules;
+w4_status w4_logits_adjust(const w4_logit_rules* u, const void* logits, int type, long long ld, int R, const int* row_start,
+                           const int* drafts, const unsigned long long* mask, const unsigned* allowed, void* out,
+                           long long ld_out, unsigned flags, w4_stream_t s);
+
+/* ------------------------------------------------------------------------
  * A chain of per-row INT4 decode linears in one launch (a decode step's
  * linear set).  Linear i computes exactly what w4a8_linear computes for
  * descs[i]; linear i+1 reads its x only after every output of linear i is
