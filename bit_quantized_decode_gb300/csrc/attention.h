@@ -55,6 +55,8 @@ cudaError_t launch_rope_table(const double* inv_freq, double factor, double scal
 // ---------------------------------------------- tree attention (attn_tree.cu)
 constexpr int kAtUnit = 16;                     // cached tokens of a unit of work
 constexpr int kAtRows = 16;                     // query rows of a tile: (token, head of the group)
+constexpr int kAtTcUnit = 64;                   // the same of the tensor-core kernel (attn_tc.cu)
+constexpr int kAtTcRows = 128;
 constexpr int kAtMaxSeq = 1024;
 constexpr int kAtMaxTok = 64;                   // drafted tokens of a sequence: the bits of a mask
 constexpr int kAtMaxBlocks = 160;
@@ -70,12 +72,17 @@ struct AttnArgs {
     int ytype;
     long long* head;          // workspace: share, then B + 1 prefix sums of units
     float* part;              // workspace: two partial results per block
+    int part_rows;            // rows of one
     unsigned* err;
 };
 __host__ __device__ inline size_t attn_head_bytes(int B) { return (8 * (static_cast<size_t>(B) + 2) + 127) / 128 * 128; }
 // A partial result: running maxima, sums, and rows of D.
 __host__ __device__ inline size_t attn_part_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
 cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s);
+cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s);
+// Joins the partial results of either kernel (tiles of `rows` rows, units of `unit` tokens).
+cudaError_t launch_attn_join(const AttnArgs& a, int rows, int unit, cudaStream_t s);
+cudaError_t encode_kv_map(CUtensorMap* map, const AttnArgs& a, const void* base, int box_bytes, int box_rows);
 
 // ------------------------------------------------------ logits (logits.cu)
 constexpr int kLgThreads = 256;

@@ -62,9 +62,23 @@ KvView view(const w4_kv_cache* c)
 }
 BatchView view(const w4_kv_batch* b) { return BatchView{b->table, b->ctx, b->q_start, b->B, b->max_pages, b->max_tokens}; }
 
-size_t attention_workspace(const w4_kv_cache* c, const w4_kv_batch* b)
+// Which kernel a call takes, and the rows of its partial results.
+struct AttnPlan {
+    bool tc;
+    int part_rows;
+};
+AttnPlan plan_attention(const w4_kv_batch* b, int T, int G)
 {
-    return attn_head_bytes(b->B) + static_cast<size_t>(kAtMaxBlocks) * 2 * attn_part_floats(kAtRows, c->D) * 4;
+    const int rows = (b->max_tokens < T ? b->max_tokens : T) * G;
+    AttnPlan p;
+    p.tc = rows > kAtRows;
+    const int tile = p.tc ? kAtTcRows : kAtRows;
+    p.part_rows = rows < tile ? (rows + 7) / 8 * 8 : tile;   // (results begin on 16-byte boundaries)
+    return p;
+}
+size_t attention_workspace(const w4_kv_cache* c, const w4_kv_batch* b, const AttnPlan& p)
+{
+    return attn_head_bytes(b->B) + static_cast<size_t>(kAtMaxBlocks) * 2 * attn_part_floats(p.part_rows, c->D) * 4;
 }
 
 }  // namespace
@@ -126,7 +140,7 @@ w4_status w4_kv_append(const w4_kv_cache* c, const w4_kv_batch* b, const w4_rope
 size_t w4_tree_attention_workspace_bytes(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq)
 {
     if (check_call(c, b, T, Hq) != W4_OK || b->max_tokens > W4_MAX_DRAFTS || T == 0 || b->B == 0) return 0;
-    return attention_workspace(c, b);
+    return attention_workspace(c, b, plan_attention(b, T, Hq / c->Hkv));
 }
 
 w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const void* q, int q_type, int T, int Hq,
@@ -142,7 +156,8 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     if (T == 0 || b->B == 0) return W4_OK;
     r = check_call_pointers(c, b);
     if (r == W4_ERR_INVALID_ARG || !q || !y || !workspace) return W4_ERR_INVALID_ARG;
-    if (ws_bytes < attention_workspace(c, b)) return W4_ERR_UNSUPPORTED_SHAPE;
+    const AttnPlan p = plan_attention(b, T, Hq / c->Hkv);
+    if (ws_bytes < attention_workspace(c, b, p)) return W4_ERR_UNSUPPORTED_SHAPE;
     if (r != W4_OK || !aligned(q, 16) || !aligned(y, 16) || !aligned(mask, 8) || !aligned(workspace, 16)) return W4_ERR_MISALIGNED;
     DeviceFacts d;
     if (!device_facts(&d)) return W4_ERR_CUDA;
@@ -159,9 +174,14 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     a.ytype = y_type;
     a.head = static_cast<long long*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_head_bytes(b->B));
+    a.part_rows = p.part_rows;
     a.err = d.err;
     const int grid = d.sms < kAtMaxBlocks ? d.sms : kAtMaxBlocks;
-    return cuda_status(launch_attn_tree(a, q_type, grid, (flags & W4_FLAG_PDL) != 0, reinterpret_cast<cudaStream_t>(s)));
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+    const bool pdl = (flags & W4_FLAG_PDL) != 0;
+    const cudaError_t e = p.tc ? launch_attn_tc(a, q_type, grid, pdl, cs) : launch_attn_tree(a, q_type, grid, pdl, cs);
+    if (e != cudaSuccess) return W4_ERR_CUDA;
+    return cuda_status(p.tc ? launch_attn_join(a, kAtTcRows, kAtTcUnit, cs) : launch_attn_join(a, kAtRows, kAtUnit, cs));
 }
 
 w4_status w4_logits_adjust(const w4_logit_rules* u, const void* logits, int type, long long ld, int R, const int* row_start,

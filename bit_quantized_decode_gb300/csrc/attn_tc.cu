@@ -1,0 +1,689 @@
+// Attention of many rows over a paged cache on the 5th-generation tensor
+// cores: a wide draft tree times a key head's group gives up to some hundred
+// rows for the same keys, more than mma.sync keeps up with while the cache
+// streams (see attn_tree.cu, which takes calls of few rows and defines the
+// operation and the layout of the work).
+//
+// A block takes a tile of 128 rows of one (sequence, key head) over 64 cached
+// tokens at a time:
+//   S = Q K^T   tcgen05.mma 128 x 64 x D: Q and K in shared memory as TMA's
+//               128-byte swizzle lays them, S in tensor memory (two buffers, so
+//               that the next product runs during the softmax);
+//   softmax     one thread per row (tensor-memory lane): maximum, exponentials
+//               and sum need no exchange.  The maximum in use is raised only when it
+//               is passed by more than 2^8: probabilities are then at most 256
+//               (exact scaling, the sums stay in fp32), and the output, which
+//               lies in tensor memory, is rescaled a few times per segment
+//               instead of once per tile;
+//   O += P V    P goes back to tensor memory in 16 bits (two or three parts for
+//               an fp32 output) and is the A operand; V as it lies, 64 values of a token in a row,
+//               is an operand with its columns contiguous.
+// Warps: one orders copies, one issues MMAs, four take the softmax; INT8
+// caches add four that widen codes to 16 bits (exact) in shared memory.  All
+// are joined by mbarriers with bounded waits.
+#include "attn_tree.cuh"
+#include "gemm_w8.cuh"
+
+namespace w4k {
+namespace {
+
+constexpr int kTcRows = kAtTcRows, kTcUnit = kAtTcUnit;
+constexpr float kRaise = 8.0f;                  // log2 of what a probability may reach
+
+template <int D, int CT>
+struct Tc {
+    static constexpr bool kI8 = CT == T_I8;
+    static constexpr int kBoxes = D / 64;                     // 128-byte column groups of 16-bit values
+    static constexpr int kQ = kTcRows * D * 2;
+    static constexpr int kHalf = kTcUnit * D * 2;             // a tile's keys (or values) in 16 bits
+    static constexpr int kRaw = 2 * kTcUnit * D;              // a tile's codes
+    static constexpr int kStages = kI8 ? (D == 64 ? 10 : D == 128 ? 5 : 2) : (D == 64 ? 8 : D == 128 ? 5 : 2);   // copies
+    static constexpr int kConv = kI8 ? (D == 256 ? 1 : 2) : kStages;   // 16-bit tiles
+    static constexpr int kMeta = kStages + kConv;             // tiles between a copy's order and its softmax, at most
+    static constexpr int kThreads = kI8 ? 384 : 256;
+    static constexpr int kPBufs = D == 256 ? 1 : 2;
+    static constexpr int kCols = 512;
+    static constexpr int cS = D, cP = D + 2 * kTcUnit;        // tensor-memory columns of S and P; O begins at 0
+    // shared memory
+    static constexpr int oQ = 0;
+    static constexpr int oKv = kQ;                            // [kConv] keys, values
+    static constexpr int oRaw = oKv + kConv * 2 * kHalf;
+    static constexpr int oScale = oRaw + (kI8 ? kStages * kRaw : 0);        // [kMeta][2][64]
+    static constexpr int oMeta = oScale + (kI8 ? kMeta * 2 * kTcUnit * 4 : 0);   // [kMeta]: which sixteenths of a tile have a page
+    static constexpr int oBars = (oMeta + kMeta * 4 + 7) / 8 * 8;
+    static constexpr int nBars = 2 * kStages + 4 * kConv + 8;
+    static constexpr int oMisc = oBars + nBars * 8;           // tensor memory's base, failure flag, odd values flag
+    static constexpr int oWarpSum = oMisc + 16;
+    static constexpr int oPre = oWarpSum + kThreads / 32 * 8;
+    static constexpr int smem(int B) { return oPre + (B + 1) * 8 + 1024; }
+    static_assert(smem(kAtMaxSeq) <= 232448, "shared memory of a block");
+    // (all of tensor memory: no other block of this library that takes some may be on the SM; the least of them has 106 KB)
+    static_assert(smem(1) > 123 * 1024, "alone with its tensor memory on an SM");
+};
+
+// Shared-memory matrix descriptors with the 128-byte swizzle.  Rows of 128 bytes
+// (64 values of K): groups of eight rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t a)
+{
+    return static_cast<uint64_t>((a & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+// Rows of 128 bytes that run along N: groups of eight K are 1024 bytes apart, groups of 64 N `lbo`.
+__device__ __forceinline__ uint64_t desc_cols(uint32_t a, uint32_t lbo)
+{
+    return static_cast<uint64_t>((a & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t tc_pair(float a, float b)
+{
+    if constexpr (T == T_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <int T>
+__device__ __forceinline__ float2 tc_unpair(uint32_t u)
+{
+    if constexpr (T == T_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+template <int D, int CT, int QT, bool kWide>
+__global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs A)
+{
+    using C = Tc<D, CT>;
+    constexpr bool kI8 = C::kI8;
+    constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
+    constexpr int kParts = !kWide ? 1 : PT == T_F16 ? 2 : 3;  // of a probability: 11 or 8 bits each
+    constexpr int S = C::kStages, NC = C::kConv;
+    extern __shared__ uint8_t raw_s[];
+    uint8_t* smem = raw_s + ((1024u - (smem_u32(raw_s) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bars = smem_u32(smem + C::oBars);
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * S;                    // codes (INT8)
+    const uint32_t k_full = raw_empty + 8 * S, k_empty = k_full + 8 * NC;            // 16-bit keys
+    const uint32_t v_full = k_empty + 8 * NC, v_empty = v_full + 8 * NC;             // and values
+    const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8;
+    uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::oMisc);
+    volatile uint32_t* dead_s = misc + 1;
+    volatile uint32_t* odd_s = misc + 2;
+    volatile uint32_t* meta_s = reinterpret_cast<volatile uint32_t*>(smem + C::oMeta);
+    float* scale_s = reinterpret_cast<float*>(smem + C::oScale);
+    long long* pre_s = reinterpret_cast<long long*>(smem + C::oPre);
+
+    if (tid == 0) {
+        for (int k = 0; k < S; ++k) {
+            mbar_init(raw_full + 8 * k, 1);
+            mbar_init(raw_empty + 8 * k, 4);
+        }
+        for (int k = 0; k < NC; ++k) {
+            mbar_init(k_full + 8 * k, kI8 ? 4 : 1);
+            mbar_init(k_empty + 8 * k, 1);
+            mbar_init(v_full + 8 * k, kI8 ? 4 : 1);
+            mbar_init(v_empty + 8 * k, 1);
+        }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(s_full + 8 * k, 1);
+            mbar_init(p_full + 8 * k, 4);
+            mbar_init(pv_done + 8 * k, 1);
+        }
+        mbar_init(q_full, 4);
+        mbar_init(wg_bar, 4);
+        fence_mbar_init();
+        *dead_s = 0u;
+        *odd_s = 0u;
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    seq_prefix<C::kThreads>(A, kTcRows, kTcUnit, pre_s, reinterpret_cast<long long*>(smem + C::oWarpSum));
+    const long long total = pre_s[A.b.B];
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < 1) share = 1;
+    if (blockIdx.x == 0) {                      // for the joining launch
+        if (tid == 0) A.head[0] = share;
+        for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[1 + b] = pre_s[b];
+    }
+    const long long us = min(static_cast<long long>(blockIdx.x) * share, total), ue = min(us + share, total);
+    if (us >= ue) return;
+    __syncwarp();
+    if (warp == 1) {
+        tmem_alloc(smem_u32(misc), C::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = misc[0];
+    auto fail = [&]() {
+        *dead_s = 1u;
+        if (A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- copies
+        const int per = min(A.c.page, kTcUnit), boxes = kTcUnit / per;       // tokens of a copy, copies of a tile
+        int it = 0;
+        bool ok = true;
+        for (long long begin = us; begin < ue && ok;) {
+            const Segment sg = find_segment(A, pre_s, begin, kTcRows, kTcUnit);
+            const long long end = min(sg.u0 + sg.units, ue);
+            for (long long u = begin; u < end; ++u, ++it) {
+                const int t0 = static_cast<int>(u - sg.u0) * kTcUnit;
+                int page = -1;
+                const int t = t0 + lane * per;
+                if (lane < boxes && t < sg.f.len)
+                    page = __ldg(A.b.table + static_cast<size_t>(sg.b) * A.b.max_pages + (t >> A.c.lg));
+                const bool there = page >= 0 && page < A.c.pages;
+                const uint32_t have = __ballot_sync(0xffffffffu, there);
+                const int z = there ? page * A.c.Hkv + sg.h : 0, y = t & (A.c.page - 1);
+                const int n = __popc(have);
+                uint32_t sixteenths = 0;
+                for (int k = 0; k < boxes; ++k)
+                    if (have >> k & 1u) sixteenths |= ((1u << (per / 16)) - 1u) << (k * (per / 16));
+                const int st = it % S;
+                const uint32_t ph = static_cast<uint32_t>(it / S - 1) & 1u;
+                if constexpr (kI8) {
+                    if (it >= S) ok = warp_wait(raw_empty + 8 * st, ph);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        meta_s[it % C::kMeta] = sixteenths;
+                        mbar_arrive_expect_tx(raw_full + 8 * st, static_cast<uint32_t>(n * per * 2 * (D + 4)));
+                    }
+                    __syncwarp();
+                    if (there) {
+                        const uint32_t dst = smem_u32(smem + C::oRaw) + st * C::kRaw, bar = raw_full + 8 * st;
+                        const size_t at = static_cast<size_t>(z) * A.c.page + y;
+                        bulk_copy(dst + lane * per * D, static_cast<const uint8_t*>(A.c.k) + at * D, per * D, bar);
+                        bulk_copy(dst + kTcUnit * D + lane * per * D, static_cast<const uint8_t*>(A.c.v) + at * D, per * D, bar);
+                        const uint32_t sc = smem_u32(scale_s + (it % C::kMeta) * 2 * kTcUnit + lane * per);
+                        bulk_copy(sc, A.c.ks + at, per * 4, bar);
+                        bulk_copy(sc + kTcUnit * 4, A.c.vs + at, per * 4, bar);
+                    }
+                } else {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t bar = (half ? v_full : k_full) + 8 * st;
+                        if (it >= S) ok = warp_wait((half ? v_empty : k_empty) + 8 * st, ph);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            if (half == 0) meta_s[it % C::kMeta] = sixteenths;
+                            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * per * D * 2));
+                        }
+                        __syncwarp();
+                        if (there) {
+                            const uint32_t dst = smem_u32(smem + C::oKv) + st * 2 * C::kHalf + half * C::kHalf + lane * per * 128;
+#pragma unroll
+                            for (int x = 0; x < C::kBoxes; ++x)
+                                tma_load_3d(dst + x * kTcUnit * 128, half ? &A.vmap : &A.kmap, 64 * x, y, z, bar);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) {                  // (a tile whose keys alone were ordered: they land, too)
+                        warp_wait(k_full + 8 * st, static_cast<uint32_t>(it / S) & 1u);
+                        break;
+                    }
+                }
+                __syncwarp();
+            }
+            begin = end;
+        }
+        if (!ok && lane == 0) fail();
+        // every copy has landed before the block ends (also after a failure)
+        for (int k = max(0, it - S); k < it; ++k) {
+            const uint32_t ph = static_cast<uint32_t>(k / S) & 1u;
+            if constexpr (kI8) {
+                if (!warp_wait(raw_full + 8 * (k % S), ph)) break;
+            } else {
+                if (!warp_wait(k_full + 8 * (k % S), ph) || !warp_wait(v_full + 8 * (k % S), ph)) break;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t qf = QT == T_BF16 ? 1u : 0u, pf = PT == T_BF16 ? 1u : 0u;
+        constexpr uint32_t iqk = (1u << 4) | (qf << 7) | (qf << 10) | (static_cast<uint32_t>(kTcUnit >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
+        constexpr uint32_t ipv = (1u << 4) | (pf << 7) | (pf << 10) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
+        const uint32_t q_a = smem_u32(smem + C::oQ), kv_a = smem_u32(smem + C::oKv);
+        int it = 0, pieces = 0;
+        bool ok = true;
+        auto scores = [&](int i) {              // S of tile i
+            ok = ok && warp_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t k_a = kv_a + (i % NC) * 2 * C::kHalf;
+                const uint32_t d = tb + C::cS + (i & 1) * kTcUnit;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    mma_ss(d, desc_rows(q_a + (j >> 2) * kTcRows * 128 + (j & 3) * 32), desc_rows(k_a + (j >> 2) * kTcUnit * 128 + (j & 3) * 32),
+                           iqk, j > 0);
+                tc_commit(k_empty + 8 * (i % NC));
+                tc_commit(s_full + 8 * (i & 1));
+            }
+            __syncwarp();
+        };
+        for (long long begin = us; begin < ue && ok; ++pieces) {
+            const Segment sg = find_segment(A, pre_s, begin, kTcRows, kTcUnit);
+            const long long end = min(sg.u0 + sg.units, ue);
+            const int n = static_cast<int>(end - begin);
+            ok = warp_wait(q_full, static_cast<uint32_t>(pieces) & 1u);
+            scores(it);
+            for (int k = 0; k < n && ok; ++k, ++it) {
+                if (k + 1 < n) scores(it + 1);
+                ok = ok && warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u) &&
+                     warp_wait(v_full + 8 * (it % NC), static_cast<uint32_t>(it / NC) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t v_a = kv_a + (it % NC) * 2 * C::kHalf + C::kHalf;
+                    const uint32_t p = tb + C::cP + (it % C::kPBufs) * 32 * kParts;
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                        for (int j = 0; j < kTcUnit / 16; ++j)
+                            mma_ts(tb, p + 32 * part + 8 * j, desc_cols(v_a + j * 2048, kTcUnit * 128), ipv);
+                    tc_commit(v_empty + 8 * (it % NC));
+                    tc_commit(pv_done + 8 * (it & 1));
+                }
+                __syncwarp();
+            }
+            begin = end;
+        }
+        if (!ok && lane == 0) fail();
+        // every MMA has completed before the tensor memory is freed
+        if (it > 0) warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
+    } else if (warp >= 4 && warp < 8) {
+        // --------------------------------------------------------- softmax
+        const int row = tid - 128;
+        const uint32_t tl = tb + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        int it = 0;
+        uint32_t wg_phase = 0;
+        bool ok = true;
+        auto wg_sync = [&]() {                  // the four warps, with a bounded wait
+            __syncwarp();
+            if (lane == 0) mbar_arrive(wg_bar);
+            const bool all = warp_wait(wg_bar, wg_phase & 1u);
+            ++wg_phase;
+            return all;
+        };
+        for (long long begin = us; begin < ue && ok;) {
+            const Segment sg = find_segment(A, pre_s, begin, kTcRows, kTcUnit);
+            const long long end = min(sg.u0 + sg.units, ue);
+            const int rows = min(kTcRows, sg.f.n * A.G - sg.tile * kTcRows);
+            const bool have = row < rows;
+            const int rr = sg.tile * kTcRows + (have ? row : 0), tok = rr / A.G, tq = sg.f.q0 + tok;
+            const size_t at = (static_cast<size_t>(tq) * A.Hq + sg.h * A.G + (rr - tok * A.G)) * D;
+            unsigned long long see = A.mask != nullptr ? __ldg(A.mask + tq) : (2ull << tok) - 1ull;
+            const int drafts = sg.f.len - sg.f.ctx;           // at most 64
+            if (drafts < 64) see &= (1ull << drafts) - 1ull;
+            // the row's query; the products of the last piece that read the old one are done
+            {
+                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at);
+                uint8_t* d = smem + C::oQ + row * 128;
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    const uint4 v = have ? __ldg(q + j) : make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(d + (j >> 3) * kTcRows * 128 + (((j & 7) ^ (row & 7)) << 4)) = v;
+                }
+                const uint32_t zero[16] = {};
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) tmem_st16(tl + 16 * j, zero);
+                tmem_wait_st();
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            float m = neg_inf(), l = 0.0f;
+            for (long long u = begin; u < end; ++u, ++it) {
+                ok = warp_wait(s_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+                float s[kTcUnit];
+                {
+                    uint32_t r0[16], r1[16];
+#pragma unroll
+                    for (int j = 0; j < kTcUnit / 32; ++j) {
+                        const uint32_t a = tl + C::cS + (it & 1) * kTcUnit + 32 * j;
+                        tmem_ld16x2(a, r0, a + 16, r1);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            s[32 * j + k] = __uint_as_float(r0[k]);
+                            s[32 * j + 16 + k] = __uint_as_float(r1[k]);
+                        }
+                    }
+                }
+                const int t0 = static_cast<int>(u - sg.u0) * kTcUnit;
+                const uint32_t there = meta_s[it % C::kMeta];
+                const bool special = t0 + kTcUnit > sg.f.ctx || there != 15u;
+                unsigned long long vis = ~0ull;
+                if constexpr (kI8) {
+                    const float4* ks = reinterpret_cast<const float4*>(scale_s + (it % C::kMeta) * 2 * kTcUnit);
+#pragma unroll
+                    for (int j = 0; j < kTcUnit / 4; ++j) {
+                        const float4 k4 = ks[j];
+                        s[4 * j] *= k4.x;
+                        s[4 * j + 1] *= k4.y;
+                        s[4 * j + 2] *= k4.z;
+                        s[4 * j + 3] *= k4.w;
+                    }
+                }
+                if (special) {
+                    // places before the drafts, the row's drafts, of pages that are there
+                    const int o = sg.f.ctx - t0;
+                    const unsigned long long old = o >= 64 ? ~0ull : o > 0 ? (1ull << o) - 1ull : 0ull;
+                    const unsigned long long own = o >= 64 || o <= -64 ? 0ull : o >= 0 ? see << o : see >> -o;
+                    vis = 0ull;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (there >> k & 1u) vis |= 0xffffull << (16 * k);
+                    vis &= old | own;
+#pragma unroll
+                    for (int j = 0; j < kTcUnit; ++j)
+                        if (!(vis >> j & 1ull)) s[j] = neg_inf();
+                }
+                float top = s[0];
+#pragma unroll
+                for (int j = 1; j < kTcUnit; ++j) top = fmaxf(top, s[j]);
+                top *= A.scale;
+                const bool raise = top > m + kRaise || (m == neg_inf() && top > m);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float was = m;
+                    if (raise) m = top;
+                    const float f = was == neg_inf() ? 0.0f : exp2_fast(was - m);
+                    l *= f;
+                    if (u > begin) {            // (before the first tile the output is zero)
+                        ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int j = 0; j < D / 16; ++j) {
+                            uint32_t r[16];
+                            tmem_ld16(tl + 16 * j, r);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
+                            tmem_st16(tl + 16 * j, r);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                const float base = m == neg_inf() ? 0.0f : -m;
+                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kTcUnit; j += 2) {
+                    s[j] = exp2_fast(__fmaf_rn(s[j], A.scale, base));
+                    s[j + 1] = exp2_fast(__fmaf_rn(s[j + 1], A.scale, base));
+                    sum0 += s[j];
+                    sum1 += s[j + 1];
+                }
+                l += sum0 + sum1;
+                if constexpr (kI8) {
+                    const float4* vs = reinterpret_cast<const float4*>(scale_s + (it % C::kMeta) * 2 * kTcUnit + kTcUnit);
+#pragma unroll
+                    for (int j = 0; j < kTcUnit / 4; ++j) {
+                        const float4 v4 = vs[j];
+                        s[4 * j] *= v4.x;
+                        s[4 * j + 1] *= v4.y;
+                        s[4 * j + 2] *= v4.z;
+                        s[4 * j + 3] *= v4.w;
+                    }
+                    if (special) {
+#pragma unroll
+                        for (int j = 0; j < kTcUnit; ++j)
+                            if (!(vis >> j & 1ull)) s[j] = 0.0f;
+                    }
+                } else if (special) {
+                    // Values that nothing may see: zeros in their stead.  A draft's infinities and NaN would reach the rows
+                    // that do not see it (0 times them): such a tile's drafts are added row by row.
+                    ok = warp_wait(v_full + 8 * (it % NC), static_cast<uint32_t>(it / NC) & 1u);
+                    if (!ok) break;
+                    uint8_t* v = smem + C::oKv + (it % NC) * 2 * C::kHalf + C::kHalf;
+                    const uint32_t top16 = CT == T_F16 ? 0x7c00u : 0x7f80u;
+                    auto word = [&](int t, int c) { return reinterpret_cast<uint4*>(v + (c >> 3) * kTcUnit * 128 + t * 128 + (((c & 7) ^ (t & 7)) << 4)); };
+                    const int from = min(max(sg.f.ctx - t0, 0), kTcUnit);
+                    bool odd = false;
+                    for (int k = row; k < kTcUnit * (D / 8); k += 128) {
+                        const int t = k / (D / 8);
+                        uint4* w = word(t, k % (D / 8));
+                        if (t0 + t >= sg.f.len || !(there >> (t >> 4) & 1u)) {
+                            *w = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (t >= from) {
+                            const uint32_t x[4] = {w->x, w->y, w->z, w->w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) odd |= (x[i] & top16) == top16 || (x[i] >> 16 & top16) == top16;
+                        }
+                    }
+                    if (odd) *odd_s = 1u;
+                    ok = wg_sync();
+                    if (!ok) break;
+                    const bool plain = *odd_s != 0u;
+                    if (plain) {
+                        // (the last product on this output is done: as for the rescaling)
+                        if (u > begin) ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; c += 2) {
+                            uint32_t r[16];
+                            tmem_ld16(tl + 8 * c, r);
+#pragma unroll
+                            for (int j = 0; j < kTcUnit; ++j) {
+                                if (j >= from && (vis >> j & 1ull)) {
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        const uint4 w = *word(j, c + h);
+                                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const float2 f = tc_unpair<CT>(x[i]);
+                                            r[8 * h + 2 * i] = __float_as_uint(__uint_as_float(r[8 * h + 2 * i]) + s[j] * f.x);
+                                            r[8 * h + 2 * i + 1] = __float_as_uint(__uint_as_float(r[8 * h + 2 * i + 1]) + s[j] * f.y);
+                                        }
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                            tmem_st16(tl + 8 * c, r);
+                        }
+                        tmem_wait_st();
+                        ok = wg_sync();         // every row has read the drafts
+                        if (!ok) break;
+                        for (int k = row; k < kTcUnit * (D / 8); k += 128)
+                            if (k / (D / 8) >= from) *word(k / (D / 8), k % (D / 8)) = make_uint4(0u, 0u, 0u, 0u);
+                        if (row == 0) *odd_s = 0u;
+                    }
+                    ok = wg_sync();             // (the flag was read, or is down, before a later tile sets it)
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                }
+                if (it >= C::kPBufs) {          // P's buffer has been read
+                    const int b = it - C::kPBufs;
+                    ok = warp_wait(pv_done + 8 * (b & 1), static_cast<uint32_t>(b >> 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                const uint32_t p = tl + C::cP + (it % C::kPBufs) * 32 * kParts;
+#pragma unroll
+                for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int j = 32 * h + 2 * k;
+                            w[k] = tc_pair<PT>(s[j], s[j + 1]);
+                            if (part + 1 < kParts) {
+                                const float2 f = tc_unpair<PT>(w[k]);
+                                s[j] -= f.x;
+                                s[j + 1] -= f.y;
+                            }
+                        }
+                        tmem_st16(p + 32 * part + 16 * h, w);
+                    }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * (it & 1));
+            }
+            if (ok) ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
+            if (!ok) {
+                if (lane == 0) fail();
+                break;
+            }
+            tc_fence_after();
+            // ------------------------------------------------- the row's result
+            const bool whole = begin == sg.u0 && end == sg.u0 + sg.units;
+            float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
+            if (have && !whole) {
+                part[row] = m;
+                part[A.part_rows + row] = l;
+            }
+            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+#pragma unroll 1
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t r[16];
+                tmem_ld16(tl + 16 * j, r);
+                if (have) {
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]) * inv;
+                if (!whole || A.ytype == T_F32) {
+                    float4* d = reinterpret_cast<float4*>(whole ? static_cast<float*>(A.y) + at + 16 * j
+                                                                : part + 2 * A.part_rows + static_cast<size_t>(row) * D + 16 * j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) d[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                } else {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        w[k] = A.ytype == T_F16 ? tc_pair<T_F16>(v[2 * k], v[2 * k + 1]) : tc_pair<T_BF16>(v[2 * k], v[2 * k + 1]);
+                    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.y) + at + 16 * j);
+                    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+                }
+                __syncwarp();
+            }
+            __syncwarp();
+            begin = end;
+        }
+    } else if (kI8 && warp >= 8) {
+        // ---------------------------------------------------- codes to 16 bits
+        const int w = tid - 256;
+        const long long n = ue - us;
+        bool ok = true;
+        for (int it = 0; it < n && ok; ++it) {
+            const int st = it % S, cv = it % NC;
+            const uint32_t ph = static_cast<uint32_t>(it / NC - 1) & 1u;
+            ok = warp_wait(raw_full + 8 * st, static_cast<uint32_t>(it / S) & 1u);
+            const uint8_t* src = smem + C::oRaw + st * C::kRaw;
+            uint8_t* dst = smem + C::oKv + cv * 2 * C::kHalf;
+#pragma unroll 1
+            for (int half = 0; half < 2 && ok; ++half) {
+                if (it >= NC) ok = warp_wait((half ? v_empty : k_empty) + 8 * cv, ph);
+                if (!ok) break;
+#pragma unroll 2
+                for (int k = w; k < kTcUnit * D / 16; k += 128) {
+                    const int t = k / (D / 16), c = k % (D / 16);                   // sixteen codes: two 16-byte words
+                    const uint4 q = *reinterpret_cast<const uint4*>(src + half * kTcUnit * D + 16 * k);
+                    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (half == 0 && QT == T_F16) i8_to_f16(x[i], h[2 * i], h[2 * i + 1]);
+                        else i8_to_bf16(x[i], h[2 * i], h[2 * i + 1]);
+                    }
+                    uint8_t* d = dst + half * C::kHalf + (c >> 2) * kTcUnit * 128 + t * 128;
+                    const int a = ((2 * c) & 7) ^ (t & 7), b = a ^ 1;
+                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                    // (every other column group the other way round: eight lanes on eight different words)
+                    const bool flip = (c >> 2) & 1;
+                    *reinterpret_cast<uint4*>(d + ((flip ? b : a) << 4)) = flip ? hi : lo;
+                    *reinterpret_cast<uint4*>(d + ((flip ? a : b) << 4)) = flip ? lo : hi;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive((half ? v_full : k_full) + 8 * cv);
+            }
+            if (ok && lane == 0) mbar_arrive(raw_empty + 8 * st);
+            __syncwarp();
+        }
+        if (!ok && lane == 0) fail();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tb, C::kCols);
+}
+
+template <int D, int CT, int QT, bool kWide>
+cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+{
+    using C = Tc<D, CT>;
+    auto kern = attn_tc_kernel<D, CT, QT, kWide>;
+    static SmemLimit limit;
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, C::smem(kAtMaxSeq));
+    if constexpr (CT != T_I8) {
+        const int rows = a.c.page < kTcUnit ? a.c.page : kTcUnit;
+        if (e == cudaSuccess) e = encode_kv_map(&a.kmap, a, a.c.k, 128, rows);
+        if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, 128, rows);
+    }
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::smem(a.b.B);
+    cfg.stream = s;
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int D, int CT, int QT>
+cudaError_t launch_w(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+{
+    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, pdl, s) : launch<D, CT, QT, false>(a, grid, pdl, s);
+}
+
+template <int D>
+cudaError_t launch_d(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+{
+    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, pdl, s);
+    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, pdl, s);
+    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, pdl, s) : launch_w<D, T_I8, T_BF16>(a, grid, pdl, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+{
+    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, pdl, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, pdl, s)
+                                                                            : launch_d<256>(a, qtype, grid, pdl, s);
+}
+
+}  // namespace w4k

@@ -120,18 +120,6 @@ __device__ __forceinline__ float2 unpair16(uint32_t u)
     else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// Four int8 -> four bf16, exactly: the low seven bits on 128.0 (whose last place is 1), less 128 or, for a negative code,
-// 256.
-__device__ __forceinline__ void i8_to_bf16(uint32_t c, uint32_t& h01, uint32_t& h23)
-{
-    const uint32_t m = c & 0x7f7f7f7fu, n = c & 0x80808080u;
-    const uint32_t a = __byte_perm(m, 0x43434343u, 0x4140), b = __byte_perm(m, 0x43434343u, 0x4342);
-    const uint32_t s = __byte_perm(n, 0x43434343u, 0x4140), t = __byte_perm(n, 0x43434343u, 0x4342);
-    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&s));
-    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&t));
-    h01 = *reinterpret_cast<const uint32_t*>(&x);
-    h23 = *reinterpret_cast<const uint32_t*>(&y);
-}
 template <int T>
 __device__ __forceinline__ void codes16(uint32_t c, uint32_t& h01, uint32_t& h23)
 {
@@ -512,10 +500,10 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             __syncthreads();
         }
         const bool whole = begin == sg.u0 && end == sg.u0 + sg.units;
-        float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(kAtRows, D);
+        float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
         if (!whole && tid < rows) {
             part[tid] = fin_s[tid];
-            part[kAtRows + tid] = fin_s[kAtRows + tid];
+            part[A.part_rows + tid] = fin_s[kAtRows + tid];
         }
         for (int k = tid; k < rows * (D / 4); k += C::kThreads) {
             const int r = k / (D / 4), d = k % (D / 4) * 4;
@@ -526,7 +514,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                 v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
             }
             if (!whole) {
-                *reinterpret_cast<float4*>(part + 2 * kAtRows + r * D + d) = v;
+                *reinterpret_cast<float4*>(part + 2 * A.part_rows + r * D + d) = v;
             } else {
                 const float sum = fin_s[kAtRows + r], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 const int rr = sg.tile * kAtRows + r, tok = rr / A.G;
@@ -571,7 +559,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int j0 = static_cast<int>(u0 / share), j1 = static_cast<int>((u0 + units - 1) / share);
     if (j0 == j1) return;                       // one block's: written
     const int pieces = j1 - j0 + 1;
-    const size_t pf = attn_part_floats(tile_rows, D);
+    const size_t pf = attn_part_floats(A.part_rows, D);
     // (a block's first piece is in its first place; a piece that begins within the block in the second)
     auto part = [&](int k) {
         const int j = j0 + k;
@@ -592,7 +580,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     for (int k = tid; k < pieces; k += kJoinThreads) {
         const float w = exp2_fast(w_s[k] - base);
         w_s[k] = w;
-        sum += w * part(k)[tile_rows + row];
+        sum += w * part(k)[A.part_rows + row];
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -603,7 +591,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     float acc[kV] = {};
 #pragma unroll 4
     for (int k = warp; k < pieces; k += kJoinThreads / 32) {
-        const float* p = part(k) + 2 * tile_rows + static_cast<size_t>(row) * D;
+        const float* p = part(k) + 2 * A.part_rows + static_cast<size_t>(row) * D;
         const float w = w_s[k];
 #pragma unroll
         for (int v = 0; v < kV; ++v) acc[v] += w * __ldcg(p + 32 * v + lane);
@@ -618,33 +606,6 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         for (int w = 0; w < kJoinThreads / 32; ++w) v += red_s[w][d];
         store_typed(A.y, A.ytype, (static_cast<size_t>(t) * A.Hq + head) * D + d, v * inv);
     }
-}
-
-cudaError_t encode_kv_map(CUtensorMap* map, const AttnArgs& a, const void* base, int box_bytes, int box_rows)
-{
-    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static std::atomic<void*> cached{nullptr};
-    void* fn = cached.load(std::memory_order_acquire);
-    if (fn == nullptr) {
-        cudaDriverEntryPointQueryResult got;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got);
-        if (e != cudaSuccess) return e;
-        if (got != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
-        cached.store(fn, std::memory_order_release);
-    }
-    const cuuint64_t eb = a.c.type == T_I8 ? 1 : 2;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.D), static_cast<cuuint64_t>(a.c.page),
-                                static_cast<cuuint64_t>(a.c.pages) * a.c.Hkv};
-    const cuuint64_t strides[2] = {a.c.D * eb, a.c.D * eb * a.c.page};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / eb), static_cast<cuuint32_t>(box_rows), 1};
-    const cuuint32_t ones[3] = {1, 1, 1};
-    const CUresult r = reinterpret_cast<Encode>(fn)(
-        map, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides,
-        box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, bool pdl)
@@ -673,14 +634,7 @@ cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
     cfg.dynamicSmemBytes = C::smem(a.b.B);
     cfg.stream = s;
     dependent(cfg, attr, pdl);
-    e = cudaLaunchKernelEx(&cfg, kern, a);
-    if (e != cudaSuccess || grid == 1) return e;
-    cudaLaunchConfig_t join = {};
-    join.gridDim = dim3(static_cast<unsigned>(a.T) * static_cast<unsigned>(a.Hq));
-    join.blockDim = dim3(kJoinThreads);
-    join.stream = s;
-    dependent(join, attr, true);
-    return cudaLaunchKernelEx(&join, attn_join_kernel<D>, a, kAtRows, kAtUnit);
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int D, int CT, int QT>
@@ -698,6 +652,45 @@ cudaError_t launch_d(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
 }
 
 }  // namespace
+
+cudaError_t encode_kv_map(CUtensorMap* map, const AttnArgs& a, const void* base, int box_bytes, int box_rows)
+{
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<void*> cached{nullptr};
+    void* fn = cached.load(std::memory_order_acquire);
+    if (fn == nullptr) {
+        cudaDriverEntryPointQueryResult got;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &got);
+        if (e != cudaSuccess) return e;
+        if (got != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
+        cached.store(fn, std::memory_order_release);
+    }
+    const cuuint64_t eb = a.c.type == T_I8 ? 1 : 2;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.D), static_cast<cuuint64_t>(a.c.page),
+                                static_cast<cuuint64_t>(a.c.pages) * a.c.Hkv};
+    const cuuint64_t strides[2] = {a.c.D * eb, a.c.D * eb * a.c.page};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / eb), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r = reinterpret_cast<Encode>(fn)(
+        map, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides,
+        box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attn_join(const AttnArgs& a, int rows, int unit, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(a.T) * static_cast<unsigned>(a.Hq));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    dependent(cfg, attr, true);
+    return cudaLaunchKernelEx(&cfg, a.c.D == 64 ? attn_join_kernel<64> : a.c.D == 128 ? attn_join_kernel<128> : attn_join_kernel<256>,
+                              a, rows, unit);
+}
 
 cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
 {

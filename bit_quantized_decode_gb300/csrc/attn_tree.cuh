@@ -119,6 +119,19 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Four int8 -> four bf16, exactly: the low seven bits on 128.0 (whose last place is 1), less 128 or, for a negative code,
+// 256.
+__device__ __forceinline__ void i8_to_bf16(uint32_t c, uint32_t& h01, uint32_t& h23)
+{
+    const uint32_t m = c & 0x7f7f7f7fu, n = c & 0x80808080u;
+    const uint32_t a = __byte_perm(m, 0x43434343u, 0x4140), b = __byte_perm(m, 0x43434343u, 0x4342);
+    const uint32_t s = __byte_perm(n, 0x43434343u, 0x4140), t = __byte_perm(n, 0x43434343u, 0x4342);
+    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&t));
+    h01 = *reinterpret_cast<const uint32_t*>(&x);
+    h23 = *reinterpret_cast<const uint32_t*>(&y);
+}
+
 constexpr uint64_t kAtWaitNs = 250ull * 1000ull * 1000ull;
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
