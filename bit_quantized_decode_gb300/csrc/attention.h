@@ -70,12 +70,13 @@ struct AttnArgs {
     int T, Hq, G;             // G = Hq / Hkv
     void* y;                  // [T][Hq][D] of ytype
     int ytype;
-    long long* head;          // workspace: share, then B + 1 prefix sums of units
+    int blocks, least;        // of the first launch: blocks, units of one at least
+    int* head;                // workspace: B + 1 prefix sums of units (more than 32 sequences)
     float* part;              // workspace: two partial results per block
     int part_rows;            // rows of one
     unsigned* err;
 };
-__host__ __device__ inline size_t attn_head_bytes(int B) { return (8 * (static_cast<size_t>(B) + 2) + 127) / 128 * 128; }
+__host__ __device__ inline size_t attn_head_bytes(int B) { return (4 * (static_cast<size_t>(B) + 1) + 127) / 128 * 128; }
 // A partial result: running maxima, sums, and rows of D.
 __host__ __device__ inline size_t attn_part_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
 cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s);

@@ -22,6 +22,7 @@ inline bool half_type(int t) { return t == W4_F16 || t == W4_BF16; }
 
 constexpr int kMaxHeads = 1024;
 constexpr long long kMaxPlaces = 1ll << 30;
+constexpr long long kMaxUnits = 0x7fffffffll - 1024;      // (the kernels count units of work in 32 bits)
 
 int log2_of(int v)
 {
@@ -66,13 +67,16 @@ BatchView view(const w4_kv_batch* b) { return BatchView{b->table, b->ctx, b->q_s
 struct AttnPlan {
     bool tc;
     int part_rows;
+    long long units;          // of work, at most
 };
-AttnPlan plan_attention(const w4_kv_batch* b, int T, int G)
+AttnPlan plan_attention(const w4_kv_cache* c, const w4_kv_batch* b, int T, int G)
 {
     const int rows = (b->max_tokens < T ? b->max_tokens : T) * G;
     AttnPlan p;
     p.tc = rows > kAtRows;
-    const int tile = p.tc ? kAtTcRows : kAtRows;
+    const int tile = p.tc ? kAtTcRows : kAtRows, unit = p.tc ? kAtTcUnit : kAtUnit;
+    p.units = static_cast<long long>(b->B) * c->Hkv * ((rows + tile - 1) / tile) *
+              ((static_cast<long long>(b->max_pages) * c->page_size + unit - 1) / unit);
     p.part_rows = rows < tile ? (rows + 7) / 8 * 8 : tile;   // (results begin on 16-byte boundaries)
     return p;
 }
@@ -140,7 +144,8 @@ w4_status w4_kv_append(const w4_kv_cache* c, const w4_kv_batch* b, const w4_rope
 size_t w4_tree_attention_workspace_bytes(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq)
 {
     if (check_call(c, b, T, Hq) != W4_OK || b->max_tokens > W4_MAX_DRAFTS || T == 0 || b->B == 0) return 0;
-    return attention_workspace(c, b, plan_attention(b, T, Hq / c->Hkv));
+    const AttnPlan p = plan_attention(c, b, T, Hq / c->Hkv);
+    return p.units <= kMaxUnits ? attention_workspace(c, b, p) : 0;
 }
 
 w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const void* q, int q_type, int T, int Hq,
@@ -156,8 +161,8 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     if (T == 0 || b->B == 0) return W4_OK;
     r = check_call_pointers(c, b);
     if (r == W4_ERR_INVALID_ARG || !q || !y || !workspace) return W4_ERR_INVALID_ARG;
-    const AttnPlan p = plan_attention(b, T, Hq / c->Hkv);
-    if (ws_bytes < attention_workspace(c, b, p)) return W4_ERR_UNSUPPORTED_SHAPE;
+    const AttnPlan p = plan_attention(c, b, T, Hq / c->Hkv);
+    if (p.units > kMaxUnits || ws_bytes < attention_workspace(c, b, p)) return W4_ERR_UNSUPPORTED_SHAPE;
     if (r != W4_OK || !aligned(q, 16) || !aligned(y, 16) || !aligned(mask, 8) || !aligned(workspace, 16)) return W4_ERR_MISALIGNED;
     DeviceFacts d;
     if (!device_facts(&d)) return W4_ERR_CUDA;
@@ -172,7 +177,7 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     a.G = Hq / c->Hkv;
     a.y = y;
     a.ytype = y_type;
-    a.head = static_cast<long long*>(workspace);
+    a.head = static_cast<int*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_head_bytes(b->B));
     a.part_rows = p.part_rows;
     a.err = d.err;

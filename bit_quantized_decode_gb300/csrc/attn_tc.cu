@@ -9,17 +9,17 @@
 //   S = Q K^T   tcgen05.mma 128 x 64 x D: Q and K in shared memory as TMA's
 //               128-byte swizzle lays them, S in tensor memory (two buffers, so
 //               that the next product runs during the softmax);
-//   softmax     one thread per row (tensor-memory lane): maximum, exponentials
-//               and sum need no exchange.  The maximum in use is raised only when it
-//               is passed by more than 2^8: probabilities are then at most 256
+//   softmax     two threads per row (tensor-memory lane), 32 tokens each; they
+//               exchange their maxima.  The maximum in use is raised only when it
+//               is passed by more than 2^12: probabilities are then at most 4096
 //               (exact scaling, the sums stay in fp32), and the output, which
 //               lies in tensor memory, is rescaled a few times per segment
 //               instead of once per tile;
 //   O += P V    P goes back to tensor memory in 16 bits (two or three parts for
 //               an fp32 output) and is the A operand; V as it lies, 64 values of a token in a row,
 //               is an operand with its columns contiguous.
-// Warps: one orders copies, one issues MMAs, four take the softmax; INT8
-// caches add four that widen codes to 16 bits (exact) in shared memory.  All
+// Warps: one orders copies, one issues MMAs, eight take the softmax; for an INT8
+// cache six widen codes to 16 bits (exact) in shared memory.  All
 // are joined by mbarriers with bounded waits.
 #include "attn_tree.cuh"
 #include "gemm_w8.cuh"
@@ -28,7 +28,8 @@ namespace w4k {
 namespace {
 
 constexpr int kTcRows = kAtTcRows, kTcUnit = kAtTcUnit;
-constexpr float kRaise = 8.0f;                  // log2 of what a probability may reach
+constexpr int kConvWarps = 6;                   // warps 2, 3, 12 .. 15
+constexpr float kRaise = 12.0f;                 // log2 of what a probability may reach
 
 template <int D, int CT>
 struct Tc {
@@ -40,7 +41,7 @@ struct Tc {
     static constexpr int kStages = kI8 ? (D == 64 ? 10 : D == 128 ? 5 : 2) : (D == 64 ? 8 : D == 128 ? 5 : 2);   // copies
     static constexpr int kConv = kI8 ? (D == 256 ? 1 : 2) : kStages;   // 16-bit tiles
     static constexpr int kMeta = kStages + kConv;             // tiles between a copy's order and its softmax, at most
-    static constexpr int kThreads = kI8 ? 384 : 256;
+    static constexpr int kThreads = kI8 ? 512 : 384;
     static constexpr int kPBufs = D == 256 ? 1 : 2;
     static constexpr int kCols = 512;
     static constexpr int cS = D, cP = D + 2 * kTcUnit;        // tensor-memory columns of S and P; O begins at 0
@@ -50,12 +51,13 @@ struct Tc {
     static constexpr int oRaw = oKv + kConv * 2 * kHalf;
     static constexpr int oScale = oRaw + (kI8 ? kStages * kRaw : 0);        // [kMeta][2][64]
     static constexpr int oMeta = oScale + (kI8 ? kMeta * 2 * kTcUnit * 4 : 0);   // [kMeta]: which sixteenths of a tile have a page
-    static constexpr int oBars = (oMeta + kMeta * 4 + 7) / 8 * 8;
-    static constexpr int nBars = 2 * kStages + 4 * kConv + 8;
+    static constexpr int oTop = oMeta + kMeta * 4;            // [2][2][128]: maxima of a row's halves, of even and odd tiles
+    static constexpr int oBars = (oTop + 4 * kTcRows * 4 + 7) / 8 * 8;
+    static constexpr int nBars = 2 * kStages + 4 * kConv + 12;
     static constexpr int oMisc = oBars + nBars * 8;           // tensor memory's base, failure flag, odd values flag
     static constexpr int oWarpSum = oMisc + 16;
-    static constexpr int oPre = oWarpSum + kThreads / 32 * 8;
-    static constexpr int smem(int B) { return oPre + (B + 1) * 8 + 1024; }
+    static constexpr int oPre = oWarpSum + kThreads / 32 * 4;
+    static constexpr int smem(int B) { return oPre + (B + 1) * 4 + 1024; }
     static_assert(smem(kAtMaxSeq) <= 232448, "shared memory of a block");
     // (all of tensor memory: no other block of this library that takes some may be on the SM; the least of them has 106 KB)
     static_assert(smem(1) > 123 * 1024, "alone with its tensor memory on an SM");
@@ -74,19 +76,28 @@ __device__ __forceinline__ uint64_t desc_cols(uint32_t a, uint32_t lbo)
     return static_cast<uint64_t>((a & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
            (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// Four MMAs of 16 K each in one statement (the operands in uniform registers once): both operands in shared memory, 32 bytes
+// of a row to a step; the first overwrites unless `accumulate`.
+__device__ __forceinline__ void mma_ss_x4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, b1;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %4, %4;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "add.u64 a1, %1, 4;\n\tadd.u64 b1, %2, 4;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "add.u64 a1, %1, 6;\n\tadd.u64 b1, %2, 6;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
+// The same with A in tensor memory (eight columns to a step) and B's rows along N (16 rows of 128 bytes to a step).
+__device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred q;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\tsetp.eq.b32 q, %0, %0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, 128;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "add.u32 a1, %1, 16;\n\tadd.u64 b1, %2, 256;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "add.u32 a1, %1, 24;\n\tadd.u64 b1, %2, 384;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc)
         : "memory");
 }
@@ -124,48 +135,42 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
     const uint32_t raw_full = bars, raw_empty = raw_full + 8 * S;                    // codes (INT8)
     const uint32_t k_full = raw_empty + 8 * S, k_empty = k_full + 8 * NC;            // 16-bit keys
     const uint32_t v_full = k_empty + 8 * NC, v_empty = v_full + 8 * NC;             // and values
-    const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8;
+    const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8,
+                   pair_bar = wg_bar + 8;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::oMisc);
     volatile uint32_t* dead_s = misc + 1;
     volatile uint32_t* odd_s = misc + 2;
     volatile uint32_t* meta_s = reinterpret_cast<volatile uint32_t*>(smem + C::oMeta);
     float* scale_s = reinterpret_cast<float*>(smem + C::oScale);
-    long long* pre_s = reinterpret_cast<long long*>(smem + C::oPre);
+    int* pre_s = reinterpret_cast<int*>(smem + C::oPre);
 
     if (tid == 0) {
         for (int k = 0; k < S; ++k) {
             mbar_init(raw_full + 8 * k, 1);
-            mbar_init(raw_empty + 8 * k, 4);
+            mbar_init(raw_empty + 8 * k, kConvWarps);
         }
         for (int k = 0; k < NC; ++k) {
-            mbar_init(k_full + 8 * k, kI8 ? 4 : 1);
+            mbar_init(k_full + 8 * k, kI8 ? kConvWarps : 1);
             mbar_init(k_empty + 8 * k, 1);
-            mbar_init(v_full + 8 * k, kI8 ? 4 : 1);
+            mbar_init(v_full + 8 * k, kI8 ? kConvWarps : 1);
             mbar_init(v_empty + 8 * k, 1);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(s_full + 8 * k, 1);
-            mbar_init(p_full + 8 * k, 4);
+            mbar_init(p_full + 8 * k, 8);
             mbar_init(pv_done + 8 * k, 1);
         }
-        mbar_init(q_full, 4);
-        mbar_init(wg_bar, 4);
+        mbar_init(q_full, 8);
+        mbar_init(wg_bar, 8);
+        for (int k = 0; k < 4; ++k) mbar_init(pair_bar + 8 * k, 2);
         fence_mbar_init();
         *dead_s = 0u;
         *odd_s = 0u;
     }
-    pdl_launch_dependents();
-    pdl_wait();
-    seq_prefix<C::kThreads>(A, kTcRows, kTcUnit, pre_s, reinterpret_cast<long long*>(smem + C::oWarpSum));
-    const long long total = pre_s[A.b.B];
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < 1) share = 1;
-    if (blockIdx.x == 0) {                      // for the joining launch
-        if (tid == 0) A.head[0] = share;
-        for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[1 + b] = pre_s[b];
+    if (tid == 32 && !kI8) {
+        prefetch_map(&A.kmap);
+        prefetch_map(&A.vmap);
     }
-    const long long us = min(static_cast<long long>(blockIdx.x) * share, total), ue = min(us + share, total);
-    if (us >= ue) return;
     __syncwarp();
     if (warp == 1) {
         tmem_alloc(smem_u32(misc), C::kCols);
@@ -175,6 +180,17 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = misc[0];
+    pdl_wait();
+    pdl_launch_dependents();                    // (this block holds its tensor memory; the joining launch reads this one's inputs early)
+    const Layout lay = block_layout<C::kThreads>(A, kTcRows, kTcUnit, pre_s, reinterpret_cast<int*>(smem + C::oWarpSum));
+    const int total = lay.total, share = block_share(total, A.blocks, A.least);
+    if (blockIdx.x == 0 && A.b.B > 32)          // for the joining launch
+        for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[b] = pre_s[b];
+    const int us = min(static_cast<int>(min(static_cast<long long>(blockIdx.x) * share, 0x7fffffffll)), total), ue = us + min(share, total - us);
+    if (us >= ue) {
+        if (warp == 1) tmem_dealloc(tb, C::kCols);
+        return;
+    }
     auto fail = [&]() {
         *dead_s = 1u;
         if (A.err != nullptr) atomicExch(A.err, kErrWaitTimeout);
@@ -185,11 +201,11 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
         const int per = min(A.c.page, kTcUnit), boxes = kTcUnit / per;       // tokens of a copy, copies of a tile
         int it = 0;
         bool ok = true;
-        for (long long begin = us; begin < ue && ok;) {
-            const Segment sg = find_segment(A, pre_s, begin, kTcRows, kTcUnit);
-            const long long end = min(sg.u0 + sg.units, ue);
-            for (long long u = begin; u < end; ++u, ++it) {
-                const int t0 = static_cast<int>(u - sg.u0) * kTcUnit;
+        for (int begin = us; begin < ue && ok;) {
+            const Segment sg = find_segment(A, lay, begin, kTcRows, kTcUnit);
+            const int end = min(sg.u0 + sg.units, ue);
+            for (int u = begin; u < end; ++u, ++it) {
+                const int t0 = (u - sg.u0) * kTcUnit;
                 int page = -1;
                 const int t = t0 + lane * per;
                 if (lane < boxes && t < sg.f.len)
@@ -263,72 +279,93 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
         constexpr uint32_t qf = QT == T_BF16 ? 1u : 0u, pf = PT == T_BF16 ? 1u : 0u;
         constexpr uint32_t iqk = (1u << 4) | (qf << 7) | (qf << 10) | (static_cast<uint32_t>(kTcUnit >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
         constexpr uint32_t ipv = (1u << 4) | (pf << 7) | (pf << 10) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (static_cast<uint32_t>(kTcRows >> 4) << 24);
-        const uint32_t q_a = smem_u32(smem + C::oQ), kv_a = smem_u32(smem + C::oKv);
+        const uint64_t q_desc = desc_rows(smem_u32(smem + C::oQ)), k_desc = desc_rows(smem_u32(smem + C::oKv));
+        const uint64_t v_desc = desc_cols(smem_u32(smem + C::oKv) + C::kHalf, kTcUnit * 128);
         int it = 0, pieces = 0;
         bool ok = true;
-        auto scores = [&](int i) {              // S of tile i
-            ok = ok && warp_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u);
-            if (!ok) return;
+        auto scores = [&](int i) {              // S of tile i, whose keys are there
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t k_a = kv_a + (i % NC) * 2 * C::kHalf;
+                const uint64_t k = k_desc + static_cast<uint64_t>((i % NC) * (2 * C::kHalf >> 4));
                 const uint32_t d = tb + C::cS + (i & 1) * kTcUnit;
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-                    mma_ss(d, desc_rows(q_a + (j >> 2) * kTcRows * 128 + (j & 3) * 32), desc_rows(k_a + (j >> 2) * kTcUnit * 128 + (j & 3) * 32),
-                           iqk, j > 0);
+                for (int x = 0; x < C::kBoxes; ++x) mma_ss_x4(d, q_desc + x * (kTcRows * 128 >> 4), k + x * (kTcUnit * 128 >> 4), iqk, x > 0);
                 tc_commit(k_empty + 8 * (i % NC));
                 tc_commit(s_full + 8 * (i & 1));
             }
             __syncwarp();
         };
-        for (long long begin = us; begin < ue && ok; ++pieces) {
-            const Segment sg = find_segment(A, pre_s, begin, kTcRows, kTcUnit);
-            const long long end = min(sg.u0 + sg.units, ue);
-            const int n = static_cast<int>(end - begin);
-            ok = warp_wait(q_full, static_cast<uint32_t>(pieces) & 1u);
-            scores(it);
-            for (int k = 0; k < n && ok; ++k, ++it) {
-                if (k + 1 < n) scores(it + 1);
-                ok = ok && warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u) &&
+        auto keys = [&](int i) { return warp_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u); };
+        for (int begin = us; begin < ue && ok; ++pieces) {
+            const Segment sg = find_segment(A, lay, begin, kTcRows, kTcUnit);
+            const int end = min(sg.u0 + sg.units, ue), last = it + end - begin;
+            ok = warp_wait(q_full, static_cast<uint32_t>(pieces) & 1u) && keys(it);
+            if (ok) scores(it);
+            if (ok && it + 1 < last) {
+                ok = keys(it + 1);
+                if (ok) scores(it + 1);
+            }
+            for (; it < last && ok; ++it) {
+                ok = warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u) &&
                      warp_wait(v_full + 8 * (it % NC), static_cast<uint32_t>(it / NC) & 1u);
                 if (!ok) break;
                 tc_fence_after();
+                // The scores after next first, whose buffer P has left: the softmax waits for them sooner than for this
+                // product.  (But not if their keys are not there yet: their place may wait for this product.)
+                const bool more = it + 2 < last;
+                const int i = it + 2;
+                const bool early = more && __all_sync(0xffffffffu, mbar_test_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u));
+                if (early) scores(i);
                 if (elect_one()) {
-                    const uint32_t v_a = kv_a + (it % NC) * 2 * C::kHalf + C::kHalf;
+                    const uint64_t v = v_desc + static_cast<uint64_t>((it % NC) * (2 * C::kHalf >> 4));
                     const uint32_t p = tb + C::cP + (it % C::kPBufs) * 32 * kParts;
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                        for (int j = 0; j < kTcUnit / 16; ++j)
-                            mma_ts(tb, p + 32 * part + 8 * j, desc_cols(v_a + j * 2048, kTcUnit * 128), ipv);
+                    for (int part = 0; part < kParts; ++part) mma_ts_x4(tb, p + 32 * part, v, ipv);
                     tc_commit(v_empty + 8 * (it % NC));
                     tc_commit(pv_done + 8 * (it & 1));
                 }
                 __syncwarp();
+                if (more && !early) {
+                    ok = keys(i);
+                    if (ok) scores(i);
+                }
             }
             begin = end;
         }
         if (!ok && lane == 0) fail();
         // every MMA has completed before the tensor memory is freed
         if (it > 0) warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4 && warp < 12) {
         // --------------------------------------------------------- softmax
-        const int row = tid - 128;
+        constexpr int kHalfCols = kTcUnit / 2;
+        const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, wid = tid - 128;
+        float* top_s = reinterpret_cast<float*>(smem + C::oTop);
         const uint32_t tl = tb + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         int it = 0;
-        uint32_t wg_phase = 0;
+        uint32_t wg_phase = 0, pair_phase = 0;
         bool ok = true;
-        auto wg_sync = [&]() {                  // the four warps, with a bounded wait
+        auto wg_sync = [&]() {                  // the eight warps, with a bounded wait
             __syncwarp();
             if (lane == 0) mbar_arrive(wg_bar);
             const bool all = warp_wait(wg_bar, wg_phase & 1u);
             ++wg_phase;
             return all;
         };
-        for (long long begin = us; begin < ue && ok;) {
-            const Segment sg = find_segment(A, pre_s, begin, kTcRows, kTcUnit);
-            const long long end = min(sg.u0 + sg.units, ue);
+        // This thread's number and that of the row's other half.
+        auto exchanged = [&](float v, float& other) {
+            float* at = top_s + (pair_phase & 1u) * 2 * kTcRows;
+            at[half * kTcRows + row] = v;
+            __syncwarp();
+            const uint32_t bar = pair_bar + 8 * (warp & 3);
+            if (lane == 0) mbar_arrive(bar);
+            const bool all = warp_wait(bar, pair_phase & 1u);
+            ++pair_phase;
+            other = at[(half ^ 1) * kTcRows + row];
+            return all;
+        };
+        for (int begin = us; begin < ue && ok;) {
+            const Segment sg = find_segment(A, lay, begin, kTcRows, kTcUnit);
+            const int end = min(sg.u0 + sg.units, ue);
             const int rows = min(kTcRows, sg.f.n * A.G - sg.tile * kTcRows);
             const bool have = row < rows;
             const int rr = sg.tile * kTcRows + (have ? row : 0), tok = rr / A.G, tq = sg.f.q0 + tok;
@@ -341,13 +378,14 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at);
                 uint8_t* d = smem + C::oQ + row * 128;
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
+                for (int k = 0; k < D / 16; ++k) {
+                    const int j = half * (D / 16) + k;
                     const uint4 v = have ? __ldg(q + j) : make_uint4(0u, 0u, 0u, 0u);
                     *reinterpret_cast<uint4*>(d + (j >> 3) * kTcRows * 128 + (((j & 7) ^ (row & 7)) << 4)) = v;
                 }
                 const uint32_t zero[16] = {};
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) tmem_st16(tl + 16 * j, zero);
+                for (int j = 0; j < D / 32; ++j) tmem_st16(tl + half * (D / 2) + 16 * j, zero);
                 tmem_wait_st();
                 tc_fence_before();
                 fence_proxy_async_smem();
@@ -355,32 +393,29 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 if (lane == 0) mbar_arrive(q_full);
             }
             float m = neg_inf(), l = 0.0f;
-            for (long long u = begin; u < end; ++u, ++it) {
+            for (int u = begin; u < end; ++u, ++it) {
                 ok = warp_wait(s_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u);
                 if (!ok) break;
                 tc_fence_after();
-                float s[kTcUnit];
+                float s[kHalfCols];
                 {
                     uint32_t r0[16], r1[16];
+                    const uint32_t a = tl + C::cS + (it & 1) * kTcUnit + kHalfCols * half;
+                    tmem_ld16x2(a, r0, a + 16, r1);
 #pragma unroll
-                    for (int j = 0; j < kTcUnit / 32; ++j) {
-                        const uint32_t a = tl + C::cS + (it & 1) * kTcUnit + 32 * j;
-                        tmem_ld16x2(a, r0, a + 16, r1);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            s[32 * j + k] = __uint_as_float(r0[k]);
-                            s[32 * j + 16 + k] = __uint_as_float(r1[k]);
-                        }
+                    for (int k = 0; k < 16; ++k) {
+                        s[k] = __uint_as_float(r0[k]);
+                        s[16 + k] = __uint_as_float(r1[k]);
                     }
                 }
-                const int t0 = static_cast<int>(u - sg.u0) * kTcUnit;
+                const int t0 = (u - sg.u0) * kTcUnit;
                 const uint32_t there = meta_s[it % C::kMeta];
                 const bool special = t0 + kTcUnit > sg.f.ctx || there != 15u;
-                unsigned long long vis = ~0ull;
+                uint32_t vis = ~0u;                // this half's tokens
                 if constexpr (kI8) {
-                    const float4* ks = reinterpret_cast<const float4*>(scale_s + (it % C::kMeta) * 2 * kTcUnit);
+                    const float4* ks = reinterpret_cast<const float4*>(scale_s + (it % C::kMeta) * 2 * kTcUnit + kHalfCols * half);
 #pragma unroll
-                    for (int j = 0; j < kTcUnit / 4; ++j) {
+                    for (int j = 0; j < kHalfCols / 4; ++j) {
                         const float4 k4 = ks[j];
                         s[4 * j] *= k4.x;
                         s[4 * j + 1] *= k4.y;
@@ -393,19 +428,22 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                     const int o = sg.f.ctx - t0;
                     const unsigned long long old = o >= 64 ? ~0ull : o > 0 ? (1ull << o) - 1ull : 0ull;
                     const unsigned long long own = o >= 64 || o <= -64 ? 0ull : o >= 0 ? see << o : see >> -o;
-                    vis = 0ull;
+                    vis = static_cast<uint32_t>((old | own) >> (kHalfCols * half));
+                    if (!(there >> (2 * half) & 1u)) vis &= 0xffff0000u;
+                    if (!(there >> (2 * half + 1) & 1u)) vis &= 0x0000ffffu;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (there >> k & 1u) vis |= 0xffffull << (16 * k);
-                    vis &= old | own;
-#pragma unroll
-                    for (int j = 0; j < kTcUnit; ++j)
-                        if (!(vis >> j & 1ull)) s[j] = neg_inf();
+                    for (int j = 0; j < kHalfCols; ++j)
+                        if (!(vis >> j & 1u)) s[j] = neg_inf();
                 }
                 float top = s[0];
 #pragma unroll
-                for (int j = 1; j < kTcUnit; ++j) top = fmaxf(top, s[j]);
-                top *= A.scale;
+                for (int j = 1; j < kHalfCols; ++j) top = fmaxf(top, s[j]);
+                {
+                    float other;
+                    ok = exchanged(top, other);
+                    if (!ok) break;
+                    top = fmaxf(top, other) * A.scale;
+                }
                 const bool raise = top > m + kRaise || (m == neg_inf() && top > m);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float was = m;
@@ -417,12 +455,13 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int j = 0; j < D / 16; ++j) {
+                        for (int j = 0; j < D / 32; ++j) {
+                            const uint32_t a = tl + half * (D / 2) + 16 * j;
                             uint32_t r[16];
-                            tmem_ld16(tl + 16 * j, r);
+                            tmem_ld16(a, r);
 #pragma unroll
                             for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
-                            tmem_st16(tl + 16 * j, r);
+                            tmem_st16(a, r);
                         }
                         tmem_wait_st();
                     }
@@ -430,7 +469,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 const float base = m == neg_inf() ? 0.0f : -m;
                 float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kTcUnit; j += 2) {
+                for (int j = 0; j < kHalfCols; j += 2) {
                     s[j] = exp2_fast(__fmaf_rn(s[j], A.scale, base));
                     s[j + 1] = exp2_fast(__fmaf_rn(s[j + 1], A.scale, base));
                     sum0 += s[j];
@@ -438,9 +477,9 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 }
                 l += sum0 + sum1;
                 if constexpr (kI8) {
-                    const float4* vs = reinterpret_cast<const float4*>(scale_s + (it % C::kMeta) * 2 * kTcUnit + kTcUnit);
+                    const float4* vs = reinterpret_cast<const float4*>(scale_s + (it % C::kMeta) * 2 * kTcUnit + kTcUnit + kHalfCols * half);
 #pragma unroll
-                    for (int j = 0; j < kTcUnit / 4; ++j) {
+                    for (int j = 0; j < kHalfCols / 4; ++j) {
                         const float4 v4 = vs[j];
                         s[4 * j] *= v4.x;
                         s[4 * j + 1] *= v4.y;
@@ -449,8 +488,8 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                     }
                     if (special) {
 #pragma unroll
-                        for (int j = 0; j < kTcUnit; ++j)
-                            if (!(vis >> j & 1ull)) s[j] = 0.0f;
+                        for (int j = 0; j < kHalfCols; ++j)
+                            if (!(vis >> j & 1u)) s[j] = 0.0f;
                     }
                 } else if (special) {
                     // Values that nothing may see: zeros in their stead.  A draft's infinities and NaN would reach the rows
@@ -462,7 +501,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                     auto word = [&](int t, int c) { return reinterpret_cast<uint4*>(v + (c >> 3) * kTcUnit * 128 + t * 128 + (((c & 7) ^ (t & 7)) << 4)); };
                     const int from = min(max(sg.f.ctx - t0, 0), kTcUnit);
                     bool odd = false;
-                    for (int k = row; k < kTcUnit * (D / 8); k += 128) {
+                    for (int k = wid; k < kTcUnit * (D / 8); k += 256) {
                         const int t = k / (D / 8);
                         uint4* w = word(t, k % (D / 8));
                         if (t0 + t >= sg.f.len || !(there >> (t >> 4) & 1u)) {
@@ -481,17 +520,20 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                         // (the last product on this output is done: as for the rescaling)
                         if (u > begin) ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
                         if (!ok) break;
+                        // one half of each row's tokens after the other
+                        if (half == 1) ok = wg_sync();
+                        if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 8; c += 2) {
                             uint32_t r[16];
                             tmem_ld16(tl + 8 * c, r);
 #pragma unroll
-                            for (int j = 0; j < kTcUnit; ++j) {
-                                if (j >= from && (vis >> j & 1ull)) {
+                            for (int j = 0; j < kHalfCols; ++j) {
+                                if (j + kHalfCols * half >= from && (vis >> j & 1u)) {
 #pragma unroll
                                     for (int h = 0; h < 2; ++h) {
-                                        const uint4 w = *word(j, c + h);
+                                        const uint4 w = *word(j + kHalfCols * half, c + h);
                                         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                                         for (int i = 0; i < 4; ++i) {
@@ -506,11 +548,13 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                             tmem_st16(tl + 8 * c, r);
                         }
                         tmem_wait_st();
-                        ok = wg_sync();         // every row has read the drafts
+                        tc_fence_before();
+                        if (half == 0) ok = wg_sync();
+                        ok = ok && wg_sync();   // every row has read the drafts
                         if (!ok) break;
-                        for (int k = row; k < kTcUnit * (D / 8); k += 128)
+                        for (int k = wid; k < kTcUnit * (D / 8); k += 256)
                             if (k / (D / 8) >= from) *word(k / (D / 8), k % (D / 8)) = make_uint4(0u, 0u, 0u, 0u);
-                        if (row == 0) *odd_s = 0u;
+                        if (wid == 0) *odd_s = 0u;
                     }
                     ok = wg_sync();             // (the flag was read, or is down, before a later tile sets it)
                     if (!ok) break;
@@ -524,43 +568,44 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 }
                 const uint32_t p = tl + C::cP + (it % C::kPBufs) * 32 * kParts;
 #pragma unroll
-                for (int part = 0; part < kParts; ++part)
+                for (int part = 0; part < kParts; ++part) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int j = 32 * h + 2 * k;
-                            w[k] = tc_pair<PT>(s[j], s[j + 1]);
-                            if (part + 1 < kParts) {
-                                const float2 f = tc_unpair<PT>(w[k]);
-                                s[j] -= f.x;
-                                s[j + 1] -= f.y;
-                            }
+                    for (int k = 0; k < 16; ++k) {
+                        w[k] = tc_pair<PT>(s[2 * k], s[2 * k + 1]);
+                        if (part + 1 < kParts) {
+                            const float2 f = tc_unpair<PT>(w[k]);
+                            s[2 * k] -= f.x;
+                            s[2 * k + 1] -= f.y;
                         }
-                        tmem_st16(p + 32 * part + 16 * h, w);
                     }
+                    tmem_st16(p + 32 * part + 16 * half, w);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * (it & 1));
             }
             if (ok) ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
+            float l2 = 0.0f;
+            if (ok) ok = exchanged(l, l2);
             if (!ok) {
                 if (lane == 0) fail();
                 break;
             }
+            l = half ? l2 + l : l + l2;
             tc_fence_after();
             // ------------------------------------------------- the row's result
             const bool whole = begin == sg.u0 && end == sg.u0 + sg.units;
             float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
-            if (have && !whole) {
+            if (have && !whole && half == 0) {
                 part[row] = m;
                 part[A.part_rows + row] = l;
             }
             const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1
-            for (int j = 0; j < D / 16; ++j) {
+            for (int k = 0; k < D / 32; ++k) {
+                const int j = half * (D / 32) + k;
                 uint32_t r[16];
                 tmem_ld16(tl + 16 * j, r);
                 if (have) {
@@ -587,10 +632,10 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
             __syncwarp();
             begin = end;
         }
-    } else if (kI8 && warp >= 8) {
+    } else if (kI8) {
         // ---------------------------------------------------- codes to 16 bits
-        const int w = tid - 256;
-        const long long n = ue - us;
+        const int w = warp < 4 ? tid - 64 : tid - 384 + 64;
+        const int n = ue - us;
         bool ok = true;
         for (int it = 0; it < n && ok; ++it) {
             const int st = it % S, cv = it % NC;
@@ -603,7 +648,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 if (it >= NC) ok = warp_wait((half ? v_empty : k_empty) + 8 * cv, ph);
                 if (!ok) break;
 #pragma unroll 2
-                for (int k = w; k < kTcUnit * D / 16; k += 128) {
+                for (int k = w; k < kTcUnit * D / 16; k += 32 * kConvWarps) {
                     const int t = k / (D / 16), c = k % (D / 16);                   // sixteen codes: two 16-byte words
                     const uint4 q = *reinterpret_cast<const uint4*>(src + half * kTcUnit * D + 16 * k);
                     const uint32_t x[4] = {q.x, q.y, q.z, q.w};
@@ -649,6 +694,8 @@ cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
         if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, 128, rows);
     }
     if (e != cudaSuccess) return e;
+    a.blocks = grid;
+    a.least = 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>(grid));

@@ -44,6 +44,7 @@ struct At {
     static constexpr int kPad = D + 8;                        // floats of a joined row: rows spread over the banks
     // shared memory
     static constexpr int oRing = 0;
+    static_assert(kWarps * kAtRows * kPad * 4 <= kWarps * kSlots * kSlot, "the rings hold every warp's result");
     static constexpr int oJoin = kWarps * kSlots * kSlot;                              // [kParts][16][kPad]
     static constexpr int oScale = oJoin + kParts * kAtRows * kPad * 4;             // [warps][slots][2][16]
     static constexpr int oMl = oScale + (CT == T_I8 ? kWarps * kSlots * 2 * kAtUnit * 4 : 0);   // [warps][2][16]
@@ -51,10 +52,10 @@ struct At {
     static constexpr int oBars = oFin + 2 * kAtRows * 4;
     static constexpr int oOk = oBars + kWarps * kSlots * 8;                            // [warps][slots]: the page is there
     static constexpr int oWarpSum = (oOk + kWarps * kSlots * 4 + 7) / 8 * 8;
-    static constexpr int oPre = oWarpSum + kWarps * 8;
-    static constexpr int smem(int B) { return oPre + (B + 1) * 8 + 1024; }              // and the alignment of the ring
+    static constexpr int oPre = oWarpSum + kWarps * 4;
+    static constexpr int smem(int B) { return oPre + (B + 1) * 4 + 1024; }              // and the alignment of the ring
     static_assert(kSlots >= 2, "two units per warp");
-    static_assert(oPre + (kAtMaxSeq + 1) * 8 + 1024 <= 232448, "shared memory of a block");
+    static_assert(oPre + (kAtMaxSeq + 1) * 4 + 1024 <= 232448, "shared memory of a block");
 };
 
 // The byte at column x of token t in a half slot, as the copies with a swizzle lay it.
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
 {
     using C = At<D, CT>;
     constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
+    constexpr int kParts = !kWide ? 1 : PT == T_F16 ? 2 : 3;  // of a probability: 11 or 8 bits each
     constexpr int W = C::kWarps;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -141,58 +143,66 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
     float* ml_s = reinterpret_cast<float*>(smem + C::oMl);
     float* fin_s = reinterpret_cast<float*>(smem + C::oFin);
     volatile int* ok_s = reinterpret_cast<volatile int*>(smem + C::oOk) + warp * C::kSlots;
-    long long* pre_s = reinterpret_cast<long long*>(smem + C::oPre);
+    int* pre_s = reinterpret_cast<int*>(smem + C::oPre);
     const uint32_t bars = smem_u32(smem + C::oBars) + static_cast<uint32_t>(warp * C::kSlots * 8);
     uint8_t* ring = smem + C::oRing + warp * C::kSlots * C::kSlot;
     const uint32_t ring_a = smem_u32(ring);
     float* scale_s = reinterpret_cast<float*>(smem + C::oScale) + warp * C::kSlots * 2 * kAtUnit;
 
     if (lane == 0) {
+        if (warp == 0) {
+            prefetch_map(&A.kmap);
+            prefetch_map(&A.vmap);
+        }
         for (int k = 0; k < C::kSlots; ++k) mbar_init(bars + 8 * k, 1);
         fence_mbar_init();
     }
     __syncwarp();
-    pdl_launch_dependents();
     pdl_wait();
-    seq_prefix<C::kThreads>(A, kAtRows, kAtUnit, pre_s, reinterpret_cast<long long*>(smem + C::oWarpSum));
-    const long long total = pre_s[A.b.B];
-    long long share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < W) share = W;                   // a unit for each warp
-    if (blockIdx.x == 0) {                      // for the joining launch
-        if (tid == 0) A.head[0] = share;
-        for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[1 + b] = pre_s[b];
-    }
-    const long long us = min(static_cast<long long>(blockIdx.x) * share, total), ue = min(us + share, total);
+    pdl_launch_dependents();                    // (behind the wait: the joining launch reads this one's inputs early)
+    const Layout lay = block_layout<C::kThreads>(A, kAtRows, kAtUnit, pre_s, reinterpret_cast<int*>(smem + C::oWarpSum));
+    const int total = lay.total, share = block_share(total, A.blocks, A.least);
+    if (blockIdx.x == 0 && A.b.B > 32)          // for the joining launch
+        for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[b] = pre_s[b];
+    const int us = min(static_cast<int>(min(static_cast<long long>(blockIdx.x) * share, 0x7fffffffll)), total), ue = us + min(share, total - us);
     if (us >= ue) return;
 
     // ------------------------------------------------- copies, units ahead
     // The warp's units of a piece are its begin + warp, + W, ..; pieces follow each other.
-    Segment ps = find_segment(A, pre_s, us, kAtRows, kAtUnit);
-    long long pend = min(ps.u0 + ps.units, ue), pu = us + warp;
-    int page_ahead = -1;
-    auto settle = [&]() {                       // pu: the next unit to order (or none: pu >= ue); its page
-        while (pu >= pend && pend < ue) {
-            const long long begin = pend;
-            ps = find_segment(A, pre_s, begin, kAtRows, kAtUnit);
-            pend = min(ps.u0 + ps.units, ue);
-            pu = begin + warp;
-        }
-        if (pu < pend) {
-            const int t = static_cast<int>(pu - ps.u0) * kAtUnit;
-            page_ahead = __ldg(A.b.table + static_cast<size_t>(ps.b) * A.b.max_pages + (t >> A.c.lg));
+    Segment ps = find_segment(A, lay, us, kAtRows, kAtUnit);
+    int pend = min(ps.u0 + ps.units, ue), pu = us + warp;
+    int pages_l = -1, next = 0;                 // pages of the next 32 of the warp's units, one to a lane
+    auto fetch_pages = [&]() {
+        const int u = pu + lane * W;
+        if (u < pend)
+            pages_l = __ldg(A.b.table + static_cast<size_t>(ps.b) * A.b.max_pages + ((u - ps.u0) * kAtUnit >> A.c.lg));
+        next = 0;
+    };
+    auto settle = [&]() {                       // pu: the next unit to order (or none: pu >= pend)
+        if (pu >= pend) {
+            if (pend >= ue) return;
+            do {
+                const int begin = pend;
+                ps = find_segment(A, lay, begin, kAtRows, kAtUnit);
+                pend = min(ps.u0 + ps.units, ue);
+                pu = begin + warp;
+            } while (pu >= pend && pend < ue);
+            fetch_pages();
+        } else if (next == 32) {
+            fetch_pages();
         }
     };
-    settle();
     int issued = 0;
     auto order = [&](int slot) {
         if (pu >= pend) return;
         const uint32_t bar = bars + 8 * slot;
-        const bool there = page_ahead >= 0 && page_ahead < A.c.pages;
+        const int page = __shfl_sync(0xffffffffu, pages_l, next);
+        const bool there = page >= 0 && page < A.c.pages;
         if (lane == 0) {
             ok_s[slot] = there;
             if (there) {
-                const int y = static_cast<int>(pu - ps.u0) * kAtUnit & (A.c.page - 1);
-                const int z = page_ahead * A.c.Hkv + ps.h;
+                const int y = (pu - ps.u0) * kAtUnit & (A.c.page - 1);
+                const int z = page * A.c.Hkv + ps.h;
                 mbar_arrive_expect_tx(bar, C::kSlot + (CT == T_I8 ? 2 * kAtUnit * 4 : 0));
                 const uint32_t dst = ring_a + slot * C::kSlot;
 #pragma unroll
@@ -211,24 +221,18 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
         }
         __syncwarp();
         ++issued;
+        ++next;
         pu += W;
         settle();
     };
-#pragma unroll 1
-    for (int k = 0; k < C::kSlots; ++k) order(k);
 
     // ------------------------------------------------------------ segments
     int slot = 0, seen = 0;
     uint32_t phase = 0;
     bool dead = false;
-#pragma unroll 1
-    for (long long begin = us; begin < ue;) {
-        const Segment sg = find_segment(A, pre_s, begin, kAtRows, kAtUnit);
-        const long long end = min(sg.u0 + sg.units, ue);
-        const int rows = min(kAtRows, sg.f.n * A.G - sg.tile * kAtRows);
-        // this lane's rows g and g + 8: queries, masks
-        uint32_t qa[D / 16][4];
-        unsigned long long see[2];
+    uint32_t qa[D / 16][4];
+    unsigned long long see[2];
+    auto load_rows = [&](const Segment& sg, int rows) {       // this lane's rows g and g + 8: queries, masks
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = g + 8 * e;
@@ -239,24 +243,41 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             const uint16_t* q = static_cast<const uint16_t*>(A.q) + (static_cast<size_t>(t) * A.Hq + sg.h * A.G + (rr - tok * A.G)) * D;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
-                uint2 v;
-                if constexpr (CT == T_I8) {     // a lane's K values of a step are four codes in a row
-                    v = __ldg(reinterpret_cast<const uint2*>(q + 16 * j + 4 * c));
-                } else {
-                    v.x = __ldg(reinterpret_cast<const unsigned*>(q + 16 * j + 2 * c));
-                    v.y = __ldg(reinterpret_cast<const unsigned*>(q + 16 * j + 8 + 2 * c));
+                uint2 v = make_uint2(0u, 0u);
+                if (have) {
+                    if constexpr (CT == T_I8) { // a lane's K values of a step are four codes in a row
+                        v = __ldg(reinterpret_cast<const uint2*>(q + 16 * j + 4 * c));
+                    } else {
+                        v.x = __ldg(reinterpret_cast<const unsigned*>(q + 16 * j + 2 * c));
+                        v.y = __ldg(reinterpret_cast<const unsigned*>(q + 16 * j + 8 + 2 * c));
+                    }
                 }
-                qa[j][e] = have ? v.x : 0u;
-                qa[j][2 + e] = have ? v.y : 0u;
+                qa[j][e] = v.x;
+                qa[j][2 + e] = v.y;
             }
         }
+    };
+    auto rows_of = [&](const Segment& sg) { return min(kAtRows, sg.f.n * A.G - sg.tile * kAtRows); };
+    Segment sg = ps;
+    fetch_pages();
+    load_rows(sg, rows_of(sg));
+    settle();
+#pragma unroll 1
+    for (int k = 0; k < C::kSlots; ++k) order(k);
+#pragma unroll 1
+    for (int begin = us; begin < ue;) {
+        if (begin != us) {
+            sg = find_segment(A, lay, begin, kAtRows, kAtUnit);
+            load_rows(sg, rows_of(sg));
+        }
+        const int end = min(sg.u0 + sg.units, ue), rows = rows_of(sg);
         float o[D / 8][4];
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
         float m[2] = {neg_inf(), neg_inf()}, l[2] = {0.0f, 0.0f};
 
 #pragma unroll 1
-        for (long long u = begin + warp; u < end; u += W) {
+        for (int u = begin + warp; u < end; u += W) {
             if (!dead) {
                 const bool ok = mbar_wait_bounded(bars + 8 * slot, phase, kAtWaitNs);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -269,7 +290,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             uint8_t* ks = ring + slot * C::kSlot;
             uint8_t* vs = ks + C::kHalf;
             const uint32_t ka = ring_a + slot * C::kSlot, va = ka + C::kHalf;
-            const int t0 = static_cast<int>(u - sg.u0) * kAtUnit;
+            const int t0 = (u - sg.u0) * kAtUnit;
             if (ok_s[slot] != 0) {
                 // scores: tokens 2c, 2c + 1, 8 + 2c, 9 + 2c of rows g, g + 8
                 float s[2][4] = {};
@@ -327,7 +348,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                             }
                         }
                 }
-                uint32_t hi[4], lo[4];
+                uint32_t pa[kParts][4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float top = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
@@ -359,13 +380,27 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t p = pair16<PT>(s[h][2 * e], s[h][2 * e + 1]);
-                        hi[2 * h + e] = p;
-                        if constexpr (kWide) {
-                            const float2 r = unpair16<PT>(p);
-                            lo[2 * h + e] = pair16<PT>(s[h][2 * e] - r.x, s[h][2 * e + 1] - r.y);
+                        float x = s[h][2 * e], y = s[h][2 * e + 1];
+#pragma unroll
+                        for (int k = 0; k < kParts; ++k) {
+                            pa[k][2 * h + e] = pair16<PT>(x, y);
+                            const float2 r = unpair16<PT>(pa[k][2 * h + e]);
+                            x -= r.x;
+                            y -= r.y;
                         }
                     }
+                // (the tensor cores cut a sum's low bits: in 32 bits an output's steps over the units are added here)
+                auto pv = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+                    if constexpr (kWide) {
+                        float d[4] = {};
+#pragma unroll
+                        for (int k = kParts - 1; k >= 0; --k) mma16<PT>(d, pa[k], b0, b1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[k] += d[k];
+                    } else {
+                        mma16<PT>(acc, pa[0], b0, b1);
+                    }
+                };
                 if constexpr (CT == T_I8) {
                     // four tokens' words of four columns, transposed: columns 4 (g + 8 jj) + i of tokens 2c, 2c + 1, 8 + 2c, 9 + 2c
 #pragma unroll
@@ -382,8 +417,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                         for (int i = 0; i < 4; ++i) {
                             uint32_t b0, b1;
                             i8_to_bf16(col[i], b0, b1);
-                            mma16<PT>(o[4 * jj + i], hi, b0, b1);
-                            if constexpr (kWide) mma16<PT>(o[4 * jj + i], lo, b0, b1);
+                            pv(o[4 * jj + i], b0, b1);
                         }
                     }
                 } else {
@@ -408,12 +442,8 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                         for (int j = 0; j < D / 16; ++j) {
                             uint32_t b[4];
                             ldsm_x4_t(va + place_of<D, CT>(t, 32 * j + x), b);
-                            mma16<PT>(o[2 * j], hi, b[0], b[1]);
-                            mma16<PT>(o[2 * j + 1], hi, b[2], b[3]);
-                            if constexpr (kWide) {
-                                mma16<PT>(o[2 * j], lo, b[0], b[1]);
-                                mma16<PT>(o[2 * j + 1], lo, b[2], b[3]);
-                            }
+                            pv(o[2 * j], b[0], b[1]);
+                            pv(o[2 * j + 1], b[2], b[3]);
                         }
                     } else {
 #pragma unroll 1
@@ -461,7 +491,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                 ml_s[(warp * 2 + 1) * kAtRows + g + 8 * e] = l[e];
             }
         }
-        __syncthreads();
+        const bool lost = __syncthreads_or(dead) != 0;
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -482,10 +512,15 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             const int d = CT == T_I8 ? 4 * (2 * c + k + 8 * (j >> 2)) + (j & 3) : 8 * j + 2 * c + k;
             return (g + 8 * e) * C::kPad + d;
         };
-        float* mine = join_s + (warp % C::kParts) * kAtRows * C::kPad;
+        // Behind the block's last unit the rings are free (every copy was waited for): a place for each warp.  Before, four
+        // warps take turns on one.
+        const bool idle = end == ue && !lost;
+        float* area = idle ? reinterpret_cast<float*>(smem + C::oRing) : join_s;
+        const int parts = idle ? W : C::kParts, turns = idle ? 1 : 4;
+        float* mine = area + (warp % parts) * kAtRows * C::kPad;
 #pragma unroll 1
-        for (int turn = 0; turn < 4; ++turn) {
-            if (warp / C::kParts == turn) {
+        for (int turn = 0; turn < turns; ++turn) {
+            if (warp / parts == turn) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     if (g + 8 * e < rows)
@@ -508,10 +543,13 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
         for (int k = tid; k < rows * (D / 4); k += C::kThreads) {
             const int r = k / (D / 4), d = k % (D / 4) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int w = 0; w < parts; w += C::kParts) {
 #pragma unroll
-            for (int w = 0; w < C::kParts; ++w) {
-                const float4 t = *reinterpret_cast<const float4*>(join_s + (w * kAtRows + r) * C::kPad + d);
-                v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+                for (int i = 0; i < C::kParts; ++i) {
+                    const float4 t = *reinterpret_cast<const float4*>(area + ((w + i) * kAtRows + r) * C::kPad + d);
+                    v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+                }
             }
             if (!whole) {
                 *reinterpret_cast<float4*>(part + 2 * A.part_rows + r * D + d) = v;
@@ -534,77 +572,148 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             if (!mbar_wait_bounded(bars + 8 * (k % C::kSlots), static_cast<uint32_t>(k / C::kSlots) & 1u, kAtWaitNs)) break;
 }
 
-// Rows of segments that several blocks share: the pieces' results weighted by
-// 2^(maximum - the largest) and added in the pieces' order, one block per row.
-constexpr int kJoinThreads = 128;
+// Segments that several blocks share: their pieces' results, weighted by 2^(maximum - the largest) and added in a fixed
+// order.  The grid has some blocks for each border between two shares.  A segment of p pieces has p - 1 borders inside, which
+// deal its rows among them: a border's work is about the same whether a few segments are in many pieces or many in two.
+// A row of few pieces is a warp's, of many the block's: eight warps, every eighth piece each, eight at a time.  Maximum, sum
+// and values are loaded together, so a row costs one round of loads per 8 (or 64) pieces.
+constexpr int kJoinWarps = 8, kJoinFew = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs A, int tile_rows, int unit)
+struct JoinRow {
+    static constexpr int kV = D / 32;
+    float m, l, acc[kV];
+};
+// Pieces from, from + step, .. of a row.
+template <int D>
+__device__ __forceinline__ void join_pieces(JoinRow<D>& R, const float* first, const float* others, size_t pf, int part_rows,
+                                            int row, int from, int step, int pieces, int lane)
 {
-    __shared__ float w_s[kAtMaxBlocks];
-    __shared__ float red_s[kJoinThreads / 32][D];
-    __shared__ float sum_s[kJoinThreads / 32], top_s[kJoinThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int t = static_cast<int>(blockIdx.x) / A.Hq, head = static_cast<int>(blockIdx.x) - t * A.Hq;
-    const int b = row_sequence(A.b.q_start, A.b.B, t, lane);
-    if (b >= A.b.B) return;
-    const SeqFacts f = seq_facts(A, b);
-    const int i = t - f.q0;
-    if (i < 0 || i >= f.n) return;
-    const int h = head / A.G, r = i * A.G + (head - h * A.G), tile = r / tile_rows, row = r - tile * tile_rows;
-    const int units = seq_units(f, unit);
-    const long long u0 = A.head[1 + b] + (static_cast<long long>(h) * seq_tiles(A, f, tile_rows) + tile) * units;
-    const long long share = A.head[0];
-    const int j0 = static_cast<int>(u0 / share), j1 = static_cast<int>((u0 + units - 1) / share);
-    if (j0 == j1) return;                       // one block's: written
-    const int pieces = j1 - j0 + 1;
-    const size_t pf = attn_part_floats(A.part_rows, D);
-    // (a block's first piece is in its first place; a piece that begins within the block in the second)
-    auto part = [&](int k) {
-        const int j = j0 + k;
-        return A.part + (static_cast<size_t>(j) * 2 + (j * share < u0 ? 1 : 0)) * pf;
-    };
-    float top = neg_inf();
-    for (int k = tid; k < pieces; k += kJoinThreads) {
-        w_s[k] = part(k)[row];
-        top = fmaxf(top, w_s[k]);
-    }
+    constexpr int kV = JoinRow<D>::kV, kBatch = 8;
+    R.m = neg_inf();
+    R.l = 0.0f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane == 0) top_s[warp] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
-    const float base = top == neg_inf() ? 0.0f : top;
-    float sum = 0.0f;
-    for (int k = tid; k < pieces; k += kJoinThreads) {
-        const float w = exp2_fast(w_s[k] - base);
-        w_s[k] = w;
-        sum += w * part(k)[A.part_rows + row];
-    }
+    for (int v = 0; v < kV; ++v) R.acc[v] = 0.0f;
+#pragma unroll 1
+    for (int k0 = from; k0 < pieces; k0 += step * kBatch) {
+        float pm[kBatch], pl[kBatch], pv[kBatch][kV];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) sum_s[warp] = sum;
-    __syncthreads();
-    sum = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+        for (int e = 0; e < kBatch; ++e) {
+            pm[e] = neg_inf();
+            if (k0 + step * e < pieces) {
+                const int k = k0 + step * e;
+                const float* p = k == 0 ? first : others + 2 * k * pf;
+                pm[e] = __ldcg(p + row);
+                pl[e] = __ldcg(p + part_rows + row);
+                const float* o = p + 2 * part_rows + row * D + kV * lane;
+                if constexpr (kV == 2) {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+                    pv[e][0] = v.x;
+                    pv[e][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kV; q += 4) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(o + q));
+                        pv[e][q] = v.x; pv[e][q + 1] = v.y; pv[e][q + 2] = v.z; pv[e][q + 3] = v.w;
+                    }
+                }
+            }
+        }
+        float top = R.m;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) top = fmaxf(top, pm[e]);
+        const float base = top == neg_inf() ? 0.0f : top, w = exp2_fast(R.m - base);
+        R.m = top;
+        R.l *= w;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) R.acc[v] *= w;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            if (pm[e] == neg_inf()) continue;                 // nothing was seen (or no such piece)
+            const float x = exp2_fast(pm[e] - base);
+            R.l += x * pl[e];
+#pragma unroll
+            for (int v = 0; v < kV; ++v) R.acc[v] += x * pv[e][v];
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnArgs A, int tile_rows, int unit)
+{
     constexpr int kV = D / 32;
-    float acc[kV] = {};
-#pragma unroll 4
-    for (int k = warp; k < pieces; k += kJoinThreads / 32) {
-        const float* p = part(k) + 2 * A.part_rows + static_cast<size_t>(row) * D;
-        const float w = w_s[k];
-#pragma unroll
-        for (int v = 0; v < kV; ++v) acc[v] += w * __ldcg(p + 32 * v + lane);
+    __shared__ __align__(16) float acc_s[kJoinWarps][D];
+    __shared__ float m_s[kJoinWarps], l_s[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    Layout lay;
+    if (A.b.B <= 32) lay = lane_layout(A, tile_rows, unit, lane);
+    else pdl_wait();
+    if (A.b.B > 32) {
+        lay.pre = A.head;
+        lay.total = A.head[A.b.B];
     }
+    const int share = block_share(lay.total, A.blocks, A.least), j = static_cast<int>(blockIdx.x);
+    const long long border = static_cast<long long>(j + 1) * share;
+    Segment sg = {};
+    bool inside = border < lay.total;
+    if (inside) {
+        sg = find_segment(A, lay, static_cast<int>(border), tile_rows, unit);
+        inside = sg.u0 != border;
+    }
+    if (A.b.B <= 32) pdl_wait();                // (every thread: the launch ends behind the one before it)
+    if (!inside) return;
+    const int j0 = sg.u0 / share, pieces = (sg.u0 + sg.units - 1) / share - j0 + 1;
+    const int rows = min(tile_rows, sg.f.n * A.G - sg.tile * tile_rows);
+    const size_t pf = attn_part_floats(A.part_rows, D);
+    // (a block's first piece is in its first place, a segment that begins within the block in the second)
+    const float* first = A.part + (static_cast<size_t>(j0) * 2 + (j0 * share < sg.u0 ? 1 : 0)) * pf;
+    const float* others = A.part + static_cast<size_t>(j0) * 2 * pf;
+    auto write = [&](const JoinRow<D>& R, int row) {
+        const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
+        const int rr = sg.tile * tile_rows + row, tok = rr / A.G;
+        const size_t y = (static_cast<size_t>(sg.f.q0 + tok) * A.Hq + sg.h * A.G + (rr - tok * A.G)) * D + kV * lane;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) red_s[warp][32 * v + lane] = acc[v];
-    __syncthreads();
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int d = tid; d < D; d += kJoinThreads) {
-        float v = 0.0f;
+        for (int v = 0; v < kV; ++v) store_typed(A.y, A.ytype, y + v, R.acc[v] * inv);
+    };
+    JoinRow<D> R;
+    const int stride = pieces - 1, mine = j - j0;             // this border's rows: mine, mine + stride, ..
+    if (pieces <= kJoinFew) {
+#pragma unroll 1
+        for (int row = mine + (static_cast<int>(blockIdx.y) * kJoinWarps + warp) * stride; row < rows;
+             row += static_cast<int>(gridDim.y) * kJoinWarps * stride) {
+            join_pieces<D>(R, first, others, pf, A.part_rows, row, 0, 1, pieces, lane);
+            write(R, row);
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int row = mine + static_cast<int>(blockIdx.y) * stride; row < rows; row += static_cast<int>(gridDim.y) * stride) {
+        join_pieces<D>(R, first, others, pf, A.part_rows, row, warp, kJoinWarps, pieces, lane);
+        if (lane == 0) {
+            m_s[warp] = R.m;
+            l_s[warp] = R.l;
+        }
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) v += red_s[w][d];
-        store_typed(A.y, A.ytype, (static_cast<size_t>(t) * A.Hq + head) * D + d, v * inv);
+        for (int v = 0; v < kV; ++v) acc_s[warp][kV * lane + v] = R.acc[v];
+        __syncthreads();
+        if (warp == 0) {
+            float top = m_s[0];
+#pragma unroll
+            for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, m_s[w]);
+            const float base = top == neg_inf() ? 0.0f : top;
+            R.l = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) R.acc[v] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float x = exp2_fast(m_s[w] - base);
+                R.l += x * l_s[w];
+#pragma unroll
+                for (int v = 0; v < kV; ++v) R.acc[v] += x * acc_s[w][kV * lane + v];
+            }
+            write(R, row);
+        }
+        __syncthreads();
     }
 }
 
@@ -627,6 +736,8 @@ cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
     if (e == cudaSuccess) e = encode_kv_map(&a.kmap, a, a.c.k, C::kBox, kAtUnit);
     if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, C::kBox, kAtUnit);
     if (e != cudaSuccess) return e;
+    a.blocks = grid;
+    a.least = C::kWarps;                        // a unit for each warp
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -682,10 +793,11 @@ cudaError_t encode_kv_map(CUtensorMap* map, const AttnArgs& a, const void* base,
 
 cudaError_t launch_attn_join(const AttnArgs& a, int rows, int unit, cudaStream_t s)
 {
+    if (a.blocks < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(a.T) * static_cast<unsigned>(a.Hq));
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.blocks - 1), a.part_rows <= 16 ? 1u : 4u);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     dependent(cfg, attr, true);
     return cudaLaunchKernelEx(&cfg, a.c.D == 64 ? attn_join_kernel<64> : a.c.D == 128 ? attn_join_kernel<128> : attn_join_kernel<256>,

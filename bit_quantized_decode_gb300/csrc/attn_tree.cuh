@@ -32,66 +32,122 @@ __device__ __forceinline__ SeqFacts seq_facts(const AttnArgs& A, int b)
 __device__ __forceinline__ int seq_units(const SeqFacts& f, int unit) { return f.n > 0 ? (f.len + unit - 1) / unit : 0; }
 __device__ __forceinline__ int seq_tiles(const AttnArgs& A, const SeqFacts& f, int rows) { return (f.n * A.G + rows - 1) / rows; }
 
-// Prefix sums of the sequences' units into pre[0 .. B], by the whole block; pre needs kAtMaxSeq + 1 places.
-template <int NT>
-__device__ __forceinline__ void seq_prefix(const AttnArgs& A, int rows, int unit, long long* pre, long long* warp_s)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kW = NT / 32;
-    long long carry = 0;
-    for (int base = 0; base < A.b.B; base += NT) {
-        const int b = base + tid;
-        long long v = 0;
-        if (b < A.b.B) {
-            const SeqFacts f = seq_facts(A, b);
-            v = static_cast<long long>(A.c.Hkv) * seq_tiles(A, f, rows) * seq_units(f, unit);
-        }
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long w = __shfl_up_sync(0xffffffffu, v, off);
-            if (lane >= off) v += w;
-        }
-        if (lane == 31) warp_s[warp] = v;
-        __syncthreads();
-        long long before = carry, all = 0;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            if (w < warp) before += warp_s[w];
-            all += warp_s[w];
-        }
-        if (b < A.b.B) pre[b + 1] = before + v;
-        carry += all;
-        __syncthreads();
-    }
-    if (tid == 0) pre[0] = 0;
-    __syncthreads();
-}
-
 // One (sequence, key head, tile of rows): its units are [u0, u0 + units) of the call's.
 struct Segment {
-    long long u0;
+    int u0;
     int units;
     int b, h, tile;
     SeqFacts f;
 };
-__device__ __forceinline__ Segment find_segment(const AttnArgs& A, const long long* pre, long long u, int rows, int unit)
+
+// How a call's units lie (fewer than 2^31 - 1024: the host's check): sequences one behind the other, in each its key heads, in each its tiles of rows.  Up to 32
+// sequences every warp holds them itself, one to a lane (one round of loads, no barrier); more lie as prefix sums in shared
+// memory.  All calls are a whole warp's.
+struct Layout {
+    const int* pre;           // [B + 1] in shared memory; null: in the lanes
+    int mine;            // units before this lane's sequence
+    SeqFacts f;               // this lane's sequence
+    int total;
+};
+__device__ __forceinline__ int seq_cost(const AttnArgs& A, const SeqFacts& f, int rows, int unit)
 {
-    int lo = 0, hi = A.b.B;                     // pre[lo] <= u < pre[hi]
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (pre[m] <= u) lo = m;
-        else hi = m;
+    return A.c.Hkv * seq_tiles(A, f, rows) * seq_units(f, unit);
+}
+__device__ __forceinline__ int warp_scan(int v, int lane)
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += w;
     }
+    return v;
+}
+__device__ __forceinline__ Layout lane_layout(const AttnArgs& A, int rows, int unit, int lane)
+{
+    Layout L;
+    L.pre = nullptr;
+    int v = 0;
+    L.f = SeqFacts{0, 0, 0, 0};
+    if (lane < A.b.B) {
+        L.f = seq_facts(A, lane);
+        v = seq_cost(A, L.f, rows, unit);
+    }
+    const int upto = warp_scan(v, lane);
+    L.mine = upto - v;
+    L.total = __shfl_sync(0xffffffffu, upto, 31);
+    return L;
+}
+// By the whole block of NT threads; pre needs kAtMaxSeq + 1 places, warp_s one for each warp.
+template <int NT>
+__device__ __forceinline__ Layout block_layout(const AttnArgs& A, int rows, int unit, int* pre, int* warp_s)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (A.b.B <= 32) return lane_layout(A, rows, unit, lane);
+    int carry = 0;
+    for (int base = 0; base < A.b.B; base += NT) {
+        const int b = base + tid;
+        const int v = warp_scan(b < A.b.B ? seq_cost(A, seq_facts(A, b), rows, unit) : 0, lane);
+        if (lane == 31) warp_s[warp] = v;
+        __syncthreads();
+        int before = carry;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < warp) before += warp_s[w];
+            carry += warp_s[w];
+        }
+        if (b < A.b.B) pre[b + 1] = before + v;
+        __syncthreads();
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+    Layout L;
+    L.pre = pre;
+    L.mine = 0;
+    L.f = SeqFacts{0, 0, 0, 0};
+    L.total = pre[A.b.B];
+    return L;
+}
+__device__ __forceinline__ SeqFacts facts_of(const Layout& L, int b)
+{
+    SeqFacts f;
+    f.q0 = __shfl_sync(0xffffffffu, L.f.q0, b);
+    f.n = __shfl_sync(0xffffffffu, L.f.n, b);
+    f.ctx = __shfl_sync(0xffffffffu, L.f.ctx, b);
+    f.len = __shfl_sync(0xffffffffu, L.f.len, b);
+    return f;
+}
+__device__ __forceinline__ Segment find_segment(const AttnArgs& A, const Layout& L, int u, int rows, int unit)
+{
     Segment s;
-    s.b = lo;
-    s.f = seq_facts(A, lo);
+    int first;
+    if (L.pre == nullptr) {                     // the last sequence that begins at u or before
+        const int lane = threadIdx.x & 31;
+        s.b = __popc(__ballot_sync(0xffffffffu, lane < A.b.B && L.mine <= u)) - 1;
+        s.f = facts_of(L, s.b);
+        first = __shfl_sync(0xffffffffu, L.mine, s.b);
+    } else {
+        int lo = 0, hi = A.b.B;                 // pre[lo] <= u < pre[hi]
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if (L.pre[m] <= u) lo = m;
+            else hi = m;
+        }
+        s.b = lo;
+        s.f = seq_facts(A, lo);
+        first = L.pre[lo];
+    }
     s.units = seq_units(s.f, unit);
     const int tiles = seq_tiles(A, s.f, rows);
-    const long long seg = (u - pre[lo]) / s.units;
-    s.h = static_cast<int>(seg / tiles);
-    s.tile = static_cast<int>(seg - static_cast<long long>(s.h) * tiles);
-    s.u0 = pre[lo] + seg * s.units;
+    const int seg = (u - first) / s.units;
+    s.h = seg / tiles;
+    s.tile = seg - s.h * tiles;
+    s.u0 = first + seg * s.units;
     return s;
+}
+// Units of each block.  (The sum over all blocks stays below 2^31: the host's check.)
+__device__ __forceinline__ int block_share(int total, int blocks, int least)
+{
+    return max((total + blocks - 1) / blocks, least);
 }
 
 // Box of a 3-D tensor map -> shared memory.
@@ -102,6 +158,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
             dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 // Bulk copy without a cache hint.
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
