@@ -12,6 +12,9 @@
 
 namespace w4k {
 
+// Every launch here is a programmatic dependent of the kernel before it: the kernels touch no memory before their dependency
+// wait (the joining launch of the attention reads what its first launch has waited for), so that is legal behind anything.
+
 constexpr int T_I8 = 3;                         // W4_I8: a cache of INT8 codes
 
 // One layer's paged cache and the rows of a call (w4_kv_cache, w4_kv_batch).
@@ -47,8 +50,9 @@ struct AppendArgs {
     float eps;
     void* q;                  // [T][Hq][D]
     int qtype;
+    int per;                  // loads of heads to a warp (set by the launch)
 };
-cudaError_t launch_kv_append(const AppendArgs& a, int xtype, bool pdl, cudaStream_t s);
+cudaError_t launch_kv_append(AppendArgs& a, int xtype, cudaStream_t s);
 cudaError_t launch_rope_table(const double* inv_freq, double factor, double scale, int positions, int half, float* turns,
                               cudaStream_t s);
 
@@ -79,15 +83,14 @@ struct AttnArgs {
 __host__ __device__ inline size_t attn_head_bytes(int B) { return (4 * (static_cast<size_t>(B) + 1) + 127) / 128 * 128; }
 // A partial result: running maxima, sums, and rows of D.
 __host__ __device__ inline size_t attn_part_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
-cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s);
-cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s);
+cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, cudaStream_t s);
+cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, cudaStream_t s);
 // Joins the partial results of either kernel (tiles of `rows` rows, units of `unit` tokens).
 cudaError_t launch_attn_join(const AttnArgs& a, int rows, int unit, cudaStream_t s);
 cudaError_t encode_kv_map(CUtensorMap* map, const AttnArgs& a, const void* base, int box_bytes, int box_rows);
 
 // ------------------------------------------------------ logits (logits.cu)
 constexpr int kLgThreads = 256;
-constexpr int kLgSlice = 8192;                  // vocabulary entries of a block
 constexpr int kLgMaxBias = 1024;
 struct LogitArgs {
     const void* x;            // [R] rows of ld values
@@ -108,10 +111,10 @@ struct LogitArgs {
     const int* drafts;        // [R], or null
     const unsigned long long* mask;   // [R], or null
     const unsigned* allowed;  // [R][ceil(V / 32)], or null
-    int slices;
-    int vec;                  // rows on 16-byte boundaries
+    int slices;               // blocks of a copied row (set by the launch)
+    int vec;                  // 16-byte words of x are such words of y
 };
-cudaError_t launch_logits(const LogitArgs& a, int type, bool pdl, cudaStream_t s);
+cudaError_t launch_logits(LogitArgs& a, int type, cudaStream_t s);
 
 // -------------------------------------------------------- device helpers
 #ifdef __CUDACC__

@@ -138,7 +138,7 @@ w4_status w4_kv_append(const w4_kv_cache* c, const w4_kv_batch* b, const w4_rope
     a.eps = eps;
     a.q = q;
     a.qtype = q_type;
-    return cuda_status(launch_kv_append(a, x_type, (flags & W4_FLAG_PDL) != 0, reinterpret_cast<cudaStream_t>(s)));
+    return cuda_status(launch_kv_append(a, x_type, reinterpret_cast<cudaStream_t>(s)));
 }
 
 size_t w4_tree_attention_workspace_bytes(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq)
@@ -183,8 +183,7 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     a.err = d.err;
     const int grid = d.sms < kAtMaxBlocks ? d.sms : kAtMaxBlocks;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-    const bool pdl = (flags & W4_FLAG_PDL) != 0;
-    const cudaError_t e = p.tc ? launch_attn_tc(a, q_type, grid, pdl, cs) : launch_attn_tree(a, q_type, grid, pdl, cs);
+    const cudaError_t e = p.tc ? launch_attn_tc(a, q_type, grid, cs) : launch_attn_tree(a, q_type, grid, cs);
     if (e != cudaSuccess) return W4_ERR_CUDA;
     return cuda_status(p.tc ? launch_attn_join(a, kAtTcRows, kAtTcUnit, cs) : launch_attn_join(a, kAtRows, kAtUnit, cs));
 }
@@ -196,7 +195,7 @@ w4_status w4_logits_adjust(const w4_logit_rules* u, const void* logits, int type
     if (!u || R < 0 || u->V < 0 || u->S < 0 || u->cap < 0 || u->n_bias < 0 || !elem_type(type) || (flags & ~W4_FLAG_PDL) != 0)
         return W4_ERR_INVALID_ARG;
     if (ld < u->V || ld_out < u->V || (drafts && !row_start) || (mask && !drafts)) return W4_ERR_INVALID_ARG;
-    if (R > W4_MAX_TOKENS || u->V > (1 << 24) || u->n_bias > W4_MAX_BIASES || u->S > W4_MAX_TOKENS) return W4_ERR_UNSUPPORTED_SHAPE;
+    if (R > W4_MAX_TOKENS || u->V > (1 << 24) || static_cast<long long>(R) * u->V > (1ll << 42) || u->n_bias > W4_MAX_BIASES || u->S > W4_MAX_TOKENS) return W4_ERR_UNSUPPORTED_SHAPE;
     if (R == 0 || u->V == 0 || u->S == 0) return W4_OK;
     const bool hist = u->cap > 0, bias = u->n_bias > 0;
     if (!logits || !out || (hist && (!u->ids || !u->length)) || (bias && (!u->bias_ids || !u->bias))) return W4_ERR_INVALID_ARG;
@@ -227,10 +226,9 @@ w4_status w4_logits_adjust(const w4_logit_rules* u, const void* logits, int type
     a.drafts = drafts;
     a.mask = mask;
     a.allowed = allowed;
-    a.slices = (u->V + kLgSlice - 1) / kLgSlice;
-    a.vec = aligned(logits, 16) && aligned(out, 16) && ld * eb % 16 == 0 && ld_out * eb % 16 == 0;
-    if (static_cast<long long>(R) * a.slices > 0x7fffffffll) return W4_ERR_UNSUPPORTED_SHAPE;
-    return cuda_status(launch_logits(a, type, (flags & W4_FLAG_PDL) != 0, reinterpret_cast<cudaStream_t>(s)));
+const size_t between = (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(logits)) % 16;
+    a.vec = between == 0 && (R == 1 || ((ld - ld_out) * static_cast<long long>(eb)) % 16 == 0);
+    return cuda_status(launch_logits(a, type, reinterpret_cast<cudaStream_t>(s)));
 }
 
 }  // extern "C"

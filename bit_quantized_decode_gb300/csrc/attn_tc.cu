@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
 }
 
 template <int D, int CT, int QT, bool kWide>
-cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 {
     using C = Tc<D, CT>;
     auto kern = attn_tc_kernel<D, CT, QT, kWide>;
@@ -702,35 +702,33 @@ cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::smem(a.b.B);
     cfg.stream = s;
-    if (pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int D, int CT, int QT>
-cudaError_t launch_w(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch_w(AttnArgs& a, int grid, cudaStream_t s)
 {
-    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, pdl, s) : launch<D, CT, QT, false>(a, grid, pdl, s);
+    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, s) : launch<D, CT, QT, false>(a, grid, s);
 }
 
 template <int D>
-cudaError_t launch_d(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch_d(AttnArgs& a, int qtype, int grid, cudaStream_t s)
 {
-    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, pdl, s);
-    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, pdl, s);
-    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, pdl, s) : launch_w<D, T_I8, T_BF16>(a, grid, pdl, s);
+    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, s);
+    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, s);
+    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, s) : launch_w<D, T_I8, T_BF16>(a, grid, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, cudaStream_t s)
 {
-    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, pdl, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, pdl, s)
-                                                                            : launch_d<256>(a, qtype, grid, pdl, s);
+    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, s)
+                                                                            : launch_d<256>(a, qtype, grid, s);
 }
 
 }  // namespace w4k

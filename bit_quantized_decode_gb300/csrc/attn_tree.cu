@@ -717,9 +717,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     }
 }
 
-void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, bool pdl)
+void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr)
 {
-    if (!pdl) return;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
@@ -727,7 +726,7 @@ void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, bool pdl)
 }
 
 template <int D, int CT, int QT, bool kWide>
-cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 {
     using C = At<D, CT>;
     auto kern = attn_tree_kernel<D, CT, QT, kWide>;
@@ -744,22 +743,22 @@ cudaError_t launch(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::smem(a.b.B);
     cfg.stream = s;
-    dependent(cfg, attr, pdl);
+    dependent(cfg, attr);
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int D, int CT, int QT>
-cudaError_t launch_w(AttnArgs& a, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch_w(AttnArgs& a, int grid, cudaStream_t s)
 {
-    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, pdl, s) : launch<D, CT, QT, false>(a, grid, pdl, s);
+    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, s) : launch<D, CT, QT, false>(a, grid, s);
 }
 
 template <int D>
-cudaError_t launch_d(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch_d(AttnArgs& a, int qtype, int grid, cudaStream_t s)
 {
-    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, pdl, s);
-    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, pdl, s);
-    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, pdl, s) : launch_w<D, T_I8, T_BF16>(a, grid, pdl, s);
+    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, s);
+    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, s);
+    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, s) : launch_w<D, T_I8, T_BF16>(a, grid, s);
 }
 
 }  // namespace
@@ -799,15 +798,15 @@ cudaError_t launch_attn_join(const AttnArgs& a, int rows, int unit, cudaStream_t
     cfg.gridDim = dim3(static_cast<unsigned>(a.blocks - 1), a.part_rows <= 16 ? 1u : 4u);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
-    dependent(cfg, attr, true);
+    dependent(cfg, attr);
     return cudaLaunchKernelEx(&cfg, a.c.D == 64 ? attn_join_kernel<64> : a.c.D == 128 ? attn_join_kernel<128> : attn_join_kernel<256>,
                               a, rows, unit);
 }
 
-cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, bool pdl, cudaStream_t s)
+cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, cudaStream_t s)
 {
-    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, pdl, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, pdl, s)
-                                                                            : launch_d<256>(a, qtype, grid, pdl, s);
+    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, s)
+                                                                            : launch_d<256>(a, qtype, grid, s);
 }
 
 }  // namespace w4k

@@ -8,12 +8,13 @@
 //
 // D / 8 lanes take a head, eight values to a lane: a lane of the half layout
 // holds four values and their four partners, so a rotation needs no exchange,
-// and a pair's (cos, sin) is read once.  A warp takes 4, 2 or 1 heads of a
-// token (D 64, 128, 256).  An INT8 code hangs on the last bit of a value, so a
-// key for an INT8 cache is rotated with exact products and a compensated sum
-// (rounded once), and the squares are summed in compensated pairs as in the
-// other fused norms.  Memory bound for prompts; for a few tokens the chain of
-// loads (row's sequence, its length, the page) is.
+// and a pair's (cos, sin) is read once for all heads of a warp.  A warp takes 4, 2 or
+// 1 heads of a token at a time (D 64, 128, 256).  An INT8 code hangs on the last bit of a
+// value, so a key for an INT8 cache is rotated with exact products and a compensated
+// sum (rounded once), and its squares are summed in compensated pairs as in the other
+// fused norms; numbers that are rounded to 16 bits take plain fp32 sums and rsqrtf
+// (2^-20 of the value at most).  Prompts are bound by memory and, with norms, by
+// instructions; a few tokens by the chain of loads (row's sequence, its length, the page).
 #include "attention.h"
 #include "fusion.cuh"
 #include "ptx.cuh"
@@ -74,72 +75,112 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
     pdl_launch_dependents();
     pdl_wait();
     const int H = A.Hq + 2 * A.c.Hkv;
-    const int groups = (H + kHeads - 1) / kHeads;
+    const int groups = (H + kHeads - 1) / kHeads;             // warps' loads of a token's heads
+    const int parts = (groups + A.per - 1) / A.per;           // warps of a token
     const long long task = (static_cast<long long>(blockIdx.x) * kKaThreads + threadIdx.x) >> 5;
-    if (task >= static_cast<long long>(A.T) * groups) return;
-    const int t = static_cast<int>(task / groups);
-    const int head = static_cast<int>(task - static_cast<long long>(t) * groups) * kHeads + lane / kLanes;
+    if (task >= static_cast<long long>(A.T) * parts) return;
+    const int t = static_cast<int>(task / parts);
+    const int g0 = static_cast<int>(task - static_cast<long long>(t) * parts) * A.per, g1 = min(g0 + A.per, groups);
     const int u = lane % kLanes;                // eight values of the head
 
-    // the values, as they lie: of a rotated half-layout unit 4u.. and rot/2 + 4u.., else 8u..
-    const bool turned = 8 * u < A.rot && head < A.Hq + A.c.Hkv;
-    const bool split = turned && !A.interleaved;
-    const int at0 = split ? 4 * u : 8 * u, at1 = split ? A.rot / 2 + 4 * u : 8 * u + 4;
-    float x[8];
-    const bool have = head < H;
-    const size_t base = static_cast<size_t>(t) * A.ld + static_cast<size_t>(have ? head : 0) * D;
-    load4<XT>(A.x, base + at0, x);
-    load4<XT>(A.x, base + at1, x + 4);
+    // a head's values as they lie: of a rotated half-layout unit 4u.. and rot/2 + 4u.., else 8u..
+    const int rotated = A.Hq + A.c.Hkv;
+    const size_t row = static_cast<size_t>(t) * A.ld;
+    auto load = [&](int g, float* x) {
+        const int head = g * kHeads + lane / kLanes;
+        const bool split = 8 * u < A.rot && head < rotated && !A.interleaved;
+        const size_t base = row + static_cast<size_t>(head < H ? head : 0) * D;
+        load4<XT>(A.x, base + (split ? 4 * u : 8 * u), x);
+        load4<XT>(A.x, base + (split ? A.rot / 2 + 4 * u : 8 * u + 4), x + 4);
+    };
+    float ahead[8];
+    load(g0, ahead);
 
     const int b = row_sequence(A.b.q_start, A.b.B, t, lane);
     if (b >= A.b.B) return;                     // behind the last sequence
     const int i = t - __ldg(A.b.q_start + b);
     if (i < 0) return;
     const long long place = static_cast<long long>(max(__ldg(A.b.ctx + b), 0)) + i;
-
-    const bool is_q = head < A.Hq, is_k = !is_q && head < A.Hq + A.c.Hkv;
     const bool i8 = A.c.type == T_I8;
-    const float* g = is_q ? A.q_norm : is_k ? A.k_norm : nullptr;
-    if (A.q_norm != nullptr || A.k_norm != nullptr) {
-        float hi = 0.0f, lo = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sq_acc(x[k], hi, lo);
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) {
-            const float h2 = __shfl_xor_sync(0xffffffffu, hi, off), l2 = __shfl_xor_sync(0xffffffffu, lo, off);
-            pair_merge(hi, lo, h2, l2);
-        }
-        hi = __shfl_sync(0xffffffffu, hi, lane - u);          // (the same sum in every lane of the head)
-        lo = __shfl_sync(0xffffffffu, lo, lane - u);
-        if (g != nullptr) {
-            const float r = rms_scale(hi, lo, D, A.eps);
-            float w[8];
-            load4<T_F32>(g, at0, w);
-            load4<T_F32>(g, at1, w + 4);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(__fmul_rn(x[k], r), w[k]);
-        }
-    }
     bool lost = false;                          // a position that the table does not have
+    float cs[8];                                // (cos, sin) of pairs 4u .. 4u + 3
     if (A.rot > 0) {
         const long long p = A.pos != nullptr ? __ldg(A.pos + t) : place;
         lost = p < 0 || p >= A.positions;
-        if (turned) {
-            float cs[8], pa[4], pb[4];          // (cos, sin) of pairs 4u .. 4u + 3; the pairs
+        if (8 * u < A.rot) {
             load4<T_F32>(A.turns, static_cast<size_t>(lost ? 0 : p) * A.rot + 8 * u, cs);
             load4<T_F32>(A.turns, static_cast<size_t>(lost ? 0 : p) * A.rot + 8 * u + 4, cs + 4);
+            if (lost)
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) cs[k] = __int_as_float(0x7fc00000);
+        }
+    }
+    // the page; a place past the table, or a page that the cache does not have, is not written
+    const long long pi = place >> A.c.lg;
+    const int page = pi < A.b.max_pages ? __ldg(A.b.table + static_cast<size_t>(b) * A.b.max_pages + pi) : -1;
+    const bool stored = page >= 0 && page < A.c.pages;
+    const size_t slot0 = static_cast<size_t>(stored ? page : 0) * A.c.Hkv * A.c.page + static_cast<size_t>(place & (A.c.page - 1));
+
+#pragma unroll 1
+    for (int g = g0; g < g1; ++g) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = ahead[k];
+        if (g + 1 < g1) load(g + 1, ahead);
+        const int head = g * kHeads + lane / kLanes;
+        const bool have = head < H, is_q = head < A.Hq, is_k = !is_q && head < rotated;
+        const bool turned = 8 * u < A.rot && head < rotated, split = turned && !A.interleaved;
+        const int at0 = split ? 4 * u : 8 * u, at1 = split ? A.rot / 2 + 4 * u : 8 * u + 4;
+        // codes hang on the last bit of an INT8 cache's keys; what is rounded to 16 bits takes plain fp32 sums
+        const bool coded = i8 && g * kHeads < rotated && (g + 1) * kHeads > A.Hq;     // (of the whole warp)
+        const float* w_n = is_q ? A.q_norm : is_k ? A.k_norm : nullptr;
+        if ((A.q_norm != nullptr || A.k_norm != nullptr) && g * kHeads < rotated) {
+            float r;
+            if (coded) {
+                float hi = 0.0f, lo = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sq_acc(x[k], hi, lo);
+#pragma unroll
+                for (int off = kLanes / 2; off > 0; off >>= 1) {
+                    const float h2 = __shfl_xor_sync(0xffffffffu, hi, off), l2 = __shfl_xor_sync(0xffffffffu, lo, off);
+                    pair_merge(hi, lo, h2, l2);
+                }
+                hi = __shfl_sync(0xffffffffu, hi, lane - u);  // (the same sum in every lane of the head)
+                lo = __shfl_sync(0xffffffffu, lo, lane - u);
+                r = rms_scale(hi, lo, D, A.eps);
+            } else {
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum = __fmaf_rn(x[k], x[k], sum);
+#pragma unroll
+                for (int off = kLanes / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                r = rsqrtf(__fmaf_rn(sum, 1.0f / D, A.eps));
+            }
+            if (w_n != nullptr) {
+                float w[8];
+                load4<T_F32>(w_n, at0, w);
+                load4<T_F32>(w_n, at1, w + 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(__fmul_rn(x[k], r), w[k]);
+            }
+        }
+        if (turned) {
+            float pa[4], pb[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) pa[k] = split ? x[k] : x[2 * k], pb[k] = split ? x[4 + k] : x[2 * k + 1];
+            if (coded) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float c = lost ? __int_as_float(0x7fc00000) : cs[2 * k], s = cs[2 * k + 1];
-                const float a = pa[k], v = pb[k];
-                if (i8 && is_k) {
-                    pa[k] = dot2_once(a, c, -v, s);
-                    pb[k] = dot2_once(v, c, a, s);
-                } else {
-                    pa[k] = __fmaf_rn(a, c, -__fmul_rn(v, s));
-                    pb[k] = __fmaf_rn(v, c, __fmul_rn(a, s));
+                for (int k = 0; k < 4; ++k) {
+                    const float a = pa[k], v = pb[k];
+                    pa[k] = dot2_once(a, cs[2 * k], -v, cs[2 * k + 1]);
+                    pb[k] = dot2_once(v, cs[2 * k], a, cs[2 * k + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float a = pa[k], v = pb[k];
+                    pa[k] = __fmaf_rn(a, cs[2 * k], -__fmul_rn(v, cs[2 * k + 1]));
+                    pb[k] = __fmaf_rn(v, cs[2 * k], __fmul_rn(a, cs[2 * k + 1]));
                 }
             }
             x[0] = pa[0];
@@ -151,66 +192,68 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
             x[6] = split ? pb[2] : pa[3];
             x[7] = pb[3];
         }
-    }
-    if (is_q && have) {
-        uint16_t* q = static_cast<uint16_t*>(A.q) + (static_cast<size_t>(t) * A.Hq + head) * D;
-        *reinterpret_cast<uint2*>(q + at0) = make_uint2(pack16(A.qtype, x[0], x[1]), pack16(A.qtype, x[2], x[3]));
-        *reinterpret_cast<uint2*>(q + at1) = make_uint2(pack16(A.qtype, x[4], x[5]), pack16(A.qtype, x[6], x[7]));
-    }
-    // the page; a place past the table, or a page that the cache does not have, is not written
-    const long long pi = place >> A.c.lg;
-    const int page = pi < A.b.max_pages ? __ldg(A.b.table + static_cast<size_t>(b) * A.b.max_pages + pi) : -1;
-    const bool store = have && !is_q && page >= 0 && page < A.c.pages;
-    const int hk = is_k ? head - A.Hq : head - A.Hq - A.c.Hkv;
-    const size_t slot = (static_cast<size_t>(store ? page : 0) * A.c.Hkv + (store ? hk : 0)) * A.c.page +
-                        static_cast<size_t>(place & (A.c.page - 1));
-    if (!i8) {
-        if (store) {
-            uint16_t* d = static_cast<uint16_t*>(is_k ? A.c.k : A.c.v) + slot * D;
-            *reinterpret_cast<uint2*>(d + at0) = make_uint2(pack16(A.c.type, x[0], x[1]), pack16(A.c.type, x[2], x[3]));
-            *reinterpret_cast<uint2*>(d + at1) = make_uint2(pack16(A.c.type, x[4], x[5]), pack16(A.c.type, x[6], x[7]));
+        const int hk = is_k ? head - A.Hq : head - rotated;
+        const size_t slot = slot0 + static_cast<size_t>(is_q || !have ? 0 : hk) * A.c.page;
+        const bool store = have && !is_q && stored;
+        if (is_q || (store && !i8)) {
+            const int type = is_q ? A.qtype : A.c.type;
+            uint16_t* d = is_q ? static_cast<uint16_t*>(A.q) + (static_cast<size_t>(t) * A.Hq + head) * D
+                               : static_cast<uint16_t*>(is_k ? A.c.k : A.c.v) + slot * D;
+            const uint2 lo = make_uint2(pack16(type, x[0], x[1]), pack16(type, x[2], x[3]));
+            const uint2 hi = make_uint2(pack16(type, x[4], x[5]), pack16(type, x[6], x[7]));
+            if (split) {
+                *reinterpret_cast<uint2*>(d + at0) = lo;
+                *reinterpret_cast<uint2*>(d + at1) = hi;
+            } else {
+                *reinterpret_cast<uint4*>(d + at0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
         }
-        return;
+        if (!i8 || (g + 1) * kHeads <= A.Hq) continue;        // (of the whole warp)
+        float top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        if (store) {
+            const A8Scale ks = a8_scale(top);
+            uint2 q = quant8(x, ks);
+            const bool nan = lost && is_k;
+            if (nan) q = make_uint2(0u, 0u);
+            int8_t* d = static_cast<int8_t*>(is_k ? A.c.k : A.c.v) + slot * D;
+            *reinterpret_cast<uint32_t*>(d + at0) = q.x;
+            *reinterpret_cast<uint32_t*>(d + at1) = q.y;
+            if (u == 0) (is_k ? A.c.ks : A.c.vs)[slot] = nan ? __int_as_float(0x7fc00000) : ks.s;
+        }
+        __syncwarp();
     }
-    float top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (!store) return;
-    const A8Scale ks = a8_scale(top);
-    uint2 q = quant8(x, ks);
-    lost = lost && is_k;
-    if (lost) q = make_uint2(0u, 0u);
-    int8_t* d = static_cast<int8_t*>(is_k ? A.c.k : A.c.v) + slot * D;
-    *reinterpret_cast<uint32_t*>(d + at0) = q.x;
-    *reinterpret_cast<uint32_t*>(d + at1) = q.y;
-    if (u == 0) (is_k ? A.c.ks : A.c.vs)[slot] = lost ? __int_as_float(0x7fc00000) : ks.s;
 }
 
 template <int XT, int D>
-cudaError_t launch(const AppendArgs& a, bool pdl, cudaStream_t s)
+cudaError_t launch(AppendArgs& a, cudaStream_t s)
 {
-    constexpr int kHeads = 32 / (D / 8);
-    const long long tasks = static_cast<long long>(a.T) * ((a.Hq + 2 * a.c.Hkv + kHeads - 1) / kHeads);
+    // Few tokens: a warp for every load of heads.  Many: a warp takes more of a token's heads (the token's lookups once),
+    // as long as the SMs keep some 32 warps each.
+    constexpr int kHeads = 32 / (D / 8), kWarps = 152 * 32;
+    const long long groups = (a.Hq + 2 * a.c.Hkv + kHeads - 1) / kHeads;
+    const long long per = static_cast<long long>(a.T) * groups / kWarps;
+    a.per = static_cast<int>(per < 1 ? 1 : per < groups ? per : groups);
+    const long long tasks = static_cast<long long>(a.T) * ((groups + a.per - 1) / a.per);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((tasks * 32 + kKaThreads - 1) / kKaThreads));
     cfg.blockDim = dim3(kKaThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    if (pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kv_append_kernel<XT, D>, a);
 }
 
 template <int XT>
-cudaError_t launch_d(const AppendArgs& a, bool pdl, cudaStream_t s)
+cudaError_t launch_d(AppendArgs& a, cudaStream_t s)
 {
-    return a.c.D == 64 ? launch<XT, 64>(a, pdl, s) : a.c.D == 128 ? launch<XT, 128>(a, pdl, s) : launch<XT, 256>(a, pdl, s);
+    return a.c.D == 64 ? launch<XT, 64>(a, s) : a.c.D == 128 ? launch<XT, 128>(a, s) : launch<XT, 256>(a, s);
 }
 
 // (cos, sin) of position * factor * inv_freq, times scale: angles of far positions
@@ -227,9 +270,9 @@ __global__ void rope_table_kernel(const double* inv_freq, double factor, double 
 
 }  // namespace
 
-cudaError_t launch_kv_append(const AppendArgs& a, int xtype, bool pdl, cudaStream_t s)
+cudaError_t launch_kv_append(AppendArgs& a, int xtype, cudaStream_t s)
 {
-    return xtype == T_F32 ? launch_d<T_F32>(a, pdl, s) : xtype == T_F16 ? launch_d<T_F16>(a, pdl, s) : launch_d<T_BF16>(a, pdl, s);
+    return xtype == T_F32 ? launch_d<T_F32>(a, s) : xtype == T_F16 ? launch_d<T_F16>(a, s) : launch_d<T_BF16>(a, s);
 }
 
 cudaError_t launch_rope_table(const double* inv_freq, double factor, double scale, int positions, int half, float* turns,
