@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
     pdl_wait();
     pdl_launch_dependents();                    // (this block holds its tensor memory; the joining launch reads this one's inputs early)
     const Layout lay = block_layout<C::kThreads>(A, kTcRows, kTcUnit, pre_s, reinterpret_cast<int*>(smem + C::oWarpSum));
-    const int total = lay.total, share = block_share(total, A.blocks, A.least);
     if (blockIdx.x == 0 && A.b.B > 32)          // for the joining launch
         for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[b] = pre_s[b];
-    const int us = min(static_cast<int>(min(static_cast<long long>(blockIdx.x) * share, 0x7fffffffll)), total), ue = us + min(share, total - us);
+    const int2 range = block_units(lay, A, static_cast<int>(blockIdx.x), kTcUnit);
+    const int us = range.x, ue = range.y;
     if (us >= ue) {
         if (warp == 1) tmem_dealloc(tb, C::kCols);
         return;

@@ -40,7 +40,7 @@ struct At {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRing = 192 * 1024 / (kWarps * kSlot);
     static constexpr int kSlots = kRing > 6 ? 6 : kRing;      // units ahead of a warp
-    static constexpr int kParts = kWarps / 4;                 // joined row blocks: four warps take turns on one
+    static constexpr int kParts = kWarps == 4 ? 1 : 2;        // joined row blocks: warps take turns on one
     static constexpr int kPad = D + 8;                        // floats of a joined row: rows spread over the banks
     // shared memory
     static constexpr int oRing = 0;
@@ -161,10 +161,10 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
     pdl_wait();
     pdl_launch_dependents();                    // (behind the wait: the joining launch reads this one's inputs early)
     const Layout lay = block_layout<C::kThreads>(A, kAtRows, kAtUnit, pre_s, reinterpret_cast<int*>(smem + C::oWarpSum));
-    const int total = lay.total, share = block_share(total, A.blocks, A.least);
     if (blockIdx.x == 0 && A.b.B > 32)          // for the joining launch
         for (int b = tid; b <= A.b.B; b += C::kThreads) A.head[b] = pre_s[b];
-    const int us = min(static_cast<int>(min(static_cast<long long>(blockIdx.x) * share, 0x7fffffffll)), total), ue = us + min(share, total - us);
+    const int2 range = block_units(lay, A, static_cast<int>(blockIdx.x), kAtUnit);
+    const int us = range.x, ue = range.y;
     if (us >= ue) return;
 
     // ------------------------------------------------- copies, units ahead
@@ -512,11 +512,11 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             const int d = CT == T_I8 ? 4 * (2 * c + k + 8 * (j >> 2)) + (j & 3) : 8 * j + 2 * c + k;
             return (g + 8 * e) * C::kPad + d;
         };
-        // Behind the block's last unit the rings are free (every copy was waited for): a place for each warp.  Before, four
-        // warps take turns on one.
+        // Behind the block's last unit the rings are free (every copy was waited for): a place for each warp.  Before, the
+        // warps take turns on two.
         const bool idle = end == ue && !lost;
         float* area = idle ? reinterpret_cast<float*>(smem + C::oRing) : join_s;
-        const int parts = idle ? W : C::kParts, turns = idle ? 1 : 4;
+        const int parts = idle ? W : C::kParts, turns = W / parts;
         float* mine = area + (warp % parts) * kAtRows * C::kPad;
 #pragma unroll 1
         for (int turn = 0; turn < turns; ++turn) {
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
 }
 
 // Segments that several blocks share: their pieces' results, weighted by 2^(maximum - the largest) and added in a fixed
-// order.  The grid has some blocks for each border between two shares.  A segment of p pieces has p - 1 borders inside, which
+// order.  The grid has some blocks for each border between two blocks of the first launch.  A segment of p pieces has p - 1 borders inside, which
 // deal its rows among them: a border's work is about the same whether a few segments are in many pieces or many in two.
 // A row of few pieces is a warp's, of many the block's: eight warps, every eighth piece each, eight at a time.  Maximum, sum
 // and values are loaded together, so a row costs one round of loads per 8 (or 64) pieces.
@@ -646,27 +646,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     Layout lay;
-    if (A.b.B <= 32) lay = lane_layout(A, tile_rows, unit, lane);
-    else pdl_wait();
-    if (A.b.B > 32) {
+    if (A.b.B <= 32) {
+        lay = lane_layout(A, tile_rows, unit, lane);
+    } else {
+        pdl_wait();
         lay.pre = A.head;
         lay.total = A.head[A.b.B];
+        lay.share = max((lay.total + A.blocks - 1) / A.blocks, A.least);
+        lay.mine = lay.n = lay.mine_b = lay.blocks = 0;
+        lay.f = SeqFacts{0, 0, 0, 0};
     }
-    const int share = block_share(lay.total, A.blocks, A.least), j = static_cast<int>(blockIdx.x);
-    const long long border = static_cast<long long>(j + 1) * share;
+    // the border before block j: the one inside a segment whose pieces are those of blocks j0, j0 + 1, ..
+    const int j = static_cast<int>(blockIdx.x) + 1;
     Segment sg = {};
-    bool inside = border < lay.total;
-    if (inside) {
-        sg = find_segment(A, lay, static_cast<int>(border), tile_rows, unit);
-        inside = sg.u0 != border;
+    bool inside = false;
+    int j0 = 0, pieces = 0;
+    if (lay.share == 0) {
+        const OwnPiece p = own_piece(lay, A, j, unit);
+        inside = p.j > 0;
+        if (inside) {
+            sg = find_segment(A, lay, p.us, tile_rows, unit);
+            j0 = j - p.j;
+            pieces = p.n;
+        }
+    } else {
+        const long long border = static_cast<long long>(j) * lay.share;
+        if (border < lay.total) {
+            sg = find_segment(A, lay, static_cast<int>(border), tile_rows, unit);
+            inside = sg.u0 != border;
+            j0 = sg.u0 / lay.share;
+            pieces = (sg.u0 + sg.units - 1) / lay.share - j0 + 1;
+        }
     }
     if (A.b.B <= 32) pdl_wait();                // (every thread: the launch ends behind the one before it)
     if (!inside) return;
-    const int j0 = sg.u0 / share, pieces = (sg.u0 + sg.units - 1) / share - j0 + 1;
     const int rows = min(tile_rows, sg.f.n * A.G - sg.tile * tile_rows);
     const size_t pf = attn_part_floats(A.part_rows, D);
     // (a block's first piece is in its first place, a segment that begins within the block in the second)
-    const float* first = A.part + (static_cast<size_t>(j0) * 2 + (j0 * share < sg.u0 ? 1 : 0)) * pf;
+    const float* first = A.part + (static_cast<size_t>(j0) * 2 + (lay.share > 0 && j0 * lay.share < sg.u0 ? 1 : 0)) * pf;
     const float* others = A.part + static_cast<size_t>(j0) * 2 * pf;
     auto write = [&](const JoinRow<D>& R, int row) {
         const float inv = R.l == 0.0f ? 0.0f : 1.0f / R.l;
@@ -676,7 +693,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
         for (int v = 0; v < kV; ++v) store_typed(A.y, A.ytype, y + v, R.acc[v] * inv);
     };
     JoinRow<D> R;
-    const int stride = pieces - 1, mine = j - j0;             // this border's rows: mine, mine + stride, ..
+    const int stride = pieces - 1, mine = j - 1 - j0;           // this border's rows: mine, mine + stride, ..
     if (pieces <= kJoinFew) {
 #pragma unroll 1
         for (int row = mine + (static_cast<int>(blockIdx.y) * kJoinWarps + warp) * stride; row < rows;

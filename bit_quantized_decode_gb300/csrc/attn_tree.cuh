@@ -40,14 +40,20 @@ struct Segment {
     SeqFacts f;
 };
 
-// How a call's units lie (fewer than 2^31 - 1024: the host's check): sequences one behind the other, in each its key heads, in each its tiles of rows.  Up to 32
-// sequences every warp holds them itself, one to a lane (one round of loads, no barrier); more lie as prefix sums in shared
-// memory.  All calls are a whole warp's.
+// How a call's units lie (fewer than 2^31 - 1024: the host's check): sequences one behind the other, in each its key heads,
+// in each its tiles of rows.  Up to 32 sequences every warp holds them itself, one to a lane (one round of loads, no
+// barrier); more lie as prefix sums in shared memory.  All calls are a whole warp's.
+//
+// Blocks take equal shares of the units, across segments.  A block that ends one segment and begins another pays twice
+// for queries and joining (4.5 us of 10.7 for one token over 1000 places), so where segments are few (a quarter of the
+// blocks at most) each gets blocks of its own instead: n for every segment of a sequence, in near equal parts.
 struct Layout {
     const int* pre;           // [B + 1] in shared memory; null: in the lanes
     int mine;            // units before this lane's sequence
     SeqFacts f;               // this lane's sequence
     int total;
+    int share;                // units of a block; 0: segments have blocks of their own
+    int n, mine_b, blocks;    // those of each of this lane's segments, those before its sequence, of all
 };
 __device__ __forceinline__ int seq_cost(const AttnArgs& A, const SeqFacts& f, int rows, int unit)
 {
@@ -66,15 +72,30 @@ __device__ __forceinline__ Layout lane_layout(const AttnArgs& A, int rows, int u
 {
     Layout L;
     L.pre = nullptr;
-    int v = 0;
+    int v = 0, units = 0, segs = 0;
     L.f = SeqFacts{0, 0, 0, 0};
     if (lane < A.b.B) {
         L.f = seq_facts(A, lane);
-        v = seq_cost(A, L.f, rows, unit);
+        units = seq_units(L.f, unit);
+        segs = A.c.Hkv * seq_tiles(A, L.f, rows);
+        v = segs * units;
     }
     const int upto = warp_scan(v, lane);
     L.mine = upto - v;
     L.total = __shfl_sync(0xffffffffu, upto, 31);
+    const int all = __reduce_add_sync(0xffffffffu, segs);
+    L.n = L.mine_b = L.blocks = 0;
+    if (4 * all > A.blocks) {
+        L.share = max((L.total + A.blocks - 1) / A.blocks, A.least);
+        return L;
+    }
+    // as many units to a block that the segments' last, partly filled blocks still have room
+    L.share = 0;
+    const int part = max((L.total + A.blocks - all - 1) / (A.blocks - all), A.least);
+    L.n = (units + part - 1) / part;
+    const int b = warp_scan(segs * L.n, lane);
+    L.mine_b = b - segs * L.n;
+    L.blocks = __shfl_sync(0xffffffffu, b, 31);
     return L;
 }
 // By the whole block of NT threads; pre needs kAtMaxSeq + 1 places, warp_s one for each warp.
@@ -105,6 +126,8 @@ __device__ __forceinline__ Layout block_layout(const AttnArgs& A, int rows, int 
     L.mine = 0;
     L.f = SeqFacts{0, 0, 0, 0};
     L.total = pre[A.b.B];
+    L.share = max((L.total + A.blocks - 1) / A.blocks, A.least);
+    L.n = L.mine_b = L.blocks = 0;
     return L;
 }
 __device__ __forceinline__ SeqFacts facts_of(const Layout& L, int b)
@@ -144,10 +167,34 @@ __device__ __forceinline__ Segment find_segment(const AttnArgs& A, const Layout&
     s.u0 = first + seg * s.units;
     return s;
 }
-// Units of each block.  (The sum over all blocks stays below 2^31: the host's check.)
-__device__ __forceinline__ int block_share(int total, int blocks, int least)
+// A block's piece of a segment that has blocks of its own: number j of n.
+struct OwnPiece {
+    int j, n, us, ue;
+};
+__device__ __forceinline__ OwnPiece own_piece(const Layout& L, const AttnArgs& A, int block, int unit)
 {
-    return max((total + blocks - 1) / blocks, least);
+    OwnPiece p = {0, 0, 0, 0};
+    if (block >= L.blocks) return p;
+    const int lane = threadIdx.x & 31;
+    const int b = __popc(__ballot_sync(0xffffffffu, lane < A.b.B && L.mine_b <= block)) - 1;
+    const SeqFacts f = facts_of(L, b);
+    p.n = __shfl_sync(0xffffffffu, L.n, b);
+    const int at = block - __shfl_sync(0xffffffffu, L.mine_b, b), units = seq_units(f, unit), seg = at / p.n;
+    p.j = at - seg * p.n;
+    const int u0 = __shfl_sync(0xffffffffu, L.mine, b) + seg * units;
+    p.us = u0 + static_cast<int>(static_cast<long long>(units) * p.j / p.n);
+    p.ue = u0 + static_cast<int>(static_cast<long long>(units) * (p.j + 1) / p.n);
+    return p;
+}
+// The units [x, y) of a block.
+__device__ __forceinline__ int2 block_units(const Layout& L, const AttnArgs& A, int block, int unit)
+{
+    if (L.share == 0) {
+        const OwnPiece p = own_piece(L, A, block, unit);
+        return make_int2(p.us, p.ue);
+    }
+    const int us = static_cast<int>(min(static_cast<long long>(block) * L.share, static_cast<long long>(L.total)));
+    return make_int2(us, us + min(L.share, L.total - us));
 }
 
 // Box of a 3-D tensor map -> shared memory.
