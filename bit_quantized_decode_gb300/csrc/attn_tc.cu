@@ -19,7 +19,7 @@
 //               an fp32 output) and is the A operand; V as it lies, 64 values of a token in a row,
 //               is an operand with its columns contiguous.
 // Warps: one orders copies, one issues MMAs, eight take the softmax; for an INT8
-// cache six widen codes to 16 bits (exact) in shared memory.  All
+// cache eight widen codes to 16 bits (exact) in shared memory.  All
 // are joined by mbarriers with bounded waits.
 #include "attn_tree.cuh"
 #include "gemm_w8.cuh"
@@ -28,7 +28,7 @@ namespace w4k {
 namespace {
 
 constexpr int kTcRows = kAtTcRows, kTcUnit = kAtTcUnit;
-constexpr int kConvWarps = 6;                   // warps 2, 3, 12 .. 15
+constexpr int kConvWarps = 8;                   // warps 2, 3, 12 .. 17: four for keys, four for values
 constexpr float kRaise = 12.0f;                 // log2 of what a probability may reach
 
 template <int D, int CT>
@@ -37,11 +37,11 @@ struct Tc {
     static constexpr int kBoxes = D / 64;                     // 128-byte column groups of 16-bit values
     static constexpr int kQ = kTcRows * D * 2;
     static constexpr int kHalf = kTcUnit * D * 2;             // a tile's keys (or values) in 16 bits
-    static constexpr int kRaw = 2 * kTcUnit * D;              // a tile's codes
+    static constexpr int kRaw = kTcUnit * D;                  // the same in codes
     static constexpr int kStages = kI8 ? (D == 64 ? 10 : D == 128 ? 5 : 2) : (D == 64 ? 8 : D == 128 ? 5 : 2);   // copies
     static constexpr int kConv = kI8 ? (D == 256 ? 1 : 2) : kStages;   // 16-bit tiles
-    static constexpr int kMeta = kStages + kConv;             // tiles between a copy's order and its softmax, at most
-    static constexpr int kThreads = kI8 ? 512 : 384;
+    static constexpr int kMeta = kStages + kConv + 2;         // tiles between the order of a tile's keys and the end of its softmax, at most
+    static constexpr int kThreads = kI8 ? 384 + 32 * (kConvWarps - 2) : 384;
     static constexpr int kPBufs = D == 256 ? 1 : 2;
     static constexpr int kCols = 512;
     static constexpr int cS = D, cP = D + 2 * kTcUnit;        // tensor-memory columns of S and P; O begins at 0
@@ -49,11 +49,11 @@ struct Tc {
     static constexpr int oQ = 0;
     static constexpr int oKv = kQ;                            // [kConv] keys, values
     static constexpr int oRaw = oKv + kConv * 2 * kHalf;
-    static constexpr int oScale = oRaw + (kI8 ? kStages * kRaw : 0);        // [kMeta][2][64]
+    static constexpr int oScale = oRaw + (kI8 ? kStages * 2 * kRaw : 0);    // [kMeta][2][64]
     static constexpr int oMeta = oScale + (kI8 ? kMeta * 2 * kTcUnit * 4 : 0);   // [kMeta]: which sixteenths of a tile have a page
     static constexpr int oTop = oMeta + kMeta * 4;            // [2][2][128]: maxima of a row's halves, of even and odd tiles
     static constexpr int oBars = (oTop + 4 * kTcRows * 4 + 7) / 8 * 8;
-    static constexpr int nBars = 2 * kStages + 4 * kConv + 12;
+    static constexpr int nBars = 4 * kStages + 4 * kConv + 12;
     static constexpr int oMisc = oBars + nBars * 8;           // tensor memory's base, failure flag, odd values flag
     static constexpr int oWarpSum = oMisc + 16;
     static constexpr int oPre = oWarpSum + kThreads / 32 * 4;
@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
     uint8_t* smem = raw_s + ((1024u - (smem_u32(raw_s) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bars = smem_u32(smem + C::oBars);
-    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * S;                    // codes (INT8)
-    const uint32_t k_full = raw_empty + 8 * S, k_empty = k_full + 8 * NC;            // 16-bit keys
+    const uint32_t raw_full = bars, raw_empty = raw_full + 16 * S;                   // codes (INT8): keys, then values
+    const uint32_t k_full = raw_empty + 16 * S, k_empty = k_full + 8 * NC;            // 16-bit keys
     const uint32_t v_full = k_empty + 8 * NC, v_empty = v_full + 8 * NC;             // and values
     const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8,
                    pair_bar = wg_bar + 8;
@@ -145,14 +145,14 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
     int* pre_s = reinterpret_cast<int*>(smem + C::oPre);
 
     if (tid == 0) {
-        for (int k = 0; k < S; ++k) {
+        for (int k = 0; k < 2 * S; ++k) {
             mbar_init(raw_full + 8 * k, 1);
-            mbar_init(raw_empty + 8 * k, kConvWarps);
+            mbar_init(raw_empty + 8 * k, kConvWarps / 2);
         }
         for (int k = 0; k < NC; ++k) {
-            mbar_init(k_full + 8 * k, kI8 ? kConvWarps : 1);
+            mbar_init(k_full + 8 * k, kI8 ? kConvWarps / 2 : 1);
             mbar_init(k_empty + 8 * k, 1);
-            mbar_init(v_full + 8 * k, kI8 ? kConvWarps : 1);
+            mbar_init(v_full + 8 * k, kI8 ? kConvWarps / 2 : 1);
             mbar_init(v_empty + 8 * k, 1);
         }
         for (int k = 0; k < 2; ++k) {
@@ -220,21 +220,28 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 const int st = it % S;
                 const uint32_t ph = static_cast<uint32_t>(it / S - 1) & 1u;
                 if constexpr (kI8) {
-                    if (it >= S) ok = warp_wait(raw_empty + 8 * st, ph);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        meta_s[it % C::kMeta] = sixteenths;
-                        mbar_arrive_expect_tx(raw_full + 8 * st, static_cast<uint32_t>(n * per * 2 * (D + 4)));
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t bar = raw_full + 8 * (half * S + st);
+                        if (it >= S) ok = warp_wait(raw_empty + 8 * (half * S + st), ph);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            if (half == 0) meta_s[it % C::kMeta] = sixteenths;
+                            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * per * (D + 4)));
+                        }
+                        __syncwarp();
+                        if (there) {
+                            const size_t at = static_cast<size_t>(z) * A.c.page + y;
+                            bulk_copy(smem_u32(smem + C::oRaw) + (2 * st + half) * C::kRaw + lane * per * D,
+                                      static_cast<const uint8_t*>(half ? A.c.v : A.c.k) + at * D, per * D, bar);
+                            bulk_copy(smem_u32(scale_s + ((it % C::kMeta) * 2 + half) * kTcUnit + lane * per), (half ? A.c.vs : A.c.ks) + at, per * 4,
+                                      bar);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (there) {
-                        const uint32_t dst = smem_u32(smem + C::oRaw) + st * C::kRaw, bar = raw_full + 8 * st;
-                        const size_t at = static_cast<size_t>(z) * A.c.page + y;
-                        bulk_copy(dst + lane * per * D, static_cast<const uint8_t*>(A.c.k) + at * D, per * D, bar);
-                        bulk_copy(dst + kTcUnit * D + lane * per * D, static_cast<const uint8_t*>(A.c.v) + at * D, per * D, bar);
-                        const uint32_t sc = smem_u32(scale_s + (it % C::kMeta) * 2 * kTcUnit + lane * per);
-                        bulk_copy(sc, A.c.ks + at, per * 4, bar);
-                        bulk_copy(sc + kTcUnit * 4, A.c.vs + at, per * 4, bar);
+                    if (!ok) {                  // (a tile whose keys alone were ordered: they land, too)
+                        warp_wait(raw_full + 8 * st, static_cast<uint32_t>(it / S) & 1u);
+                        break;
                     }
                 } else {
 #pragma unroll
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
         for (int k = max(0, it - S); k < it; ++k) {
             const uint32_t ph = static_cast<uint32_t>(k / S) & 1u;
             if constexpr (kI8) {
-                if (!warp_wait(raw_full + 8 * (k % S), ph)) break;
+                if (!warp_wait(raw_full + 8 * (k % S), ph) || !warp_wait(raw_full + 8 * (S + k % S), ph)) break;
             } else {
                 if (!warp_wait(k_full + 8 * (k % S), ph) || !warp_wait(v_full + 8 * (k % S), ph)) break;
             }
@@ -306,29 +313,28 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 if (ok) scores(it + 1);
             }
             for (; it < last && ok; ++it) {
-                ok = warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u) &&
-                     warp_wait(v_full + 8 * (it % NC), static_cast<uint32_t>(it / NC) & 1u);
+                // All that can be known before P is: the values are there, the keys of the scores after next as a rule.  What
+                // follows P's arrival is the way of the next scores.  They come behind this product: once the softmax has
+                // them, its place for P is free (and an INT8 cache's keys may wait for this product).
+                ok = warp_wait(v_full + 8 * (it % NC), static_cast<uint32_t>(it / NC) & 1u);
+                if (!ok) break;
+                const int i = it + 2;
+                const bool more = i < last;
+                const bool early = more && __all_sync(0xffffffffu, mbar_test_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u));
+                const uint64_t v = v_desc + static_cast<uint64_t>((it % NC) * (2 * C::kHalf >> 4));
+                const uint32_t p = tb + C::cP + (it % C::kPBufs) * 32 * kParts;
+                ok = warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u);
                 if (!ok) break;
                 tc_fence_after();
-                // The scores after next first, whose buffer P has left: the softmax waits for them sooner than for this
-                // product.  (But not if their keys are not there yet: their place may wait for this product.)
-                const bool more = it + 2 < last;
-                const int i = it + 2;
-                const bool early = more && __all_sync(0xffffffffu, mbar_test_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u));
-                if (early) scores(i);
                 if (elect_one()) {
-                    const uint64_t v = v_desc + static_cast<uint64_t>((it % NC) * (2 * C::kHalf >> 4));
-                    const uint32_t p = tb + C::cP + (it % C::kPBufs) * 32 * kParts;
 #pragma unroll
                     for (int part = 0; part < kParts; ++part) mma_ts_x4(tb, p + 32 * part, v, ipv);
                     tc_commit(v_empty + 8 * (it % NC));
                     tc_commit(pv_done + 8 * (it & 1));
                 }
                 __syncwarp();
-                if (more && !early) {
-                    ok = keys(i);
-                    if (ok) scores(i);
-                }
+                if (more && !early) ok = keys(i);
+                if (more && ok) scores(i);
             }
             begin = end;
         }
@@ -560,9 +566,8 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                     if (!ok) break;
                     fence_proxy_async_smem();
                 }
-                if (it >= C::kPBufs) {          // P's buffer has been read
-                    const int b = it - C::kPBufs;
-                    ok = warp_wait(pv_done + 8 * (b & 1), static_cast<uint32_t>(b >> 1) & 1u);
+                if (C::kPBufs == 1 && it > 0) { // P's place has been read (with two places: before these scores were formed)
+                    ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -634,43 +639,46 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
         }
     } else if (kI8) {
         // ---------------------------------------------------- codes to 16 bits
-        const int w = warp < 4 ? tid - 64 : tid - 384 + 64;
+        // Half of the warps takes the keys, half the values, each at its own pace.
+        const int cw = warp < 4 ? warp - 2 : warp - 10, half = cw & 1, w = (cw >> 1) * 32 + lane;
+        const uint32_t full = raw_full + 8 * half * S, empty = raw_empty + 8 * half * S;
+        const uint32_t to_full = half ? v_full : k_full, to_empty = half ? v_empty : k_empty;
         const int n = ue - us;
         bool ok = true;
         for (int it = 0; it < n && ok; ++it) {
             const int st = it % S, cv = it % NC;
-            const uint32_t ph = static_cast<uint32_t>(it / NC - 1) & 1u;
-            ok = warp_wait(raw_full + 8 * st, static_cast<uint32_t>(it / S) & 1u);
-            const uint8_t* src = smem + C::oRaw + st * C::kRaw;
-            uint8_t* dst = smem + C::oKv + cv * 2 * C::kHalf;
-#pragma unroll 1
-            for (int half = 0; half < 2 && ok; ++half) {
-                if (it >= NC) ok = warp_wait((half ? v_empty : k_empty) + 8 * cv, ph);
-                if (!ok) break;
-#pragma unroll 2
-                for (int k = w; k < kTcUnit * D / 16; k += 32 * kConvWarps) {
-                    const int t = k / (D / 16), c = k % (D / 16);                   // sixteen codes: two 16-byte words
-                    const uint4 q = *reinterpret_cast<const uint4*>(src + half * kTcUnit * D + 16 * k);
-                    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
-                    uint32_t h[8];
+            ok = warp_wait(full + 8 * st, static_cast<uint32_t>(it / S) & 1u);
+            if (it >= NC) ok = ok && warp_wait(to_empty + 8 * cv, static_cast<uint32_t>(it / NC - 1) & 1u);
+            if (!ok) break;
+            const uint8_t* src = smem + C::oRaw + (2 * st + half) * C::kRaw;
+            uint8_t* dst = smem + C::oKv + (2 * cv + half) * C::kHalf;
+            constexpr int kStep = 16 * kConvWarps, kTimes = kTcUnit * D / 16 / kStep;
+            static_assert(kTcUnit * D / 16 % kStep == 0, "whole steps");
+#pragma unroll 4
+            for (int i = 0; i < kTimes; ++i) {
+                const int k = w + kStep * i, t = k / (D / 16), c = k % (D / 16);    // sixteen codes: two 16-byte words
+                const uint4 q = *reinterpret_cast<const uint4*>(src + 16 * k);
+                const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+                uint32_t h[8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (half == 0 && QT == T_F16) i8_to_f16(x[i], h[2 * i], h[2 * i + 1]);
-                        else i8_to_bf16(x[i], h[2 * i], h[2 * i + 1]);
-                    }
-                    uint8_t* d = dst + half * C::kHalf + (c >> 2) * kTcUnit * 128 + t * 128;
-                    const int a = ((2 * c) & 7) ^ (t & 7), b = a ^ 1;
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    // (every other column group the other way round: eight lanes on eight different words)
-                    const bool flip = (c >> 2) & 1;
-                    *reinterpret_cast<uint4*>(d + ((flip ? b : a) << 4)) = flip ? hi : lo;
-                    *reinterpret_cast<uint4*>(d + ((flip ? a : b) << 4)) = flip ? lo : hi;
+                for (int e = 0; e < 4; ++e) {
+                    if (QT == T_F16 && half == 0) i8_to_f16(x[e], h[2 * e], h[2 * e + 1]);
+                    else i8_to_bf16(x[e], h[2 * e], h[2 * e + 1]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive((half ? v_full : k_full) + 8 * cv);
+                uint8_t* d = dst + (c >> 2) * kTcUnit * 128 + t * 128;
+                const int a = ((2 * c) & 7) ^ (t & 7), b = a ^ 1;
+                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                // (every other column group the other way round: eight lanes on eight different words)
+                const bool flip = (c >> 2) & 1;
+                *reinterpret_cast<uint4*>(d + ((flip ? b : a) << 4)) = flip ? hi : lo;
+                *reinterpret_cast<uint4*>(d + ((flip ? a : b) << 4)) = flip ? lo : hi;
             }
-            if (ok && lane == 0) mbar_arrive(raw_empty + 8 * st);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(to_full + 8 * cv);
+                mbar_arrive(empty + 8 * st);
+            }
             __syncwarp();
         }
         if (!ok && lane == 0) fail();
