@@ -12,7 +12,7 @@ from . import _lib
 from ._lib import (W4_FLAG_PDL, W4Error, a8_quantize, clear_device_error, device_error, i8g32_gemv,
                    i8g32_linear, i8g32_quantize, i8g32_repack, i8g32_repacked_bytes, q4_0_gemv, q4_0_linear,
                    q4_0_quantize, q4_0_repack, q4_0_repacked_bytes, w4_concat_f32, w4_quantize_rows, w4_repack,
-                   w4_kv_append, w4_logits_adjust, w4_moe_experts, w4_moe_layer, w4_moe_route, w4_repacked_bytes,
+                   w4_kv_append, w4_kv_values, w4_logits_adjust, w4_moe_experts, w4_moe_layer, w4_moe_route, w4_repacked_bytes,
                    w4_rope_table, w4_tree_attention, w4_tree_attention_workspace_bytes, w4a8_gemv, w4a8_linear, w8_repack_glu,
                    w8a8_linear, w8a8_matmul)
 from .attention import CachedAttention, KVBatch, KVCache, RopeTable
@@ -24,7 +24,8 @@ __all__ = [
     "W4_FLAG_PDL", "W4Error", "CachedAttention", "KVBatch", "KVCache", "LinearChain", "LogitRules", "MoeLayer", "MoeRouter", "QuantLinear",
     "RopeTable", "a8_quantize", "clear_device_error", "device_error",
     "i8g32_gemv", "i8g32_linear", "i8g32_quantize", "i8g32_repack", "i8g32_repacked_bytes", "q4_0_gemv",
-    "q4_0_linear", "q4_0_quantize", "q4_0_repack", "q4_0_repacked_bytes", "w4_concat_f32", "w4_kv_append", "w4_logits_adjust", "w4_moe_experts", "w4_moe_layer",
+    "q4_0_linear", "q4_0_quantize", "q4_0_repack", "q4_0_repacked_bytes", "w4_concat_f32", "w4_kv_append", "w4_kv_values", "w4_logits_adjust",
+    "w4_moe_experts", "w4_moe_layer",
     "w4_moe_route", "w4_quantize_rows", "w4_rope_table", "w4_tree_attention",
     "w4_tree_attention_workspace_bytes", "w4_repack", "w4_repacked_bytes", "w4a8_gemv", "w4a8_linear", "w8_repack_glu",
     "w8a8_linear", "w8a8_matmul",

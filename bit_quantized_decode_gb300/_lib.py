@@ -197,6 +197,7 @@ class LogitRulesDesc(ctypes.Structure):
 _PC = ctypes.POINTER(KVCacheDesc)
 _PB = ctypes.POINTER(KVBatchDesc)
 SIGNATURES["w4_rope_table"] = ([_P, ctypes.c_double, ctypes.c_double, _I, _I, _P, _P], _I)
+SIGNATURES["w4_kv_values"] = ([_PC, _I, _P, _P], _I)
 SIGNATURES["w4_kv_append"] = ([_PC, _PB, ctypes.POINTER(RopeDesc), _P, _I, _LL, _I, _I, _P, _P, _P, _F, _P, _I, _U, _P], _I)
 SIGNATURES["w4_tree_attention_workspace_bytes"] = ([_PC, _PB, _I, _I], _SZ)
 SIGNATURES["w4_tree_attention"] = ([_PC, _PB, _P, _I, _I, _I, _P, _F, _P, _I, _P, _SZ, _U, _P], _I)
@@ -960,6 +961,13 @@ def w4_kv_append(cache, batch, rope, qkv, q, positions=None, q_norm=None, k_norm
                                                qkv.data_ptr(), ELEM_TYPES[qkv.dtype], ld, T, Hq, _addr(positions), _addr(q_norm),
                                                _addr(k_norm), float(eps), q.data_ptr(), ELEM_TYPES[q.dtype], flags,
                                                _raw_stream(stream, dev)))
+
+
+def w4_kv_values(cache, which: str, out, stream=None):
+    """out float32 [pages][Hkv][page_size][D]: an int8 cache's keys ("k") or values ("v"), codes times scales."""
+    dev = _check_tensors(("out", out, _F32, (cache.pages, cache.Hkv, cache.page_size, cache.D)))
+    _check_home(dev, cache)
+    _check("w4_kv_values", load().w4_kv_values(ctypes.byref(cache), {"k": 0, "v": 1}[which], out.data_ptr(), _raw_stream(stream, dev)))
 
 
 def w4_tree_attention_workspace_bytes(cache, batch, T: int, Hq: int) -> int:

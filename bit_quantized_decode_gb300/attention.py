@@ -34,10 +34,17 @@ class KVCache:
             return cls(k, v)
         return cls(k, v, torch.zeros(shape[:3], device=device), torch.zeros(shape[:3], device=device))
 
-    def values(self, which: str):
-        """All cached keys ("k") or values ("v") as numbers: the 16-bit tensor itself, or codes times scales in float32."""
-        t, s = {"k": (self.k, self.k_scale), "v": (self.v, self.v_scale)}[which]
-        return t if s is None else t * s[..., None]
+    def values(self, which: str, out=None, stream=None):
+        """All cached keys ("k") or values ("v") as numbers: the 16-bit tensor itself, or an int8 cache's codes times scales
+        in float32."""
+        t = {"k": self.k, "v": self.v}[which]
+        if t.dtype != torch.int8:
+            return t
+        if out is None:
+            with _lib.allocating_on(stream):
+                out = torch.empty(t.shape, dtype=torch.float32, device=t.device)
+        _lib.w4_kv_values(self.desc, which, out, stream)
+        return out
 
 
 class KVBatch:

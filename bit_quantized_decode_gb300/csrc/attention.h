@@ -53,6 +53,7 @@ struct AppendArgs {
     int per;                  // loads of heads to a warp (set by the launch)
 };
 cudaError_t launch_kv_append(AppendArgs& a, int xtype, cudaStream_t s);
+cudaError_t launch_kv_values(const KvView& c, bool values, float* out, cudaStream_t s);
 cudaError_t launch_rope_table(const double* inv_freq, double factor, double scale, int positions, int half, float* turns,
                               cudaStream_t s);
 

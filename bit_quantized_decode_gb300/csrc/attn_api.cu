@@ -31,28 +31,39 @@ int log2_of(int v)
     return n;
 }
 
-// Numbers of a call on a cache; its pointers come after the empty calls.
-w4_status check_call(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq)
+w4_status check_cache(const w4_kv_cache* c)
 {
-    if (!c || !b || T < 0 || Hq <= 0 || b->B < 0 || b->max_pages < 1 || b->max_tokens < 1) return W4_ERR_INVALID_ARG;
+    if (!c) return W4_ERR_INVALID_ARG;
     if ((!half_type(c->type) && c->type != W4_I8) || c->pages < 1 || c->page_size < 1 || c->Hkv < 1 || c->D < 1)
         return W4_ERR_INVALID_ARG;
     if (c->D != 64 && c->D != 128 && c->D != 256) return W4_ERR_UNSUPPORTED_SHAPE;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return W4_ERR_UNSUPPORTED_SHAPE;
+    return static_cast<long long>(c->pages) * c->Hkv > 0x7fffffffll ? W4_ERR_UNSUPPORTED_SHAPE : W4_OK;
+}
+
+// Numbers of a call on a cache; its pointers come after the empty calls.
+w4_status check_call(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq)
+{
+    if (!b || T < 0 || Hq <= 0 || b->B < 0 || b->max_pages < 1 || b->max_tokens < 1) return W4_ERR_INVALID_ARG;
+    const w4_status r = check_cache(c);
+    if (r != W4_OK) return r;
     if (Hq % c->Hkv != 0 || Hq > kMaxHeads || T > W4_MAX_TOKENS || b->B > W4_MAX_SEQUENCES) return W4_ERR_UNSUPPORTED_SHAPE;
-    if (static_cast<long long>(c->pages) * c->Hkv > 0x7fffffffll ||
-        static_cast<long long>(b->max_pages) * c->page_size > kMaxPlaces)
+    if (static_cast<long long>(b->max_pages) * c->page_size > kMaxPlaces)
         return W4_ERR_UNSUPPORTED_SHAPE;
     return W4_OK;
 }
 
-w4_status check_call_pointers(const w4_kv_cache* c, const w4_kv_batch* b)
+w4_status check_cache_pointers(const w4_kv_cache* c)
 {
     const bool i8 = c->type == W4_I8;
     if (!c->k || !c->v || i8 != (c->k_scale != nullptr) || i8 != (c->v_scale != nullptr)) return W4_ERR_INVALID_ARG;
-    if (!b->table || !b->ctx || !b->q_start) return W4_ERR_INVALID_ARG;
-    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16) ||
-        !aligned(b->table, 4) || !aligned(b->ctx, 4) || !aligned(b->q_start, 4))
+    return aligned(c->k, 16) && aligned(c->v, 16) && aligned(c->k_scale, 16) && aligned(c->v_scale, 16) ? W4_OK : W4_ERR_MISALIGNED;
+}
+w4_status check_call_pointers(const w4_kv_cache* c, const w4_kv_batch* b)
+{
+    const w4_status r = check_cache_pointers(c);
+    if (r == W4_ERR_INVALID_ARG || !b->table || !b->ctx || !b->q_start) return W4_ERR_INVALID_ARG;
+    if (r != W4_OK || !aligned(b->table, 4) || !aligned(b->ctx, 4) || !aligned(b->q_start, 4))
         return W4_ERR_MISALIGNED;
     return W4_OK;
 }
@@ -139,6 +150,18 @@ w4_status w4_kv_append(const w4_kv_cache* c, const w4_kv_batch* b, const w4_rope
     a.q = q;
     a.qtype = q_type;
     return cuda_status(launch_kv_append(a, x_type, reinterpret_cast<cudaStream_t>(s)));
+}
+
+w4_status w4_kv_values(const w4_kv_cache* c, int which, float* out, w4_stream_t s)
+{
+    w4_status r = check_cache(c);
+    if (r != W4_OK) return r;
+    if (c->type != W4_I8 || (which != W4_KEYS && which != W4_VALUES)) return W4_ERR_INVALID_ARG;
+    if (static_cast<long long>(c->pages) * c->Hkv * c->page_size * (c->D / 8) > (1ll << 38)) return W4_ERR_UNSUPPORTED_SHAPE;
+    r = check_cache_pointers(c);
+    if (r == W4_ERR_INVALID_ARG || !out) return W4_ERR_INVALID_ARG;
+    if (r != W4_OK || !aligned(out, 16)) return W4_ERR_MISALIGNED;
+    return cuda_status(launch_kv_values(view(c), which == W4_VALUES, out, reinterpret_cast<cudaStream_t>(s)));
 }
 
 size_t w4_tree_attention_workspace_bytes(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq)

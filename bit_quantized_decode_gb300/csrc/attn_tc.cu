@@ -6,9 +6,11 @@
 //
 // A block takes a tile of 128 rows of one (sequence, key head) over 64 cached
 // tokens at a time:
-//   S = Q K^T   tcgen05.mma 128 x 64 x D: Q and K in shared memory as TMA's
-//               128-byte swizzle lays them, S in tensor memory (two buffers, so
-//               that the next product runs during the softmax);
+//   S = Q K^T   tcgen05.mma 128 x 64 x D: K in shared memory as TMA's 128-byte
+//               swizzle lays it, Q in tensor memory (heads of 256, for which that has no
+//               room, in shared memory: an MMA of 128 x 64 x 16 then takes 62 cycles,
+//               bound by reading Q), S in tensor memory (two buffers, so that
+//               the next product runs during the softmax);
 //   softmax     two threads per row (tensor-memory lane), 32 tokens each; they
 //               exchange their maxima.  The maximum in use is raised only when it
 //               is passed by more than 2^12: probabilities are then at most 4096
@@ -31,29 +33,32 @@ constexpr int kTcRows = kAtTcRows, kTcUnit = kAtTcUnit;
 constexpr int kConvWarps = 8;                   // warps 2, 3, 12 .. 17: four for keys, four for values
 constexpr float kRaise = 12.0f;                 // log2 of what a probability may reach
 
-template <int D, int CT>
+template <int D, int CT, bool kWide>
 struct Tc {
     static constexpr bool kI8 = CT == T_I8;
     static constexpr int kBoxes = D / 64;                     // 128-byte column groups of 16-bit values
-    static constexpr int kQ = kTcRows * D * 2;
+    static constexpr bool kQInT = D <= 128;                   // queries in tensor memory
+    static constexpr int kQ = kQInT ? 0 : kTcRows * D * 2;
     static constexpr int kHalf = kTcUnit * D * 2;             // a tile's keys (or values) in 16 bits
     static constexpr int kRaw = kTcUnit * D;                  // the same in codes
-    static constexpr int kStages = kI8 ? (D == 64 ? 10 : D == 128 ? 5 : 2) : (D == 64 ? 8 : D == 128 ? 5 : 2);   // copies
+    static constexpr int kStages = kI8 ? (D == 64 ? 14 : D == 128 ? 7 : 2) : (D == 64 ? 10 : D == 128 ? 6 : 2);   // copies
     static constexpr int kConv = kI8 ? (D == 256 ? 1 : 2) : kStages;   // 16-bit tiles
     static constexpr int kMeta = kStages + kConv + 2;         // tiles between the order of a tile's keys and the end of its softmax, at most
     static constexpr int kThreads = kI8 ? 384 + 32 * (kConvWarps - 2) : 384;
-    static constexpr int kPBufs = D == 256 ? 1 : 2;
+    static constexpr int kPBufs = !kWide ? 3 : D == 256 ? 1 : 2;      // places for P
     static constexpr int kCols = 512;
-    static constexpr int cS = D, cP = D + 2 * kTcUnit;        // tensor-memory columns of S and P; O begins at 0
+    static constexpr int cS = D, cP = D + 2 * kTcUnit, cQ = cP + 192;   // tensor-memory columns of S, P and Q; O begins at 0
+    static_assert(!kQInT || cQ + D / 2 <= kCols, "tensor memory");
+    static_assert(cP + kPBufs * (kWide ? 96 : 32) <= (kQInT ? cQ : kCols), "tensor memory");
     // shared memory
     static constexpr int oQ = 0;
     static constexpr int oKv = kQ;                            // [kConv] keys, values
     static constexpr int oRaw = oKv + kConv * 2 * kHalf;
     static constexpr int oScale = oRaw + (kI8 ? kStages * 2 * kRaw : 0);    // [kMeta][2][64]
     static constexpr int oMeta = oScale + (kI8 ? kMeta * 2 * kTcUnit * 4 : 0);   // [kMeta]: which sixteenths of a tile have a page
-    static constexpr int oTop = oMeta + kMeta * 4;            // [2][2][128]: maxima of a row's halves, of even and odd tiles
-    static constexpr int oBars = (oTop + 4 * kTcRows * 4 + 7) / 8 * 8;
-    static constexpr int nBars = 4 * kStages + 4 * kConv + 12;
+    static constexpr int oTop = (oMeta + kMeta * 4 + 7) / 8 * 8;       // [2][2][128]: numbers of a row's halves with their turn, even and odd
+    static constexpr int oBars = oTop + 4 * kTcRows * 8;
+    static constexpr int nBars = 4 * kStages + 4 * kConv + 8;
     static constexpr int oMisc = oBars + nBars * 8;           // tensor memory's base, failure flag, odd values flag
     static constexpr int oWarpSum = oMisc + 16;
     static constexpr int oPre = oWarpSum + kThreads / 32 * 4;
@@ -89,6 +94,18 @@ __device__ __forceinline__ void mma_ss_x4(uint32_t d, uint64_t a, uint64_t b, ui
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same with A in tensor memory, eight columns to a step.
+__device__ __forceinline__ void mma_ts_rows_x4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %4, %4;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, 2;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "add.u32 a1, %1, 16;\n\tadd.u64 b1, %2, 4;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "add.u32 a1, %1, 24;\n\tadd.u64 b1, %2, 6;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // The same with A in tensor memory (eight columns to a step) and B's rows along N (16 rows of 128 bytes to a step).
 __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
 {
@@ -121,9 +138,9 @@ __device__ __forceinline__ float2 tc_unpair(uint32_t u)
 }
 
 template <int D, int CT, int QT, bool kWide>
-__global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs A)
+__global__ void __launch_bounds__(Tc<D, CT, kWide>::kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs A)
 {
-    using C = Tc<D, CT>;
+    using C = Tc<D, CT, kWide>;
     constexpr bool kI8 = C::kI8;
     constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
     constexpr int kParts = !kWide ? 1 : PT == T_F16 ? 2 : 3;  // of a probability: 11 or 8 bits each
@@ -135,8 +152,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
     const uint32_t raw_full = bars, raw_empty = raw_full + 16 * S;                   // codes (INT8): keys, then values
     const uint32_t k_full = raw_empty + 16 * S, k_empty = k_full + 8 * NC;            // 16-bit keys
     const uint32_t v_full = k_empty + 8 * NC, v_empty = v_full + 8 * NC;             // and values
-    const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8,
-                   pair_bar = wg_bar + 8;
+    const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::oMisc);
     volatile uint32_t* dead_s = misc + 1;
     volatile uint32_t* odd_s = misc + 2;
@@ -162,11 +178,11 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
         }
         mbar_init(q_full, 8);
         mbar_init(wg_bar, 8);
-        for (int k = 0; k < 4; ++k) mbar_init(pair_bar + 8 * k, 2);
         fence_mbar_init();
         *dead_s = 0u;
         *odd_s = 0u;
     }
+    for (int k = tid; k < 4 * kTcRows; k += C::kThreads) reinterpret_cast<unsigned long long*>(smem + C::oTop)[k] = 0ull;   // (turns begin at 1)
     if (tid == 32 && !kI8) {
         prefetch_map(&A.kmap);
         prefetch_map(&A.vmap);
@@ -296,7 +312,10 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 const uint64_t k = k_desc + static_cast<uint64_t>((i % NC) * (2 * C::kHalf >> 4));
                 const uint32_t d = tb + C::cS + (i & 1) * kTcUnit;
 #pragma unroll
-                for (int x = 0; x < C::kBoxes; ++x) mma_ss_x4(d, q_desc + x * (kTcRows * 128 >> 4), k + x * (kTcUnit * 128 >> 4), iqk, x > 0);
+                for (int x = 0; x < C::kBoxes; ++x) {
+                    if constexpr (C::kQInT) mma_ts_rows_x4(d, tb + C::cQ + 32 * x, k + x * (kTcUnit * 128 >> 4), iqk, x > 0);
+                    else mma_ss_x4(d, q_desc + x * (kTcRows * 128 >> 4), k + x * (kTcUnit * 128 >> 4), iqk, x > 0);
+                }
                 tc_commit(k_empty + 8 * (i % NC));
                 tc_commit(s_full + 8 * (i & 1));
             }
@@ -314,8 +333,8 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
             }
             for (; it < last && ok; ++it) {
                 // All that can be known before P is: the values are there, the keys of the scores after next as a rule.  What
-                // follows P's arrival is the way of the next scores.  They come behind this product: once the softmax has
-                // them, its place for P is free (and an INT8 cache's keys may wait for this product).
+                // follows P's arrival is the way of the next scores, so those come first: the softmax waits for them sooner
+                // than for this product.  (But not if their keys are not there yet: an INT8 cache's may wait for this product.)
                 ok = warp_wait(v_full + 8 * (it % NC), static_cast<uint32_t>(it / NC) & 1u);
                 if (!ok) break;
                 const int i = it + 2;
@@ -325,6 +344,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                 const uint32_t p = tb + C::cP + (it % C::kPBufs) * 32 * kParts;
                 ok = warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u);
                 if (!ok) break;
+                if (early) scores(i);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -333,8 +353,10 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                     tc_commit(pv_done + 8 * (it & 1));
                 }
                 __syncwarp();
-                if (more && !early) ok = keys(i);
-                if (more && ok) scores(i);
+                if (more && !early) {
+                    ok = keys(i);
+                    if (ok) scores(i);
+                }
             }
             begin = end;
         }
@@ -345,10 +367,10 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
         // --------------------------------------------------------- softmax
         constexpr int kHalfCols = kTcUnit / 2;
         const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, wid = tid - 128;
-        float* top_s = reinterpret_cast<float*>(smem + C::oTop);
+        unsigned long long* top_s = reinterpret_cast<unsigned long long*>(smem + C::oTop);
         const uint32_t tl = tb + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         int it = 0;
-        uint32_t wg_phase = 0, pair_phase = 0;
+        uint32_t wg_phase = 0, turn = 1;
         bool ok = true;
         auto wg_sync = [&]() {                  // the eight warps, with a bounded wait
             __syncwarp();
@@ -357,16 +379,31 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
             ++wg_phase;
             return all;
         };
-        // This thread's number and that of the row's other half.
+        // This thread's number and that of the row's other half: each writes its number with the turn in one word and looks at
+        // the other's until it has the turn, too (half of what an mbarrier takes).  The words of a turn are written again two
+        // turns later, by when the other half has read them.
         auto exchanged = [&](float v, float& other) {
-            float* at = top_s + (pair_phase & 1u) * 2 * kTcRows;
-            at[half * kTcRows + row] = v;
-            __syncwarp();
-            const uint32_t bar = pair_bar + 8 * (warp & 3);
-            if (lane == 0) mbar_arrive(bar);
-            const bool all = warp_wait(bar, pair_phase & 1u);
-            ++pair_phase;
-            other = at[(half ^ 1) * kTcRows + row];
+            unsigned long long* at = top_s + (turn & 1u) * 2 * kTcRows;
+            *reinterpret_cast<volatile unsigned long long*>(at + half * kTcRows + row) =
+                static_cast<unsigned long long>(turn) << 32 | __float_as_uint(v);
+            const volatile unsigned long long* from = at + (half ^ 1) * kTcRows + row;
+            unsigned long long got = *from;
+            bool all = __all_sync(0xffffffffu, static_cast<uint32_t>(got >> 32) == turn);
+            if (!all) {
+                uint64_t t0 = 0;
+#pragma unroll 1
+                for (uint32_t i = 1; !all; ++i) {
+                    got = *from;
+                    all = __all_sync(0xffffffffu, static_cast<uint32_t>(got >> 32) == turn);
+                    if (!all && (i & 255u) == 0u) {
+                        const uint64_t now = globaltimer_ns();
+                        if (i == 256u) t0 = now;
+                        else if (__any_sync(0xffffffffu, now - t0 > kAtWaitNs)) break;
+                    }
+                }
+            }
+            ++turn;
+            other = __uint_as_float(static_cast<uint32_t>(got));
             return all;
         };
         for (int begin = us; begin < ue && ok;) {
@@ -382,12 +419,27 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
             // the row's query; the products of the last piece that read the old one are done
             {
                 const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at);
-                uint8_t* d = smem + C::oQ + row * 128;
+                if constexpr (C::kQInT) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const int j = half * (D / 16) + k;
-                    const uint4 v = have ? __ldg(q + j) : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(d + (j >> 3) * kTcRows * 128 + (((j & 7) ^ (row & 7)) << 4)) = v;
+                    for (int k = 0; k < D / 64; ++k) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 v = have ? __ldg(q + half * (D / 16) + 4 * k + e) : make_uint4(0u, 0u, 0u, 0u);
+                            w[4 * e] = v.x; w[4 * e + 1] = v.y; w[4 * e + 2] = v.z; w[4 * e + 3] = v.w;
+                        }
+                        __syncwarp();
+                        tmem_st16(tl + C::cQ + half * (D / 4) + 16 * k, w);
+                    }
+                } else {
+                    uint8_t* d = smem + C::oQ + row * 128;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int j = half * (D / 16) + k;
+                        const uint4 v = have ? __ldg(q + j) : make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(d + (j >> 3) * kTcRows * 128 + (((j & 7) ^ (row & 7)) << 4)) = v;
+                    }
+                    __syncwarp();
                 }
                 const uint32_t zero[16] = {};
 #pragma unroll
@@ -566,8 +618,10 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
                     if (!ok) break;
                     fence_proxy_async_smem();
                 }
-                if (C::kPBufs == 1 && it > 0) { // P's place has been read (with two places: before these scores were formed)
-                    ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
+                // P's place has been read: of three, by the product that was ordered before these scores
+                if (C::kPBufs < 3 && it >= C::kPBufs) {
+                    const int b = it - C::kPBufs;
+                    ok = warp_wait(pv_done + 8 * (b & 1), static_cast<uint32_t>(b >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -654,7 +708,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
             uint8_t* dst = smem + C::oKv + (2 * cv + half) * C::kHalf;
             constexpr int kStep = 16 * kConvWarps, kTimes = kTcUnit * D / 16 / kStep;
             static_assert(kTcUnit * D / 16 % kStep == 0, "whole steps");
-#pragma unroll 4
+#pragma unroll
             for (int i = 0; i < kTimes; ++i) {
                 const int k = w + kStep * i, t = k / (D / 16), c = k % (D / 16);    // sixteen codes: two 16-byte words
                 const uint4 q = *reinterpret_cast<const uint4*>(src + 16 * k);
@@ -692,7 +746,7 @@ __global__ void __launch_bounds__(Tc<D, CT>::kThreads, 1) attn_tc_kernel(const _
 template <int D, int CT, int QT, bool kWide>
 cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 {
-    using C = Tc<D, CT>;
+    using C = Tc<D, CT, kWide>;
     auto kern = attn_tc_kernel<D, CT, QT, kWide>;
     static SmemLimit limit;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, C::smem(kAtMaxSeq));

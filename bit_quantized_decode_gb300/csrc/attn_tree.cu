@@ -599,6 +599,9 @@ __device__ __forceinline__ void join_pieces(JoinRow<D>& R, const float* first, c
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
             pm[e] = neg_inf();
+            pl[e] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) pv[e][v] = 0.0f;
             if (k0 + step * e < pieces) {
                 const int k = k0 + step * e;
                 const float* p = k == 0 ? first : others + 2 * k * pf;
@@ -628,8 +631,7 @@ __device__ __forceinline__ void join_pieces(JoinRow<D>& R, const float* first, c
         for (int v = 0; v < kV; ++v) R.acc[v] *= w;
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
-            if (pm[e] == neg_inf()) continue;                 // nothing was seen (or no such piece)
-            const float x = exp2_fast(pm[e] - base);
+            const float x = exp2_fast(pm[e] - base);          // (0 where nothing was seen; a sum that is NaN stays one)
             R.l += x * pl[e];
 #pragma unroll
             for (int v = 0; v < kV; ++v) R.acc[v] += x * pv[e][v];

@@ -268,7 +268,41 @@ __global__ void rope_table_kernel(const double* inv_freq, double factor, double 
     turns[e] = make_float2(static_cast<float>(c * scale), static_cast<float>(s * scale));
 }
 
+// An INT8 cache's codes times their scales, eight to a thread.
+__global__ void __launch_bounds__(256) kv_values_kernel(const int8_t* codes, const float* scale, long long words, int lg_words, float* out)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long w = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (w >= words) return;
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(codes) + w);
+    const float s = __ldg(scale + (w >> lg_words));
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(static_cast<float>(static_cast<int8_t>((k < 4 ? q.x : q.y) >> (8 * (k & 3)))), s);
+    float4* d = reinterpret_cast<float4*>(out) + 2 * w;
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 }  // namespace
+
+cudaError_t launch_kv_values(const KvView& c, bool values, float* out, cudaStream_t s)
+{
+    const int lg_words = c.D == 64 ? 3 : c.D == 128 ? 4 : 5;  // of eight codes, in a token
+    const long long words = static_cast<long long>(c.pages) * c.Hkv * c.page << lg_words;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((words + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_values_kernel, static_cast<const int8_t*>(values ? c.v : c.k),
+                              static_cast<const float*>(values ? c.vs : c.ks), words, lg_words, out);
+}
 
 cudaError_t launch_kv_append(AppendArgs& a, int xtype, cudaStream_t s)
 {

@@ -602,6 +602,9 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   once, or as the codes and scale that a8_quantize gives for a head's
  *   values (the norm's steps as in rms_a8_quantize; a rotated value of a key
  *   rounded once to fp32).  Two rows with the same place race.
+ * w4_kv_values: out float [pages][Hkv][page_size][D], 16-byte aligned: the
+ *   numbers that an INT8 cache's keys (W4_KEYS) or values (W4_VALUES) stand
+ *   for, codes times scales, every page of the cache.
  * w4_tree_attention: y[t][h] = sum p v / sum p, p = exp(scale q.k), over the
  *   places below ctx and the drafts of the row's own sequence (the rows of
  *   this call, already appended) whose bit the row's mask has: bit j of
@@ -617,11 +620,15 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   GPU.  Two launches.  For given inputs the result is the same in every
  *   call, but it depends on the other sequences of the call in its last bits
  *   (how a sequence is split).
- * flags: 0 or W4_FLAG_PDL.  T = 0 or B = 0 is a valid empty call.
+ * flags: 0 or W4_FLAG_PDL (the same: these kernels touch no memory before
+ * their dependency wait, so every launch is a programmatic dependent of the
+ * one before it).  T = 0 or B = 0 is a valid empty call.
  * ------------------------------------------------------------------------ */
 #define W4_I8 3
 #define W4_ROPE_HALF 0
 #define W4_ROPE_INTERLEAVED 1
+#define W4_KEYS 0
+#define W4_VALUES 1
 #define W4_MAX_SEQUENCES 1024
 #define W4_MAX_DRAFTS 64
 typedef struct {
@@ -654,13 +661,14 @@ w4_status w4_rope_table(const double* inv_freq, double factor, double scale, int
 w4_status w4_kv_append(const w4_kv_cache* c, const w4_kv_batch* b, const w4_rope* rope, const void* qkv, int x_type,
                        long long ld, int T, int Hq, const int* positions, const float* q_norm, const float* k_norm,
                        float eps, void* q, int q_type, unsigned flags, w4_stream_t s);
+w4_status w4_kv_values(const w4_kv_cache* c, int which, float* out, w4_stream_t s);
 size_t w4_tree_attention_workspace_bytes(const w4_kv_cache* c, const w4_kv_batch* b, int T, int Hq); /* 0: refused or empty */
 w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const void* q, int q_type, int T, int Hq,
                             const unsigned long long* mask, float scale, void* y, int y_type, void* workspace,
                             size_t ws_bytes, unsigned flags, w4_stream_t s);
 
 /* ------------------------------------------------------------------------
- * w4_logits_adjust, one launch: penalties for repeated tokens, biases and a
+ * w4_logits_adjust, one or two launches: penalties for repeated tokens, biases and a
  * grammar's mask on rows of logits, behind the vocabulary projection.
  *   Sequence s < S has length[s] tokens ids[s][..] (ids int [S][cap]), the
  *   first prompt[s] of them the prompt (prompt NULL: none), the others
@@ -678,7 +686,8 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
  *   factors float [S] may be NULL (1, 0 and 0), so may allowed (uint32 [R][ceil(V / 32)]).
  *   Ids outside 0 .. V - 1 are passed over.  logits: [R] rows of ld values of
  *   `type`, out the same with ld_out (it may be logits itself).  V <= 2^24,
- *   n_bias <= W4_MAX_BIASES.  flags: 0 or W4_FLAG_PDL.
+ *   n_bias <= W4_MAX_BIASES.  The rows must not overlap other than that.  flags:
+ *   0 or W4_FLAG_PDL (the same, as above).
  * ------------------------------------------------------------------------ */
 #define W4_MAX_BIASES 1024
 typedef struct {
