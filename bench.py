@@ -60,6 +60,10 @@ def parse_args(argv=None):
     p.add_argument("--decoder", choices=("off", "fused", "unfused"), default="off",
                    help="run the step with the RMSNorm, SwiGLU and residual adds of a decoder layer around "
                         "the linears: fused into them, or as separate kernels")
+    p.add_argument("--context", type=int, default=0, metavar="TOKENS",
+                   help="with --decoder: run the attention between QKV and O, too (rotation, append to a paged cache, "
+                        "28 query over 4 key heads of 128), over this many cached tokens; 0 leaves it out")
+    p.add_argument("--kv", choices=("bf16", "f16", "int8"), default="bf16", help="type of the cache of --context")
     p.add_argument("--suite", action="store_true",
                    help="instead of the step line: every GEMV of the single, 7B-layer, Gemma Q4_0 and lm_head "
                         "workloads on its own, then the full step at M = 1, 2, 4, 8, 16 (one JSON line each)")
@@ -89,7 +93,10 @@ def parse_args(argv=None):
                    help="profiler mode: eager step, graph warm-up and timed replays only (no e2e, no CPU "
                         "baseline, no clock sampling); the launch order is fixed: one eager step, then "
                         "warmup + steps graph replays")
-    return p.parse_args(argv)
+    args = p.parse_args(argv)
+    if args.context < 0 or (args.context and args.decoder == "off"):
+        p.error("--context takes a number of tokens and needs --decoder")
+    return args
 
 
 # ----------------------------------------------------------------- workload
@@ -138,7 +145,9 @@ def workload_config(args, n_gpus):
     } | ({} if args.decoder == "off" else {
         "decoder": args.decoder,
         "dataflow": ("decoder layers: RMSNorm -> QKV -> O (+ residual) -> RMSNorm -> gate/up -> SwiGLU -> down "
-                     "(+ residual); final RMSNorm -> lm_head; O reads the first M*3584 QKV outputs"),
+                     "(+ residual); final RMSNorm -> lm_head; "
+                     + (f"O reads the attention over {args.context} cached tokens and the step's own ({args.kv} cache, pages "
+                        "of 64)" if args.context else "O reads the first M*3584 QKV outputs")),
         "operators": ("fused into the linears (norm prologue, SwiGLU and residual epilogues)"
                       if args.decoder == "fused" else "separate kernels (w4_rmsnorm, w4_glu, w4_add)"),
     })
@@ -462,11 +471,24 @@ def build_step(args, device):
 NORM_EPS = 1e-6
 
 
+HEAD_DIM, KV_PAGE = 128, 64
+
+
+def attention_bytes(context: int, M: int, kv: str) -> int:
+    """Bytes the attention between QKV and O must move beside QKV's outputs and O's inputs: the cached keys and values (with
+    a scale per token and head for INT8) read once, the step's own written, and the rotated queries in 16 bits, both ways."""
+    token = 2 * (wl.QWEN7B_KV_DIM * (1 if kv == "int8" else 2) + (4 * wl.QWEN7B_KV_DIM // HEAD_DIM if kv == "int8" else 0))
+    return (context + 2 * M) * token + 2 * 2 * M * wl.QWEN7B_HIDDEN
+
+
 def build_decoder(args, device):
     """The step with the operators a decoder layer runs around its linears:
     per layer h += O(QKV(RMSNorm(h))[:, :3584]) and h += down(SiLU(gate) * up
-    of RMSNorm(h)), then logits = lm_head(RMSNorm(h)); attention is out of the
-    path (O reads the first M*3584 values of the QKV output in its place).
+    of RMSNorm(h)), then logits = lm_head(RMSNorm(h)).  Without --context
+    attention is out of the path (O reads the first M*3584 values of the QKV
+    output in its place); with it each layer has a paged cache of that many
+    tokens, and between QKV and O the step's M tokens (each sees those before
+    it) are rotated, appended and attend: three launches more a layer.
     decoder="fused": RMSNorm in the quantize prologue, SwiGLU and the residual
     add in the epilogue (gate/up paired per tile): 4 launches a layer + 1.
     decoder="unfused": the same arithmetic with w4_rmsnorm, w4_glu and w4_add
@@ -476,7 +498,7 @@ def build_decoder(args, device):
     each op takes the launch flags."""
     import torch
 
-    from bit_quantized_decode_gb300 import QuantLinear, _lib
+    from bit_quantized_decode_gb300 import CachedAttention, KVBatch, KVCache, QuantLinear, RopeTable, _lib
     fused = args.decoder == "fused"
     M = args.M
     H = wl.QWEN7B_HIDDEN
@@ -501,6 +523,15 @@ def build_decoder(args, device):
 
     h_in = wl.torch_normal((M, H), 4.0, 4999, device).contiguous()
     h = buf(M, H)
+    if args.context:
+        dims = dict(page_size=KV_PAGE, heads=wl.QWEN7B_KV_DIM // HEAD_DIM, head_dim=HEAD_DIM,
+                    dtype={"bf16": torch.bfloat16, "f16": torch.float16, "int8": torch.int8}[args.kv], device=device)
+        n_pages = (args.context + M + KV_PAGE - 1) // KV_PAGE
+        rope = RopeTable.build(args.context + M, HEAD_DIM, 1e6, device=device)
+        rows = KVBatch(torch.randperm(n_pages, device=device, dtype=torch.int32)[None].contiguous(),
+                       torch.full((1,), args.context, dtype=torch.int32, device=device),
+                       torch.tensor([0, M], dtype=torch.int32, device=device), max_tokens=M)
+        shared = None
     xn = buf(M, H)
     ops = []
     bytes_per_step = 0
@@ -512,6 +543,19 @@ def build_decoder(args, device):
         h_src = h_in if layer == 0 else h
         y_qkv = buf(M, qkv_l.N)
         x_o = y_qkv.view(-1)[: M * H].view(M, H)
+        attention = []
+        if args.context:
+            cache = KVCache.empty(n_pages, **dims)
+            for t in (cache.k, cache.v):                 # N(0, 1) keys and values, or codes with scales of 1/60
+                t.random_(-127, 128) if args.kv == "int8" else t.normal_()
+            if args.kv == "int8":
+                cache.k_scale.fill_(1 / 60)
+                cache.v_scale.fill_(1 / 60)
+            att = CachedAttention(cache, H // HEAD_DIM, rope=rope)
+            shared = shared or att.buffers(M, rows)
+            attention = [lambda f, a=att, y=y_qkv: a.append(y, rows, None, shared.q, f),
+                         lambda f, a=att: a.attend(shared.q, rows, None, shared.y, shared.workspace, f)]
+            x_o = shared.y.view(M, H)
         act = buf(M, wl.QWEN7B_INTERMEDIATE)
         q1, q2, q3, q4 = buf(M, H, dtype=torch.int8), buf(M, H, dtype=torch.int8), \
             buf(M, H, dtype=torch.int8), buf(M, down_l.K, dtype=torch.int8)
@@ -519,6 +563,7 @@ def build_decoder(args, device):
         if fused:
             ops += [
                 lambda f, a=h_src, y=y_qkv, q=q1, s=s1, L=qkv, g=g_attn: L(a, y, q, s, f, norm=g, eps=NORM_EPS),
+                *attention,
                 lambda f, a=x_o, r=h_src, q=q2, s=s2, L=o: L(a, h, q, s, f, residual=r),
                 lambda f, y=act, q=q3, s=s3, L=gu, g=g_mlp: L(h, y, q, s, f, norm=g, eps=NORM_EPS,
                                                                glu=_lib.W4_GLU_SILU),
@@ -531,6 +576,7 @@ def build_decoder(args, device):
             ops += [
                 lambda f, a=h_src, g=g_attn: _lib.w4_rmsnorm(a, g, NORM_EPS, xn, f),
                 lambda f, y=y_qkv, q=q1, s=s1, L=qkv: L(xn, y, q, s, f),
+                *attention,
                 lambda f, y=y_o, a=x_o, q=q2, s=s2, L=o: L(a, y, q, s, f),
                 lambda f, a=h_src, y=y_o: _lib.w4_add(a, y, h, f),
                 lambda f, g=g_mlp: _lib.w4_rmsnorm(h, g, NORM_EPS, xn, f),
@@ -544,6 +590,8 @@ def build_decoder(args, device):
         for lin in (qkv_l, o_l, gu_l, down_l):
             bytes_per_step += algorithmic_bytes(lin, M)
         bytes_per_step += 2 * 4 * H + 2 * 4 * M * H - 4 * M * wl.QWEN7B_INTERMEDIATE
+        if args.context:
+            bytes_per_step += attention_bytes(args.context, M, args.kv)
     head_l = wl.qwen7b_lm_head()
     head = linear(head_l)
     g_final = norm_weight()
@@ -599,7 +647,7 @@ def run_ours(args, rank, world, local_rank):
     if args.decoder != "off":
         ops, x_all, y_all, bytes_per_step = build_decoder(args, dev)
         items = []
-        launches = len(ops)
+        launches = len(ops) + (args.layers if args.context else 0)       # the attention joins its parts in a launch of its own
     else:
         items, x_all, y_all = build_step(args, dev)
         bytes_per_step = sum(algorithmic_bytes(lin, M) for _, lin, *_ in items)

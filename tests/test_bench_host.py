@@ -100,3 +100,15 @@ def test_suite_token_count_options():
     args = bench.parse_args(["--suite", "--suite-gemv-ms", "1,9,16", "--suite-ms", ""])
     assert args.suite and args.suite_gemv_ms == "1,9,16" and args.suite_ms == ""
     assert bench.parse_args([]).suite_gemv_ms == "1"      # single GEMVs at one token by default
+
+
+def test_attention_bytes_and_option():
+    """4096 cached tokens of 4 heads of 128: keys and values read once, the step's own written and read, queries both ways."""
+    assert bench.attention_bytes(4096, 1, "bf16") == (4096 + 2) * 2 * 512 * 2 + 2 * 2 * 3584
+    assert bench.attention_bytes(100, 16, "int8") == (100 + 32) * 2 * (512 + 16) + 2 * 2 * 16 * 3584
+    a = bench.parse_args(["--decoder", "fused", "--context", "4096", "--kv", "int8"])
+    assert a.context == 4096 and "4096 cached tokens" in bench.workload_config(a, 1)["dataflow"]
+    assert bench.parse_args([]).context == 0 and "attention" not in str(bench.workload_config(bench.parse_args(["--decoder", "fused"]), 1))
+    for bad in (["--context", "10"], ["--decoder", "fused", "--context", "-1"]):
+        with pytest.raises(SystemExit):
+            bench.parse_args(bad)
