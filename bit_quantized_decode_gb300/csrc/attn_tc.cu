@@ -17,8 +17,7 @@
 //               (exact scaling, the sums stay in fp32), and the output, which
 //               lies in tensor memory, is rescaled a few times per segment
 //               instead of once per tile;
-//   O += P V    P goes back to tensor memory in 16 bits (two or three parts for
-//               an fp32 output) and is the A operand; V as it lies, 64 values of a token in a row,
+//   O += P V    P goes back to tensor memory in 16 bits (in parts, as there) and is the A operand; V as it lies, 64 values of a token in a row,
 //               is an operand with its columns contiguous.
 // Warps: one orders copies, one issues MMAs, eight take the softmax; for an INT8
 // cache eight widen codes to 16 bits (exact) in shared memory.  All
@@ -33,7 +32,7 @@ constexpr int kTcRows = kAtTcRows, kTcUnit = kAtTcUnit;
 constexpr int kConvWarps = 8;                   // warps 2, 3, 12 .. 17: four for keys, four for values
 constexpr float kRaise = 12.0f;                 // log2 of what a probability may reach
 
-template <int D, int CT, bool kWide>
+template <int D, int CT, int kParts>
 struct Tc {
     static constexpr bool kI8 = CT == T_I8;
     static constexpr int kBoxes = D / 64;                     // 128-byte column groups of 16-bit values
@@ -45,11 +44,11 @@ struct Tc {
     static constexpr int kConv = kI8 ? (D == 256 ? 1 : 2) : kStages;   // 16-bit tiles
     static constexpr int kMeta = kStages + kConv + 2;         // tiles between the order of a tile's keys and the end of its softmax, at most
     static constexpr int kThreads = kI8 ? 384 + 32 * (kConvWarps - 2) : 384;
-    static constexpr int kPBufs = !kWide ? 3 : D == 256 ? 1 : 2;      // places for P
+    static constexpr int kPBufs = kParts == 1 ? 3 : D == 256 ? (kParts == 2 ? 2 : 1) : (kParts == 2 ? 3 : 2);   // places for P
     static constexpr int kCols = 512;
     static constexpr int cS = D, cP = D + 2 * kTcUnit, cQ = cP + 192;   // tensor-memory columns of S, P and Q; O begins at 0
     static_assert(!kQInT || cQ + D / 2 <= kCols, "tensor memory");
-    static_assert(cP + kPBufs * (kWide ? 96 : 32) <= (kQInT ? cQ : kCols), "tensor memory");
+    static_assert(cP + kPBufs * 32 * kParts <= (kQInT ? cQ : kCols), "tensor memory");
     // shared memory
     static constexpr int oQ = 0;
     static constexpr int oKv = kQ;                            // [kConv] keys, values
@@ -137,13 +136,12 @@ __device__ __forceinline__ float2 tc_unpair(uint32_t u)
     else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-template <int D, int CT, int QT, bool kWide>
-__global__ void __launch_bounds__(Tc<D, CT, kWide>::kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs A)
+template <int D, int CT, int QT, int kParts>
+__global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs A)
 {
-    using C = Tc<D, CT, kWide>;
+    using C = Tc<D, CT, kParts>;
     constexpr bool kI8 = C::kI8;
     constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
-    constexpr int kParts = !kWide ? 1 : PT == T_F16 ? 2 : 3;  // of a probability: 11 or 8 bits each
     constexpr int S = C::kStages, NC = C::kConv;
     extern __shared__ uint8_t raw_s[];
     uint8_t* smem = raw_s + ((1024u - (smem_u32(raw_s) & 1023u)) & 1023u);
@@ -743,11 +741,11 @@ __global__ void __launch_bounds__(Tc<D, CT, kWide>::kThreads, 1) attn_tc_kernel(
     if (warp == 1) tmem_dealloc(tb, C::kCols);
 }
 
-template <int D, int CT, int QT, bool kWide>
+template <int D, int CT, int QT, int kParts>
 cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 {
-    using C = Tc<D, CT, kWide>;
-    auto kern = attn_tc_kernel<D, CT, QT, kWide>;
+    using C = Tc<D, CT, kParts>;
+    auto kern = attn_tc_kernel<D, CT, QT, kParts>;
     static SmemLimit limit;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, C::smem(kAtMaxSeq));
     if constexpr (CT != T_I8) {
@@ -774,7 +772,9 @@ cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 template <int D, int CT, int QT>
 cudaError_t launch_w(AttnArgs& a, int grid, cudaStream_t s)
 {
-    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, s) : launch<D, CT, QT, false>(a, grid, s);
+    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, grid, s) : launch<D, CT, QT, 1>(a, grid, s);
+    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, grid, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, grid, s)
+                                                                                       : launch<D, CT, QT, 1>(a, grid, s);
 }
 
 template <int D>

@@ -18,8 +18,9 @@
 // result depends on timing.
 //
 // Precision: products of 16-bit numbers in fp32 sums; probabilities enter the
-// second product in 16 bits, as two numbers (high and low part) where the
-// output is fp32.  INT8 codes are exact in 16 bits; a key's scale multiplies its
+// second product in the values' 16-bit type, in as many parts (11 or 8 bits
+// each) as the output's type can tell: fp32 two of fp16 or three of bf16, fp16
+// two of bf16, else one.  INT8 codes are exact in 16 bits; a key's scale multiplies its
 // score, a value's scale its probability (bf16: no range of the scales is lost).
 #include <atomic>
 
@@ -128,12 +129,11 @@ __device__ __forceinline__ void codes16(uint32_t c, uint32_t& h01, uint32_t& h23
     else i8_to_bf16(c, h01, h23);
 }
 
-template <int D, int CT, int QT, bool kWide>
+template <int D, int CT, int QT, int kParts>
 __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const __grid_constant__ AttnArgs A)
 {
     using C = At<D, CT>;
     constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
-    constexpr int kParts = !kWide ? 1 : PT == T_F16 ? 2 : 3;  // of a probability: 11 or 8 bits each
     constexpr int W = C::kWarps;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                     }
                 // (the tensor cores cut a sum's low bits: in 32 bits an output's steps over the units are added here)
                 auto pv = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-                    if constexpr (kWide) {
+                    if constexpr (kParts > 1) {
                         float d[4] = {};
 #pragma unroll
                         for (int k = kParts - 1; k >= 0; --k) mma16<PT>(d, pa[k], b0, b1);
@@ -744,11 +744,11 @@ void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr)
     cfg.numAttrs = 1;
 }
 
-template <int D, int CT, int QT, bool kWide>
+template <int D, int CT, int QT, int kParts>
 cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 {
     using C = At<D, CT>;
-    auto kern = attn_tree_kernel<D, CT, QT, kWide>;
+    auto kern = attn_tree_kernel<D, CT, QT, kParts>;
     static SmemLimit limit;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, C::smem(kAtMaxSeq));
     if (e == cudaSuccess) e = encode_kv_map(&a.kmap, a, a.c.k, C::kBox, kAtUnit);
@@ -769,7 +769,9 @@ cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 template <int D, int CT, int QT>
 cudaError_t launch_w(AttnArgs& a, int grid, cudaStream_t s)
 {
-    return a.ytype == T_F32 ? launch<D, CT, QT, true>(a, grid, s) : launch<D, CT, QT, false>(a, grid, s);
+    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, grid, s) : launch<D, CT, QT, 1>(a, grid, s);
+    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, grid, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, grid, s)
+                                                                                       : launch<D, CT, QT, 1>(a, grid, s);
 }
 
 template <int D>

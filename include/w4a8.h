@@ -613,8 +613,9 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   does not reach it, infinities and NaN included.  q [T][Hq][D] of the
  *   cache's type (either 16-bit type for W4_I8), y [T][Hq][D] of y_type, both
  *   16-byte aligned; query head h reads key head h / (Hq / Hkv).
- *   Sums in fp32; probabilities in the second product are rounded to 16 bits
- *   for a 16-bit y, and are held in two 16-bit parts for W4_F32.
+ *   Sums in fp32; a probability enters the second product in the 16-bit type
+ *   of the values (bf16 for W4_I8): in one part where y is of no more bits, in
+ *   two or three where y is W4_F32, in two where y is W4_F16 and it is bf16.
  *   workspace: w4_tree_attention_workspace_bytes(..) bytes, 16-byte aligned,
  *   with no contents to keep; calls that share one must not overlap on the
  *   GPU.  Two launches.  For given inputs the result is the same in every

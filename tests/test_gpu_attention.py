@@ -45,9 +45,10 @@ def on_gpu(bq, lay, tensors, max_tokens=None):
 
 
 def units(cache_dtype, y_dtype):
-    """Relative rounding of a probability, of an output (a 32-bit one is divided and rounded too)."""
+    """Relative rounding of a probability (two parts and more where the output has more bits), of an output (a 32-bit one is
+    divided and rounded too)."""
     pt = F16 if cache_dtype == F16 else BF16
-    p = half_unit(pt) ** 2 * 2 if y_dtype == F32 else half_unit(pt)
+    p = half_unit(pt) ** 2 * 2 if y_dtype == F32 or (y_dtype, pt) == (F16, BF16) else half_unit(pt)
     return p, half_unit(y_dtype) + 2.0 ** -22
 
 
