@@ -75,7 +75,7 @@ struct AttnArgs {
     int T, Hq, G;             // G = Hq / Hkv
     void* y;                  // [T][Hq][D] of ytype
     int ytype;
-    int blocks, least;        // of the first launch: blocks, units of one at least
+    int blocks, least, extra; // of the first launch: blocks, units of one at least, units that a second piece is worth
     int* head;                // workspace: B + 1 prefix sums of units (more than 32 sequences)
     float* part;              // workspace: two partial results per block
     int part_rows;            // rows of one
@@ -84,8 +84,8 @@ struct AttnArgs {
 __host__ __device__ inline size_t attn_head_bytes(int B) { return (4 * (static_cast<size_t>(B) + 1) + 127) / 128 * 128; }
 // A partial result: running maxima, sums, and rows of D.
 __host__ __device__ inline size_t attn_part_floats(int rows, int D) { return static_cast<size_t>(rows) * (D + 2); }
-cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, cudaStream_t s);
-cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, cudaStream_t s);
+cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int sms, cudaStream_t s);
+cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int sms, cudaStream_t s);
 // Joins the partial results of either kernel (tiles of `rows` rows, units of `unit` tokens).
 cudaError_t launch_attn_join(const AttnArgs& a, int rows, int unit, cudaStream_t s);
 cudaError_t encode_kv_map(CUtensorMap* map, const AttnArgs& a, const void* base, int box_bytes, int box_rows);

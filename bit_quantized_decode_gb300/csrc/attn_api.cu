@@ -204,9 +204,8 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_head_bytes(b->B));
     a.part_rows = p.part_rows;
     a.err = d.err;
-    const int grid = d.sms < kAtMaxBlocks ? d.sms : kAtMaxBlocks;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-    const cudaError_t e = p.tc ? launch_attn_tc(a, q_type, grid, cs) : launch_attn_tree(a, q_type, grid, cs);
+    const cudaError_t e = p.tc ? launch_attn_tc(a, q_type, d.sms, cs) : launch_attn_tree(a, q_type, d.sms, cs);
     if (e != cudaSuccess) return W4_ERR_CUDA;
     return cuda_status(p.tc ? launch_attn_join(a, kAtTcRows, kAtTcUnit, cs) : launch_attn_join(a, kAtRows, kAtUnit, cs));
 }

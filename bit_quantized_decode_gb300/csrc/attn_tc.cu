@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
 }
 
 template <int D, int CT, int QT, int kParts>
-cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
+cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 {
     using C = Tc<D, CT, kParts>;
     auto kern = attn_tc_kernel<D, CT, QT, kParts>;
@@ -754,11 +754,12 @@ cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
         if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, 128, rows);
     }
     if (e != cudaSuccess) return e;
-    a.blocks = grid;
+    a.blocks = sms < kAtMaxBlocks ? sms : kAtMaxBlocks;
+    a.extra = 6;                                // (4 us at 0.7 us a unit)
     a.least = 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.blocks));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::smem(a.b.B);
     cfg.stream = s;
@@ -770,27 +771,27 @@ cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 }
 
 template <int D, int CT, int QT>
-cudaError_t launch_w(AttnArgs& a, int grid, cudaStream_t s)
+cudaError_t launch_w(AttnArgs& a, int sms, cudaStream_t s)
 {
-    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, grid, s) : launch<D, CT, QT, 1>(a, grid, s);
-    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, grid, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, grid, s)
-                                                                                       : launch<D, CT, QT, 1>(a, grid, s);
+    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, sms, s) : launch<D, CT, QT, 1>(a, sms, s);
+    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, sms, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, sms, s)
+                                                                                       : launch<D, CT, QT, 1>(a, sms, s);
 }
 
 template <int D>
-cudaError_t launch_d(AttnArgs& a, int qtype, int grid, cudaStream_t s)
+cudaError_t launch_d(AttnArgs& a, int qtype, int sms, cudaStream_t s)
 {
-    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, s);
-    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, s);
-    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, s) : launch_w<D, T_I8, T_BF16>(a, grid, s);
+    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, sms, s);
+    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, sms, s);
+    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, sms, s) : launch_w<D, T_I8, T_BF16>(a, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int grid, cudaStream_t s)
+cudaError_t launch_attn_tc(AttnArgs& a, int qtype, int sms, cudaStream_t s)
 {
-    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, s)
-                                                                            : launch_d<256>(a, qtype, grid, s);
+    return a.c.D == 64 ? launch_d<64>(a, qtype, sms, s) : a.c.D == 128 ? launch_d<128>(a, qtype, sms, s)
+                                                                            : launch_d<256>(a, qtype, sms, s);
 }
 
 }  // namespace w4k

@@ -37,11 +37,12 @@ struct At {
     static constexpr int kBoxes = kRow / kBox;
     static constexpr int kHalf = kAtUnit * kRow;              // a unit's keys (or values)
     static constexpr int kSlot = 2 * kHalf;
+    // (two blocks of four warps per SM: 1 token over 131071 places 52.1 us, one of eight 48.7; 64 streams the same)
     static constexpr int kWarps = D == 256 ? 4 : 8;
+    static constexpr int kParts = kWarps == 4 ? 1 : 2;        // joined row blocks: warps take turns on one
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRing = 192 * 1024 / (kWarps * kSlot);
     static constexpr int kSlots = kRing > 6 ? 6 : kRing;      // units ahead of a warp
-    static constexpr int kParts = kWarps == 4 ? 1 : 2;        // joined row blocks: warps take turns on one
     static constexpr int kPad = D + 8;                        // floats of a joined row: rows spread over the banks
     // shared memory
     static constexpr int oRing = 0;
@@ -266,10 +267,6 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
     for (int k = 0; k < C::kSlots; ++k) order(k);
 #pragma unroll 1
     for (int begin = us; begin < ue;) {
-        if (begin != us) {
-            sg = find_segment(A, lay, begin, kAtRows, kAtUnit);
-            load_rows(sg, rows_of(sg));
-        }
         const int end = min(sg.u0 + sg.units, ue), rows = rows_of(sg);
         float o[D / 8][4];
 #pragma unroll
@@ -482,6 +479,11 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
         }
 
         // -------------------------------------------- the warps' results joined
+        const Segment done = sg;
+        if (end < ue) {                         // (the next queries are on their way meanwhile)
+            sg = find_segment(A, lay, end, kAtRows, kAtUnit);
+            load_rows(sg, rows_of(sg));
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             return (g + 8 * e) * C::kPad + d;
         };
         // Behind the block's last unit the rings are free (every copy was waited for): a place for each warp.  Before, the
-        // warps take turns on two.
+        // warps take turns on one or two.
         const bool idle = end == ue && !lost;
         float* area = idle ? reinterpret_cast<float*>(smem + C::oRing) : join_s;
         const int parts = idle ? W : C::kParts, turns = W / parts;
@@ -534,8 +536,8 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             }
             __syncthreads();
         }
-        const bool whole = begin == sg.u0 && end == sg.u0 + sg.units;
-        float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
+        const bool whole = begin == done.u0 && end == done.u0 + done.units;
+        float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < done.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
         if (!whole && tid < rows) {
             part[tid] = fin_s[tid];
             part[A.part_rows + tid] = fin_s[kAtRows + tid];
@@ -544,19 +546,16 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
             const int r = k / (D / 4), d = k % (D / 4) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int w = 0; w < parts; w += C::kParts) {
-#pragma unroll
-                for (int i = 0; i < C::kParts; ++i) {
-                    const float4 t = *reinterpret_cast<const float4*>(area + ((w + i) * kAtRows + r) * C::kPad + d);
-                    v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
-                }
+            for (int w = 0; w < parts; ++w) {
+                const float4 t = *reinterpret_cast<const float4*>(area + (w * kAtRows + r) * C::kPad + d);
+                v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
             }
             if (!whole) {
                 *reinterpret_cast<float4*>(part + 2 * A.part_rows + r * D + d) = v;
             } else {
                 const float sum = fin_s[kAtRows + r], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const int rr = sg.tile * kAtRows + r, tok = rr / A.G;
-                const size_t y = (static_cast<size_t>(sg.f.q0 + tok) * A.Hq + sg.h * A.G + (rr - tok * A.G)) * D + d;
+                const int rr = done.tile * kAtRows + r, tok = rr / A.G;
+                const size_t y = (static_cast<size_t>(done.f.q0 + tok) * A.Hq + done.h * A.G + (rr - tok * A.G)) * D + d;
                 const float w[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
                 if (A.ytype == T_F32) *reinterpret_cast<float4*>(static_cast<float*>(A.y) + y) = make_float4(w[0], w[1], w[2], w[3]);
                 else if (A.ytype == T_F16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + y) = make_uint2(pair16<T_F16>(w[0], w[1]), pair16<T_F16>(w[2], w[3]));
@@ -745,7 +744,7 @@ void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr)
 }
 
 template <int D, int CT, int QT, int kParts>
-cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
+cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 {
     using C = At<D, CT>;
     auto kern = attn_tree_kernel<D, CT, QT, kParts>;
@@ -754,11 +753,12 @@ cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
     if (e == cudaSuccess) e = encode_kv_map(&a.kmap, a, a.c.k, C::kBox, kAtUnit);
     if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, C::kBox, kAtUnit);
     if (e != cudaSuccess) return e;
-    a.blocks = grid;
+    a.blocks = sms < kAtMaxBlocks ? sms : kAtMaxBlocks;
+    a.extra = 16;                               // (3 us at 185 ns a unit)
     a.least = C::kWarps;                        // a unit for each warp
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.blocks));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::smem(a.b.B);
     cfg.stream = s;
@@ -767,19 +767,19 @@ cudaError_t launch(AttnArgs& a, int grid, cudaStream_t s)
 }
 
 template <int D, int CT, int QT>
-cudaError_t launch_w(AttnArgs& a, int grid, cudaStream_t s)
+cudaError_t launch_w(AttnArgs& a, int sms, cudaStream_t s)
 {
-    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, grid, s) : launch<D, CT, QT, 1>(a, grid, s);
-    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, grid, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, grid, s)
-                                                                                       : launch<D, CT, QT, 1>(a, grid, s);
+    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, sms, s) : launch<D, CT, QT, 1>(a, sms, s);
+    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, sms, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, sms, s)
+                                                                                       : launch<D, CT, QT, 1>(a, sms, s);
 }
 
 template <int D>
-cudaError_t launch_d(AttnArgs& a, int qtype, int grid, cudaStream_t s)
+cudaError_t launch_d(AttnArgs& a, int qtype, int sms, cudaStream_t s)
 {
-    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, grid, s);
-    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, grid, s);
-    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, grid, s) : launch_w<D, T_I8, T_BF16>(a, grid, s);
+    if (a.c.type == T_F16) return launch_w<D, T_F16, T_F16>(a, sms, s);
+    if (a.c.type == T_BF16) return launch_w<D, T_BF16, T_BF16>(a, sms, s);
+    return qtype == T_F16 ? launch_w<D, T_I8, T_F16>(a, sms, s) : launch_w<D, T_I8, T_BF16>(a, sms, s);
 }
 
 }  // namespace
@@ -824,10 +824,10 @@ cudaError_t launch_attn_join(const AttnArgs& a, int rows, int unit, cudaStream_t
                               a, rows, unit);
 }
 
-cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int grid, cudaStream_t s)
+cudaError_t launch_attn_tree(AttnArgs& a, int qtype, int sms, cudaStream_t s)
 {
-    return a.c.D == 64 ? launch_d<64>(a, qtype, grid, s) : a.c.D == 128 ? launch_d<128>(a, qtype, grid, s)
-                                                                            : launch_d<256>(a, qtype, grid, s);
+    return a.c.D == 64 ? launch_d<64>(a, qtype, sms, s) : a.c.D == 128 ? launch_d<128>(a, qtype, sms, s)
+                                                                            : launch_d<256>(a, qtype, sms, s);
 }
 
 }  // namespace w4k

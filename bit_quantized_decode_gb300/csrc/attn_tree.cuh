@@ -45,8 +45,9 @@ struct Segment {
 // barrier); more lie as prefix sums in shared memory.  All calls are a whole warp's.
 //
 // Blocks take equal shares of the units, across segments.  A block that ends one segment and begins another pays twice
-// for queries and joining (4.5 us of 10.7 for one token over 1000 places), so where segments are few (a quarter of the
-// blocks at most) each gets blocks of its own instead: n for every segment of a sequence, in near equal parts.
+// for queries and joining (4.5 us of 10.7 for one token over 1000 places, since then 3).  So segments get blocks of their own
+// instead, n for every segment of a sequence in near equal parts, where that makes no block's share longer by more than
+// those 3 us.
 struct Layout {
     const int* pre;           // [B + 1] in shared memory; null: in the lanes
     int mine;            // units before this lane's sequence
@@ -83,16 +84,24 @@ __device__ __forceinline__ Layout lane_layout(const AttnArgs& A, int rows, int u
     const int upto = warp_scan(v, lane);
     L.mine = upto - v;
     L.total = __shfl_sync(0xffffffffu, upto, 31);
-    const int all = __reduce_add_sync(0xffffffffu, segs);
     L.n = L.mine_b = L.blocks = 0;
-    if (4 * all > A.blocks) {
-        L.share = max((L.total + A.blocks - 1) / A.blocks, A.least);
-        return L;
+    L.share = max((L.total + A.blocks - 1) / A.blocks, A.least);
+    // the fewest units to a block with which all segments' parts find one, if that is not much more than an equal share
+    auto fits = [&](int part) { return __reduce_add_sync(0xffffffffu, segs * ((units + part - 1) / part)) <= A.blocks; };
+    if (__reduce_max_sync(0xffffffffu, segs) > A.blocks) return L;
+    int hi = L.share;
+    if (!fits(hi)) {                            // (each look costs some 0.1 us, so an even split comes first)
+        hi += A.extra;
+        if (!fits(hi)) return L;
+        int lo = L.share + 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (fits(mid)) hi = mid;
+            else lo = mid + 1;
+        }
     }
-    // as many units to a block that the segments' last, partly filled blocks still have room
     L.share = 0;
-    const int part = max((L.total + A.blocks - all - 1) / (A.blocks - all), A.least);
-    L.n = (units + part - 1) / part;
+    L.n = (units + hi - 1) / hi;
     const int b = warp_scan(segs * L.n, lane);
     L.mine_b = b - segs * L.n;
     L.blocks = __shfl_sync(0xffffffffu, b, 31);
