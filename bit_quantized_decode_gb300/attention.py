@@ -22,8 +22,9 @@ class KVCache:
     float32 [pages][heads][page_size]."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.desc = _lib.kv_cache(k, v, k_scale, v_scale)
+
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self.desc._tensors[i]) for i in range(4))
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda") -> "KVCache":
@@ -61,8 +62,11 @@ class RopeTable:
     "interleaved" (pairs 2 i, 2 i + 1)."""
 
     def __init__(self, turns, layout: str = "half"):
-        self.turns = turns
         self.desc = _lib.rope_desc(turns, layout)
+
+    @property
+    def turns(self):
+        return self.desc._tensors[0]
 
     @staticmethod
     def frequencies(rot: int, base: float = 10000.0, scaling: dict = None):

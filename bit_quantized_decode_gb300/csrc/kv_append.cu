@@ -6,15 +6,16 @@
 //   a' = a c - b s, b' = b c + a s   over pairs of the first `rot` values
 //   16-bit cache: rounded once; INT8: s = max|x'| / 127, q = clip(rint(x' / s)).
 //
-// D / 8 lanes take a head, eight values to a lane: a lane of the half layout
-// holds four values and their four partners, so a rotation needs no exchange,
-// and a pair's (cos, sin) is read once for all heads of a warp.  A warp takes 4, 2 or
+// D / 8 lanes take a head, eight values to a lane, pairs within a lane: a
+// rotation needs no exchange, and a pair's (cos, sin) is read once for all heads of a warp.  A warp takes 4, 2 or
 // 1 heads of a token at a time (D 64, 128, 256).  An INT8 code hangs on the last bit of a
 // value, so a key for an INT8 cache is rotated with exact products and a compensated
 // sum (rounded once), and its squares are summed in compensated pairs as in the other
 // fused norms; numbers that are rounded to 16 bits take plain fp32 sums and rsqrtf
-// (2^-20 of the value at most).  Prompts are bound by memory and, with norms, by
-// instructions; a few tokens by the chain of loads (row's sequence, its length, the page).
+// (2^-20 of the value at most).  A few tokens are bound by the launch and the chain of
+// loads (row's sequence and length, then page and rotation, beside the values): one token 2.2 us,
+// 16 drafts to INT8 2.5.  Prompts (12,300 rows of 2560 bf16 values with norms to fp16, 136 MB): 45 us, 3.0 TB/s,
+// without norms 37: the same chain at the start of each warp, then instructions (issue slots 57% taken).
 #include "attention.h"
 #include "fusion.cuh"
 #include "ptx.cuh"
@@ -23,28 +24,40 @@
 namespace w4k {
 namespace {
 
-template <int T>
-__device__ __forceinline__ void load4(const void* base, size_t at, float* v)
+// Four consecutive fp32 values.
+__device__ __forceinline__ void load4(const float* p, float* v)
 {
-    if constexpr (T == T_F32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + at));
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at));
-        const uint32_t w[2] = {u.x, u.y};
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+
+// Four values as they lie in memory, and widened.
+template <int T>
+struct Raw4 {
+    uint2 v;
+    __device__ __forceinline__ void load(const void* base, size_t at) { v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at)); }
+    __device__ __forceinline__ void widen(float* f) const
+    {
+        const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if constexpr (T == T_F16) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                v[2 * k] = f.x;
-                v[2 * k + 1] = f.y;
-            } else {
-                v[2 * k] = __uint_as_float(w[k] << 16);
-                v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                f[2 * k] = h.x;
+                f[2 * k + 1] = h.y;
+            } else {                                          // bf16: the upper half of an fp32
+                f[2 * k] = __uint_as_float(w[k] << 16);
+                f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
         }
     }
-}
+};
+template <>
+struct Raw4<T_F32> {
+    float4 v;
+    __device__ __forceinline__ void load(const void* base, size_t at) { v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + at)); }
+    __device__ __forceinline__ void widen(float* f) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
 
 __device__ __forceinline__ uint32_t pack16(int type, float a, float b)
 {
@@ -83,33 +96,57 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
     const int g0 = static_cast<int>(task - static_cast<long long>(t) * parts) * A.per, g1 = min(g0 + A.per, groups);
     const int u = lane % kLanes;                // eight values of the head
 
-    // a head's values as they lie: of a rotated half-layout unit 4u.. and rot/2 + 4u.., else 8u..
+    // A lane's eight values are two fours, half of a part of the head apart (the rotated part, the rest, or a value head's
+    // whole), so that lanes beside each other read and write beside each other: whole sectors in every access.  In the half
+    // layout the second four are the partners of the first; interleaved pairs lie within a four.
     const int rotated = A.Hq + A.c.Hkv;
-    const size_t row = static_cast<size_t>(t) * A.ld;
-    auto load = [&](int g, float* x) {
-        const int head = g * kHeads + lane / kLanes;
-        const bool split = 8 * u < A.rot && head < rotated && !A.interleaved;
-        const size_t base = row + static_cast<size_t>(head < H ? head : 0) * D;
-        load4<XT>(A.x, base + (split ? 4 * u : 8 * u), x);
-        load4<XT>(A.x, base + (split ? A.rot / 2 + 4 * u : 8 * u + 4), x + 4);
+    const bool turns = 8 * u < A.rot;           // (this lane's values of a query or key head)
+    const int at0 = turns ? 4 * u : A.rot / 2 + 4 * u, at1 = at0 + (turns ? A.rot : D - A.rot) / 2;
+    const size_t row = static_cast<size_t>(t) * A.ld + (lane / kLanes) * D;
+    constexpr int kAhead = 2;                   // heads whose loads are in flight
+    Raw4<XT> lo[kAhead], hi[kAhead];
+    auto load = [&](int g) {
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            const int head = (g + e) * kHeads + lane / kLanes;
+            if (g + e < g1) {
+                const size_t base = head < H ? row + (g + e) * (kHeads * D) : row;
+                const bool plain = head >= rotated;
+                lo[e].load(A.x, base + (plain ? 4 * u : at0));
+                hi[e].load(A.x, base + (plain ? D / 2 + 4 * u : at1));
+            }
+        }
     };
-    float ahead[8];
-    load(g0, ahead);
+    load(g0);
 
-    const int b = row_sequence(A.b.q_start, A.b.B, t, lane);
-    if (b >= A.b.B) return;                     // behind the last sequence
-    const int i = t - __ldg(A.b.q_start + b);
-    if (i < 0) return;
-    const long long place = static_cast<long long>(max(__ldg(A.b.ctx + b), 0)) + i;
+    // the row's sequence: with up to 32 of them everything about them is asked for at once (a round of loads is a third of a
+    // few tokens' time)
+    const int told = A.pos != nullptr ? __ldg(A.pos + t) : 0;
+    int b, i, before;
+    if (A.b.B <= 32) {
+        const bool is = lane < A.b.B;
+        const int q0 = is ? __ldg(A.b.q_start + lane) : 0, q1 = is ? __ldg(A.b.q_start + lane + 1) : 0;
+        before = is ? __ldg(A.b.ctx + lane) : 0;
+        b = __popc(__ballot_sync(0xffffffffu, is && q1 <= t));
+        i = t - __shfl_sync(0xffffffffu, q0, b & 31);
+        before = __shfl_sync(0xffffffffu, before, b & 31);
+    } else {
+        b = row_sequence(A.b.q_start, A.b.B, t, lane);
+        i = b < A.b.B ? t - __ldg(A.b.q_start + b) : 0;
+        before = b < A.b.B ? __ldg(A.b.ctx + b) : 0;
+    }
+    if (b >= A.b.B || i < 0) return;            // behind the last sequence
+    const long long place = static_cast<long long>(max(before, 0)) + i;
     const bool i8 = A.c.type == T_I8;
     bool lost = false;                          // a position that the table does not have
-    float cs[8];                                // (cos, sin) of pairs 4u .. 4u + 3
+    float cs[8];                                // (cos, sin) of this lane's four pairs
     if (A.rot > 0) {
-        const long long p = A.pos != nullptr ? __ldg(A.pos + t) : place;
+        const long long p = A.pos != nullptr ? told : place;
         lost = p < 0 || p >= A.positions;
-        if (8 * u < A.rot) {
-            load4<T_F32>(A.turns, static_cast<size_t>(lost ? 0 : p) * A.rot + 8 * u, cs);
-            load4<T_F32>(A.turns, static_cast<size_t>(lost ? 0 : p) * A.rot + 8 * u + 4, cs + 4);
+        if (turns) {
+            const float* cp = A.turns + static_cast<size_t>(lost ? 0 : p) * A.rot;
+            load4(cp + (A.interleaved ? 4 * u : 8 * u), cs);
+            load4(cp + (A.interleaved ? A.rot / 2 + 4 * u : 8 * u + 4), cs + 4);
             if (lost)
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) cs[k] = __int_as_float(0x7fc00000);
@@ -121,33 +158,38 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
     const bool stored = page >= 0 && page < A.c.pages;
     const size_t slot0 = static_cast<size_t>(stored ? page : 0) * A.c.Hkv * A.c.page + static_cast<size_t>(place & (A.c.page - 1));
 
-#pragma unroll 1
-    for (int g = g0; g < g1; ++g) {
+    const bool normed = A.q_norm != nullptr || A.k_norm != nullptr;
+    const float* w_of = nullptr;                // the norm weights at hand
+    float w[8];
+    uint16_t* const q_row = static_cast<uint16_t*>(A.q) + static_cast<size_t>(t) * A.Hq * D;
+    auto one = [&](int g, const Raw4<XT>& l, const Raw4<XT>& h4) {
         float x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = ahead[k];
-        if (g + 1 < g1) load(g + 1, ahead);
+        l.widen(x);
+        h4.widen(x + 4);
         const int head = g * kHeads + lane / kLanes;
         const bool have = head < H, is_q = head < A.Hq, is_k = !is_q && head < rotated;
-        const bool turned = 8 * u < A.rot && head < rotated, split = turned && !A.interleaved;
-        const int at0 = split ? 4 * u : 8 * u, at1 = split ? A.rot / 2 + 4 * u : 8 * u + 4;
         // codes hang on the last bit of an INT8 cache's keys; what is rounded to 16 bits takes plain fp32 sums
         const bool coded = i8 && g * kHeads < rotated && (g + 1) * kHeads > A.Hq;     // (of the whole warp)
-        const float* w_n = is_q ? A.q_norm : is_k ? A.k_norm : nullptr;
-        if ((A.q_norm != nullptr || A.k_norm != nullptr) && g * kHeads < rotated) {
+        if (normed && g * kHeads < rotated) {
+            const float* const w_n = is_q ? A.q_norm : is_k ? A.k_norm : nullptr;
+            if (w_n != w_of && w_n != nullptr) {
+                w_of = w_n;
+                load4(w_n + at0, w);
+                load4(w_n + at1, w + 4);
+            }
             float r;
             if (coded) {
-                float hi = 0.0f, lo = 0.0f;
+                float sh = 0.0f, sl = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sq_acc(x[k], hi, lo);
+                for (int k = 0; k < 8; ++k) sq_acc(x[k], sh, sl);
 #pragma unroll
                 for (int off = kLanes / 2; off > 0; off >>= 1) {
-                    const float h2 = __shfl_xor_sync(0xffffffffu, hi, off), l2 = __shfl_xor_sync(0xffffffffu, lo, off);
-                    pair_merge(hi, lo, h2, l2);
+                    const float h2 = __shfl_xor_sync(0xffffffffu, sh, off), l2 = __shfl_xor_sync(0xffffffffu, sl, off);
+                    pair_merge(sh, sl, h2, l2);
                 }
-                hi = __shfl_sync(0xffffffffu, hi, lane - u);  // (the same sum in every lane of the head)
-                lo = __shfl_sync(0xffffffffu, lo, lane - u);
-                r = rms_scale(hi, lo, D, A.eps);
+                sh = __shfl_sync(0xffffffffu, sh, lane - u);  // (the same sum in every lane of the head)
+                sl = __shfl_sync(0xffffffffu, sl, lane - u);
+                r = rms_scale(sh, sl, D, A.eps);
             } else {
                 float sum = 0.0f;
 #pragma unroll
@@ -157,58 +199,45 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
                 r = rsqrtf(__fmaf_rn(sum, 1.0f / D, A.eps));
             }
             if (w_n != nullptr) {
-                float w[8];
-                load4<T_F32>(w_n, at0, w);
-                load4<T_F32>(w_n, at1, w + 4);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(__fmul_rn(x[k], r), w[k]);
             }
         }
-        if (turned) {
-            float pa[4], pb[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) pa[k] = split ? x[k] : x[2 * k], pb[k] = split ? x[4 + k] : x[2 * k + 1];
-            if (coded) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float a = pa[k], v = pb[k];
-                    pa[k] = dot2_once(a, cs[2 * k], -v, cs[2 * k + 1]);
-                    pb[k] = dot2_once(v, cs[2 * k], a, cs[2 * k + 1]);
+        if (turns && head < rotated) {
+            auto turn = [&](float& a, float& v, float c, float s) {
+                const float p = a, q = v;
+                if (coded) {
+                    a = dot2_once(p, c, -q, s);
+                    v = dot2_once(q, c, p, s);
+                } else {
+                    a = __fmaf_rn(p, c, -__fmul_rn(q, s));
+                    v = __fmaf_rn(q, c, __fmul_rn(p, s));
                 }
+            };
+            if (A.interleaved) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) turn(x[2 * k], x[2 * k + 1], cs[2 * k], cs[2 * k + 1]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float a = pa[k], v = pb[k];
-                    pa[k] = __fmaf_rn(a, cs[2 * k], -__fmul_rn(v, cs[2 * k + 1]));
-                    pb[k] = __fmaf_rn(v, cs[2 * k], __fmul_rn(a, cs[2 * k + 1]));
-                }
+                for (int k = 0; k < 4; ++k) turn(x[k], x[4 + k], cs[2 * k], cs[2 * k + 1]);
             }
-            x[0] = pa[0];
-            x[1] = split ? pa[1] : pb[0];
-            x[2] = split ? pa[2] : pa[1];
-            x[3] = split ? pa[3] : pb[1];
-            x[4] = split ? pb[0] : pa[2];
-            x[5] = split ? pb[1] : pb[2];
-            x[6] = split ? pb[2] : pa[3];
-            x[7] = pb[3];
         }
+        const bool plain = head >= rotated;
+        const int o0 = plain ? 4 * u : at0, o1 = plain ? D / 2 + 4 * u : at1;
         const int hk = is_k ? head - A.Hq : head - rotated;
         const size_t slot = slot0 + static_cast<size_t>(is_q || !have ? 0 : hk) * A.c.page;
         const bool store = have && !is_q && stored;
         if (is_q || (store && !i8)) {
-            const int type = is_q ? A.qtype : A.c.type;
-            uint16_t* d = is_q ? static_cast<uint16_t*>(A.q) + (static_cast<size_t>(t) * A.Hq + head) * D
-                               : static_cast<uint16_t*>(is_k ? A.c.k : A.c.v) + slot * D;
-            const uint2 lo = make_uint2(pack16(type, x[0], x[1]), pack16(type, x[2], x[3]));
-            const uint2 hi = make_uint2(pack16(type, x[4], x[5]), pack16(type, x[6], x[7]));
-            if (split) {
-                *reinterpret_cast<uint2*>(d + at0) = lo;
-                *reinterpret_cast<uint2*>(d + at1) = hi;
-            } else {
-                *reinterpret_cast<uint4*>(d + at0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            }
+            uint16_t* d = is_q ? q_row + head * D : static_cast<uint16_t*>(is_k ? A.c.k : A.c.v) + slot * D;
+            uint4 h;
+            if ((is_q ? A.qtype : A.c.type) == T_F16)
+                h = make_uint4(pack16(T_F16, x[0], x[1]), pack16(T_F16, x[2], x[3]), pack16(T_F16, x[4], x[5]), pack16(T_F16, x[6], x[7]));
+            else
+                h = make_uint4(pack16(T_BF16, x[0], x[1]), pack16(T_BF16, x[2], x[3]), pack16(T_BF16, x[4], x[5]), pack16(T_BF16, x[6], x[7]));
+            *reinterpret_cast<uint2*>(d + o0) = make_uint2(h.x, h.y);
+            *reinterpret_cast<uint2*>(d + o1) = make_uint2(h.z, h.w);
         }
-        if (!i8 || (g + 1) * kHeads <= A.Hq) continue;        // (of the whole warp)
+        if (!i8 || (g + 1) * kHeads <= A.Hq) return;          // (of the whole warp)
         float top = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
@@ -220,11 +249,18 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
             const bool nan = lost && is_k;
             if (nan) q = make_uint2(0u, 0u);
             int8_t* d = static_cast<int8_t*>(is_k ? A.c.k : A.c.v) + slot * D;
-            *reinterpret_cast<uint32_t*>(d + at0) = q.x;
-            *reinterpret_cast<uint32_t*>(d + at1) = q.y;
+            *reinterpret_cast<uint32_t*>(d + o0) = q.x;
+            *reinterpret_cast<uint32_t*>(d + o1) = q.y;
             if (u == 0) (is_k ? A.c.ks : A.c.vs)[slot] = nan ? __int_as_float(0x7fc00000) : ks.s;
         }
         __syncwarp();
+    };
+#pragma unroll 1
+    for (int g = g0; g < g1; g += kAhead) {
+        if (g > g0) load(g);
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+            if (g + e < g1) one(g + e, lo[e], hi[e]);
     }
 }
 

@@ -17,6 +17,8 @@
 // counts in dense slices had a block wait for its history in every slice: 200
 // rows of 262144 with 1500 tokens took 100 us, 63 of them the bytes.)
 // Integer counts: their order does not matter.
+// 200 rows of 262144 fp32 logits under a grammar, 1500 tokens each: 87 us, the copy 62 of them (6.8 TB/s); rows of an odd width
+// as fast.  One row of 152064 with 4096 tokens and 40 biases: 6.4 us.
 #include "attention.h"
 #include "ptx.cuh"
 #include "typed_io.cuh"

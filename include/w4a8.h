@@ -599,9 +599,10 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   (W4_ROPE_INTERLEAVED): a' = a c - b s, b' = b c + a s.  A position that
  *   the table does not have gives NaN (in an INT8 cache: the scale).  q [T][Hq][D] of q_type
  *   (W4_F16 or W4_BF16), 16-byte aligned; k and v go to the cache, rounded
- *   once, or as the codes and scale that a8_quantize gives for a head's
- *   values (the norm's steps as in rms_a8_quantize; a rotated value of a key
- *   rounded once to fp32).  Two rows with the same place race.
+ *   once (norms of what goes to 16 bits are plain fp32 sums), or as the codes
+ *   and scale that a8_quantize gives for a head's values (the norm's steps
+ *   then as in rms_a8_quantize, a rotated value of a key rounded once to
+ *   fp32).  Two rows with the same place race.
  * w4_kv_values: out float [pages][Hkv][page_size][D], 16-byte aligned: the
  *   numbers that an INT8 cache's keys (W4_KEYS) or values (W4_VALUES) stand
  *   for, codes times scales, every page of the cache.
@@ -686,7 +687,8 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
  *   each step an fp32 operation, rounded to the logits' type.  The arrays of
  *   factors float [S] may be NULL (1, 0 and 0), so may allowed (uint32 [R][ceil(V / 32)]).
  *   Ids outside 0 .. V - 1 are passed over.  logits: [R] rows of ld values of
- *   `type`, out the same with ld_out (it may be logits itself).  V <= 2^24,
+ *   `type`, out the same with ld_out (it may be logits itself, with
+ *   the same ld).  V <= 2^24,
  *   n_bias <= W4_MAX_BIASES.  The rows must not overlap other than that.  flags:
  *   0 or W4_FLAG_PDL (the same, as above).
  * ------------------------------------------------------------------------ */

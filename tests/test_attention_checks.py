@@ -141,7 +141,7 @@ LOGITS = dict(logits=FAKE, type=0, ld=100, R=3, row_start=None, drafts=None, mas
     ({}, dict(ld=99), INVALID), ({}, dict(ld_out=99), INVALID), ({}, dict(drafts=FAKE), INVALID),
     ({}, dict(mask=FAKE, row_start=FAKE), INVALID), ({}, dict(logits=None), INVALID), ({}, dict(out=None), INVALID),
     ({}, dict(logits=ODD2), MISALIGNED), ({}, dict(out=ODD2), MISALIGNED), ({}, dict(type=2, out=ctypes.c_void_p(0x1001)), MISALIGNED),
-    ({}, dict(row_start=ODD2), MISALIGNED), ({}, dict(allowed=ODD2), MISALIGNED),
+    ({}, dict(row_start=ODD2), MISALIGNED), ({}, dict(allowed=ODD2), MISALIGNED), ({}, dict(ld_out=104), INVALID),
     ({}, dict(row_start=FAKE, drafts=FAKE, mask=ODD), MISALIGNED), ({}, dict(R=0, logits=None, out=None), OK),
     (dict(V=0), dict(logits=None, out=None, ld=0, ld_out=0), OK), (dict(S=0), dict(logits=None, out=None), OK)])
 def test_logit_arguments(L, rules, change, status):
@@ -238,3 +238,45 @@ def test_scaled_frequencies():
     mid = (turns > 1) & (turns < 32)
     assert bool(((parts < inv) & (parts * 4 > inv))[mid].all()) and abs(scale - (0.1 * math.log(4) + 1)) < 1e-15
     assert RopeTable.frequencies(128, 1e6, {"kind": "by_parts", "factor": 4.0, "trained": 4096, "attention": 1.0})[1] == 1.0
+
+
+def test_memory_that_moved_is_checked_again(L, monkeypatch):
+    """A cache, a batch or rules whose tensors got other memory behind them: the addresses of the call, checked again."""
+    import types
+
+    import bit_quantized_decode_gb300 as bq
+    seen = []
+    fake = types.SimpleNamespace(**{n: (lambda *a, n=n: seen.append((n, a)) or 0) for n in ("w4_kv_append", "w4_tree_attention", "w4_logits_adjust")},
+                                 w4_tree_attention_workspace_bytes=L.load().w4_tree_attention_workspace_bytes)
+    monkeypatch.setattr(L, "load", lambda: fake)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: getattr(t, "at", 0))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(L, "_raw_stream", lambda stream, device: 0)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)                          # noqa: E731
+    k = torch.zeros((4, 2, 16, 64), dtype=torch.float16)
+    c, b = bq.KVCache(k, k.clone()), bq.KVBatch(i32(1, 4), i32(1), i32(2), 1)
+    att, rules = bq.CachedAttention(c, 4, rope=bq.RopeTable(torch.zeros(8, 32, 2))), bq.LogitRules(64, i32(1, 8), i32(1), repetition=torch.ones(1))
+    q, ws, x = torch.zeros((1, 4, 64), dtype=torch.float16), torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros((1, 64))
+    def calls():                                                                # noqa: E306
+        att.append(torch.zeros(1, 8 * 64), b, q=q)
+        att.attend(q, b, y=q, workspace=ws)
+        rules(x, x)
+    calls()
+    assert [n for n, _ in seen] == ["w4_kv_append", "w4_tree_attention", "w4_logits_adjust"]
+    keep = []
+    for t, desc, field in ((c.k, c.desc, "k"), (c.v, c.desc, "v"), (b.desc._tensors[1], b.desc, "ctx"), (att.rope.turns, att.rope.desc, "turns"),
+                           (rules.desc._tensors[0], rules.desc, "ids")):
+        keep.append(t.data)
+        t.data = t.data.clone()
+        calls()
+        assert getattr(desc, field) == t.data_ptr()
+    n = len(seen)
+    for t, bad in ((c.k, k[:2].clone()), (c.v, torch.zeros_like(k, dtype=torch.bfloat16)), (b.desc._tensors[0], i32(2, 4)),
+                   (att.rope.turns, torch.zeros(8, 16, 2))):
+        old, t.data = t.data, bad
+        with pytest.raises(ValueError):
+            calls()
+        t.data = old
+    with pytest.raises(AttributeError):
+        c.k = k
+    assert all(name == "w4_kv_append" for name, _ in seen[n:]) or len(seen) == n
