@@ -7,10 +7,10 @@
 // A block takes a tile of 128 rows of one (sequence, key head) over 64 cached
 // tokens at a time:
 //   S = Q K^T   tcgen05.mma 128 x 64 x D: K in shared memory as TMA's 128-byte
-//               swizzle lays it, Q in tensor memory (heads of 256, for which that has no
-//               room, in shared memory: an MMA of 128 x 64 x 16 then takes 62 cycles,
-//               bound by reading Q), S in tensor memory (two buffers, so that
-//               the next product runs during the softmax);
+//               swizzle lays it, Q in tensor memory (heads of 256 with an fp32
+//               output, for which that has no room, in shared memory: an MMA of 128 x 64 x 16 then takes 62 cycles,
+//               bound by reading Q), S in tensor memory (the next product runs
+//               during the softmax, into a second buffer or, heads of 256, when the first is read);
 //   softmax     two threads per row (tensor-memory lane), 32 tokens each; they
 //               exchange their maxima.  The maximum in use is raised only when it
 //               is passed by more than 2^12: probabilities are then at most 4096
@@ -26,7 +26,7 @@
 // A tile of 128 rows by 64 tokens takes 1330 cycles, the softmax's time (maximum and exchange 400, exponentials 400, the way
 // from the scores' arrival to P's 1100 in all); its MMAs take 530, its bytes 1470 at the SM's share of the memory rate (bf16,
 // heads of 128).  An fp32 output takes 1850 (three parts).  16 drafts of 28 heads over 4096 bf16 places: 16.9 us, over 131071
-// 73; 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active).  INT8 with heads of 256: 3600 cycles a tile, of
+// 68; 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active).  INT8 with heads of 256: 3600 cycles a tile, of
 // which its bytes take 1470; one 16-bit tile fits beside Q, so widening waits for the products.
 #include "attn_tree.cuh"
 #include "gemm_w8.cuh"
@@ -42,17 +42,18 @@ template <int D, int CT, int kParts>
 struct Tc {
     static constexpr bool kI8 = CT == T_I8;
     static constexpr int kBoxes = D / 64;                     // 128-byte column groups of 16-bit values
-    static constexpr bool kQInT = D <= 128;                   // queries in tensor memory
+    static constexpr bool kQInT = D <= 128 || kParts < 3;     // queries in tensor memory
+    static constexpr int kSBufs = D == 256 && kQInT ? 1 : 2;  // places for the scores
     static constexpr int kQ = kQInT ? 0 : kTcRows * D * 2;
     static constexpr int kHalf = kTcUnit * D * 2;             // a tile's keys (or values) in 16 bits
     static constexpr int kRaw = kTcUnit * D;                  // the same in codes
-    static constexpr int kStages = kI8 ? (D == 64 ? 14 : D == 128 ? 7 : 2) : (D == 64 ? 10 : D == 128 ? 6 : 2);   // copies
-    static constexpr int kConv = kI8 ? (D == 256 ? 1 : 2) : kStages;   // 16-bit tiles
+    static constexpr int kStages = kI8 ? (D == 64 ? 14 : D == 128 ? 7 : 2) : (D == 64 ? 10 : D == 128 ? 6 : kQInT ? 3 : 2);   // copies
+    static constexpr int kConv = kI8 ? (D == 256 && !kQInT ? 1 : 2) : kStages;   // 16-bit tiles
     static constexpr int kMeta = kStages + kConv + 2;         // tiles between the order of a tile's keys and the end of its softmax, at most
     static constexpr int kThreads = kI8 ? 384 + 32 * (kConvWarps - 2) : 384;
-    static constexpr int kPBufs = kParts == 1 ? 3 : D == 256 ? (kParts == 2 ? 2 : 1) : (kParts == 2 ? 3 : 2);   // places for P
+    static constexpr int kPBufs = D == 256 ? (kParts == 1 ? 2 : 1) : kParts < 3 ? 3 : 2;              // places for P
     static constexpr int kCols = 512;
-    static constexpr int cS = D, cP = D + 2 * kTcUnit, cQ = cP + 192;   // tensor-memory columns of S, P and Q; O begins at 0
+    static constexpr int cS = D, cP = D + kSBufs * kTcUnit, cQ = D == 256 ? 384 : cP + 192;   // tensor-memory columns of S, P and Q; O begins at 0
     static_assert(!kQInT || cQ + D / 2 <= kCols, "tensor memory");
     static_assert(cP + kPBufs * 32 * kParts <= (kQInT ? cQ : kCols), "tensor memory");
     // shared memory
@@ -63,7 +64,7 @@ struct Tc {
     static constexpr int oMeta = oScale + (kI8 ? kMeta * 2 * kTcUnit * 4 : 0);   // [kMeta]: which sixteenths of a tile have a page
     static constexpr int oTop = (oMeta + kMeta * 4 + 7) / 8 * 8;       // [2][2][128]: numbers of a row's halves with their turn, even and odd
     static constexpr int oBars = oTop + 4 * kTcRows * 8;
-    static constexpr int nBars = 4 * kStages + 4 * kConv + 8;
+    static constexpr int nBars = 4 * kStages + 4 * kConv + 9;
     static constexpr int oMisc = oBars + nBars * 8;           // tensor memory's base, failure flag, odd values flag
     static constexpr int oWarpSum = oMisc + 16;
     static constexpr int oPre = oWarpSum + kThreads / 32 * 4;
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
     const uint32_t raw_full = bars, raw_empty = raw_full + 16 * S;                   // codes (INT8): keys, then values
     const uint32_t k_full = raw_empty + 16 * S, k_empty = k_full + 8 * NC;            // 16-bit keys
     const uint32_t v_full = k_empty + 8 * NC, v_empty = v_full + 8 * NC;             // and values
-    const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8;
+    const uint32_t s_full = v_empty + 8 * NC, p_full = s_full + 16, pv_done = p_full + 16, q_full = pv_done + 16, wg_bar = q_full + 8, s_empty = wg_bar + 8;
     uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::oMisc);
     volatile uint32_t* dead_s = misc + 1;
     volatile uint32_t* odd_s = misc + 2;
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
         }
         mbar_init(q_full, 8);
         mbar_init(wg_bar, 8);
+        mbar_init(s_empty, 8);
         fence_mbar_init();
         *dead_s = 0u;
         *odd_s = 0u;
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t k = k_desc + static_cast<uint64_t>((i % NC) * (2 * C::kHalf >> 4));
-                const uint32_t d = tb + C::cS + (i & 1) * kTcUnit;
+                const uint32_t d = tb + C::cS + (i % C::kSBufs) * kTcUnit;
 #pragma unroll
                 for (int x = 0; x < C::kBoxes; ++x) {
                     if constexpr (C::kQInT) mma_ts_rows_x4(d, tb + C::cQ + 32 * x, k + x * (kTcUnit * 128 >> 4), iqk, x > 0);
@@ -325,11 +327,42 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
             }
             __syncwarp();
         };
+        auto product = [&](int i) {             // O += P V of tile i, both of which are there
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t v = v_desc + static_cast<uint64_t>((i % NC) * (2 * C::kHalf >> 4));
+                const uint32_t p = tb + C::cP + (i % C::kPBufs) * 32 * kParts;
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) mma_ts_x4(tb, p + 32 * part, v, ipv);
+                tc_commit(v_empty + 8 * (i % NC));
+                tc_commit(pv_done + 8 * (i & 1));
+            }
+            __syncwarp();
+        };
         auto keys = [&](int i) { return warp_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u); };
         for (int begin = us; begin < ue && ok; ++pieces) {
             const Segment sg = find_segment(A, lay, begin, kTcRows, kTcUnit);
             const int end = min(sg.u0 + sg.units, ue), last = it + end - begin;
             ok = warp_wait(q_full, static_cast<uint32_t>(pieces) & 1u) && keys(it);
+            if constexpr (C::kSBufs == 1) {
+                // one place for scores: the next come when the softmax has read these
+                auto place = [&](int i) { return i == 0 || warp_wait(s_empty, static_cast<uint32_t>(i - 1) & 1u); };
+                ok = ok && place(it);
+                if (ok) scores(it);
+                for (; it < last && ok; ++it) {
+                    if (it + 1 < last) {
+                        ok = keys(it + 1) && place(it + 1);
+                        if (!ok) break;
+                        scores(it + 1);
+                    }
+                    ok = warp_wait(v_full + 8 * (it % NC), static_cast<uint32_t>(it / NC) & 1u) &&
+                         warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u);
+                    if (!ok) break;
+                    product(it);
+                }
+                begin = end;
+                continue;
+            }
             if (ok) scores(it);
             if (ok && it + 1 < last) {
                 ok = keys(it + 1);
@@ -344,19 +377,10 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 const int i = it + 2;
                 const bool more = i < last;
                 const bool early = more && __all_sync(0xffffffffu, mbar_test_wait(k_full + 8 * (i % NC), static_cast<uint32_t>(i / NC) & 1u));
-                const uint64_t v = v_desc + static_cast<uint64_t>((it % NC) * (2 * C::kHalf >> 4));
-                const uint32_t p = tb + C::cP + (it % C::kPBufs) * 32 * kParts;
                 ok = warp_wait(p_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u);
                 if (!ok) break;
                 if (early) scores(i);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int part = 0; part < kParts; ++part) mma_ts_x4(tb, p + 32 * part, v, ipv);
-                    tc_commit(v_empty + 8 * (it % NC));
-                    tc_commit(pv_done + 8 * (it & 1));
-                }
-                __syncwarp();
+                product(it);
                 if (more && !early) {
                     ok = keys(i);
                     if (ok) scores(i);
@@ -462,13 +486,18 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 float s[kHalfCols];
                 {
                     uint32_t r0[16], r1[16];
-                    const uint32_t a = tl + C::cS + (it & 1) * kTcUnit + kHalfCols * half;
+                    const uint32_t a = tl + C::cS + (it % C::kSBufs) * kTcUnit + kHalfCols * half;
                     tmem_ld16x2(a, r0, a + 16, r1);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         s[k] = __uint_as_float(r0[k]);
                         s[16 + k] = __uint_as_float(r1[k]);
                     }
+                }
+                if constexpr (C::kSBufs == 1) { // read: the next scores may come
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty);
                 }
                 const int t0 = (u - sg.u0) * kTcUnit;
                 const uint32_t there = meta_s[it % C::kMeta];
