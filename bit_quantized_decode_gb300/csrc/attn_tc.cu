@@ -26,8 +26,9 @@
 // A tile of 128 rows by 64 tokens takes 1330 cycles, the softmax's time (maximum and exchange 400, exponentials 400, the way
 // from the scores' arrival to P's 1100 in all); its MMAs take 530, its bytes 1470 at the SM's share of the memory rate (bf16,
 // heads of 128).  An fp32 output takes 1850 (three parts).  16 drafts of 28 heads over 4096 bf16 places: 16.9 us, over 131071
-// 68; 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active).  INT8 with heads of 256: 3600 cycles a tile, of
-// which its bytes take 1470; one 16-bit tile fits beside Q, so widening waits for the products.
+// 68; 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active). INT8 with heads of 256: 2700 cycles a
+// tile (its bytes take 1480): widening and the softmax share the issue slots; 5 drafts of 8 heads over 120001 places 38 us, over a
+// bf16 cache 39 (2600 cycles, its bytes 2940 at that rate).
 #include "attn_tree.cuh"
 #include "gemm_w8.cuh"
 
