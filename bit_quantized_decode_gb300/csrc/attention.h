@@ -79,6 +79,7 @@ struct AttnArgs {
     int* head;                // workspace: B + 1 prefix sums of units (more than 32 sequences)
     float* part;              // workspace: two partial results per block
     int part_rows;            // rows of one
+    float* kept;              // workspace of the tensor-core kernel: a block's rows of D
     unsigned* err;
 };
 __host__ __device__ inline size_t attn_head_bytes(int B) { return (4 * (static_cast<size_t>(B) + 1) + 127) / 128 * 128; }

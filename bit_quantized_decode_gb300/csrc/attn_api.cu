@@ -76,7 +76,7 @@ BatchView view(const w4_kv_batch* b) { return BatchView{b->table, b->ctx, b->q_s
 
 // Which kernel a call takes, and the rows of its partial results.  Up to 16 rows to a key head are one tile of the mma.sync
 // kernel; more would read the cache again for every 16, where the tcgen05 kernel takes 128.  28 query and 4 key heads of 128,
-// 3 drafts (21 rows): 65536 bf16 places 38.2 us on tcgen05, 45.6 on mma.sync; INT8 44.6 and 55.6; 30 streams of 400 to 4000
+// 3 drafts (21 rows): 65536 bf16 places 42 us on tcgen05, 45.6 on mma.sync; INT8 50 and 55.6; 30 streams of 400 to 4000
 // places 36.7 and 48.2; 4096 places 12.0 and 11.3.  8 query heads of 256 over one key head, 3 drafts (24 rows), 120001 INT8 places:
 // 42.8 and 65.2.
 struct AttnPlan {
@@ -97,7 +97,8 @@ AttnPlan plan_attention(const w4_kv_cache* c, const w4_kv_batch* b, int T, int G
 }
 size_t attention_workspace(const w4_kv_cache* c, const w4_kv_batch* b, const AttnPlan& p)
 {
-    return attn_head_bytes(b->B) + static_cast<size_t>(kAtMaxBlocks) * 2 * attn_part_floats(p.part_rows, c->D) * 4;
+    const size_t block = 2 * attn_part_floats(p.part_rows, c->D) + (p.tc ? static_cast<size_t>(p.part_rows) * c->D : 0);
+    return attn_head_bytes(b->B) + kAtMaxBlocks * block * 4;
 }
 
 }  // namespace
@@ -207,6 +208,7 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     a.head = static_cast<int*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_head_bytes(b->B));
     a.part_rows = p.part_rows;
+    a.kept = a.part + kAtMaxBlocks * 2 * attn_part_floats(p.part_rows, c->D);
     a.err = d.err;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
     const cudaError_t e = p.tc ? launch_attn_tc(a, q_type, d.sms, cs) : launch_attn_tree(a, q_type, d.sms, cs);

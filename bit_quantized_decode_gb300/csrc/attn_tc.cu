@@ -17,8 +17,11 @@
 //               (exact scaling, the sums stay in fp32), and the output, which
 //               lies in tensor memory, is rescaled a few times per segment
 //               instead of once per tile;
-//   O += P V    P goes back to tensor memory in 16 bits (in parts, as there) and is the A operand; V as it lies, 64 values of a token in a row,
-//               is an operand with its columns contiguous.
+//   O += P V    P goes back to tensor memory in 16 bits (in parts, as there)
+//               and is the A operand; V as it lies, 64 values of a token in a
+//               row, is an operand with its columns contiguous.  For an output
+//               of more parts O is taken out every 16 tiles and summed in fp32:
+//               see kFlush.
 // Warps: one orders copies, one issues MMAs, eight take the softmax; for an INT8
 // cache eight widen codes to 16 bits (exact) in shared memory.  All
 // are joined by mbarriers with bounded waits.
@@ -26,7 +29,7 @@
 // A tile of 128 rows by 64 tokens takes 1330 cycles, the softmax's time (maximum and exchange 400, exponentials 400, the way
 // from the scores' arrival to P's 1100 in all); its MMAs take 530, its bytes 1470 at the SM's share of the memory rate (bf16,
 // heads of 128).  An fp32 output takes 1850 (three parts).  16 drafts of 28 heads over 4096 bf16 places: 16.9 us, over 131071
-// 68; 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active). INT8 with heads of 256: 2700 cycles a
+// 73 (70 without kFlush); 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active). INT8 with heads of 256: 2700 cycles a
 // tile (its bytes take 1480): widening and the softmax share the issue slots; 5 drafts of 8 heads over 120001 places 38 us, over a
 // bf16 cache 39 (2600 cycles, its bytes 2940 at that rate).
 #include "attn_tree.cuh"
@@ -37,6 +40,10 @@ namespace {
 
 constexpr int kTcRows = kAtTcRows, kTcUnit = kAtTcUnit;
 constexpr int kConvWarps = 8;                   // warps 2, 3, 12 .. 17: four for keys, four for values
+// Tiles whose products add up in tensor memory, for an output of more parts: the error stops growing with the context.  Values that
+// are all positive, 25 to 100 tiles to a block: 0.9e-6 to 3.2e-6 off with 8, 1.4e-6 to 6.6e-6 with 16, 2.9e-6 to 13e-6 with 32.
+// 16 drafts over 131071 places: 78, 73, 72 us, 70 without; over 65536 48, 45, 43, 43, INT8 68, 56, 54, 54.
+constexpr int kFlush = 16;
 constexpr float kRaise = 12.0f;                 // log2 of what a probability may reach
 
 template <int D, int CT, int kParts>
@@ -480,7 +487,52 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 if (lane == 0) mbar_arrive(q_full);
             }
             float m = neg_inf(), l = 0.0f;
+            // The tensor cores cut a sum's low bits at every step, always towards zero.  Where the output has more parts the sum
+            // is taken out every 16 tiles and added in fp32 to what lies in the block's place in the workspace (column groups
+            // of four, the rows of one beside each other): the error stays below 192 steps' 2^-23 each, however long the
+            // context.
+            float* const part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
+            float4* const kept = reinterpret_cast<float4*>(A.kept + static_cast<size_t>(blockIdx.x) * A.part_rows * D) + (have ? row : 0);
+            float m_kept = neg_inf();           // the maximum in use for the kept sum
+            bool keeps = false;
+            auto kept_factor = [&]() { return m_kept == neg_inf() ? 0.0f : exp2_fast(m_kept - m); };
             for (int u = begin; u < end; ++u, ++it) {
+                if (kParts > 1 && u > begin && (u - begin) % kFlush == 0) {
+                    ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float f = kept_factor();
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        const int j = half * (D / 32) + k;
+                        uint32_t r[16];
+                        tmem_ld16(tl + 16 * j, r);
+                        if (have) {
+                            float4* d = kept + 4 * j * A.part_rows;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                                                       __uint_as_float(r[4 * e + 3]));
+                                if (keeps && f == 1.0f) {                // nothing to wait for (the thread's own place: one order)
+                                    atomicAdd(d + e * A.part_rows, v);
+                                    continue;
+                                }
+                                if (keeps) {
+                                    const float4 o = __ldcg(d + e * A.part_rows);
+                                    v = make_float4(v.x + f * o.x, v.y + f * o.y, v.z + f * o.z, v.w + f * o.w);
+                                }
+                                __stcg(d + e * A.part_rows, v);
+                            }
+                        }
+                        __syncwarp();
+                        const uint32_t zero[16] = {};
+                        tmem_st16(tl + 16 * j, zero);
+                    }
+                    tmem_wait_st();
+                    keeps = true;
+                    m_kept = m;
+                }
+
                 ok = warp_wait(s_full + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u);
                 if (!ok) break;
                 tc_fence_after();
@@ -690,12 +742,11 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
             tc_fence_after();
             // ------------------------------------------------- the row's result
             const bool whole = begin == sg.u0 && end == sg.u0 + sg.units;
-            float* part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
             if (have && !whole && half == 0) {
                 part[row] = m;
                 part[A.part_rows + row] = l;
             }
-            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f, f_kept = kept_factor();
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
                 const int j = half * (D / 32) + k;
@@ -704,7 +755,16 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 if (have) {
                 float v[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]) * inv;
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+                if (kParts > 1 && keeps) {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 o = __ldcg(kept + (4 * j + k / 4) * A.part_rows);
+                        v[k] += f_kept * o.x; v[k + 1] += f_kept * o.y; v[k + 2] += f_kept * o.z; v[k + 3] += f_kept * o.w;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] *= inv;
                 if (!whole || A.ytype == T_F32) {
                     float4* d = reinterpret_cast<float4*>(whole ? static_cast<float*>(A.y) + at + 16 * j
                                                                 : part + 2 * A.part_rows + static_cast<size_t>(row) * D + 16 * j);

@@ -121,6 +121,40 @@ def test_long_contexts(bq, n, Hq, Hkv, D, dtype):
     check_attention(bq, 5, [n], [131071], 64, Hq, Hkv, D, dtype, F32, masks)
 
 
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, F16), (128, I8), (256, BF16)])
+def test_long_sums_keep_their_precision(bq, D, dtype):
+    """Some hundred tiles to a block, fp32 outputs, against 64 bits on the GPU: what the tensor cores cut from a sum at each
+    step (2^-23 at most, 12 steps a tile) must not add up over more than the 16 tiles after which sums are taken out."""
+    Hkv, Hq, n, page = 16, 256, 2, 64
+    ctx = 60000 * 64 // D
+    lay = ref.Paged(3, [n], [ctx], page)
+    shape = (lay.pages, Hkv, page, D)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    if dtype == I8:
+        k, v = (torch.randint(-127, 128, shape, generator=g, dtype=torch.int8, device="cuda") for _ in range(2))
+        ks, vs = (torch.full(shape[:3], s, device="cuda") for s in (0.004, 0.03))
+    else:
+        k, v = ((s * torch.randn(shape, generator=g, device="cuda")).to(dtype) for s in (0.3, 1.0))
+        ks = vs = None
+    v = v.abs() if dtype != I8 else v.abs().clamp(max=127)      # all of one sign: sums that only grow
+    q = torch.randn((n, Hq, D), generator=g, device="cuda").to(F16 if dtype == F16 else BF16)
+    cache = bq.KVCache(k, v, ks, vs)
+    batch = bq.KVBatch(*[t.cuda() for t in lay.tensors()], max_tokens=n)
+    y = bq.CachedAttention(cache, Hq).attend(q, batch, y=torch.empty((n, Hq, D), device="cuda"))
+    table = torch.tensor(lay.table[0], device="cuda")
+    want = torch.empty((n, Hq, D), dtype=torch.float64, device="cuda")
+    for h in range(Hkv):
+        K, V = (t[table, h].reshape(-1, D).double()[: ctx + n] for t in (k, v))
+        if dtype == I8:
+            K, V = K * ks[0, 0, 0].double(), V * vs[0, 0, 0].double()
+        for i in range(n):
+            s = (q[i, 16 * h: 16 * h + 16].double() @ K[: ctx + i + 1].T) * D ** -0.5
+            want[i, 16 * h: 16 * h + 16] = torch.softmax(s, -1) @ V[: ctx + i + 1]
+    off = float((y.double() - want).norm() / want.norm())
+    # 16 tiles of 12 steps; scores and exponentials (2^-19 in all at these sizes); the parts of a probability (2^-17)
+    assert off <= 192 * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -17, off
+
+
 # ----------------------------------------------------------------- 32 bits
 @pytest.mark.parametrize("dtype,pages", [(I8, 70000), (BF16, 36000)])
 def test_caches_past_32_bit_offsets(bq, dtype, pages):
