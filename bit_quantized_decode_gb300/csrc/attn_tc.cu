@@ -250,6 +250,8 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 const int st = it % S;
                 const uint32_t ph = static_cast<uint32_t>(it / S - 1) & 1u;
                 if constexpr (kI8) {
+                    // The softmax reads both scales behind the scores, which wait for the keys alone: so the values' scales
+                    // come with the keys, too.
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t bar = raw_full + 8 * (half * S + st);
@@ -257,15 +259,18 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                         if (!ok) break;
                         if (lane == 0) {
                             if (half == 0) meta_s[it % C::kMeta] = sixteenths;
-                            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * per * (D + 4)));
+                            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n * per * (half ? D : D + 8)));
                         }
                         __syncwarp();
                         if (there) {
                             const size_t at = static_cast<size_t>(z) * A.c.page + y;
                             bulk_copy(smem_u32(smem + C::oRaw) + (2 * st + half) * C::kRaw + lane * per * D,
                                       static_cast<const uint8_t*>(half ? A.c.v : A.c.k) + at * D, per * D, bar);
-                            bulk_copy(smem_u32(scale_s + ((it % C::kMeta) * 2 + half) * kTcUnit + lane * per), (half ? A.c.vs : A.c.ks) + at, per * 4,
-                                      bar);
+                            if (half == 0) {
+                                const uint32_t to = smem_u32(scale_s + (it % C::kMeta) * 2 * kTcUnit + lane * per);
+                                bulk_copy(to, A.c.ks + at, per * 4, bar);
+                                bulk_copy(to + kTcUnit * 4, A.c.vs + at, per * 4, bar);
+                            }
                         }
                         __syncwarp();
                     }

@@ -1,0 +1,81 @@
+"""Attention over a paged cache against 64 bits with bounds that do not grow to percents over long contexts: scales that differ
+from tile to tile, probabilities far below the largest, sums of one sign."""
+import pytest
+import torch
+
+import attention_reference as ref
+from helpers import cuda_ok
+from test_gpu_attention import BF16, F16, F32, I8, half_unit, on_gpu
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not cuda_ok(), reason="needs a CUDA GPU")]
+
+
+@pytest.fixture(scope="module")
+def bq():
+    import bit_quantized_decode_gb300 as pkg
+    pkg._lib.load()
+    pkg._lib.clear_device_error()
+    yield pkg
+    assert pkg._lib.device_error() == 0
+
+
+def parts_unit(cache_dtype, y_dtype):
+    """Relative rounding of a probability: the square of its type's where it has two parts or more (fp32 outputs, and fp16
+    ones where it is bf16)."""
+    u = half_unit(F16 if cache_dtype == F16 else BF16)
+    return 2 * u * u if y_dtype == F32 or (y_dtype == F16 and cache_dtype != F16) else u
+
+
+def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit):
+    """Outputs in 64 bits and the bound of the kernels' error, on q's device.  The score's and the exponential's part is that of
+    attention_reference.attend.  The sums': a product's step on the tensor cores cuts 2^-23 of the sum at most, 192 of them
+    add up (12 a tile of 64 places, 16 tiles) before the sum is taken out; the sums in fp32 take a step of 2^-24 for every
+    16 places at most, and some 64 to join the parts.  Numerator and sum have them both."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    y, bound = torch.zeros_like(q), torch.zeros_like(q)
+    for b, (n, ctx) in enumerate(zip(lay.ns, lay.ctxs)):
+        page = torch.tensor(lay.table[b][: (ctx + n + lay.page - 1) // lay.page], device=q.device)
+        K, V = (t[page].transpose(0, 1).reshape(Hkv, -1, D)[:, : ctx + n] for t in (k, v))
+        for i in range(n):
+            t = lay.q_start[b] + i
+            see = torch.arange(ctx + n, device=q.device) < ctx
+            for j in range(n):
+                see[ctx + j] = bool(masks[t] >> j & 1)
+            qq, Ks, Vs = q[t].view(Hkv, -1, D), K[:, see], V[:, see]
+            s = scale * torch.einsum("hgd,hld->hgl", qq, Ks)
+            p = torch.softmax(s, -1)
+            y[t] = torch.einsum("hgl,hld->hgd", p, Vs).reshape(Hq, D)
+            mag = scale * torch.einsum("hgd,hld->hgl", qq.abs(), Ks.abs()).amax(-1, keepdim=True)
+            ds = mag * (D + 16) * 2.0 ** -23 + 3 * s.abs().amax(-1, keepdim=True) * 2.0 ** -22
+            e = 2 * ds + 2.0 ** -20 + 2 * (192 * 2.0 ** -23 + (Ks.shape[1] / 16 + 64) * 2.0 ** -24)
+            weight = torch.einsum("hgl,hld->hgd", p, Vs.abs())
+            bound[t] = (weight * (e + p_unit)).reshape(Hq, D) + y[t].abs() * (half_unit(y_dtype) + 2.0 ** -22)
+    return y, bound
+
+
+def check(bq, lay, tensors, k64, v64, q, masks, y_dtype):
+    cache, batch = on_gpu(bq, lay, tensors)
+    T, Hq, D = q.shape
+    att = bq.CachedAttention(cache, Hq, q_dtype=q.dtype)
+    y = att.attend(q.cuda(), batch, ref.as_int64(masks).cuda(), torch.empty((T, Hq, D), dtype=y_dtype, device="cuda"))
+    want, bound = attend_64(lay, q.cuda().double(), k64.cuda(), v64.cuda(), masks, att.scale, y_dtype,
+                            parts_unit(tensors[0].dtype, y_dtype))
+    err = (y.double() - want).abs()
+    assert bool((err <= bound + 1e-30).all()), f"error {float(err.max())}, {float((err / (bound + 1e-30)).max())} of the bound"
+
+
+@pytest.mark.parametrize("y_dtype", [F32, F16])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (40, 2, 64), (2, 1, 128), (28, 4, 128), (64, 2, 128), (2, 1, 256), (8, 1, 256), (32, 2, 256)])
+def test_int8_scales_that_differ_from_tile_to_tile(bq, Hq, Hkv, D, y_dtype):
+    """Every tile of 16 places has scales of its own, up to 32 times another's: the scales of another tile give percents."""
+    for ns, ctxs, page in (([5], [2900], 16), ([5, 2], [700, 61], 64), ([5] * 40, [130 + 16 * b for b in range(40)], 32)):
+        lay = ref.Paged(D + Hq, ns, ctxs, page)
+        g = torch.Generator().manual_seed(D + Hq)
+        shape = (lay.pages, Hkv, page, D)
+        k, v = (torch.randint(-127, 128, shape, generator=g, dtype=torch.int8) for _ in range(2))
+        power = torch.randint(0, 6, (2, lay.pages, Hkv, page // 16, 1), generator=g).expand(-1, -1, -1, -1, 16).reshape(2, *shape[:3])
+        ks, vs = 2.0 ** power * 0.002 * (0.5 + torch.rand((2, *shape[:3]), generator=g))
+        masks = [m for n in ns for m in [1, 3, 5, 13, 17][:n]]
+        q = (0.2 * torch.randn((lay.T, Hq, D), generator=g)).to(BF16)
+        check(bq, lay, (k, v, ks, vs), k.double() * ks.double()[..., None], v.double() * vs.double()[..., None], q, masks, y_dtype)
