@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
     const int rotated = A.Hq + A.c.Hkv;
     const bool turns = 8 * u < A.rot;           // (this lane's values of a query or key head)
     const int at0 = turns ? 4 * u : A.rot / 2 + 4 * u, at1 = at0 + (turns ? A.rot : D - A.rot) / 2;
-    const size_t row = static_cast<size_t>(t) * A.ld + (lane / kLanes) * D;
+    const size_t row0 = static_cast<size_t>(t) * A.ld, row = row0 + (lane / kLanes) * D;
     constexpr int kAhead = 2;                   // heads whose loads are in flight
     Raw4<XT> lo[kAhead], hi[kAhead];
     auto load = [&](int g) {
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kKaThreads) kv_append_kernel(const AppendArgs 
         for (int e = 0; e < kAhead; ++e) {
             const int head = (g + e) * kHeads + lane / kLanes;
             if (g + e < g1) {
-                const size_t base = head < H ? row + (g + e) * (kHeads * D) : row;
+                const size_t base = head < H ? row + (g + e) * (kHeads * D) : row0;   // (lanes without a head read the first one's)
                 const bool plain = head >= rotated;
                 lo[e].load(A.x, base + (plain ? 4 * u : at0));
                 hi[e].load(A.x, base + (plain ? D / 2 + 4 * u : at1));
