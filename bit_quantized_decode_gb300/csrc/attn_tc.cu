@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                         tmem_st16(tl + 16 * j, zero);
                     }
                     tmem_wait_st();
+                    tc_fence_before();          // (a tile with odd drafts: the row's other half reads these columns, behind wg_sync)
                     keeps = true;
                     m_kept = m;
                 }
@@ -613,6 +614,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                             tmem_st16(a, r);
                         }
                         tmem_wait_st();
+                        tc_fence_before();      // (as above)
                     }
                 }
                 const float base = m == neg_inf() ? 0.0f : -m;

@@ -54,7 +54,8 @@ def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit):
     return y, bound
 
 
-def check(bq, lay, tensors, k64, v64, q, masks, y_dtype):
+def check(bq, lay, tensors, k64, v64, q, masks, y_dtype, but=()):
+    """All rows but some against 64 bits; the outputs."""
     cache, batch = on_gpu(bq, lay, tensors)
     T, Hq, D = q.shape
     att = bq.CachedAttention(cache, Hq, q_dtype=q.dtype)
@@ -62,7 +63,9 @@ def check(bq, lay, tensors, k64, v64, q, masks, y_dtype):
     want, bound = attend_64(lay, q.cuda().double(), k64.cuda(), v64.cuda(), masks, att.scale, y_dtype,
                             parts_unit(tensors[0].dtype, y_dtype))
     err = (y.double() - want).abs()
+    err[list(but)] = 0.0
     assert bool((err <= bound + 1e-30).all()), f"error {float(err.max())}, {float((err / (bound + 1e-30)).max())} of the bound"
+    return y.cpu()
 
 
 @pytest.mark.parametrize("y_dtype", [F32, F16])
@@ -79,3 +82,28 @@ def test_int8_scales_that_differ_from_tile_to_tile(bq, Hq, Hkv, D, y_dtype):
         masks = [m for n in ns for m in [1, 3, 5, 13, 17][:n]]
         q = (0.2 * torch.randn((lay.T, Hq, D), generator=g)).to(BF16)
         check(bq, lay, (k, v, ks, vs), k.double() * ks.double()[..., None], v.double() * vs.double()[..., None], q, masks, y_dtype)
+
+
+@pytest.mark.parametrize("y_dtype", [F32, F16])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("B,ctx", [(1, 100), (3, 700), (160, 1030)])
+def test_hidden_infinities_in_a_tile_that_raises_the_maximum(bq, B, ctx, dtype, y_dtype):
+    """The tile of the drafts holds a key that all rows like 2^20 and more better than those before: the output so far is
+    rescaled (with 160 sequences, it is also taken out before, 16 tiles into a block), and an infinite draft that one row of
+    three sees is added by both halves of a row's threads."""
+    D, Hq, n, page = 64, 8, 3, 32
+    lay = ref.Paged(B, [n] * B, [ctx] * B, page)
+    g = torch.Generator().manual_seed(B)
+    like = torch.randn(D, generator=g)
+    like *= D ** 0.5 / like.norm()
+    q = (like + 0.1 * torch.randn((lay.T, Hq, D), generator=g)).to(dtype)
+    k, v = (torch.randn((lay.pages, 1, page, D), generator=g) for _ in range(2))
+    k *= 0.3
+    for b in range(B):
+        liked, hidden = ctx // 64 * 64, ctx + 1
+        k[lay.table[b][liked // page], 0, liked % page] = 2.5 * like
+        v[lay.table[b][hidden // page], 0, hidden % page] = float("inf")
+    k, v = k.to(dtype), v.to(dtype)
+    seeing = [lay.q_start[b] + 1 for b in range(B)]
+    y = check(bq, lay, (k, v, None, None), k.double(), v.double(), q, [1, 3, 5] * B, y_dtype, but=seeing)
+    assert not bool(torch.isfinite(y[seeing]).any())
