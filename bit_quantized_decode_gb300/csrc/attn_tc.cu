@@ -13,8 +13,8 @@
 //               during the softmax, into a second buffer or, heads of 256, when the first is read);
 //   softmax     two threads per row (tensor-memory lane), 32 tokens each; they
 //               exchange their maxima.  The maximum in use is raised only when it
-//               is passed by more than 2^12: probabilities are then at most 4096
-//               (exact scaling, the sums stay in fp32), and the output, which
+//               is passed by more than 2^12 (fp16 values: 2^6): probabilities are then at most
+//               4096 (exact scaling, the sums stay in fp32), and the output, which
 //               lies in tensor memory, is rescaled a few times per segment
 //               instead of once per tile;
 //   O += P V    P goes back to tensor memory in 16 bits (in parts, as there)
@@ -44,7 +44,6 @@ constexpr int kConvWarps = 8;                   // warps 2, 3, 12 .. 17: four fo
 // are all positive, 25 to 100 tiles to a block: 0.9e-6 to 3.2e-6 off with 8, 1.4e-6 to 6.6e-6 with 16, 2.9e-6 to 13e-6 with 32.
 // 16 drafts over 131071 places: 78, 73, 72 us, 70 without; over 65536 48, 45, 43, 43, INT8 68, 56, 54, 54.
 constexpr int kFlush = 16;
-constexpr float kRaise = 12.0f;                 // log2 of what a probability may reach
 
 template <int D, int CT, int kParts>
 struct Tc {
@@ -158,6 +157,11 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
     constexpr bool kI8 = C::kI8;
     constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
     constexpr int S = C::kStages, NC = C::kConv;
+    // log2 of what a probability may reach before the maximum in use is raised; in fp16 that is lost from the range below: a
+    // probability is off by 2^-34 of the row's largest.  (8 x 64 drafts over an fp16 cache, scores of 1.5 nats about their
+    // mean, fp32 outputs: 63.2 us with 2^12, 63.6 with 2^7, 65.3 with 2^6, 69.9 with 2^5, 74 with 2^4; fp16 outputs 52.2, 52.3,
+    // 52.4, 53.9 and 57.6)
+    constexpr float kRaise = PT == T_F16 ? 6.0f : 12.0f, kLift = prob_lift(PT, kRaise);
     extern __shared__ uint8_t raw_s[];
     uint8_t* smem = raw_s + ((1024u - (smem_u32(raw_s) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -617,7 +621,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                         tc_fence_before();      // (as above)
                     }
                 }
-                const float base = m == neg_inf() ? 0.0f : -m;
+                const float base = kLift - (m == neg_inf() ? 0.0f : m);
                 float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
                 for (int j = 0; j < kHalfCols; j += 2) {

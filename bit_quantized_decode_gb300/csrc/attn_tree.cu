@@ -20,7 +20,7 @@
 // Precision: products of 16-bit numbers in fp32 sums; probabilities enter the
 // second product in the values' 16-bit type, in as many parts (11 or 8 bits
 // each) as the output's type can tell: fp32 two of fp16 or three of bf16, fp16
-// two of bf16, else one.  INT8 codes are exact in 16 bits; a key's scale multiplies its
+// two of bf16, else one; fp16 ones times 2^15 (prob_lift).  INT8 codes are exact in 16 bits; a key's scale multiplies its
 // score, a value's scale its probability (bf16: no range of the scales is lost).
 //
 // One token over 131071 bf16 places (4 key heads of 128): 49 us, 5.5 TB/s; the stream itself runs at 7.1 TB/s for 38 us,
@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
     using C = At<D, CT>;
     constexpr int PT = CT == T_F16 ? T_F16 : T_BF16;          // type of the second product
     constexpr int W = C::kWarps;
+    constexpr float kLift = prob_lift(PT, 0.0f);
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                             o[j][2 * e + 1] *= f;
                         }
                     }
-                    const float base = m[e] == neg_inf() ? 0.0f : m[e];
+                    const float base = (m[e] == neg_inf() ? 0.0f : m[e]) - kLift;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll

@@ -248,6 +248,11 @@ __device__ __forceinline__ void i8_to_bf16(uint32_t c, uint32_t& h01, uint32_t& 
     h23 = *reinterpret_cast<const uint32_t*>(&y);
 }
 
+// Probabilities in fp16 are made so much larger that the largest is near 2^15, and so are their sums (the quotient is the
+// same): fp16's least step is 2^-24, and a long context's many small probabilities would vanish beside a large one while their
+// sum counts them.  log2 of that factor, where a probability reaches 2^raise.
+__host__ __device__ constexpr float prob_lift(int type, float raise) { return type == T_F16 ? 15.0f - raise : 0.0f; }
+
 constexpr uint64_t kAtWaitNs = 250ull * 1000ull * 1000ull;
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 

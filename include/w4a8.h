@@ -617,6 +617,7 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   Sums in fp32; a probability enters the second product in the 16-bit type
  *   of the values (bf16 for W4_I8): in one part where y is of no more bits, in
  *   two or three where y is W4_F32, in two where y is W4_F16 and it is bf16.
+ *   In fp16 it is off by 2^-34 of the row's largest besides (fp16's least step).
  *   workspace: w4_tree_attention_workspace_bytes(..) bytes, 16-byte aligned,
  *   with no contents to keep; calls that share one must not overlap on the
  *   GPU.  Two launches.  For given inputs the result is the same in every

@@ -26,11 +26,13 @@ def parts_unit(cache_dtype, y_dtype):
     return 2 * u * u if y_dtype == F32 or (y_dtype == F16 and cache_dtype != F16) else u
 
 
-def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit):
+def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit, half, exact):
     """Outputs in 64 bits and the bound of the kernels' error, on q's device.  The score's and the exponential's part is that of
     attention_reference.attend.  The sums': a product's step on the tensor cores cuts 2^-23 of the sum at most, 192 of them
     add up (12 a tile of 64 places, 16 tiles) before the sum is taken out; the sums in fp32 take a step of 2^-24 for every
-    16 places at most, and some 64 to join the parts.  Numerator and sum have them both."""
+    16 places at most, and some 64 to join the parts.  Numerator and sum have them both.  A probability in fp16 parts is
+    2^9 times as large as it stands to the largest, or more, and off by half of fp16's least step, 2^-25.  exact: the scores'
+    products and their sums are fp32 numbers."""
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     y, bound = torch.zeros_like(q), torch.zeros_like(q)
@@ -47,21 +49,24 @@ def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit):
             p = torch.softmax(s, -1)
             y[t] = torch.einsum("hgl,hld->hgd", p, Vs).reshape(Hq, D)
             mag = scale * torch.einsum("hgd,hld->hgl", qq.abs(), Ks.abs()).amax(-1, keepdim=True)
-            ds = mag * (D + 16) * 2.0 ** -23 + 3 * s.abs().amax(-1, keepdim=True) * 2.0 ** -22
+            ds = (0.0 if exact else mag * (D + 16) * 2.0 ** -23) + 3 * s.abs().amax(-1, keepdim=True) * 2.0 ** -22
             e = 2 * ds + 2.0 ** -20 + 2 * (192 * 2.0 ** -23 + (Ks.shape[1] / 16 + 64) * 2.0 ** -24)
             weight = torch.einsum("hgl,hld->hgd", p, Vs.abs())
-            bound[t] = (weight * (e + p_unit)).reshape(Hq, D) + y[t].abs() * (half_unit(y_dtype) + 2.0 ** -22)
+            least = 2.0 ** -34 * p.amax(-1, keepdim=True) * Vs.abs().sum(1)[:, None] if half else 0.0
+            bound[t] = (weight * (e + p_unit) + least).reshape(Hq, D) + y[t].abs() * (half_unit(y_dtype) + 2.0 ** -22)
+            if y_dtype == F16:                  # an output below 2^-14 has fp16's least step, 2^-24: off by half of it
+                bound[t] += 2.0 ** -25
     return y, bound
 
 
-def check(bq, lay, tensors, k64, v64, q, masks, y_dtype, but=()):
+def check(bq, lay, tensors, k64, v64, q, masks, y_dtype, but=(), exact=False):
     """All rows but some against 64 bits; the outputs."""
     cache, batch = on_gpu(bq, lay, tensors)
     T, Hq, D = q.shape
     att = bq.CachedAttention(cache, Hq, q_dtype=q.dtype)
     y = att.attend(q.cuda(), batch, ref.as_int64(masks).cuda(), torch.empty((T, Hq, D), dtype=y_dtype, device="cuda"))
     want, bound = attend_64(lay, q.cuda().double(), k64.cuda(), v64.cuda(), masks, att.scale, y_dtype,
-                            parts_unit(tensors[0].dtype, y_dtype))
+                            parts_unit(tensors[0].dtype, y_dtype), tensors[0].dtype == F16, exact)
     err = (y.double() - want).abs()
     err[list(but)] = 0.0
     assert bool((err <= bound + 1e-30).all()), f"error {float(err.max())}, {float((err / (bound + 1e-30)).max())} of the bound"
@@ -107,3 +112,26 @@ def test_hidden_infinities_in_a_tile_that_raises_the_maximum(bq, B, ctx, dtype, 
     seeing = [lay.q_start[b] + 1 for b in range(B)]
     y = check(bq, lay, (k, v, None, None), k.double(), v.double(), q, [1, 3, 5] * B, y_dtype, but=seeing)
     assert not bool(torch.isfinite(y[seeing]).any())
+
+
+@pytest.mark.parametrize("gap", [6, 10, 14, 18, 22])
+@pytest.mark.parametrize("y_dtype", [F32, F16])
+@pytest.mark.parametrize("Hq,D,n", [(4, 64, 1), (28, 128, 1), (28, 128, 5), (8, 256, 4)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_one_place_far_ahead_of_all_others(bq, dtype, Hq, D, n, y_dtype, gap):
+    """A place that is `gap` nats ahead and adds next to nothing (an attention sink), first, in the middle and last: what the
+    others add, each e^-gap of it, must not be lost in a probability's 16 bits.  Queries of ones, keys of one magnitude or
+    zero: exact scores."""
+    ctx, page, Hkv = 8190, 64, 1
+    for ahead in (0, 4000, ctx - 1):
+        lay = ref.Paged(gap, [n], [ctx], page)
+        g = torch.Generator().manual_seed(gap)
+        like = torch.ones(D)
+        like[torch.randperm(D, generator=g)[: D // 2]] = -1.0
+        k = torch.zeros((lay.pages, Hkv, page, D))
+        v = 1.0 + torch.rand((lay.pages, Hkv, page, D), generator=g)
+        at = lay.table[0][ahead // page], 0, ahead % page
+        k[at], v[at] = gap / D ** 0.5 * like, 0.0
+        q = like.expand(lay.T, Hq, D).to(dtype)
+        k, v = k.to(dtype), v.to(dtype)
+        check(bq, lay, (k, v, None, None), k.double(), v.double(), q, [(2 << i) - 1 for i in range(n)], y_dtype, exact=True)
