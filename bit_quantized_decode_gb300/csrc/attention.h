@@ -75,6 +75,7 @@ struct AttnArgs {
     int T, Hq, G;             // G = Hq / Hkv
     void* y;                  // [T][Hq][D] of ytype
     int ytype;
+    long long units;          // of work, at most (by the table's width)
     int blocks, least, extra; // of the first launch: blocks, units of one at least, units that a second piece is worth
     int* head;                // workspace: B + 1 prefix sums of units (more than 32 sequences)
     float* part;              // workspace: two partial results per block

@@ -208,6 +208,7 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     a.head = static_cast<int*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + attn_head_bytes(b->B));
     a.part_rows = p.part_rows;
+    a.units = p.units;
     a.kept = a.part + kAtMaxBlocks * 2 * attn_part_floats(p.part_rows, c->D);
     a.err = d.err;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);

@@ -19,9 +19,8 @@
 //               instead of once per tile;
 //   O += P V    P goes back to tensor memory in 16 bits (in parts, as there)
 //               and is the A operand; V as it lies, 64 values of a token in a
-//               row, is an operand with its columns contiguous.  For an output
-//               of more parts O is taken out every 16 tiles and summed in fp32:
-//               see kFlush.
+//               row, is an operand with its columns contiguous.  Over long
+//               contexts O is taken out now and then and summed in fp32: see kFlushParts.
 // Warps: one orders copies, one issues MMAs, eight take the softmax; for an INT8
 // cache eight widen codes to 16 bits (exact) in shared memory.  All
 // are joined by mbarriers with bounded waits.
@@ -29,7 +28,7 @@
 // A tile of 128 rows by 64 tokens takes 1330 cycles, the softmax's time (maximum and exchange 400, exponentials 400, the way
 // from the scores' arrival to P's 1100 in all); its MMAs take 530, its bytes 1470 at the SM's share of the memory rate (bf16,
 // heads of 128).  An fp32 output takes 1850 (three parts).  16 drafts of 28 heads over 4096 bf16 places: 16.9 us, over 131071
-// 73 (70 without kFlush); 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active). INT8 with heads of 256: 2700 cycles a
+// 73 (70 if sums stay in tensor memory); 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active). INT8 with heads of 256: 2700 cycles a
 // tile (its bytes take 1480): widening and the softmax share the issue slots; 5 drafts of 8 heads over 120001 places 38 us, over a
 // bf16 cache 39 (2600 cycles, its bytes 2940 at that rate).
 #include "attn_tree.cuh"
@@ -40,10 +39,16 @@ namespace {
 
 constexpr int kTcRows = kAtTcRows, kTcUnit = kAtTcUnit;
 constexpr int kConvWarps = 8;                   // warps 2, 3, 12 .. 17: four for keys, four for values
-// Tiles whose products add up in tensor memory, for an output of more parts: the error stops growing with the context.  Values that
-// are all positive, 25 to 100 tiles to a block: 0.9e-6 to 3.2e-6 off with 8, 1.4e-6 to 6.6e-6 with 16, 2.9e-6 to 13e-6 with 32.
+// Tiles whose products add up in tensor memory before the sum is taken out, so that the error stops growing with the context: the
+// tensor cores cut a sum's low bits at every step, always towards zero.  Values that are all positive, fp32 outputs (12 steps a
+// tile of three parts), 25 to 100 tiles to a block: 0.9e-6 to 3.2e-6 off with 8, 1.4e-6 to 6.6e-6 with 16, 2.9e-6 to 13e-6 with 32.
 // 16 drafts over 131071 places: 78, 73, 72 us, 70 without; over 65536 48, 45, 43, 43, INT8 68, 56, 54, 54.
-constexpr int kFlush = 16;
+constexpr int kFlushParts = 16;
+// One part (four steps a tile, 16-bit outputs): 0.4e-6 a tile.  2048 tiles to a block, 8.3e-4 (3.4 half steps of fp16); 1.0e-4
+// with 256, 0.2e-4 with 64.  16 drafts of 8 sequences over 131071 places, 431 tiles to a block, bf16: 322 us without, 328 with 256,
+// 347 with 64, INT8 420, 440, 486.  The code alone costs 8 x 64 drafts over 4096 places 52.5 -> 53.8, so calls in which
+// no block can have more than 256 tiles of a segment do without.
+constexpr int kFlushOne = 256;
 
 template <int D, int CT, int kParts>
 struct Tc {
@@ -150,7 +155,49 @@ __device__ __forceinline__ float2 tc_unpair(uint32_t u)
     else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-template <int D, int CT, int QT, int kParts>
+// A warp's half of the columns out of tensor memory, onto f times what the rows' place in the workspace holds (if it holds
+// something; row null: none).
+template <int D>
+__device__ __forceinline__ void take_out(uint32_t tl, int half, float4* row, int part_rows, bool holds, float f)
+{
+#pragma unroll 1
+    for (int k = 0; k < D / 32; ++k) {
+        const int j = half * (D / 32) + k;
+        uint32_t r[16];
+        tmem_ld16(tl + 16 * j, r);
+        if (row != nullptr) {
+            float4* d = row + 4 * j * part_rows;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                                       __uint_as_float(r[4 * e + 3]));
+                if (holds && f == 1.0f) {       // nothing to wait for (the thread's own place: one order)
+                    atomicAdd(d + e * part_rows, v);
+                    continue;
+                }
+                if (holds) {
+                    const float4 o = __ldcg(d + e * part_rows);
+                    v = make_float4(v.x + f * o.x, v.y + f * o.y, v.z + f * o.z, v.w + f * o.w);
+                }
+                __stcg(d + e * part_rows, v);
+            }
+        }
+        __syncwarp();
+        const uint32_t zero[16] = {};
+        tmem_st16(tl + 16 * j, zero);
+    }
+    tmem_wait_st();
+}
+
+// Out of line for the loop that comes here once in many tiles.
+template <int D>
+__device__ __noinline__ void take_out_seldom(uint32_t tl, int half, float4* row, int part_rows, bool holds, float f)
+{
+    take_out<D>(tl, half, row, part_rows, holds, f);
+}
+
+// kFlush: the tiles after which a sum is taken out, 0: never.
+template <int D, int CT, int QT, int kParts, int kFlush>
 __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnArgs A)
 {
     using C = Tc<D, CT, kParts>;
@@ -496,48 +543,21 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 if (lane == 0) mbar_arrive(q_full);
             }
             float m = neg_inf(), l = 0.0f;
-            // The tensor cores cut a sum's low bits at every step, always towards zero.  Where the output has more parts the sum
-            // is taken out every 16 tiles and added in fp32 to what lies in the block's place in the workspace (column groups
-            // of four, the rows of one beside each other): the error stays below 192 steps' 2^-23 each, however long the
-            // context.
+            // A sum that is taken out is added in fp32 to what lies in the block's place in the workspace (column groups of
+            // four, the rows of one beside each other): the error stays below 192 steps' 2^-23 each (1024 with one part),
+            // however long the context.
             float* const part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
             float4* const kept = reinterpret_cast<float4*>(A.kept + static_cast<size_t>(blockIdx.x) * A.part_rows * D) + (have ? row : 0);
             float m_kept = neg_inf();           // the maximum in use for the kept sum
             bool keeps = false;
             auto kept_factor = [&]() { return m_kept == neg_inf() ? 0.0f : exp2_fast(m_kept - m); };
             for (int u = begin; u < end; ++u, ++it) {
-                if (kParts > 1 && u > begin && (u - begin) % kFlush == 0) {
+                if (kFlush > 0 && u > begin && (u - begin) % (kFlush > 0 ? kFlush : 1) == 0) {
                     ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    const float f = kept_factor();
-#pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
-                        const int j = half * (D / 32) + k;
-                        uint32_t r[16];
-                        tmem_ld16(tl + 16 * j, r);
-                        if (have) {
-                            float4* d = kept + 4 * j * A.part_rows;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float4 v = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
-                                                       __uint_as_float(r[4 * e + 3]));
-                                if (keeps && f == 1.0f) {                // nothing to wait for (the thread's own place: one order)
-                                    atomicAdd(d + e * A.part_rows, v);
-                                    continue;
-                                }
-                                if (keeps) {
-                                    const float4 o = __ldcg(d + e * A.part_rows);
-                                    v = make_float4(v.x + f * o.x, v.y + f * o.y, v.z + f * o.z, v.w + f * o.w);
-                                }
-                                __stcg(d + e * A.part_rows, v);
-                            }
-                        }
-                        __syncwarp();
-                        const uint32_t zero[16] = {};
-                        tmem_st16(tl + 16 * j, zero);
-                    }
-                    tmem_wait_st();
+                    if constexpr (kParts > 1) take_out<D>(tl, half, have ? kept : nullptr, A.part_rows, keeps, kept_factor());
+                    else take_out_seldom<D>(tl, half, have ? kept : nullptr, A.part_rows, keeps, kept_factor());
                     tc_fence_before();          // (a tile with odd drafts: the row's other half reads these columns, behind wg_sync)
                     keeps = true;
                     m_kept = m;
@@ -767,7 +787,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 float v[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
-                if (kParts > 1 && keeps) {
+                if (kFlush > 0 && keeps) {
 #pragma unroll
                     for (int k = 0; k < 16; k += 4) {
                         const float4 o = __ldcg(kept + (4 * j + k / 4) * A.part_rows);
@@ -848,11 +868,14 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
     if (warp == 1) tmem_dealloc(tb, C::kCols);
 }
 
-template <int D, int CT, int QT, int kParts>
+constexpr int kExtra = 6;                       // (4 us at 0.7 us a unit)
+int blocks_of(int sms) { return sms < kAtMaxBlocks ? sms : kAtMaxBlocks; }
+
+template <int D, int CT, int QT, int kParts, int kFlush = kFlushParts>
 cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 {
     using C = Tc<D, CT, kParts>;
-    auto kern = attn_tc_kernel<D, CT, QT, kParts>;
+    auto kern = attn_tc_kernel<D, CT, QT, kParts, kFlush>;
     static SmemLimit limit;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, C::smem(kAtMaxSeq));
     if constexpr (CT != T_I8) {
@@ -861,8 +884,8 @@ cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
         if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, 128, rows);
     }
     if (e != cudaSuccess) return e;
-    a.blocks = sms < kAtMaxBlocks ? sms : kAtMaxBlocks;
-    a.extra = 6;                                // (4 us at 0.7 us a unit)
+    a.blocks = blocks_of(sms);
+    a.extra = kExtra;
     a.least = 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -880,9 +903,13 @@ cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 template <int D, int CT, int QT>
 cudaError_t launch_w(AttnArgs& a, int sms, cudaStream_t s)
 {
-    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, sms, s) : launch<D, CT, QT, 1>(a, sms, s);
-    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, sms, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, sms, s)
-                                                                                       : launch<D, CT, QT, 1>(a, sms, s);
+    constexpr int f16_parts = CT == T_F16 ? 1 : 2;
+    if (a.ytype == T_F32) return launch<D, CT, QT, f16_parts + 1>(a, sms, s);
+    if (f16_parts > 1 && a.ytype == T_F16) return launch<D, CT, QT, 2>(a, sms, s);
+    // tiles of a segment, and of a block in equal shares (segments with blocks of their own: kExtra more), at most
+    const long long segment = (static_cast<long long>(a.b.max_pages) * a.c.page + kTcUnit - 1) / kTcUnit;
+    const long long share = a.units / blocks_of(sms) + 1 + kExtra;
+    return (segment < share ? segment : share) > kFlushOne ? launch<D, CT, QT, 1, kFlushOne>(a, sms, s) : launch<D, CT, QT, 1, 0>(a, sms, s);
 }
 
 template <int D>

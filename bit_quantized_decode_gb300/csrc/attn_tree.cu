@@ -391,7 +391,9 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                             y -= r.y;
                         }
                     }
-                // (the tensor cores cut a sum's low bits: in 32 bits an output's steps over the units are added here)
+                // The tensor cores cut a sum's low bits at every step: for an output of more parts the units are added here.
+                // (One part: 1024 steps over 131071 places of one warp's eighth, 1.0e-4 off if all values are positive, 0.4 half
+                // steps of fp16; added here, 64 streams of D 64, 128, 256 71.1, 102.8, 113.8 -> 72.8, 103.5, 118.9 us.)
                 auto pv = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
                     if constexpr (kParts > 1) {
                         float d[4] = {};

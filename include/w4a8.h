@@ -614,7 +614,9 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   does not reach it, infinities and NaN included.  q [T][Hq][D] of the
  *   cache's type (either 16-bit type for W4_I8), y [T][Hq][D] of y_type, both
  *   16-byte aligned; query head h reads key head h / (Hq / Hkv).
- *   Sums in fp32; a probability enters the second product in the 16-bit type
+ *   Sums in fp32, of which the tensor cores cut up to 2^-23 a step: 192 steps
+ *   at most where y has more bits than a part of a probability, else 1024 (up
+ *   to 16 rows to a key head: one for every 64 or 128 places).  A probability enters the second product in the 16-bit type
  *   of the values (bf16 for W4_I8): in one part where y is of no more bits, in
  *   two or three where y is W4_F32, in two where y is W4_F16 and it is bf16.
  *   In fp16 it is off by 2^-34 of the row's largest besides (fp16's least step).

@@ -29,7 +29,8 @@ def parts_unit(cache_dtype, y_dtype):
 def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit, half, exact):
     """Outputs in 64 bits and the bound of the kernels' error, on q's device.  The score's and the exponential's part is that of
     attention_reference.attend.  The sums': a product's step on the tensor cores cuts 2^-23 of the sum at most, 192 of them
-    add up (12 a tile of 64 places, 16 tiles) before the sum is taken out; the sums in fp32 take a step of 2^-24 for every
+    add up (12 a tile of 64 places, 16 tiles) before the sum is taken out, or 1024 where probabilities have one part (4 a tile,
+    256 tiles; few rows: every fourth 16 places); the sums in fp32 take a step of 2^-24 for every
     16 places at most, and some 64 to join the parts.  Numerator and sum have them both.  A probability in fp16 parts is
     2^9 times as large as it stands to the largest, or more, and off by half of fp16's least step, 2^-25.  exact: the scores'
     products and their sums are fp32 numbers."""
@@ -50,7 +51,8 @@ def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit, half, exact):
             y[t] = torch.einsum("hgl,hld->hgd", p, Vs).reshape(Hq, D)
             mag = scale * torch.einsum("hgd,hld->hgl", qq.abs(), Ks.abs()).amax(-1, keepdim=True)
             ds = (0.0 if exact else mag * (D + 16) * 2.0 ** -23) + 3 * s.abs().amax(-1, keepdim=True) * 2.0 ** -22
-            e = 2 * ds + 2.0 ** -20 + 2 * (192 * 2.0 ** -23 + (Ks.shape[1] / 16 + 64) * 2.0 ** -24)
+            cuts = 192 if p_unit < 2.0 ** -15 else max(1024, Ks.shape[1] / 64)
+            e = 2 * ds + 2.0 ** -20 + 2 * (cuts * 2.0 ** -23 + (Ks.shape[1] / 16 + 64) * 2.0 ** -24)
             weight = torch.einsum("hgl,hld->hgd", p, Vs.abs())
             least = 2.0 ** -34 * p.amax(-1, keepdim=True) * Vs.abs().sum(1)[:, None] if half else 0.0
             bound[t] = (weight * (e + p_unit) + least).reshape(Hq, D) + y[t].abs() * (half_unit(y_dtype) + 2.0 ** -22)
@@ -135,3 +137,75 @@ def test_one_place_far_ahead_of_all_others(bq, dtype, Hq, D, n, y_dtype, gap):
         q = like.expand(lay.T, Hq, D).to(dtype)
         k, v = k.to(dtype), v.to(dtype)
         check(bq, lay, (k, v, None, None), k.double(), v.double(), q, [(2 << i) - 1 for i in range(n)], y_dtype, exact=True)
+
+
+# ------------------------------- long sums for 16-bit outputs (probabilities of one part)
+def on_gpu_only(bq, B, n, ctx, Hkv, D, dtype, seed, grow=False, sign=False):
+    """A cache made on the GPU: its parts, their numbers in 64 bits are the caller's."""
+    page = 64
+    lay = ref.Paged(seed, [n] * B, [ctx] * B, page)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shape = (lay.pages, Hkv, page, D)
+    kind = F16 if dtype == F16 else BF16
+    if dtype == I8:
+        k, v = (torch.randint(-127, 128, shape, generator=g, dtype=torch.int8, device="cuda") for _ in range(2))
+        scales = [0.004 * (0.5 + torch.rand(shape[:3], generator=g, device="cuda")) for _ in range(2)]
+    else:
+        k, v = (torch.empty(shape, dtype=dtype, device="cuda").normal_(generator=g) for _ in range(2))
+        k *= 0.3
+        scales = [None, None]
+    if sign:
+        v.abs_()
+    if grow:                                    # keys (their scales) that grow with the place
+        table = torch.tensor(lay.table, device="cuda").clamp(min=0).flatten()
+        by = torch.zeros(lay.pages, device="cuda")
+        by[table] = 0.02 + 3.0 * torch.arange(len(lay.table[0]), device="cuda").repeat(B) / len(lay.table[0])
+        if dtype == I8:
+            scales[0] *= by[:, None, None]
+        else:
+            k *= by[:, None, None, None].to(dtype)
+    batch = bq.KVBatch(*[t.cuda() for t in lay.tensors()], max_tokens=n)
+    q = lambda Hq: torch.randn((lay.T, Hq, D), generator=g, device="cuda").to(kind)          # noqa: E731
+    return lay, bq.KVCache(k, v, *scales), batch, q
+
+
+@pytest.mark.parametrize("G,n", [(16, 2), (8, 1)])
+def test_long_sums_of_one_sign_stay_centred(bq, G, n):
+    """131071 places to a block, values that are all positive, fp16 outputs: what the tensor cores cut from the sums is 1024
+    steps of 2^-23 at most, however long the context (few rows: 16 places a step, eight warps: 1024 steps, too).  The mean over
+    many outputs, which their rounding leaves alone: it is 2^-12 / sqrt(3) / sqrt(count) off, taken six times."""
+    B, ctx, Hkv, D = 19, 131071, 8, 64
+    lay, cache, batch, make_q = on_gpu_only(bq, B, n, ctx, Hkv, D, F16, 3, sign=True)
+    q = make_q(G * Hkv)
+    y = bq.CachedAttention(cache, G * Hkv).attend(q, batch)
+    off = []
+    for b in (0, 7, 18):
+        table = torch.tensor(lay.table[b], device="cuda")
+        for h in range(0, Hkv, 2):
+            K, V = (t[table, h].reshape(-1, D).double()[: ctx + n] for t in (cache.k, cache.v))
+            for i in range(n):
+                t, rows = lay.q_start[b] + i, slice(G * h, G * h + G)
+                s = (q[t, rows].double() @ K[: ctx + i + 1].T) * D ** -0.5
+                off.append((y[t, rows].double() / (torch.softmax(s, -1) @ V[: ctx + i + 1]) - 1).flatten())
+    off = torch.cat(off)
+    assert abs(float(off.mean())) <= 1024 * 2.0 ** -23 + 2.0 ** -19 + 6 * 2.0 ** -12 / 3 ** 0.5 / off.numel() ** 0.5, float(off.mean())
+
+
+@pytest.mark.parametrize("D,dtype,y_dtype", [(64, F16, F16), (64, BF16, BF16), (128, F16, F16), (128, I8, BF16), (256, F16, F16), (256, I8, BF16)])
+def test_sums_taken_out_late(bq, D, dtype, y_dtype):
+    """313 tiles to a block, one part: the sum is taken out once, at another maximum than in the end."""
+    B, ctx, Hkv, n, Hq = 38, 20000, 4, 2, 64
+    lay, cache, batch, make_q = on_gpu_only(bq, B, n, ctx, Hkv, D, dtype, D, grow=True)
+    q = make_q(Hq)
+    att = bq.CachedAttention(cache, Hq)
+    y = att.attend(q, batch, y=torch.empty(q.shape, dtype=y_dtype, device="cuda"))
+    for b in (0, 20, 37):
+        one = ref.Paged(0, [n], [ctx], 64)
+        one.table = [list(range(len(lay.table[b])))]
+        table = torch.tensor(lay.table[b], device="cuda")
+        k, v = (t[table].double() * (1.0 if s is None else s[table].double()[..., None])
+                for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+        rows = slice(lay.q_start[b], lay.q_start[b] + n)
+        want, bound = attend_64(one, q[rows].double(), k, v, [1, 3], att.scale, y_dtype, parts_unit(dtype, y_dtype), dtype == F16, False)
+        err = (y[rows].double() - want).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
