@@ -73,7 +73,7 @@ struct Tc {
     static constexpr int oKv = kQ;                            // [kConv] keys, values
     static constexpr int oRaw = oKv + kConv * 2 * kHalf;
     static constexpr int oScale = oRaw + (kI8 ? kStages * 2 * kRaw : 0);    // [kMeta][2][64]
-    static constexpr int oMeta = oScale + (kI8 ? kMeta * 2 * kTcUnit * 4 : 0);   // [kMeta]: which sixteenths of a tile have a page
+    static constexpr int oMeta = oScale + (kI8 ? kMeta * 2 * kTcUnit * 4 : 0);   // [kMeta]: which sixteenths of a tile have a page; 16: a vast scale
     static constexpr int oTop = (oMeta + kMeta * 4 + 7) / 8 * 8;       // [2][2][128]: numbers of a row's halves with their turn, even and odd
     static constexpr int oBars = oTop + 4 * kTcRows * 8;
     static constexpr int nBars = 4 * kStages + 4 * kConv + 9;
@@ -135,24 +135,6 @@ __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a, uint64_t b, ui
         "add.u32 a1, %1, 24;\n\tadd.u64 b1, %2, 384;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc)
         : "memory");
-}
-
-template <int T>
-__device__ __forceinline__ uint32_t tc_pair(float a, float b)
-{
-    if constexpr (T == T_F16) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-template <int T>
-__device__ __forceinline__ float2 tc_unpair(uint32_t u)
-{
-    if constexpr (T == T_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
-    else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
 // A warp's half of the columns out of tensor memory, onto f times what the rows' place in the workspace holds (if it holds
@@ -712,7 +694,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                                         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                                         for (int i = 0; i < 4; ++i) {
-                                            const float2 f = tc_unpair<CT>(x[i]);
+                                            const float2 f = unpair16<CT>(x[i]);
                                             r[8 * h + 2 * i] = __float_as_uint(__uint_as_float(r[8 * h + 2 * i]) + s[j] * f.x);
                                             r[8 * h + 2 * i + 1] = __float_as_uint(__uint_as_float(r[8 * h + 2 * i + 1]) + s[j] * f.y);
                                         }
@@ -747,17 +729,25 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 for (int part = 0; part < kParts; ++part) {
                     uint32_t w[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        w[k] = tc_pair<PT>(s[2 * k], s[2 * k + 1]);
-                        if (part + 1 < kParts) {
-                            const float2 f = tc_unpair<PT>(w[k]);
-                            s[2 * k] -= f.x;
-                            s[2 * k + 1] -= f.y;
-                        }
-                    }
+                    for (int k = 0; k < 16; ++k) w[k] = part16<PT, kI8>(s[2 * k], s[2 * k + 1], part + 1 == kParts);
                     tmem_st16(p + 32 * part + 16 * half, w);
                 }
                 tmem_wait_st();
+                if constexpr (kI8 && kParts > 1) {
+                    if (there > 15u) {          // a scale of this tile is vast
+                        const uint32_t vasts =  // of this half's tokens
+                            __ballot_sync(0xffffffffu, vast(scale_s[(it % C::kMeta) * 2 * kTcUnit + kTcUnit + kHalfCols * half + lane]));
+#pragma unroll 1
+                        for (int part = 1; part < kParts; ++part) {
+                            uint32_t w[16];
+                            tmem_ld16(p + 32 * part + 16 * half, w);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) w[k] = only_first(w[k], vasts >> (2 * k) & 1u, vasts >> (2 * k + 1) & 1u);
+                            tmem_st16(p + 32 * part + 16 * half, w);
+                        }
+                        tmem_wait_st();
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * (it & 1));
@@ -805,7 +795,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                     uint32_t w[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        w[k] = A.ytype == T_F16 ? tc_pair<T_F16>(v[2 * k], v[2 * k + 1]) : tc_pair<T_BF16>(v[2 * k], v[2 * k + 1]);
+                        w[k] = A.ytype == T_F16 ? pair16<T_F16>(v[2 * k], v[2 * k + 1]) : pair16<T_BF16>(v[2 * k], v[2 * k + 1]);
                     uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.y) + at + 16 * j);
                     d[0] = make_uint4(w[0], w[1], w[2], w[3]);
                     d[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -829,6 +819,11 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
             ok = warp_wait(full + 8 * st, static_cast<uint32_t>(it / S) & 1u);
             if (it >= NC) ok = ok && warp_wait(to_empty + 8 * cv, static_cast<uint32_t>(it / NC - 1) & 1u);
             if (!ok) break;
+            if (kParts > 1 && cw == 0) {        // (a value's scale that the softmax has to know of)
+                const float* vs = scale_s + (it % C::kMeta) * 2 * kTcUnit + kTcUnit;
+                if (__any_sync(0xffffffffu, vast(vs[lane]) || vast(vs[32 + lane])) && lane == 0) meta_s[it % C::kMeta] |= 16u;
+                __syncwarp();
+            }
             const uint8_t* src = smem + C::oRaw + (2 * st + half) * C::kRaw;
             uint8_t* dst = smem + C::oKv + (2 * cv + half) * C::kHalf;
             constexpr int kStep = 16 * kConvWarps, kTimes = kTcUnit * D / 16 / kStep;

@@ -108,25 +108,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two fp32 as a pair of 16-bit numbers (the first in the low half).
-template <int T>
-__device__ __forceinline__ uint32_t pair16(float a, float b)
-{
-    if constexpr (T == T_F16) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-template <int T>
-__device__ __forceinline__ float2 unpair16(uint32_t u)
-{
-    if constexpr (T == T_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
-    else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-
 template <int T>
 __device__ __forceinline__ void codes16(uint32_t c, uint32_t& h01, uint32_t& h23)
 {
@@ -384,13 +365,15 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                     for (int e = 0; e < 2; ++e) {
                         float x = s[h][2 * e], y = s[h][2 * e + 1];
 #pragma unroll
-                        for (int k = 0; k < kParts; ++k) {
-                            pa[k][2 * h + e] = pair16<PT>(x, y);
-                            const float2 r = unpair16<PT>(pa[k][2 * h + e]);
-                            x -= r.x;
-                            y -= r.y;
-                        }
+                        for (int k = 0; k < kParts; ++k) pa[k][2 * h + e] = part16<PT, CT == T_I8>(x, y, k + 1 == kParts);
                     }
+                if constexpr (CT == T_I8 && kParts > 1) {
+                    if (__any_sync(0xffffffffu, vast(vsc[0]) || vast(vsc[1]) || vast(vsc[2]) || vast(vsc[3])))
+#pragma unroll
+                        for (int k = 1; k < kParts; ++k)
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) pa[k][w] = only_first(pa[k][w], vast(vsc[w & 2]), vast(vsc[(w & 2) + 1]));
+                }
                 // The tensor cores cut a sum's low bits at every step: for an output of more parts the units are added here.
                 // (One part: 1024 steps over 131071 places of one warp's eighth, 1.0e-4 off if all values are positive, 0.4 half
                 // steps of fp16; added here, 64 streams of D 64, 128, 256 71.1, 102.8, 113.8 -> 72.8, 103.5, 118.9 us.)

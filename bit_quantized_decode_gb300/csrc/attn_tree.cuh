@@ -253,6 +253,65 @@ __device__ __forceinline__ void i8_to_bf16(uint32_t c, uint32_t& h01, uint32_t& 
 // sum counts them.  log2 of that factor, where a probability reaches 2^raise.
 __host__ __device__ constexpr float prob_lift(int type, float raise) { return type == T_F16 ? 15.0f - raise : 0.0f; }
 
+// Two fp32 as a pair of 16-bit numbers (the first in the low half), to nearest or towards zero, and back.
+template <int T>
+__device__ __forceinline__ uint32_t pair16(float a, float b)
+{
+    if constexpr (T == T_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <int T>
+__device__ __forceinline__ uint32_t pair16_cut(float a, float b)
+{
+    uint32_t r;
+    if constexpr (T == T_F16) asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+template <int T>
+__device__ __forceinline__ float2 unpair16(uint32_t u)
+{
+    if constexpr (T == T_F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+    else return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// One 16-bit part of two probabilities, which become what is left of them; the last part is rounded.
+//
+// A value that a row sees may be infinite, and then every part times it has to be that infinity: a part that is 0 or of the
+// other sign would make it a NaN.  So parts are cut towards zero and what is left counts a step of the last part more than it
+// is (2^-23 of the probability, fp16 2^-21): it has the probability's sign and is not 0 (down to 2^-87; fp16, whose least step
+// is 2^-24, to 2^-13 of the largest and on the mma.sync kernel 2^-19).  An INT8 cache's codes are finite: its parts are
+// rounded, and where a value's scale, which the probability has taken in, makes that infinite, the first part has it all
+// (only_first).
+template <int T, bool kCodes>
+__device__ __forceinline__ uint32_t part16(float& x, float& y, bool last)
+{
+    if (kCodes || last) {
+        const uint32_t w = pair16<T>(x, y);
+        const float2 r = unpair16<T>(w);
+        x -= r.x;
+        y -= r.y;
+        return w;
+    }
+    constexpr float more = T == T_F16 ? 1.0f + 1.0f / (1 << 21) : 1.0f + 1.0f / (1 << 23);
+    const uint32_t w = pair16_cut<T>(x, y);
+    const float2 r = unpair16<T>(w);
+    x = __fmaf_rn(x, more, -r.x);
+    y = __fmaf_rn(y, more, -r.y);
+    return w;
+}
+// Scales from which a probability's product with them may pass fp32: one in a tile is looked for, not one in each product.
+__device__ __forceinline__ bool vast(float scale) { return fabsf(scale) >= 1.2676506e30f; }      // 2^100
+__device__ __forceinline__ uint32_t only_first(uint32_t w, bool first, bool second)
+{
+    return (first ? 0u : w & 0xffffu) | (second ? 0u : w & 0xffff0000u);
+}
+
 constexpr uint64_t kAtWaitNs = 250ull * 1000ull * 1000ull;
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 

@@ -209,3 +209,50 @@ def test_sums_taken_out_late(bq, D, dtype, y_dtype):
         want, bound = attend_64(one, q[rows].double(), k, v, [1, 3], att.scale, y_dtype, parts_unit(dtype, y_dtype), dtype == F16, False)
         err = (y[rows].double() - want).abs()
         assert bool((err <= bound).all()), float((err / bound).max())
+
+
+# -------------------------------------------------------- infinities that are seen
+@pytest.mark.parametrize("y_dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,D,n,B,ctx", [(4, 64, 1, 1, 300), (28, 128, 1, 2, 1000), (28, 128, 2, 1, 300), (8, 256, 4, 1, 700), (32, 64, 2, 160, 1500)])
+def test_infinite_values_give_infinities(bq, Hq, D, n, B, ctx, dtype, y_dtype):
+    """A cached place has infinities in ten columns and those of the other sign in ten others: so have all rows, and their other
+    columns are what they are without.  (160 sequences: 24 tiles to a block, so sums are taken out.)"""
+    page = 32
+    lay = ref.Paged(5, [n] * B, [ctx] * B, page)
+    g = torch.Generator().manual_seed(D)
+    k, v = (torch.randn((lay.pages, 1, page, D), generator=g).to(dtype) for _ in range(2))
+    q = (0.3 * torch.randn((lay.T, Hq, D), generator=g)).to(dtype)
+    for b in range(B):
+        p = (7 + 64 * b) % ctx
+        at = lay.table[b][p // page], 0, p % page
+        v[at][:10], v[at][10:20] = float("inf"), float("-inf")
+    cache, batch = on_gpu(bq, lay, (k, v, None, None))
+    y = bq.CachedAttention(cache, Hq).attend(q.cuda(), batch, y=torch.empty((lay.T, Hq, D), dtype=y_dtype, device="cuda"))
+    assert bool((y[..., :10] == float("inf")).all()) and bool((y[..., 10:20] == float("-inf")).all())
+    masks = [(2 << i) - 1 for i in range(n)] * B
+    want, bound = attend_64(lay, q.cuda().double(), k.cuda().double(), v.cuda().double().nan_to_num(0, 0, 0), masks, D ** -0.5, y_dtype,
+                            parts_unit(dtype, y_dtype), dtype == F16, False)
+    err = (y.double() - want).abs()[..., 20:]
+    assert bool((err <= bound[..., 20:]).all()), float((err / bound[..., 20:]).max())
+
+
+@pytest.mark.parametrize("y_dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("Hq,D,n", [(4, 64, 1), (28, 128, 2), (8, 256, 1), (8, 256, 4)])
+def test_an_infinite_scale_gives_infinities(bq, Hq, D, n, y_dtype):
+    """An INT8 cache's value scale: the codes' signs decide, and a code of 0 times infinity is not a number."""
+    lay = ref.Paged(5, [n], [300], 32)
+    g = torch.Generator().manual_seed(D)
+    shape = (lay.pages, 1, 32, D)
+    k, v = (torch.randint(-127, 128, shape, generator=g, dtype=torch.int8) for _ in range(2))
+    ks, vs = (torch.full(shape[:3], 0.01) for _ in range(2))
+    at = lay.table[0][3], 0, 7
+    vs[at], v[at][0] = float("inf"), 0
+    cache, batch = on_gpu(bq, lay, (k, v, ks, vs))
+    q = (0.3 * torch.randn((n, Hq, D), generator=g)).to(BF16)
+    y = bq.CachedAttention(cache, Hq).attend(q.cuda(), batch, y=torch.empty((n, Hq, D), dtype=y_dtype, device="cuda")).cpu()
+    want = v[at].float() * float("inf")
+    assert bool(torch.isnan(y[..., 0]).all())
+    assert torch.equal(torch.isnan(y), torch.isnan(want).expand_as(y))
+    good = ~torch.isnan(want)
+    assert bool((y[..., good].float() == want[good]).all())
