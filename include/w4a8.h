@@ -597,7 +597,8 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   (rope NULL: none) by row positions[t] of the table (NULL: the row's
  *   place), in pairs (i, i + rot / 2) (W4_ROPE_HALF) or (2 i, 2 i + 1)
  *   (W4_ROPE_INTERLEAVED): a' = a c - b s, b' = b c + a s.  A position that
- *   the table does not have gives NaN (in an INT8 cache: the scale).  q [T][Hq][D] of q_type
+ *   the table does not have gives NaN.  A head that holds a NaN has codes of 0
+ *   and the scale NaN in an INT8 cache.  q [T][Hq][D] of q_type
  *   (W4_F16 or W4_BF16), 16-byte aligned; k and v go to the cache, rounded
  *   once (norms of what goes to 16 bits are plain fp32 sums), or as the codes
  *   and scale that a8_quantize gives for a head's values (the norm's steps
