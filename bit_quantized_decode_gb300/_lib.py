@@ -18,7 +18,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a8.so")
 
-W4_OK = 0
+W4_OK, W4_INVALID_ARG, W4_UNSUPPORTED_SHAPE, W4_MISALIGNED = range(4)
 STATUS = {
     0: "W4_OK",
     1: "W4_ERR_INVALID_ARG",
@@ -995,9 +995,8 @@ def w4_tree_attention_workspace_bytes(cache, batch, T: int, Hq: int) -> int:
     return int(load().w4_tree_attention_workspace_bytes(ctypes.byref(cache), ctypes.byref(batch), T, Hq))
 
 
-def w4_tree_attention(cache, batch, q, y, workspace, mask=None, scale: float = None, flags: int = 0, stream=None):
-    """y [T][Hq][D] (fp32, fp16 or bf16) of q [T][Hq][D] over the cache; mask int64 [T]: bit j is the sequence's row j
-    (None: a row sees the rows up to itself); scale: 1 / sqrt(D) if None."""
+def _attention_tensors(cache, batch, q, y, workspace, mask):
+    """Checks the tensors of a tree attention: their device, T and Hq."""
     dev, D, s = torch.cuda.current_device(), cache.D, q.shape
     if len(s) != 3 or s[2] != D:
         raise ValueError(f"q: shape {tuple(s)} is not [rows][heads][{D}]")
@@ -1006,11 +1005,41 @@ def w4_tree_attention(cache, batch, q, y, workspace, mask=None, scale: float = N
             and _fits(dev, workspace, _U8, workspace.shape)):
         _check_tensors(("q", q, _HALVES, None), ("y", y, _FLOATS, s), ("mask", mask, _I64, (T,)), ("workspace", workspace, _U8, None))
     _check_home(dev, cache, batch)
+    return dev, T, Hq
+
+
+def check_tree_attention(cache, batch, q, y, workspace, mask=None, scale: float = None):
+    """Raises what w4_tree_attention would, and launches nothing: for a caller that writes the cache first.  The tensors'
+    device, rows and heads, for launch_tree_attention."""
+    home = _attention_tensors(cache, batch, q, y, workspace, mask)
+    _, T, Hq = home
+    if T == 0 or batch.B == 0:
+        return home
+    need = w4_tree_attention_workspace_bytes(cache, batch, T, Hq)
+    if need == 0 or workspace.numel() < need:
+        raise W4Error("w4_tree_attention", W4_UNSUPPORTED_SHAPE)
+    if (cache.type != CACHE_TYPES[torch.int8] and ELEM_TYPES[q.dtype] != cache.type) or not (scale is None or 0.0 < scale < 3e38):
+        raise W4Error("w4_tree_attention", W4_INVALID_ARG)
+    if (q.data_ptr() | y.data_ptr() | workspace.data_ptr()) % 16 or (mask is not None and mask.data_ptr() % 8):
+        raise W4Error("w4_tree_attention", W4_MISALIGNED)
+    return home
+
+
+def launch_tree_attention(home, cache, batch, q, y, workspace, mask, scale, flags, stream):
+    """w4_tree_attention of tensors that are checked."""
+    dev, T, Hq = home
     st = load().w4_tree_attention(cache._ref, batch._ref, q.data_ptr(), ELEM_TYPES[q.dtype], T, Hq, _addr(mask),
-                                  D ** -0.5 if scale is None else scale, y.data_ptr(), ELEM_TYPES[y.dtype], workspace.data_ptr(),
+                                  cache.D ** -0.5 if scale is None else scale, y.data_ptr(), ELEM_TYPES[y.dtype], workspace.data_ptr(),
                                   workspace.numel(), flags, _raw_stream(stream, dev))
     if st != W4_OK:
         raise W4Error("w4_tree_attention", st)
+
+
+def w4_tree_attention(cache, batch, q, y, workspace, mask=None, scale: float = None, flags: int = 0, stream=None):
+    """y [T][Hq][D] (fp32, fp16 or bf16) of q [T][Hq][D] over the cache; mask int64 [T]: bit j is the sequence's row j
+    (None: a row sees the rows up to itself); scale: 1 / sqrt(D) if None."""
+    launch_tree_attention(_attention_tensors(cache, batch, q, y, workspace, mask), cache, batch, q, y, workspace, mask, scale, flags,
+                          stream)
 
 
 def logit_rules(vocab: int, ids=None, length=None, prompt=None, repetition=None, frequency=None, presence=None, bias_ids=None,

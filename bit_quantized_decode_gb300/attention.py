@@ -133,8 +133,11 @@ class CachedAttention:
         self._rope = None if rope is None else rope.desc
 
     def workspace(self, T: int, batch: KVBatch):
-        return torch.empty(_lib.w4_tree_attention_workspace_bytes(self.cache.desc, batch.desc, T, self.heads), dtype=torch.uint8,
-                           device=self.cache.k.device)
+        """A workspace for the attention of T rows (W4Error for a batch that it refuses)."""
+        n = _lib.w4_tree_attention_workspace_bytes(self.cache.desc, batch.desc, T, self.heads)
+        if n == 0 and T != 0 and batch.desc.B != 0:
+            raise _lib.W4Error("w4_tree_attention_workspace_bytes", _lib.W4_UNSUPPORTED_SHAPE)
+        return torch.empty(n, dtype=torch.uint8, device=self.cache.k.device)
 
     def buffers(self, T: int, batch: KVBatch, dtype=torch.float32) -> AttentionBuffers:
         """What the calls on T rows write; y of `dtype`.  Calls that share buffers must not overlap on the GPU."""
@@ -165,10 +168,12 @@ class CachedAttention:
     def __call__(self, qkv, batch: KVBatch, positions=None, mask=None, buffers: AttentionBuffers = None, flags: int = 0,
                  stream=None):
         """append, then attend: three launches, the second a programmatic dependent of the first.  Without buffers y has
-        qkv's type."""
+        qkv's type.  What either refuses is refused before the cache is written."""
         b = buffers
         if b is None:
             with _lib.allocating_on(stream):
                 b = self.buffers(qkv.shape[0], batch, qkv.dtype)
+        home = _lib.check_tree_attention(self.cache.desc, batch.desc, b.q, b.y, b.workspace, mask, self.scale)
         self.append(qkv, batch, positions, b.q, flags, stream)
-        return self.attend(b.q, batch, mask, b.y, b.workspace, _lib.W4_FLAG_PDL, stream)
+        _lib.launch_tree_attention(home, self.cache.desc, batch.desc, b.q, b.y, b.workspace, mask, self.scale, _lib.W4_FLAG_PDL, stream)
+        return b.y
