@@ -22,6 +22,7 @@ inline bool half_type(int t) { return t == W4_F16 || t == W4_BF16; }
 
 constexpr int kMaxHeads = 1024;
 constexpr long long kMaxPlaces = 1ll << 30;
+constexpr int kMaxHistory = 1 << 28;                      // (tokens are counted in fours and walked in 32 bits)
 constexpr long long kMaxUnits = 0x7fffffffll - 1024;      // (the kernels count units of work in 32 bits)
 
 int log2_of(int v)
@@ -226,7 +227,9 @@ w4_status w4_logits_adjust(const w4_logit_rules* u, const void* logits, int type
     if (ld < u->V || ld_out < u->V || (drafts && !row_start) || (mask && !drafts) ||
         (logits == out && ld != ld_out && R > 1))
         return W4_ERR_INVALID_ARG;
-    if (R > W4_MAX_TOKENS || u->V > (1 << 24) || static_cast<long long>(R) * u->V > (1ll << 42) || u->n_bias > W4_MAX_BIASES || u->S > W4_MAX_TOKENS) return W4_ERR_UNSUPPORTED_SHAPE;
+    if (R > W4_MAX_TOKENS || u->V > (1 << 24) || static_cast<long long>(R) * u->V > (1ll << 42) || u->n_bias > W4_MAX_BIASES ||
+        u->S > W4_MAX_TOKENS || u->cap > kMaxHistory)
+        return W4_ERR_UNSUPPORTED_SHAPE;
     if (R == 0 || u->V == 0 || u->S == 0) return W4_OK;
     const bool hist = u->cap > 0, bias = u->n_bias > 0;
     if (!logits || !out || (hist && (!u->ids || !u->length)) || (bias && (!u->bias_ids || !u->bias))) return W4_ERR_INVALID_ARG;
@@ -257,7 +260,7 @@ w4_status w4_logits_adjust(const w4_logit_rules* u, const void* logits, int type
     a.drafts = drafts;
     a.mask = mask;
     a.allowed = allowed;
-const size_t between = (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(logits)) % 16;
+    const size_t between = (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(logits)) % 16;
     a.vec = between == 0 && (R == 1 || ((ld - ld_out) * static_cast<long long>(eb)) % 16 == 0);
     return cuda_status(launch_logits(a, type, reinterpret_cast<cudaStream_t>(s)));
 }

@@ -695,7 +695,7 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
  *   factors float [S] may be NULL (1, 0 and 0), so may allowed (uint32 [R][ceil(V / 32)]).
  *   Ids outside 0 .. V - 1 are passed over.  logits: [R] rows of ld values of
  *   `type`, out the same with ld_out (it may be logits itself, with
- *   the same ld).  V <= 2^24,
+ *   the same ld).  V <= 2^24, cap <= 2^28,
  *   n_bias <= W4_MAX_BIASES.  The rows must not overlap other than that.  flags:
  *   0 or W4_FLAG_PDL (the same, as above).
  * ------------------------------------------------------------------------ */

@@ -1,4 +1,5 @@
 """What the attention refuses, it refuses before the cache is written; arguments at the ends of their ranges.  No GPU."""
+import ctypes
 import types
 
 import pytest
@@ -70,3 +71,11 @@ def test_a_workspace_for_a_refused_call_is_an_error(L, calls):
             att.workspace(T, b)
         with pytest.raises((L.W4Error, RuntimeError)):
             att.buffers(T, b)
+
+
+def test_histories_that_32_bits_do_not_count_are_refused(L):
+    u = L.LogitRulesDesc(V=100, S=1, ids=0x1000, cap=(1 << 28) + 1, length=0x1000)
+    call = lambda: L.load().w4_logits_adjust(ctypes.byref(u), 0x1000, 0, 100, 1, None, None, None, None, 0x1000, 100, 0, None)  # noqa: E731
+    assert call() == L.W4_UNSUPPORTED_SHAPE
+    u.cap, u.length = 1 << 28, 0x1002            # the longest: refused for its misaligned lengths, only
+    assert call() == L.W4_MISALIGNED
