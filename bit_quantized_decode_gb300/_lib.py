@@ -1018,7 +1018,7 @@ def check_tree_attention(cache, batch, q, y, workspace, mask=None, scale: float 
     need = w4_tree_attention_workspace_bytes(cache, batch, T, Hq)
     if need == 0 or workspace.numel() < need:
         raise W4Error("w4_tree_attention", W4_UNSUPPORTED_SHAPE)
-    if (cache.type != CACHE_TYPES[torch.int8] and ELEM_TYPES[q.dtype] != cache.type) or not (scale is None or 0.0 < scale < 3e38):
+    if (cache.type != CACHE_TYPES[torch.int8] and ELEM_TYPES[q.dtype] != cache.type) or not (scale is None or 0.0 < scale < 2e38):
         raise W4Error("w4_tree_attention", W4_INVALID_ARG)
     if (q.data_ptr() | y.data_ptr() | workspace.data_ptr()) % 16 or (mask is not None and mask.data_ptr() % 8):
         raise W4Error("w4_tree_attention", W4_MISALIGNED)

@@ -184,7 +184,7 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
     w4_status r = check_call(c, b, T, Hq);
     if (r != W4_OK) return r;
     if (!half_type(q_type) || (c->type != W4_I8 && q_type != c->type) || !elem_type(y_type) || (flags & ~W4_FLAG_PDL) != 0 ||
-        !(scale > 0.0f) || !(scale < 3.0e38f))
+        !(scale > 0.0f) || !(scale < 2.0e38f))             // (times log2(e) it is an fp32 number)
         return W4_ERR_INVALID_ARG;
     if (b->max_tokens > W4_MAX_DRAFTS) return W4_ERR_UNSUPPORTED_SHAPE;
     if (T == 0 || b->B == 0) return W4_OK;

@@ -607,7 +607,8 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  * w4_kv_values: out float [pages][Hkv][page_size][D], 16-byte aligned: the
  *   numbers that an INT8 cache's keys (W4_KEYS) or values (W4_VALUES) stand
  *   for, codes times scales, every page of the cache.
- * w4_tree_attention: y[t][h] = sum p v / sum p, p = exp(scale q.k), over the
+ * w4_tree_attention: y[t][h] = sum p v / sum p, p = exp(scale q.k) (0 < scale <
+ *   2e38), over the
  *   places below ctx and the drafts of the row's own sequence (the rows of
  *   this call, already appended) whose bit the row's mask has: bit j of
  *   mask[t] (uint64, device) is row j of the sequence.  mask NULL: row i sees

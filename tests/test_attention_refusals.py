@@ -79,3 +79,11 @@ def test_histories_that_32_bits_do_not_count_are_refused(L):
     assert call() == L.W4_UNSUPPORTED_SHAPE
     u.cap, u.length = 1 << 28, 0x1002            # the longest: refused for its misaligned lengths, only
     assert call() == L.W4_MISALIGNED
+
+
+def test_scales_that_pass_fp32_times_log2_e_are_refused(L):
+    c = L.KVCacheDesc(k=0x1000, v=0x1000, type=2, pages=10, page_size=16, Hkv=2, D=64)
+    b = L.KVBatchDesc(table=0x1000, ctx=0x1000, q_start=0x1000, B=2, max_pages=4, max_tokens=4)
+    f = lambda scale, y: L.load().w4_tree_attention(ctypes.byref(c), ctypes.byref(b), 0x1000, 2, 3, 4, None, scale, y, 0, 0x1000,  # noqa: E731
+                                                    1 << 40, 0, None)
+    assert f(2.5e38, 0x1000) == L.W4_INVALID_ARG and f(1.9e38, 0x1004) == L.W4_MISALIGNED
