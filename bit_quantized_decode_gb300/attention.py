@@ -73,8 +73,9 @@ class RopeTable:
         """Angles per position (float64 [rot / 2]) and the factor of the rotated values.  scaling, for contexts past the
         trained length: {"kind": "linear", "factor"} divides all angles; {"kind": "base", "factor"} raises the base so that
         the slowest pair is divided by it; {"kind": "by_parts", "factor", "trained", "slow": 1, "fast": 32} divides the pairs that turn
-        less than `slow` times over the trained length, leaves those that turn more than `fast` times, goes linearly between
-        them, and scales the rotated values by 0.1 ln(factor) + 1 (or "attention")."""
+        less than `slow` times over the trained length, leaves those that turn more than `fast` times, goes linearly in the turns
+        between them, and scales the rotated values by 0.1 ln(factor) + 1 (or "attention").  Programs that go linearly in the
+        pair's number between two rounded borders get other angles in between: their tables go to RopeTable itself."""
         if rot < 0 or rot % 8:
             raise ValueError(f"rot {rot} is not a multiple of 8")
         s = dict(scaling or {"kind": "none"})
@@ -89,6 +90,8 @@ class RopeTable:
             inv = inv / f
         elif kind == "by_parts":
             slow, fast = float(s.pop("slow", 1.0)), float(s.pop("fast", 32.0))
+            if "trained" not in s or not float(s["trained"]) > 0.0 or not 0.0 <= slow < fast:
+                raise ValueError(f"scaling {scaling!r}: by_parts takes a trained length and slow below fast")
             scale = float(s.pop("attention", 0.1 * math.log(f) + 1.0))
             turns = float(s.pop("trained")) * inv / (2 * math.pi)
             keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)

@@ -87,3 +87,11 @@ def test_scales_that_pass_fp32_times_log2_e_are_refused(L):
     f = lambda scale, y: L.load().w4_tree_attention(ctypes.byref(c), ctypes.byref(b), 0x1000, 2, 3, 4, None, scale, y, 0, 0x1000,  # noqa: E731
                                                     1 << 40, 0, None)
     assert f(2.5e38, 0x1000) == L.W4_INVALID_ARG and f(1.9e38, 0x1004) == L.W4_MISALIGNED
+
+
+@pytest.mark.parametrize("scaling", [{}, {"trained": 0}, {"trained": float("nan")}, {"trained": 4096, "slow": 32.0}, {"trained": 4096, "slow": -1.0},
+                                     {"trained": 4096, "fast": 0.5}])
+def test_scaling_by_parts_that_says_too_little(scaling):
+    from bit_quantized_decode_gb300 import RopeTable
+    with pytest.raises(ValueError):
+        RopeTable.frequencies(64, 1e4, {"kind": "by_parts", "factor": 4.0, **scaling})
