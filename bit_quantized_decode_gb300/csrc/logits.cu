@@ -4,7 +4,7 @@
 //   path among it); seen: n > 0 or v in the prompt
 //   l = l > 0 ? l / rep : l rep    where seen
 //   l = l - freq n - pres          where n > 0
-//   l = l + bias (entries for the same v added in their order)
+//   l = l + the sum of v's biases (added up from 0 in their order)
 //   l = -inf                       where v is not allowed
 // each step one fp32 operation, rounded to the logits' type at the end.
 //

@@ -690,7 +690,7 @@ w4_status w4_tree_attention(const w4_kv_cache* c, const w4_kv_batch* b, const vo
  *   For token v with n occurrences among the generated ones:
  *     l = l > 0 ? l / repetition[s] : l * repetition[s]   if n > 0 or v is in the prompt,
  *     l = l - frequency[s] * n - presence[s]              if n > 0,
- *     l = l + the biases of v, added in their order (bias_ids int [S][n_bias], bias float),
+ *     l = l + the sum of v's biases, added up from 0 in their order (bias_ids int [S][n_bias], bias float),
  *     l = -inf                                            if bit v % 32 of allowed[r][v / 32] is 0,
  *   each step an fp32 operation, rounded to the logits' type.  The arrays of
  *   factors float [S] may be NULL (1, 0 and 0), so may allowed (uint32 [R][ceil(V / 32)]).
