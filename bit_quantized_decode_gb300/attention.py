@@ -51,7 +51,9 @@ class KVCache:
 class KVBatch:
     """table int32 [B][max_pages], ctx int32 [B], q_start int32 [B + 1]: sequence b has rows q_start[b] .. q_start[b + 1] - 1
     behind ctx[b] cached tokens.  The tensors stay on the device and may be updated in place between calls.
-    max_tokens: the most rows of a sequence."""
+    max_tokens: the most rows of a sequence.  It decides which kernel attends (up to 16 rows of max_tokens times query heads to a
+    key head, or more) and the workspace's size, so a program that has steps of one token and of many drafts makes a batch
+    object for each, on the same tensors."""
 
     def __init__(self, table, ctx, q_start, max_tokens: int):
         self.desc = _lib.kv_batch(table, ctx, q_start, max_tokens)
@@ -160,7 +162,7 @@ class CachedAttention:
 
     def attend(self, q, batch: KVBatch, mask=None, y=None, workspace=None, flags: int = 0, stream=None):
         """y [T][heads][head_dim] over the cache and the drafts of each row's mask (int64 [T], bit j: the sequence's row j;
-        None: the rows up to itself).  Without y it has q's type."""
+        None: the rows up to itself).  Without y it has q's type.  Sequences of up to 64 rows."""
         if y is None or workspace is None:
             with _lib.allocating_on(stream):
                 y = torch.empty_like(q) if y is None else y

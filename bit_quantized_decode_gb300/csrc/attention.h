@@ -12,8 +12,9 @@
 
 namespace w4k {
 
-// Every launch here is a programmatic dependent of the kernel before it: the kernels touch no memory before their dependency
-// wait (the joining launch of the attention reads what its first launch has waited for), so that is legal behind anything.
+// Every launch here but the rotation table's is a programmatic dependent of the kernel before it: the kernels touch no memory
+// before their dependency wait (the joining launch of the attention reads what its first launch has waited for), so that is legal
+// behind anything.
 
 constexpr int T_I8 = 3;                         // W4_I8: a cache of INT8 codes
 

@@ -25,12 +25,14 @@
 // cache eight widen codes to 16 bits (exact) in shared memory.  All
 // are joined by mbarriers with bounded waits.
 //
-// A tile of 128 rows by 64 tokens takes 1330 cycles, the softmax's time (maximum and exchange 400, exponentials 400, the way
-// from the scores' arrival to P's 1100 in all); its MMAs take 530, its bytes 1470 at the SM's share of the memory rate (bf16,
-// heads of 128).  An fp32 output takes 1850 (three parts).  16 drafts of 28 heads over 4096 bf16 places: 16.9 us, over 131071
-// 73 (70 if sums stay in tensor memory); 8 x 64 drafts over 2800 to 4000 places 52 (tensor pipe 28% active). INT8 with heads of 256: 2700 cycles a
-// tile (its bytes take 1480): widening and the softmax share the issue slots; 5 drafts of 8 heads over 120001 places 38 us, over a
-// bf16 cache 39 (2600 cycles, its bytes 2940 at that rate).
+// A tile of 128 rows by 64 tokens takes 1330 cycles with one part to a probability, the softmax's time (maximum and exchange 400,
+// exponentials 400, the way from the scores' arrival to P's 1100 in all); its MMAs take 530, its bytes 1470 at the SM's share of
+// the memory rate (bf16, heads of 128).  Three parts (fp32 outputs) take 1850.  16 drafts of 28 heads over 4096 bf16 places, fp32
+// outputs: 16.9 us, over 131071 73 (70 if sums stay in tensor memory); 8 x 64 drafts over 2800 to 4000 places, two parts: 60 (52
+// with one, tensor pipe 28% active then).  INT8 with heads of 256, one part: 2700 cycles a tile (its bytes take 1480) with no
+// resource full (issue slots 50%, tensor pipe 25%, DRAM 26% of the time): a tile's way from codes to 16 bits, scores, softmax and
+// product, of which two 16-bit tiles and one place for scores let little overlap; warps wait for loads most.  5 drafts of 8 heads
+// over 120001 places, two parts: 41 us, over a bf16 cache 40.
 #include "attn_tree.cuh"
 #include "gemm_w8.cuh"
 
@@ -44,11 +46,11 @@ constexpr int kConvWarps = 8;                   // warps 2, 3, 12 .. 17: four fo
 // tile of three parts), 25 to 100 tiles to a block: 0.9e-6 to 3.2e-6 off with 8, 1.4e-6 to 6.6e-6 with 16, 2.9e-6 to 13e-6 with 32.
 // 16 drafts over 131071 places: 78, 73, 72 us, 70 without; over 65536 48, 45, 43, 43, INT8 68, 56, 54, 54.
 constexpr int kFlushParts = 16;
-// One part (four steps a tile, 16-bit outputs): 0.4e-6 a tile.  2048 tiles to a block, 8.3e-4 (3.4 half steps of fp16); 1.0e-4
-// with 256, 0.2e-4 with 64.  16 drafts of 8 sequences over 131071 places, 431 tiles to a block, bf16: 322 us without, 328 with 256,
-// 347 with 64, INT8 420, 440, 486.  The code alone costs 8 x 64 drafts over 4096 places 52.5 -> 53.8, so calls in which
-// no block can have more than 256 tiles of a segment do without.
-constexpr int kFlushOne = 256;
+// 16-bit outputs: 0.4e-6 a tile and part.  One part, 2048 tiles to a block: 8.3e-4 (3.4 half steps of fp16); 1.0e-4 with 256,
+// 0.2e-4 with 64.  16 drafts of 8 sequences over 131071 places, 431 tiles to a block, one part of bf16: 322 us without, 328 with
+// 256, 347 with 64, INT8 420, 440, 486.  The code alone costs 8 x 64 drafts over 4096 places 52.5 -> 53.8, so calls in which no
+// block can have more than 128 tiles of a segment do without.
+constexpr int kFlushLate = 128;
 
 template <int D, int CT, int kParts>
 struct Tc {
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
             }
             float m = neg_inf(), l = 0.0f;
             // A sum that is taken out is added in fp32 to what lies in the block's place in the workspace (column groups of
-            // four, the rows of one beside each other): the error stays below 192 steps' 2^-23 each (1024 with one part),
+            // four, the rows of one beside each other): the error stays below 192 steps' 2^-23 each (late: 1024 a part),
             // however long the context.
             float* const part = A.part + (static_cast<size_t>(blockIdx.x) * 2 + (us < sg.u0 ? 1 : 0)) * attn_part_floats(A.part_rows, D);
             float4* const kept = reinterpret_cast<float4*>(A.kept + static_cast<size_t>(blockIdx.x) * A.part_rows * D) + (have ? row : 0);
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                     ok = warp_wait(pv_done + 8 * ((it - 1) & 1), static_cast<uint32_t>((it - 1) >> 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
-                    if constexpr (kParts > 1) take_out<D>(tl, half, have ? kept : nullptr, A.part_rows, keeps, kept_factor());
+                    if constexpr (kFlush < kFlushLate) take_out<D>(tl, half, have ? kept : nullptr, A.part_rows, keeps, kept_factor());
                     else take_out_seldom<D>(tl, half, have ? kept : nullptr, A.part_rows, keeps, kept_factor());
                     tc_fence_before();          // (a tile with odd drafts: the row's other half reads these columns, behind wg_sync)
                     keeps = true;
@@ -774,32 +776,32 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
                 uint32_t r[16];
                 tmem_ld16(tl + 16 * j, r);
                 if (have) {
-                float v[16];
+                    float v[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
-                if (kFlush > 0 && keeps) {
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+                    if (kFlush > 0 && keeps) {
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        const float4 o = __ldcg(kept + (4 * j + k / 4) * A.part_rows);
-                        v[k] += f_kept * o.x; v[k + 1] += f_kept * o.y; v[k + 2] += f_kept * o.z; v[k + 3] += f_kept * o.w;
+                        for (int k = 0; k < 16; k += 4) {
+                            const float4 o = __ldcg(kept + (4 * j + k / 4) * A.part_rows);
+                            v[k] += f_kept * o.x; v[k + 1] += f_kept * o.y; v[k + 2] += f_kept * o.z; v[k + 3] += f_kept * o.w;
+                        }
                     }
-                }
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] *= inv;
-                if (!whole || A.ytype == T_F32) {
-                    float4* d = reinterpret_cast<float4*>(whole ? static_cast<float*>(A.y) + at + 16 * j
-                                                                : part + 2 * A.part_rows + static_cast<size_t>(row) * D + 16 * j);
+                    for (int k = 0; k < 16; ++k) v[k] *= inv;
+                    if (!whole || A.ytype == T_F32) {
+                        float4* d = reinterpret_cast<float4*>(whole ? static_cast<float*>(A.y) + at + 16 * j
+                                                                    : part + 2 * A.part_rows + static_cast<size_t>(row) * D + 16 * j);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) d[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                } else {
-                    uint32_t w[8];
+                        for (int k = 0; k < 4; ++k) d[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    } else {
+                        uint32_t w[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        w[k] = A.ytype == T_F16 ? pair16<T_F16>(v[2 * k], v[2 * k + 1]) : pair16<T_BF16>(v[2 * k], v[2 * k + 1]);
-                    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.y) + at + 16 * j);
-                    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = A.ytype == T_F16 ? pair16<T_F16>(v[2 * k], v[2 * k + 1]) : pair16<T_BF16>(v[2 * k], v[2 * k + 1]);
+                        uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.y) + at + 16 * j);
+                        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
                 }
                 __syncwarp();
             }
@@ -863,10 +865,9 @@ __global__ void __launch_bounds__(Tc<D, CT, kParts>::kThreads, 1) attn_tc_kernel
     if (warp == 1) tmem_dealloc(tb, C::kCols);
 }
 
-constexpr int kExtra = 6;                       // (4 us at 0.7 us a unit)
-int blocks_of(int sms) { return sms < kAtMaxBlocks ? sms : kAtMaxBlocks; }
+constexpr int kExtra = 6;                       // (4 us at 0.7 us a unit, heads of 128 and bf16; 8 us of INT8 heads of 256)
 
-template <int D, int CT, int QT, int kParts, int kFlush = kFlushParts>
+template <int D, int CT, int QT, int kParts, int kFlush>
 cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 {
     using C = Tc<D, CT, kParts>;
@@ -898,13 +899,14 @@ cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 template <int D, int CT, int QT>
 cudaError_t launch_w(AttnArgs& a, int sms, cudaStream_t s)
 {
-    constexpr int f16_parts = CT == T_F16 ? 1 : 2;
-    if (a.ytype == T_F32) return launch<D, CT, QT, f16_parts + 1>(a, sms, s);
-    if (f16_parts > 1 && a.ytype == T_F16) return launch<D, CT, QT, 2>(a, sms, s);
-    // tiles of a segment, and of a block in equal shares (segments with blocks of their own: kExtra more), at most
-    const long long segment = (static_cast<long long>(a.b.max_pages) * a.c.page + kTcUnit - 1) / kTcUnit;
-    const long long share = a.units / blocks_of(sms) + 1 + kExtra;
-    return (segment < share ? segment : share) > kFlushOne ? launch<D, CT, QT, 1, kFlushOne>(a, sms, s) : launch<D, CT, QT, 1, 0>(a, sms, s);
+    if (a.ytype == T_F32) return launch<D, CT, QT, CT == T_F16 ? 2 : 3, kFlushParts>(a, sms, s);
+    const bool lasts = piece_units(a, blocks_of(sms), kTcUnit, kExtra) > kFlushLate;
+    if constexpr (CT == T_F16) {
+        if (a.ytype == T_BF16) return lasts ? launch<D, CT, QT, 1, kFlushLate>(a, sms, s) : launch<D, CT, QT, 1, 0>(a, sms, s);
+    } else {
+        if (a.ytype == T_F16) return launch<D, CT, QT, 2, kFlushParts>(a, sms, s);
+    }
+    return lasts ? launch<D, CT, QT, 2, kFlushLate>(a, sms, s) : launch<D, CT, QT, 2, 0>(a, sms, s);
 }
 
 template <int D>

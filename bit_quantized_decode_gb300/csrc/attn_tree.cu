@@ -18,14 +18,21 @@
 // result depends on timing.
 //
 // Precision: products of 16-bit numbers in fp32 sums; probabilities enter the
-// second product in the values' 16-bit type, in as many parts (11 or 8 bits
-// each) as the output's type can tell: fp32 two of fp16 or three of bf16, fp16
-// two of bf16, else one; fp16 ones times 2^15 (prob_lift).  INT8 codes are exact in 16 bits; a key's scale multiplies its
-// score, a value's scale its probability (bf16: no range of the scales is lost).
+// second product in the values' 16-bit type (bf16 for INT8 codes, which are
+// exact in 16 bits: a key's scale multiplies its score, a value's scale its
+// probability, and no range of the scales is lost), fp16 ones times 2^15
+// (prob_lift).  They have parts of 11 or 8 bits, so many that the output's own
+// rounding is what is left of their error: two, three of bf16 for an fp32 output, one
+// of fp16 for a bf16 output.  With one part of as many bits as the output a place
+// that has most of the weight moves all values of a row the same way: errors 1.3 to
+// 1.5 times those of the rounded definition, where they are now the same.  One
+// part would take 64 streams of D 64, 128, 256 in 70, 102, 113 us instead of 73, 103, 129,
+// 8 x 64 drafts in 52 instead of 60, 5 drafts over 120001 INT8 places in 38 instead of 41.
 //
-// One token over 131071 bf16 places (4 key heads of 128): 49 us, 5.5 TB/s; the stream itself runs at 7.1 TB/s for 38 us,
+// One token over 131071 bf16 places (4 key heads of 128): 49 to 50 us, 5.4 TB/s; the stream itself runs at 7.1 TB/s for 38 us,
 // between 5 us of start (lengths, page, first copies) and 4 of joining.  1000 places: 8.4 us.  64 streams of 400 to 8190
-// places: 102 us (565 MB).  INT8 codes cost instructions to widen: 14 rows over 65536 places (69 MB) 34 us, bf16 (134 MB) 30.
+// places: 103 us (565 MB).  INT8 codes cost instructions to widen: 14 rows over 65536 places (69 MB) 34 us, 7 rows 33, bf16
+// (134 MB) 30.
 #include <atomic>
 
 #include "attn_tree.cuh"
@@ -115,7 +122,8 @@ __device__ __forceinline__ void codes16(uint32_t c, uint32_t& h01, uint32_t& h23
     else i8_to_bf16(c, h01, h23);
 }
 
-template <int D, int CT, int QT, int kParts>
+// kAdd: a unit's products are added to the output in fp32.
+template <int D, int CT, int QT, int kParts, bool kAdd>
 __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const __grid_constant__ AttnArgs A)
 {
     using C = At<D, CT>;
@@ -374,18 +382,19 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
 #pragma unroll
                             for (int w = 0; w < 4; ++w) pa[k][w] = only_first(pa[k][w], vast(vsc[w & 2]), vast(vsc[(w & 2) + 1]));
                 }
-                // The tensor cores cut a sum's low bits at every step: for an output of more parts the units are added here.
-                // (One part: 1024 steps over 131071 places of one warp's eighth, 1.0e-4 off if all values are positive, 0.4 half
+                // The tensor cores cut a sum's low bits at every step: for an output of more bits the units are added here.
+                // (16 bits: 1024 steps over 131071 places of one warp's eighth, 1.0e-4 off if all values are positive, 0.4 half
                 // steps of fp16; added here, 64 streams of D 64, 128, 256 71.1, 102.8, 113.8 -> 72.8, 103.5, 118.9 us.)
                 auto pv = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-                    if constexpr (kParts > 1) {
+                    if constexpr (kAdd) {
                         float d[4] = {};
 #pragma unroll
                         for (int k = kParts - 1; k >= 0; --k) mma16<PT>(d, pa[k], b0, b1);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) acc[k] += d[k];
                     } else {
-                        mma16<PT>(acc, pa[0], b0, b1);
+#pragma unroll
+                        for (int k = kParts - 1; k >= 0; --k) mma16<PT>(acc, pa[k], b0, b1);
                     }
                 };
                 if constexpr (CT == T_I8) {
@@ -733,18 +742,20 @@ void dependent(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr)
     cfg.numAttrs = 1;
 }
 
-template <int D, int CT, int QT, int kParts>
+constexpr int kExtra = 16;                      // (3 us at 185 ns a unit, measured on bf16 heads of 128)
+
+template <int D, int CT, int QT, int kParts, bool kAdd>
 cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 {
     using C = At<D, CT>;
-    auto kern = attn_tree_kernel<D, CT, QT, kParts>;
+    auto kern = attn_tree_kernel<D, CT, QT, kParts, kAdd>;
     static SmemLimit limit;
     cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), limit, C::smem(kAtMaxSeq));
     if (e == cudaSuccess) e = encode_kv_map(&a.kmap, a, a.c.k, C::kBox, kAtUnit);
     if (e == cudaSuccess) e = encode_kv_map(&a.vmap, a, a.c.v, C::kBox, kAtUnit);
     if (e != cudaSuccess) return e;
-    a.blocks = sms < kAtMaxBlocks ? sms : kAtMaxBlocks;
-    a.extra = 16;                               // (3 us at 185 ns a unit)
+    a.blocks = blocks_of(sms);
+    a.extra = kExtra;
     a.least = C::kWarps;                        // a unit for each warp
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -759,9 +770,15 @@ cudaError_t launch(AttnArgs& a, int sms, cudaStream_t s)
 template <int D, int CT, int QT>
 cudaError_t launch_w(AttnArgs& a, int sms, cudaStream_t s)
 {
-    if constexpr (CT == T_F16) return a.ytype == T_F32 ? launch<D, CT, QT, 2>(a, sms, s) : launch<D, CT, QT, 1>(a, sms, s);
-    else return a.ytype == T_F32 ? launch<D, CT, QT, 3>(a, sms, s) : a.ytype == T_F16 ? launch<D, CT, QT, 2>(a, sms, s)
-                                                                                       : launch<D, CT, QT, 1>(a, sms, s);
+    if (a.ytype == T_F32) return launch<D, CT, QT, CT == T_F16 ? 2 : 3, true>(a, sms, s);
+    if constexpr (CT == T_F16) {
+        if (a.ytype == T_BF16) return launch<D, CT, QT, 1, false>(a, sms, s);
+    } else {
+        if (a.ytype == T_F16) return launch<D, CT, QT, 2, true>(a, sms, s);
+    }
+    // as many bits as the output has: the sums may stay on the tensor cores for 1024 steps of a warp, or 8192 where it is bf16
+    const long long steps = 2 * (piece_units(a, blocks_of(sms), kAtUnit, kExtra) / At<D, CT>::kWarps + 1);
+    return steps > (a.ytype == T_F16 ? 1024 : 8192) ? launch<D, CT, QT, 2, true>(a, sms, s) : launch<D, CT, QT, 2, false>(a, sms, s);
 }
 
 template <int D>

@@ -206,6 +206,15 @@ __device__ __forceinline__ int2 block_units(const Layout& L, const AttnArgs& A, 
     return make_int2(us, us + min(L.share, L.total - us));
 }
 
+// Of the host: blocks of a launch; units of one segment that a block takes at most, by the table's width (equal shares, or
+// `extra` more where segments have blocks of their own).
+inline int blocks_of(int sms) { return sms < kAtMaxBlocks ? sms : kAtMaxBlocks; }
+inline long long piece_units(const AttnArgs& a, int blocks, int unit, int extra)
+{
+    const long long segment = (static_cast<long long>(a.b.max_pages) * a.c.page + unit - 1) / unit, share = a.units / blocks + 1 + extra;
+    return segment < share ? segment : share;
+}
+
 // Box of a 3-D tensor map -> shared memory.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar)
 {

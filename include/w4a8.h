@@ -620,11 +620,12 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   cache's type (either 16-bit type for W4_I8), y [T][Hq][D] of y_type, both
  *   16-byte aligned; query head h reads key head h / (Hq / Hkv).
  *   Sums in fp32, of which the tensor cores cut up to 2^-23 a step: 192 steps
- *   at most where y has more bits than a part of a probability, else 1024 (up
- *   to 16 rows to a key head: one for every 64 or 128 places).  A probability enters the second product in the 16-bit type
- *   of the values (bf16 for W4_I8): in one part where y is of no more bits, in
- *   two or three where y is W4_F32, in two where y is W4_F16 and it is bf16.
- *   In fp16 it is off by 2^-34 of the row's largest besides (fp16's least step).
+ *   at most where y is W4_F32 (or W4_F16 of another cache), 1024 where it is
+ *   W4_F16 over a W4_F16 cache, 8192 where it is W4_BF16.  A probability enters
+ *   the second product in the 16-bit type of the values (bf16 for W4_I8) in two
+ *   parts, in three where that is bf16 and y is W4_F32, in one where it is fp16
+ *   and y W4_BF16.  In fp16 it is off by 2^-34 of the row's largest besides
+ *   (fp16's least step).
  *   workspace: w4_tree_attention_workspace_bytes(..) bytes, 16-byte aligned,
  *   with no contents to keep; calls that share one must not overlap on the
  *   GPU.  Two launches.  For given inputs the result is the same in every

@@ -20,17 +20,22 @@ def bq():
 
 
 def parts_unit(cache_dtype, y_dtype):
-    """Relative rounding of a probability: the square of its type's where it has two parts or more (fp32 outputs, and fp16
-    ones where it is bf16)."""
+    """Relative rounding of a probability: the square of its type's, twice, where it has two parts or more (all but bf16
+    outputs over an fp16 cache: 11 bits)."""
     u = half_unit(F16 if cache_dtype == F16 else BF16)
-    return 2 * u * u if y_dtype == F32 or (y_dtype == F16 and cache_dtype != F16) else u
+    return u if cache_dtype == F16 and y_dtype == BF16 else 2 * u * u
+
+
+def cuts_of(half, y_dtype):
+    """Steps on the tensor cores that add up in a sum: 192 (12 a tile of 64 places, 16 tiles); 1024 for fp16 over an fp16 cache,
+    8192 for bf16."""
+    return 192 if y_dtype == F32 else 8192 if y_dtype == BF16 else 1024 if half else 192
 
 
 def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit, half, exact):
     """Outputs in 64 bits and the bound of the kernels' error, on q's device.  The score's and the exponential's part is that of
-    attention_reference.attend.  The sums': a product's step on the tensor cores cuts 2^-23 of the sum at most, 192 of them
-    add up (12 a tile of 64 places, 16 tiles) before the sum is taken out, or 1024 where probabilities have one part (4 a tile,
-    256 tiles; few rows: every fourth 16 places); the sums in fp32 take a step of 2^-24 for every
+    attention_reference.attend.  The sums': a product's step on the tensor cores cuts 2^-23 of the sum at most, cuts_of of them
+    add up; the sums in fp32 take a step of 2^-24 for every
     16 places at most, and some 64 to join the parts.  Numerator and sum have them both.  A probability in fp16 parts is
     2^9 times as large as it stands to the largest, or more, and off by half of fp16's least step, 2^-25.  exact: the scores'
     products and their sums are fp32 numbers."""
@@ -51,7 +56,7 @@ def attend_64(lay, q, k, v, masks, scale, y_dtype, p_unit, half, exact):
             y[t] = torch.einsum("hgl,hld->hgd", p, Vs).reshape(Hq, D)
             mag = scale * torch.einsum("hgd,hld->hgl", qq.abs(), Ks.abs()).amax(-1, keepdim=True)
             ds = (0.0 if exact else mag * (D + 16) * 2.0 ** -23) + 3 * s.abs().amax(-1, keepdim=True) * 2.0 ** -22
-            cuts = 192 if p_unit < 2.0 ** -15 else max(1024, Ks.shape[1] / 64)
+            cuts = cuts_of(half, y_dtype)
             e = 2 * ds + 2.0 ** -20 + 2 * (cuts * 2.0 ** -23 + (Ks.shape[1] / 16 + 64) * 2.0 ** -24)
             weight = torch.einsum("hgl,hld->hgd", p, Vs.abs())
             least = 2.0 ** -34 * p.amax(-1, keepdim=True) * Vs.abs().sum(1)[:, None] if half else 0.0
@@ -172,8 +177,8 @@ def on_gpu_only(bq, B, n, ctx, Hkv, D, dtype, seed, grow=False, sign=False):
 @pytest.mark.parametrize("G,n", [(16, 2), (8, 1)])
 def test_long_sums_of_one_sign_stay_centred(bq, G, n):
     """131071 places to a block, values that are all positive, fp16 outputs: what the tensor cores cut from the sums is 1024
-    steps of 2^-23 at most, however long the context (few rows: 16 places a step, eight warps: 1024 steps, too).  The mean over
-    many outputs, which their rounding leaves alone: it is 2^-12 / sqrt(3) / sqrt(count) off, taken six times."""
+    steps of 2^-23 at most, however long the context.  The mean over many outputs, which their rounding leaves alone: it is
+    2^-12 / sqrt(3) / sqrt(count) off, taken six times."""
     B, ctx, Hkv, D = 19, 131071, 8, 64
     lay, cache, batch, make_q = on_gpu_only(bq, B, n, ctx, Hkv, D, F16, 3, sign=True)
     q = make_q(G * Hkv)
@@ -256,3 +261,40 @@ def test_an_infinite_scale_gives_infinities(bq, Hq, D, n, y_dtype):
     assert torch.equal(torch.isnan(y), torch.isnan(want).expand_as(y))
     good = ~torch.isnan(want)
     assert bool((y[..., good].float() == want[good]).all())
+
+
+# ------------------------------------------------------------- 16-bit outputs
+@pytest.mark.parametrize("dtype,y_dtype", [(BF16, BF16), (I8, BF16), (F16, F16), (BF16, F16), (I8, F16), (F16, BF16)])
+@pytest.mark.parametrize("Hq,Hkv,D,n,B", [(4, 2, 64, 1, 40), (28, 4, 128, 1, 20), (28, 4, 128, 16, 3), (8, 1, 256, 1, 30), (8, 1, 256, 5, 8)])
+def test_16_bit_outputs_are_as_good_as_rounded_ones(bq, Hq, Hkv, D, n, B, dtype, y_dtype):
+    """One place of 300 has values; its probability, below 1 by a place's five before it, is some number that 8 bits do not hold: all
+    values of a row would be off by its rounding, the same way.  In two parts they are off by 2^-15 (fp16 2^-20, or 2^-11 in the one
+    part that a bf16 output has) and what exponentials and scores (2^-19) and 40 steps of the sums (2^-17) take, and rounded: a value
+    that rounding takes to the same side differs as the definition's rounded value does, another one by twice that more.  Exact
+    scores: rows and keys of one magnitude."""
+    ctx, page = 300, 32
+    lay = ref.Paged(D, [n] * B, [ctx] * B, page)
+    g = torch.Generator().manual_seed(D + n)
+    shape = (lay.pages, Hkv, page, D)
+    like = torch.where(torch.rand(D, generator=g) < 0.5, -1.0, 1.0)
+    q = (like * (0.5 + torch.rand((lay.T, Hq, 1), generator=g))).to(F16 if dtype == F16 else BF16)
+    k, v = torch.zeros(shape), torch.zeros(shape)
+    ks, vs = (0.5 + torch.rand(shape[:3], generator=g) for _ in range(2))
+    for b in range(B):
+        for place, size in ((195, 127.0), (200, 64.0)):
+            k[lay.table[b][place // page], :, place % page] = like * size
+        at = lay.table[b][200 // page], slice(None), 200 % page
+        v[at] = (60 * torch.randn((Hkv, D), generator=g)).clamp(-127, 127).round()
+        ks[lay.table[b][195 // page], :, 195 % page] = ks[at] = 2.0 ** -8 / D ** 0.5
+    if dtype == I8:
+        tensors = (k.to(torch.int8), v.to(torch.int8), ks, vs)
+        k64, v64 = k.double() * ks.double()[..., None], v.double() * vs.double()[..., None]
+    else:
+        k, v = (k * 2.0 ** -8 / D ** 0.5).to(dtype), v.to(dtype)
+        tensors, k64, v64 = (k, v, None, None), k.double(), v.double()
+    masks = [(2 << i) - 1 for i in range(n)] * B
+    y = check(bq, lay, tensors, k64, v64, q, masks, y_dtype, exact=True).double()
+    want, _ = attend_64(lay, q.double(), k64, v64, masks, D ** -0.5, y_dtype, 0.0, dtype == F16, True)
+    rounded = want.to(y_dtype).double()
+    most = (rounded - want).norm() + 2 * (parts_unit(dtype, y_dtype) + 2.0 ** -17 + 2.0 ** -19) * want.norm()
+    assert float((y - want).norm()) <= float(most), float((y - want).norm() / (rounded - want).norm())
