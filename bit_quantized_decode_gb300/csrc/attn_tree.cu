@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(At<D, CT>::kThreads, 1) attn_tree_kernel(const
                             for (int w = 0; w < 4; ++w) pa[k][w] = only_first(pa[k][w], vast(vsc[w & 2]), vast(vsc[(w & 2) + 1]));
                 }
                 // The tensor cores cut a sum's low bits at every step: for an output of more bits the units are added here.
-                // (16 bits: 1024 steps over 131071 places of one warp's eighth, 1.0e-4 off if all values are positive, 0.4 half
-                // steps of fp16; added here, 64 streams of D 64, 128, 256 71.1, 102.8, 113.8 -> 72.8, 103.5, 118.9 us.)
+                // (16 bits: 1024 steps are 1.0e-4 off if all values are positive, 0.4 half steps of fp16; added here, 64 streams of
+                // two parts and D 64, 128, 256 take 78, 104, 160 us instead of 74, 103, 129.)
                 auto pv = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
                     if constexpr (kAdd) {
                         float d[4] = {};

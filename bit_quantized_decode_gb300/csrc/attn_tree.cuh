@@ -293,8 +293,9 @@ __device__ __forceinline__ float2 unpair16(uint32_t u)
 //
 // A value that a row sees may be infinite, and then every part times it has to be that infinity: a part that is 0 or of the
 // other sign would make it a NaN.  So parts are cut towards zero and what is left counts a step of the last part more than it
-// is (2^-23 of the probability, fp16 2^-21): it has the probability's sign and is not 0 (down to 2^-87; fp16, whose least step
-// is 2^-24, to 2^-13 of the largest and on the mma.sync kernel 2^-19).  An INT8 cache's codes are finite: its parts are
+// is (2^-23 of the probability, fp16 2^-21; against what the tensor cores cut from the sums: with the sum of the probabilities
+// made as much larger, errors of 0.6e-6 to 3.8e-6 become 0.9e-6 to 3.9e-6): it has the probability's sign and is not 0 (down to
+// 2^-87; fp16, whose least step is 2^-24, to 2^-13 of the largest and on the mma.sync kernel 2^-19).  An INT8 cache's codes are finite: its parts are
 // rounded, and where a value's scale, which the probability has taken in, makes that infinite, the first part has it all
 // (only_first).
 template <int T, bool kCodes>

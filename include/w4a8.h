@@ -615,7 +615,7 @@ w4_status w4_moe_layer(const w4_router* r, const w4_experts* e, const void* x, i
  *   rows 0 .. i.  A row that sees nothing gets 0.  What a row does not see
  *   does not reach it, infinities and NaN included.  An infinite value (or
  *   scale of values) that it sees makes its outputs infinite, or NaN where the
- *   probability is 0 in 16 bits or, of fp16 with y W4_F32, below 2^-13 of the
+ *   probability is 0 in 16 bits or, in two parts of fp16, below 2^-13 of the
  *   row's largest.  q [T][Hq][D] of the
  *   cache's type (either 16-bit type for W4_I8), y [T][Hq][D] of y_type, both
  *   16-byte aligned; query head h reads key head h / (Hq / Hkv).
